@@ -26,7 +26,7 @@ SUPPORTED_HEAD_DIMS = ((64, 64), (128, 128), (192, 128))
 __all__ = [
     "attn_fwd", "attn_fwd_block_sparse", "attn_fwd_varlen", "attn_bwd", "attn_bwd_block_sparse",
     "block_lists_from_mask", "attn_bwd_varlen", "attn_exp2_eval",
-    "attn_get_device_status", "attention", "AttnError", "SUPPORTED_HEAD_DIMS", "library_path",
+    "attn_get_device_status", "attention", "attention_varlen", "AttnError", "SUPPORTED_HEAD_DIMS", "library_path",
 ]
 
 
@@ -34,9 +34,9 @@ def library_path() -> str:
     return _abi.LIB_PATH
 
 
-def _stream(stream) -> ctypes.c_void_p:
+def _stream(stream, device=None) -> ctypes.c_void_p:
     if stream is None:
-        stream = torch.cuda.current_stream()
+        stream = torch.cuda.current_stream(device)
     return ctypes.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
 
 
@@ -94,7 +94,7 @@ def _fill_fwd(p: AttnFwdParams, q, k, v, o, lse, strides, scale, causal):
     (p.v_batch_stride, p.v_row_stride, p.v_head_stride) = strides(v)
     (p.o_batch_stride, p.o_row_stride, p.o_head_stride) = strides(o)
     p.d_qk, p.d_v = q.shape[-1], v.shape[-1]
-    p.heads = q.shape[-2]
+    p.heads, p.heads_kv = q.shape[-2], k.shape[-2]
     p.softmax_scale = scale
     p.causal = 1 if causal else 0
 
@@ -115,10 +115,55 @@ def _set_score_mod(p: AttnFwdParams, q: torch.Tensor, softcap, alibi_slopes):
         p.score_mod, p.alibi_slopes = _abi.SCORE_ALIBI, _ptr(t)
 
 
-def _workspace(size: int, device) -> Tuple[Optional[torch.Tensor], int]:
+def _workspace(size: int, device, stream=None) -> Tuple[Optional[torch.Tensor], int]:
     if size == 0:
         return None, 0
-    return torch.empty(size, dtype=torch.uint8, device=device), size
+    ws = torch.empty(size, dtype=torch.uint8, device=device)
+    _used_on(stream, ws)
+    return ws, size
+
+
+def _used_on(stream, *tensors):
+    """Tensors that a call allocates belong to the current stream; when the call runs on another one,
+    their memory must not be handed out again before that stream is done with it."""
+    if stream is None:
+        return
+    for t in tensors:
+        s = stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream), device=t.device)
+        if s.cuda_stream != torch.cuda.current_stream(t.device).cuda_stream:
+            t.record_stream(s)
+
+
+def _check_kv(q, k, v):
+    """k and v of a call whose query heads may share K/V heads: q [..., H, d_qk], k [..., Hkv, d_qk] and
+    v [..., Hkv, d_v] with Hkv a divisor of H, rows of k and v alike (dense: batches of q alike)."""
+    h, hk = q.shape[-2], k.shape[-2]
+    if k.shape[-1] != q.shape[-1] or v.shape[:-1] != k.shape[:-1] or (k.dim() == 4 and k.shape[0] != q.shape[0]):
+        raise ValueError(f"shape mismatch q{tuple(q.shape)} k{tuple(k.shape)} v{tuple(v.shape)}")
+    if hk < 1 or h % hk != 0:
+        raise ValueError(f"{hk} K/V heads do not divide {h} query heads")
+    for n, t in (("k", k), ("v", v)):
+        if t.device != q.device:
+            raise ValueError(f"{n} is on {t.device} but q is on {q.device}")
+
+
+def _check_bwd(q, k, v, out, lse, dout, lse_shape, grads):
+    """The forward's outputs and dO of a backward call, and gradient buffers the caller passed in."""
+    _check_kv(q, k, v)
+    want = q.shape[:-1] + v.shape[-1:]
+    for n, t in (("out", out), ("dout", dout)):
+        if t.shape != want:
+            raise ValueError(f"{n} must be {tuple(want)}, got {tuple(t.shape)}")
+    if tuple(lse.shape) != lse_shape or not lse.is_contiguous() or lse.dtype != torch.float32:
+        raise ValueError(f"lse must be a contiguous float32 tensor of shape {lse_shape}")
+    for n, t, like in (("dq", grads[0], q), ("dk", grads[1], k), ("dv", grads[2], v)):
+        if t is not None:
+            _check_bf16(n, t, like.dim())
+            if t.shape != like.shape:
+                raise ValueError(f"{n} must be {tuple(like.shape)}, got {tuple(t.shape)}")
+    for n, t in (("out", out), ("lse", lse), ("dout", dout)):
+        if t.device != q.device:
+            raise ValueError(f"{n} is on {t.device} but q is on {q.device}")
 
 
 def attn_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, *, causal: bool = False,
@@ -127,7 +172,8 @@ def attn_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, *, causal: bool 
              exp2_emu_period: int = 0, softcap: Optional[float] = None,
              alibi_slopes: Optional[torch.Tensor] = None, q_descale: float = 1.0, k_descale: float = 1.0,
              v_descale: float = 1.0, cta_pair: bool = False, stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
-    """Dense forward. q [B, Nq, H, d_qk], k [B, Nk, H, d_qk], v [B, Nk, H, d_v] (bf16, CUDA).
+    """Dense forward. q [B, Nq, H, d_qk], k [B, Nk, Hkv, d_qk], v [B, Nk, Hkv, d_v] (bf16, CUDA); Hkv
+    divides H, and query head h reads K/V head h // (H // Hkv).
     Returns (O [B, Nq, H, d_v] bf16, LSE [B, H, Nq] fp32, natural log). ``exp2_emu_period`` (0, 4, 8)
     sends one column in that many of every row's exp2 to the FMA-pipe polynomial. ``softcap`` or
     ``alibi_slopes`` select a score modification (include/attn.h, attn_fwd_params.score_mod).
@@ -136,14 +182,17 @@ def attn_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, *, causal: bool 
     f8 = _check_inputs(q, k, v, 4)
     B, Nq, H, dqk = q.shape
     Nk, dv = k.shape[1], v.shape[-1]
-    if k.shape != (B, Nk, H, dqk) or v.shape[:3] != (B, Nk, H):
-        raise ValueError(f"shape mismatch q{tuple(q.shape)} k{tuple(k.shape)} v{tuple(v.shape)}")
+    _check_kv(q, k, v)
     scale = float(softmax_scale) if softmax_scale is not None else 1.0 / math.sqrt(dqk)
     if out is None:
         out = torch.empty((B, Nq, H, dv), dtype=torch.bfloat16, device=q.device)
+        _used_on(stream, out)
     _check_bf16("out", out, 4)
+    if out.shape != (B, Nq, H, dv):
+        raise ValueError(f"out must be {(B, Nq, H, dv)}, got {tuple(out.shape)}")
     if lse is None:
         lse = torch.empty((B, H, Nq), dtype=torch.float32, device=q.device)
+        _used_on(stream, lse)
     if lse.shape != (B, H, Nq) or not lse.is_contiguous() or lse.dtype != torch.float32:
         raise ValueError("lse must be a contiguous float32 [B, H, Nq] tensor")
     p = AttnFwdParams()
@@ -154,8 +203,8 @@ def attn_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, *, causal: bool 
     _set_score_mod(p, q, softcap, alibi_slopes)
     _set_input_dtype(p, f8, q_descale, k_descale, v_descale)
     p.cta_pair = 1 if cta_pair else 0
-    ws, nbytes = _workspace(_lib.attn_fwd_workspace_size(ctypes.byref(p)), q.device)
-    _abi.check(_lib.attn_fwd(ctypes.byref(p), _ptr(ws), nbytes, _stream(stream)), "attn_fwd")
+    ws, nbytes = _workspace(_lib.attn_fwd_workspace_size(ctypes.byref(p)), q.device, stream)
+    _abi.check(_lib.attn_fwd(ctypes.byref(p), _ptr(ws), nbytes, _stream(stream, q.device)), "attn_fwd")
     return out, lse
 
 
@@ -224,9 +273,9 @@ def attn_fwd_block_sparse(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, kv_
     _fill_fwd(p, q, k, v, out, lse, _strides4, scale, causal)
     p.batch, p.seqlen_q, p.seqlen_k = B, Nq, Nk
     _set_score_mod(p, q, softcap, alibi_slopes)
-    ws, nbytes = _workspace(_lib.attn_fwd_workspace_size(ctypes.byref(p)), q.device)
+    ws, nbytes = _workspace(_lib.attn_fwd_workspace_size(ctypes.byref(p)), q.device, stream)
     _abi.check(_lib.attn_fwd_block_sparse(ctypes.byref(p), _ptr(kv_count), _ptr(kv_index), max_kv, per_head,
-                                          _ptr(ws), nbytes, _stream(stream)), "attn_fwd_block_sparse")
+                                          _ptr(ws), nbytes, _stream(stream, q.device)), "attn_fwd_block_sparse")
     return out, lse
 
 
@@ -238,8 +287,8 @@ def attn_fwd_varlen(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqlen
                     alibi_slopes: Optional[torch.Tensor] = None, q_descale: float = 1.0, k_descale: float = 1.0,
                     v_descale: float = 1.0, cta_pair: bool = False,
                     stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
-    """Packed variable-length forward. q [total_q, H, d_qk], k/v [total_k, H, d]; cu_seqlens int32 on
-    the device. Returns (O [total_q, H, d_v], LSE [H, total_q]). Score modifications and E4M3 inputs
+    """Packed variable-length forward. q [total_q, H, d_qk], k/v [total_k, Hkv, d] with Hkv a divisor of H
+    (query head h reads K/V head h // (H // Hkv)); cu_seqlens int32 on the device. Returns (O [total_q, H, d_v], LSE [H, total_q]). Score modifications and E4M3 inputs
     as in :func:`attn_fwd`, positions counted within each sequence."""
     f8 = _check_inputs(q, k, v, 3)
     for n, t in (("cu_seqlens_q", cu_seqlens_q), ("cu_seqlens_k", cu_seqlens_k)):
@@ -247,11 +296,19 @@ def attn_fwd_varlen(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqlen
             raise ValueError(f"{n} must be a contiguous int32 CUDA tensor")
     tq, H, dqk = q.shape
     tk, dv = k.shape[0], v.shape[-1]
+    _check_kv(q, k, v)
     scale = float(softmax_scale) if softmax_scale is not None else 1.0 / math.sqrt(dqk)
     if out is None:
         out = torch.empty((tq, H, dv), dtype=torch.bfloat16, device=q.device)
+        _used_on(stream, out)
+    _check_bf16("out", out, 3)
+    if out.shape != (tq, H, dv):
+        raise ValueError(f"out must be {(tq, H, dv)}, got {tuple(out.shape)}")
     if lse is None:
         lse = torch.empty((H, tq), dtype=torch.float32, device=q.device)
+        _used_on(stream, lse)
+    if lse.shape != (H, tq) or not lse.is_contiguous() or lse.dtype != torch.float32:
+        raise ValueError("lse must be a contiguous float32 [H, total_q] tensor")
     p = AttnFwdParams()
     _fill_fwd(p, q, k, v, out, lse, _strides3, scale, causal)
     p.cu_seqlens_q, p.cu_seqlens_k = _ptr(cu_seqlens_q), _ptr(cu_seqlens_k)
@@ -264,8 +321,8 @@ def attn_fwd_varlen(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqlen
     _set_score_mod(p, q, softcap, alibi_slopes)
     _set_input_dtype(p, f8, q_descale, k_descale, v_descale)
     p.cta_pair = 1 if cta_pair else 0
-    ws, nbytes = _workspace(_lib.attn_fwd_workspace_size(ctypes.byref(p)), q.device)
-    _abi.check(_lib.attn_fwd_varlen(ctypes.byref(p), _ptr(ws), nbytes, _stream(stream)), "attn_fwd_varlen")
+    ws, nbytes = _workspace(_lib.attn_fwd_workspace_size(ctypes.byref(p)), q.device, stream)
+    _abi.check(_lib.attn_fwd_varlen(ctypes.byref(p), _ptr(ws), nbytes, _stream(stream, q.device)), "attn_fwd_varlen")
     return out, lse
 
 
@@ -278,6 +335,16 @@ def _fill_bwd(p: AttnBwdParams, do, dq, dk, dv, strides, deterministic, cta_pair
     p.deterministic = 1 if deterministic else 0
     p.cta_pair = 1 if cta_pair else 0
     p.single_pass = 1 if single_pass else 0
+
+
+def _grad_buffers(stream, *pairs):
+    out = []
+    for grad, like in pairs:
+        if grad is None:
+            grad = torch.empty_like(like)
+            _used_on(stream, grad)
+        out.append(grad)
+    return out
 
 
 def _event_handles(events):
@@ -298,7 +365,8 @@ def attn_bwd(q, k, v, out, lse, dout, *, causal: bool = False, softmax_scale: Op
              deterministic: bool = False, dq=None, dk=None, dv=None, stream=None, phase_events=None,
              cta_pair: bool = False, softcap: Optional[float] = None, alibi_slopes: Optional[torch.Tensor] = None,
              single_pass: bool = False):
-    """Dense backward: returns (dQ, dK, dV) bf16 for the loss <O, dO>. ``phase_events`` (optional, three
+    """Dense backward: returns (dQ, dK, dV) bf16 for the loss <O, dO>; where query heads share K/V heads
+    (attn_fwd), dK and dV are the sums over them. ``phase_events`` (optional, three
     torch.cuda.Event) are recorded after the D pass, the dK/dV kernel and the dQ kernel. ``cta_pair``
     selects the two-SM (cta_group::2) dK/dV kernel (d = 128); ``single_pass`` the one-kernel backward
     whose dQ partials are reduced across CTAs (d = 64; ordered by key tile when ``deterministic``).
@@ -307,10 +375,9 @@ def attn_bwd(q, k, v, out, lse, dout, *, causal: bool = False, softmax_scale: Op
         _check_bf16(n, t, 4)
     B, Nq, H, dqk = q.shape
     Nk = k.shape[1]
+    _check_bwd(q, k, v, out, lse, dout, (B, H, Nq), (dq, dk, dv))
     scale = float(softmax_scale) if softmax_scale is not None else 1.0 / math.sqrt(dqk)
-    dq = torch.empty_like(q) if dq is None else dq
-    dk = torch.empty_like(k) if dk is None else dk
-    dv = torch.empty_like(v) if dv is None else dv
+    dq, dk, dv = _grad_buffers(stream, (dq, q), (dk, k), (dv, v))
     p = AttnBwdParams()
     _fill_fwd(p.fwd, q, k, v, out, lse, _strides4, scale, causal)
     p.fwd.batch, p.fwd.seqlen_q, p.fwd.seqlen_k = B, Nq, Nk
@@ -320,8 +387,8 @@ def attn_bwd(q, k, v, out, lse, dout, *, causal: bool = False, softmax_scale: Op
     if handles is not None:
         for i, h in enumerate(handles):
             p.phase_events[i] = h
-    ws, nbytes = _workspace(_lib.attn_bwd_workspace_size(ctypes.byref(p)), q.device)
-    _abi.check(_lib.attn_bwd(ctypes.byref(p), _ptr(ws), nbytes, _stream(stream)), "attn_bwd")
+    ws, nbytes = _workspace(_lib.attn_bwd_workspace_size(ctypes.byref(p)), q.device, stream)
+    _abi.check(_lib.attn_bwd(ctypes.byref(p), _ptr(ws), nbytes, _stream(stream, q.device)), "attn_bwd")
     return dq, dk, dv
 
 
@@ -335,19 +402,18 @@ def attn_bwd_block_sparse(q, k, v, out, lse, dout, kv_count, kv_index, *, causal
         _check_bf16(n, t, 4)
     B, Nq, H, dqk = q.shape
     Nk = k.shape[1]
+    _check_bwd(q, k, v, out, lse, dout, (B, H, Nq), (dq, dk, dv))
     max_kv, per_head = _check_lists(q, kv_count, kv_index)
     scale = float(softmax_scale) if softmax_scale is not None else 1.0 / math.sqrt(dqk)
-    dq = torch.empty_like(q) if dq is None else dq
-    dk = torch.empty_like(k) if dk is None else dk
-    dv = torch.empty_like(v) if dv is None else dv
+    dq, dk, dv = _grad_buffers(stream, (dq, q), (dk, k), (dv, v))
     p = AttnBwdParams()
     _fill_fwd(p.fwd, q, k, v, out, lse, _strides4, scale, causal)
     p.fwd.batch, p.fwd.seqlen_q, p.fwd.seqlen_k = B, Nq, Nk
     _fill_bwd(p, dout, dq, dk, dv, _strides4, deterministic)
     _set_score_mod(p.fwd, q, softcap, alibi_slopes)
-    ws, nbytes = _workspace(_lib.attn_bwd_block_sparse_workspace_size(ctypes.byref(p), per_head), q.device)
+    ws, nbytes = _workspace(_lib.attn_bwd_block_sparse_workspace_size(ctypes.byref(p), per_head), q.device, stream)
     _abi.check(_lib.attn_bwd_block_sparse(ctypes.byref(p), _ptr(kv_count), _ptr(kv_index), max_kv, per_head,
-                                          _ptr(ws), nbytes, _stream(stream)), "attn_bwd_block_sparse")
+                                          _ptr(ws), nbytes, _stream(stream, q.device)), "attn_bwd_block_sparse")
     return dq, dk, dv
 
 
@@ -355,14 +421,17 @@ def attn_bwd_varlen(q, k, v, out, lse, dout, cu_seqlens_q, cu_seqlens_k, max_seq
                     causal: bool = False, softmax_scale: Optional[float] = None, deterministic: bool = False,
                     dq=None, dk=None, dv=None, stream=None, cta_pair: bool = False, softcap: Optional[float] = None,
                     alibi_slopes: Optional[torch.Tensor] = None, single_pass: bool = False):
-    """Packed variable-length backward: returns (dQ, dK, dV) packed like q, k, v."""
+    """Packed variable-length backward: returns (dQ, dK, dV) packed like q, k, v; where query heads share
+    K/V heads (attn_fwd_varlen), dK and dV are the sums over them."""
     for n, t in (("q", q), ("k", k), ("v", v), ("out", out), ("dout", dout)):
         _check_bf16(n, t, 3)
     tq, H, dqk = q.shape
+    _check_bwd(q, k, v, out, lse, dout, (H, tq), (dq, dk, dv))
+    for n, t in (("cu_seqlens_q", cu_seqlens_q), ("cu_seqlens_k", cu_seqlens_k)):
+        if t.dtype != torch.int32 or not t.is_cuda or not t.is_contiguous():
+            raise ValueError(f"{n} must be a contiguous int32 CUDA tensor")
     scale = float(softmax_scale) if softmax_scale is not None else 1.0 / math.sqrt(dqk)
-    dq = torch.empty_like(q) if dq is None else dq
-    dk = torch.empty_like(k) if dk is None else dk
-    dv = torch.empty_like(v) if dv is None else dv
+    dq, dk, dv = _grad_buffers(stream, (dq, q), (dk, k), (dv, v))
     p = AttnBwdParams()
     _fill_fwd(p.fwd, q, k, v, out, lse, _strides3, scale, causal)
     p.fwd.cu_seqlens_q, p.fwd.cu_seqlens_k = _ptr(cu_seqlens_q), _ptr(cu_seqlens_k)
@@ -372,8 +441,8 @@ def attn_bwd_varlen(q, k, v, out, lse, dout, cu_seqlens_q, cu_seqlens_k, max_seq
     p.fwd.batch = 1
     _fill_bwd(p, dout, dq, dk, dv, _strides3, deterministic, cta_pair, single_pass)
     _set_score_mod(p.fwd, q, softcap, alibi_slopes)
-    ws, nbytes = _workspace(_lib.attn_bwd_workspace_size(ctypes.byref(p)), q.device)
-    _abi.check(_lib.attn_bwd_varlen(ctypes.byref(p), _ptr(ws), nbytes, _stream(stream)), "attn_bwd_varlen")
+    ws, nbytes = _workspace(_lib.attn_bwd_workspace_size(ctypes.byref(p)), q.device, stream)
+    _abi.check(_lib.attn_bwd_varlen(ctypes.byref(p), _ptr(ws), nbytes, _stream(stream, q.device)), "attn_bwd_varlen")
     return dq, dk, dv
 
 
@@ -427,8 +496,38 @@ class _Attention(torch.autograd.Function):
 def attention(q, k, v, causal: bool = False, softmax_scale: Optional[float] = None, deterministic: bool = False,
               block_mask: Optional[Tuple[torch.Tensor, torch.Tensor]] = None, softcap: Optional[float] = None,
               alibi_slopes: Optional[torch.Tensor] = None):
-    """Autograd wrapper over attn_fwd / attn_bwd for [B, N, H, d] bf16 tensors. ``block_mask``
+    """Autograd wrapper over attn_fwd / attn_bwd for [B, N, H, d] bf16 tensors; k and v may have fewer
+    heads, a divisor of H, shared among the query heads as in attn_fwd. ``block_mask``
     = (kv_count, kv_index) selects the block-sparse pair attn_fwd_block_sparse / attn_bwd_block_sparse;
     ``softcap`` / ``alibi_slopes`` a score modification."""
     kv_count, kv_index = block_mask if block_mask is not None else (None, None)
     return _Attention.apply(q, k, v, causal, softmax_scale, deterministic, kv_count, kv_index, softcap, alibi_slopes)
+
+
+class _AttentionVarlen(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, q, k, v, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, max_seqlen_k, causal, softmax_scale,
+                deterministic, softcap, alibi_slopes):
+        mod = dict(softcap=softcap, alibi_slopes=alibi_slopes)
+        o, lse = attn_fwd_varlen(q, k, v, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, max_seqlen_k, causal=causal,
+                                 softmax_scale=softmax_scale, **mod)
+        ctx.save_for_backward(q, k, v, o, lse, cu_seqlens_q, cu_seqlens_k)
+        ctx.lengths = (max_seqlen_q, max_seqlen_k)
+        ctx.causal, ctx.scale, ctx.det, ctx.mod = causal, softmax_scale, deterministic, mod
+        return o
+
+    @staticmethod
+    def backward(ctx, do):
+        q, k, v, o, lse, cu_q, cu_k = ctx.saved_tensors
+        grads = attn_bwd_varlen(q, k, v, o, lse, do.contiguous(), cu_q, cu_k, *ctx.lengths, causal=ctx.causal,
+                                softmax_scale=ctx.scale, deterministic=ctx.det, **ctx.mod)
+        return (*grads, *(None,) * 9)
+
+
+def attention_varlen(q, k, v, cu_seqlens_q, cu_seqlens_k, max_seqlen_q: int, max_seqlen_k: int, causal: bool = False,
+                     softmax_scale: Optional[float] = None, deterministic: bool = False,
+                     softcap: Optional[float] = None, alibi_slopes: Optional[torch.Tensor] = None):
+    """Autograd wrapper over attn_fwd_varlen / attn_bwd_varlen for packed bf16 tensors q [total_q, H, d_qk],
+    k [total_k, Hkv, d_qk] and v [total_k, Hkv, d_v]; ``softcap`` / ``alibi_slopes`` select a score modification."""
+    return _AttentionVarlen.apply(q, k, v, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, max_seqlen_k, causal,
+                                  softmax_scale, deterministic, softcap, alibi_slopes)

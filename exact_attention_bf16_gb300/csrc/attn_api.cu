@@ -158,6 +158,10 @@ bool supported_dims(int dqk, int dv) {
   return (dqk == 64 && dv == 64) || (dqk == 128 && dv == 128) || (dqk == 192 && dv == 128);
 }
 
+// Heads of k and v: heads_kv, or one per query head.
+int kv_heads(const attn_fwd_params* p) { return p->heads_kv == 0 ? p->heads : p->heads_kv; }
+bool shared_kv(const attn_fwd_params* p) { return kv_heads(p) != p->heads; }
+
 // Shape-level checks shared by every entry point.
 attn_status_t check_common(const attn_fwd_params* p, bool varlen) {
   if (!p) return ATTN_ERR_INVALID_ARG;
@@ -166,6 +170,7 @@ attn_status_t check_common(const attn_fwd_params* p, bool varlen) {
     return ATTN_ERR_UNSUPPORTED;
   }
   if (p->heads < 1) return ATTN_ERR_INVALID_ARG;
+  if (p->heads_kv < 0 || p->heads % kv_heads(p) != 0) return ATTN_ERR_INVALID_ARG;
   if (!(std::isfinite(p->softmax_scale) && p->softmax_scale > 0.f)) return ATTN_ERR_INVALID_ARG;
   if (varlen) {
     if (!p->cu_seqlens_q || !p->cu_seqlens_k) return ATTN_ERR_INVALID_ARG;
@@ -285,10 +290,10 @@ size_t seq_scratch_bytes(int num_seqs) { return round256(static_cast<int64_t>(nu
 // (packed variable length) the tile list and its scratch, or (split keys) the
 // ranges' fp32 O and LSE.
 size_t fwd_v16_bytes(const attn_fwd_params* p, bool varlen) {
-  if (p->heads < 1 || p->d_v <= 0) return 0;
+  if (p->heads < 1 || p->heads_kv < 0 || p->d_v <= 0) return 0;
   const int64_t rows = varlen ? static_cast<int64_t>(p->total_k) : static_cast<int64_t>(p->batch) * p->seqlen_k;
   if (rows <= 0) return 0;
-  return static_cast<size_t>((rows * p->heads * p->d_v * 2 + 255) / 256 * 256);
+  return static_cast<size_t>((rows * kv_heads(p) * p->d_v * 2 + 255) / 256 * 256);
 }
 ListPlan fwd_list_plan(const attn_fwd_params* p, bool varlen) {  // the pair forward takes no list
   return varlen && !p->cta_pair ? list_plan(p->total_q, p->num_seqs, p->heads, p->max_seqlen_q, 256) : ListPlan{};
@@ -361,6 +366,8 @@ attn_status_t run_fwd(const attn_fwd_params* p, bool varlen, cudaStream_t stream
   if (p->cta_pair && (p->d_qk != 128 || p->d_v != 128 || f8 || p->exp2_emu_period != 0 ||
                       p->score_mod != ATTN_SCORE_NONE || sp.kv_count != nullptr || diag_limit))
     return ATTN_ERR_UNSUPPORTED;
+  if (shared_kv(p) && (p->cta_pair || sp.kv_count != nullptr || diag_limit)) return ATTN_ERR_UNSUPPORTED;
+  const int hkv = kv_heads(p);
   const int nq_rows = varlen ? p->total_q : p->seqlen_q;
   const int nk_rows = varlen ? p->total_k : p->seqlen_k;
   const int units = varlen ? p->num_seqs : p->batch;
@@ -384,6 +391,7 @@ attn_status_t run_fwd(const attn_fwd_params* p, bool varlen, cudaStream_t stream
   a.o_sh = p->o_head_stride;
   a.batch = varlen ? 1 : p->batch;
   a.heads = p->heads;
+  a.kv_group = p->heads / hkv;
   a.seqlen_q = varlen ? p->total_q : p->seqlen_q;
   a.seqlen_k = varlen ? p->total_k : p->seqlen_k;
   a.lse_sb = varlen ? 0 : static_cast<int64_t>(p->heads) * p->seqlen_q;
@@ -431,9 +439,9 @@ attn_status_t run_fwd(const attn_fwd_params* p, bool varlen, cudaStream_t stream
   const int eb = f8 ? 1 : 2;
   ATTN_TRY(make_map(&tq, p->q, p->d_qk, p->heads, nq_rows, nb, p->q_batch_stride, p->q_row_stride,
                     p->q_head_stride, 128, eb));
-  ATTN_TRY(make_map(&tk, p->k, p->d_qk, p->heads, nk_rows, nb, p->k_batch_stride, p->k_row_stride,
+  ATTN_TRY(make_map(&tk, p->k, p->d_qk, hkv, nk_rows, nb, p->k_batch_stride, p->k_row_stride,
                     p->k_head_stride, 128, eb));
-  ATTN_TRY(make_map(&tv, p->v, p->d_v, p->heads, nk_rows, nb, p->v_batch_stride, p->v_row_stride,
+  ATTN_TRY(make_map(&tv, p->v, p->d_v, hkv, nk_rows, nb, p->v_batch_stride, p->v_row_stride,
                     p->v_head_stride, 128, eb));
   if (diag_limit) {
     e = launch_fwd_diag_timeout(tq, tk, tv, a, stream);
@@ -444,15 +452,15 @@ attn_status_t run_fwd(const attn_fwd_params* p, bool varlen, cudaStream_t stream
   void* v16 = static_cast<uint8_t*>(ws) + 256;
   const int64_t v16_rows = varlen ? p->total_k : p->seqlen_k;
   CUtensorMap tv16;
-  ATTN_TRY(make_map(&tv16, v16, p->d_v, p->heads, nk_rows, nb, v16_rows * p->heads * p->d_v,
-                    static_cast<int64_t>(p->heads) * p->d_v, p->d_v, 128));
+  ATTN_TRY(make_map(&tv16, v16, p->d_v, hkv, nk_rows, nb, v16_rows * hkv * p->d_v,
+                    static_cast<int64_t>(hkv) * p->d_v, p->d_v, 128));
   e = cudaMemsetAsync(flag, 0, sizeof(uint32_t), stream);
   if (e == cudaSuccess && f8)  // exact: every E4M3 value is an fp16 value, the flag stays 0
     e = launch_v_e4m3_to_f16(p->v, varlen ? 0 : p->v_batch_stride, p->v_row_stride, p->v_head_stride, nb, nk_rows,
-                             p->heads, p->d_v, v16, stream);
+                             hkv, p->d_v, v16, stream);
   else if (e == cudaSuccess)
     e = launch_v_to_f16(p->v, varlen ? 0 : p->v_batch_stride, p->v_row_stride, p->v_head_stride, nb, nk_rows,
-                        p->heads, p->d_v, v16, flag, stream);
+                        hkv, p->d_v, v16, flag, stream);
   if (e != cudaSuccess) return cuda_fail(e, "fwd V conversion");
   a.v16_flag = flag;
   const ListPlan lp = fwd_list_plan(p, varlen);
@@ -505,7 +513,7 @@ size_t bwd_d_bytes(const attn_bwd_params* p, bool varlen) {
 }
 ListPlan bwd_kv_plan(const attn_bwd_params* p, bool varlen) {
   const attn_fwd_params& f = p->fwd;
-  return varlen && !p->cta_pair ? list_plan(f.total_k, f.num_seqs, f.heads, f.max_seqlen_k, 128) : ListPlan{};
+  return varlen && !p->cta_pair ? list_plan(f.total_k, f.num_seqs, kv_heads(&f), f.max_seqlen_k, 128) : ListPlan{};
 }
 ListPlan bwd_q_plan(const attn_bwd_params* p, bool varlen) {
   const attn_fwd_params& f = p->fwd;
@@ -598,6 +606,8 @@ attn_status_t run_bwd(const attn_bwd_params* p, void* ws, size_t ws_bytes, bool 
   if (p->single_pass && (f.d_qk != 64 || f.d_v != 64 || sp.kv_count || f.score_mod != ATTN_SCORE_NONE ||
                          p->cta_pair))
     return ATTN_ERR_UNSUPPORTED;
+  if (shared_kv(&f) && (p->cta_pair || p->single_pass || sp.kv_count)) return ATTN_ERR_UNSUPPORTED;
+  const int hkv = kv_heads(&f);
   const int nq_rows = varlen ? f.total_q : f.seqlen_q;
   const int nk_rows = varlen ? f.total_k : f.seqlen_k;
   if (nq_rows == 0 && nk_rows == 0) return ATTN_OK;
@@ -633,6 +643,8 @@ attn_status_t run_bwd(const attn_bwd_params* p, void* ws, size_t ws_bytes, bool 
   a.lse_sh = varlen ? f.total_q : f.seqlen_q;
   a.batch = varlen ? 1 : f.batch;
   a.heads = f.heads;
+  a.heads_kv = hkv;
+  a.kv_group = f.heads / hkv;
   a.seqlen_q = nq_rows;
   a.seqlen_k = nk_rows;
   a.cu_q = varlen ? f.cu_seqlens_q : nullptr;
@@ -650,6 +662,13 @@ attn_status_t run_bwd(const attn_bwd_params* p, void* ws, size_t ws_bytes, bool 
   if (f.causal && sp.kv_count == nullptr && !(p->single_pass && p->deterministic) && a.n_kblk >= 16)
     a.n_groups = group_count(a.num_units * f.heads,
                              static_cast<int64_t>(max_q > max_k ? max_q : max_k) * (f.d_qk + f.d_v) * 2);
+  // dK/dV: one pair per K/V head, which streams the Q and dO of its whole group
+  a.n_groups_kv = a.n_groups;
+  if (a.kv_group > 1)
+    a.n_groups_kv = a.n_groups == a.num_units * f.heads
+                        ? a.num_units * hkv
+                        : group_count(a.num_units * hkv, static_cast<int64_t>(max_q > max_k ? max_q : max_k) *
+                                                             (f.d_qk + f.d_v) * 2 * a.kv_group);
   fill_score_mod(a, &f);
   const int n_kb_sparse = (f.seqlen_k + 127) / 128;
   if (sp.kv_count) {
@@ -674,7 +693,7 @@ attn_status_t run_bwd(const attn_bwd_params* p, void* ws, size_t ws_bytes, bool 
       TileEntry* list = reinterpret_cast<TileEntry*>(lbase);
       // the deterministic single pass launches key tiles in descending order (its adds' order)
       const bool desc = p->single_pass && p->deterministic;
-      e = launch_tile_list(f.cu_seqlens_q, f.cu_seqlens_k, f.num_seqs, f.heads, 128, true, desc, kv.max_nblk, list,
+      e = launch_tile_list(f.cu_seqlens_q, f.cu_seqlens_k, f.num_seqs, hkv, 128, true, desc, kv.max_nblk, list,
                            scratch, kv.bound, stream);
       if (e != cudaSuccess) return cuda_fail(e, "bwd tile list");
       a.tiles_kv = list;
@@ -701,8 +720,8 @@ attn_status_t run_bwd(const attn_bwd_params* p, void* ws, size_t ws_bytes, bool 
   const int qrows = bwd_dkdv_rows(f.d_qk);
   CUtensorMap tq, tk, tv, tdo, tq2, tdo2;
   ATTN_TRY(make_map(&tq, f.q, f.d_qk, f.heads, nq_rows, nb, f.q_batch_stride, f.q_row_stride, f.q_head_stride, 128));
-  ATTN_TRY(make_map(&tk, f.k, f.d_qk, f.heads, nk_rows, nb, f.k_batch_stride, f.k_row_stride, f.k_head_stride, 128));
-  ATTN_TRY(make_map(&tv, f.v, f.d_v, f.heads, nk_rows, nb, f.v_batch_stride, f.v_row_stride, f.v_head_stride, 128));
+  ATTN_TRY(make_map(&tk, f.k, f.d_qk, hkv, nk_rows, nb, f.k_batch_stride, f.k_row_stride, f.k_head_stride, 128));
+  ATTN_TRY(make_map(&tv, f.v, f.d_v, hkv, nk_rows, nb, f.v_batch_stride, f.v_row_stride, f.v_head_stride, 128));
   ATTN_TRY(make_map(&tdo, p->dout, f.d_v, f.heads, nq_rows, nb, p->do_batch_stride, p->do_row_stride,
                     p->do_head_stride, 128));
   ATTN_TRY(make_map(&tq2, f.q, f.d_qk, f.heads, nq_rows, nb, f.q_batch_stride, f.q_row_stride, f.q_head_stride,
@@ -813,7 +832,7 @@ attn_status_t attn_fwd_block_sparse(const attn_fwd_params* p, const int32_t* kv_
 }
 
 size_t attn_bwd_block_sparse_workspace_size(const attn_bwd_params* p, int32_t lists_per_head) {
-  if (!p || p->fwd.cu_seqlens_q != nullptr || (lists_per_head != 0 && lists_per_head != 1)) return 0;
+  if (!p || p->fwd.heads_kv < 0 || p->fwd.cu_seqlens_q != nullptr || (lists_per_head != 0 && lists_per_head != 1)) return 0;
   if (p->fwd.batch < 0 || p->fwd.heads < 0 || p->fwd.seqlen_q < 0 || p->fwd.seqlen_k < 0) return 0;
   return bwd_workspace_bytes(p, false) + bwd_sparse_extra_bytes(p->fwd, lists_per_head);
 }

@@ -120,6 +120,14 @@ cudaError_t launch_bwd_dkdv(int d_qk, int d_v, const CUtensorMap& tq, const CUte
     if (d_qk == 192 && d_v == 128) return bwd::launch_dkdv_t<192, 128, true>(tq, tk, tv, tdo, a, stream);
     return cudaErrorInvalidValue;
   }
+  if (a.kv_group > 1) {  // shared K/V heads
+    if (d_qk == 64 && d_v == 64)
+      return bwd::launch_dkdv_t<64, 64, false, kModNone, false, true>(tq, tk, tv, tdo, a, stream);
+    if (d_qk == 128 && d_v == 128) return bwd::launch_dkdv_wide<false, kModNone, true>(tq, tk, tv, tdo, a, stream);
+    if (d_qk == 192 && d_v == 128)
+      return bwd::launch_dkdv_t<192, 128, false, kModNone, false, true>(tq, tk, tv, tdo, a, stream);
+    return cudaErrorInvalidValue;
+  }
   if (d_qk == 64 && d_v == 64) return bwd::launch_dkdv_t<64, 64, false>(tq, tk, tv, tdo, a, stream);
   if (d_qk == 128 && d_v == 128) return bwd::launch_dkdv_wide<false>(tq, tk, tv, tdo, a, stream);
   if (d_qk == 192 && d_v == 128) return bwd::launch_dkdv_t<192, 128, false>(tq, tk, tv, tdo, a, stream);
@@ -202,17 +210,17 @@ cudaError_t launch_bwd_dq_merge(const BwdArgs& a, int d_qk, cudaStream_t stream)
 }
 
 cudaError_t launch_bwd_zero(const BwdArgs& a, int d_qk, int d_v, bool zero_dq, bool zero_dkdv, cudaStream_t stream) {
-  auto go = [&](void* p, int64_t sb, int64_t sn, int64_t sh, int nrows, int d) -> cudaError_t {
-    const int64_t total = static_cast<int64_t>(a.batch) * nrows * a.heads;
+  auto go = [&](void* p, int64_t sb, int64_t sn, int64_t sh, int nrows, int heads, int d) -> cudaError_t {
+    const int64_t total = static_cast<int64_t>(a.batch) * nrows * heads;
     if (total == 0) return cudaSuccess;
     const int blocks = static_cast<int>(total / 256 + 1 < 4096 ? total / 256 + 1 : 4096);
-    bwd::zero_kernel<<<blocks, 256, 0, stream>>>(p, sb, sn, sh, a.batch, nrows, a.heads, d);
+    bwd::zero_kernel<<<blocks, 256, 0, stream>>>(p, sb, sn, sh, a.batch, nrows, heads, d);
     return cudaGetLastError();
   };
   cudaError_t e = cudaSuccess;
-  if (zero_dq) e = go(a.dq, a.dq_sb, a.dq_sn, a.dq_sh, a.seqlen_q, d_qk);
-  if (e == cudaSuccess && zero_dkdv) e = go(a.dk, a.dk_sb, a.dk_sn, a.dk_sh, a.seqlen_k, d_qk);
-  if (e == cudaSuccess && zero_dkdv) e = go(a.dv, a.dv_sb, a.dv_sn, a.dv_sh, a.seqlen_k, d_v);
+  if (zero_dq) e = go(a.dq, a.dq_sb, a.dq_sn, a.dq_sh, a.seqlen_q, a.heads, d_qk);
+  if (e == cudaSuccess && zero_dkdv) e = go(a.dk, a.dk_sb, a.dk_sn, a.dk_sh, a.seqlen_k, a.heads_kv, d_qk);
+  if (e == cudaSuccess && zero_dkdv) e = go(a.dv, a.dv_sb, a.dv_sn, a.dv_sh, a.seqlen_k, a.heads_kv, d_v);
   return e;
 }
 

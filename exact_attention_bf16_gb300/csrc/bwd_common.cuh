@@ -41,9 +41,10 @@ __device__ __forceinline__ Unit unit_bounds(const BwdArgs& a, int unit) {
 // (unit, head), blocks in descending (dQ: the last query blocks are the
 // heaviest under the causal mask) or ascending (dK/dV: the first key blocks)
 // order. Returns false for an empty list entry (the CTA has no work).
+// heads, groups: heads per unit and dispatch groups (the dK/dV kernels run over K/V heads).
 // slot: the work item (blockIdx.x unless the kernel launches several CTAs per item).
 __device__ __forceinline__ bool bwd_work(const BwdArgs& a, const TileEntry* tiles, int nblk, bool descending,
-                                         Unit& U, int& h, int& blk, int slot = -1) {
+                                         Unit& U, int& h, int& blk, int heads, int groups, int slot = -1) {
   if (slot < 0) slot = static_cast<int>(blockIdx.x);
   if (tiles != nullptr) {
     const int4* te = reinterpret_cast<const int4*>(tiles + slot);
@@ -54,11 +55,11 @@ __device__ __forceinline__ bool bwd_work(const BwdArgs& a, const TileEntry* tile
     blk = t1.y;
     return true;
   }
-  const GridSlot g = grid_slot(slot, a.num_units * a.heads, nblk, a.n_groups);
+  const GridSlot g = grid_slot(slot, a.num_units * heads, nblk, groups);
   const int bh = g.pair;
   blk = descending ? nblk - 1 - g.rank : g.rank;
-  h = bh % a.heads;
-  U = unit_bounds(a, bh / a.heads);
+  h = bh % heads;
+  U = unit_bounds(a, bh / heads);
   return true;
 }
 

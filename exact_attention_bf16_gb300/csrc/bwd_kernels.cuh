@@ -146,7 +146,12 @@ __device__ __forceinline__ bool sem_wait(const int* sem, int target, uint32_t* s
 
 // SPARSE: the key block's query tiles are those of the query blocks in its
 // transposed block-sparse list (a.q_index), not m_begin .. m_end - 1.
-template <int DQK, int DV, bool SPARSE = false, int MOD = 0, bool FUSED = false>
+//
+// GQA (shared K/V heads; both dK/dV kernels): the CTA's head h is a K/V head and
+// the loop runs over the query tiles of its a.kv_group query heads, one head
+// after another, so that the sums over them stay in the same TMEM accumulators:
+// K and V are read once for the whole group, and no partial gradient leaves the SM.
+template <int DQK, int DV, bool SPARSE = false, int MOD = 0, bool FUSED = false, bool GQA = false>
 __global__ void __launch_bounds__(kThreads, 1)
     dkdv_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUtensorMap tmk,
                 const __grid_constant__ CUtensorMap tmv, const __grid_constant__ CUtensorMap tmdo, const BwdArgs a) {
@@ -168,7 +173,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   int h, n;
   // FUSED with semaphores: key tiles in descending order, the shortest (fewest
   // query tiles under the causal mask) first, matching the adds' order below
-  if (!bwd_work(a, a.tiles_kv, a.n_kblk, FUSED && a.dq_sem != nullptr, U, h, n)) return;
+  if (!bwd_work(a, a.tiles_kv, a.n_kblk, FUSED && a.dq_sem != nullptr, U, h, n, a.heads_kv, a.n_groups_kv)) return;
   const int k0 = n * KB;
   if (k0 >= U.nk) return;
   int m_begin = 0;
@@ -182,6 +187,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int64_t kv_list = SPARSE ? (a.lists_per_head ? (static_cast<int64_t>(U.b) * a.heads + h) * a.n_kblk : 0) + n
                                  : 0;
   if constexpr (SPARSE) T = __ldg(a.q_count + kv_list) * (256 / QB);
+  const int T1 = T;  // GQA: steps of one query head
+  if constexpr (GQA) T *= a.kv_group;
   // first query row of step t
   auto q_row = [&](int t) -> int {
     if constexpr (SPARSE) {
@@ -231,10 +238,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     // of their own (the slot is recycled only after dV, dK of that tile ran).
     int issued = 0;
     bool ok = true;
+    int tt = 0, hq = GQA ? h * a.kv_group : h;  // step within the query head hq
     for (int t = 0; t < T && ok; ++t) {
       const int st = t % C::NST;
       const uint32_t use = static_cast<uint32_t>(t / C::NST);
-      const int tile = q_row(t);
+      const int tile = q_row(GQA ? tt : t);
       // fetch the vectors first, so their latency overlaps the wait for the slot
       float nl[QB / 32], nd[QB / 32];
 #pragma unroll
@@ -243,7 +251,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         nl[u] = -INFINITY;  // rows past the end: P = 0
         nd[u] = 0.f;
         if (tile + r < U.nq) {
-          const int64_t idx = U.b * a.lse_sb + h * a.lse_sh + U.q_start + tile + r;
+          const int64_t idx = U.b * a.lse_sb + hq * a.lse_sh + U.q_start + tile + r;
           const float l = a.lse[idx];
           nl[u] = (l == -INFINITY) ? -INFINITY : -l * 1.4426950408889634f;  // P = 2^(S * scale * log2e + nl)
           nd[u] = -a.dsum[idx];
@@ -255,9 +263,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint8_t* dst = sST + st * C::STAGE;
         const int row = U.q_start + tile;
         mbar_arrive_expect_tx(&bar->st_full[st], C::STAGE);
-        for (int c = 0; c < C::QCH; ++c) tma_load_4d(dst + c * QB * 128, &tmq, &bar->st_full[st], c * 64, h, row, U.b);
+        for (int c = 0; c < C::QCH; ++c) tma_load_4d(dst + c * QB * 128, &tmq, &bar->st_full[st], c * 64, hq, row, U.b);
         for (int c = 0; c < C::VCH; ++c)
-          tma_load_4d(dst + C::QT_BYTES + c * QB * 128, &tmdo, &bar->st_full[st], c * 64, h, row, U.b);
+          tma_load_4d(dst + C::QT_BYTES + c * QB * 128, &tmdo, &bar->st_full[st], c * 64, hq, row, U.b);
       }
       float* vec = sVec + st * 2 * QB;
 #pragma unroll
@@ -267,6 +275,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       mbar_arrive(&bar->st_full[st]);
       ++issued;
+      if constexpr (GQA) {
+        if (++tt == T1) tt = 0, ++hq;
+      }
     }
     if (lane == 0) {
       if (!ok)
@@ -377,7 +388,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int i_vis = a.causal ? kj - (U.nk - U.nq) : -0x40000000;
     const bool key_ok = kj < U.nk;
     const float sl2 = a.scale_log2;
-    const float alibi_slope = MOD == kModAlibi ? __ldg(a.alibi_slopes + h) * a.inv_scale : 0.f;  // raw units
+    int tt = 0, hq = GQA ? h * a.kv_group : h;  // step within the query head hq
+    float alibi_slope = MOD == kModAlibi ? __ldg(a.alibi_slopes + hq) * a.inv_scale : 0.f;  // raw units
     const uint32_t my_cols = C::tS + 32 * wg;     // this warpgroup's S^T columns
     const uint32_t my_pds = C::tPdS + 32 * wg;    // its P^T (16) and dS^T (16) columns
     bool ok = mbar_wait_warp(&bar->kv_full, 0, a.status, 0x1301);
@@ -432,7 +444,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       return good;
     };
     for (int t = 0; t < T && ok; ++t) {
-      const int q0 = q_row(t);
+      const int q0 = q_row(GQA ? tt : t);
       ok = mbar_wait_warp(&bar->s_full, static_cast<uint32_t>(t) & 1u, a.status, 0x1300);
       // this tile's (-LSE*log2e, -D) vectors, written by the loader lanes
       if (ok) ok = mbar_wait_warp(&bar->st_full[t % C::NST], static_cast<uint32_t>(t / C::NST) & 1u, a.status, 0x1302);
@@ -513,6 +525,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&bar->ds_full);
+      if constexpr (GQA) {
+        if (++tt == T1) {
+          tt = 0, ++hq;
+          if (MOD == kModAlibi && t + 1 < T) alibi_slope = __ldg(a.alibi_slopes + hq) * a.inv_scale;
+        }
+      }
       if constexpr (FUSED) {
         if (t > 0) ok = reduce_dq(qv, q_row(t - 1)) && ok;
       }
@@ -624,7 +642,7 @@ __device__ __forceinline__ int vec_slot(int q) {
   return (q & 64) + ((r & 3) * 4 + c) * 4 + (r >> 2) * 2 + j;
 }
 
-template <bool SPARSE = false, int MOD = 0>
+template <bool SPARSE = false, int MOD = 0, bool GQA = false>
 __global__ void __launch_bounds__(kThreads, 1)
     dkdv_wide_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUtensorMap tmk,
                      const __grid_constant__ CUtensorMap tmv, const __grid_constant__ CUtensorMap tmdo, const BwdArgs a) {
@@ -645,7 +663,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   // same work order as dkdv_kernel: (unit, head) slow, key tile 0 (the heaviest under causal) first
   Unit U;
   int h, n;
-  if (!bwd_work(a, a.tiles_kv, a.n_kblk, false, U, h, n)) return;
+  if (!bwd_work(a, a.tiles_kv, a.n_kblk, false, U, h, n, a.heads_kv, a.n_groups_kv)) return;
   const int k0 = n * KB;
   if (k0 >= U.nk) return;
   int m_begin = 0;
@@ -659,6 +677,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int64_t kv_list = SPARSE ? (a.lists_per_head ? (static_cast<int64_t>(U.b) * a.heads + h) * a.n_kblk : 0) + n
                                  : 0;
   if constexpr (SPARSE) T = __ldg(a.q_count + kv_list) * (256 / QB);
+  const int T1 = T;  // GQA: steps of one query head
+  if constexpr (GQA) T *= a.kv_group;
   // first query row of step t
   auto q_row = [&](int t) -> int {
     if constexpr (SPARSE) {
@@ -713,8 +733,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     // 128 (-LSE*log2e, -D) pairs into the vector ring and arrives on its barrier.
     int nq_issued = 0, ng_issued = 0;
     bool ok = true;
+    int tt = 0, hq = GQA ? h * a.kv_group : h;  // step within the query head hq
     for (int t = 0; t < T && ok; ++t) {
-      const int tile = q_row(t);
+      const int tile = q_row(GQA ? tt : t);
       const int row = U.q_start + tile;
       float nl[QB / 32], nd[QB / 32];  // fetched first, so their latency overlaps the waits below
 #pragma unroll
@@ -723,7 +744,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         nl[u] = -INFINITY;  // rows past the end: P = 0
         nd[u] = 0.f;
         if (tile + r < U.nq) {
-          const int64_t idx = U.b * a.lse_sb + h * a.lse_sh + U.q_start + tile + r;
+          const int64_t idx = U.b * a.lse_sb + hq * a.lse_sh + U.q_start + tile + r;
           const float l = a.lse[idx];
           nl[u] = (l == -INFINITY) ? -INFINITY : -l * 1.4426950408889634f;  // P = 2^(S * scale * log2e + nl)
           nd[u] = -a.dsum[idx];
@@ -735,7 +756,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lane == 0) {
         mbar_arrive_expect_tx(&bar->q_full[qs], C::TILE);
         for (int c = 0; c < 2; ++c)
-          tma_load_4d(sQ + qs * C::TILE + c * QB * 128, &tmq, &bar->q_full[qs], c * 64, h, row, U.b);
+          tma_load_4d(sQ + qs * C::TILE + c * QB * 128, &tmq, &bar->q_full[qs], c * 64, hq, row, U.b);
       }
       ++nq_issued;
       ok = mbar_wait(&bar->g_empty[gs], (static_cast<uint32_t>(t / C::NG) & 1u) ^ 1u, a.status, 0x1408 + gs);
@@ -743,7 +764,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lane == 0) {
         mbar_arrive_expect_tx(&bar->g_full[gs], C::TILE);
         for (int c = 0; c < 2; ++c)
-          tma_load_4d(sG + gs * C::TILE + c * QB * 128, &tmdo, &bar->g_full[gs], c * 64, h, row, U.b);
+          tma_load_4d(sG + gs * C::TILE + c * QB * 128, &tmdo, &bar->g_full[gs], c * 64, hq, row, U.b);
       }
       ++ng_issued;
       ok = mbar_wait(&bar->v_empty[vs], (static_cast<uint32_t>(t / C::NVEC) & 1u) ^ 1u, a.status, 0x1410 + vs);
@@ -756,6 +777,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         vec[QB + p] = nd[u];
       }
       mbar_arrive(&bar->v_full[vs]);
+      if constexpr (GQA) {
+        if (++tt == T1) tt = 0, ++hq;
+      }
     }
     if (lane == 0) {
       if (!ok) {  // let the copies in flight land before the CTA exits
@@ -871,11 +895,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     const bool all_keys = kok[0][0] && kok[0][1] && kok[1][0] && kok[1][1];
     const int vis_max = max(max(vis[0][0], vis[0][1]), max(vis[1][0], vis[1][1]));
     const float2 sl2v = make_float2(a.scale_log2, a.scale_log2);
-    const float alibi_slope = MOD == kModAlibi ? __ldg(a.alibi_slopes + h) * a.inv_scale : 0.f;  // raw units
+    int tt = 0, hq = GQA ? h * a.kv_group : h;  // step within the query head hq
+    float alibi_slope = MOD == kModAlibi ? __ldg(a.alibi_slopes + hq) * a.inv_scale : 0.f;  // raw units
     auto lanes = [&](int lg) { return tbase + ((quarter * 32u + 16u * static_cast<uint32_t>(lg)) << 16); };
     bool ok = true;
     for (int t = 0; t < T && ok; ++t) {
-      const int q0 = q_row(t) + 64 * wg;  // this warpgroup's first query
+      const int q0 = q_row(GQA ? tt : t) + 64 * wg;  // this warpgroup's first query
       const uint32_t col = region(t) + 64 * wg;
       // ---- phase A: P from S^T(t), written over S^T(t) as bf16 P^T
       ok = mbar_wait_warp(&bar->s_full, static_cast<uint32_t>(t) & 1u, a.status, 0x1430) &&
@@ -984,6 +1009,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lane == 0) {
         mbar_arrive(&bar->ds_full);
         mbar_arrive(&bar->v_empty[t % C::NVEC]);
+      }
+      if constexpr (GQA) {
+        if (++tt == T1) {
+          tt = 0, ++hq;
+          if (MOD == kModAlibi && t + 1 < T) alibi_slope = __ldg(a.alibi_slopes + hq) * a.inv_scale;
+        }
       }
     }
     // ---- epilogue: warpgroup 0 writes dV, warpgroup 1 writes scale * dK (one key row per thread)
@@ -1107,7 +1138,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   // split keys (dense, no block lists): range `split` of this query tile's key blocks
   const bool split = !SPARSE && a.dq_split > 1;
   const int range = split ? static_cast<int>(blockIdx.x % static_cast<unsigned>(a.dq_split)) : 0;
-  if (!bwd_work(a, a.tiles_q, a.n_qblk, true, U, h, m,
+  if (!bwd_work(a, a.tiles_q, a.n_qblk, true, U, h, m, a.heads, a.n_groups,
                 split ? static_cast<int>(blockIdx.x / static_cast<unsigned>(a.dq_split)) : -1))
     return;
   const int q0 = m * MB;
@@ -1174,6 +1205,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tma_load_4d(sQ + c * MB * 128, &tmq, &bar->q_full, c * 64, h, U.q_start + q0, U.b);
       for (int c = 0; c < C::VCH; ++c)
         tma_load_4d(sdO + c * MB * 128, &tmdo, &bar->q_full, c * 64, h, U.q_start + q0, U.b);
+      const int hk = h / a.kv_group;  // the K/V head of this query head
       int nk_issued = 0, nv_issued = 0;
       bool ok = true;
       for (int t = 0; t < T && ok; ++t) {
@@ -1183,13 +1215,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!ok) break;
         mbar_arrive_expect_tx(&bar->k_full[ks], C::K_BYTES);
         for (int c = 0; c < C::QCH; ++c)
-          tma_load_4d(sKr + ks * C::K_BYTES + c * KB * 128, &tmk, &bar->k_full[ks], c * 64, h, row, U.b);
+          tma_load_4d(sKr + ks * C::K_BYTES + c * KB * 128, &tmk, &bar->k_full[ks], c * 64, hk, row, U.b);
         ++nk_issued;
         ok = mbar_wait(&bar->v_empty[vs], (static_cast<uint32_t>(t / C::VST) & 1u) ^ 1u, a.status, 0x2108 + vs);
         if (!ok) break;
         mbar_arrive_expect_tx(&bar->v_full[vs], C::V_BYTES);
         for (int c = 0; c < C::VCH; ++c)
-          tma_load_4d(sVr + vs * C::V_BYTES + c * KB * 128, &tmv, &bar->v_full[vs], c * 64, h, row, U.b);
+          tma_load_4d(sVr + vs * C::V_BYTES + c * KB * 128, &tmv, &bar->v_full[vs], c * 64, hk, row, U.b);
         ++nv_issued;
       }
       if (!ok) {  // let the copies in flight land before the CTA exits
@@ -1513,31 +1545,34 @@ cudaError_t set_smem(K kern, int bytes) {
   return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
 }
 
-template <int DQK, int DV, bool SPARSE, int MOD = 0, bool FUSED = false>
+template <int DQK, int DV, bool SPARSE, int MOD = 0, bool FUSED = false, bool GQA = false>
 cudaError_t launch_dkdv_t(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const CUtensorMap& tdo,
                           const BwdArgs& a, cudaStream_t stream) {
   using C = DkdvCfg<DQK, DV, FUSED>;
-  auto kern = dkdv_kernel<DQK, DV, SPARSE, MOD, FUSED>;
+  if (GQA != (a.kv_group > 1)) return cudaErrorInvalidValue;
+  auto kern = dkdv_kernel<DQK, DV, SPARSE, MOD, FUSED, GQA>;
   static PerDeviceOnce once;
   cudaError_t e = once.run([&] { return set_smem(kern, C::SMEM); });
   if (e != cudaSuccess) return e;
-  const int64_t grid = a.tiles_kv ? a.n_tiles_kv : static_cast<int64_t>(a.n_kblk) * a.num_units * a.heads;
+  const int64_t grid = a.tiles_kv ? a.n_tiles_kv : static_cast<int64_t>(a.n_kblk) * a.num_units * a.heads_kv;
   if (grid <= 0) return cudaSuccess;
   if (grid > 0x7fffffff) return cudaErrorInvalidConfiguration;
   kern<<<static_cast<unsigned>(grid), kThreads, C::SMEM, stream>>>(tq, tk, tv, tdo, a);
   return cudaGetLastError();
 }
 
-template <bool SPARSE, int MOD = 0>
+template <bool SPARSE, int MOD = 0, bool GQA = false>
 cudaError_t launch_dkdv_wide(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                              const CUtensorMap& tdo, const BwdArgs& a, cudaStream_t stream) {
+  if (GQA != (a.kv_group > 1)) return cudaErrorInvalidValue;
   static PerDeviceOnce once;
-  cudaError_t e = once.run([] { return set_smem(dkdv_wide_kernel<SPARSE, MOD>, DkdvWCfg::SMEM); });
+  cudaError_t e = once.run([] { return set_smem(dkdv_wide_kernel<SPARSE, MOD, GQA>, DkdvWCfg::SMEM); });
   if (e != cudaSuccess) return e;
-  const int64_t grid = a.tiles_kv ? a.n_tiles_kv : static_cast<int64_t>(a.n_kblk) * a.num_units * a.heads;
+  const int64_t grid = a.tiles_kv ? a.n_tiles_kv : static_cast<int64_t>(a.n_kblk) * a.num_units * a.heads_kv;
   if (grid <= 0) return cudaSuccess;
   if (grid > 0x7fffffff) return cudaErrorInvalidConfiguration;
-  dkdv_wide_kernel<SPARSE, MOD><<<static_cast<unsigned>(grid), kThreads, DkdvWCfg::SMEM, stream>>>(tq, tk, tv, tdo, a);
+  dkdv_wide_kernel<SPARSE, MOD, GQA>
+      <<<static_cast<unsigned>(grid), kThreads, DkdvWCfg::SMEM, stream>>>(tq, tk, tv, tdo, a);
   return cudaGetLastError();
 }
 

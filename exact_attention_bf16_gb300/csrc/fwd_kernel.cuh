@@ -267,7 +267,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int kb0 = key_block(0);
           mbar_arrive_expect_tx(&bar->kv_full[0], C::K_BYTES);
           for (int c = 0; c < C::QCH; ++c)
-            tma_load_4d(sKV + c * kChunk, &tmk, &bar->kv_full[0], c * C::QX, h, k_start + kb0 * BN, b);
+            tma_load_4d(sKV + c * kChunk, &tmk, &bar->kv_full[0], c * C::QX, h / a.kv_group, k_start + kb0 * BN, b);
         }
       }
     }
@@ -295,6 +295,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       tma_prefetch_desc(&tmk);
+      const int hk = h / a.kv_group;  // the K/V head of this query head
       // read while the Q copies fly: V from the fp16 copy, or the bf16 original
       const CUtensorMap* tmvv = v_is_f16(a) ? &tmv16 : &tmv;
       tma_prefetch_desc(tmvv);
@@ -318,11 +319,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           if ((u & 1) == 0) {
             mbar_arrive_expect_tx(&bar->kv_full[slot], C::K_BYTES);
             for (int c = 0; c < C::QCH; ++c)
-              tma_load_4d(dst + c * kChunk, &tmk, &bar->kv_full[slot], c * C::QX, h, k_start + kb * BN, b);
+              tma_load_4d(dst + c * kChunk, &tmk, &bar->kv_full[slot], c * C::QX, hk, k_start + kb * BN, b);
           } else {
             mbar_arrive_expect_tx(&bar->kv_full[slot], C::V_BYTES);
             for (int c = 0; c < C::VCH; ++c)
-              tma_load_4d(dst + c * kChunk, tmvv, &bar->kv_full[slot], c * 64, h, k_start + kb * BN, b);
+              tma_load_4d(dst + c * kChunk, tmvv, &bar->kv_full[slot], c * 64, hk, k_start + kb * BN, b);
           }
           last_use[slot] = static_cast<int>(use);
         }
@@ -347,11 +348,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (which == 0) {
               mbar_arrive_expect_tx(&bar->kv_full[slot], C::K_BYTES);
               for (int c = 0; c < C::QCH; ++c)
-                tma_load_4d(dst + c * kChunk, &tmk, &bar->kv_full[slot], c * C::QX, h, k_start + kb * BN, b);
+                tma_load_4d(dst + c * kChunk, &tmk, &bar->kv_full[slot], c * C::QX, hk, k_start + kb * BN, b);
             } else {
               mbar_arrive_expect_tx(&bar->kv_full[slot], C::V_BYTES);
               for (int c = 0; c < C::VCH; ++c)
-                tma_load_4d(dst + c * kChunk, tmvv, &bar->kv_full[slot], c * 64, h, k_start + kb * BN, b);
+                tma_load_4d(dst + c * kChunk, tmvv, &bar->kv_full[slot], c * 64, hk, k_start + kb * BN, b);
             }
             ++issued;
           }

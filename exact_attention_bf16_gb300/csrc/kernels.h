@@ -160,6 +160,7 @@ struct FwdArgs {
   float* o_part;
   float* lse_part;
   int64_t part_rows;
+  int kv_group;              // query heads per K/V head: head h reads K/V head h / kv_group
 };
 
 cudaError_t launch_fwd(int d_qk, int d_v, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
@@ -266,6 +267,11 @@ struct BwdArgs {
   int dq_split;
   int dq_kb_per_split;
   float* dq_part;
+  // Shared K/V heads: query head h reads K/V head h / kv_group; heads_kv =
+  // heads / kv_group. The dK/dV launches run over K/V heads, in n_groups_kv
+  // dispatch groups of grid_slot.
+  int kv_group, heads_kv;
+  int n_groups_kv;
 };
 
 // Single-pass backward (d_qk = d_v = 64): dK, dV and the fp32 dQ partials of

@@ -63,7 +63,7 @@
 extern "C" {
 #endif
 
-#define ATTN_ABI_VERSION 5
+#define ATTN_ABI_VERSION 6
 
 typedef enum {
   ATTN_OK = 0,
@@ -185,6 +185,15 @@ typedef struct attn_fwd_params {
    * then launches from the block index (no tile list). The default (0) is
    * the one-SM kernel, the faster of the two on GB300. */
   int32_t cta_pair;
+  /* Heads of k and v (and of dK and dV): 0 or `heads` gives every query head
+   * its own; a divisor of `heads` (else ATTN_ERR_INVALID_ARG) shares each K/V
+   * head among heads / heads_kv consecutive query heads, query head h reading
+   * K/V head h / (heads / heads_kv). dK and dV are then the sums over the
+   * query heads that share them, accumulated in fp32 and rounded once. Shared
+   * heads work with the dense and the variable-length forward and backward,
+   * score modifications, E4M3 inputs and split keys; cta_pair, single_pass,
+   * the block-sparse pair and the diagnostic give ATTN_ERR_UNSUPPORTED. */
+  int32_t heads_kv;
 } attn_fwd_params;
 
 /* Backward parameters. `fwd` holds q, k, v, the forward's outputs o and lse

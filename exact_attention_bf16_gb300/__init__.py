@@ -12,12 +12,13 @@ from __future__ import annotations
 
 import ctypes
 import math
-from typing import Optional, Tuple
+from typing import Optional, Tuple, Union
 
 import torch
 
 from . import _abi
-from ._abi import AttnBwdParams, AttnError, AttnFwdParams  # noqa: F401
+from ._abi import (AttnBwdParams, AttnError, AttnFwdParams, AttnKvAppendParams, AttnKvPlanParams,  # noqa: F401
+                   AttnPagedParams)
 
 _lib = _abi.load()
 
@@ -26,7 +27,7 @@ SUPPORTED_HEAD_DIMS = ((64, 64), (128, 128), (192, 128))
 __all__ = [
     "attn_fwd", "attn_fwd_block_sparse", "attn_fwd_varlen", "attn_bwd", "attn_bwd_block_sparse",
     "block_lists_from_mask", "attn_bwd_varlen", "attn_exp2_eval",
-    "attn_get_device_status", "attention", "attention_varlen", "AttnError", "SUPPORTED_HEAD_DIMS", "library_path",
+    "attn_kv_plan", "attn_kv_append", "attn_fwd_paged", "attn_get_device_status", "attention", "attention_varlen", "AttnError", "SUPPORTED_HEAD_DIMS", "library_path",
 ]
 
 
@@ -444,6 +445,176 @@ def attn_bwd_varlen(q, k, v, out, lse, dout, cu_seqlens_q, cu_seqlens_k, max_seq
     ws, nbytes = _workspace(_lib.attn_bwd_workspace_size(ctypes.byref(p)), q.device, stream)
     _abi.check(_lib.attn_bwd_varlen(ctypes.byref(p), _ptr(ws), nbytes, _stream(stream, q.device)), "attn_bwd_varlen")
     return dq, dk, dv
+
+
+def _check_ints(device, **arrays):
+    """int32 arrays of a paged-cache call: (tensor, shape), contiguous on `device`; None in a shape leaves it free."""
+    for n, (t, shape) in arrays.items():
+        if not isinstance(t, torch.Tensor) or t.dtype != torch.int32 or not t.is_cuda or not t.is_contiguous():
+            raise ValueError(f"{n} must be a contiguous int32 CUDA tensor")
+        if t.device != device:
+            raise ValueError(f"{n} is on {t.device} but the call is on {device}")
+        if t.dim() != len(shape) or any(w is not None and w != g for w, g in zip(shape, t.shape)):
+            raise ValueError(f"{n} must have shape {shape}, got {tuple(t.shape)}")
+
+
+def _check_table(t, device, num_seqs):
+    if not isinstance(t, torch.Tensor) or t.dtype != torch.int32 or not t.is_cuda or t.dim() != 2:
+        raise ValueError("block_table must be an int32 CUDA tensor [requests, max_pages]")
+    if t.device != device:
+        raise ValueError(f"block_table is on {t.device} but the call is on {device}")
+    if t.shape[0] != num_seqs or t.shape[1] < 1 or t.stride(1) != 1 or (num_seqs > 1 and t.stride(0) < t.shape[1]):
+        raise ValueError(f"block_table must be [{num_seqs}, max_pages] with contiguous rows that do not overlap, got "
+                         f"{tuple(t.shape)} with strides {t.stride()}")
+    return max(t.stride(0), t.shape[1])
+
+
+def attn_kv_plan(seqlens_old: torch.Tensor, seqlens_new: torch.Tensor, block_table: torch.Tensor,
+                 free_pages: torch.Tensor, free_count: torch.Tensor, page_size: int,
+                 slot_mapping: Union[torch.Tensor, int], *, cu_seqlens_q: Optional[torch.Tensor] = None,
+                 seqlens_k: Optional[torch.Tensor] = None, free_count_out: Optional[torch.Tensor] = None,
+                 status: Optional[torch.Tensor] = None, stream=None):
+    """Plans one step of a paged KV cache on the GPU (include/attn.h, attn_kv_plan): pages for every request's
+    new tokens, and their slots. Request s holds ``seqlens_old[s]`` tokens and adds ``seqlens_new[s]`` (negative:
+    it ends and returns its pages); its pages are listed in row s of ``block_table`` [requests, max_pages], and free
+    ones on the stack ``free_pages[:free_count]``. The table, the stack and ``free_count`` (or ``free_count_out``,
+    when given) are updated. ``slot_mapping`` is an int64 tensor, or the number of entries of one to make; entries
+    past the step's tokens become -1. All other arrays are int32.
+    Returns (cu_seqlens_q [requests + 1], seqlens_k [requests], slot_mapping, status [1]): status 0, or 1 (too few
+    free pages), 2 (a row of the table is too short), 3 (slot_mapping is), 4 (free_pages is), and then nothing is
+    changed and the step holds no tokens."""
+    n = seqlens_old.numel() if isinstance(seqlens_old, torch.Tensor) else 0
+    dev = seqlens_old.device if isinstance(seqlens_old, torch.Tensor) else None
+    _check_ints(dev, seqlens_old=(seqlens_old, (n,)), seqlens_new=(seqlens_new, (n,)), free_pages=(free_pages, (None,)),
+                free_count=(free_count, (1,)))
+    if n < 1:
+        raise ValueError("attn_kv_plan needs at least one request")
+    table_stride = _check_table(block_table, dev, n)
+
+    def given(t, shape, dtype=torch.int32):
+        if t is None:
+            t = torch.empty(shape, dtype=dtype, device=dev)
+            _used_on(stream, t)
+        return t
+
+    cu_seqlens_q, seqlens_k, status = given(cu_seqlens_q, (n + 1,)), given(seqlens_k, (n,)), given(status, (1,))
+    free_count_out = free_count if free_count_out is None else free_count_out
+    _check_ints(dev, cu_seqlens_q=(cu_seqlens_q, (n + 1,)), seqlens_k=(seqlens_k, (n,)), status=(status, (1,)),
+                free_count_out=(free_count_out, (1,)))
+    if isinstance(slot_mapping, int):
+        slot_mapping = given(None, (slot_mapping,), torch.int64)
+    if slot_mapping.dtype != torch.int64 or slot_mapping.dim() != 1 or not slot_mapping.is_contiguous() or \
+            slot_mapping.device != dev:
+        raise ValueError(f"slot_mapping must be a contiguous int64 tensor [max_tokens] on {dev}")
+    p = AttnKvPlanParams()
+    p.seqlens_old, p.seqlens_new, p.block_table = _ptr(seqlens_old), _ptr(seqlens_new), _ptr(block_table)
+    p.block_table_stride = table_stride
+    p.free_pages, p.free_count, p.free_count_out = _ptr(free_pages), _ptr(free_count), _ptr(free_count_out)
+    p.cu_seqlens_q, p.seqlens_k, p.slot_mapping, p.status = (_ptr(cu_seqlens_q), _ptr(seqlens_k), _ptr(slot_mapping),
+                                                             _ptr(status))
+    p.num_seqs, p.max_pages, p.page_size = n, block_table.shape[1], int(page_size)
+    p.free_capacity, p.max_tokens = free_pages.numel(), slot_mapping.numel()
+    _abi.check(_lib.attn_kv_plan(ctypes.byref(p), _stream(stream, dev)), "attn_kv_plan")
+    return cu_seqlens_q, seqlens_k, slot_mapping, status
+
+
+def _check_caches(k_cache, v_cache, device, heads_kv=None):
+    _check_bf16("k_cache", k_cache, 4)
+    _check_bf16("v_cache", v_cache, 4)
+    if k_cache.shape[:3] != v_cache.shape[:3] or (heads_kv is not None and k_cache.shape[2] != heads_kv):
+        raise ValueError(f"k_cache {tuple(k_cache.shape)} and v_cache {tuple(v_cache.shape)} must be [pages, page_size, "
+                         f"{'heads' if heads_kv is None else heads_kv}, d]")
+    for n, t in (("k_cache", k_cache), ("v_cache", v_cache)):
+        if t.device != device:
+            raise ValueError(f"{n} is on {t.device} but the call is on {device}")
+
+
+def _row_strides(t: torch.Tensor):
+    """Element strides of all but the last dim; a dim of one element may carry any stride and gets a valid one."""
+    return tuple(s if n > 1 else t.shape[-1] for s, n in zip(t.stride()[:-1], t.shape[:-1]))
+
+
+def attn_kv_append(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                   slot_mapping: torch.Tensor, *, stream=None) -> None:
+    """Writes new tokens' k [tokens, Hkv, d_qk] and v [tokens, Hkv, d_v] into the paged caches k_cache [pages,
+    page_size, Hkv, d_qk] and v_cache [pages, page_size, Hkv, d_v] (bf16, any strides with contiguous d): row i goes
+    to slot ``slot_mapping[i]`` (int64; page slot // page_size, row slot % page_size). Slots outside the cache, as -1,
+    write nothing; slots must differ."""
+    _check_bf16("k", k, 3)
+    _check_bf16("v", v, 3)
+    _check_caches(k_cache, v_cache, k.device, k.shape[1])
+    if v.shape[:2] != k.shape[:2] or v.device != k.device:
+        raise ValueError(f"shape or device mismatch k{tuple(k.shape)} v{tuple(v.shape)}")
+    if k_cache.shape[3] != k.shape[2] or v_cache.shape[3] != v.shape[2]:
+        raise ValueError(f"k_cache {tuple(k_cache.shape)} and v_cache {tuple(v_cache.shape)} do not hold rows of "
+                         f"{k.shape[2]} and {v.shape[2]}")
+    if slot_mapping.dtype != torch.int64 or slot_mapping.shape != (k.shape[0],) or not slot_mapping.is_contiguous() or \
+            slot_mapping.device != k.device:
+        raise ValueError(f"slot_mapping must be a contiguous int64 tensor [{k.shape[0]}] on {k.device}")
+    p = AttnKvAppendParams()
+    p.k, p.v, p.k_cache, p.v_cache, p.slot_mapping = (_ptr(k), _ptr(v), _ptr(k_cache), _ptr(v_cache),
+                                                      _ptr(slot_mapping))
+    p.k_row_stride, p.k_head_stride = _row_strides(k)
+    p.v_row_stride, p.v_head_stride = _row_strides(v)
+    p.k_cache_page_stride, p.k_cache_row_stride, p.k_cache_head_stride = _row_strides(k_cache)
+    p.v_cache_page_stride, p.v_cache_row_stride, p.v_cache_head_stride = _row_strides(v_cache)
+    p.tokens, p.heads_kv, p.d_qk, p.d_v = k.shape[0], k.shape[1], k.shape[2], v.shape[2]
+    p.page_size, p.num_pages = k_cache.shape[1], k_cache.shape[0]
+    _abi.check(_lib.attn_kv_append(ctypes.byref(p), _stream(stream, k.device)), "attn_kv_append")
+
+
+def attn_fwd_paged(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, block_table: torch.Tensor,
+                   cu_seqlens_q: torch.Tensor, seqlens_k: torch.Tensor, max_seqlen_q: int, *, causal: bool = True,
+                   softmax_scale: Optional[float] = None, softcap: Optional[float] = None,
+                   alibi_slopes: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+                   lse: Optional[torch.Tensor] = None, stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """Attention of new tokens over a paged KV cache (include/attn.h, attn_fwd_paged). q [total_q, H, d_qk] (bf16)
+    packs the requests' new tokens, request s's in rows cu_seqlens_q[s] .. cu_seqlens_q[s + 1] - 1 (one for a decoding
+    request, a chunk for a prompt, or none); its keys are the first seqlens_k[s] tokens on the pages of row s of
+    ``block_table`` [requests, max_pages], the new ones among them, in k_cache [pages, page_size, Hkv, d_qk] and
+    v_cache [pages, page_size, Hkv, d_v]; Hkv divides H. With ``causal`` (the default) query i of n sees the keys up
+    to position i + seqlens_k[s] - n. cu_seqlens_q [requests + 1], seqlens_k [requests] and the table are int32 on
+    q's GPU; ``max_seqlen_q`` bounds the queries of a request. Score modifications as in :func:`attn_fwd`.
+    Returns (O [total_q, H, d_v] bf16, LSE [H, total_q] fp32); rows behind the last request are not written."""
+    _check_bf16("q", q, 3)
+    _check_caches(k_cache, v_cache, q.device)
+    tq, H, dqk = q.shape
+    hk, dv = k_cache.shape[2], v_cache.shape[3]
+    if k_cache.shape[3] != dqk:
+        raise ValueError(f"k_cache {tuple(k_cache.shape)} does not match q {tuple(q.shape)}")
+    if hk < 1 or H % hk != 0:
+        raise ValueError(f"{hk} K/V heads do not divide {H} query heads")
+    n = seqlens_k.numel() if isinstance(seqlens_k, torch.Tensor) else 0
+    _check_ints(q.device, seqlens_k=(seqlens_k, (n,)), cu_seqlens_q=(cu_seqlens_q, (n + 1,)))
+    table_stride = _check_table(block_table, q.device, n)
+    if out is None:
+        out = torch.empty((tq, H, dv), dtype=torch.bfloat16, device=q.device)
+        _used_on(stream, out)
+    _check_bf16("out", out, 3)
+    if out.shape != (tq, H, dv) or out.device != q.device:
+        raise ValueError(f"out must be {(tq, H, dv)} on {q.device}, got {tuple(out.shape)} on {out.device}")
+    if lse is None:
+        lse = torch.empty((H, tq), dtype=torch.float32, device=q.device)
+        _used_on(stream, lse)
+    if lse.shape != (H, tq) or not lse.is_contiguous() or lse.dtype != torch.float32 or lse.device != q.device:
+        raise ValueError(f"lse must be a contiguous float32 [H, total_q] tensor on {q.device}")
+    p = AttnPagedParams()
+    p.q, p.k_cache, p.v_cache, p.o, p.lse = _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(out), _ptr(lse)
+    p.q_row_stride, p.q_head_stride = _row_strides(q)
+    p.o_row_stride, p.o_head_stride = _row_strides(out)
+    p.k_page_stride, p.k_row_stride, p.k_head_stride = _row_strides(k_cache)
+    p.v_page_stride, p.v_row_stride, p.v_head_stride = _row_strides(v_cache)
+    p.block_table, p.block_table_stride = _ptr(block_table), table_stride
+    p.cu_seqlens_q, p.seqlens_k = _ptr(cu_seqlens_q), _ptr(seqlens_k)
+    p.num_seqs, p.heads, p.heads_kv, p.d_qk, p.d_v = n, H, hk, dqk, dv
+    p.page_size, p.num_pages, p.max_pages = k_cache.shape[1], k_cache.shape[0], block_table.shape[1]
+    p.total_q, p.max_seqlen_q = tq, int(max_seqlen_q)
+    p.softmax_scale = float(softmax_scale) if softmax_scale is not None else 1.0 / math.sqrt(dqk)
+    p.causal = 1 if causal else 0
+    _set_score_mod(p, q, softcap, alibi_slopes)
+    ws, nbytes = _workspace(_lib.attn_fwd_paged_workspace_size(ctypes.byref(p)), q.device, stream)
+    _abi.check(_lib.attn_fwd_paged(ctypes.byref(p), _ptr(ws), nbytes, _stream(stream, q.device)), "attn_fwd_paged")
+    return out, lse
 
 
 def attn_exp2_eval(x: torch.Tensor, stream=None) -> Tuple[torch.Tensor, torch.Tensor]:

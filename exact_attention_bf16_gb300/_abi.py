@@ -1,5 +1,5 @@
 """ctypes view of include/attn.h: the shared library, its status codes and the
-two parameter structs. Loading fails loudly if the library is missing; there is
+parameter structs. Loading fails loudly if the library is missing; there is
 no fallback implementation."""
 from __future__ import annotations
 
@@ -62,6 +62,41 @@ class AttnBwdParams(ctypes.Structure):
     ]
 
 
+class AttnKvPlanParams(ctypes.Structure):
+    _fields_ = [
+        ("seqlens_old", c_vp), ("seqlens_new", c_vp), ("block_table", c_vp), ("block_table_stride", c_i64),
+        ("free_pages", c_vp), ("free_count", c_vp), ("free_count_out", c_vp), ("cu_seqlens_q", c_vp),
+        ("seqlens_k", c_vp), ("slot_mapping", c_vp), ("status", c_vp),
+        ("num_seqs", c_i32), ("max_pages", c_i32), ("page_size", c_i32), ("free_capacity", c_i32),
+        ("max_tokens", c_i32),
+    ]
+
+
+class AttnKvAppendParams(ctypes.Structure):
+    _fields_ = [
+        ("k", c_vp), ("v", c_vp), ("k_cache", c_vp), ("v_cache", c_vp),
+        ("k_row_stride", c_i64), ("k_head_stride", c_i64), ("v_row_stride", c_i64), ("v_head_stride", c_i64),
+        ("k_cache_page_stride", c_i64), ("k_cache_row_stride", c_i64), ("k_cache_head_stride", c_i64),
+        ("v_cache_page_stride", c_i64), ("v_cache_row_stride", c_i64), ("v_cache_head_stride", c_i64),
+        ("slot_mapping", c_vp),
+        ("tokens", c_i32), ("heads_kv", c_i32), ("d_qk", c_i32), ("d_v", c_i32), ("page_size", c_i32),
+        ("num_pages", c_i32),
+    ]
+
+
+class AttnPagedParams(ctypes.Structure):
+    _fields_ = [
+        ("q", c_vp), ("k_cache", c_vp), ("v_cache", c_vp), ("o", c_vp), ("lse", c_vp),
+        ("q_row_stride", c_i64), ("q_head_stride", c_i64), ("o_row_stride", c_i64), ("o_head_stride", c_i64),
+        ("k_page_stride", c_i64), ("k_row_stride", c_i64), ("k_head_stride", c_i64),
+        ("v_page_stride", c_i64), ("v_row_stride", c_i64), ("v_head_stride", c_i64),
+        ("block_table", c_vp), ("block_table_stride", c_i64), ("cu_seqlens_q", c_vp), ("seqlens_k", c_vp),
+        ("num_seqs", c_i32), ("heads", c_i32), ("heads_kv", c_i32), ("d_qk", c_i32), ("d_v", c_i32),
+        ("page_size", c_i32), ("num_pages", c_i32), ("max_pages", c_i32), ("total_q", c_i32), ("max_seqlen_q", c_i32),
+        ("softmax_scale", c_f32), ("causal", c_i32), ("score_mod", c_i32), ("softcap", c_f32), ("alibi_slopes", c_vp),
+    ]
+
+
 _lib = None
 
 
@@ -89,6 +124,13 @@ def load(path: str = LIB_PATH):
         "attn_bwd": (ctypes.c_int, [P(AttnBwdParams), c_vp, ctypes.c_size_t, c_vp]),
         "attn_bwd_varlen": (ctypes.c_int, [P(AttnBwdParams), c_vp, ctypes.c_size_t, c_vp]),
         "attn_bwd_noalloc": (ctypes.c_int, [P(AttnBwdParams), c_vp]),
+        "attn_kv_plan": (ctypes.c_int, [P(AttnKvPlanParams), c_vp]),
+        "attn_kv_append": (ctypes.c_int, [P(AttnKvAppendParams), c_vp]),
+        "attn_fwd_paged_workspace_size": (ctypes.c_size_t, [P(AttnPagedParams)]),
+        "attn_fwd_paged": (ctypes.c_int, [P(AttnPagedParams), c_vp, ctypes.c_size_t, c_vp]),
+        "attn_kv_plan_params_size": (ctypes.c_size_t, []),
+        "attn_kv_append_params_size": (ctypes.c_size_t, []),
+        "attn_paged_params_size": (ctypes.c_size_t, []),
         "attn_exp2_eval": (ctypes.c_int, [c_vp, c_vp, c_vp, c_i64, c_vp]),
         "attn_diag_wait_timeout": (ctypes.c_int, [P(AttnFwdParams), ctypes.c_uint32, c_vp]),
         "attn_get_device_status": (ctypes.c_int, [c_vp, P(ctypes.c_uint32)]),
@@ -105,7 +147,10 @@ def load(path: str = LIB_PATH):
     if lib.attn_abi_version() != ABI_VERSION:
         raise ImportError(f"libattn_gb300.so ABI {lib.attn_abi_version()} != binding ABI {ABI_VERSION}")
     if lib.attn_fwd_params_size() != ctypes.sizeof(AttnFwdParams) or \
-            lib.attn_bwd_params_size() != ctypes.sizeof(AttnBwdParams):
+            lib.attn_bwd_params_size() != ctypes.sizeof(AttnBwdParams) or \
+            lib.attn_kv_plan_params_size() != ctypes.sizeof(AttnKvPlanParams) or \
+            lib.attn_kv_append_params_size() != ctypes.sizeof(AttnKvAppendParams) or \
+            lib.attn_paged_params_size() != ctypes.sizeof(AttnPagedParams):
         raise ImportError("libattn_gb300.so parameter-struct layout differs from the binding")
     _lib = lib
     return lib

@@ -2,7 +2,7 @@
 // argument validation, TMA tensor-map encoding, workspace accounting and
 // kernel launches. All compute runs in the CUDA kernels (fwd_kernel.cuh and
 // bwd_kernels.cuh with the translation units that instantiate them, the pair
-// kernels, schedule.cu); this file holds host logic only.
+// kernels, attn_paged.cu, kv_cache.cu, schedule.cu); this file holds host logic only.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <cuda_runtime.h>
@@ -162,6 +162,20 @@ bool supported_dims(int dqk, int dv) {
 int kv_heads(const attn_fwd_params* p) { return p->heads_kv == 0 ? p->heads : p->heads_kv; }
 bool shared_kv(const attn_fwd_params* p) { return kv_heads(p) != p->heads; }
 
+bool scale_ok(float scale) { return std::isfinite(scale) && scale > 0.f; }
+
+attn_status_t check_scores(float scale, int32_t score_mod, float softcap, const float* alibi_slopes) {
+  if (!scale_ok(scale)) return ATTN_ERR_INVALID_ARG;
+  switch (score_mod) {
+    case ATTN_SCORE_NONE: return ATTN_OK;
+    case ATTN_SCORE_SOFTCAP:
+      return std::isfinite(softcap) && softcap > 0.f && std::isfinite(softcap / scale) ? ATTN_OK : ATTN_ERR_INVALID_ARG;
+    case ATTN_SCORE_ALIBI:
+      return alibi_slopes && !(reinterpret_cast<uintptr_t>(alibi_slopes) & 3u) ? ATTN_OK : ATTN_ERR_INVALID_ARG;
+    default: return ATTN_ERR_INVALID_ARG;
+  }
+}
+
 // Shape-level checks shared by every entry point.
 attn_status_t check_common(const attn_fwd_params* p, bool varlen) {
   if (!p) return ATTN_ERR_INVALID_ARG;
@@ -171,7 +185,7 @@ attn_status_t check_common(const attn_fwd_params* p, bool varlen) {
   }
   if (p->heads < 1) return ATTN_ERR_INVALID_ARG;
   if (p->heads_kv < 0 || p->heads % kv_heads(p) != 0) return ATTN_ERR_INVALID_ARG;
-  if (!(std::isfinite(p->softmax_scale) && p->softmax_scale > 0.f)) return ATTN_ERR_INVALID_ARG;
+  if (!scale_ok(p->softmax_scale)) return ATTN_ERR_INVALID_ARG;
   if (varlen) {
     if (!p->cu_seqlens_q || !p->cu_seqlens_k) return ATTN_ERR_INVALID_ARG;
     if (p->num_seqs < 1 || p->total_q < 0 || p->total_k < 0) return ATTN_ERR_INVALID_ARG;
@@ -209,23 +223,12 @@ attn_status_t check_fwd(const attn_fwd_params* p, bool varlen) {
   ATTN_TRY(check_tensor(p->v, p->v_batch_stride, p->v_row_stride, p->v_head_stride, varlen, ek));
   ATTN_TRY(check_tensor(p->o, p->o_batch_stride, p->o_row_stride, p->o_head_stride, varlen, eq));
   if ((!p->lse && !eq) || (reinterpret_cast<uintptr_t>(p->lse) & 3u)) return ATTN_ERR_INVALID_ARG;
-  switch (p->score_mod) {
-    case ATTN_SCORE_NONE: break;
-    case ATTN_SCORE_SOFTCAP:
-      if (!(std::isfinite(p->softcap) && p->softcap > 0.f && std::isfinite(p->softcap / p->softmax_scale)))
-        return ATTN_ERR_INVALID_ARG;
-      break;
-    case ATTN_SCORE_ALIBI:
-      if (!p->alibi_slopes || (reinterpret_cast<uintptr_t>(p->alibi_slopes) & 3u)) return ATTN_ERR_INVALID_ARG;
-      break;
-    default: return ATTN_ERR_INVALID_ARG;
-  }
-  return ATTN_OK;
+  return check_scores(p->softmax_scale, p->score_mod, p->softcap, p->alibi_slopes);
 }
 
 // Score-modification constants for the kernels (score_mod.cuh).
-template <typename Args>
-void fill_score_mod(Args& a, const attn_fwd_params* p) {
+template <typename Args, typename Params>
+void fill_score_mod(Args& a, const Params* p) {
   a.score_mod = p->score_mod;
   a.inv_scale = 1.f / p->softmax_scale;
   a.alibi_slopes = p->score_mod == ATTN_SCORE_ALIBI ? p->alibi_slopes : nullptr;
@@ -772,6 +775,162 @@ attn_status_t run_bwd(const attn_bwd_params* p, void* ws, size_t ws_bytes, bool 
   return ATTN_OK;
 }
 
+// ---- paged KV cache ---------------------------------------------------------
+bool aligned4(const void* p) { return p != nullptr && (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+// log2 of a page size this library takes (a power of two from 16 to 32768), else -1.
+int page_shift(int page_size) {
+  for (int s = 4; s <= 15; ++s)
+    if (page_size == (1 << s)) return s;
+  return -1;
+}
+
+attn_status_t check_cache(const void* base, int64_t page, int64_t row, int64_t head) {
+  if (!base || !aligned16(base)) return ATTN_ERR_INVALID_ARG;
+  return stride_ok(page) && stride_ok(row) && stride_ok(head) ? ATTN_OK : ATTN_ERR_INVALID_ARG;
+}
+
+attn_status_t bind_device(DeviceScope* scope, const void* ptr) {
+  const cudaError_t e = scope->bind(ptr);
+  if (e == cudaSuccess) return ATTN_OK;
+  return e == cudaErrorInvalidDevicePointer ? ATTN_ERR_INVALID_ARG : cuda_fail(e, "device");
+}
+
+attn_status_t run_kv_plan(const attn_kv_plan_params* p, cudaStream_t stream) {
+  if (!p) return ATTN_ERR_INVALID_ARG;
+  KvPlanArgs a{};
+  a.page_shift = page_shift(p->page_size);
+  if (a.page_shift < 0 || p->num_seqs < 1 || p->max_pages < 1 || p->free_capacity < 0 || p->max_tokens < 0 ||
+      p->block_table_stride < p->max_pages)
+    return ATTN_ERR_INVALID_ARG;
+  for (const void* x : std::initializer_list<const void*>{p->seqlens_old, p->seqlens_new, p->block_table,
+                                                          p->free_count, p->free_count_out, p->cu_seqlens_q,
+                                                          p->seqlens_k, p->status})
+    if (!aligned4(x)) return ATTN_ERR_INVALID_ARG;
+  if (p->free_capacity > 0 && !aligned4(p->free_pages)) return ATTN_ERR_INVALID_ARG;
+  if (p->max_tokens > 0 && (!p->slot_mapping || (reinterpret_cast<uintptr_t>(p->slot_mapping) & 7u)))
+    return ATTN_ERR_INVALID_ARG;
+  if (p->num_seqs > kMaxPlanSeqs) return ATTN_ERR_UNSUPPORTED;
+  ATTN_TRY(check_lists_device(p->seqlens_old, {p->seqlens_new, p->block_table, p->free_capacity ? p->free_pages : nullptr,
+                                               p->free_count, p->free_count_out, p->cu_seqlens_q, p->seqlens_k,
+                                               p->max_tokens ? p->slot_mapping : nullptr, p->status}));
+  DeviceScope scope;
+  ATTN_TRY(bind_device(&scope, p->seqlens_old));
+  a.seqlens_old = p->seqlens_old;
+  a.seqlens_new = p->seqlens_new;
+  a.block_table = p->block_table;
+  a.block_table_stride = p->block_table_stride;
+  a.free_pages = p->free_pages;
+  a.free_count = p->free_count;
+  a.free_count_out = p->free_count_out;
+  a.cu_seqlens_q = p->cu_seqlens_q;
+  a.seqlens_k = p->seqlens_k;
+  a.slot_mapping = p->slot_mapping;
+  a.status = p->status;
+  a.num_seqs = p->num_seqs;
+  a.max_pages = p->max_pages;
+  a.page_size = p->page_size;
+  a.free_capacity = p->free_capacity;
+  a.max_tokens = p->max_tokens;
+  const cudaError_t e = launch_kv_plan(a, stream);
+  return e == cudaSuccess ? ATTN_OK : cuda_fail(e, "kv plan launch");
+}
+
+attn_status_t run_kv_append(const attn_kv_append_params* p, cudaStream_t stream) {
+  if (!p) return ATTN_ERR_INVALID_ARG;
+  if (!supported_dims(p->d_qk, p->d_v))
+    return p->d_qk <= 0 || p->d_v <= 0 ? ATTN_ERR_INVALID_ARG : ATTN_ERR_UNSUPPORTED;
+  KvAppendArgs a{};
+  a.page_shift = page_shift(p->page_size);
+  if (a.page_shift < 0 || p->num_pages < 1 || p->heads_kv < 1 || p->tokens < 0) return ATTN_ERR_INVALID_ARG;
+  const bool none = p->tokens == 0;
+  ATTN_TRY(check_tensor(p->k, 0, p->k_row_stride, p->k_head_stride, true, none));
+  ATTN_TRY(check_tensor(p->v, 0, p->v_row_stride, p->v_head_stride, true, none));
+  ATTN_TRY(check_cache(p->k_cache, p->k_cache_page_stride, p->k_cache_row_stride, p->k_cache_head_stride));
+  ATTN_TRY(check_cache(p->v_cache, p->v_cache_page_stride, p->v_cache_row_stride, p->v_cache_head_stride));
+  if (none) return ATTN_OK;
+  if (!p->slot_mapping || (reinterpret_cast<uintptr_t>(p->slot_mapping) & 7u)) return ATTN_ERR_INVALID_ARG;
+  ATTN_TRY(check_lists_device(p->k, {p->v, p->k_cache, p->v_cache, p->slot_mapping}));
+  DeviceScope scope;
+  ATTN_TRY(bind_device(&scope, p->k));
+  a.k = static_cast<const __nv_bfloat16*>(p->k);
+  a.v = static_cast<const __nv_bfloat16*>(p->v);
+  a.k_cache = static_cast<__nv_bfloat16*>(p->k_cache);
+  a.v_cache = static_cast<__nv_bfloat16*>(p->v_cache);
+  a.k_row = p->k_row_stride, a.k_head = p->k_head_stride;
+  a.v_row = p->v_row_stride, a.v_head = p->v_head_stride;
+  a.kc_page = p->k_cache_page_stride, a.kc_row = p->k_cache_row_stride, a.kc_head = p->k_cache_head_stride;
+  a.vc_page = p->v_cache_page_stride, a.vc_row = p->v_cache_row_stride, a.vc_head = p->v_cache_head_stride;
+  a.slot_mapping = p->slot_mapping;
+  a.tokens = p->tokens;
+  a.heads_kv = p->heads_kv;
+  a.page_size = p->page_size;
+  a.num_pages = p->num_pages;
+  const cudaError_t e = launch_kv_append(p->d_qk, p->d_v, a, stream);
+  return e == cudaSuccess ? ATTN_OK : cuda_fail(e, "kv append launch");
+}
+
+// The parameters' checks that need no GPU.
+attn_status_t check_paged(const attn_paged_params* p) {
+  if (!p) return ATTN_ERR_INVALID_ARG;
+  if (!supported_dims(p->d_qk, p->d_v))
+    return p->d_qk <= 0 || p->d_v <= 0 ? ATTN_ERR_INVALID_ARG : ATTN_ERR_UNSUPPORTED;
+  if (page_shift(p->page_size) < 0 || p->num_pages < 1 || p->max_pages < 1 || p->num_seqs < 1 || p->total_q < 0 ||
+      p->max_seqlen_q < 0 || p->max_seqlen_q > p->total_q || p->block_table_stride < p->max_pages)
+    return ATTN_ERR_INVALID_ARG;
+  if (p->heads < 1 || p->heads_kv < 1 || p->heads % p->heads_kv != 0) return ATTN_ERR_INVALID_ARG;
+  if (p->heads / p->heads_kv > 128) return ATTN_ERR_UNSUPPORTED;
+  const bool none = p->total_q == 0;
+  ATTN_TRY(check_tensor(p->q, 0, p->q_row_stride, p->q_head_stride, true, none));
+  ATTN_TRY(check_tensor(p->o, 0, p->o_row_stride, p->o_head_stride, true, none));
+  ATTN_TRY(check_cache(p->k_cache, p->k_page_stride, p->k_row_stride, p->k_head_stride));
+  ATTN_TRY(check_cache(p->v_cache, p->v_page_stride, p->v_row_stride, p->v_head_stride));
+  if (!none && !aligned4(p->lse)) return ATTN_ERR_INVALID_ARG;
+  if (!aligned4(p->block_table) || !aligned4(p->cu_seqlens_q) || !aligned4(p->seqlens_k)) return ATTN_ERR_INVALID_ARG;
+  return check_scores(p->softmax_scale, p->score_mod, p->softcap, p->alibi_slopes);
+}
+
+attn_status_t run_fwd_paged(const attn_paged_params* p, void* ws, size_t ws_bytes, cudaStream_t stream) {
+  ATTN_TRY(check_paged(p));
+  if (p->total_q == 0 || p->max_seqlen_q == 0) return ATTN_OK;
+  ATTN_TRY(check_lists_device(p->q, {p->k_cache, p->v_cache, p->o, p->lse, p->block_table, p->cu_seqlens_q, p->seqlens_k,
+                                     p->score_mod == ATTN_SCORE_ALIBI ? p->alibi_slopes : nullptr}));
+  DeviceScope scope;
+  ATTN_TRY(bind_device(&scope, p->q));
+  (void)ws, (void)ws_bytes;
+  PagedArgs a{};
+  a.q = static_cast<const __nv_bfloat16*>(p->q);
+  a.k = static_cast<const __nv_bfloat16*>(p->k_cache);
+  a.v = static_cast<const __nv_bfloat16*>(p->v_cache);
+  a.o = static_cast<__nv_bfloat16*>(p->o);
+  a.lse = p->lse;
+  a.q_row = p->q_row_stride, a.q_head = p->q_head_stride;
+  a.o_row = p->o_row_stride, a.o_head = p->o_head_stride;
+  a.k_page = p->k_page_stride, a.k_row = p->k_row_stride, a.k_head = p->k_head_stride;
+  a.v_page = p->v_page_stride, a.v_row = p->v_row_stride, a.v_head = p->v_head_stride;
+  a.block_table = p->block_table;
+  a.block_table_stride = p->block_table_stride;
+  a.cu_q = p->cu_seqlens_q;
+  a.seqlens_k = p->seqlens_k;
+  a.num_seqs = p->num_seqs;
+  a.heads = p->heads;
+  a.heads_kv = p->heads_kv;
+  a.kv_group = p->heads / p->heads_kv;
+  a.page_size = p->page_size;
+  a.page_shift = page_shift(p->page_size);
+  a.num_pages = p->num_pages;
+  a.max_keys = static_cast<int>(std::min<int64_t>(static_cast<int64_t>(p->max_pages) << a.page_shift, 0x7fff0000));
+  a.total_q = p->total_q;
+  a.max_q = p->max_seqlen_q;
+  a.scale_log2 = p->softmax_scale * 1.4426950408889634f;
+  a.causal = p->causal ? 1 : 0;
+  fill_score_mod(a, p);
+  cudaError_t e = status_ptr(&a.status);
+  if (e != cudaSuccess) return cuda_fail(e, "status word");
+  e = launch_fwd_paged(p->d_qk, p->d_v, a, stream);
+  return e == cudaSuccess ? ATTN_OK : cuda_fail(e, "paged fwd launch");
+}
+
 }  // namespace
 
 size_t bwd_workspace_min_size(const attn_bwd_params* p) {
@@ -862,6 +1021,24 @@ attn_status_t attn_bwd_varlen(const attn_bwd_params* p, void* workspace, size_t 
   return run_bwd(p, workspace, workspace_bytes, true, static_cast<cudaStream_t>(stream));
 }
 
+attn_status_t attn_kv_plan(const attn_kv_plan_params* p, attn_stream_t stream) {
+  return run_kv_plan(p, static_cast<cudaStream_t>(stream));
+}
+
+attn_status_t attn_kv_append(const attn_kv_append_params* p, attn_stream_t stream) {
+  return run_kv_append(p, static_cast<cudaStream_t>(stream));
+}
+
+size_t attn_fwd_paged_workspace_size(const attn_paged_params* p) {
+  (void)p;
+  return 0;
+}
+
+attn_status_t attn_fwd_paged(const attn_paged_params* p, void* workspace, size_t workspace_bytes,
+                             attn_stream_t stream) {
+  return run_fwd_paged(p, workspace, workspace_bytes, static_cast<cudaStream_t>(stream));
+}
+
 attn_status_t attn_exp2_eval(const float* x, float* y_poly, float* y_hw, int64_t n, attn_stream_t stream) {
   if (n < 0 || (n > 0 && !x) || (!y_poly && !y_hw)) return ATTN_ERR_INVALID_ARG;
   if (n == 0) return ATTN_OK;
@@ -917,5 +1094,8 @@ const char* attn_last_cuda_error(void) { return t_last_cuda_error; }
 int32_t attn_abi_version(void) { return ATTN_ABI_VERSION; }
 size_t attn_fwd_params_size(void) { return sizeof(attn_fwd_params); }
 size_t attn_bwd_params_size(void) { return sizeof(attn_bwd_params); }
+size_t attn_kv_plan_params_size(void) { return sizeof(attn_kv_plan_params); }
+size_t attn_kv_append_params_size(void) { return sizeof(attn_kv_append_params); }
+size_t attn_paged_params_size(void) { return sizeof(attn_paged_params); }
 
 }  // extern "C"

@@ -2,6 +2,7 @@
 // translation units. Not part of the public ABI.
 #pragma once
 #include <cuda.h>
+#include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <atomic>
 #include <cstdint>
@@ -306,6 +307,61 @@ cudaError_t launch_bwd_dq(int d_qk, int d_v, const CUtensorMap& tq, const CUtens
 cudaError_t launch_bwd_dq_merge(const BwdArgs& a, int d_qk, cudaStream_t stream);
 // Zero-fills dQ, dK, dV rows of a problem with no keys or no queries.
 cudaError_t launch_bwd_zero(const BwdArgs& a, int d_qk, int d_v, bool zero_dq, bool zero_dkdv, cudaStream_t stream);
+
+// Paged KV cache (kv_cache.cu, attn_paged.cu); fields as in include/attn.h,
+// page_size = 1 << page_shift.
+constexpr int kMaxPlanSeqs = 16384;  // three sums per request in a CTA's shared memory
+struct KvPlanArgs {
+  const int* seqlens_old;
+  const int* seqlens_new;
+  int* block_table;
+  int64_t block_table_stride;
+  int* free_pages;
+  const int* free_count;
+  int* free_count_out;
+  int* cu_seqlens_q;
+  int* seqlens_k;
+  int64_t* slot_mapping;
+  int* status;
+  int num_seqs, max_pages, page_size, page_shift, free_capacity, max_tokens;
+};
+cudaError_t launch_kv_plan(const KvPlanArgs& a, cudaStream_t stream);
+
+struct KvAppendArgs {
+  const __nv_bfloat16* k;
+  const __nv_bfloat16* v;
+  __nv_bfloat16* k_cache;
+  __nv_bfloat16* v_cache;
+  int64_t k_row, k_head, v_row, v_head;           // element strides
+  int64_t kc_page, kc_row, kc_head, vc_page, vc_row, vc_head;
+  const int64_t* slot_mapping;
+  int tokens, heads_kv, page_size, page_shift, num_pages;
+};
+cudaError_t launch_kv_append(int d_qk, int d_v, const KvAppendArgs& a, cudaStream_t stream);
+
+struct PagedArgs {
+  const __nv_bfloat16* q;
+  const __nv_bfloat16* k;  // caches
+  const __nv_bfloat16* v;
+  __nv_bfloat16* o;
+  float* lse;
+  int64_t q_row, q_head, o_row, o_head;  // element strides
+  int64_t k_page, k_row, k_head, v_page, v_row, v_head;
+  const int* block_table;
+  int64_t block_table_stride;
+  const int* cu_q;
+  const int* seqlens_k;
+  int num_seqs, heads, heads_kv, kv_group;
+  int page_size, page_shift, num_pages, max_keys;  // max_keys: what a table row can name
+  int total_q, max_q;
+  float scale_log2;
+  int causal;
+  uint32_t* status;
+  int score_mod;  // as in FwdArgs
+  float mod_k2, mod_b, inv_scale;
+  const float* alibi_slopes;
+};
+cudaError_t launch_fwd_paged(int d_qk, int d_v, const PagedArgs& a, cudaStream_t stream);
 
 cudaError_t launch_exp2_eval(const float* x, float* y_poly, float* y_hw, int64_t n, cudaStream_t stream);
 

@@ -354,6 +354,145 @@ attn_status_t attn_bwd_block_sparse(const attn_bwd_params* p, const int32_t* kv_
 #define ATTN_BWD_NOALLOC_SCRATCH_BYTES (8u << 20)
 attn_status_t attn_bwd_noalloc(const attn_bwd_params* p, attn_stream_t stream);
 
+/* ---------------------------------------------------------------------------
+ * Serving from a paged KV cache. Keys and values of all requests live in two
+ * caches of fixed-size pages,
+ *   k_cache [num_pages, page_size, heads_kv, d_qk],
+ *   v_cache [num_pages, page_size, heads_kv, d_v]          (bf16, any strides),
+ * and request s finds its tokens through row s of a block table: token t is
+ * row t % page_size of page block_table[s][t / page_size]. page_size is a power
+ * of two from 16 to 32768. A step of a server is attn_kv_plan (pages and slots
+ * for the step's new tokens), then per layer attn_kv_append (their K and V into
+ * the cache) and attn_fwd_paged (attention of the new tokens over everything).
+ * All lengths, tables and maps are device arrays, so a step can be captured
+ * into a CUDA graph and replayed as lengths change. Every array must be on the
+ * same GPU (else ATTN_ERR_INVALID_ARG) and stay unchanged until the work on
+ * the stream has run.
+ * ------------------------------------------------------------------------- */
+
+/* Plans one step. Request s holds seqlens_old[s] >= 0 tokens and adds
+ * seqlens_new[s] >= 0; seqlens_new[s] < 0 ends it. With have = ceil(old / page_size)
+ * and want = ceil((old + new) / page_size):
+ *   - ended requests, in order, push their pages block_table[s][0 .. have) on the
+ *     stack of free pages free_pages[0 .. *free_count);
+ *   - growing requests, in order, then take pages have .. want-1 of their rows off
+ *     its top, one after another, into block_table[s][have .. want);
+ *   - cu_seqlens_q [num_seqs + 1] = running sums of the tokens added,
+ *     seqlens_k [num_seqs] = old + new (0 for ended requests), slot_mapping
+ *     [max_tokens] = page * page_size + row of each new token, requests in order,
+ *     then -1, *free_count_out = the stack's new height, *status = 0.
+ * Table entries outside have .. want-1 and stack entries below both heights
+ * stay as they were. All or nothing: *status is 1 when the stack holds too few
+ * pages, 2 when a request needs more than max_pages entries, 3 when the tokens
+ * exceed max_tokens, 4 when the stack would outgrow free_capacity (the first
+ * that applies); then the table and the stack are left alone, cu_seqlens_q is
+ * 0 throughout, slot_mapping -1, seqlens_k = seqlens_old and *free_count_out =
+ * *free_count, so that the step's other calls do nothing. seqlens_k may be
+ * seqlens_old and free_count_out may be free_count (updated in place); no
+ * other arrays may overlap. The result is the same bits on every call.
+ * num_seqs is 1 to 16384 (more: ATTN_ERR_UNSUPPORTED). */
+typedef struct attn_kv_plan_params {
+  const int32_t* seqlens_old;
+  const int32_t* seqlens_new;
+  int32_t* block_table; /* [num_seqs] rows of max_pages entries, block_table_stride apart */
+  int64_t block_table_stride;
+  int32_t* free_pages; /* [free_capacity] */
+  const int32_t* free_count;
+  int32_t* free_count_out;
+  int32_t* cu_seqlens_q;
+  int32_t* seqlens_k;
+  int64_t* slot_mapping;
+  int32_t* status;
+  int32_t num_seqs;
+  int32_t max_pages;
+  int32_t page_size;
+  int32_t free_capacity;
+  int32_t max_tokens;
+} attn_kv_plan_params;
+attn_status_t attn_kv_plan(const attn_kv_plan_params* p, attn_stream_t stream);
+
+/* Writes K and V rows of new tokens into the caches: row i of k
+ * [tokens, heads_kv, d_qk] and v [tokens, heads_kv, d_v] goes to slot
+ * slot_mapping[i] (page slot / page_size, row slot % page_size). A slot outside
+ * [0, num_pages * page_size), as -1, writes nothing. Slots must differ; of rows
+ * with the same slot any one may stay, in 16-byte pieces. The rest of the
+ * caches is left as it was. (d_qk, d_v), bases and strides as for attn_fwd. */
+typedef struct attn_kv_append_params {
+  const void* k;
+  const void* v;
+  void* k_cache;
+  void* v_cache;
+  int64_t k_row_stride, k_head_stride;
+  int64_t v_row_stride, v_head_stride;
+  int64_t k_cache_page_stride, k_cache_row_stride, k_cache_head_stride;
+  int64_t v_cache_page_stride, v_cache_row_stride, v_cache_head_stride;
+  const int64_t* slot_mapping;
+  int32_t tokens;
+  int32_t heads_kv;
+  int32_t d_qk;
+  int32_t d_v;
+  int32_t page_size;
+  int32_t num_pages;
+} attn_kv_append_params;
+attn_status_t attn_kv_append(const attn_kv_append_params* p, attn_stream_t stream);
+
+/* Attention of packed new tokens over the paged cache. Request s's queries are
+ * rows cu_seqlens_q[s] .. cu_seqlens_q[s+1]-1 of q [total_q, heads, d_qk] (none,
+ * one, or a chunk of a prompt), its keys the first seqlens_k[s] tokens of its
+ * row of the block table, the new tokens' own among them; query head h reads
+ * K/V head h / (heads / heads_kv), heads / heads_kv <= 128. causal != 0: query i
+ * of nq sees key j <= i + seqlens_k[s] - nq (aligned to the last key); else all
+ * keys. o [total_q, heads, d_v] (bf16) and lse [heads, total_q] (fp32,
+ * contiguous) as for attn_fwd_varlen, score modifications too; a row that sees
+ * no key gets O = 0 and LSE = -inf. Rows of o and lse behind the last request
+ * are left as they were.
+ * Lengths are clamped: seqlens_k to [0, max_pages * page_size], the offsets of
+ * q to [0, total_q] and each request's queries to max_seqlen_q (a bound the
+ * caller gives; it sizes the launch). Keys on a page whose table entry is
+ * outside [0, num_pages) are masked. Cache rows past seqlens_k may hold
+ * anything, infinities and NaN included, and reach no result; a non-finite
+ * value among a request's own visible keys or values reaches every query row
+ * of that request whose 128-key block holds it, also rows that the causal mask
+ * hides it from.
+ * P enters the PV product in bf16 (V's type). Results depend on the batch only
+ * through the order of additions (keys may be split across SMs and merged in
+ * key order): the same call gives the same bits.
+ * The workspace (256-byte aligned) is attn_fwd_paged_workspace_size(p) bytes;
+ * calls that may run at once, or graphs replayed at once, need one each. */
+typedef struct attn_paged_params {
+  const void* q;
+  const void* k_cache;
+  const void* v_cache;
+  void* o;
+  float* lse;
+  int64_t q_row_stride, q_head_stride;
+  int64_t o_row_stride, o_head_stride;
+  int64_t k_page_stride, k_row_stride, k_head_stride;
+  int64_t v_page_stride, v_row_stride, v_head_stride;
+  const int32_t* block_table; /* [num_seqs] rows of max_pages entries, block_table_stride apart */
+  int64_t block_table_stride;
+  const int32_t* cu_seqlens_q;
+  const int32_t* seqlens_k;
+  int32_t num_seqs;
+  int32_t heads;
+  int32_t heads_kv;
+  int32_t d_qk;
+  int32_t d_v;
+  int32_t page_size;
+  int32_t num_pages;
+  int32_t max_pages;
+  int32_t total_q;
+  int32_t max_seqlen_q;
+  float softmax_scale;
+  int32_t causal;
+  int32_t score_mod;
+  float softcap;
+  const float* alibi_slopes;
+} attn_paged_params;
+size_t attn_fwd_paged_workspace_size(const attn_paged_params* p);
+attn_status_t attn_fwd_paged(const attn_paged_params* p, void* workspace, size_t workspace_bytes,
+                             attn_stream_t stream);
+
 /* Diagnostic: evaluates the kernels' two exp2 paths on n device floats x:
  * y_poly = Cody-Waite split + cubic on the FMA pipe (NULL to skip),
  * y_hw = the hardware ex2 approximation (NULL to skip). Same code as the
@@ -388,6 +527,9 @@ const char* attn_last_cuda_error(void);
 int32_t attn_abi_version(void);
 size_t attn_fwd_params_size(void);
 size_t attn_bwd_params_size(void);
+size_t attn_kv_plan_params_size(void);
+size_t attn_kv_append_params_size(void);
+size_t attn_paged_params_size(void);
 
 #ifdef __cplusplus
 }

@@ -67,13 +67,13 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
 }
 
 // TMA map over a bf16 tensor viewed as [n_b, n_rows, n_heads, d] with element
-// strides (sb, sn, sh) and unit stride on d. Box: 64 columns x 1 head x
+// strides (sb, sn, sh) and unit stride on d. Box: 64 columns x `box_heads` heads (1) x
 // `box_rows` rows x 1 batch, 128-byte swizzle (the UMMA K-major / MN-major
 // SW128 layout). Out-of-range rows read as zero.
 // elem_bytes 2: bf16 / fp16 elements, 64-column boxes; 1: E4M3 bytes, 128-column
 // boxes. Either way a box row is one 128-byte swizzled chunk.
 attn_status_t make_map(CUtensorMap* m, const void* base, int d, int n_heads, int64_t n_rows, int n_b, int64_t sb,
-                       int64_t sn, int64_t sh, int box_rows, int elem_bytes = 2) {
+                       int64_t sn, int64_t sh, int box_rows, int elem_bytes = 2, int box_heads = 1) {
   auto enc = encode_fn();
   if (!enc) return cuda_fail(cudaErrorNotSupported, "cuTensorMapEncodeTiled unavailable");
   // Size-1 dimensions may carry any stride; give them a valid one.
@@ -84,7 +84,7 @@ attn_status_t make_map(CUtensorMap* m, const void* base, int d, int n_heads, int
   const cuuint64_t eb = static_cast<cuuint64_t>(elem_bytes);
   cuuint64_t strides[3] = {static_cast<cuuint64_t>(sh) * eb, static_cast<cuuint64_t>(sn) * eb,
                            static_cast<cuuint64_t>(sb) * eb};
-  cuuint32_t box[4] = {static_cast<cuuint32_t>(128 / elem_bytes), 1, static_cast<cuuint32_t>(box_rows), 1};
+  cuuint32_t box[4] = {static_cast<cuuint32_t>(128 / elem_bytes), static_cast<cuuint32_t>(box_heads), static_cast<cuuint32_t>(box_rows), 1};
   cuuint32_t es[4] = {1, 1, 1, 1};
   const CUtensorMapDataType ty = elem_bytes == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
   CUresult r = enc(m, ty, 4, const_cast<void*>(base), dims, strides, box, es,
@@ -890,6 +890,33 @@ attn_status_t check_paged(const attn_paged_params* p) {
   return check_scores(p->softmax_scale, p->score_mod, p->softcap, p->alibi_slopes);
 }
 
+// Rows, slots and workspace of a paged call (a function of the parameters alone).
+struct PagedPlan {
+  bool even = true;
+  int tile_tokens = 0, part_rows = 0;
+  int64_t items = 0;
+  size_t off_lse = 0, off_merge = 0, off_list = 0, off_items = 0, bytes = 0;
+};
+PagedPlan paged_plan(const attn_paged_params* p) {
+  PagedPlan pl;
+  const int group = p->heads / p->heads_kv;
+  pl.tile_tokens = 128 / group;
+  pl.even = p->max_seqlen_q <= pl.tile_tokens;  // one tile of rows holds any request's queries
+  pl.part_rows = pl.even ? 128 : 256;
+  const int64_t rows = 2ll * kPagedMaxCtas * pl.part_rows;
+  pl.off_lse = round256(rows * p->d_v * 4);
+  pl.off_merge = pl.off_lse + round256(rows * 4);
+  pl.bytes = pl.off_merge + round256(kPagedMaxCtas * static_cast<int64_t>(sizeof(MergeUnit)));
+  if (!pl.even) {
+    // units of 2 * tile_tokens tokens (the last of each request may be shorter) per K/V head, and a cut per CTA
+    pl.items = p->heads_kv * (static_cast<int64_t>(p->total_q) / (2 * pl.tile_tokens) + p->num_seqs) + 2 * kPagedMaxCtas;
+    pl.off_list = pl.bytes;
+    pl.off_items = pl.off_list + 256 + round256(static_cast<int64_t>(p->num_seqs) * 4);
+    pl.bytes = pl.off_items + round256(pl.items * static_cast<int64_t>(sizeof(ChunkItem)));
+  }
+  return pl;
+}
+
 attn_status_t run_fwd_paged(const attn_paged_params* p, void* ws, size_t ws_bytes, cudaStream_t stream) {
   ATTN_TRY(check_paged(p));
   if (p->total_q == 0 || p->max_seqlen_q == 0) return ATTN_OK;
@@ -897,17 +924,12 @@ attn_status_t run_fwd_paged(const attn_paged_params* p, void* ws, size_t ws_byte
                                      p->score_mod == ATTN_SCORE_ALIBI ? p->alibi_slopes : nullptr}));
   DeviceScope scope;
   ATTN_TRY(bind_device(&scope, p->q));
-  (void)ws, (void)ws_bytes;
+  const PagedPlan pl = paged_plan(p);
+  if (ws == nullptr || ws_bytes < pl.bytes || (reinterpret_cast<uintptr_t>(ws) & 255u)) return ATTN_ERR_WORKSPACE;
   PagedArgs a{};
-  a.q = static_cast<const __nv_bfloat16*>(p->q);
-  a.k = static_cast<const __nv_bfloat16*>(p->k_cache);
-  a.v = static_cast<const __nv_bfloat16*>(p->v_cache);
   a.o = static_cast<__nv_bfloat16*>(p->o);
   a.lse = p->lse;
-  a.q_row = p->q_row_stride, a.q_head = p->q_head_stride;
   a.o_row = p->o_row_stride, a.o_head = p->o_head_stride;
-  a.k_page = p->k_page_stride, a.k_row = p->k_row_stride, a.k_head = p->k_head_stride;
-  a.v_page = p->v_page_stride, a.v_row = p->v_row_stride, a.v_head = p->v_head_stride;
   a.block_table = p->block_table;
   a.block_table_stride = p->block_table_stride;
   a.cu_q = p->cu_seqlens_q;
@@ -927,7 +949,32 @@ attn_status_t run_fwd_paged(const attn_paged_params* p, void* ws, size_t ws_byte
   fill_score_mod(a, p);
   cudaError_t e = status_ptr(&a.status);
   if (e != cudaSuccess) return cuda_fail(e, "status word");
-  e = launch_fwd_paged(p->d_qk, p->d_v, a, stream);
+  a.tile_tokens = pl.tile_tokens;
+  uint8_t* base = static_cast<uint8_t*>(ws);
+  a.part_rows = pl.part_rows;
+  a.part_o = reinterpret_cast<float*>(base);
+  a.part_lse = reinterpret_cast<float*>(base + pl.off_lse);
+  a.merge = reinterpret_cast<MergeUnit*>(base + pl.off_merge);
+  if (!pl.even) {
+    a.n_items = reinterpret_cast<int*>(base + pl.off_list);
+    a.next_item = a.n_items + 1;
+    a.list_scratch = reinterpret_cast<int*>(base + pl.off_list + 256);
+    a.items = reinterpret_cast<ChunkItem*>(base + pl.off_items);
+    a.items_bound = static_cast<int>(pl.items);
+  }
+  int dev = 0, sms = 0;
+  e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e != cudaSuccess) return cuda_fail(e, "device");
+  CUtensorMap tq, tk, tv;
+  const int box = std::min(p->page_size, 128);
+  ATTN_TRY(make_map(&tq, p->q, p->d_qk, p->heads, p->total_q, 1, 0, p->q_row_stride, p->q_head_stride, pl.tile_tokens, 2,
+                    a.kv_group));
+  ATTN_TRY(make_map(&tk, p->k_cache, p->d_qk, p->heads_kv, p->page_size, p->num_pages, p->k_page_stride, p->k_row_stride,
+                    p->k_head_stride, box));
+  ATTN_TRY(make_map(&tv, p->v_cache, p->d_v, p->heads_kv, p->page_size, p->num_pages, p->v_page_stride, p->v_row_stride,
+                    p->v_head_stride, box));
+  e = launch_fwd_paged(p->d_qk, p->d_v, tq, tk, tv, a, pl.even, std::min(sms, kPagedMaxCtas), stream);
   return e == cudaSuccess ? ATTN_OK : cuda_fail(e, "paged fwd launch");
 }
 
@@ -1030,8 +1077,8 @@ attn_status_t attn_kv_append(const attn_kv_append_params* p, attn_stream_t strea
 }
 
 size_t attn_fwd_paged_workspace_size(const attn_paged_params* p) {
-  (void)p;
-  return 0;
+  if (check_paged(p) != ATTN_OK || p->total_q == 0 || p->max_seqlen_q == 0) return 0;
+  return paged_plan(p).bytes;
 }
 
 attn_status_t attn_fwd_paged(const attn_paged_params* p, void* workspace, size_t workspace_bytes,

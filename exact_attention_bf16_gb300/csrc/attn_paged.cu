@@ -1,9 +1,43 @@
 // Attention of packed new tokens over a paged KV cache (attn_fwd_paged).
 //
 // O_i = sum_j softmax_j(a_ij) v_j over the visible keys of query i, a_ij =
-// scale q_i . k_j, in one pass over the keys with a running maximum m, sum l
-// and accumulator (log2 units): for a new block of keys with maximum m',
-//   alpha = 2^(m - max(m, m')), l = l alpha + sum 2^(a - m), acc = acc alpha + 2^(a - m) v.
+// scale q_i . k_j, in one pass over the keys with a running maximum m and sum l
+// (log2 units) per row, the conditional rescale of fwd_kernel.cuh (a row's m is
+// replaced only when a block exceeds it by more than 8) and O accumulated in
+// Tensor Memory.
+//
+// Rows. The query heads of one K/V head share its keys, so the rows of a tile
+// are (token, head of the group) pairs, token-major: a 128-row tile holds
+// 128 / group tokens, and K/V are read once for the whole group. A unit of work
+// is up to 256 such rows (two tiles, each with its own S and O) of one request
+// and K/V head, or up to 128 rows, which then run as two streams over the even
+// and the odd key blocks (one computes S while the other's softmax runs), merged
+// at the end: a decoding request has few rows and many keys, and one stream's
+// chain S -> softmax -> PV would leave the copies waiting.
+//
+// Splitting. A unit's key blocks may be cut into segments taken by different
+// CTAs; each writes its normalised fp32 O and its LSE (log2), and
+// merge_kernel adds them with the weights 2^(LSE_r - LSE), in key order.
+// One persistent CTA per SM (shared memory and Tensor Memory are taken whole):
+//   - up to 128 rows per request (decoding, a few proposed tokens): bound by
+//     HBM (every K/V byte is read once and used for a handful of rows), so the
+//     key blocks of all (request, K/V head) units, laid end to end, are cut into
+//     equal ranges, one per CTA. A CTA finds its range from the lengths alone.
+//   - longer chunks: bound by the tensor cores, and by L2 where concurrent CTAs
+//     read different keys, so units are taken one after another from a list
+//     that chunk_list_kernel builds, a request's units together, long requests
+//     and late units (the most keys under the causal mask) first. Only units
+//     longer than an equal share of the work are cut.
+//
+// Warps: 0 work and TMA copies, 1 MMA issue, 4..7 and 8..11 softmax of tile or
+// stream 0 and 1. K and V have rings of their own; a copy is one box per page
+// and 64 columns, each lane of warp 0 issuing one. Pages past a request's last
+// key and entries outside the cache become a page index past the cache, whose
+// boxes read zeros.
+//
+// P enters the PV product in bf16, V's type in the cache (half a step is 2^-9 of
+// each weight): an fp16 copy of V, as the contiguous forward makes, would cost a
+// second pass over keys that a decoding step reads only once. Every sum is fp32.
 #include "kernels.h"
 #include "ptx_sm100.cuh"
 #include "score_mod.cuh"
@@ -11,96 +45,930 @@
 namespace gb300 {
 namespace paged {
 
-// One warp per (query row, head): 32 keys at a time, one per lane for the
-// logits, then one after another for the PV sums (lane l holds columns l, l +
-// 32, ...). Every sum is fp32. Correct for every case; each warp reads its keys
-// alone, so it is bound by L2 and issue, not by HBM or the tensor cores.
+constexpr int BM = 128, BN = 128;
+constexpr int kThreads = 384;
+constexpr int kChunk = BM * 128;     // bytes of one 64-column chunk of a 128-row tile
+constexpr float kThreshold = 8.0f;   // log2 units
+constexpr int kSegs = 4;             // segment descriptors in flight
+
+__host__ __device__ constexpr uint32_t tS(int i) { return 128u * i; }
+__host__ __device__ constexpr uint32_t tO(int i) { return 256u + 128u * i; }
+
 template <int DQK, int DV>
-__global__ void __launch_bounds__(128) paged_row_kernel(const PagedArgs a) {
-  __shared__ float sq[4][DQK];
-  const int lane = static_cast<int>(threadIdx.x & 31u), warp = static_cast<int>(threadIdx.x >> 5);
-  const int64_t r = blockIdx.x * 4ll + warp;
-  if (r >= static_cast<int64_t>(a.total_q) * a.heads) return;
-  const int t = static_cast<int>(r / a.heads), h = static_cast<int>(r % a.heads), hk = h / a.kv_group;
-  int lo = 0, hi = a.num_seqs;  // the request whose rows hold t
-  if (t < a.cu_q[0] || t >= a.cu_q[a.num_seqs]) return;
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (a.cu_q[mid] <= t) lo = mid;
-    else hi = mid;
+struct Cfg {
+  static constexpr int QCH = DQK / 64, VCH = DV / 64;
+  static constexpr int Q_BYTES = QCH * kChunk;
+  static constexpr int K_BYTES = QCH * kChunk;
+  static constexpr int V_BYTES = VCH * kChunk;
+  // ring slots: what shared memory holds beside the two Q tiles
+  static constexpr int NK = DQK == 64 ? 5 : 2;
+  static constexpr int NV = DQK == 64 ? 5 : (DQK == 128 ? 2 : 1);
+  static constexpr int OFF_K = 2 * Q_BYTES;
+  static constexpr int OFF_V = OFF_K + NK * K_BYTES;
+  static constexpr int OFF_X = OFF_V + NV * V_BYTES;  // the streams' (m, l): [2 streams][128] float2
+  static constexpr int OFF_SEG = OFF_X + 2 * BM * 8;
+  static constexpr int OFF_BAR = OFF_SEG + kSegs * 64;
+  static constexpr int SMEM = OFF_BAR + 512;  // the base is 1024-byte aligned (checked)
+  static_assert(SMEM <= 232448, "shared memory budget");
+  static constexpr uint32_t REG_LO = 96, REG_HI = 200;
+  static constexpr int REG_BUDGET = 128 * REG_LO + 256 * REG_HI;
+};
+
+// One segment of work, written by warp 0 and read by every other warp.
+struct Seg {
+  int more;       // 0: no more work
+  int seq, hk;
+  int q_row;      // first token's row of q and o
+  int ntok;       // tokens of the unit
+  int pos0;       // position of the first token among the keys (bottom-right aligned; may be negative)
+  int nk;         // keys of the request
+  int kt0;        // first key block
+  int n0, n1;     // key blocks of tile 0 and 1 (dual: n0 in all, alternating)
+  int dual;       // one tile of rows, two streams of key blocks
+  int part;       // >= 0: the slot of this segment's partial O and LSE
+  int pad[4];
+};
+static_assert(sizeof(Seg) == 64, "OFF_SEG");
+
+struct Bars {
+  uint64_t q_full, q_free;
+  uint64_t k_full[5], k_empty[5], v_full[5], v_empty[5];
+  uint64_t s_full[2], p_full[2], o_full[2];
+  uint64_t o_free;              // a segment is over: its O has been read, its MMAs issued
+  uint64_t x_full[2];           // dual: a stream's (m, l) are in shared memory
+  uint64_t seg_full[kSegs], seg_empty[kSegs];
+  uint64_t mma_done;
+  uint32_t tmem_base;
+  // even split: the request that holds this CTA's first key block
+  int first_seq;
+  long long first_start, total;
+  long long warp_sum[12];
+};
+static_assert(sizeof(Bars) <= 512, "barriers must fit their reserved bytes");
+
+__device__ __forceinline__ int ceil_div(int a, int b) { return (a + b - 1) / b; }
+
+// Bounds of request s: rows of q (clamped to the rows there are and to max_q) and keys.
+struct Bounds {
+  int q0, nq, nk;
+};
+__device__ __forceinline__ Bounds bounds(const PagedArgs& a, int s) {
+  const int c0 = __ldg(a.cu_q + s), c1 = __ldg(a.cu_q + s + 1), k = __ldg(a.seqlens_k + s);
+  Bounds b;
+  b.q0 = max(0, min(c0, a.total_q));
+  b.nq = max(0, min(min(c1, a.total_q) - b.q0, a.max_q));
+  b.nk = max(0, min(k, a.max_keys));
+  return b;
+}
+// Keys that tokens up to `last` (0-based in the request) see.
+__device__ __forceinline__ int keys_seen(const PagedArgs& a, const Bounds& b, int last) {
+  return a.causal ? max(0, min(b.nk, last + b.nk - b.nq + 1)) : b.nk;
+}
+// Key blocks that a unit of a request costs; a unit whose rows see no key still writes them.
+__device__ __forceinline__ int unit_blocks(const PagedArgs& a, const Bounds& b, int last) {
+  return max(1, ceil_div(keys_seen(a, b, last), BN));
+}
+
+// Fills a segment: tokens tok0 .. of request s, K/V head hk, key blocks [kt0, kt1).
+__device__ __forceinline__ Seg make_seg(const PagedArgs& a, const Bounds& b, int s, int hk, int tok0, int ntok, int kt0,
+                                        int kt1, int part) {
+  Seg g;
+  g.more = 1;
+  g.seq = s, g.hk = hk;
+  g.q_row = b.q0 + tok0;
+  g.ntok = ntok;
+  g.pos0 = tok0 + b.nk - b.nq;
+  g.nk = b.nk;
+  g.kt0 = kt0;
+  g.dual = ntok <= a.tile_tokens ? 1 : 0;
+  g.part = part;
+  const int last0 = tok0 + min(ntok, a.tile_tokens) - 1;
+  g.n0 = max(0, min(ceil_div(keys_seen(a, b, last0), BN), kt1) - kt0);
+  g.n1 = g.dual ? 0 : max(0, min(ceil_div(keys_seen(a, b, tok0 + ntok - 1), BN), kt1) - kt0);
+  return g;
+}
+
+// The CTA of `ctas` whose range [c W / ctas, (c + 1) W / ctas) holds block x.
+__device__ __forceinline__ int range_owner(long long x, long long W, int ctas) {
+  return static_cast<int>(((x + 1) * ctas + W - 1) / W) - 1;
+}
+
+// EVEN: the even split of all units' key blocks (at most one tile of rows per
+// request); else the list of chunk_list_kernel.
+template <int DQK, int DV, int MOD, bool EVEN>
+__global__ void __launch_bounds__(kThreads, 1)
+    paged_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUtensorMap tmk,
+                 const __grid_constant__ CUtensorMap tmv, const PagedArgs a) {
+  using C = Cfg<DQK, DV>;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  if ((smem_u32(smem) & 1023u) != 0u) {  // the 128-byte-swizzled tiles need 1024-byte alignment
+    if (threadIdx.x == 0) record_error(a.status, DEV_BAD_CONFIG, 0x3000);
+    return;
   }
-  const int i = t - a.cu_q[lo], nq = min(a.cu_q[lo + 1] - a.cu_q[lo], a.max_q);
-  if (i >= nq) return;
-  const int nk = max(0, min(a.seqlens_k[lo], a.max_keys));
-  const int lim = a.causal ? min(nk, i + (nk - nq) + 1) : nk;
-  const int qpos = i + (nk - nq);
-  const int* table = a.block_table + lo * a.block_table_stride;
-  for (int c = lane; c < DQK; c += 32) sq[warp][c] = __bfloat162float(a.q[t * a.q_row + h * a.q_head + c]);
-  __syncwarp();
-  const float slope = a.score_mod == kModAlibi ? a.alibi_slopes[h] * a.inv_scale : 0.f;
-  float m = -INFINITY, l = 0.f, acc[DV / 32];
-#pragma unroll
-  for (int c = 0; c < DV / 32; ++c) acc[c] = 0.f;
-  for (int j0 = 0; j0 < lim; j0 += 32) {
-    const int j = j0 + lane;
-    float s = -INFINITY;
-    const __nv_bfloat16* vrow = nullptr;
-    if (j < lim) {
-      const int page = table[j >> a.page_shift];
-      if (page >= 0 && page < a.num_pages) {
-        const int64_t row = j & (a.page_size - 1);
-        const __nv_bfloat16* krow = a.k + page * a.k_page + row * a.k_row + hk * a.k_head;
-        vrow = a.v + page * a.v_page + row * a.v_row + hk * a.v_head;
-        float dot = 0.f;
-        for (int c = 0; c < DQK; c += 2) {
-          const float2 kf = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(krow + c));
-          dot = fmaf(kf.x, sq[warp][c], dot);
-          dot = fmaf(kf.y, sq[warp][c + 1], dot);
+  uint8_t* sQ = smem;
+  uint8_t* sK = smem + C::OFF_K;
+  uint8_t* sV = smem + C::OFF_V;
+  float2* sX = reinterpret_cast<float2*>(smem + C::OFF_X);
+  Seg* sSeg = reinterpret_cast<Seg*>(smem + C::OFF_SEG);
+  Bars* bar = reinterpret_cast<Bars*>(smem + C::OFF_BAR);
+  const uint32_t warp = warp_id(), lane = lane_id();
+  const int tid = static_cast<int>(threadIdx.x);
+
+  if (tid == 0) {
+    mbar_init(&bar->q_full, 1);
+    mbar_init(&bar->q_free, 1);
+    for (int s = 0; s < 5; ++s) {
+      mbar_init(&bar->k_full[s], 1);
+      mbar_init(&bar->k_empty[s], 1);
+      mbar_init(&bar->v_full[s], 1);
+      mbar_init(&bar->v_empty[s], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&bar->s_full[i], 1);
+      mbar_init(&bar->p_full[i], 4);
+      mbar_init(&bar->o_full[i], 1);
+      mbar_init(&bar->x_full[i], 4);
+    }
+    mbar_init(&bar->o_free, 9);  // eight softmax warps and the MMA thread, so that neither side gets two segments ahead
+    for (int s = 0; s < kSegs; ++s) {
+      mbar_init(&bar->seg_full[s], 1);
+      mbar_init(&bar->seg_empty[s], 9);  // the MMA thread and eight softmax warps
+    }
+    mbar_init(&bar->mma_done, 1);
+    bar->first_seq = -1;
+    fence_barrier_init();
+    tma_prefetch_desc(&tmq);
+    tma_prefetch_desc(&tmk);
+    tma_prefetch_desc(&tmv);
+  }
+  if (warp == 1) {
+    tmem_alloc(&bar->tmem_base, 512);
+    tmem_relinquish();
+  }
+  // Even split: running sums of the requests' key blocks (per K/V head), kThreads
+  // requests at a time; the second pass finds the one that holds this CTA's first block.
+  long long range0 = 0, range1 = 0;
+  int ctas = 0;
+  if constexpr (EVEN) {
+    long long total = 0;
+    for (int pass = 0; pass < 2; ++pass) {
+      long long base = 0;
+      for (int s0 = 0; s0 < a.num_seqs; s0 += kThreads) {
+        const int s = s0 + tid;
+        int n = 0;
+        if (s < a.num_seqs) {
+          const Bounds b = bounds(a, s);
+          n = b.nq > 0 ? unit_blocks(a, b, b.nq - 1) : 0;
         }
-        if (a.score_mod == kModSoftcap) dot = a.mod_b * tanh_scaled(dot, a.mod_k2);
-        if (a.score_mod == kModAlibi) dot -= fabsf(slope) * fabsf(static_cast<float>(j - qpos));
-        s = dot * a.scale_log2;
+        long long inc = n;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+          const long long u = __shfl_up_sync(0xffffffffu, inc, d);
+          if (static_cast<int>(lane) >= d) inc += u;
+        }
+        if (lane == 31) bar->warp_sum[warp] = inc;
+        __syncthreads();
+        long long before = base, all = base;
+        for (uint32_t w = 0; w < kThreads / 32; ++w) {
+          const long long x = bar->warp_sum[w];
+          if (w < warp) before += x;
+          all += x;
+        }
+        const long long start = (before + inc - n) * a.heads_kv;
+        // (one chunk of requests: the total is known in the first pass)
+        if (pass == 1 && n > 0 && start <= range0 && range0 < start + static_cast<long long>(n) * a.heads_kv) {
+          bar->first_seq = s;
+          bar->first_start = start;
+        }
+        base = all;
+        __syncthreads();
+      }
+      if (pass == 0) {
+        total = base * a.heads_kv;
+        // at least kMinBlocks key blocks per CTA: fewer would cost more to merge than they save
+        const long long want = (total + kPagedMinBlocks - 1) / kPagedMinBlocks;
+        ctas = static_cast<int>(want < static_cast<long long>(gridDim.x) ? want : gridDim.x);
+        const int c = static_cast<int>(blockIdx.x);
+        if (c < ctas) {
+          range0 = c * total / ctas;
+          range1 = (c + 1) * total / ctas;
+        }
       }
     }
-    float mx = s;
+    if (tid == 0) bar->total = total;
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tbase = bar->tmem_base;
+
+  if (warp < 4) {
+    regs_dec<C::REG_LO>();
+    if (warp == 0) {
+      // ===================== work and copies ================================
+      const int np = a.page_size < BN ? BN >> a.page_shift : 1;  // pages (boxes along the keys) of a key block
+      const int box_rows = a.page_size < BN ? a.page_size : BN;
+      const int my_page = static_cast<int>(lane) % np, my_chunk = static_cast<int>(lane) / np;
+      const uint32_t q_bytes = static_cast<uint32_t>(a.kv_group * a.tile_tokens) * 128u * C::QCH;
+      uint32_t ck = 0, cv = 0, cq = 0, seg_i = 0;  // copies and segments so far
+      bool ok = true;
+      // even split: where this CTA is
+      int s = 0, hk = 0, kt = 0, unit = 0;
+      Bounds b{0, 0, 0};
+      long long g = range0;
+      int merge_units = 0;  // units that begin in this range and end beyond it: at most one
+      if constexpr (EVEN) {
+        if (range0 < range1) {
+          s = bar->first_seq;
+          b = bounds(a, s);
+          unit = unit_blocks(a, b, b.nq - 1);
+          const long long off = range0 - bar->first_start;
+          hk = static_cast<int>(off / unit);
+          kt = static_cast<int>(off - static_cast<long long>(hk) * unit);
+        }
+      }
+      int item = static_cast<int>(blockIdx.x);  // list: this CTA's entry
+      const int n_items = EVEN ? 0 : *a.n_items;
+      while (ok) {
+        // ---- the next segment
+        Seg w;
+        w.more = 0;
+        if constexpr (EVEN) {
+          if (g < range1) {
+            const int take = static_cast<int>(min(static_cast<long long>(unit - kt), range1 - g));
+            int part = -1;
+            if (kt > 0) part = static_cast<int>(blockIdx.x);                     // continues an earlier CTA's unit
+            else if (take < unit) part = static_cast<int>(gridDim.x + blockIdx.x);  // begins here, ends beyond
+            w = make_seg(a, b, s, hk, 0, b.nq, kt, kt + take, part);
+            if (kt == 0 && take < unit) {
+              merge_units = 1;
+              if (lane == 0) {
+                MergeUnit m;
+                m.q_row = w.q_row, m.ntok = w.ntok, m.hk = hk;
+                m.first = part;
+                m.rest = static_cast<int>(blockIdx.x) + 1;
+                m.n = range_owner(g + unit - 1, bar->total, ctas) - static_cast<int>(blockIdx.x) + 1;
+                a.merge[blockIdx.x] = m;
+              }
+            }
+            g += take;
+            kt = 0;
+            if (g < range1 && ++hk == a.heads_kv) {  // (the unit ended, or the range did)
+              hk = 0;
+              do {
+                b = bounds(a, ++s);
+              } while (b.nq == 0 && s + 1 < a.num_seqs);
+              unit = unit_blocks(a, b, b.nq - 1);
+            }
+          }
+        } else {
+          if (item < n_items) {
+            const ChunkItem it = a.items[item];
+            b = bounds(a, it.seq);
+            w = make_seg(a, b, it.seq, it.hk, it.tok0, min(b.nq - it.tok0, 2 * a.tile_tokens), it.kt0, it.kt1, it.part);
+            int nx = 0;
+            if (lane == 0) nx = atomicAdd(a.next_item, 1);
+            item = __shfl_sync(0xffffffffu, nx, 0);
+          }
+        }
+        const int slot = static_cast<int>(seg_i % kSegs);
+        ok = mbar_wait_warp(&bar->seg_empty[slot], ((seg_i / kSegs) & 1u) ^ 1u, a.status, 0x3100);
+        if (!ok) break;
+        if (lane == 0) {
+          sSeg[slot] = w;
+          mbar_arrive(&bar->seg_full[slot]);
+        }
+        ++seg_i;
+        if (!w.more) break;
+        // ---- its copies
+        const int n = max(w.n0, w.n1);
+        if (n == 0) continue;
+        const int* table = a.block_table + w.seq * a.block_table_stride;
+        auto page_of = [&](int j) -> int {  // this lane's page of key block kt0 + j; num_pages (zeros) past the end
+          const long long key = (static_cast<long long>(w.kt0 + j) << 7) + (static_cast<long long>(my_page) << a.page_shift);
+          if (key >= w.nk) return a.num_pages;
+          const int pg = __ldg(table + (key >> a.page_shift));
+          return pg < 0 || pg > a.num_pages ? a.num_pages : pg;
+        };
+        int page = page_of(0);
+        for (int j = 0; j < n; ++j) {
+          const int next = j + 1 < n ? page_of(j + 1) : 0;  // fetched ahead of the waits
+          const int row = a.page_size > BN ? ((w.kt0 + j) << 7) & (a.page_size - 1) : 0;
+          const uint32_t ks = ck % C::NK;
+          ok = mbar_wait_warp(&bar->k_empty[ks], ((ck / C::NK) & 1u) ^ 1u, a.status, 0x3110);
+          if (!ok) break;
+          if (lane == 0) mbar_arrive_expect_tx(&bar->k_full[ks], C::K_BYTES);
+          __syncwarp();
+          if (my_chunk < C::QCH)
+            tma_load_4d(sK + ks * C::K_BYTES + my_chunk * kChunk + my_page * box_rows * 128, &tmk, &bar->k_full[ks],
+                        my_chunk * 64, w.hk, row, page);
+          ++ck;
+          if (j == 0) {  // Q behind the first K: that slot may be free long before the previous Q is
+            ok = mbar_wait_warp(&bar->q_free, (cq & 1u) ^ 1u, a.status, 0x3120);
+            if (!ok) break;
+            if (lane == 0) mbar_arrive_expect_tx(&bar->q_full, q_bytes * (w.dual ? 1u : 2u));
+            __syncwarp();
+            const int tiles = w.dual ? 1 : 2;
+            if (static_cast<int>(lane) < tiles * C::QCH) {
+              const int t = static_cast<int>(lane) / C::QCH, c = static_cast<int>(lane) % C::QCH;
+              tma_load_4d(sQ + t * C::Q_BYTES + c * kChunk, &tmq, &bar->q_full, c * 64, w.hk * a.kv_group,
+                          w.q_row + t * a.tile_tokens, 0);
+            }
+            ++cq;
+          }
+          const uint32_t vs = cv % C::NV;
+          ok = mbar_wait_warp(&bar->v_empty[vs], ((cv / C::NV) & 1u) ^ 1u, a.status, 0x3130);
+          if (!ok) break;
+          if (lane == 0) mbar_arrive_expect_tx(&bar->v_full[vs], C::V_BYTES);
+          __syncwarp();
+          if (my_chunk < C::VCH)
+            tma_load_4d(sV + vs * C::V_BYTES + my_chunk * kChunk + my_page * box_rows * 128, &tmv, &bar->v_full[vs],
+                        my_chunk * 64, w.hk, row, page);
+          ++cv;
+          page = next;
+        }
+      }
+      if (EVEN && merge_units == 0 && lane == 0) a.merge[blockIdx.x].n = 0;
+      if (!ok) {  // let the copies in flight land before the CTA exits
+        for (uint32_t u = 0; u < C::NK && u < ck; ++u)
+          mbar_wait(&bar->k_full[(ck - 1 - u) % C::NK], ((ck - 1 - u) / C::NK) & 1u, nullptr, 0);
+        for (uint32_t u = 0; u < C::NV && u < cv; ++u)
+          mbar_wait(&bar->v_full[(cv - 1 - u) % C::NV], ((cv - 1 - u) / C::NV) & 1u, nullptr, 0);
+        if (cq > 0) mbar_wait(&bar->q_full, (cq - 1) & 1u, nullptr, 0);
+      }
+    } else if (warp == 1 && lane == 0) {
+      // ===================== MMA issue ======================================
+      constexpr uint32_t idS = idesc_bf16_f32(BM, BN, false, false);
+      constexpr uint32_t idO = idesc_bf16_f32(BM, DV, false, true);
+      uint32_t ck = 0, cv = 0, cq = 0, seg_i = 0, cp[2] = {0, 0};
+      bool ok = true;
+      auto issue_s = [&](int i, int q_tile, uint32_t k_slot) {
+        const uint64_t dq = smem_desc(smem_u32(sQ + q_tile * C::Q_BYTES), 16, 1024, SWZ_128B);
+        const uint64_t dk = smem_desc(smem_u32(sK + k_slot * C::K_BYTES), 16, 1024, SWZ_128B);
 #pragma unroll
-    for (int d = 16; d > 0; d >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
-    if (mx == -INFINITY) continue;
-    const float mn = fmaxf(m, mx), alpha = exp2f(m - mn);
-    m = mn;
-    const float p = exp2f(s - mn);
-    l = l * alpha + p;
+        for (int kk = 0; kk < DQK / 16; ++kk) {
+          const uint32_t off = (kk / 4) * kChunk + (kk % 4) * 32;
+          mma_ss(tbase + tS(i), desc_add(dq, off), desc_add(dk, off), idS, kk > 0 ? 1u : 0u);
+        }
+        mma_commit(&bar->s_full[i]);
+      };
+      auto issue_pv = [&](int i, uint32_t v_slot, bool first) {
+        const uint64_t dv = smem_desc(smem_u32(sV + v_slot * C::V_BYTES), kChunk, 1024, SWZ_128B);
 #pragma unroll
-    for (int c = 0; c < DV / 32; ++c) acc[c] *= alpha;
-    for (int u = 0; u < 32; ++u) {
-      const float pu = __shfl_sync(0xffffffffu, p, u);
-      const __nv_bfloat16* vu = reinterpret_cast<const __nv_bfloat16*>(
-          __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(vrow), u));
-      if (vu == nullptr) continue;
+        for (int kk = 0; kk < BN / 16; ++kk)
+          mma_ts(tbase + tO(i), tbase + tS(i) + kk * 8, desc_add(dv, kk * 2048), idO, (kk > 0 || !first) ? 1u : 0u);
+      };
+      for (;;) {
+        const int slot = static_cast<int>(seg_i % kSegs);
+        ok = mbar_wait(&bar->seg_full[slot], (seg_i / kSegs) & 1u, a.status, 0x3200);
+        if (!ok) break;
+        const Seg* w = sSeg + slot;
+        const int more = w->more, n0 = w->n0, n1 = w->n1, dual = w->dual;
+        mbar_arrive(&bar->seg_empty[slot]);
+        if (!more) break;
+        const int n = max(n0, n1);
+        // the previous segment's O has been read: before the first PV overwrites it
+        auto wait_o = [&]() { return seg_i == 0 || mbar_wait(&bar->o_free, (seg_i - 1) & 1u, a.status, 0x3210); };
+        if (n == 0) {
+          ok = wait_o();
+          if (!ok) break;
+          mbar_arrive(&bar->o_free);
+          ++seg_i;
+          continue;
+        }
+        for (int j = 0; j <= n && ok; ++j) {
+          if (j < n) {
+            ok = mbar_wait(&bar->k_full[ck % C::NK], (ck / C::NK) & 1u, a.status, 0x3220);
+            if (ok && j == 0) ok = mbar_wait(&bar->q_full, cq & 1u, a.status, 0x3230);
+            if (!ok) break;
+            tc_fence_after();
+          }
+          if (dual) {
+            if (j < n) {
+              issue_s(j & 1, 0, ck % C::NK);
+              mma_commit(&bar->k_empty[ck % C::NK]);
+              ++ck;
+              if (j == n - 1) mma_commit(&bar->q_free);
+            }
+            if (j > 0) {
+              const int i = (j - 1) & 1;
+              if (j == 1) ok = wait_o();
+              ok = ok && mbar_wait(&bar->v_full[cv % C::NV], (cv / C::NV) & 1u, a.status, 0x3240) &&
+                   mbar_wait(&bar->p_full[i], cp[i] & 1u, a.status, 0x3250);
+              if (!ok) break;
+              tc_fence_after();
+              ++cp[i];
+              issue_pv(i, cv % C::NV, j <= 2);
+              mma_commit(&bar->v_empty[cv % C::NV]);
+              ++cv;
+              if (j - 1 >= n - 2) mma_commit(&bar->o_full[i]);
+            }
+          } else {
+            if (j > 0) {
+              if (j == 1) ok = wait_o();
+              ok = ok && mbar_wait(&bar->v_full[cv % C::NV], (cv / C::NV) & 1u, a.status, 0x3240);
+              if (!ok) break;
+            }
 #pragma unroll
-      for (int c = 0; c < DV / 32; ++c) acc[c] = fmaf(pu, __bfloat162float(vu[lane + 32 * c]), acc[c]);
+            for (int i = 0; i < 2; ++i) {
+              const int ni = i == 0 ? n0 : n1;
+              if (j > 0 && j - 1 < ni) {
+                ok = mbar_wait(&bar->p_full[i], cp[i] & 1u, a.status, 0x3250);
+                if (!ok) break;
+                tc_fence_after();
+                ++cp[i];
+                issue_pv(i, cv % C::NV, j == 1);
+                if (j == ni) mma_commit(&bar->o_full[i]);
+              }
+              if (j < ni) issue_s(i, i, ck % C::NK);
+            }
+            if (!ok) break;
+            if (j > 0) {
+              mma_commit(&bar->v_empty[cv % C::NV]);
+              ++cv;
+            }
+            if (j < n) {
+              mma_commit(&bar->k_empty[ck % C::NK]);
+              ++ck;
+              if (j == n - 1) mma_commit(&bar->q_free);
+            }
+          }
+        }
+        if (!ok) break;
+        mbar_arrive(&bar->o_free);
+        ++cq;
+        ++seg_i;
+      }
+      mma_commit(&bar->mma_done);
+      mbar_wait(&bar->mma_done, 0, a.status, 0x32ff);
+    }
+  } else {
+    regs_inc<C::REG_HI>();
+    // ======================= softmax and output =============================
+    const int i = (static_cast<int>(warp) - 4) / 4;  // tile or stream
+    const uint32_t quarter = warp & 3u;
+    const int r = static_cast<int>(quarter * 32 + lane);  // row of the tile
+    const int r_tok = r / a.kv_group, r_head = r - r_tok * a.kv_group;
+    const bool r_used = r < a.kv_group * a.tile_tokens;
+    const uint32_t lane_base = tbase + ((quarter * 32u) << 16);
+    const float sl2 = a.scale_log2;
+    const int np = a.page_size < BN ? BN >> a.page_shift : 1;
+    // segments, blocks of this stream, V blocks, dual segments, and segments in which each O was written
+    uint32_t seg_i = 0, cs = 0, cv0 = 0, cx = 0, co0 = 0, co1 = 0;
+    bool ok = true;
+    for (;;) {
+      const int slot = static_cast<int>(seg_i % kSegs);
+      ok = mbar_wait_warp(&bar->seg_full[slot], (seg_i / kSegs) & 1u, a.status, 0x3300);
+      if (!ok) break;
+      // read where needed (volatile: not kept in registers across the blocks' loop)
+      const volatile Seg& w = sSeg[slot];
+      if (!w.more) break;
+      const int mine = w.dual ? (w.n0 + 1 - i) / 2 : (i == 0 ? w.n0 : w.n1);
+      const int tok = r_tok + (w.dual ? 0 : i * a.tile_tokens);
+      const bool valid = r_used && tok < w.ntok;
+      const int pos = w.pos0 + tok;  // the row's position among the keys
+      const int klim = !valid ? 0 : (a.causal ? max(0, min(w.nk, pos + 1)) : w.nk);
+      const bool work = __any_sync(0xffffffffu, valid);  // a warp without rows only keeps the barriers in step
+      const float slope =
+          MOD == kModAlibi && valid ? fabsf(__ldg(a.alibi_slopes + w.hk * a.kv_group + r_head) * a.inv_scale) : 0.f;
+      // pages of key block kt that hold keys (one bit per page, the lanes' ballot)
+      auto page_ok = [&](int kt) -> bool {
+        const long long key = (static_cast<long long>(kt) << 7) + (static_cast<long long>(lane) << a.page_shift);
+        if (static_cast<int>(lane) >= np || key >= w.nk) return true;
+        const int pg = __ldg(a.block_table + w.seq * a.block_table_stride + (key >> a.page_shift));
+        return pg >= 0 && pg < a.num_pages;
+      };
+      float m_used = -INFINITY, l = 0.f;
+      const int dual = w.dual, step = dual ? 2 : 1;
+      int kt = w.kt0 + (dual ? i : 0);
+      bool pg_ok = mine > 0 ? page_ok(kt) : true;
+      for (int j = 0; j < mine; ++j, kt += step) {
+        const uint32_t pages = __ballot_sync(0xffffffffu, pg_ok);
+        if (j + 1 < mine) pg_ok = page_ok(kt + step);  // fetched one block ahead
+        ok = mbar_wait_warp(&bar->s_full[i], cs & 1u, a.status, 0x3310 + i);
+        if (!ok) break;
+        ++cs;
+        tc_fence_after();
+        if (work) {
+          uint32_t s[BN];
+          tmem_ld32(lane_base + tS(i) + 0, *reinterpret_cast<uint32_t(*)[32]>(&s[0]));
+          tmem_ld32(lane_base + tS(i) + 32, *reinterpret_cast<uint32_t(*)[32]>(&s[32]));
+          tmem_ld32(lane_base + tS(i) + 64, *reinterpret_cast<uint32_t(*)[32]>(&s[64]));
+          tmem_ld32(lane_base + tS(i) + 96, *reinterpret_cast<uint32_t(*)[32]>(&s[96]));
+          tmem_wait_ld();
+          if constexpr (MOD == kModSoftcap) {
+#pragma unroll
+            for (int c = 0; c < BN; ++c) s[c] = __float_as_uint(a.mod_b * tanh_scaled(__uint_as_float(s[c]), a.mod_k2));
+          } else if constexpr (MOD == kModAlibi) {
+            const float base = slope * static_cast<float>(kt * BN - pos);
+#pragma unroll
+            for (int c = 0; c < BN; ++c)
+              s[c] = __float_as_uint(__uint_as_float(s[c]) - fabsf(fmaf(slope, static_cast<float>(c), base)));
+          }
+          const int cnt = klim - kt * BN;  // visible keys of this row in the block
+          if (cnt < BN) {
+#pragma unroll
+            for (int c = 0; c < BN; ++c)
+              if (c >= cnt) s[c] = __float_as_uint(-INFINITY);
+          }
+          if (pages != 0xffffffffu) {  // keys on pages outside the cache (warp-uniform branch)
+            const int sh = a.page_size < BN ? a.page_shift : 7;
+#pragma unroll
+            for (int c = 0; c < BN; c += 16)
+              if (!((pages >> (c >> sh)) & 1u)) {
+#pragma unroll
+                for (int u = 0; u < 16; ++u) s[c + u] = __float_as_uint(-INFINITY);
+              }
+          }
+          float mp[8];
+#pragma unroll
+          for (int c = 0; c < 8; ++c) mp[c] = fmaxf(__uint_as_float(s[c]), __uint_as_float(s[c + 8]));
+#pragma unroll
+          for (int c = 16; c < BN; c += 16)
+#pragma unroll
+            for (int z = 0; z < 8; ++z) mp[z] = fmax3(mp[z], __uint_as_float(s[c + z]), __uint_as_float(s[c + 8 + z]));
+          const float mx = fmax3(fmax3(mp[0], mp[1], mp[2]), fmax3(mp[3], mp[4], mp[5]), fmaxf(mp[6], mp[7]));
+          const float m_tile = mx * sl2;
+          const bool need = m_tile > m_used + kThreshold;
+          float alpha = 1.f;
+          if (need) {
+            alpha = (m_used == -INFINITY) ? 0.f : ex2_mufu(m_used - m_tile);
+            m_used = m_tile;
+          }
+          l *= alpha;
+          const float mu = (m_used == -INFINITY) ? 0.f : m_used;
+          uint32_t pk[BN / 2];
+          float2 rs[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+          const float2 sl2v = make_float2(sl2, sl2), negmu = make_float2(-mu, -mu);
+#pragma unroll
+          for (int c = 0; c < BN / 2; ++c) {
+            const float2 x = ffma2(make_float2(__uint_as_float(s[2 * c]), __uint_as_float(s[2 * c + 1])), sl2v, negmu);
+            const float2 p = make_float2(ex2_mufu(x.x), ex2_mufu(x.y));
+            pk[c] = pack_bf16x2(p.x, p.y);
+            rs[c & 1] = fadd2(rs[c & 1], p);
+          }
+          l += (rs[0].x + rs[0].y) + (rs[1].x + rs[1].y);
+          tmem_st32(lane_base + tS(i) + 0, *reinterpret_cast<uint32_t(*)[32]>(&pk[0]));
+          tmem_st32(lane_base + tS(i) + 32, *reinterpret_cast<uint32_t(*)[32]>(&pk[32]));
+          if (j > 0 && __any_sync(0xffffffffu, need)) {
+#pragma unroll
+            for (int c = 0; c < DV / 32; ++c) {
+              uint32_t o[32];
+              tmem_ld32(lane_base + tO(i) + c * 32, o);
+              tmem_wait_ld();
+#pragma unroll
+              for (int t = 0; t < 32; ++t) o[t] = __float_as_uint(__uint_as_float(o[t]) * alpha);
+              tmem_st32(lane_base + tO(i) + c * 32, o);
+            }
+          }
+        }
+        // The request's last block: cache rows past its last key, on the page that holds it, may be
+        // anything (0 x NaN is NaN), so they are zeroed before the PV product reads them. Tile 0's
+        // warps do it where it has this block: its PV comes first and waits for them.
+        const int tail = w.nk - kt * BN;  // keys of the request in this block
+        if (tail < BN && tail > 0 && (tail & (a.page_size - 1)) != 0 && (w.dual || i == 0 || j >= w.n0)) {
+          const uint32_t u = cv0 + static_cast<uint32_t>(w.dual ? 2 * j + i : j), vs = u % C::NV;
+          // one slot: the block before may not have been read yet, and its phase of v_full not have come
+          if (C::NV == 1 && u > 0) ok = mbar_wait_warp(&bar->v_empty[0], (u - 1) & 1u, a.status, 0x3321);
+          ok = ok && mbar_wait_warp(&bar->v_full[vs], (u / C::NV) & 1u, a.status, 0x3320);
+          if (!ok) break;
+          const int end = min(BN, (tail | (a.page_size - 1)) + 1);
+          uint8_t* v = sV + vs * C::V_BYTES;
+          const int units = (end - tail) * 8;  // 16-byte pieces of a chunk
+          for (int x = r; x < units * C::VCH; x += 128)
+            *reinterpret_cast<uint4*>(v + (x / units) * kChunk + tail * 128 + (x % units) * 16) = make_uint4(0, 0, 0, 0);
+          fence_proxy_async_smem();
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bar->p_full[i]);
+      }
+      if (!ok) break;
+      cv0 += static_cast<uint32_t>(max(w.n0, w.n1));
+      // ---- output
+      const bool has0 = w.dual ? w.n0 > 0 : mine > 0;  // O_0 (dual) or this tile's O was written
+      const bool has1 = w.dual && w.n0 > 1;
+      const uint32_t po0 = co0 & 1u, po1 = co1 & 1u;
+      co0 += w.n0 > 0;
+      co1 += w.dual ? w.n0 > 1 : w.n1 > 0;
+      float inv_l, lse2;     // tile: 1 / l and the LSE in log2 units
+      float w0 = 0.f, w1 = 0.f;  // dual: weights of the streams' O
+      // every warp has left the segment before (its reads of sX among them)
+      if (seg_i > 0) ok = mbar_wait_warp(&bar->o_free, (seg_i - 1) & 1u, a.status, 0x3328);
+      if (!ok) break;
+      if (w.dual) {
+        float2* x = sX;
+        x[i * BM + r] = make_float2(m_used, l);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bar->x_full[i]);
+        ok = mbar_wait_warp(&bar->x_full[1 - i], cx & 1u, a.status, 0x3330);
+        if (!ok) break;
+        ++cx;
+        const float2 y = x[(1 - i) * BM + r];
+        const float ma = i == 0 ? m_used : y.x, la = i == 0 ? l : y.y, mb = i == 0 ? y.x : m_used, lb = i == 0 ? y.y : l;
+        const float mm = fmaxf(ma, mb);
+        const float ea = la > 0.f ? ex2_mufu(ma - mm) : 0.f, eb = lb > 0.f ? ex2_mufu(mb - mm) : 0.f;
+        const float lt = la * ea + lb * eb;
+        inv_l = lt > 0.f ? 1.f / lt : 0.f;
+        lse2 = lt > 0.f ? mm + log2f(lt) : -INFINITY;
+        w0 = ea * inv_l, w1 = eb * inv_l;
+        // (the exchange above also says that the other warpgroup has left the segment before, so
+        // that its O barrier is at most one phase behind)
+        if (has0) ok = mbar_wait_warp(&bar->o_full[0], po0, a.status, 0x3340);
+        if (ok && has1) ok = mbar_wait_warp(&bar->o_full[1], po1, a.status, 0x3341);
+      } else {
+        inv_l = l > 0.f ? 1.f / l : 0.f;
+        lse2 = l > 0.f ? m_used + log2f(l) : -INFINITY;
+        if (has0) ok = mbar_wait_warp(&bar->o_full[i], i == 0 ? po0 : po1, a.status, 0x3340 + i);
+      }
+      if (!ok) break;
+      tc_fence_after();
+      const int head = w.hk * a.kv_group + r_head;
+      const int c_lo = w.dual ? i * (DV / 64) : 0, c_hi = w.dual ? (i + 1) * (DV / 64) : DV / 32;  // 32-column groups
+      const int64_t prow = static_cast<int64_t>(w.part) * a.part_rows + (w.dual ? 0 : i * BM) + r;
+      __nv_bfloat16* orow = a.o + static_cast<int64_t>(w.q_row + tok) * a.o_row + static_cast<int64_t>(head) * a.o_head;
+      if (work) {
+        for (int c = c_lo; c < c_hi; ++c) {
+          uint32_t o[32];
+          if (w.dual) {
+            uint32_t o1[32];
+            if (has0) tmem_ld32(lane_base + tO(0) + c * 32, o);
+            if (has1) tmem_ld32(lane_base + tO(1) + c * 32, o1);
+            tmem_wait_ld();
+#pragma unroll
+            for (int t = 0; t < 32; ++t) {
+              const float x0 = has0 ? __uint_as_float(o[t]) * w0 : 0.f;
+              o[t] = __float_as_uint(has1 ? fmaf(__uint_as_float(o1[t]), w1, x0) : x0);
+            }
+          } else {
+            if (has0) {
+              tmem_ld32(lane_base + tO(i) + c * 32, o);
+              tmem_wait_ld();
+            }
+#pragma unroll
+            for (int t = 0; t < 32; ++t) o[t] = __float_as_uint(has0 ? __uint_as_float(o[t]) * inv_l : 0.f);
+          }
+          if (valid) {
+            if (w.part >= 0) {
+              float4* op = reinterpret_cast<float4*>(a.part_o + prow * DV) + c * 8;
+#pragma unroll
+              for (int t = 0; t < 8; ++t)
+                op[t] = make_float4(__uint_as_float(o[4 * t]), __uint_as_float(o[4 * t + 1]), __uint_as_float(o[4 * t + 2]),
+                                    __uint_as_float(o[4 * t + 3]));
+            } else {
+              uint32_t pw[16];
+#pragma unroll
+              for (int t = 0; t < 16; ++t) pw[t] = pack_bf16x2(__uint_as_float(o[2 * t]), __uint_as_float(o[2 * t + 1]));
+              store_row64(orow + c * 32, pw);
+            }
+          }
+        }
+        if (valid && (!w.dual || i == 0)) {
+          if (w.part >= 0) a.part_lse[prow] = lse2;
+          else a.lse[static_cast<int64_t>(head) * a.total_q + w.q_row + tok] = lse2 * 0.69314718055994531f;
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(&bar->o_free);
+        mbar_arrive(&bar->seg_empty[slot]);
+      }
+      ++seg_i;
     }
   }
+
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 1) tmem_dealloc(tbase, 512);
+}
+
+// Merges the units that were cut: with the segments' LSE_r in log2 units, M their
+// maximum, O = sum_r 2^(LSE_r - M) O_r / sum_r 2^(LSE_r - M), the segments in key
+// order. One warp per row; lane l holds columns [DV/32 l, DV/32 (l + 1)).
+template <int DV>
+__global__ void __launch_bounds__(256) merge_kernel(const PagedArgs a) {
+  constexpr int CPL = DV / 32;
+  const MergeUnit m = a.merge[blockIdx.x];
+  if (m.n < 1) return;
+  const int lane = static_cast<int>(threadIdx.x & 31u);
+  const int rr = static_cast<int>(blockIdx.y * 8 + (threadIdx.x >> 5));
+  if (rr >= m.ntok * a.kv_group) return;
+  const int tok = rr / a.kv_group, hd = rr - tok * a.kv_group, tile = tok / a.tile_tokens;
+  const int row = tile * BM + (tok - tile * a.tile_tokens) * a.kv_group + hd;
+  auto at = [&](int r) -> int64_t {
+    return static_cast<int64_t>(r == 0 ? m.first : m.rest + r - 1) * a.part_rows + row;
+  };
+  float mx = -INFINITY;
+  for (int r = lane; r < m.n; r += 32) mx = fmaxf(mx, a.part_lse[at(r)]);
 #pragma unroll
-  for (int d = 16; d > 0; d >>= 1) l += __shfl_xor_sync(0xffffffffu, l, d);
-  const float inv = l > 0.f ? 1.f / l : 0.f;
+  for (int d = 16; d > 0; d >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
+  float sum = 0.f, acc[CPL];
 #pragma unroll
-  for (int c = 0; c < DV / 32; ++c) a.o[t * a.o_row + h * a.o_head + lane + 32 * c] = __float2bfloat16_rn(acc[c] * inv);
-  if (lane == 0)
-    a.lse[static_cast<int64_t>(h) * a.total_q + t] = l > 0.f ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
+  for (int c = 0; c < CPL; ++c) acc[c] = 0.f;
+  if (mx != -INFINITY) {
+#pragma unroll 4
+    for (int r = 0; r < m.n; ++r) {
+      const int64_t x = at(r);
+      const float wr = ex2_mufu(a.part_lse[x] - mx);
+      sum += wr;
+      const float* src = a.part_o + x * DV + lane * CPL;
+      if constexpr (CPL == 4) {
+        const float4 v = *reinterpret_cast<const float4*>(src);
+        acc[0] = fmaf(wr, v.x, acc[0]);
+        acc[1] = fmaf(wr, v.y, acc[1]);
+        acc[2] = fmaf(wr, v.z, acc[2]);
+        acc[3] = fmaf(wr, v.w, acc[3]);
+      } else {
+        const float2 v = *reinterpret_cast<const float2*>(src);
+        acc[0] = fmaf(wr, v.x, acc[0]);
+        acc[1] = fmaf(wr, v.y, acc[1]);
+      }
+    }
+  }
+  const float inv = sum > 0.f ? 1.f / sum : 0.f;
+  const int64_t head = static_cast<int64_t>(m.hk) * a.kv_group + hd;
+  __nv_bfloat16* o = a.o + static_cast<int64_t>(m.q_row + tok) * a.o_row + head * a.o_head + lane * CPL;
+  if constexpr (CPL == 4)
+    *reinterpret_cast<uint2*>(o) = make_uint2(pack_bf16x2(acc[0] * inv, acc[1] * inv), pack_bf16x2(acc[2] * inv, acc[3] * inv));
+  else
+    *reinterpret_cast<uint32_t*>(o) = pack_bf16x2(acc[0] * inv, acc[1] * inv);
+  if (lane == 0) a.lse[head * a.total_q + m.q_row + tok] = sum > 0.f ? (mx + log2f(sum)) * 0.69314718055994531f : -INFINITY;
+}
+
+// The list of paged_kernel<EVEN = false>: per unit (request, 2 * tile_tokens
+// tokens, K/V head) one item, or several where its cost (key blocks, doubled
+// for two tiles of rows) exceeds an equal share of the whole, cut evenly.
+// Requests with the most keys come first (a counting sort by key blocks), a
+// request's last tokens, which see the most keys, before its first, the K/V
+// heads of the same tokens side by side. One block; the order affects only
+// scheduling.
+constexpr int kListThreads = 1024, kBins = 2048;
+
+__global__ void __launch_bounds__(kListThreads, 1) chunk_list_kernel(const PagedArgs a, int ctas) {
+  __shared__ int bins[kBins];
+  __shared__ long long sums[kListThreads / 32];
+  __shared__ int chunk_sum[kListThreads];
+  __shared__ int n_slots, n_merge;
+  const int tid = static_cast<int>(threadIdx.x), lane = tid & 31, warp = tid >> 5;
+  const int unit_tokens = 2 * a.tile_tokens;
+  for (int x = tid; x < kBins; x += kListThreads) bins[x] = 0;
+  if (tid == 0) n_slots = n_merge = 0;
+  // cost and blocks of the unit that ends before token `end` of a request
+  auto blocks = [&](const Bounds& b, int tok0) { return unit_blocks(a, b, min(tok0 + unit_tokens, b.nq) - 1); };
+  auto weight = [&](const Bounds& b, int tok0) { return b.nq - tok0 > a.tile_tokens ? 2 : 1; };
+  long long w = 0;
+  for (int s = tid; s < a.num_seqs; s += kListThreads) {
+    const Bounds b = bounds(a, s);
+    for (int t = 0; t < b.nq; t += unit_tokens) w += static_cast<long long>(blocks(b, t)) * weight(b, t);
+  }
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) w += __shfl_xor_sync(0xffffffffu, w, d);
+  if (lane == 0) sums[warp] = w;
+  __syncthreads();
+  w = 0;
+  for (int x = 0; x < kListThreads / 32; ++x) w += sums[x];
+  w *= a.heads_kv;
+  const long long cap = max(static_cast<long long>(kPagedMinItem), (w + ctas - 1) / ctas);
+  auto cuts = [&](const Bounds& b, int tok0) -> int {
+    return static_cast<int>((static_cast<long long>(blocks(b, tok0)) * weight(b, tok0) + cap - 1) / cap);
+  };
+  auto bin_of = [&](const Bounds& b) { return kBins - 1 - min(kBins - 1, ceil_div(b.nk, BN)); };  // most keys first
+  for (int s = tid; s < a.num_seqs; s += kListThreads) {
+    const Bounds b = bounds(a, s);
+    int n = 0;
+    for (int t = 0; t < b.nq; t += unit_tokens) n += cuts(b, t);
+    n *= a.heads_kv;
+    a.list_scratch[s] = n;
+    if (n > 0) atomicAdd(&bins[bin_of(b)], n);
+  }
+  __syncthreads();
+  // bins -> first item of each bin: every thread scans two bins, thread 0's warp the pairs' sums
+  const int b0 = bins[2 * tid], b1 = bins[2 * tid + 1];
+  chunk_sum[tid] = b0 + b1;
+  __syncthreads();
+  for (int d = 1; d < kListThreads; d <<= 1) {
+    const int x = tid >= d ? chunk_sum[tid - d] : 0;
+    __syncthreads();
+    chunk_sum[tid] += x;
+    __syncthreads();
+  }
+  const int before = chunk_sum[tid] - b0 - b1;
+  bins[2 * tid] = before;
+  bins[2 * tid + 1] = before + b0;
+  const int total = chunk_sum[kListThreads - 1];
+  __syncthreads();
+  for (int s = tid; s < a.num_seqs; s += kListThreads) {
+    const int n = a.list_scratch[s];
+    if (n > 0) a.list_scratch[s] = atomicAdd(&bins[bin_of(bounds(a, s))], n);
+  }
+  __syncthreads();
+  for (int s = warp; s < a.num_seqs; s += kListThreads / 32) {
+    const Bounds b = bounds(a, s);
+    const int units = ceil_div(b.nq, unit_tokens);
+    int at = a.list_scratch[s];
+    for (int u0 = 0; u0 < units; u0 += 32) {
+      const int u = units - 1 - u0 - lane;  // the last tokens first
+      const int tok0 = u * unit_tokens;
+      const int k = u >= 0 ? cuts(b, tok0) : 0;
+      int inc = k;
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const int x = __shfl_up_sync(0xffffffffu, inc, d);
+        if (lane >= d) inc += x;
+      }
+      const int mine = at + (inc - k) * a.heads_kv;
+      at += __shfl_sync(0xffffffffu, inc, 31) * a.heads_kv;
+      if (k == 0) continue;
+      const int nb = blocks(b, tok0), ntok = min(unit_tokens, b.nq - tok0);
+      for (int hk = 0; hk < a.heads_kv; ++hk) {
+        int slot = -1;
+        if (k > 1) {
+          // fewer than `ctas` units cost more than a share (their costs sum to at most ctas shares), and
+          // their cuts number at most cost / share + 1 each: below 2 * ctas in all
+          slot = atomicAdd(&n_slots, k);
+          const int x = atomicAdd(&n_merge, 1);
+          a.merge[x] = MergeUnit{b.q0 + tok0, ntok, hk, slot, slot + 1, k};
+        }
+        for (int x = 0; x < k; ++x) {
+          const int i = mine + hk * k + x;
+          if (i >= a.items_bound) break;
+          a.items[i] = ChunkItem{s, hk, tok0, static_cast<int>(static_cast<long long>(nb) * x / k),
+                                 static_cast<int>(static_cast<long long>(nb) * (x + 1) / k), slot < 0 ? -1 : slot + x};
+        }
+      }
+    }
+  }
+  __syncthreads();
+  for (int x = tid; x < ctas; x += kListThreads)
+    if (x >= n_merge) a.merge[x].n = 0;
+  if (tid == 0) {
+    *a.n_items = min(total, a.items_bound);
+    *a.next_item = ctas;
+  }
+}
+
+template <int DQK, int DV, int MOD, bool EVEN>
+cudaError_t launch_main(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const PagedArgs& a, int ctas,
+                        cudaStream_t stream) {
+  using C = Cfg<DQK, DV>;
+  auto kern = paged_kernel<DQK, DV, MOD, EVEN>;
+  static PerDeviceOnce once;
+  const cudaError_t e = once.run([&]() -> cudaError_t {
+    cudaError_t r = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+    if (r != cudaSuccess) return r;
+    cudaFuncAttributes fa{};
+    r = cudaFuncGetAttributes(&fa, kern);
+    if (r != cudaSuccess) return r;
+    // The setmaxnreg split must fit in the registers the CTA is launched with.
+    return fa.numRegs * kThreads < C::REG_BUDGET ? cudaErrorInvalidConfiguration : cudaSuccess;
+  });
+  if (e != cudaSuccess) return e;
+  kern<<<ctas, kThreads, C::SMEM, stream>>>(tq, tk, tv, a);
+  return cudaGetLastError();
+}
+
+template <int DQK, int DV>
+cudaError_t launch_d(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const PagedArgs& a, bool even,
+                     int ctas, cudaStream_t stream) {
+  cudaError_t e = cudaSuccess;
+  if (!even) {
+    chunk_list_kernel<<<1, kListThreads, 0, stream>>>(a, ctas);
+    e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+  }
+  switch (a.score_mod) {
+    case kModNone:
+      e = even ? launch_main<DQK, DV, kModNone, true>(tq, tk, tv, a, ctas, stream)
+               : launch_main<DQK, DV, kModNone, false>(tq, tk, tv, a, ctas, stream);
+      break;
+    case kModSoftcap:
+      e = even ? launch_main<DQK, DV, kModSoftcap, true>(tq, tk, tv, a, ctas, stream)
+               : launch_main<DQK, DV, kModSoftcap, false>(tq, tk, tv, a, ctas, stream);
+      break;
+    case kModAlibi:
+      e = even ? launch_main<DQK, DV, kModAlibi, true>(tq, tk, tv, a, ctas, stream)
+               : launch_main<DQK, DV, kModAlibi, false>(tq, tk, tv, a, ctas, stream);
+      break;
+    default: return cudaErrorInvalidValue;
+  }
+  if (e != cudaSuccess) return e;
+  const int rows = min(a.max_q, (even ? 1 : 2) * a.tile_tokens) * a.kv_group;
+  merge_kernel<DV><<<dim3(ctas, (rows + 7) / 8), 256, 0, stream>>>(a);
+  return cudaGetLastError();
 }
 
 }  // namespace paged
 
-cudaError_t launch_fwd_paged(int d_qk, int d_v, const PagedArgs& a, cudaStream_t stream) {
-  const int64_t blocks = (static_cast<int64_t>(a.total_q) * a.heads + 3) / 4;
-  if (blocks > 0x7fffffff) return cudaErrorInvalidConfiguration;
-  const unsigned g = static_cast<unsigned>(blocks);
-  if (d_qk == 64 && d_v == 64) paged::paged_row_kernel<64, 64><<<g, 128, 0, stream>>>(a);
-  else if (d_qk == 128 && d_v == 128) paged::paged_row_kernel<128, 128><<<g, 128, 0, stream>>>(a);
-  else if (d_qk == 192 && d_v == 128) paged::paged_row_kernel<192, 128><<<g, 128, 0, stream>>>(a);
-  else return cudaErrorInvalidValue;
-  return cudaGetLastError();
+cudaError_t launch_fwd_paged(int d_qk, int d_v, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
+                             const PagedArgs& a, bool even, int ctas, cudaStream_t stream) {
+  if (ctas < 1 || a.merge == nullptr || a.part_o == nullptr || (!even && a.items == nullptr)) return cudaErrorInvalidValue;
+  if (d_qk == 64 && d_v == 64) return paged::launch_d<64, 64>(tq, tk, tv, a, even, ctas, stream);
+  if (d_qk == 128 && d_v == 128) return paged::launch_d<128, 128>(tq, tk, tv, a, even, ctas, stream);
+  if (d_qk == 192 && d_v == 128) return paged::launch_d<192, 128>(tq, tk, tv, a, even, ctas, stream);
+  return cudaErrorInvalidValue;
 }
 
 }  // namespace gb300

@@ -339,14 +339,23 @@ struct KvAppendArgs {
 };
 cudaError_t launch_kv_append(int d_qk, int d_v, const KvAppendArgs& a, cudaStream_t stream);
 
+// A unit of attn_fwd_paged whose keys were cut into n segments (n < 1: none): its
+// first token's row of q, its tokens, K/V head, the partial slot of segment 0
+// (`first`) and those of segments 1 .. n - 1 (rest, rest + 1, ...).
+struct MergeUnit {
+  int q_row, ntok, hk, first, rest, n;
+};
+// One item of the chunks' list: 2 * tile_tokens tokens from tok0 on, key blocks [kt0, kt1).
+struct ChunkItem {
+  int seq, hk, tok0, kt0, kt1, part;
+};
+constexpr int kPagedMaxCtas = 152;    // one per SM
+constexpr int kPagedMinBlocks = 2;    // least key blocks of a CTA of the even split
+constexpr int kPagedMinItem = 8;      // least cost at which a unit of the list is cut
 struct PagedArgs {
-  const __nv_bfloat16* q;
-  const __nv_bfloat16* k;  // caches
-  const __nv_bfloat16* v;
   __nv_bfloat16* o;
   float* lse;
-  int64_t q_row, q_head, o_row, o_head;  // element strides
-  int64_t k_page, k_row, k_head, v_page, v_row, v_head;
+  int64_t o_row, o_head;  // element strides
   const int* block_table;
   int64_t block_table_stride;
   const int* cu_q;
@@ -360,8 +369,23 @@ struct PagedArgs {
   int score_mod;  // as in FwdArgs
   float mod_k2, mod_b, inv_scale;
   const float* alibi_slopes;
+  int tile_tokens;  // tokens of a 128-row tile: 128 / kv_group
+  // partial results, 2 * ctas slots of part_rows rows: fp32 O normalised over its keys, LSE in log2 units
+  int part_rows;
+  float* part_o;
+  float* part_lse;
+  MergeUnit* merge;  // [ctas]
+  // chunks only: the list, its bound and length, the next item to take, one int per request
+  ChunkItem* items;
+  int items_bound;
+  int* n_items;
+  int* next_item;
+  int* list_scratch;
 };
-cudaError_t launch_fwd_paged(int d_qk, int d_v, const PagedArgs& a, cudaStream_t stream);
+// Maps: q boxes of 64 columns x kv_group heads x tile_tokens rows; k and v (caches as [pages, page_size, heads_kv, d])
+// of 64 columns x min(page_size, 128) rows. even: no request has more than one tile of rows.
+cudaError_t launch_fwd_paged(int d_qk, int d_v, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
+                             const PagedArgs& a, bool even, int ctas, cudaStream_t stream);
 
 cudaError_t launch_exp2_eval(const float* x, float* y_poly, float* y_hw, int64_t n, cudaStream_t stream);
 

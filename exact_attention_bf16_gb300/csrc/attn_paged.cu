@@ -54,16 +54,18 @@ constexpr int kSegs = 4;             // segment descriptors in flight
 __host__ __device__ constexpr uint32_t tS(int i) { return 128u * i; }
 __host__ __device__ constexpr uint32_t tO(int i) { return 256u + 128u * i; }
 
-template <int DQK, int DV>
+// The even split has one tile of rows, so its shared memory holds more of K and V.
+template <int DQK, int DV, bool EVEN>
 struct Cfg {
+  static constexpr int QT = EVEN ? 1 : 2;
   static constexpr int QCH = DQK / 64, VCH = DV / 64;
   static constexpr int Q_BYTES = QCH * kChunk;
   static constexpr int K_BYTES = QCH * kChunk;
   static constexpr int V_BYTES = VCH * kChunk;
-  // ring slots: what shared memory holds beside the two Q tiles
-  static constexpr int NK = DQK == 64 ? 5 : 2;
-  static constexpr int NV = DQK == 64 ? 5 : (DQK == 128 ? 2 : 1);
-  static constexpr int OFF_K = 2 * Q_BYTES;
+  // ring slots: what shared memory holds beside the Q tiles
+  static constexpr int NK = DQK == 64 ? 6 : (DQK == 128 ? 3 : 2);
+  static constexpr int NV = DQK == 64 ? 6 : (EVEN ? (DQK == 128 ? 3 : 2) : (DQK == 128 ? 2 : 1));
+  static constexpr int OFF_K = QT * Q_BYTES;
   static constexpr int OFF_V = OFF_K + NK * K_BYTES;
   static constexpr int OFF_X = OFF_V + NV * V_BYTES;  // the streams' (m, l): [2 streams][128] float2
   static constexpr int OFF_SEG = OFF_X + 2 * BM * 8;
@@ -74,7 +76,8 @@ struct Cfg {
   static constexpr int REG_BUDGET = 128 * REG_LO + 256 * REG_HI;
 };
 
-// One segment of work, written by warp 0 and read by every other warp.
+// One segment of work, written by warp 0 and read by every other warp. It carries
+// the pipeline's counters too (the warps' registers hold a row of S).
 struct Seg {
   int more;       // 0: no more work
   int seq, hk;
@@ -86,25 +89,11 @@ struct Seg {
   int n0, n1;     // key blocks of tile 0 and 1 (dual: n0 in all, alternating)
   int dual;       // one tile of rows, two streams of key blocks
   int part;       // >= 0: the slot of this segment's partial O and LSE
-  int pad[4];
+  uint32_t v0;    // key blocks copied before this segment
+  uint32_t s0, s1;  // S tiles of stream 0 and 1 before it
+  uint32_t phase; // bit 0, 1: segments before it in which O_0, O_1 were written; bit 2: dual segments (all mod 2)
 };
 static_assert(sizeof(Seg) == 64, "OFF_SEG");
-
-struct Bars {
-  uint64_t q_full, q_free;
-  uint64_t k_full[5], k_empty[5], v_full[5], v_empty[5];
-  uint64_t s_full[2], p_full[2], o_full[2];
-  uint64_t o_free;              // a segment is over: its O has been read, its MMAs issued
-  uint64_t x_full[2];           // dual: a stream's (m, l) are in shared memory
-  uint64_t seg_full[kSegs], seg_empty[kSegs];
-  uint64_t mma_done;
-  uint32_t tmem_base;
-  // even split: the request that holds this CTA's first key block
-  int first_seq;
-  long long first_start, total;
-  long long warp_sum[12];
-};
-static_assert(sizeof(Bars) <= 512, "barriers must fit their reserved bytes");
 
 __device__ __forceinline__ int ceil_div(int a, int b) { return (a + b - 1) / b; }
 
@@ -120,6 +109,23 @@ __device__ __forceinline__ Bounds bounds(const PagedArgs& a, int s) {
   b.nk = max(0, min(k, a.max_keys));
   return b;
 }
+struct Bars {
+  uint64_t q_full, q_free;
+  uint64_t k_full[6], k_empty[6], v_full[6], v_empty[6];
+  uint64_t s_full[2], p_full[2], o_full[2];
+  uint64_t o_free;              // a segment is over: its O has been read, its MMAs issued
+  uint64_t x_full[2];           // dual: a stream's (m, l) are in shared memory
+  uint64_t seg_full[kSegs], seg_empty[kSegs];
+  uint64_t mma_done;
+  uint32_t tmem_base;
+  // even split: the request that holds this CTA's first key block
+  int first_seq;
+  Bounds first;
+  long long first_start, total;
+  long long warp_sum[12];
+};
+static_assert(sizeof(Bars) <= 512, "barriers must fit their reserved bytes");
+
 // Keys that tokens up to `last` (0-based in the request) see.
 __device__ __forceinline__ int keys_seen(const PagedArgs& a, const Bounds& b, int last) {
   return a.causal ? max(0, min(b.nk, last + b.nk - b.nq + 1)) : b.nk;
@@ -159,7 +165,7 @@ template <int DQK, int DV, int MOD, bool EVEN>
 __global__ void __launch_bounds__(kThreads, 1)
     paged_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUtensorMap tmk,
                  const __grid_constant__ CUtensorMap tmv, const PagedArgs a) {
-  using C = Cfg<DQK, DV>;
+  using C = Cfg<DQK, DV, EVEN>;
   extern __shared__ __align__(1024) uint8_t smem[];
   if ((smem_u32(smem) & 1023u) != 0u) {  // the 128-byte-swizzled tiles need 1024-byte alignment
     if (threadIdx.x == 0) record_error(a.status, DEV_BAD_CONFIG, 0x3000);
@@ -177,7 +183,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (tid == 0) {
     mbar_init(&bar->q_full, 1);
     mbar_init(&bar->q_free, 1);
-    for (int s = 0; s < 5; ++s) {
+    for (int s = 0; s < 6; ++s) {
       mbar_init(&bar->k_full[s], 1);
       mbar_init(&bar->k_empty[s], 1);
       mbar_init(&bar->v_full[s], 1);
@@ -206,18 +212,21 @@ __global__ void __launch_bounds__(kThreads, 1)
     tmem_relinquish();
   }
   // Even split: running sums of the requests' key blocks (per K/V head), kThreads
-  // requests at a time; the second pass finds the one that holds this CTA's first block.
+  // requests at a time, to the total; then the request that holds this CTA's first
+  // block is found, in a second pass where there are more than kThreads requests.
   long long range0 = 0, range1 = 0;
   int ctas = 0;
   if constexpr (EVEN) {
     long long total = 0;
-    for (int pass = 0; pass < 2; ++pass) {
+    const bool one_pass = a.num_seqs <= kThreads;
+    for (int pass = 0; pass < (one_pass ? 1 : 2); ++pass) {
       long long base = 0;
       for (int s0 = 0; s0 < a.num_seqs; s0 += kThreads) {
         const int s = s0 + tid;
         int n = 0;
+        Bounds b{0, 0, 0};
         if (s < a.num_seqs) {
-          const Bounds b = bounds(a, s);
+          b = bounds(a, s);
           n = b.nq > 0 ? unit_blocks(a, b, b.nq - 1) : 0;
         }
         long long inc = n;
@@ -234,25 +243,26 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (w < warp) before += x;
           all += x;
         }
+        if (one_pass || (pass == 0 && s0 + kThreads >= a.num_seqs)) {
+          total = all * a.heads_kv;
+          // at least kPagedMinBlocks key blocks per CTA: fewer would cost more to merge than they save
+          const long long want = (total + kPagedMinBlocks - 1) / kPagedMinBlocks;
+          ctas = static_cast<int>(want < static_cast<long long>(gridDim.x) ? want : gridDim.x);
+          const int c = static_cast<int>(blockIdx.x);
+          if (c < ctas) {
+            range0 = c * total / ctas;
+            range1 = (c + 1) * total / ctas;
+          }
+        }
         const long long start = (before + inc - n) * a.heads_kv;
-        // (one chunk of requests: the total is known in the first pass)
-        if (pass == 1 && n > 0 && start <= range0 && range0 < start + static_cast<long long>(n) * a.heads_kv) {
+        if ((one_pass || pass == 1) && n > 0 && start <= range0 &&
+            range0 < start + static_cast<long long>(n) * a.heads_kv) {
           bar->first_seq = s;
+          bar->first = b;
           bar->first_start = start;
         }
         base = all;
-        __syncthreads();
-      }
-      if (pass == 0) {
-        total = base * a.heads_kv;
-        // at least kMinBlocks key blocks per CTA: fewer would cost more to merge than they save
-        const long long want = (total + kPagedMinBlocks - 1) / kPagedMinBlocks;
-        ctas = static_cast<int>(want < static_cast<long long>(gridDim.x) ? want : gridDim.x);
-        const int c = static_cast<int>(blockIdx.x);
-        if (c < ctas) {
-          range0 = c * total / ctas;
-          range1 = (c + 1) * total / ctas;
-        }
+        if (!one_pass) __syncthreads();
       }
     }
     if (tid == 0) bar->total = total;
@@ -261,6 +271,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tbase = bar->tmem_base;
+  // merge_kernel may be launched (its blocks fit only as these CTAs leave), and this kernel's own
+  // reads of chunk_list_kernel's list begin
+  if constexpr (!EVEN) asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
   if (warp < 4) {
     regs_dec<C::REG_LO>();
@@ -271,28 +285,32 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int my_page = static_cast<int>(lane) % np, my_chunk = static_cast<int>(lane) / np;
       const uint32_t q_bytes = static_cast<uint32_t>(a.kv_group * a.tile_tokens) * 128u * C::QCH;
       uint32_t ck = 0, cv = 0, cq = 0, seg_i = 0;  // copies and segments so far
+      uint32_t cs0 = 0, cs1 = 0, phase = 0;
       bool ok = true;
       // even split: where this CTA is
       int s = 0, hk = 0, kt = 0, unit = 0;
-      Bounds b{0, 0, 0};
+      Bounds b{0, 0, 0}, b_next{0, 0, 0};  // request s and, fetched ahead, s + 1
       long long g = range0;
       int merge_units = 0;  // units that begin in this range and end beyond it: at most one
+      auto fetch_next = [&]() {
+        if (s + 1 < a.num_seqs) b_next = bounds(a, s + 1);
+      };
       if constexpr (EVEN) {
         if (range0 < range1) {
           s = bar->first_seq;
-          b = bounds(a, s);
+          b = bar->first;
           unit = unit_blocks(a, b, b.nq - 1);
           const long long off = range0 - bar->first_start;
           hk = static_cast<int>(off / unit);
           kt = static_cast<int>(off - static_cast<long long>(hk) * unit);
+          fetch_next();
         }
       }
-      int item = static_cast<int>(blockIdx.x);  // list: this CTA's entry
+      int item = static_cast<int>(blockIdx.x);  // list: this CTA's next entry
       const int n_items = EVEN ? 0 : *a.n_items;
-      while (ok) {
-        // ---- the next segment
+      auto next_seg = [&]() -> Seg {
         Seg w;
-        w.more = 0;
+        w.more = 0, w.n0 = w.n1 = 0;
         if constexpr (EVEN) {
           if (g < range1) {
             const int take = static_cast<int>(min(static_cast<long long>(unit - kt), range1 - g));
@@ -316,7 +334,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (g < range1 && ++hk == a.heads_kv) {  // (the unit ended, or the range did)
               hk = 0;
               do {
-                b = bounds(a, ++s);
+                b = b_next, ++s;
+                fetch_next();
               } while (b.nq == 0 && s + 1 < a.num_seqs);
               unit = unit_blocks(a, b, b.nq - 1);
             }
@@ -324,35 +343,49 @@ __global__ void __launch_bounds__(kThreads, 1)
         } else {
           if (item < n_items) {
             const ChunkItem it = a.items[item];
+            int nx = 0;
+            if (lane == 0) nx = atomicAdd(a.next_item, 1);  // needed one segment later
             b = bounds(a, it.seq);
             w = make_seg(a, b, it.seq, it.hk, it.tok0, min(b.nq - it.tok0, 2 * a.tile_tokens), it.kt0, it.kt1, it.part);
-            int nx = 0;
-            if (lane == 0) nx = atomicAdd(a.next_item, 1);
             item = __shfl_sync(0xffffffffu, nx, 0);
           }
         }
+        return w;
+      };
+      // this lane's page of key block kt0 + j; num_pages (its boxes read zeros) past the last key
+      auto page_of = [&](const Seg& w, int j) -> int {
+        const long long key = (static_cast<long long>(w.kt0 + j) << 7) + (static_cast<long long>(my_page) << a.page_shift);
+        if (key >= w.nk) return a.num_pages;
+        const int pg = __ldg(a.block_table + w.seq * a.block_table_stride + (key >> a.page_shift));
+        return pg < 0 || pg > a.num_pages ? a.num_pages : pg;
+      };
+      Seg w = next_seg();
+      int page = w.more ? page_of(w, 0) : 0;
+      for (;;) {
         const int slot = static_cast<int>(seg_i % kSegs);
         ok = mbar_wait_warp(&bar->seg_empty[slot], ((seg_i / kSegs) & 1u) ^ 1u, a.status, 0x3100);
         if (!ok) break;
+        const int n = max(w.n0, w.n1);
         if (lane == 0) {
+          w.v0 = cv, w.s0 = cs0, w.s1 = cs1, w.phase = phase;
           sSeg[slot] = w;
           mbar_arrive(&bar->seg_full[slot]);
         }
         ++seg_i;
         if (!w.more) break;
-        // ---- its copies
-        const int n = max(w.n0, w.n1);
-        if (n == 0) continue;
-        const int* table = a.block_table + w.seq * a.block_table_stride;
-        auto page_of = [&](int j) -> int {  // this lane's page of key block kt0 + j; num_pages (zeros) past the end
-          const long long key = (static_cast<long long>(w.kt0 + j) << 7) + (static_cast<long long>(my_page) << a.page_shift);
-          if (key >= w.nk) return a.num_pages;
-          const int pg = __ldg(table + (key >> a.page_shift));
-          return pg < 0 || pg > a.num_pages ? a.num_pages : pg;
-        };
-        int page = page_of(0);
+        cs0 += w.dual ? (w.n0 + 1) / 2 : w.n0;
+        cs1 += w.dual ? w.n0 / 2 : w.n1;
+        phase ^= (w.n0 > 0 ? 1u : 0u) | ((w.dual ? w.n0 > 1 : w.n1 > 0) ? 2u : 0u) | (w.dual ? 4u : 0u);
+        // ---- its copies; the next segment and its first page are looked up behind the first few
+        Seg nw;
+        nw.more = 0;
+        int npage = 0;
+        if (n == 0) {
+          nw = next_seg();
+          npage = nw.more ? page_of(nw, 0) : 0;
+        }
         for (int j = 0; j < n; ++j) {
-          const int next = j + 1 < n ? page_of(j + 1) : 0;  // fetched ahead of the waits
+          const int next = j + 1 < n ? page_of(w, j + 1) : 0;  // fetched ahead of the waits
           const int row = a.page_size > BN ? ((w.kt0 + j) << 7) & (a.page_size - 1) : 0;
           const uint32_t ks = ck % C::NK;
           ok = mbar_wait_warp(&bar->k_empty[ks], ((ck / C::NK) & 1u) ^ 1u, a.status, 0x3110);
@@ -386,7 +419,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                         my_chunk * 64, w.hk, row, page);
           ++cv;
           page = next;
+          if (j == min(n - 1, C::NK - 1)) {
+            nw = next_seg();
+            npage = nw.more ? page_of(nw, 0) : 0;
+          }
         }
+        if (!ok) break;
+        w = nw;
+        page = npage;
       }
       if (EVEN && merge_units == 0 && lane == 0) a.merge[blockIdx.x].n = 0;
       if (!ok) {  // let the copies in flight land before the CTA exits
@@ -423,7 +463,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         ok = mbar_wait(&bar->seg_full[slot], (seg_i / kSegs) & 1u, a.status, 0x3200);
         if (!ok) break;
         const Seg* w = sSeg + slot;
-        const int more = w->more, n0 = w->n0, n1 = w->n1, dual = w->dual;
+        const int more = w->more, n0 = w->n0, n1 = w->n1;
+        const bool dual = EVEN || w->dual != 0;
         mbar_arrive(&bar->seg_empty[slot]);
         if (!more) break;
         const int n = max(n0, n1);
@@ -507,194 +548,198 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ======================= softmax and output =============================
     const int i = (static_cast<int>(warp) - 4) / 4;  // tile or stream
     const uint32_t quarter = warp & 3u;
-    const int r = static_cast<int>(quarter * 32 + lane);  // row of the tile
-    const int r_tok = r / a.kv_group, r_head = r - r_tok * a.kv_group;
-    const bool r_used = r < a.kv_group * a.tile_tokens;
     const uint32_t lane_base = tbase + ((quarter * 32u) << 16);
-    const float sl2 = a.scale_log2;
-    const int np = a.page_size < BN ? BN >> a.page_shift : 1;
-    // segments, blocks of this stream, V blocks, dual segments, and segments in which each O was written
-    uint32_t seg_i = 0, cs = 0, cv0 = 0, cx = 0, co0 = 0, co1 = 0;
+    // This thread's row of a segment: token and head of the group (divided anew where needed).
+    auto row_tok = [&](int dual) {
+      const int r = static_cast<int>(quarter * 32 + lane);
+      return r / a.kv_group + (EVEN || dual ? 0 : i * a.tile_tokens);
+    };
+    auto row_valid = [&](const volatile Seg& w) {
+      const int r = static_cast<int>(quarter * 32 + lane);
+      return r < a.kv_group * a.tile_tokens && row_tok(EVEN || w.dual) < w.ntok;
+    };
     bool ok = true;
-    for (;;) {
-      const int slot = static_cast<int>(seg_i % kSegs);
-      ok = mbar_wait_warp(&bar->seg_full[slot], (seg_i / kSegs) & 1u, a.status, 0x3300);
-      if (!ok) break;
+    for (uint32_t seg_i = 0;; ++seg_i) {
       // read where needed (volatile: not kept in registers across the blocks' loop)
-      const volatile Seg& w = sSeg[slot];
-      if (!w.more) break;
-      const int mine = w.dual ? (w.n0 + 1 - i) / 2 : (i == 0 ? w.n0 : w.n1);
-      const int tok = r_tok + (w.dual ? 0 : i * a.tile_tokens);
-      const bool valid = r_used && tok < w.ntok;
-      const int pos = w.pos0 + tok;  // the row's position among the keys
-      const int klim = !valid ? 0 : (a.causal ? max(0, min(w.nk, pos + 1)) : w.nk);
-      const bool work = __any_sync(0xffffffffu, valid);  // a warp without rows only keeps the barriers in step
-      const float slope =
-          MOD == kModAlibi && valid ? fabsf(__ldg(a.alibi_slopes + w.hk * a.kv_group + r_head) * a.inv_scale) : 0.f;
-      // pages of key block kt that hold keys (one bit per page, the lanes' ballot)
-      auto page_ok = [&](int kt) -> bool {
-        const long long key = (static_cast<long long>(kt) << 7) + (static_cast<long long>(lane) << a.page_shift);
-        if (static_cast<int>(lane) >= np || key >= w.nk) return true;
-        const int pg = __ldg(a.block_table + w.seq * a.block_table_stride + (key >> a.page_shift));
-        return pg >= 0 && pg < a.num_pages;
-      };
+      const volatile Seg& w = sSeg[seg_i % kSegs];
+      ok = mbar_wait_warp(&bar->seg_full[seg_i % kSegs], (seg_i / kSegs) & 1u, a.status, 0x3300);
+      if (!ok || !w.more) break;
       float m_used = -INFINITY, l = 0.f;
-      const int dual = w.dual, step = dual ? 2 : 1;
-      int kt = w.kt0 + (dual ? i : 0);
-      bool pg_ok = mine > 0 ? page_ok(kt) : true;
-      for (int j = 0; j < mine; ++j, kt += step) {
-        const uint32_t pages = __ballot_sync(0xffffffffu, pg_ok);
-        if (j + 1 < mine) pg_ok = page_ok(kt + step);  // fetched one block ahead
-        ok = mbar_wait_warp(&bar->s_full[i], cs & 1u, a.status, 0x3310 + i);
-        if (!ok) break;
-        ++cs;
-        tc_fence_after();
-        if (work) {
-          uint32_t s[BN];
-          tmem_ld32(lane_base + tS(i) + 0, *reinterpret_cast<uint32_t(*)[32]>(&s[0]));
-          tmem_ld32(lane_base + tS(i) + 32, *reinterpret_cast<uint32_t(*)[32]>(&s[32]));
-          tmem_ld32(lane_base + tS(i) + 64, *reinterpret_cast<uint32_t(*)[32]>(&s[64]));
-          tmem_ld32(lane_base + tS(i) + 96, *reinterpret_cast<uint32_t(*)[32]>(&s[96]));
-          tmem_wait_ld();
-          if constexpr (MOD == kModSoftcap) {
+      {
+        const bool valid = row_valid(w);
+        const int pos = w.pos0 + row_tok(w.dual);  // the row's position among the keys
+        const int klim = !valid ? 0 : (a.causal ? max(0, min(w.nk, pos + 1)) : w.nk);
+        const bool work = __any_sync(0xffffffffu, valid);  // a warp without rows only keeps the barriers in step
+        float slope = 0.f;
+        if (MOD == kModAlibi && valid)
+          slope = fabsf(__ldg(a.alibi_slopes + w.hk * a.kv_group + static_cast<int>(quarter * 32 + lane) % a.kv_group) *
+                        a.inv_scale);
+        // whether this lane's page of key block kt holds keys (one lane per page of a block)
+        auto page_ok = [&](int kt) -> bool {
+          const int np = a.page_size < BN ? BN >> a.page_shift : 1;
+          const long long key = (static_cast<long long>(kt) << 7) + (static_cast<long long>(lane) << a.page_shift);
+          if (static_cast<int>(lane) >= np || key >= w.nk) return true;
+          const int pg = __ldg(a.block_table + w.seq * a.block_table_stride + (key >> a.page_shift));
+          return pg >= 0 && pg < a.num_pages;
+        };
+        const int step = EVEN || w.dual ? 2 : 1;
+        int kt = w.kt0 + (EVEN || w.dual ? i : 0);
+        const int kt_end = w.kt0 + (EVEN || w.dual || i == 0 ? w.n0 : w.n1);
+        uint32_t s_phase = i == 0 ? w.s0 : w.s1;
+        bool first = true;
+        bool pg_ok = kt < kt_end ? page_ok(kt) : true;
+        for (; kt < kt_end; kt += step, ++s_phase, first = false) {
+          const uint32_t pages = __ballot_sync(0xffffffffu, pg_ok);
+          if (kt + step < kt_end) pg_ok = page_ok(kt + step);  // fetched one block ahead
+          ok = mbar_wait_warp(&bar->s_full[i], s_phase & 1u, a.status, 0x3310 + i);
+          if (!ok) break;
+          tc_fence_after();
+          if (work) {
+            uint32_t s[BN];
+            tmem_ld32(lane_base + tS(i) + 0, *reinterpret_cast<uint32_t(*)[32]>(&s[0]));
+            tmem_ld32(lane_base + tS(i) + 32, *reinterpret_cast<uint32_t(*)[32]>(&s[32]));
+            tmem_ld32(lane_base + tS(i) + 64, *reinterpret_cast<uint32_t(*)[32]>(&s[64]));
+            tmem_ld32(lane_base + tS(i) + 96, *reinterpret_cast<uint32_t(*)[32]>(&s[96]));
+            tmem_wait_ld();
+            if constexpr (MOD == kModSoftcap) {
 #pragma unroll
-            for (int c = 0; c < BN; ++c) s[c] = __float_as_uint(a.mod_b * tanh_scaled(__uint_as_float(s[c]), a.mod_k2));
-          } else if constexpr (MOD == kModAlibi) {
-            const float base = slope * static_cast<float>(kt * BN - pos);
+              for (int c = 0; c < BN; ++c) s[c] = __float_as_uint(a.mod_b * tanh_scaled(__uint_as_float(s[c]), a.mod_k2));
+            } else if constexpr (MOD == kModAlibi) {
+              const float base = slope * static_cast<float>(kt * BN - pos);
 #pragma unroll
-            for (int c = 0; c < BN; ++c)
-              s[c] = __float_as_uint(__uint_as_float(s[c]) - fabsf(fmaf(slope, static_cast<float>(c), base)));
-          }
-          const int cnt = klim - kt * BN;  // visible keys of this row in the block
-          if (cnt < BN) {
+              for (int c = 0; c < BN; ++c)
+                s[c] = __float_as_uint(__uint_as_float(s[c]) - fabsf(fmaf(slope, static_cast<float>(c), base)));
+            }
+            const int cnt = klim - kt * BN;  // visible keys of this row in the block
+            if (cnt < BN) {
 #pragma unroll
-            for (int c = 0; c < BN; ++c)
-              if (c >= cnt) s[c] = __float_as_uint(-INFINITY);
-          }
-          if (pages != 0xffffffffu) {  // keys on pages outside the cache (warp-uniform branch)
-            const int sh = a.page_size < BN ? a.page_shift : 7;
+              for (int c = 0; c < BN; ++c)
+                if (c >= cnt) s[c] = __float_as_uint(-INFINITY);
+            }
+            if (pages != 0xffffffffu) {  // keys on pages outside the cache (warp-uniform branch)
+              const int sh = a.page_size < BN ? a.page_shift : 7;
 #pragma unroll
-            for (int c = 0; c < BN; c += 16)
-              if (!((pages >> (c >> sh)) & 1u)) {
+              for (int c = 0; c < BN; c += 16)
+                if (!((pages >> (c >> sh)) & 1u)) {
 #pragma unroll
-                for (int u = 0; u < 16; ++u) s[c + u] = __float_as_uint(-INFINITY);
+                  for (int u = 0; u < 16; ++u) s[c + u] = __float_as_uint(-INFINITY);
+                }
+            }
+            float mp[8];
+#pragma unroll
+            for (int c = 0; c < 8; ++c) mp[c] = fmaxf(__uint_as_float(s[c]), __uint_as_float(s[c + 8]));
+#pragma unroll
+            for (int c = 16; c < BN; c += 16)
+#pragma unroll
+              for (int z = 0; z < 8; ++z) mp[z] = fmax3(mp[z], __uint_as_float(s[c + z]), __uint_as_float(s[c + 8 + z]));
+            const float mx = fmax3(fmax3(mp[0], mp[1], mp[2]), fmax3(mp[3], mp[4], mp[5]), fmaxf(mp[6], mp[7]));
+            const float sl2 = a.scale_log2;
+            const float m_tile = mx * sl2;
+            const bool need = m_tile > m_used + kThreshold;
+            float alpha = 1.f;
+            if (need) {
+              alpha = (m_used == -INFINITY) ? 0.f : ex2_mufu(m_used - m_tile);
+              m_used = m_tile;
+            }
+            l *= alpha;
+            const float mu = (m_used == -INFINITY) ? 0.f : m_used;
+            uint32_t pk[BN / 2];
+            float2 rs[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+            const float2 sl2v = make_float2(sl2, sl2), negmu = make_float2(-mu, -mu);
+#pragma unroll
+            for (int c = 0; c < BN / 2; ++c) {
+              const float2 x = ffma2(make_float2(__uint_as_float(s[2 * c]), __uint_as_float(s[2 * c + 1])), sl2v, negmu);
+              const float2 p = make_float2(ex2_mufu(x.x), ex2_mufu(x.y));
+              pk[c] = pack_bf16x2(p.x, p.y);
+              rs[c & 1] = fadd2(rs[c & 1], p);
+            }
+            l += (rs[0].x + rs[0].y) + (rs[1].x + rs[1].y);
+            tmem_st32(lane_base + tS(i) + 0, *reinterpret_cast<uint32_t(*)[32]>(&pk[0]));
+            tmem_st32(lane_base + tS(i) + 32, *reinterpret_cast<uint32_t(*)[32]>(&pk[32]));
+            if (!first && __any_sync(0xffffffffu, need)) {
+#pragma unroll
+              for (int c = 0; c < DV / 32; ++c) {
+                uint32_t o[32];
+                tmem_ld32(lane_base + tO(i) + c * 32, o);
+                tmem_wait_ld();
+#pragma unroll
+                for (int t = 0; t < 32; ++t) o[t] = __float_as_uint(__uint_as_float(o[t]) * alpha);
+                tmem_st32(lane_base + tO(i) + c * 32, o);
               }
-          }
-          float mp[8];
-#pragma unroll
-          for (int c = 0; c < 8; ++c) mp[c] = fmaxf(__uint_as_float(s[c]), __uint_as_float(s[c + 8]));
-#pragma unroll
-          for (int c = 16; c < BN; c += 16)
-#pragma unroll
-            for (int z = 0; z < 8; ++z) mp[z] = fmax3(mp[z], __uint_as_float(s[c + z]), __uint_as_float(s[c + 8 + z]));
-          const float mx = fmax3(fmax3(mp[0], mp[1], mp[2]), fmax3(mp[3], mp[4], mp[5]), fmaxf(mp[6], mp[7]));
-          const float m_tile = mx * sl2;
-          const bool need = m_tile > m_used + kThreshold;
-          float alpha = 1.f;
-          if (need) {
-            alpha = (m_used == -INFINITY) ? 0.f : ex2_mufu(m_used - m_tile);
-            m_used = m_tile;
-          }
-          l *= alpha;
-          const float mu = (m_used == -INFINITY) ? 0.f : m_used;
-          uint32_t pk[BN / 2];
-          float2 rs[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-          const float2 sl2v = make_float2(sl2, sl2), negmu = make_float2(-mu, -mu);
-#pragma unroll
-          for (int c = 0; c < BN / 2; ++c) {
-            const float2 x = ffma2(make_float2(__uint_as_float(s[2 * c]), __uint_as_float(s[2 * c + 1])), sl2v, negmu);
-            const float2 p = make_float2(ex2_mufu(x.x), ex2_mufu(x.y));
-            pk[c] = pack_bf16x2(p.x, p.y);
-            rs[c & 1] = fadd2(rs[c & 1], p);
-          }
-          l += (rs[0].x + rs[0].y) + (rs[1].x + rs[1].y);
-          tmem_st32(lane_base + tS(i) + 0, *reinterpret_cast<uint32_t(*)[32]>(&pk[0]));
-          tmem_st32(lane_base + tS(i) + 32, *reinterpret_cast<uint32_t(*)[32]>(&pk[32]));
-          if (j > 0 && __any_sync(0xffffffffu, need)) {
-#pragma unroll
-            for (int c = 0; c < DV / 32; ++c) {
-              uint32_t o[32];
-              tmem_ld32(lane_base + tO(i) + c * 32, o);
-              tmem_wait_ld();
-#pragma unroll
-              for (int t = 0; t < 32; ++t) o[t] = __float_as_uint(__uint_as_float(o[t]) * alpha);
-              tmem_st32(lane_base + tO(i) + c * 32, o);
             }
           }
+          // The request's last block: cache rows past its last key, on the page that holds it, may be
+          // anything (0 x NaN is NaN), so they are zeroed before the PV product reads them. Tile 0's
+          // warps do it where it has this block: its PV comes first and waits for them.
+          const int tail = w.nk - kt * BN;  // keys of the request in this block
+          if (tail < BN && tail > 0 && (tail & (a.page_size - 1)) != 0 && (w.dual || i == 0 || kt >= w.kt0 + w.n0)) {
+            const uint32_t u = w.v0 + static_cast<uint32_t>(kt - w.kt0), vs = u % C::NV;
+            // one slot: the block before may not have been read yet, and its phase of v_full not have come
+            if (C::NV == 1 && u > 0) ok = mbar_wait_warp(&bar->v_empty[0], (u - 1) & 1u, a.status, 0x3321);
+            ok = ok && mbar_wait_warp(&bar->v_full[vs], (u / C::NV) & 1u, a.status, 0x3320);
+            if (!ok) break;
+            const int end = min(BN, (tail | (a.page_size - 1)) + 1);
+            uint8_t* v = sV + vs * C::V_BYTES;
+            const int units = (end - tail) * 8;  // 16-byte pieces of a chunk
+            for (int x = static_cast<int>(quarter * 32 + lane); x < units * C::VCH; x += 128)
+              *reinterpret_cast<uint4*>(v + (x / units) * kChunk + tail * 128 + (x % units) * 16) = make_uint4(0, 0, 0, 0);
+            fence_proxy_async_smem();
+          }
+          tmem_wait_st();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bar->p_full[i]);
         }
-        // The request's last block: cache rows past its last key, on the page that holds it, may be
-        // anything (0 x NaN is NaN), so they are zeroed before the PV product reads them. Tile 0's
-        // warps do it where it has this block: its PV comes first and waits for them.
-        const int tail = w.nk - kt * BN;  // keys of the request in this block
-        if (tail < BN && tail > 0 && (tail & (a.page_size - 1)) != 0 && (w.dual || i == 0 || j >= w.n0)) {
-          const uint32_t u = cv0 + static_cast<uint32_t>(w.dual ? 2 * j + i : j), vs = u % C::NV;
-          // one slot: the block before may not have been read yet, and its phase of v_full not have come
-          if (C::NV == 1 && u > 0) ok = mbar_wait_warp(&bar->v_empty[0], (u - 1) & 1u, a.status, 0x3321);
-          ok = ok && mbar_wait_warp(&bar->v_full[vs], (u / C::NV) & 1u, a.status, 0x3320);
-          if (!ok) break;
-          const int end = min(BN, (tail | (a.page_size - 1)) + 1);
-          uint8_t* v = sV + vs * C::V_BYTES;
-          const int units = (end - tail) * 8;  // 16-byte pieces of a chunk
-          for (int x = r; x < units * C::VCH; x += 128)
-            *reinterpret_cast<uint4*>(v + (x / units) * kChunk + tail * 128 + (x % units) * 16) = make_uint4(0, 0, 0, 0);
-          fence_proxy_async_smem();
-        }
-        tmem_wait_st();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bar->p_full[i]);
       }
       if (!ok) break;
-      cv0 += static_cast<uint32_t>(max(w.n0, w.n1));
       // ---- output
-      const bool has0 = w.dual ? w.n0 > 0 : mine > 0;  // O_0 (dual) or this tile's O was written
-      const bool has1 = w.dual && w.n0 > 1;
-      const uint32_t po0 = co0 & 1u, po1 = co1 & 1u;
-      co0 += w.n0 > 0;
-      co1 += w.dual ? w.n0 > 1 : w.n1 > 0;
-      float inv_l, lse2;     // tile: 1 / l and the LSE in log2 units
-      float w0 = 0.f, w1 = 0.f;  // dual: weights of the streams' O
+      const bool dual = EVEN || w.dual != 0;
+      const bool has0 = (dual || i == 0 ? w.n0 : w.n1) > 0;  // O_0 (dual) or this tile's O was written
+      const bool has1 = dual && w.n0 > 1;
       // every warp has left the segment before (its reads of sX among them)
       if (seg_i > 0) ok = mbar_wait_warp(&bar->o_free, (seg_i - 1) & 1u, a.status, 0x3328);
       if (!ok) break;
-      if (w.dual) {
-        float2* x = sX;
-        x[i * BM + r] = make_float2(m_used, l);
+      const int r = static_cast<int>(quarter * 32 + lane);
+      float lse2;      // the row's LSE in log2 units
+      float w0, w1 = 0.f;  // weights of O_0 (or this tile's O) and, dual, of O_1
+      if (dual) {
+        sX[i * BM + r] = make_float2(m_used, l);
         __syncwarp();
         if (lane == 0) mbar_arrive(&bar->x_full[i]);
-        ok = mbar_wait_warp(&bar->x_full[1 - i], cx & 1u, a.status, 0x3330);
+        ok = mbar_wait_warp(&bar->x_full[1 - i], (w.phase >> 2) & 1u, a.status, 0x3330);
         if (!ok) break;
-        ++cx;
-        const float2 y = x[(1 - i) * BM + r];
+        const float2 y = sX[(1 - i) * BM + r];
         const float ma = i == 0 ? m_used : y.x, la = i == 0 ? l : y.y, mb = i == 0 ? y.x : m_used, lb = i == 0 ? y.y : l;
         const float mm = fmaxf(ma, mb);
         const float ea = la > 0.f ? ex2_mufu(ma - mm) : 0.f, eb = lb > 0.f ? ex2_mufu(mb - mm) : 0.f;
         const float lt = la * ea + lb * eb;
-        inv_l = lt > 0.f ? 1.f / lt : 0.f;
+        const float inv_l = lt > 0.f ? 1.f / lt : 0.f;
         lse2 = lt > 0.f ? mm + log2f(lt) : -INFINITY;
         w0 = ea * inv_l, w1 = eb * inv_l;
         // (the exchange above also says that the other warpgroup has left the segment before, so
         // that its O barrier is at most one phase behind)
-        if (has0) ok = mbar_wait_warp(&bar->o_full[0], po0, a.status, 0x3340);
-        if (ok && has1) ok = mbar_wait_warp(&bar->o_full[1], po1, a.status, 0x3341);
+        if (has0) ok = mbar_wait_warp(&bar->o_full[0], w.phase & 1u, a.status, 0x3340);
+        if (ok && has1) ok = mbar_wait_warp(&bar->o_full[1], (w.phase >> 1) & 1u, a.status, 0x3341);
       } else {
-        inv_l = l > 0.f ? 1.f / l : 0.f;
+        w0 = l > 0.f ? 1.f / l : 0.f;
         lse2 = l > 0.f ? m_used + log2f(l) : -INFINITY;
-        if (has0) ok = mbar_wait_warp(&bar->o_full[i], i == 0 ? po0 : po1, a.status, 0x3340 + i);
+        if (has0) ok = mbar_wait_warp(&bar->o_full[i], (w.phase >> i) & 1u, a.status, 0x3340 + i);
       }
       if (!ok) break;
       tc_fence_after();
-      const int head = w.hk * a.kv_group + r_head;
-      const int c_lo = w.dual ? i * (DV / 64) : 0, c_hi = w.dual ? (i + 1) * (DV / 64) : DV / 32;  // 32-column groups
-      const int64_t prow = static_cast<int64_t>(w.part) * a.part_rows + (w.dual ? 0 : i * BM) + r;
-      __nv_bfloat16* orow = a.o + static_cast<int64_t>(w.q_row + tok) * a.o_row + static_cast<int64_t>(head) * a.o_head;
-      if (work) {
+      const int tok = row_tok(dual), head = w.hk * a.kv_group + r % a.kv_group, part = w.part;
+      const bool valid = row_valid(w);
+      if (__any_sync(0xffffffffu, valid)) {
+        const int c_lo = dual ? i * (DV / 64) : 0, c_hi = dual ? (i + 1) * (DV / 64) : DV / 32;  // 32-column groups
+        const int64_t prow = static_cast<int64_t>(part) * a.part_rows + (dual ? 0 : i * BM) + r;
+        __nv_bfloat16* orow = a.o + static_cast<int64_t>(w.q_row + tok) * a.o_row + static_cast<int64_t>(head) * a.o_head;
+#pragma unroll 1
         for (int c = c_lo; c < c_hi; ++c) {
-          uint32_t o[32];
-          if (w.dual) {
+          uint32_t o[32];  // (columns never written are read too, but not used)
+          tmem_ld32(lane_base + (dual ? tO(0) : tO(i)) + c * 32, o);
+          if (dual) {
             uint32_t o1[32];
-            if (has0) tmem_ld32(lane_base + tO(0) + c * 32, o);
-            if (has1) tmem_ld32(lane_base + tO(1) + c * 32, o1);
+            tmem_ld32(lane_base + tO(1) + c * 32, o1);
             tmem_wait_ld();
 #pragma unroll
             for (int t = 0; t < 32; ++t) {
@@ -702,15 +747,12 @@ __global__ void __launch_bounds__(kThreads, 1)
               o[t] = __float_as_uint(has1 ? fmaf(__uint_as_float(o1[t]), w1, x0) : x0);
             }
           } else {
-            if (has0) {
-              tmem_ld32(lane_base + tO(i) + c * 32, o);
-              tmem_wait_ld();
-            }
+            tmem_wait_ld();
 #pragma unroll
-            for (int t = 0; t < 32; ++t) o[t] = __float_as_uint(has0 ? __uint_as_float(o[t]) * inv_l : 0.f);
+            for (int t = 0; t < 32; ++t) o[t] = __float_as_uint(has0 ? __uint_as_float(o[t]) * w0 : 0.f);
           }
           if (valid) {
-            if (w.part >= 0) {
+            if (part >= 0) {
               float4* op = reinterpret_cast<float4*>(a.part_o + prow * DV) + c * 8;
 #pragma unroll
               for (int t = 0; t < 8; ++t)
@@ -724,8 +766,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
         }
-        if (valid && (!w.dual || i == 0)) {
-          if (w.part >= 0) a.part_lse[prow] = lse2;
+        if (valid && (!dual || i == 0)) {
+          if (part >= 0) a.part_lse[prow] = lse2;
           else a.lse[static_cast<int64_t>(head) * a.total_q + w.q_row + tok] = lse2 * 0.69314718055994531f;
         }
       }
@@ -733,9 +775,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
       if (lane == 0) {
         mbar_arrive(&bar->o_free);
-        mbar_arrive(&bar->seg_empty[slot]);
+        mbar_arrive(&bar->seg_empty[seg_i % kSegs]);
       }
-      ++seg_i;
     }
   }
 
@@ -745,17 +786,24 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 1) tmem_dealloc(tbase, 512);
 }
 
-// Merges the units that were cut: with the segments' LSE_r in log2 units, M their
+// Merges the units that were cut, launched while paged_kernel still runs (it waits for
+// it below): with the segments' LSE_r in log2 units, M their
 // maximum, O = sum_r 2^(LSE_r - M) O_r / sum_r 2^(LSE_r - M), the segments in key
-// order. One warp per row; lane l holds columns [DV/32 l, DV/32 (l + 1)).
-template <int DV>
+// order within a warp and then warp after warp. Bound by latency: WPR warps share a row,
+// each taking every WPR-th segment (8 where rows are few, as in decoding, else 1); lane l
+// holds columns [DV/32 l, DV/32 (l + 1)).
+template <int DV, int WPR>
 __global__ void __launch_bounds__(256) merge_kernel(const PagedArgs a) {
   constexpr int CPL = DV / 32;
+  __shared__ float s_acc[WPR > 1 ? WPR : 1][DV];
+  __shared__ float s_sum[WPR > 1 ? WPR : 1];
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   const MergeUnit m = a.merge[blockIdx.x];
   if (m.n < 1) return;
-  const int lane = static_cast<int>(threadIdx.x & 31u);
-  const int rr = static_cast<int>(blockIdx.y * 8 + (threadIdx.x >> 5));
-  if (rr >= m.ntok * a.kv_group) return;
+  const int lane = static_cast<int>(threadIdx.x & 31u), warp = static_cast<int>(threadIdx.x >> 5);
+  const int rr = WPR > 1 ? static_cast<int>(blockIdx.y) : static_cast<int>(blockIdx.y * 8 + warp);
+  const int part = WPR > 1 ? warp : 0;
+  if (rr >= m.ntok * a.kv_group) return;  // (whole blocks where WPR > 1)
   const int tok = rr / a.kv_group, hd = rr - tok * a.kv_group, tile = tok / a.tile_tokens;
   const int row = tile * BM + (tok - tile * a.tile_tokens) * a.kv_group + hd;
   auto at = [&](int r) -> int64_t {
@@ -770,7 +818,7 @@ __global__ void __launch_bounds__(256) merge_kernel(const PagedArgs a) {
   for (int c = 0; c < CPL; ++c) acc[c] = 0.f;
   if (mx != -INFINITY) {
 #pragma unroll 4
-    for (int r = 0; r < m.n; ++r) {
+    for (int r = part; r < m.n; r += WPR) {
       const int64_t x = at(r);
       const float wr = ex2_mufu(a.part_lse[x] - mx);
       sum += wr;
@@ -786,6 +834,22 @@ __global__ void __launch_bounds__(256) merge_kernel(const PagedArgs a) {
         acc[0] = fmaf(wr, v.x, acc[0]);
         acc[1] = fmaf(wr, v.y, acc[1]);
       }
+    }
+  }
+  if constexpr (WPR > 1) {
+#pragma unroll
+    for (int c = 0; c < CPL; ++c) s_acc[warp][lane * CPL + c] = acc[c];
+    if (lane == 0) s_sum[warp] = sum;
+    __syncthreads();
+    if (warp != 0) return;
+    sum = 0.f;
+#pragma unroll
+    for (int c = 0; c < CPL; ++c) acc[c] = 0.f;
+#pragma unroll
+    for (int w = 0; w < WPR; ++w) {
+      sum += s_sum[w];
+#pragma unroll
+      for (int c = 0; c < CPL; ++c) acc[c] += s_acc[w][lane * CPL + c];
     }
   }
   const float inv = sum > 0.f ? 1.f / sum : 0.f;
@@ -810,8 +874,9 @@ constexpr int kListThreads = 1024, kBins = 2048;
 __global__ void __launch_bounds__(kListThreads, 1) chunk_list_kernel(const PagedArgs a, int ctas) {
   __shared__ int bins[kBins];
   __shared__ long long sums[kListThreads / 32];
-  __shared__ int chunk_sum[kListThreads];
+  __shared__ int warp_items[kListThreads / 32];
   __shared__ int n_slots, n_merge;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // paged_kernel sets itself up meanwhile
   const int tid = static_cast<int>(threadIdx.x), lane = tid & 31, warp = tid >> 5;
   const int unit_tokens = 2 * a.tile_tokens;
   for (int x = tid; x < kBins; x += kListThreads) bins[x] = 0;
@@ -831,9 +896,12 @@ __global__ void __launch_bounds__(kListThreads, 1) chunk_list_kernel(const Paged
   w = 0;
   for (int x = 0; x < kListThreads / 32; ++x) w += sums[x];
   w *= a.heads_kv;
-  const long long cap = max(static_cast<long long>(kPagedMinItem), (w + ctas - 1) / ctas);
+  // an equal share of the work (a unit costs less than 2^26)
+  const uint32_t cap = static_cast<uint32_t>(
+      min(max(static_cast<long long>(kPagedMinItem), (w + ctas - 1) / ctas), static_cast<long long>(1) << 30));
   auto cuts = [&](const Bounds& b, int tok0) -> int {
-    return static_cast<int>((static_cast<long long>(blocks(b, tok0)) * weight(b, tok0) + cap - 1) / cap);
+    const uint32_t c = static_cast<uint32_t>(blocks(b, tok0) * weight(b, tok0));
+    return c <= cap ? 1 : static_cast<int>((c + cap - 1) / cap);
   };
   auto bin_of = [&](const Bounds& b) { return kBins - 1 - min(kBins - 1, ceil_div(b.nk, BN)); };  // most keys first
   for (int s = tid; s < a.num_seqs; s += kListThreads) {
@@ -845,20 +913,25 @@ __global__ void __launch_bounds__(kListThreads, 1) chunk_list_kernel(const Paged
     if (n > 0) atomicAdd(&bins[bin_of(b)], n);
   }
   __syncthreads();
-  // bins -> first item of each bin: every thread scans two bins, thread 0's warp the pairs' sums
+  // bins -> first item of each bin: two bins per thread, a scan per warp and over the warps' sums
   const int b0 = bins[2 * tid], b1 = bins[2 * tid + 1];
-  chunk_sum[tid] = b0 + b1;
-  __syncthreads();
-  for (int d = 1; d < kListThreads; d <<= 1) {
-    const int x = tid >= d ? chunk_sum[tid - d] : 0;
-    __syncthreads();
-    chunk_sum[tid] += x;
-    __syncthreads();
+  int inc = b0 + b1;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int x = __shfl_up_sync(0xffffffffu, inc, d);
+    if (lane >= d) inc += x;
   }
-  const int before = chunk_sum[tid] - b0 - b1;
+  if (lane == 31) warp_items[warp] = inc;
+  __syncthreads();
+  int before = inc - b0 - b1, total = 0;
+#pragma unroll
+  for (int x = 0; x < kListThreads / 32; ++x) {
+    const int y = warp_items[x];
+    if (x < warp) before += y;
+    total += y;
+  }
   bins[2 * tid] = before;
   bins[2 * tid + 1] = before + b0;
-  const int total = chunk_sum[kListThreads - 1];
   __syncthreads();
   for (int s = tid; s < a.num_seqs; s += kListThreads) {
     const int n = a.list_scratch[s];
@@ -910,10 +983,28 @@ __global__ void __launch_bounds__(kListThreads, 1) chunk_list_kernel(const Paged
   }
 }
 
+// A kernel that may be launched before the one ahead of it on the stream is over (it
+// waits with griddepcontrol.wait before it reads that kernel's results).
+template <typename K, typename... A>
+cudaError_t launch_early(K kern, dim3 grid, int threads, int smem, cudaStream_t stream, const A&... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute at{};
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, args...);
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
 template <int DQK, int DV, int MOD, bool EVEN>
 cudaError_t launch_main(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const PagedArgs& a, int ctas,
                         cudaStream_t stream) {
-  using C = Cfg<DQK, DV>;
+  using C = Cfg<DQK, DV, EVEN>;
   auto kern = paged_kernel<DQK, DV, MOD, EVEN>;
   static PerDeviceOnce once;
   const cudaError_t e = once.run([&]() -> cudaError_t {
@@ -926,8 +1017,11 @@ cudaError_t launch_main(const CUtensorMap& tq, const CUtensorMap& tk, const CUte
     return fa.numRegs * kThreads < C::REG_BUDGET ? cudaErrorInvalidConfiguration : cudaSuccess;
   });
   if (e != cudaSuccess) return e;
-  kern<<<ctas, kThreads, C::SMEM, stream>>>(tq, tk, tv, a);
-  return cudaGetLastError();
+  if constexpr (EVEN) {
+    kern<<<ctas, kThreads, C::SMEM, stream>>>(tq, tk, tv, a);
+    return cudaGetLastError();
+  }
+  return launch_early(kern, dim3(ctas), kThreads, C::SMEM, stream, tq, tk, tv, a);  // behind chunk_list_kernel
 }
 
 template <int DQK, int DV>
@@ -956,8 +1050,9 @@ cudaError_t launch_d(const CUtensorMap& tq, const CUtensorMap& tk, const CUtenso
   }
   if (e != cudaSuccess) return e;
   const int rows = min(a.max_q, (even ? 1 : 2) * a.tile_tokens) * a.kv_group;
-  merge_kernel<DV><<<dim3(ctas, (rows + 7) / 8), 256, 0, stream>>>(a);
-  return cudaGetLastError();
+  if (rows <= 16)  // the blocks of all rows fit the GPU at once
+    return launch_early(merge_kernel<DV, 8>, dim3(ctas, rows), 256, 0, stream, a);
+  return launch_early(merge_kernel<DV, 1>, dim3(ctas, (rows + 7) / 8), 256, 0, stream, a);
 }
 
 }  // namespace paged

@@ -143,17 +143,35 @@ __global__ void kv_plan_kernel(const KvPlanArgs a) {
     }
     for (int i = count + me; i < height - grow; i += all) a.free_pages[i] = stack(i);
     const int tokens = static_cast<int>(total.add);
-    for (int t = me; t < a.max_tokens; t += all) {
+    // four tokens in a row per thread where there are more tokens than threads: the request and the page are
+    // looked up again only where they change
+    const int run = a.max_tokens <= all ? 1 : 4;
+    for (int t0 = run * me; t0 < a.max_tokens; t0 += run * all) {
+      const int t1 = min(t0 + run, a.max_tokens);
       long long slot = -1;
-      if (t < tokens) {
-        const int s = owner(s_cu, n, t);
-        const int old = max(0, a.seqlens_old[s]), pos = old + (t - s_cu[s]);
-        const int have = static_cast<int>(pages(old)), pi = pos >> a.page_shift;
-        const int page = pi < have ? a.block_table[s * a.block_table_stride + pi]
-                                   : stack(height - 1 - (s_grow[s] + pi - have));
-        slot = (static_cast<long long>(page) << a.page_shift) + (pos & (a.page_size - 1));
+      int left = 0, end = t0;  // tokens left on the page; first token of the next request
+      int s = 0, pos = 0;
+      for (int t = t0; t < t1; ++t) {
+        if (t >= tokens) {
+          slot = -1;
+        } else if (left > 0 && t < end) {
+          ++slot, --left, ++pos;
+        } else {
+          if (t >= end || t == t0) {
+            s = owner(s_cu, n, t);
+            pos = max(0, a.seqlens_old[s]) + (t - s_cu[s]);
+            end = s_cu[s + 1];
+          } else {
+            ++pos;
+          }
+          const int have = static_cast<int>(pages(max(0, a.seqlens_old[s]))), pi = pos >> a.page_shift;
+          const int page = pi < have ? a.block_table[s * a.block_table_stride + pi]
+                                     : stack(height - 1 - (s_grow[s] + pi - have));
+          slot = (static_cast<long long>(page) << a.page_shift) + (pos & (a.page_size - 1));
+          left = a.page_size - 1 - (pos & (a.page_size - 1));
+        }
+        a.slot_mapping[t] = slot;
       }
-      a.slot_mapping[t] = slot;
     }
   } else {
     for (int t = me; t < a.max_tokens; t += all) a.slot_mapping[t] = -1;
@@ -179,16 +197,25 @@ __global__ void kv_plan_kernel(const KvPlanArgs a) {
 // A pure copy: 2 bytes read and written per element, HBM-bound for a prompt's
 // tokens, latency-bound for a decode step. One warp per (token, K or V): its
 // heads x d values are 16-byte units, lane after lane, so a row whose heads lie
-// side by side is read and written in whole 512-byte runs.
+// side by side is read and written in whole 512-byte runs, eight loads in
+// flight per lane before the first store.
 template <int D>
 __device__ __forceinline__ void append_row(const __nv_bfloat16* src, int64_t src_head, __nv_bfloat16* dst,
                                            int64_t dst_head, int heads, int lane) {
-  constexpr int UPH = D / 8;
+  constexpr int UPH = D / 8, N = 8;
   const int units = heads * UPH;
-#pragma unroll 4
-  for (int i = lane; i < units; i += 32) {
-    const int h = i / UPH, c = 8 * (i % UPH);
-    *reinterpret_cast<uint4*>(dst + h * dst_head + c) = *reinterpret_cast<const uint4*>(src + h * src_head + c);
+  for (int i0 = lane; i0 < units; i0 += 32 * N) {
+    uint4 x[N];
+#pragma unroll
+    for (int u = 0; u < N; ++u) {
+      const int i = i0 + 32 * u;
+      if (i < units) x[u] = __ldcs(reinterpret_cast<const uint4*>(src + (i / UPH) * src_head + 8 * (i % UPH)));
+    }
+#pragma unroll
+    for (int u = 0; u < N; ++u) {
+      const int i = i0 + 32 * u;
+      if (i < units) *reinterpret_cast<uint4*>(dst + (i / UPH) * dst_head + 8 * (i % UPH)) = x[u];
+    }
   }
 }
 

@@ -34,7 +34,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                      int descending, int max_nblk, TileEntry* out, int64_t* seq_start, int64_t bound) {
   __shared__ int bins[kMaxListBlocks + 1];          // sequences per block count, then cursors
   __shared__ long long bin_start[kMaxListBlocks + 1];  // first entry of each block count
-  __shared__ long long chunk_sum[kThreads];
+  __shared__ long long warp_sum[kThreads / 32];
   const int tid = static_cast<int>(threadIdx.x);
   const int nb = max_nblk + 1;
   for (int b = tid; b < nb; b += kThreads) bins[b] = 0;
@@ -51,7 +51,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   __syncthreads();
   // bin_start[b] = entries of all block counts above b: a scan from b = nb-1 down.
-  // Each thread sums a contiguous chunk of bins; thread 0 scans the chunk sums.
+  // Each thread sums a contiguous chunk of bins; the chunk sums are scanned by warp
+  // and over the warps (one thread's scan took most of the kernel: 11 us against 4).
   const int chunk = (nb + kThreads - 1) / kThreads;
   const int b_hi = nb - 1 - tid * chunk;  // this thread's chunk, from the top
   long long acc = 0;
@@ -60,18 +61,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (b < 1) break;
     acc += static_cast<long long>(bins[b]) * b * heads;
   }
-  chunk_sum[tid] = acc;
-  __syncthreads();
-  if (tid == 0) {
-    long long run = 0;
-    for (int t = 0; t < kThreads; ++t) {
-      const long long v = chunk_sum[t];
-      chunk_sum[t] = run;
-      run += v;
-    }
+  long long inc = acc;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const long long v = __shfl_up_sync(0xffffffffu, inc, d);
+    if ((tid & 31) >= d) inc += v;
   }
+  if ((tid & 31) == 31) warp_sum[tid >> 5] = inc;
   __syncthreads();
-  acc = chunk_sum[tid];
+  acc = inc - acc;
+  for (int w = 0; w < (tid >> 5); ++w) acc += warp_sum[w];
   for (int k = 0; k < chunk; ++k) {
     const int b = b_hi - k;
     if (b < 0) break;

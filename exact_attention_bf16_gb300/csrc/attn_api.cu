@@ -2,7 +2,7 @@
 // argument validation, TMA tensor-map encoding, workspace accounting and
 // kernel launches. All compute runs in the CUDA kernels (fwd_kernel.cuh and
 // bwd_kernels.cuh with the translation units that instantiate them, the pair
-// kernels, attn_paged.cu, kv_cache.cu, schedule.cu); this file holds host logic only.
+// kernels, attn_paged.cu, attn_paged_decode.cu, kv_cache.cu, schedule.cu); this file holds host logic only.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <cuda_runtime.h>
@@ -894,6 +894,7 @@ attn_status_t check_paged(const attn_paged_params* p) {
 struct PagedPlan {
   bool even = true;
   int tile_tokens = 0, part_rows = 0;
+  int decode_rows = 0, q_box_tokens = 0;
   int64_t items = 0;
   size_t off_lse = 0, off_merge = 0, off_list = 0, off_items = 0, bytes = 0;
 };
@@ -902,7 +903,11 @@ PagedPlan paged_plan(const attn_paged_params* p) {
   const int group = p->heads / p->heads_kv;
   pl.tile_tokens = 128 / group;
   pl.even = p->max_seqlen_q <= pl.tile_tokens;  // one tile of rows holds any request's queries
-  pl.part_rows = pl.even ? 128 : 256;
+  // up to 64 rows per request and K/V head: rows in the columns of the products (attn_paged_decode.cu)
+  const int64_t rows_q = static_cast<int64_t>(p->max_seqlen_q) * group;
+  if (p->score_mod == ATTN_SCORE_NONE && rows_q <= 64) pl.decode_rows = rows_q <= 16 ? 16 : rows_q <= 32 ? 32 : 64;
+  pl.q_box_tokens = (pl.decode_rows ? pl.decode_rows : 128) / group;
+  pl.part_rows = pl.decode_rows ? pl.decode_rows : pl.even ? 128 : 256;
   const int64_t rows = 2ll * kPagedMaxCtas * pl.part_rows;
   pl.off_lse = round256(rows * p->d_v * 4);
   pl.off_merge = pl.off_lse + round256(rows * 4);
@@ -950,6 +955,7 @@ attn_status_t run_fwd_paged(const attn_paged_params* p, void* ws, size_t ws_byte
   cudaError_t e = status_ptr(&a.status);
   if (e != cudaSuccess) return cuda_fail(e, "status word");
   a.tile_tokens = pl.tile_tokens;
+  a.q_box_tokens = pl.q_box_tokens;
   uint8_t* base = static_cast<uint8_t*>(ws);
   a.part_rows = pl.part_rows;
   a.part_o = reinterpret_cast<float*>(base);
@@ -968,13 +974,14 @@ attn_status_t run_fwd_paged(const attn_paged_params* p, void* ws, size_t ws_byte
   if (e != cudaSuccess) return cuda_fail(e, "device");
   CUtensorMap tq, tk, tv;
   const int box = std::min(p->page_size, 128);
-  ATTN_TRY(make_map(&tq, p->q, p->d_qk, p->heads, p->total_q, 1, 0, p->q_row_stride, p->q_head_stride, pl.tile_tokens, 2,
+  ATTN_TRY(make_map(&tq, p->q, p->d_qk, p->heads, p->total_q, 1, 0, p->q_row_stride, p->q_head_stride, pl.q_box_tokens, 2,
                     a.kv_group));
   ATTN_TRY(make_map(&tk, p->k_cache, p->d_qk, p->heads_kv, p->page_size, p->num_pages, p->k_page_stride, p->k_row_stride,
                     p->k_head_stride, box));
   ATTN_TRY(make_map(&tv, p->v_cache, p->d_v, p->heads_kv, p->page_size, p->num_pages, p->v_page_stride, p->v_row_stride,
                     p->v_head_stride, box));
-  e = launch_fwd_paged(p->d_qk, p->d_v, tq, tk, tv, a, pl.even, std::min(sms, kPagedMaxCtas), stream);
+  e = launch_fwd_paged(p->d_qk, p->d_v, tq, tk, tv, a, pl.even, pl.decode_rows, std::min(sms, kPagedMaxCtas),
+                       stream);
   return e == cudaSuccess ? ATTN_OK : cuda_fail(e, "paged fwd launch");
 }
 

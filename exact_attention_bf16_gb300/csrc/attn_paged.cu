@@ -19,7 +19,8 @@
 // CTAs; each writes its normalised fp32 O and its LSE (log2), and
 // merge_kernel adds them with the weights 2^(LSE_r - LSE), in key order.
 // One persistent CTA per SM (shared memory and Tensor Memory are taken whole):
-//   - up to 128 rows per request (decoding, a few proposed tokens): bound by
+//   - up to 128 rows per request (a few proposed tokens; up to 64 rows without a score
+//     modification run in attn_paged_decode.cu instead): bound by
 //     HBM (every K/V byte is read once and used for a handful of rows), so the
 //     key blocks of all (request, K/V head) units, laid end to end, are cut into
 //     equal ranges, one per CTA. A CTA finds its range from the lengths alone.
@@ -39,17 +40,12 @@
 // each weight): an fp16 copy of V, as the contiguous forward makes, would cost a
 // second pass over keys that a decoding step reads only once. Every sum is fp32.
 #include "kernels.h"
+#include "paged_common.cuh"
 #include "ptx_sm100.cuh"
 #include "score_mod.cuh"
 
 namespace gb300 {
 namespace paged {
-
-constexpr int BM = 128, BN = 128;
-constexpr int kThreads = 384;
-constexpr int kChunk = BM * 128;     // bytes of one 64-column chunk of a 128-row tile
-constexpr float kThreshold = 8.0f;   // log2 units
-constexpr int kSegs = 4;             // segment descriptors in flight
 
 __host__ __device__ constexpr uint32_t tS(int i) { return 128u * i; }
 __host__ __device__ constexpr uint32_t tO(int i) { return 256u + 128u * i; }
@@ -76,39 +72,6 @@ struct Cfg {
   static constexpr int REG_BUDGET = 128 * REG_LO + 256 * REG_HI;
 };
 
-// One segment of work, written by warp 0 and read by every other warp. It carries
-// the pipeline's counters too (the warps' registers hold a row of S).
-struct Seg {
-  int more;       // 0: no more work
-  int seq, hk;
-  int q_row;      // first token's row of q and o
-  int ntok;       // tokens of the unit
-  int pos0;       // position of the first token among the keys (bottom-right aligned; may be negative)
-  int nk;         // keys of the request
-  int kt0;        // first key block
-  int n0, n1;     // key blocks of tile 0 and 1 (dual: n0 in all, alternating)
-  int dual;       // one tile of rows, two streams of key blocks
-  int part;       // >= 0: the slot of this segment's partial O and LSE
-  uint32_t v0;    // key blocks copied before this segment
-  uint32_t s0, s1;  // S tiles of stream 0 and 1 before it
-  uint32_t phase; // bit 0, 1: segments before it in which O_0, O_1 were written; bit 2: dual segments (all mod 2)
-};
-static_assert(sizeof(Seg) == 64, "OFF_SEG");
-
-__device__ __forceinline__ int ceil_div(int a, int b) { return (a + b - 1) / b; }
-
-// Bounds of request s: rows of q (clamped to the rows there are and to max_q) and keys.
-struct Bounds {
-  int q0, nq, nk;
-};
-__device__ __forceinline__ Bounds bounds(const PagedArgs& a, int s) {
-  const int c0 = __ldg(a.cu_q + s), c1 = __ldg(a.cu_q + s + 1), k = __ldg(a.seqlens_k + s);
-  Bounds b;
-  b.q0 = max(0, min(c0, a.total_q));
-  b.nq = max(0, min(min(c1, a.total_q) - b.q0, a.max_q));
-  b.nk = max(0, min(k, a.max_keys));
-  return b;
-}
 struct Bars {
   uint64_t q_full, q_free;
   uint64_t k_full[6], k_empty[6], v_full[6], v_empty[6];
@@ -118,46 +81,9 @@ struct Bars {
   uint64_t seg_full[kSegs], seg_empty[kSegs];
   uint64_t mma_done;
   uint32_t tmem_base;
-  // even split: the request that holds this CTA's first key block
-  int first_seq;
-  Bounds first;
-  long long first_start, total;
-  long long warp_sum[12];
+  EvenStart even;
 };
 static_assert(sizeof(Bars) <= 512, "barriers must fit their reserved bytes");
-
-// Keys that tokens up to `last` (0-based in the request) see.
-__device__ __forceinline__ int keys_seen(const PagedArgs& a, const Bounds& b, int last) {
-  return a.causal ? max(0, min(b.nk, last + b.nk - b.nq + 1)) : b.nk;
-}
-// Key blocks that a unit of a request costs; a unit whose rows see no key still writes them.
-__device__ __forceinline__ int unit_blocks(const PagedArgs& a, const Bounds& b, int last) {
-  return max(1, ceil_div(keys_seen(a, b, last), BN));
-}
-
-// Fills a segment: tokens tok0 .. of request s, K/V head hk, key blocks [kt0, kt1).
-__device__ __forceinline__ Seg make_seg(const PagedArgs& a, const Bounds& b, int s, int hk, int tok0, int ntok, int kt0,
-                                        int kt1, int part) {
-  Seg g;
-  g.more = 1;
-  g.seq = s, g.hk = hk;
-  g.q_row = b.q0 + tok0;
-  g.ntok = ntok;
-  g.pos0 = tok0 + b.nk - b.nq;
-  g.nk = b.nk;
-  g.kt0 = kt0;
-  g.dual = ntok <= a.tile_tokens ? 1 : 0;
-  g.part = part;
-  const int last0 = tok0 + min(ntok, a.tile_tokens) - 1;
-  g.n0 = max(0, min(ceil_div(keys_seen(a, b, last0), BN), kt1) - kt0);
-  g.n1 = g.dual ? 0 : max(0, min(ceil_div(keys_seen(a, b, tok0 + ntok - 1), BN), kt1) - kt0);
-  return g;
-}
-
-// The CTA of `ctas` whose range [c W / ctas, (c + 1) W / ctas) holds block x.
-__device__ __forceinline__ int range_owner(long long x, long long W, int ctas) {
-  return static_cast<int>(((x + 1) * ctas + W - 1) / W) - 1;
-}
 
 // EVEN: the even split of all units' key blocks (at most one tile of rows per
 // request); else the list of chunk_list_kernel.
@@ -201,7 +127,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&bar->seg_empty[s], 9);  // the MMA thread and eight softmax warps
     }
     mbar_init(&bar->mma_done, 1);
-    bar->first_seq = -1;
     fence_barrier_init();
     tma_prefetch_desc(&tmq);
     tma_prefetch_desc(&tmk);
@@ -211,62 +136,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tmem_alloc(&bar->tmem_base, 512);
     tmem_relinquish();
   }
-  // Even split: running sums of the requests' key blocks (per K/V head), kThreads
-  // requests at a time, to the total; then the request that holds this CTA's first
-  // block is found, in a second pass where there are more than kThreads requests.
-  long long range0 = 0, range1 = 0;
-  int ctas = 0;
-  if constexpr (EVEN) {
-    long long total = 0;
-    const bool one_pass = a.num_seqs <= kThreads;
-    for (int pass = 0; pass < (one_pass ? 1 : 2); ++pass) {
-      long long base = 0;
-      for (int s0 = 0; s0 < a.num_seqs; s0 += kThreads) {
-        const int s = s0 + tid;
-        int n = 0;
-        Bounds b{0, 0, 0};
-        if (s < a.num_seqs) {
-          b = bounds(a, s);
-          n = b.nq > 0 ? unit_blocks(a, b, b.nq - 1) : 0;
-        }
-        long long inc = n;
-#pragma unroll
-        for (int d = 1; d < 32; d <<= 1) {
-          const long long u = __shfl_up_sync(0xffffffffu, inc, d);
-          if (static_cast<int>(lane) >= d) inc += u;
-        }
-        if (lane == 31) bar->warp_sum[warp] = inc;
-        __syncthreads();
-        long long before = base, all = base;
-        for (uint32_t w = 0; w < kThreads / 32; ++w) {
-          const long long x = bar->warp_sum[w];
-          if (w < warp) before += x;
-          all += x;
-        }
-        if (one_pass || (pass == 0 && s0 + kThreads >= a.num_seqs)) {
-          total = all * a.heads_kv;
-          // at least kPagedMinBlocks key blocks per CTA: fewer would cost more to merge than they save
-          const long long want = (total + kPagedMinBlocks - 1) / kPagedMinBlocks;
-          ctas = static_cast<int>(want < static_cast<long long>(gridDim.x) ? want : gridDim.x);
-          const int c = static_cast<int>(blockIdx.x);
-          if (c < ctas) {
-            range0 = c * total / ctas;
-            range1 = (c + 1) * total / ctas;
-          }
-        }
-        const long long start = (before + inc - n) * a.heads_kv;
-        if ((one_pass || pass == 1) && n > 0 && start <= range0 &&
-            range0 < start + static_cast<long long>(n) * a.heads_kv) {
-          bar->first_seq = s;
-          bar->first = b;
-          bar->first_start = start;
-        }
-        base = all;
-        if (!one_pass) __syncthreads();
-      }
-    }
-    if (tid == 0) bar->total = total;
-  }
+  if constexpr (EVEN) even_split(a, &bar->even);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -287,80 +157,29 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t ck = 0, cv = 0, cq = 0, seg_i = 0;  // copies and segments so far
       uint32_t cs0 = 0, cs1 = 0, phase = 0;
       bool ok = true;
-      // even split: where this CTA is
-      int s = 0, hk = 0, kt = 0, unit = 0;
-      Bounds b{0, 0, 0}, b_next{0, 0, 0};  // request s and, fetched ahead, s + 1
-      long long g = range0;
-      int merge_units = 0;  // units that begin in this range and end beyond it: at most one
-      auto fetch_next = [&]() {
-        if (s + 1 < a.num_seqs) b_next = bounds(a, s + 1);
-      };
-      if constexpr (EVEN) {
-        if (range0 < range1) {
-          s = bar->first_seq;
-          b = bar->first;
-          unit = unit_blocks(a, b, b.nq - 1);
-          const long long off = range0 - bar->first_start;
-          hk = static_cast<int>(off / unit);
-          kt = static_cast<int>(off - static_cast<long long>(hk) * unit);
-          fetch_next();
-        }
-      }
+      EvenWalk walk;
+      if constexpr (EVEN) walk.begin(a, &bar->even);
       int item = static_cast<int>(blockIdx.x);  // list: this CTA's next entry
       const int n_items = EVEN ? 0 : *a.n_items;
       auto next_seg = [&]() -> Seg {
-        Seg w;
-        w.more = 0, w.n0 = w.n1 = 0;
         if constexpr (EVEN) {
-          if (g < range1) {
-            const int take = static_cast<int>(min(static_cast<long long>(unit - kt), range1 - g));
-            int part = -1;
-            if (kt > 0) part = static_cast<int>(blockIdx.x);                     // continues an earlier CTA's unit
-            else if (take < unit) part = static_cast<int>(gridDim.x + blockIdx.x);  // begins here, ends beyond
-            w = make_seg(a, b, s, hk, 0, b.nq, kt, kt + take, part);
-            if (kt == 0 && take < unit) {
-              merge_units = 1;
-              if (lane == 0) {
-                MergeUnit m;
-                m.q_row = w.q_row, m.ntok = w.ntok, m.hk = hk;
-                m.first = part;
-                m.rest = static_cast<int>(blockIdx.x) + 1;
-                m.n = range_owner(g + unit - 1, bar->total, ctas) - static_cast<int>(blockIdx.x) + 1;
-                a.merge[blockIdx.x] = m;
-              }
-            }
-            g += take;
-            kt = 0;
-            if (g < range1 && ++hk == a.heads_kv) {  // (the unit ended, or the range did)
-              hk = 0;
-              do {
-                b = b_next, ++s;
-                fetch_next();
-              } while (b.nq == 0 && s + 1 < a.num_seqs);
-              unit = unit_blocks(a, b, b.nq - 1);
-            }
-          }
+          return walk.next(a, &bar->even);
         } else {
+          Seg w;
+          w.more = 0, w.n0 = w.n1 = 0;
           if (item < n_items) {
             const ChunkItem it = a.items[item];
             int nx = 0;
             if (lane == 0) nx = atomicAdd(a.next_item, 1);  // needed one segment later
-            b = bounds(a, it.seq);
+            const Bounds b = bounds(a, it.seq);
             w = make_seg(a, b, it.seq, it.hk, it.tok0, min(b.nq - it.tok0, 2 * a.tile_tokens), it.kt0, it.kt1, it.part);
             item = __shfl_sync(0xffffffffu, nx, 0);
           }
+          return w;
         }
-        return w;
-      };
-      // this lane's page of key block kt0 + j; num_pages (its boxes read zeros) past the last key
-      auto page_of = [&](const Seg& w, int j) -> int {
-        const long long key = (static_cast<long long>(w.kt0 + j) << 7) + (static_cast<long long>(my_page) << a.page_shift);
-        if (key >= w.nk) return a.num_pages;
-        const int pg = __ldg(a.block_table + w.seq * a.block_table_stride + (key >> a.page_shift));
-        return pg < 0 || pg > a.num_pages ? a.num_pages : pg;
       };
       Seg w = next_seg();
-      int page = w.more ? page_of(w, 0) : 0;
+      int page = w.more ? page_of(a, w, w.kt0, my_page) : 0;
       for (;;) {
         const int slot = static_cast<int>(seg_i % kSegs);
         ok = mbar_wait_warp(&bar->seg_empty[slot], ((seg_i / kSegs) & 1u) ^ 1u, a.status, 0x3100);
@@ -382,10 +201,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         int npage = 0;
         if (n == 0) {
           nw = next_seg();
-          npage = nw.more ? page_of(nw, 0) : 0;
+          npage = nw.more ? page_of(a, nw, nw.kt0, my_page) : 0;
         }
         for (int j = 0; j < n; ++j) {
-          const int next = j + 1 < n ? page_of(w, j + 1) : 0;  // fetched ahead of the waits
+          const int next = j + 1 < n ? page_of(a, w, w.kt0 + j + 1, my_page) : 0;  // fetched ahead of the waits
           const int row = a.page_size > BN ? ((w.kt0 + j) << 7) & (a.page_size - 1) : 0;
           const uint32_t ks = ck % C::NK;
           ok = mbar_wait_warp(&bar->k_empty[ks], ((ck / C::NK) & 1u) ^ 1u, a.status, 0x3110);
@@ -421,14 +240,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           page = next;
           if (j == min(n - 1, C::NK - 1)) {
             nw = next_seg();
-            npage = nw.more ? page_of(nw, 0) : 0;
+            npage = nw.more ? page_of(a, nw, nw.kt0, my_page) : 0;
           }
         }
         if (!ok) break;
         w = nw;
         page = npage;
       }
-      if (EVEN && merge_units == 0 && lane == 0) a.merge[blockIdx.x].n = 0;
+      if constexpr (EVEN) walk.finish(a);
       if (!ok) {  // let the copies in flight land before the CTA exits
         for (uint32_t u = 0; u < C::NK && u < ck; ++u)
           mbar_wait(&bar->k_full[(ck - 1 - u) % C::NK], ((ck - 1 - u) / C::NK) & 1u, nullptr, 0);
@@ -568,7 +387,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       {
         const bool valid = row_valid(w);
         const int pos = w.pos0 + row_tok(w.dual);  // the row's position among the keys
-        const int klim = !valid ? 0 : (a.causal ? max(0, min(w.nk, pos + 1)) : w.nk);
+        // (rows without a token hold whatever shared memory did: computed without masks, never stored)
+        const int klim = !valid ? 0x7fffffff : (a.causal ? max(0, min(w.nk, pos + 1)) : w.nk);
         const bool work = __any_sync(0xffffffffu, valid);  // a warp without rows only keeps the barriers in step
         float slope = 0.f;
         if (MOD == kModAlibi && valid)
@@ -635,7 +455,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const float mx = fmax3(fmax3(mp[0], mp[1], mp[2]), fmax3(mp[3], mp[4], mp[5]), fmaxf(mp[6], mp[7]));
             const float sl2 = a.scale_log2;
             const float m_tile = mx * sl2;
-            const bool need = m_tile > m_used + kThreshold;
+            const bool need = valid && m_tile > m_used + kThreshold;
             float alpha = 1.f;
             if (need) {
               alpha = (m_used == -INFINITY) ? 0.f : ex2_mufu(m_used - m_tile);
@@ -1026,14 +846,16 @@ cudaError_t launch_main(const CUtensorMap& tq, const CUtensorMap& tk, const CUte
 
 template <int DQK, int DV>
 cudaError_t launch_d(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const PagedArgs& a, bool even,
-                     int ctas, cudaStream_t stream) {
+                     int decode_rows, int ctas, cudaStream_t stream) {
   cudaError_t e = cudaSuccess;
   if (!even) {
     chunk_list_kernel<<<1, kListThreads, 0, stream>>>(a, ctas);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
   }
-  switch (a.score_mod) {
+  if (decode_rows > 0) {
+    e = launch_paged_decode(DQK, DV, decode_rows, tq, tk, tv, a, ctas, stream);
+  } else switch (a.score_mod) {
     case kModNone:
       e = even ? launch_main<DQK, DV, kModNone, true>(tq, tk, tv, a, ctas, stream)
                : launch_main<DQK, DV, kModNone, false>(tq, tk, tv, a, ctas, stream);
@@ -1058,11 +880,11 @@ cudaError_t launch_d(const CUtensorMap& tq, const CUtensorMap& tk, const CUtenso
 }  // namespace paged
 
 cudaError_t launch_fwd_paged(int d_qk, int d_v, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
-                             const PagedArgs& a, bool even, int ctas, cudaStream_t stream) {
+                             const PagedArgs& a, bool even, int decode_rows, int ctas, cudaStream_t stream) {
   if (ctas < 1 || a.merge == nullptr || a.part_o == nullptr || (!even && a.items == nullptr)) return cudaErrorInvalidValue;
-  if (d_qk == 64 && d_v == 64) return paged::launch_d<64, 64>(tq, tk, tv, a, even, ctas, stream);
-  if (d_qk == 128 && d_v == 128) return paged::launch_d<128, 128>(tq, tk, tv, a, even, ctas, stream);
-  if (d_qk == 192 && d_v == 128) return paged::launch_d<192, 128>(tq, tk, tv, a, even, ctas, stream);
+  if (d_qk == 64 && d_v == 64) return paged::launch_d<64, 64>(tq, tk, tv, a, even, decode_rows, ctas, stream);
+  if (d_qk == 128 && d_v == 128) return paged::launch_d<128, 128>(tq, tk, tv, a, even, decode_rows, ctas, stream);
+  if (d_qk == 192 && d_v == 128) return paged::launch_d<192, 128>(tq, tk, tv, a, even, decode_rows, ctas, stream);
   return cudaErrorInvalidValue;
 }
 

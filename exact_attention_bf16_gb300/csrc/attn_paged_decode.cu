@@ -1,0 +1,600 @@
+// attn_fwd_paged for few rows per K/V head (decoding, a few proposed tokens): up to
+// N = 16, 32 or 64 rows (token, head of the group) per request.
+//
+// The products are taken the other way round than in attn_paged.cu, with the long
+// side in the 128 lanes of an MMA:
+//   S^T [128 keys x N rows]  = K Q^T       (A = K block, B = Q, both K-major)
+//   O^T [d_v x N rows]      += V^T P^T     (A = V block read M-major, B = P, K-major)
+// so that a tile's softmax is spread over 128 threads, one key each with N values,
+// instead of N threads with 128, and an MMA is N wide instead of 128. The running
+// maximum of a row is then a maximum across threads; it is needed only when some
+// logit exceeds the one in use by more than 8 (log2 units), so per block the four
+// warps only vote on that (one named barrier), and the maxima, the rescale of O^T
+// and of the sums run when the vote says so (a row's first block, rarely later). Row
+// sums stay per thread (per key lane) until the end.
+//
+// Bound by HBM: per 128 keys and K/V head at d = 128 64 KB against 16 MMAs of about
+// 50 cycles. Work is the even split of paged_common.cuh; two streams over the even and
+// the odd key blocks hide the chain S^T -> softmax -> O^T, as there.
+//
+// Warps: 0 work and TMA copies, 1 MMA issue, 4..7 and 8..11 softmax of stream 0 and 1.
+#include "kernels.h"
+#include "paged_common.cuh"
+#include "ptx_sm100.cuh"
+
+namespace gb300 {
+namespace paged {
+namespace decode {
+
+template <int DQK, int DV, int N>
+struct Cfg {
+  static constexpr int QCH = DQK / 64, VCH = DV / 64;
+  static constexpr int K_BYTES = QCH * kChunk, V_BYTES = VCH * kChunk;
+  static constexpr int Q_CHUNK = N * 128, Q_BYTES = QCH * Q_CHUNK;  // 64 columns of N rows
+  static constexpr int P_CHUNK = N * 128, P_BYTES = 2 * P_CHUNK;    // 64 keys of N rows; [N][128 keys]
+  static constexpr int NQ = N == 64 ? 1 : 2;  // 2: the next segment's Q is copied while this one's is used
+  // ring slots: what 227 KB hold beside Q and P
+  static constexpr int NK = DQK == 64 ? 6 : (DQK == 128 ? 3 : 2);
+  static constexpr int NV = DQK == 64 ? (N == 64 ? 5 : 6) : (DQK == 128 ? (N == 64 ? 2 : 3) : (N == 16 ? 3 : 2));
+  static constexpr int OFF_V = NK * K_BYTES;
+  static constexpr int OFF_Q = OFF_V + NV * V_BYTES;
+  static constexpr int OFF_P = OFF_Q + NQ * Q_BYTES;
+  static constexpr int OFF_M = OFF_P + 2 * P_BYTES;  // [2 streams][N]: the maxima in use (log2 units)
+  static constexpr int OFF_W = OFF_M + 2 * N * 4;    // [2 streams][4 warps][N]: warps' maxima, rescales, then sums
+  static constexpr int OFF_SEG = OFF_W + 2 * 4 * N * 4;
+  static constexpr int OFF_BAR = OFF_SEG + kSegs * 64;
+  static constexpr int SMEM = OFF_BAR + 640;  // the base is 1024-byte aligned (checked)
+  static_assert(SMEM <= 232448, "shared memory budget");
+  // TMEM columns: S^T and O^T of the two streams
+  static constexpr uint32_t tS(int i) { return N * i; }
+  static constexpr uint32_t tO(int i) { return 2 * N + N * i; }
+  static constexpr uint32_t COLS = 4 * N;  // 64, 128 or 256: powers of two
+  static constexpr int M_O = DV;           // rows of O^T (DV = 64: an M = 64 MMA)
+};
+
+struct Bars {
+  uint64_t q_full[2], q_free[2];
+  uint64_t k_full[6], k_empty[6], v_full[6], v_empty[6];
+  uint64_t s_full[2], p_full[2], o_full[2];
+  uint64_t o_free;    // a segment is over: its O has been read, its MMAs issued
+  uint64_t x_full[2];  // a stream's maxima and sums are in shared memory
+  uint64_t seg_full[kSegs], seg_empty[kSegs];
+  uint64_t mma_done;
+  uint32_t tmem_base;
+  EvenStart even;
+};
+static_assert(sizeof(Bars) <= 640, "barriers must fit their reserved bytes");
+
+// Named barrier of one warpgroup with the OR of its threads' predicates. Every wait that
+// precedes one is bounded and its failure goes into a vote, so all warps get here.
+__device__ __forceinline__ bool group_any(int id, bool pred) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 p, %1, 0;\n\t"
+      "barrier.cta.red.or.pred.aligned q, %2, 128, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"(pred ? 1u : 0u), "r"(id)
+      : "memory");
+  return r != 0;
+}
+__device__ __forceinline__ void group_sync(int id) {
+  asm volatile("barrier.cta.sync.aligned %0, 128;" ::"r"(id) : "memory");
+}
+
+template <int N>
+__device__ __forceinline__ void tmem_ld_cols(uint32_t taddr, uint32_t (&r)[N]) {
+  if constexpr (N >= 32) {
+#pragma unroll
+    for (int c = 0; c < N / 32; ++c) tmem_ld32(taddr + 32 * c, *reinterpret_cast<uint32_t(*)[32]>(&r[32 * c]));
+  } else if constexpr (N == 16) {
+    tmem_ld16(taddr, r);
+  } else {
+    tmem_ld8(taddr, r);
+  }
+}
+template <int N>
+__device__ __forceinline__ void tmem_st_cols(uint32_t taddr, const uint32_t (&r)[N]) {
+  if constexpr (N >= 32) {
+#pragma unroll
+    for (int c = 0; c < N / 32; ++c) tmem_st32(taddr + 32 * c, *reinterpret_cast<const uint32_t(*)[32]>(&r[32 * c]));
+  } else {
+    tmem_st16(taddr, r);
+  }
+}
+
+// Reduces N values per lane over the warp, 32 (or 16) columns at a time, and writes the
+// results to out[0 .. N). At each step a lane keeps one half of its columns and hands over
+// the other: 32 columns cost 31 shuffles, not 160.
+template <int N, typename Op>
+__device__ __forceinline__ void warp_reduce_cols(const float (&x)[N], uint32_t lane, float* out, Op op) {
+  constexpr int R = N < 32 ? N : 32;
+#pragma unroll
+  for (int c0 = 0; c0 < N; c0 += R) {
+    float v[R];
+#pragma unroll
+    for (int c = 0; c < R; ++c) v[c] = x[c0 + c];
+#pragma unroll
+    for (int st = 0; (R >> (st + 1)) > 0; ++st) {
+      const int half = R >> (st + 1);
+      const uint32_t bit = 16u >> st;
+      const bool up = (lane & bit) != 0;
+#pragma unroll
+      for (int c = 0; c < R / 2; ++c) {
+        if (c < half) {
+          const float send = up ? v[c] : v[c + half], keep = up ? v[c + half] : v[c];
+          v[c] = op(keep, __shfl_xor_sync(0xffffffffu, send, bit));
+        }
+      }
+    }
+    if constexpr (R == 16) {  // lanes 2c and 2c + 1 hold the halves of column c
+      v[0] = op(v[0], __shfl_xor_sync(0xffffffffu, v[0], 1));
+      if ((lane & 1u) == 0) out[lane >> 1] = v[0];
+    } else {
+      out[c0 + lane] = v[0];
+    }
+  }
+}
+
+template <int DQK, int DV, int N>
+__global__ void __launch_bounds__(kThreads, 1)
+    paged_decode_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUtensorMap tmk,
+                        const __grid_constant__ CUtensorMap tmv, const PagedArgs a) {
+  using C = Cfg<DQK, DV, N>;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  if ((smem_u32(smem) & 1023u) != 0u) {  // the 128-byte-swizzled tiles need 1024-byte alignment
+    if (threadIdx.x == 0) record_error(a.status, DEV_BAD_CONFIG, 0x4000);
+    return;
+  }
+  uint8_t* sK = smem;
+  uint8_t* sV = smem + C::OFF_V;
+  uint8_t* sQ = smem + C::OFF_Q;
+  Seg* sSeg = reinterpret_cast<Seg*>(smem + C::OFF_SEG);
+  Bars* bar = reinterpret_cast<Bars*>(smem + C::OFF_BAR);
+  const uint32_t warp = warp_id(), lane = lane_id();
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&bar->q_full[s], 1);
+      mbar_init(&bar->q_free[s], 1);
+      mbar_init(&bar->s_full[s], 1);
+      mbar_init(&bar->p_full[s], 4);
+      mbar_init(&bar->o_full[s], 1);
+      mbar_init(&bar->x_full[s], 4);
+    }
+    for (int s = 0; s < 6; ++s) {
+      mbar_init(&bar->k_full[s], 1);
+      mbar_init(&bar->k_empty[s], 1);
+      mbar_init(&bar->v_full[s], 1);
+      mbar_init(&bar->v_empty[s], 1);
+    }
+    mbar_init(&bar->o_free, 9);  // eight softmax warps and the MMA thread, so that neither side gets two segments ahead
+    for (int s = 0; s < kSegs; ++s) {
+      mbar_init(&bar->seg_full[s], 1);
+      mbar_init(&bar->seg_empty[s], 9);  // the MMA thread and eight softmax warps
+    }
+    mbar_init(&bar->mma_done, 1);
+    fence_barrier_init();
+    tma_prefetch_desc(&tmq);
+    tma_prefetch_desc(&tmk);
+    tma_prefetch_desc(&tmv);
+  }
+  if (warp == 1) {
+    tmem_alloc(&bar->tmem_base, C::COLS);
+    tmem_relinquish();
+  }
+  // rows of Q that no copy writes: zeros, whose logits never move a maximum
+  for (int x = static_cast<int>(threadIdx.x); x < C::NQ * C::Q_BYTES / 16; x += kThreads)
+    reinterpret_cast<uint4*>(sQ)[x] = make_uint4(0, 0, 0, 0);
+  fence_proxy_async_smem();
+  even_split(a, &bar->even);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tbase = bar->tmem_base;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // merge_kernel, as SMs become free
+
+  if (warp == 0) {
+    // ===================== work and copies ==================================
+    const int np = a.page_size < BN ? BN >> a.page_shift : 1;  // pages (boxes along the keys) of a key block
+    const int box_rows = a.page_size < BN ? a.page_size : BN;
+    const int my_page = static_cast<int>(lane) % np, my_chunk = static_cast<int>(lane) / np;
+    const uint32_t q_bytes = static_cast<uint32_t>(a.kv_group * a.q_box_tokens) * 128u * C::QCH;
+    uint32_t ck = 0, cv = 0, cq = 0, seg_i = 0;  // copies and segments so far
+    uint32_t cs0 = 0, cs1 = 0, phase = 0;
+    bool ok = true;
+    EvenWalk walk;
+    walk.begin(a, &bar->even);
+    Seg w = walk.next(a, &bar->even);
+    int page = w.more ? page_of(a, w, w.kt0, my_page) : 0;
+    for (;;) {
+      const int slot = static_cast<int>(seg_i % kSegs);
+      ok = mbar_wait_warp(&bar->seg_empty[slot], ((seg_i / kSegs) & 1u) ^ 1u, a.status, 0x4100);
+      if (!ok) break;
+      const int n = w.n0;
+      if (lane == 0) {
+        w.v0 = cv, w.s0 = cs0, w.s1 = cs1, w.phase = phase;
+        sSeg[slot] = w;
+        mbar_arrive(&bar->seg_full[slot]);
+      }
+      ++seg_i;
+      if (!w.more) break;
+      cs0 += (n + 1) / 2;
+      cs1 += n / 2;
+      phase ^= (n > 0 ? 1u : 0u) | (n > 1 ? 2u : 0u) | 4u;
+      // ---- its copies; the next segment and its first page are looked up behind the first few
+      Seg nw;
+      nw.more = 0;
+      int npage = 0;
+      if (n == 0) {
+        nw = walk.next(a, &bar->even);
+        npage = nw.more ? page_of(a, nw, nw.kt0, my_page) : 0;
+      }
+      for (int j = 0; j < n; ++j) {
+        const int next = j + 1 < n ? page_of(a, w, w.kt0 + j + 1, my_page) : 0;  // fetched ahead of the waits
+        const int row = a.page_size > BN ? ((w.kt0 + j) << 7) & (a.page_size - 1) : 0;
+        const uint32_t ks = ck % C::NK;
+        ok = mbar_wait_warp(&bar->k_empty[ks], ((ck / C::NK) & 1u) ^ 1u, a.status, 0x4110);
+        if (!ok) break;
+        if (lane == 0) mbar_arrive_expect_tx(&bar->k_full[ks], C::K_BYTES);
+        __syncwarp();
+        if (my_chunk < C::QCH)
+          tma_load_4d(sK + ks * C::K_BYTES + my_chunk * kChunk + my_page * box_rows * 128, &tmk, &bar->k_full[ks],
+                      my_chunk * 64, w.hk, row, page);
+        ++ck;
+        if (j == 0) {
+          const uint32_t qs = cq % C::NQ;
+          ok = mbar_wait_warp(&bar->q_free[qs], ((cq / C::NQ) & 1u) ^ 1u, a.status, 0x4120);
+          if (!ok) break;
+          if (lane == 0) mbar_arrive_expect_tx(&bar->q_full[qs], q_bytes);
+          __syncwarp();
+          if (static_cast<int>(lane) < C::QCH)
+            tma_load_4d(sQ + qs * C::Q_BYTES + lane * C::Q_CHUNK, &tmq, &bar->q_full[qs], static_cast<int>(lane) * 64,
+                        w.hk * a.kv_group, w.q_row, 0);
+          ++cq;
+        }
+        const uint32_t vs = cv % C::NV;
+        ok = mbar_wait_warp(&bar->v_empty[vs], ((cv / C::NV) & 1u) ^ 1u, a.status, 0x4130);
+        if (!ok) break;
+        if (lane == 0) mbar_arrive_expect_tx(&bar->v_full[vs], C::V_BYTES);
+        __syncwarp();
+        if (my_chunk < C::VCH)
+          tma_load_4d(sV + vs * C::V_BYTES + my_chunk * kChunk + my_page * box_rows * 128, &tmv, &bar->v_full[vs],
+                      my_chunk * 64, w.hk, row, page);
+        ++cv;
+        page = next;
+        if (j == min(n - 1, C::NK - 1)) {
+          nw = walk.next(a, &bar->even);
+          npage = nw.more ? page_of(a, nw, nw.kt0, my_page) : 0;
+        }
+      }
+      if (!ok) break;
+      w = nw;
+      page = npage;
+    }
+    walk.finish(a);
+    if (!ok) {  // let the copies in flight land before the CTA exits
+      for (uint32_t u = 0; u < C::NK && u < ck; ++u)
+        mbar_wait(&bar->k_full[(ck - 1 - u) % C::NK], ((ck - 1 - u) / C::NK) & 1u, nullptr, 0);
+      for (uint32_t u = 0; u < C::NV && u < cv; ++u)
+        mbar_wait(&bar->v_full[(cv - 1 - u) % C::NV], ((cv - 1 - u) / C::NV) & 1u, nullptr, 0);
+      for (uint32_t u = 0; u < C::NQ && u < cq; ++u)
+        mbar_wait(&bar->q_full[(cq - 1 - u) % C::NQ], ((cq - 1 - u) / C::NQ) & 1u, nullptr, 0);
+    }
+  } else if (warp == 1) {
+    if (lane == 0) {
+      // ===================== MMA issue ======================================
+      constexpr uint32_t idS = idesc_bf16_f32(BN, N, false, false);
+      constexpr uint32_t idO = idesc_bf16_f32(C::M_O, N, true, false);
+      uint32_t ck = 0, cv = 0, cq = 0, seg_i = 0, cp[2] = {0, 0};
+      bool ok = true;
+      for (;;) {
+        const int slot = static_cast<int>(seg_i % kSegs);
+        ok = mbar_wait(&bar->seg_full[slot], (seg_i / kSegs) & 1u, a.status, 0x4200);
+        if (!ok) break;
+        const int more = sSeg[slot].more, n = sSeg[slot].n0;
+        mbar_arrive(&bar->seg_empty[slot]);
+        if (!more) break;
+        // the previous segment's O has been read: before the first PV overwrites it
+        auto wait_o = [&]() { return seg_i == 0 || mbar_wait(&bar->o_free, (seg_i - 1) & 1u, a.status, 0x4210); };
+        if (n == 0) ok = wait_o();
+        const uint32_t qs = cq % C::NQ;
+        for (int j = 0; j <= n && n > 0 && ok; ++j) {
+          if (j < n) {
+            ok = mbar_wait(&bar->k_full[ck % C::NK], (ck / C::NK) & 1u, a.status, 0x4220);
+            if (ok && j == 0) ok = mbar_wait(&bar->q_full[qs], (cq / C::NQ) & 1u, a.status, 0x4230);
+            if (!ok) break;
+            tc_fence_after();
+            const uint64_t dk = smem_desc(smem_u32(sK + (ck % C::NK) * C::K_BYTES), 16, 1024, SWZ_128B);
+            const uint64_t dq = smem_desc(smem_u32(sQ + qs * C::Q_BYTES), 16, 1024, SWZ_128B);
+#pragma unroll
+            for (int kk = 0; kk < DQK / 16; ++kk)
+              mma_ss(tbase + C::tS(j & 1), desc_add(dk, (kk / 4) * kChunk + (kk % 4) * 32),
+                     desc_add(dq, (kk / 4) * C::Q_CHUNK + (kk % 4) * 32), idS, kk > 0 ? 1u : 0u);
+            mma_commit(&bar->s_full[j & 1]);
+            mma_commit(&bar->k_empty[ck % C::NK]);
+            ++ck;
+            if (j == n - 1) mma_commit(&bar->q_free[qs]);
+          }
+          if (j > 0) {
+            const int i = (j - 1) & 1;
+            if (j == 1) ok = wait_o();
+            ok = ok && mbar_wait(&bar->v_full[cv % C::NV], (cv / C::NV) & 1u, a.status, 0x4240) &&
+                 mbar_wait(&bar->p_full[i], cp[i] & 1u, a.status, 0x4250);
+            if (!ok) break;
+            tc_fence_after();
+            ++cp[i];
+            const uint64_t dv = smem_desc(smem_u32(sV + (cv % C::NV) * C::V_BYTES), kChunk, 1024, SWZ_128B);
+            const uint64_t dp = smem_desc(smem_u32(smem + C::OFF_P + i * C::P_BYTES), 16, 1024, SWZ_128B);
+#pragma unroll
+            for (int kk = 0; kk < BN / 16; ++kk)  // 16 keys: 16 rows of V, 32 bytes of P's rows
+              mma_ss(tbase + C::tO(i), desc_add(dv, kk * 2048),
+                     desc_add(dp, (kk / 4) * C::P_CHUNK + (kk % 4) * 32), idO, (kk > 0 || j > 2) ? 1u : 0u);
+            mma_commit(&bar->v_empty[cv % C::NV]);
+            ++cv;
+            if (j - 1 >= n - 2) mma_commit(&bar->o_full[i]);
+          }
+        }
+        if (!ok) break;
+        mbar_arrive(&bar->o_free);
+        if (n > 0) ++cq;
+        ++seg_i;
+      }
+      mma_commit(&bar->mma_done);
+      mbar_wait(&bar->mma_done, 0, a.status, 0x42ff);
+    }
+  } else if (warp >= 4) {
+    // ======================= softmax and output =============================
+    const int i = (static_cast<int>(warp) - 4) / 4;  // stream
+    const uint32_t quarter = warp & 3u;
+    const int key_lane = static_cast<int>(quarter * 32 + lane);  // this thread's key of a block
+    const uint32_t lane_base = tbase + ((quarter * 32u) << 16);
+    const int bid = 1 + i;  // named barrier of this warpgroup
+    float* sM = reinterpret_cast<float*>(smem + C::OFF_M) + i * N;
+    float* sW = reinterpret_cast<float*>(smem + C::OFF_W) + i * 4 * N;
+    // P [N rows][128 keys]: this thread's column; 16-byte pieces swizzled by the row
+    uint8_t* sP = smem + C::OFF_P + i * C::P_BYTES + (key_lane / 64) * C::P_CHUNK + (key_lane % 8) * 2;
+    const int piece = (key_lane % 64) / 8;
+    const float sl2 = a.scale_log2;
+    bool ok = true;
+    for (uint32_t seg_i = 0;; ++seg_i) {
+      // (a copy: read by all lanes before the warp lets the slot go, below)
+      const volatile Seg& w = sSeg[seg_i % kSegs];
+      ok = ok && mbar_wait_warp(&bar->seg_full[seg_i % kSegs], (seg_i / kSegs) & 1u, a.status, 0x4300);
+      // every warp has left the segment before: its reads of sM and sW of both streams are done
+      if (ok && seg_i > 0) ok = mbar_wait_warp(&bar->o_free, (seg_i - 1) & 1u, a.status, 0x4328);
+      if (group_any(bid, !ok) || !w.more) break;  // (a wait that failed anywhere in the segment before, too)
+      const int n = w.n0, nk = w.nk, pos0 = w.pos0, kt0 = w.kt0;
+      const int full = a.causal ? min(nk, max(0, pos0 + 1)) : nk;  // keys that every row sees
+      auto page_ok = [&](int key) -> bool {
+        if (key >= nk) return true;
+        const int pg = __ldg(a.block_table + w.seq * a.block_table_stride + (key >> a.page_shift));
+        return pg >= 0 && pg < a.num_pages;
+      };
+      float l[N];  // this key lane's share of the row sums
+#pragma unroll
+      for (int c = 0; c < N; ++c) l[c] = 0.f;
+      uint32_t s_phase = i == 0 ? w.s0 : w.s1;
+      bool pg_ok = i < n ? page_ok((kt0 + i) * BN + key_lane) : true;
+      for (int j = i; j < n; j += 2, ++s_phase) {
+        const int key = (kt0 + j) * BN + key_lane;
+        const bool here = pg_ok;
+        if (j + 2 < n) pg_ok = page_ok(key + 2 * BN);  // fetched one block ahead
+        ok = ok && mbar_wait_warp(&bar->s_full[i], s_phase & 1u, a.status, 0x4310 + i);
+        tc_fence_after();
+        uint32_t sr[N];
+        tmem_ld_cols<N>(lane_base + C::tS(i), sr);
+        tmem_wait_ld();
+        float s[N];
+#pragma unroll
+        for (int c = 0; c < N; ++c) s[c] = __uint_as_float(sr[c]) * sl2;
+        if (!here || key >= full) {  // keys that no row or not every row sees
+          int tok = 0, left = a.kv_group;  // of column c
+#pragma unroll
+          for (int c = 0; c < N; ++c) {
+            if (!here || key >= nk || (a.causal && key > pos0 + tok)) s[c] = -INFINITY;
+            if (--left == 0) left = a.kv_group, ++tok;
+          }
+        }
+        // does any logit exceed the maximum in use by more than the threshold?
+        const bool fresh = j == i;
+        bool over = fresh || !ok;
+        if (!fresh) {
+          float t = -INFINITY;
+#pragma unroll
+          for (int c = 0; c < N; c += 4) {
+            const float4 m4 = *reinterpret_cast<const float4*>(sM + c);
+            t = fmax3(t, s[c] - m4.x, s[c + 1] - m4.y);
+            t = fmax3(t, s[c + 2] - m4.z, s[c + 3] - m4.w);
+          }
+          over = over || t > kThreshold;
+        }
+        if (group_any(bid, over)) {
+          if (group_any(bid, !ok)) {  // a wait ran out in some warp: leave together
+            ok = false;
+            break;
+          }
+          warp_reduce_cols<N>(s, lane, sW + quarter * N, [](float x, float y) { return fmaxf(x, y); });
+          group_sync(bid);
+          if (key_lane < N) {  // one thread per row: the maximum in use is replaced where the block exceeds it enough
+            const int c = key_lane;
+            const float m_blk = fmaxf(fmaxf(sW[c], sW[N + c]), fmaxf(sW[2 * N + c], sW[3 * N + c]));
+            const float m_old = fresh ? -INFINITY : sM[c];
+            const bool need = m_blk > m_old + kThreshold;
+            sW[c] = !need ? 1.f : (m_old == -INFINITY ? 0.f : ex2_mufu(m_old - m_blk));
+            sM[c] = need ? m_blk : m_old;
+          }
+          group_sync(bid);
+          if (!fresh) {
+            constexpr int STEP = 16;
+#pragma unroll
+            for (int c0 = 0; c0 < N; c0 += STEP) {
+              uint32_t o[STEP];
+              tmem_ld_cols<STEP>(lane_base + C::tO(i) + c0, o);
+              tmem_wait_ld();
+#pragma unroll
+              for (int c = 0; c < STEP; ++c) {
+                const float alpha = sW[c0 + c];
+                l[c0 + c] *= alpha;
+                o[c] = __float_as_uint(__uint_as_float(o[c]) * alpha);
+              }
+              tmem_st_cols<STEP>(lane_base + C::tO(i) + c0, o);
+            }
+            tmem_wait_st();
+          }
+          group_sync(bid);
+        }
+        // P = 2^(s - m), a column of P per thread; a row without keys so far has m = -inf: p = 0
+#pragma unroll
+        for (int c = 0; c < N; c += 4) {
+          const float4 m4 = *reinterpret_cast<const float4*>(sM + c);
+          const float mm[4] = {m4.x, m4.y, m4.z, m4.w};
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            const float p = ex2_mufu(s[c + u] - (mm[u] == -INFINITY ? 0.f : mm[u]));
+            l[c + u] += p;
+            *reinterpret_cast<__nv_bfloat16*>(sP + (c + u) * 128 + ((piece ^ ((c + u) & 7)) << 4)) = __float2bfloat16_rn(p);
+          }
+        }
+        // The request's last block: cache rows past its last key, on the page that holds it, may be
+        // anything (0 x NaN is NaN), so they are zeroed before the PV product reads them.
+        const int tail = nk - (kt0 + j) * BN;  // keys of the request in this block
+        if (tail < BN && tail > 0 && (tail & (a.page_size - 1)) != 0) {
+          const uint32_t u = w.v0 + static_cast<uint32_t>(j), vs = u % C::NV;
+          ok = ok && mbar_wait_warp(&bar->v_full[vs], (u / C::NV) & 1u, a.status, 0x4320);
+          const int end = min(BN, (tail | (a.page_size - 1)) + 1);
+          uint8_t* v = sV + vs * C::V_BYTES;
+          const int units = (end - tail) * 8;  // 16-byte pieces of a chunk
+          for (int x = key_lane; x < units * C::VCH && ok; x += 128)
+            *reinterpret_cast<uint4*>(v + (x / units) * kChunk + tail * 128 + (x % units) * 16) = make_uint4(0, 0, 0, 0);
+        }
+        fence_proxy_async_smem();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bar->p_full[i]);
+      }
+      // ---- output: sums over the key lanes, the two streams merged
+      if (ok) {
+        warp_reduce_cols<N>(l, lane, sW + quarter * N, [](float x, float y) { return x + y; });
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bar->x_full[i]);
+        const uint32_t xp = (w.phase >> 2) & 1u;
+        ok = mbar_wait_warp(&bar->x_full[i], xp, a.status, 0x4330) &&
+             mbar_wait_warp(&bar->x_full[1 - i], xp, a.status, 0x4331);
+      }
+      // (the exchange also says that the other warpgroup has left the segment before, so that
+      // its O barrier is at most one phase behind)
+      if (ok && n > 0) ok = mbar_wait_warp(&bar->o_full[0], w.phase & 1u, a.status, 0x4340);
+      if (ok && n > 1) ok = mbar_wait_warp(&bar->o_full[1], (w.phase >> 1) & 1u, a.status, 0x4341);
+      if (ok) {
+        tc_fence_after();
+        // this warpgroup writes rows [i N/2, (i + 1) N/2); lane u of each warp holds row i N/2 + u's weights
+        const float* m_of = reinterpret_cast<const float*>(smem + C::OFF_M);
+        const float* l_of = reinterpret_cast<const float*>(smem + C::OFF_W);
+        constexpr int HALF = N / 2;
+        const int row = i * HALF + static_cast<int>(lane) % HALF;
+        const int rows = w.ntok * a.kv_group, part = w.part;
+        float la = 0.f, lb = 0.f, ma = -INFINITY, mb = -INFINITY;
+        if (n > 0) {
+          ma = m_of[row];
+          la = (l_of[row] + l_of[N + row]) + (l_of[2 * N + row] + l_of[3 * N + row]);
+        }
+        if (n > 1) {
+          mb = m_of[N + row];
+          lb = (l_of[4 * N + row] + l_of[5 * N + row]) + (l_of[6 * N + row] + l_of[7 * N + row]);
+        }
+        const float mm = fmaxf(ma, mb);
+        const float ea = la > 0.f ? ex2_mufu(ma - mm) : 0.f, eb = lb > 0.f ? ex2_mufu(mb - mm) : 0.f;
+        const float lt = la * ea + lb * eb;
+        const float inv = lt > 0.f ? 1.f / lt : 0.f;
+        const float w0 = ea * inv, w1 = eb * inv;
+        const float lse2 = lt > 0.f ? mm + log2f(lt) : -INFINITY;
+        const int q_row = w.q_row, head0 = w.hk * a.kv_group;
+        if (quarter == 0 && static_cast<int>(lane) < HALF && row < rows) {
+          const int tok = row / a.kv_group;
+          if (part >= 0)
+            a.part_lse[static_cast<int64_t>(part) * a.part_rows + row] = lse2;
+          else
+            a.lse[static_cast<int64_t>(head0 + row - tok * a.kv_group) * a.total_q + q_row + tok] =
+                lse2 * 0.69314718055994531f;
+        }
+        // O^T: lane = column of O (d_v = 64: an M = 64 product, whose row m is in lane 32 (m / 16) + m % 16)
+        const bool has_col = DV == 128 || lane < 16;
+        const int col = DV == 128 ? key_lane : static_cast<int>(quarter * 16 + lane);
+        constexpr int STEP = HALF < 16 ? 8 : 16;
+#pragma unroll 1
+        for (int c0 = 0; c0 < HALF && i * HALF + c0 < rows; c0 += STEP) {
+          uint32_t o0[STEP], o1[STEP];
+          tmem_ld_cols<STEP>(lane_base + C::tO(0) + i * HALF + c0, o0);  // (columns never written are not used)
+          tmem_ld_cols<STEP>(lane_base + C::tO(1) + i * HALF + c0, o1);
+          tmem_wait_ld();
+          int tok = (i * HALF + c0) / a.kv_group, hd = i * HALF + c0 - tok * a.kv_group;
+#pragma unroll
+          for (int c = 0; c < STEP; ++c) {
+            const float x0 = __shfl_sync(0xffffffffu, w0, c0 + c), x1 = __shfl_sync(0xffffffffu, w1, c0 + c);
+            const float v0 = n > 0 ? __uint_as_float(o0[c]) * x0 : 0.f;
+            const float v = n > 1 ? fmaf(__uint_as_float(o1[c]), x1, v0) : v0;
+            const int rw = i * HALF + c0 + c;
+            if (rw < rows && has_col) {
+              if (part >= 0)
+                a.part_o[(static_cast<int64_t>(part) * a.part_rows + rw) * DV + col] = v;
+              else
+                a.o[static_cast<int64_t>(q_row + tok) * a.o_row + static_cast<int64_t>(head0 + hd) * a.o_head + col] =
+                    __float2bfloat16_rn(v);
+            }
+            if (++hd == a.kv_group) hd = 0, ++tok;
+          }
+        }
+        tc_fence_before();
+      }
+      __syncwarp();
+      if (lane == 0 && ok) {
+        mbar_arrive(&bar->o_free);
+        mbar_arrive(&bar->seg_empty[seg_i % kSegs]);
+      }
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 1) tmem_dealloc(tbase, C::COLS);
+}
+
+template <int DQK, int DV, int N>
+cudaError_t launch_n(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const PagedArgs& a, int ctas,
+                     cudaStream_t stream) {
+  using C = Cfg<DQK, DV, N>;
+  auto kern = paged_decode_kernel<DQK, DV, N>;
+  static PerDeviceOnce once;
+  const cudaError_t e =
+      once.run([&] { return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM); });
+  if (e != cudaSuccess) return e;
+  kern<<<ctas, kThreads, C::SMEM, stream>>>(tq, tk, tv, a);
+  return cudaGetLastError();
+}
+
+template <int DQK, int DV>
+cudaError_t launch_d(int n, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const PagedArgs& a,
+                     int ctas, cudaStream_t stream) {
+  switch (n) {
+    case 16: return launch_n<DQK, DV, 16>(tq, tk, tv, a, ctas, stream);
+    case 32: return launch_n<DQK, DV, 32>(tq, tk, tv, a, ctas, stream);
+    case 64: return launch_n<DQK, DV, 64>(tq, tk, tv, a, ctas, stream);
+    default: return cudaErrorInvalidValue;
+  }
+}
+
+}  // namespace decode
+}  // namespace paged
+
+cudaError_t launch_paged_decode(int d_qk, int d_v, int n, const CUtensorMap& tq, const CUtensorMap& tk,
+                                const CUtensorMap& tv, const PagedArgs& a, int ctas, cudaStream_t stream) {
+  if (d_qk == 64 && d_v == 64) return paged::decode::launch_d<64, 64>(n, tq, tk, tv, a, ctas, stream);
+  if (d_qk == 128 && d_v == 128) return paged::decode::launch_d<128, 128>(n, tq, tk, tv, a, ctas, stream);
+  if (d_qk == 192 && d_v == 128) return paged::decode::launch_d<192, 128>(n, tq, tk, tv, a, ctas, stream);
+  return cudaErrorInvalidValue;
+}
+
+}  // namespace gb300

@@ -369,7 +369,8 @@ struct PagedArgs {
   int score_mod;  // as in FwdArgs
   float mod_k2, mod_b, inv_scale;
   const float* alibi_slopes;
-  int tile_tokens;  // tokens of a 128-row tile: 128 / kv_group
+  int tile_tokens;   // tokens of a 128-row tile: 128 / kv_group
+  int q_box_tokens;  // tokens of a box of the q map
   // partial results, 2 * ctas slots of part_rows rows: fp32 O normalised over its keys, LSE in log2 units
   int part_rows;
   float* part_o;
@@ -382,10 +383,13 @@ struct PagedArgs {
   int* next_item;
   int* list_scratch;
 };
-// Maps: q boxes of 64 columns x kv_group heads x tile_tokens rows; k and v (caches as [pages, page_size, heads_kv, d])
-// of 64 columns x min(page_size, 128) rows. even: no request has more than one tile of rows.
+// Maps: q boxes of 64 columns x kv_group heads x q_box_tokens rows; k and v (caches as [pages, page_size, heads_kv, d])
+// of 64 columns x min(page_size, 128) rows. even: no request has more than one tile of rows; decode_rows > 0 (16, 32 or
+// 64): none has more than that, and launch_paged_decode's kernel takes the place of paged_kernel.
 cudaError_t launch_fwd_paged(int d_qk, int d_v, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
-                             const PagedArgs& a, bool even, int ctas, cudaStream_t stream);
+                             const PagedArgs& a, bool even, int decode_rows, int ctas, cudaStream_t stream);
+cudaError_t launch_paged_decode(int d_qk, int d_v, int n, const CUtensorMap& tq, const CUtensorMap& tk,
+                                const CUtensorMap& tv, const PagedArgs& a, int ctas, cudaStream_t stream);
 
 cudaError_t launch_exp2_eval(const float* x, float* y_poly, float* y_hw, int64_t n, cudaStream_t stream);
 

@@ -35,6 +35,51 @@ def library_path() -> str:
     return _abi.LIB_PATH
 
 
+_BF16, _I32, _I64, _F32 = torch.bfloat16, torch.int32, torch.int64, torch.float32
+_pack_fwd, _pack_bwd = _abi.packer(AttnFwdParams), _abi.packer(AttnBwdParams)
+_pack_plan, _pack_append, _pack_paged = (_abi.packer(AttnKvPlanParams), _abi.packer(AttnKvAppendParams),
+                                         _abi.packer(AttnPagedParams))
+_raw_stream = torch._C._cuda_getCurrentRawStream
+
+
+def _stream_of(stream, t: torch.Tensor) -> int:
+    """The stream handle of a call on t's GPU: the given one, or the current one of that GPU."""
+    if stream is None:
+        return _raw_stream(t.get_device())
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+
+
+def _bf16_layout(name: str, t, ndim: int):
+    """(shape, strides) of a checked bf16 CUDA tensor with contiguous last dim; a dim of at most one element, whose
+    stride may be anything, gets a valid one."""
+    if not isinstance(t, torch.Tensor) or t.dtype is not _BF16 or not t.is_cuda or t.dim() != ndim:
+        _check_bf16(name, t, ndim)
+    shape, stride = t.shape, t.stride()
+    if stride[-1] != 1:
+        _check_bf16(name, t, ndim)
+    if 1 in shape:
+        stride = tuple(s if n > 1 else shape[-1] for s, n in zip(stride, shape))
+    return shape, stride
+
+
+def _mod_fields(q, softcap, alibi_slopes):
+    """score_mod, softcap and alibi_slopes of a call (attn_fwd)."""
+    if softcap is None and alibi_slopes is None:
+        return 0, 0.0, 0
+    p = AttnFwdParams()
+    _set_score_mod(p, q, softcap, alibi_slopes)
+    return p.score_mod, p.softcap, p.alibi_slopes or 0
+
+
+def _check_int32(name: str, t, device: int, n: int):
+    if not isinstance(t, torch.Tensor) or t.dtype is not _I32 or not t.is_cuda or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous int32 CUDA tensor")
+    if t.get_device() != device:
+        raise ValueError(f"{name} is on {t.device} but the call is on cuda:{device}")
+    if t.dim() != 1 or (n >= 0 and t.shape[0] != n):
+        raise ValueError(f"{name} must have shape ({n if n >= 0 else 'n'},), got {tuple(t.shape)}")
+
+
 def _stream(stream, device=None) -> ctypes.c_void_p:
     if stream is None:
         stream = torch.cuda.current_stream(device)
@@ -124,6 +169,16 @@ def _workspace(size: int, device, stream=None) -> Tuple[Optional[torch.Tensor], 
     return ws, size
 
 
+def _workspace_ptr(size: int, like: torch.Tensor, stream):
+    """(the tensor, which must live until the call has been made; its address)"""
+    if size == 0:
+        return None, 0
+    ws = torch.empty(size, dtype=torch.uint8, device=like.device)
+    if stream is not None:
+        _used_on(stream, ws)
+    return ws, ws.data_ptr()
+
+
 def _used_on(stream, *tensors):
     """Tensors that a call allocates belong to the current stream; when the call runs on another one,
     their memory must not be handed out again before that stream is done with it."""
@@ -135,6 +190,14 @@ def _used_on(stream, *tensors):
             t.record_stream(s)
 
 
+def _check_offsets(q, cu_seqlens_q, cu_seqlens_k):
+    """The packed sequences' offsets: int32 [sequences + 1] on q's GPU, as many of q as of k."""
+    dev = q.get_device()
+    _check_int32("cu_seqlens_q", cu_seqlens_q, dev, -1)
+    if cu_seqlens_k is not cu_seqlens_q:
+        _check_int32("cu_seqlens_k", cu_seqlens_k, dev, cu_seqlens_q.shape[0])
+
+
 def _check_kv(q, k, v):
     """k and v of a call whose query heads may share K/V heads: q [..., H, d_qk], k [..., Hkv, d_qk] and
     v [..., Hkv, d_v] with Hkv a divisor of H, rows of k and v alike (dense: batches of q alike)."""
@@ -143,8 +206,9 @@ def _check_kv(q, k, v):
         raise ValueError(f"shape mismatch q{tuple(q.shape)} k{tuple(k.shape)} v{tuple(v.shape)}")
     if hk < 1 or h % hk != 0:
         raise ValueError(f"{hk} K/V heads do not divide {h} query heads")
+    dev = q.get_device()
     for n, t in (("k", k), ("v", v)):
-        if t.device != q.device:
+        if t.get_device() != dev:
             raise ValueError(f"{n} is on {t.device} but q is on {q.device}")
 
 
@@ -162,8 +226,9 @@ def _check_bwd(q, k, v, out, lse, dout, lse_shape, grads):
             _check_bf16(n, t, like.dim())
             if t.shape != like.shape:
                 raise ValueError(f"{n} must be {tuple(like.shape)}, got {tuple(t.shape)}")
+    dev = q.get_device()
     for n, t in (("out", out), ("lse", lse), ("dout", dout)):
-        if t.device != q.device:
+        if t.get_device() != dev:
             raise ValueError(f"{n} is on {t.device} but q is on {q.device}")
 
 
@@ -292,9 +357,7 @@ def attn_fwd_varlen(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqlen
     (query head h reads K/V head h // (H // Hkv)); cu_seqlens int32 on the device. Returns (O [total_q, H, d_v], LSE [H, total_q]). Score modifications and E4M3 inputs
     as in :func:`attn_fwd`, positions counted within each sequence."""
     f8 = _check_inputs(q, k, v, 3)
-    for n, t in (("cu_seqlens_q", cu_seqlens_q), ("cu_seqlens_k", cu_seqlens_k)):
-        if t.dtype != torch.int32 or not t.is_cuda or not t.is_contiguous():
-            raise ValueError(f"{n} must be a contiguous int32 CUDA tensor")
+    _check_offsets(q, cu_seqlens_q, cu_seqlens_k)
     tq, H, dqk = q.shape
     tk, dv = k.shape[0], v.shape[-1]
     _check_kv(q, k, v)
@@ -310,20 +373,21 @@ def attn_fwd_varlen(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqlen
         _used_on(stream, lse)
     if lse.shape != (H, tq) or not lse.is_contiguous() or lse.dtype != torch.float32:
         raise ValueError("lse must be a contiguous float32 [H, total_q] tensor")
-    p = AttnFwdParams()
-    _fill_fwd(p, q, k, v, out, lse, _strides3, scale, causal)
-    p.cu_seqlens_q, p.cu_seqlens_k = _ptr(cu_seqlens_q), _ptr(cu_seqlens_k)
-    p.num_seqs = cu_seqlens_q.numel() - 1
-    p.max_seqlen_q, p.max_seqlen_k = int(max_seqlen_q), int(max_seqlen_k)
-    p.total_q, p.total_k = tq, tk
-    p.batch = 1
-    p.rescale_stats = _ptr(rescale_stats)
-    p.exp2_emu_period = int(exp2_emu_period)
-    _set_score_mod(p, q, softcap, alibi_slopes)
-    _set_input_dtype(p, f8, q_descale, k_descale, v_descale)
-    p.cta_pair = 1 if cta_pair else 0
-    ws, nbytes = _workspace(_lib.attn_fwd_workspace_size(ctypes.byref(p)), q.device, stream)
-    _abi.check(_lib.attn_fwd_varlen(ctypes.byref(p), _ptr(ws), nbytes, _stream(stream, q.device)), "attn_fwd_varlen")
+    sq, sk, sv, so = q.stride(), k.stride(), v.stride(), out.stride()
+    mod, cap, slopes = _mod_fields(q, softcap, alibi_slopes)
+    p = _pack_fwd(
+        q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), lse.data_ptr(),
+        0, sq[0], sq[1], 0, sk[0], sk[1], 0, sv[0], sv[1], 0, so[0], so[1],
+        1, H, 0, 0, dqk, dv, cu_seqlens_q.data_ptr(), cu_seqlens_k.data_ptr(), cu_seqlens_q.shape[0] - 1,
+        int(max_seqlen_q), int(max_seqlen_k), tq, tk, scale, 1 if causal else 0, int(exp2_emu_period),
+        rescale_stats.data_ptr() if rescale_stats is not None else 0, mod, cap, slopes,
+        _abi.INPUT_E4M3 if f8 else _abi.INPUT_BF16, float(q_descale), float(k_descale), float(v_descale),
+        1 if cta_pair else 0, k.shape[1])
+    nbytes = _lib.attn_fwd_workspace_size(p)
+    ws, ws_ptr = _workspace_ptr(nbytes, q, stream)
+    status = _lib.attn_fwd_varlen(p, ws_ptr, nbytes, _stream_of(stream, q))
+    if status:
+        _abi.check(status, "attn_fwd_varlen")
     return out, lse
 
 
@@ -428,45 +492,40 @@ def attn_bwd_varlen(q, k, v, out, lse, dout, cu_seqlens_q, cu_seqlens_k, max_seq
         _check_bf16(n, t, 3)
     tq, H, dqk = q.shape
     _check_bwd(q, k, v, out, lse, dout, (H, tq), (dq, dk, dv))
-    for n, t in (("cu_seqlens_q", cu_seqlens_q), ("cu_seqlens_k", cu_seqlens_k)):
-        if t.dtype != torch.int32 or not t.is_cuda or not t.is_contiguous():
-            raise ValueError(f"{n} must be a contiguous int32 CUDA tensor")
+    _check_offsets(q, cu_seqlens_q, cu_seqlens_k)
     scale = float(softmax_scale) if softmax_scale is not None else 1.0 / math.sqrt(dqk)
     dq, dk, dv = _grad_buffers(stream, (dq, q), (dk, k), (dv, v))
-    p = AttnBwdParams()
-    _fill_fwd(p.fwd, q, k, v, out, lse, _strides3, scale, causal)
-    p.fwd.cu_seqlens_q, p.fwd.cu_seqlens_k = _ptr(cu_seqlens_q), _ptr(cu_seqlens_k)
-    p.fwd.num_seqs = cu_seqlens_q.numel() - 1
-    p.fwd.max_seqlen_q, p.fwd.max_seqlen_k = int(max_seqlen_q), int(max_seqlen_k)
-    p.fwd.total_q, p.fwd.total_k = tq, k.shape[0]
-    p.fwd.batch = 1
-    _fill_bwd(p, dout, dq, dk, dv, _strides3, deterministic, cta_pair, single_pass)
-    _set_score_mod(p.fwd, q, softcap, alibi_slopes)
-    ws, nbytes = _workspace(_lib.attn_bwd_workspace_size(ctypes.byref(p)), q.device, stream)
-    _abi.check(_lib.attn_bwd_varlen(ctypes.byref(p), _ptr(ws), nbytes, _stream(stream, q.device)), "attn_bwd_varlen")
+    sq, sk, sv, so, sd = q.stride(), k.stride(), v.stride(), out.stride(), dout.stride()
+    tdq, tdk, tdv = dq.stride(), dk.stride(), dv.stride()
+    mod, cap, slopes = _mod_fields(q, softcap, alibi_slopes)
+    p = _pack_bwd(
+        q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), lse.data_ptr(),
+        0, sq[0], sq[1], 0, sk[0], sk[1], 0, sv[0], sv[1], 0, so[0], so[1],
+        1, H, 0, 0, dqk, v.shape[2], cu_seqlens_q.data_ptr(), cu_seqlens_k.data_ptr(), cu_seqlens_q.shape[0] - 1,
+        int(max_seqlen_q), int(max_seqlen_k), tq, k.shape[0], scale, 1 if causal else 0, 0, 0, mod, cap, slopes,
+        0, 0.0, 0.0, 0.0, 0, k.shape[1],
+        dout.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(),
+        0, sd[0], sd[1], 0, tdq[0], tdq[1], 0, tdk[0], tdk[1], 0, tdv[0], tdv[1],
+        1 if deterministic else 0, 1 if cta_pair else 0, 0, 0, 0, 1 if single_pass else 0)
+    nbytes = _lib.attn_bwd_workspace_size(p)
+    ws, ws_ptr = _workspace_ptr(nbytes, q, stream)
+    status = _lib.attn_bwd_varlen(p, ws_ptr, nbytes, _stream_of(stream, q))
+    if status:
+        _abi.check(status, "attn_bwd_varlen")
     return dq, dk, dv
 
 
-def _check_ints(device, **arrays):
-    """int32 arrays of a paged-cache call: (tensor, shape), contiguous on `device`; None in a shape leaves it free."""
-    for n, (t, shape) in arrays.items():
-        if not isinstance(t, torch.Tensor) or t.dtype != torch.int32 or not t.is_cuda or not t.is_contiguous():
-            raise ValueError(f"{n} must be a contiguous int32 CUDA tensor")
-        if t.device != device:
-            raise ValueError(f"{n} is on {t.device} but the call is on {device}")
-        if t.dim() != len(shape) or any(w is not None and w != g for w, g in zip(shape, t.shape)):
-            raise ValueError(f"{n} must have shape {shape}, got {tuple(t.shape)}")
-
-
-def _check_table(t, device, num_seqs):
-    if not isinstance(t, torch.Tensor) or t.dtype != torch.int32 or not t.is_cuda or t.dim() != 2:
+def _check_table(t, device: int, num_seqs: int) -> int:
+    """Row stride of a checked block table."""
+    if not isinstance(t, torch.Tensor) or t.dtype is not _I32 or not t.is_cuda or t.dim() != 2:
         raise ValueError("block_table must be an int32 CUDA tensor [requests, max_pages]")
-    if t.device != device:
-        raise ValueError(f"block_table is on {t.device} but the call is on {device}")
-    if t.shape[0] != num_seqs or t.shape[1] < 1 or t.stride(1) != 1 or (num_seqs > 1 and t.stride(0) < t.shape[1]):
+    if t.get_device() != device:
+        raise ValueError(f"block_table is on {t.device} but the call is on cuda:{device}")
+    (rows, cols), (row, col) = t.shape, t.stride()
+    if rows != num_seqs or cols < 1 or (col != 1 and cols > 1) or (rows > 1 and row < cols):
         raise ValueError(f"block_table must be [{num_seqs}, max_pages] with contiguous rows that do not overlap, got "
                          f"{tuple(t.shape)} with strides {t.stride()}")
-    return max(t.stride(0), t.shape[1])
+    return max(row, cols)
 
 
 def attn_kv_plan(seqlens_old: torch.Tensor, seqlens_new: torch.Tensor, block_table: torch.Tensor,
@@ -483,55 +542,53 @@ def attn_kv_plan(seqlens_old: torch.Tensor, seqlens_new: torch.Tensor, block_tab
     Returns (cu_seqlens_q [requests + 1], seqlens_k [requests], slot_mapping, status [1]): status 0, or 1 (too few
     free pages), 2 (a row of the table is too short), 3 (slot_mapping is), 4 (free_pages is), and then nothing is
     changed and the step holds no tokens."""
-    n = seqlens_old.numel() if isinstance(seqlens_old, torch.Tensor) else 0
-    dev = seqlens_old.device if isinstance(seqlens_old, torch.Tensor) else None
-    _check_ints(dev, seqlens_old=(seqlens_old, (n,)), seqlens_new=(seqlens_new, (n,)), free_pages=(free_pages, (None,)),
-                free_count=(free_count, (1,)))
+    if not isinstance(seqlens_old, torch.Tensor) or not seqlens_old.is_cuda:
+        raise ValueError("seqlens_old must be a contiguous int32 CUDA tensor")
+    n, dev = seqlens_old.numel(), seqlens_old.get_device()
     if n < 1:
         raise ValueError("attn_kv_plan needs at least one request")
+    _check_int32("seqlens_old", seqlens_old, dev, n)
+    _check_int32("seqlens_new", seqlens_new, dev, n)
+    _check_int32("free_pages", free_pages, dev, -1)
+    _check_int32("free_count", free_count, dev, 1)
     table_stride = _check_table(block_table, dev, n)
 
-    def given(t, shape, dtype=torch.int32):
+    def given(name, t, size):
         if t is None:
-            t = torch.empty(shape, dtype=dtype, device=dev)
+            t = torch.empty((size,), dtype=_I32, device=seqlens_old.device)
             _used_on(stream, t)
+        else:
+            _check_int32(name, t, dev, size)
         return t
 
-    cu_seqlens_q, seqlens_k, status = given(cu_seqlens_q, (n + 1,)), given(seqlens_k, (n,)), given(status, (1,))
-    free_count_out = free_count if free_count_out is None else free_count_out
-    _check_ints(dev, cu_seqlens_q=(cu_seqlens_q, (n + 1,)), seqlens_k=(seqlens_k, (n,)), status=(status, (1,)),
-                free_count_out=(free_count_out, (1,)))
+    cu_seqlens_q, seqlens_k = given("cu_seqlens_q", cu_seqlens_q, n + 1), given("seqlens_k", seqlens_k, n)
+    status = given("status", status, 1)
+    free_count_out = free_count if free_count_out is None else given("free_count_out", free_count_out, 1)
     if isinstance(slot_mapping, int):
-        slot_mapping = given(None, (slot_mapping,), torch.int64)
-    if slot_mapping.dtype != torch.int64 or slot_mapping.dim() != 1 or not slot_mapping.is_contiguous() or \
-            slot_mapping.device != dev:
-        raise ValueError(f"slot_mapping must be a contiguous int64 tensor [max_tokens] on {dev}")
-    p = AttnKvPlanParams()
-    p.seqlens_old, p.seqlens_new, p.block_table = _ptr(seqlens_old), _ptr(seqlens_new), _ptr(block_table)
-    p.block_table_stride = table_stride
-    p.free_pages, p.free_count, p.free_count_out = _ptr(free_pages), _ptr(free_count), _ptr(free_count_out)
-    p.cu_seqlens_q, p.seqlens_k, p.slot_mapping, p.status = (_ptr(cu_seqlens_q), _ptr(seqlens_k), _ptr(slot_mapping),
-                                                             _ptr(status))
-    p.num_seqs, p.max_pages, p.page_size = n, block_table.shape[1], int(page_size)
-    p.free_capacity, p.max_tokens = free_pages.numel(), slot_mapping.numel()
-    _abi.check(_lib.attn_kv_plan(ctypes.byref(p), _stream(stream, dev)), "attn_kv_plan")
+        slot_mapping = torch.empty((slot_mapping,), dtype=_I64, device=seqlens_old.device)
+        _used_on(stream, slot_mapping)
+    elif slot_mapping.dtype is not _I64 or slot_mapping.dim() != 1 or not slot_mapping.is_contiguous() or \
+            not slot_mapping.is_cuda or slot_mapping.get_device() != dev:
+        raise ValueError(f"slot_mapping must be a contiguous int64 tensor [max_tokens] on cuda:{dev}")
+    p = _pack_plan(seqlens_old.data_ptr(), seqlens_new.data_ptr(), block_table.data_ptr(), table_stride,
+                   free_pages.data_ptr(), free_count.data_ptr(), free_count_out.data_ptr(), cu_seqlens_q.data_ptr(),
+                   seqlens_k.data_ptr(), slot_mapping.data_ptr(), status.data_ptr(),
+                   n, block_table.shape[1], int(page_size), free_pages.shape[0], slot_mapping.shape[0])
+    st = _lib.attn_kv_plan(p, _stream_of(stream, seqlens_old))
+    if st:
+        _abi.check(st, "attn_kv_plan")
     return cu_seqlens_q, seqlens_k, slot_mapping, status
 
 
-def _check_caches(k_cache, v_cache, device, heads_kv=None):
-    _check_bf16("k_cache", k_cache, 4)
-    _check_bf16("v_cache", v_cache, 4)
-    if k_cache.shape[:3] != v_cache.shape[:3] or (heads_kv is not None and k_cache.shape[2] != heads_kv):
-        raise ValueError(f"k_cache {tuple(k_cache.shape)} and v_cache {tuple(v_cache.shape)} must be [pages, page_size, "
-                         f"{'heads' if heads_kv is None else heads_kv}, d]")
+def _cache_layout(k_cache, v_cache, device: int):
+    """Layouts of checked caches [pages, page_size, Hkv, d]."""
+    (ks, kt), (vs, vt) = _bf16_layout("k_cache", k_cache, 4), _bf16_layout("v_cache", v_cache, 4)
+    if ks[:3] != vs[:3]:
+        raise ValueError(f"k_cache {tuple(ks)} and v_cache {tuple(vs)} must be [pages, page_size, Hkv, d] alike but for d")
     for n, t in (("k_cache", k_cache), ("v_cache", v_cache)):
-        if t.device != device:
-            raise ValueError(f"{n} is on {t.device} but the call is on {device}")
-
-
-def _row_strides(t: torch.Tensor):
-    """Element strides of all but the last dim; a dim of one element may carry any stride and gets a valid one."""
-    return tuple(s if n > 1 else t.shape[-1] for s, n in zip(t.stride()[:-1], t.shape[:-1]))
+        if t.get_device() != device:
+            raise ValueError(f"{n} is on {t.device} but the call is on cuda:{device}")
+    return ks, kt, vs, vt
 
 
 def attn_kv_append(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
@@ -540,27 +597,22 @@ def attn_kv_append(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_ca
     page_size, Hkv, d_qk] and v_cache [pages, page_size, Hkv, d_v] (bf16, any strides with contiguous d): row i goes
     to slot ``slot_mapping[i]`` (int64; page slot // page_size, row slot % page_size). Slots outside the cache, as -1,
     write nothing; slots must differ."""
-    _check_bf16("k", k, 3)
-    _check_bf16("v", v, 3)
-    _check_caches(k_cache, v_cache, k.device, k.shape[1])
-    if v.shape[:2] != k.shape[:2] or v.device != k.device:
-        raise ValueError(f"shape or device mismatch k{tuple(k.shape)} v{tuple(v.shape)}")
-    if k_cache.shape[3] != k.shape[2] or v_cache.shape[3] != v.shape[2]:
-        raise ValueError(f"k_cache {tuple(k_cache.shape)} and v_cache {tuple(v_cache.shape)} do not hold rows of "
-                         f"{k.shape[2]} and {v.shape[2]}")
-    if slot_mapping.dtype != torch.int64 or slot_mapping.shape != (k.shape[0],) or not slot_mapping.is_contiguous() or \
-            slot_mapping.device != k.device:
-        raise ValueError(f"slot_mapping must be a contiguous int64 tensor [{k.shape[0]}] on {k.device}")
-    p = AttnKvAppendParams()
-    p.k, p.v, p.k_cache, p.v_cache, p.slot_mapping = (_ptr(k), _ptr(v), _ptr(k_cache), _ptr(v_cache),
-                                                      _ptr(slot_mapping))
-    p.k_row_stride, p.k_head_stride = _row_strides(k)
-    p.v_row_stride, p.v_head_stride = _row_strides(v)
-    p.k_cache_page_stride, p.k_cache_row_stride, p.k_cache_head_stride = _row_strides(k_cache)
-    p.v_cache_page_stride, p.v_cache_row_stride, p.v_cache_head_stride = _row_strides(v_cache)
-    p.tokens, p.heads_kv, p.d_qk, p.d_v = k.shape[0], k.shape[1], k.shape[2], v.shape[2]
-    p.page_size, p.num_pages = k_cache.shape[1], k_cache.shape[0]
-    _abi.check(_lib.attn_kv_append(ctypes.byref(p), _stream(stream, k.device)), "attn_kv_append")
+    (ks, kt), (vs, vt) = _bf16_layout("k", k, 3), _bf16_layout("v", v, 3)
+    dev = k.get_device()
+    kcs, kct, vcs, vct = _cache_layout(k_cache, v_cache, dev)
+    if vs[:2] != ks[:2] or v.get_device() != dev:
+        raise ValueError(f"shape or device mismatch k{tuple(ks)} v{tuple(vs)}")
+    if kcs[2:] != ks[1:] or vcs[2:] != vs[1:]:
+        raise ValueError(f"k_cache {tuple(kcs)} and v_cache {tuple(vcs)} do not hold rows of k {tuple(ks)} and v {tuple(vs)}")
+    if slot_mapping.dtype is not _I64 or slot_mapping.dim() != 1 or slot_mapping.shape[0] != ks[0] or \
+            not slot_mapping.is_contiguous() or not slot_mapping.is_cuda or slot_mapping.get_device() != dev:
+        raise ValueError(f"slot_mapping must be a contiguous int64 tensor [{ks[0]}] on cuda:{dev}")
+    p = _pack_append(k.data_ptr(), v.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), kt[0], kt[1], vt[0], vt[1],
+                     kct[0], kct[1], kct[2], vct[0], vct[1], vct[2], slot_mapping.data_ptr(),
+                     ks[0], ks[1], ks[2], vs[2], kcs[1], kcs[0])
+    st = _lib.attn_kv_append(p, _stream_of(stream, k))
+    if st:
+        _abi.check(st, "attn_kv_append")
 
 
 def attn_fwd_paged(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, block_table: torch.Tensor,
@@ -576,44 +628,43 @@ def attn_fwd_paged(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor
     to position i + seqlens_k[s] - n. cu_seqlens_q [requests + 1], seqlens_k [requests] and the table are int32 on
     q's GPU; ``max_seqlen_q`` bounds the queries of a request. Score modifications as in :func:`attn_fwd`.
     Returns (O [total_q, H, d_v] bf16, LSE [H, total_q] fp32); rows behind the last request are not written."""
-    _check_bf16("q", q, 3)
-    _check_caches(k_cache, v_cache, q.device)
-    tq, H, dqk = q.shape
-    hk, dv = k_cache.shape[2], v_cache.shape[3]
-    if k_cache.shape[3] != dqk:
-        raise ValueError(f"k_cache {tuple(k_cache.shape)} does not match q {tuple(q.shape)}")
+    (tq, H, dqk), sq = _bf16_layout("q", q, 3)
+    dev = q.get_device()
+    ks, kt, vs, vt = _cache_layout(k_cache, v_cache, dev)
+    hk, dv = ks[2], vs[3]
+    if ks[3] != dqk:
+        raise ValueError(f"k_cache {tuple(ks)} does not match q {tuple(q.shape)}")
     if hk < 1 or H % hk != 0:
         raise ValueError(f"{hk} K/V heads do not divide {H} query heads")
-    n = seqlens_k.numel() if isinstance(seqlens_k, torch.Tensor) else 0
-    _check_ints(q.device, seqlens_k=(seqlens_k, (n,)), cu_seqlens_q=(cu_seqlens_q, (n + 1,)))
-    table_stride = _check_table(block_table, q.device, n)
+    _check_int32("seqlens_k", seqlens_k, dev, -1)
+    n = seqlens_k.shape[0]
+    _check_int32("cu_seqlens_q", cu_seqlens_q, dev, n + 1)
+    table_stride = _check_table(block_table, dev, n)
     if out is None:
-        out = torch.empty((tq, H, dv), dtype=torch.bfloat16, device=q.device)
-        _used_on(stream, out)
-    _check_bf16("out", out, 3)
-    if out.shape != (tq, H, dv) or out.device != q.device:
-        raise ValueError(f"out must be {(tq, H, dv)} on {q.device}, got {tuple(out.shape)} on {out.device}")
+        out = torch.empty((tq, H, dv), dtype=_BF16, device=q.device)
+        so = (H * dv, dv)
+    else:
+        shape, so = _bf16_layout("out", out, 3)
+        if shape != (tq, H, dv) or out.get_device() != dev:
+            raise ValueError(f"out must be {(tq, H, dv)} on cuda:{dev}, got {tuple(shape)} on {out.device}")
     if lse is None:
-        lse = torch.empty((H, tq), dtype=torch.float32, device=q.device)
-        _used_on(stream, lse)
-    if lse.shape != (H, tq) or not lse.is_contiguous() or lse.dtype != torch.float32 or lse.device != q.device:
-        raise ValueError(f"lse must be a contiguous float32 [H, total_q] tensor on {q.device}")
-    p = AttnPagedParams()
-    p.q, p.k_cache, p.v_cache, p.o, p.lse = _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(out), _ptr(lse)
-    p.q_row_stride, p.q_head_stride = _row_strides(q)
-    p.o_row_stride, p.o_head_stride = _row_strides(out)
-    p.k_page_stride, p.k_row_stride, p.k_head_stride = _row_strides(k_cache)
-    p.v_page_stride, p.v_row_stride, p.v_head_stride = _row_strides(v_cache)
-    p.block_table, p.block_table_stride = _ptr(block_table), table_stride
-    p.cu_seqlens_q, p.seqlens_k = _ptr(cu_seqlens_q), _ptr(seqlens_k)
-    p.num_seqs, p.heads, p.heads_kv, p.d_qk, p.d_v = n, H, hk, dqk, dv
-    p.page_size, p.num_pages, p.max_pages = k_cache.shape[1], k_cache.shape[0], block_table.shape[1]
-    p.total_q, p.max_seqlen_q = tq, int(max_seqlen_q)
-    p.softmax_scale = float(softmax_scale) if softmax_scale is not None else 1.0 / math.sqrt(dqk)
-    p.causal = 1 if causal else 0
-    _set_score_mod(p, q, softcap, alibi_slopes)
-    ws, nbytes = _workspace(_lib.attn_fwd_paged_workspace_size(ctypes.byref(p)), q.device, stream)
-    _abi.check(_lib.attn_fwd_paged(ctypes.byref(p), _ptr(ws), nbytes, _stream(stream, q.device)), "attn_fwd_paged")
+        lse = torch.empty((H, tq), dtype=_F32, device=q.device)
+    elif lse.shape != (H, tq) or not lse.is_contiguous() or lse.dtype is not _F32 or lse.device != q.device:
+        raise ValueError(f"lse must be a contiguous float32 [H, total_q] tensor on cuda:{dev}")
+    mod, cap, slopes = _mod_fields(q, softcap, alibi_slopes)
+    p = _pack_paged(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), out.data_ptr(), lse.data_ptr(),
+                    sq[0], sq[1], so[0], so[1], kt[0], kt[1], kt[2], vt[0], vt[1], vt[2],
+                    block_table.data_ptr(), table_stride, cu_seqlens_q.data_ptr(), seqlens_k.data_ptr(),
+                    n, H, hk, dqk, dv, ks[1], ks[0], block_table.shape[1], tq, int(max_seqlen_q),
+                    float(softmax_scale) if softmax_scale is not None else 1.0 / math.sqrt(dqk),
+                    1 if causal else 0, mod, cap, slopes)
+    nbytes = _lib.attn_fwd_paged_workspace_size(p)
+    ws, ws_ptr = _workspace_ptr(nbytes, q, stream)
+    if stream is not None:
+        _used_on(stream, out, lse)
+    st = _lib.attn_fwd_paged(p, ws_ptr, nbytes, _stream_of(stream, q))
+    if st:
+        _abi.check(st, "attn_fwd_paged")
     return out, lse
 
 

@@ -5,6 +5,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libattn_gb300.so")
@@ -97,6 +98,30 @@ class AttnPagedParams(ctypes.Structure):
     ]
 
 
+_CODES = {c_i32: "i", c_i64: "q", c_f32: "f", c_vp: "P"}
+
+
+def _format(cls) -> str:
+    out = ""
+    for _, t in cls._fields_:
+        if t in _CODES:
+            out += _CODES[t]
+        elif issubclass(t, ctypes.Array):
+            out += _CODES[t._type_] * t._length_
+        else:
+            out += _format(t)
+    return out
+
+
+def packer(cls):
+    """A function from a parameter struct's fields (in order, nested ones flattened, pointers as ints) to its bytes,
+    which the entry points take in its place: one call instead of an attribute set per field."""
+    s = struct.Struct("@" + _format(cls) + "0P")
+    if s.size != ctypes.sizeof(cls):
+        raise ImportError(f"{cls.__name__}: packed size {s.size} != {ctypes.sizeof(cls)}")
+    return s.pack
+
+
 _lib = None
 
 
@@ -111,28 +136,29 @@ def load(path: str = LIB_PATH):
             "(nvcc, sm_103a). There is no non-CUDA fallback.")
     lib = ctypes.CDLL(path)
     P = ctypes.POINTER
+    # parameter structs: byref(struct) or its packed bytes
     sig = {
-        "attn_fwd_workspace_size": (ctypes.c_size_t, [P(AttnFwdParams)]),
-        "attn_bwd_workspace_size": (ctypes.c_size_t, [P(AttnBwdParams)]),
-        "attn_fwd": (ctypes.c_int, [P(AttnFwdParams), c_vp, ctypes.c_size_t, c_vp]),
-        "attn_fwd_varlen": (ctypes.c_int, [P(AttnFwdParams), c_vp, ctypes.c_size_t, c_vp]),
-        "attn_fwd_block_sparse": (ctypes.c_int, [P(AttnFwdParams), c_vp, c_vp, ctypes.c_int32, ctypes.c_int32, c_vp,
+        "attn_fwd_workspace_size": (ctypes.c_size_t, [c_vp]),
+        "attn_bwd_workspace_size": (ctypes.c_size_t, [c_vp]),
+        "attn_fwd": (ctypes.c_int, [c_vp, c_vp, ctypes.c_size_t, c_vp]),
+        "attn_fwd_varlen": (ctypes.c_int, [c_vp, c_vp, ctypes.c_size_t, c_vp]),
+        "attn_fwd_block_sparse": (ctypes.c_int, [c_vp, c_vp, c_vp, ctypes.c_int32, ctypes.c_int32, c_vp,
                                                  ctypes.c_size_t, c_vp]),
-        "attn_bwd_block_sparse_workspace_size": (ctypes.c_size_t, [P(AttnBwdParams), ctypes.c_int32]),
-        "attn_bwd_block_sparse": (ctypes.c_int, [P(AttnBwdParams), c_vp, c_vp, ctypes.c_int32, ctypes.c_int32, c_vp,
+        "attn_bwd_block_sparse_workspace_size": (ctypes.c_size_t, [c_vp, ctypes.c_int32]),
+        "attn_bwd_block_sparse": (ctypes.c_int, [c_vp, c_vp, c_vp, ctypes.c_int32, ctypes.c_int32, c_vp,
                                                  ctypes.c_size_t, c_vp]),
-        "attn_bwd": (ctypes.c_int, [P(AttnBwdParams), c_vp, ctypes.c_size_t, c_vp]),
-        "attn_bwd_varlen": (ctypes.c_int, [P(AttnBwdParams), c_vp, ctypes.c_size_t, c_vp]),
-        "attn_bwd_noalloc": (ctypes.c_int, [P(AttnBwdParams), c_vp]),
-        "attn_kv_plan": (ctypes.c_int, [P(AttnKvPlanParams), c_vp]),
-        "attn_kv_append": (ctypes.c_int, [P(AttnKvAppendParams), c_vp]),
-        "attn_fwd_paged_workspace_size": (ctypes.c_size_t, [P(AttnPagedParams)]),
-        "attn_fwd_paged": (ctypes.c_int, [P(AttnPagedParams), c_vp, ctypes.c_size_t, c_vp]),
+        "attn_bwd": (ctypes.c_int, [c_vp, c_vp, ctypes.c_size_t, c_vp]),
+        "attn_bwd_varlen": (ctypes.c_int, [c_vp, c_vp, ctypes.c_size_t, c_vp]),
+        "attn_bwd_noalloc": (ctypes.c_int, [c_vp, c_vp]),
+        "attn_kv_plan": (ctypes.c_int, [c_vp, c_vp]),
+        "attn_kv_append": (ctypes.c_int, [c_vp, c_vp]),
+        "attn_fwd_paged_workspace_size": (ctypes.c_size_t, [c_vp]),
+        "attn_fwd_paged": (ctypes.c_int, [c_vp, c_vp, ctypes.c_size_t, c_vp]),
         "attn_kv_plan_params_size": (ctypes.c_size_t, []),
         "attn_kv_append_params_size": (ctypes.c_size_t, []),
         "attn_paged_params_size": (ctypes.c_size_t, []),
         "attn_exp2_eval": (ctypes.c_int, [c_vp, c_vp, c_vp, c_i64, c_vp]),
-        "attn_diag_wait_timeout": (ctypes.c_int, [P(AttnFwdParams), ctypes.c_uint32, c_vp]),
+        "attn_diag_wait_timeout": (ctypes.c_int, [c_vp, ctypes.c_uint32, c_vp]),
         "attn_get_device_status": (ctypes.c_int, [c_vp, P(ctypes.c_uint32)]),
         "attn_status_string": (ctypes.c_char_p, [ctypes.c_int]),
         "attn_last_cuda_error": (ctypes.c_char_p, []),

@@ -913,10 +913,10 @@ PagedPlan paged_plan(const attn_paged_params* p) {
   pl.off_merge = pl.off_lse + round256(rows * 4);
   pl.bytes = pl.off_merge + round256(kPagedMaxCtas * static_cast<int64_t>(sizeof(MergeUnit)));
   if (!pl.even) {
-    // units of 2 * tile_tokens tokens (the last of each request may be shorter) per K/V head, and a cut per CTA
+    // units of 2 * tile_tokens tokens (the last of each request may be shorter) per K/V head, behind the parts of cut ones
     pl.items = p->heads_kv * (static_cast<int64_t>(p->total_q) / (2 * pl.tile_tokens) + p->num_seqs) + 2 * kPagedMaxCtas;
     pl.off_list = pl.bytes;
-    pl.off_items = pl.off_list + 256 + round256(static_cast<int64_t>(p->num_seqs) * 4);
+    pl.off_items = pl.off_list + 256;
     pl.bytes = pl.off_items + round256(pl.items * static_cast<int64_t>(sizeof(ChunkItem)));
   }
   return pl;
@@ -962,9 +962,7 @@ attn_status_t run_fwd_paged(const attn_paged_params* p, void* ws, size_t ws_byte
   a.part_lse = reinterpret_cast<float*>(base + pl.off_lse);
   a.merge = reinterpret_cast<MergeUnit*>(base + pl.off_merge);
   if (!pl.even) {
-    a.n_items = reinterpret_cast<int*>(base + pl.off_list);
-    a.next_item = a.n_items + 1;
-    a.list_scratch = reinterpret_cast<int*>(base + pl.off_list + 256);
+    a.list = reinterpret_cast<ChunkList*>(base + pl.off_list);
     a.items = reinterpret_cast<ChunkItem*>(base + pl.off_items);
     a.items_bound = static_cast<int>(pl.items);
   }

@@ -39,6 +39,8 @@
 // P enters the PV product in bf16, V's type in the cache (half a step is 2^-9 of
 // each weight): an fp16 copy of V, as the contiguous forward makes, would cost a
 // second pass over keys that a decoding step reads only once. Every sum is fp32.
+#include <cstddef>
+
 #include "kernels.h"
 #include "paged_common.cuh"
 #include "ptx_sm100.cuh"
@@ -73,13 +75,18 @@ struct Cfg {
 };
 
 struct Bars {
+  // one arrival
   uint64_t q_full, q_free;
   uint64_t k_full[6], k_empty[6], v_full[6], v_empty[6];
-  uint64_t s_full[2], p_full[2], o_full[2];
-  uint64_t o_free;              // a segment is over: its O has been read, its MMAs issued
-  uint64_t x_full[2];           // dual: a stream's (m, l) are in shared memory
-  uint64_t seg_full[kSegs], seg_empty[kSegs];
+  uint64_t s_full[2], o_full[2];
+  uint64_t seg_full[kSegs];
   uint64_t mma_done;
+  // four: a warpgroup's warps
+  uint64_t p_full[2];
+  uint64_t x_full[2];  // dual: a stream's (m, l) are in shared memory
+  // nine: eight softmax warps and the MMA thread
+  uint64_t seg_empty[kSegs];
+  uint64_t o_free;     // a segment is over: its O has been read, its MMAs issued (so neither side gets two ahead)
   uint32_t tmem_base;
   EvenStart even;
 };
@@ -104,30 +111,15 @@ __global__ void __launch_bounds__(kThreads, 1)
   Seg* sSeg = reinterpret_cast<Seg*>(smem + C::OFF_SEG);
   Bars* bar = reinterpret_cast<Bars*>(smem + C::OFF_BAR);
   const uint32_t warp = warp_id(), lane = lane_id();
-  const int tid = static_cast<int>(threadIdx.x);
 
-  if (tid == 0) {
-    mbar_init(&bar->q_full, 1);
-    mbar_init(&bar->q_free, 1);
-    for (int s = 0; s < 6; ++s) {
-      mbar_init(&bar->k_full[s], 1);
-      mbar_init(&bar->k_empty[s], 1);
-      mbar_init(&bar->v_full[s], 1);
-      mbar_init(&bar->v_empty[s], 1);
-    }
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(&bar->s_full[i], 1);
-      mbar_init(&bar->p_full[i], 4);
-      mbar_init(&bar->o_full[i], 1);
-      mbar_init(&bar->x_full[i], 4);
-    }
-    mbar_init(&bar->o_free, 9);  // eight softmax warps and the MMA thread, so that neither side gets two segments ahead
-    for (int s = 0; s < kSegs; ++s) {
-      mbar_init(&bar->seg_full[s], 1);
-      mbar_init(&bar->seg_empty[s], 9);  // the MMA thread and eight softmax warps
-    }
-    mbar_init(&bar->mma_done, 1);
+  constexpr int kOnes = offsetof(Bars, p_full) / 8, kFours = offsetof(Bars, seg_empty) / 8,
+                kAll = offsetof(Bars, tmem_base) / 8;
+  if (threadIdx.x >= 64 && threadIdx.x < 64 + kAll) {  // one thread per barrier
+    const int x = static_cast<int>(threadIdx.x) - 64;
+    mbar_init(reinterpret_cast<uint64_t*>(bar) + x, x < kOnes ? 1 : x < kFours ? 4 : 9);
     fence_barrier_init();
+  }
+  if (threadIdx.x == 0) {
     tma_prefetch_desc(&tmq);
     tma_prefetch_desc(&tmk);
     tma_prefetch_desc(&tmv);
@@ -150,74 +142,36 @@ __global__ void __launch_bounds__(kThreads, 1)
     regs_dec<C::REG_LO>();
     if (warp == 0) {
       // ===================== work and copies ================================
-      const int np = a.page_size < BN ? BN >> a.page_shift : 1;  // pages (boxes along the keys) of a key block
-      const int box_rows = a.page_size < BN ? a.page_size : BN;
-      const int my_page = static_cast<int>(lane) % np, my_chunk = static_cast<int>(lane) / np;
       const uint32_t q_bytes = static_cast<uint32_t>(a.kv_group * a.tile_tokens) * 128u * C::QCH;
-      uint32_t ck = 0, cv = 0, cq = 0, seg_i = 0;  // copies and segments so far
-      uint32_t cs0 = 0, cs1 = 0, phase = 0;
-      bool ok = true;
+      uint32_t cq = 0;
       EvenWalk walk;
       if constexpr (EVEN) walk.begin(a, &bar->even);
       int item = static_cast<int>(blockIdx.x);  // list: this CTA's next entry
-      const int n_items = EVEN ? 0 : *a.n_items;
-      auto next_seg = [&]() -> Seg {
-        if constexpr (EVEN) {
-          return walk.next(a, &bar->even);
-        } else {
-          Seg w;
-          w.more = 0, w.n0 = w.n1 = 0;
-          if (item < n_items) {
-            const ChunkItem it = a.items[item];
-            int nx = 0;
-            if (lane == 0) nx = atomicAdd(a.next_item, 1);  // needed one segment later
-            const Bounds b = bounds(a, it.seq);
-            w = make_seg(a, b, it.seq, it.hk, it.tok0, min(b.nq - it.tok0, 2 * a.tile_tokens), it.kt0, it.kt1, it.part);
-            item = __shfl_sync(0xffffffffu, nx, 0);
-          }
-          return w;
-        }
-      };
-      Seg w = next_seg();
-      int page = w.more ? page_of(a, w, w.kt0, my_page) : 0;
-      for (;;) {
-        const int slot = static_cast<int>(seg_i % kSegs);
-        ok = mbar_wait_warp(&bar->seg_empty[slot], ((seg_i / kSegs) & 1u) ^ 1u, a.status, 0x3100);
-        if (!ok) break;
-        const int n = max(w.n0, w.n1);
-        if (lane == 0) {
-          w.v0 = cv, w.s0 = cs0, w.s1 = cs1, w.phase = phase;
-          sSeg[slot] = w;
-          mbar_arrive(&bar->seg_full[slot]);
-        }
-        ++seg_i;
-        if (!w.more) break;
-        cs0 += w.dual ? (w.n0 + 1) / 2 : w.n0;
-        cs1 += w.dual ? w.n0 / 2 : w.n1;
-        phase ^= (w.n0 > 0 ? 1u : 0u) | ((w.dual ? w.n0 > 1 : w.n1 > 0) ? 2u : 0u) | (w.dual ? 4u : 0u);
-        // ---- its copies; the next segment and its first page are looked up behind the first few
-        Seg nw;
-        nw.more = 0;
-        int npage = 0;
-        if (n == 0) {
-          nw = next_seg();
-          npage = nw.more ? page_of(a, nw, nw.kt0, my_page) : 0;
-        }
-        for (int j = 0; j < n; ++j) {
-          const int next = j + 1 < n ? page_of(a, w, w.kt0 + j + 1, my_page) : 0;  // fetched ahead of the waits
-          const int row = a.page_size > BN ? ((w.kt0 + j) << 7) & (a.page_size - 1) : 0;
-          const uint32_t ks = ck % C::NK;
-          ok = mbar_wait_warp(&bar->k_empty[ks], ((ck / C::NK) & 1u) ^ 1u, a.status, 0x3110);
-          if (!ok) break;
-          if (lane == 0) mbar_arrive_expect_tx(&bar->k_full[ks], C::K_BYTES);
-          __syncwarp();
-          if (my_chunk < C::QCH)
-            tma_load_4d(sK + ks * C::K_BYTES + my_chunk * kChunk + my_page * box_rows * 128, &tmk, &bar->k_full[ks],
-                        my_chunk * 64, w.hk, row, page);
-          ++ck;
-          if (j == 0) {  // Q behind the first K: that slot may be free long before the previous Q is
-            ok = mbar_wait_warp(&bar->q_free, (cq & 1u) ^ 1u, a.status, 0x3120);
-            if (!ok) break;
+      const int n_items = EVEN ? 0 : a.list->n_items, n_parts = EVEN ? 0 : a.list->n_parts;
+      const int first_unit = 2 * static_cast<int>(gridDim.x);
+      const bool ok = copy_loop<C>(
+          a, bar, sSeg, sK, sV, &tmk, &tmv, 0x3100,
+          [&]() -> Seg {
+            if constexpr (EVEN) {
+              return walk.next(a, &bar->even);
+            } else {
+              Seg w;
+              w.more = 0, w.n0 = w.n1 = 0;
+              while (item < n_items) {
+                const ChunkItem it = a.items[item < n_parts ? item : item - n_parts + first_unit];
+                int nx = 0;
+                if (lane == 0) nx = atomicAdd(&a.list->next, 1);  // needed one segment later
+                item = __shfl_sync(0xffffffffu, nx, 0);
+                if (it.seq < 0) continue;  // a unit that was cut: its parts are entries of their own
+                const Bounds b = bounds(a, it.seq);
+                w = make_seg(a, b, it.seq, it.hk, it.tok0, min(b.nq - it.tok0, 2 * a.tile_tokens), it.kt0, it.kt1, it.part);
+                break;
+              }
+              return w;
+            }
+          },
+          [&](const Seg& w) {
+            if (!mbar_wait_warp(&bar->q_free, (cq & 1u) ^ 1u, a.status, 0x3120)) return false;
             if (lane == 0) mbar_arrive_expect_tx(&bar->q_full, q_bytes * (w.dual ? 1u : 2u));
             __syncwarp();
             const int tiles = w.dual ? 1 : 2;
@@ -227,140 +181,122 @@ __global__ void __launch_bounds__(kThreads, 1)
                           w.q_row + t * a.tile_tokens, 0);
             }
             ++cq;
-          }
-          const uint32_t vs = cv % C::NV;
-          ok = mbar_wait_warp(&bar->v_empty[vs], ((cv / C::NV) & 1u) ^ 1u, a.status, 0x3130);
-          if (!ok) break;
-          if (lane == 0) mbar_arrive_expect_tx(&bar->v_full[vs], C::V_BYTES);
-          __syncwarp();
-          if (my_chunk < C::VCH)
-            tma_load_4d(sV + vs * C::V_BYTES + my_chunk * kChunk + my_page * box_rows * 128, &tmv, &bar->v_full[vs],
-                        my_chunk * 64, w.hk, row, page);
-          ++cv;
-          page = next;
-          if (j == min(n - 1, C::NK - 1)) {
-            nw = next_seg();
-            npage = nw.more ? page_of(a, nw, nw.kt0, my_page) : 0;
-          }
-        }
-        if (!ok) break;
-        w = nw;
-        page = npage;
-      }
+            return true;
+          });
       if constexpr (EVEN) walk.finish(a);
-      if (!ok) {  // let the copies in flight land before the CTA exits
-        for (uint32_t u = 0; u < C::NK && u < ck; ++u)
-          mbar_wait(&bar->k_full[(ck - 1 - u) % C::NK], ((ck - 1 - u) / C::NK) & 1u, nullptr, 0);
-        for (uint32_t u = 0; u < C::NV && u < cv; ++u)
-          mbar_wait(&bar->v_full[(cv - 1 - u) % C::NV], ((cv - 1 - u) / C::NV) & 1u, nullptr, 0);
-        if (cq > 0) mbar_wait(&bar->q_full, (cq - 1) & 1u, nullptr, 0);
-      }
-    } else if (warp == 1 && lane == 0) {
+      if (!ok && cq > 0) mbar_wait(&bar->q_full, (cq - 1) & 1u, nullptr, 0);
+    } else if (warp == 1) {
       // ===================== MMA issue ======================================
+      // The whole warp walks the loop, so that its counters and descriptors are uniform across it; lane 0 issues.
       constexpr uint32_t idS = idesc_bf16_f32(BM, BN, false, false);
       constexpr uint32_t idO = idesc_bf16_f32(BM, DV, false, true);
-      uint32_t ck = 0, cv = 0, cq = 0, seg_i = 0, cp[2] = {0, 0};
+      Ring<C::NK> rk;
+      Ring<C::NV> rv;
+      uint32_t cq = 0, seg_i = 0, pp = 0;  // pp: a bit per stream
       bool ok = true;
-      auto issue_s = [&](int i, int q_tile, uint32_t k_slot) {
-        const uint64_t dq = smem_desc(smem_u32(sQ + q_tile * C::Q_BYTES), 16, 1024, SWZ_128B);
-        const uint64_t dk = smem_desc(smem_u32(sK + k_slot * C::K_BYTES), 16, 1024, SWZ_128B);
+      const uint64_t dq0 = smem_desc(smem_u32(sQ), 16, 1024, SWZ_128B), dk0 = smem_desc(smem_u32(sK), 16, 1024, SWZ_128B);
+      const uint64_t dv0 = smem_desc(smem_u32(sV), kChunk, 1024, SWZ_128B);
+      // A commit costs the issuing thread several hundred cycles, so K and V slots are released by the
+      // softmax warps: S of block j follows PV of the block before on its stream in issue order. (With one V
+      // slot the last block would wait for a release that follows it: that ring is released by commits.)
+      auto issue_s = [&](int i, int q_tile) {
+        const uint64_t dq = desc_add(dq0, q_tile * C::Q_BYTES), dk = desc_add(dk0, rk.slot * C::K_BYTES);
+        if (lane == 0) {
 #pragma unroll
-        for (int kk = 0; kk < DQK / 16; ++kk) {
-          const uint32_t off = (kk / 4) * kChunk + (kk % 4) * 32;
-          mma_ss(tbase + tS(i), desc_add(dq, off), desc_add(dk, off), idS, kk > 0 ? 1u : 0u);
+          for (int kk = 0; kk < DQK / 16; ++kk) {
+            const uint32_t off = (kk / 4) * kChunk + (kk % 4) * 32;
+            mma_ss(tbase + tS(i), desc_add(dq, off), desc_add(dk, off), idS, kk > 0 ? 1u : 0u);
+          }
+          mma_commit(&bar->s_full[i]);
         }
-        mma_commit(&bar->s_full[i]);
       };
-      auto issue_pv = [&](int i, uint32_t v_slot, bool first) {
-        const uint64_t dv = smem_desc(smem_u32(sV + v_slot * C::V_BYTES), kChunk, 1024, SWZ_128B);
+      auto issue_pv = [&](int i, bool first) {
+        const uint64_t dv = desc_add(dv0, rv.slot * C::V_BYTES);
+        if (lane == 0) {
 #pragma unroll
-        for (int kk = 0; kk < BN / 16; ++kk)
-          mma_ts(tbase + tO(i), tbase + tS(i) + kk * 8, desc_add(dv, kk * 2048), idO, (kk > 0 || !first) ? 1u : 0u);
+          for (int kk = 0; kk < BN / 16; ++kk)
+            mma_ts(tbase + tO(i), tbase + tS(i) + kk * 8, desc_add(dv, kk * 2048), idO, (kk > 0 || !first) ? 1u : 0u);
+        }
+      };
+      auto v_done = [&]() {
+        if (C::NV == 1 && lane == 0) mma_commit(&bar->v_empty[rv.slot]);
+        rv.next();
       };
       for (;;) {
         const int slot = static_cast<int>(seg_i % kSegs);
-        ok = mbar_wait(&bar->seg_full[slot], (seg_i / kSegs) & 1u, a.status, 0x3200);
+        ok = mbar_wait_warp(&bar->seg_full[slot], (seg_i / kSegs) & 1u, a.status, 0x3200);
         if (!ok) break;
         const Seg* w = sSeg + slot;
-        const int more = w->more, n0 = w->n0, n1 = w->n1;
-        const bool dual = EVEN || w->dual != 0;
-        mbar_arrive(&bar->seg_empty[slot]);
+        const int more = warp_uniform(w->more), n0 = warp_uniform(w->n0), n1 = warp_uniform(w->n1);
+        const bool dual = EVEN || warp_uniform(w->dual) != 0;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bar->seg_empty[slot]);
         if (!more) break;
         const int n = max(n0, n1);
         // the previous segment's O has been read: before the first PV overwrites it
-        auto wait_o = [&]() { return seg_i == 0 || mbar_wait(&bar->o_free, (seg_i - 1) & 1u, a.status, 0x3210); };
-        if (n == 0) {
-          ok = wait_o();
-          if (!ok) break;
-          mbar_arrive(&bar->o_free);
-          ++seg_i;
-          continue;
-        }
-        for (int j = 0; j <= n && ok; ++j) {
+        auto wait_o = [&]() { return seg_i == 0 || mbar_wait_warp(&bar->o_free, (seg_i - 1) & 1u, a.status, 0x3210); };
+        if (n == 0) ok = wait_o();
+        for (int j = 0; j <= n && n > 0 && ok; ++j) {
           if (j < n) {
-            ok = mbar_wait(&bar->k_full[ck % C::NK], (ck / C::NK) & 1u, a.status, 0x3220);
-            if (ok && j == 0) ok = mbar_wait(&bar->q_full, cq & 1u, a.status, 0x3230);
+            ok = mbar_wait_warp(&bar->k_full[rk.slot], rk.phase, a.status, 0x3220);
+            if (ok && j == 0) ok = mbar_wait_warp(&bar->q_full, cq & 1u, a.status, 0x3230);
             if (!ok) break;
             tc_fence_after();
           }
           if (dual) {
             if (j < n) {
-              issue_s(j & 1, 0, ck % C::NK);
-              mma_commit(&bar->k_empty[ck % C::NK]);
-              ++ck;
-              if (j == n - 1) mma_commit(&bar->q_free);
+              issue_s(j & 1, 0);
+              rk.next();
+              if (j == n - 1 && lane == 0) mma_commit(&bar->q_free);
             }
             if (j > 0) {
               const int i = (j - 1) & 1;
               if (j == 1) ok = wait_o();
-              ok = ok && mbar_wait(&bar->v_full[cv % C::NV], (cv / C::NV) & 1u, a.status, 0x3240) &&
-                   mbar_wait(&bar->p_full[i], cp[i] & 1u, a.status, 0x3250);
+              ok = ok && mbar_wait_warp(&bar->v_full[rv.slot], rv.phase, a.status, 0x3240) &&
+                   mbar_wait_warp(&bar->p_full[i], (pp >> i) & 1u, a.status, 0x3250);
               if (!ok) break;
               tc_fence_after();
-              ++cp[i];
-              issue_pv(i, cv % C::NV, j <= 2);
-              mma_commit(&bar->v_empty[cv % C::NV]);
-              ++cv;
-              if (j - 1 >= n - 2) mma_commit(&bar->o_full[i]);
+              pp ^= 1u << i;
+              issue_pv(i, j <= 2);
+              v_done();
+              if (j - 1 >= n - 2 && lane == 0) mma_commit(&bar->o_full[i]);
             }
           } else {
             if (j > 0) {
               if (j == 1) ok = wait_o();
-              ok = ok && mbar_wait(&bar->v_full[cv % C::NV], (cv / C::NV) & 1u, a.status, 0x3240);
+              ok = ok && mbar_wait_warp(&bar->v_full[rv.slot], rv.phase, a.status, 0x3240);
               if (!ok) break;
             }
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
               const int ni = i == 0 ? n0 : n1;
               if (j > 0 && j - 1 < ni) {
-                ok = mbar_wait(&bar->p_full[i], cp[i] & 1u, a.status, 0x3250);
+                ok = mbar_wait_warp(&bar->p_full[i], (pp >> i) & 1u, a.status, 0x3250);
                 if (!ok) break;
                 tc_fence_after();
-                ++cp[i];
-                issue_pv(i, cv % C::NV, j == 1);
-                if (j == ni) mma_commit(&bar->o_full[i]);
+                pp ^= 1u << i;
+                issue_pv(i, j == 1);
+                if (j == ni && lane == 0) mma_commit(&bar->o_full[i]);
               }
-              if (j < ni) issue_s(i, i, ck % C::NK);
+              if (j < ni) issue_s(i, i);
             }
             if (!ok) break;
-            if (j > 0) {
-              mma_commit(&bar->v_empty[cv % C::NV]);
-              ++cv;
-            }
+            if (j > 0) v_done();
             if (j < n) {
-              mma_commit(&bar->k_empty[ck % C::NK]);
-              ++ck;
-              if (j == n - 1) mma_commit(&bar->q_free);
+              rk.next();
+              if (j == n - 1 && lane == 0) mma_commit(&bar->q_free);
             }
           }
         }
         if (!ok) break;
-        mbar_arrive(&bar->o_free);
-        ++cq;
+        if (lane == 0) mbar_arrive(&bar->o_free);
+        if (n > 0) ++cq;
         ++seg_i;
       }
-      mma_commit(&bar->mma_done);
-      mbar_wait(&bar->mma_done, 0, a.status, 0x32ff);
+      if (lane == 0) {
+        mma_commit(&bar->mma_done);
+        mbar_wait(&bar->mma_done, 0, a.status, 0x32ff);
+      }
     }
   } else {
     regs_inc<C::REG_HI>();
@@ -413,6 +349,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (kt + step < kt_end) pg_ok = page_ok(kt + step);  // fetched one block ahead
           ok = mbar_wait_warp(&bar->s_full[i], s_phase & 1u, a.status, 0x3310 + i);
           if (!ok) break;
+          // K of this block has been read, and V of the stream's block before (not dual: by tile 1's S, which is
+          // the last of the block's and tile 1 has every block that tile 0 has)
+          if (quarter == 0 && lane == 0 && (EVEN || w.dual || i == 1)) {
+            const uint32_t u = w.v0 + static_cast<uint32_t>(kt - w.kt0);
+            mbar_arrive(&bar->k_empty[u % C::NK]);
+            if (C::NV > 1 && !first) mbar_arrive(&bar->v_empty[(u - step) % C::NV]);
+          }
           tc_fence_after();
           if (work) {
             uint32_t s[BN];
@@ -546,6 +489,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (has0) ok = mbar_wait_warp(&bar->o_full[i], (w.phase >> i) & 1u, a.status, 0x3340 + i);
       }
       if (!ok) break;
+      if (C::NV > 1 && quarter == 0 && lane == 0 && i == (dual ? 0 : 1)) {  // the last V blocks
+        const uint32_t end = w.v0 + static_cast<uint32_t>(dual ? w.n0 : w.n1);
+        if (has1) mbar_arrive(&bar->v_empty[(end - 2) % C::NV]);
+        if (has0) mbar_arrive(&bar->v_empty[(end - 1) % C::NV]);
+      }
       tc_fence_after();
       const int tok = row_tok(dual), head = w.hk * a.kv_group + r % a.kv_group, part = w.part;
       const bool valid = row_valid(w);
@@ -682,58 +630,55 @@ __global__ void __launch_bounds__(256) merge_kernel(const PagedArgs a) {
   if (lane == 0) a.lse[head * a.total_q + m.q_row + tok] = sum > 0.f ? (mx + log2f(sum)) * 0.69314718055994531f : -INFINITY;
 }
 
-// The list of paged_kernel<EVEN = false>: per unit (request, 2 * tile_tokens
-// tokens, K/V head) one item, or several where its cost (key blocks, doubled
-// for two tiles of rows) exceeds an equal share of the whole, cut evenly.
-// Requests with the most keys come first (a counting sort by key blocks), a
-// request's last tokens, which see the most keys, before its first, the K/V
-// heads of the same tokens side by side. One block; the order affects only
-// scheduling.
+// The list of paged_kernel<EVEN = false>: first the parts of the units (request, 2 *
+// tile_tokens tokens, K/V head) that cost more than an equal share of the whole (cost:
+// key blocks, doubled for two tiles of rows), cut evenly; then one entry per unit (that
+// of a cut unit is empty), requests with the most keys first (a counting sort by key
+// blocks), a request's last tokens, which see the most keys, before its first, the K/V
+// heads of the same tokens side by side. One block; the order affects only scheduling.
+// Bound by latency: requests with few units are written by one thread each, the others
+// by a warp.
 constexpr int kListThreads = 1024, kBins = 2048;
 
 __global__ void __launch_bounds__(kListThreads, 1) chunk_list_kernel(const PagedArgs a, int ctas) {
   __shared__ int bins[kBins];
   __shared__ long long sums[kListThreads / 32];
   __shared__ int warp_items[kListThreads / 32];
-  __shared__ int n_slots, n_merge;
+  __shared__ int large[kListThreads];  // requests for the warps: (request, first entry)
+  __shared__ int large_at[kListThreads];
+  __shared__ int n_slots, n_merge, n_parts, n_large;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // paged_kernel sets itself up meanwhile
   const int tid = static_cast<int>(threadIdx.x), lane = tid & 31, warp = tid >> 5;
   const int unit_tokens = 2 * a.tile_tokens;
   for (int x = tid; x < kBins; x += kListThreads) bins[x] = 0;
-  if (tid == 0) n_slots = n_merge = 0;
-  // cost and blocks of the unit that ends before token `end` of a request
-  auto blocks = [&](const Bounds& b, int tok0) { return unit_blocks(a, b, min(tok0 + unit_tokens, b.nq) - 1); };
-  auto weight = [&](const Bounds& b, int tok0) { return b.nq - tok0 > a.tile_tokens ? 2 : 1; };
+  if (tid == 0) n_slots = n_merge = n_parts = n_large = 0;
+  __syncthreads();
+  auto bin_of = [&](const Bounds& b) { return kBins - 1 - min(kBins - 1, ceil_div(b.nk, BN)); };  // most keys first
+  // The whole's cost, bounded from above in closed form: over a request's u units the keys seen by
+  // a unit's last token sum to at most u nk, and causally, where unit u - 1 - m ends more than
+  // (m - 1) unit_tokens before the request does, to at most u nk - unit_tokens (u - 1) (u - 2) / 2.
   long long w = 0;
   for (int s = tid; s < a.num_seqs; s += kListThreads) {
     const Bounds b = bounds(a, s);
-    for (int t = 0; t < b.nq; t += unit_tokens) w += static_cast<long long>(blocks(b, t)) * weight(b, t);
+    if (b.nq == 0) continue;
+    const long long u = (b.nq + unit_tokens - 1) / unit_tokens;
+    long long keys = u * b.nk;
+    if (a.causal && b.nk >= b.nq) keys -= unit_tokens * ((u - 1) * (u - 2) / 2);
+    w += 2 * ((keys >> 7) + u + 1);
+    atomicAdd(&bins[bin_of(b)], static_cast<int>(u) * a.heads_kv);
   }
 #pragma unroll
   for (int d = 16; d > 0; d >>= 1) w += __shfl_xor_sync(0xffffffffu, w, d);
   if (lane == 0) sums[warp] = w;
   __syncthreads();
   w = 0;
+#pragma unroll
   for (int x = 0; x < kListThreads / 32; ++x) w += sums[x];
   w *= a.heads_kv;
   // an equal share of the work (a unit costs less than 2^26)
   const uint32_t cap = static_cast<uint32_t>(
       min(max(static_cast<long long>(kPagedMinItem), (w + ctas - 1) / ctas), static_cast<long long>(1) << 30));
-  auto cuts = [&](const Bounds& b, int tok0) -> int {
-    const uint32_t c = static_cast<uint32_t>(blocks(b, tok0) * weight(b, tok0));
-    return c <= cap ? 1 : static_cast<int>((c + cap - 1) / cap);
-  };
-  auto bin_of = [&](const Bounds& b) { return kBins - 1 - min(kBins - 1, ceil_div(b.nk, BN)); };  // most keys first
-  for (int s = tid; s < a.num_seqs; s += kListThreads) {
-    const Bounds b = bounds(a, s);
-    int n = 0;
-    for (int t = 0; t < b.nq; t += unit_tokens) n += cuts(b, t);
-    n *= a.heads_kv;
-    a.list_scratch[s] = n;
-    if (n > 0) atomicAdd(&bins[bin_of(b)], n);
-  }
-  __syncthreads();
-  // bins -> first item of each bin: two bins per thread, a scan per warp and over the warps' sums
+  // bins -> first entry of each bin: two bins per thread, a scan per warp and over the warps' sums
   const int b0 = bins[2 * tid], b1 = bins[2 * tid + 1];
   int inc = b0 + b1;
 #pragma unroll
@@ -753,53 +698,56 @@ __global__ void __launch_bounds__(kListThreads, 1) chunk_list_kernel(const Paged
   bins[2 * tid] = before;
   bins[2 * tid + 1] = before + b0;
   __syncthreads();
+  const int first_unit = 2 * ctas;  // the cut units' parts come before
+  // entry x (of units * heads_kv) of request s, whose entries begin at `at`
+  auto write = [&](int s, const Bounds& b, int units, int at, int x) {
+    const int u = units - 1 - x / a.heads_kv, hk = x % a.heads_kv;  // the last tokens first
+    const int tok0 = u * unit_tokens, ntok = min(unit_tokens, b.nq - tok0);
+    const int nb = unit_blocks(a, b, tok0 + ntok - 1);
+    const uint32_t cost = static_cast<uint32_t>(nb) * (ntok > a.tile_tokens ? 2u : 1u);
+    ChunkItem it{s, hk, tok0, 0, nb, -1};
+    if (cost > cap) {
+      // fewer than `ctas` units cost more than a share (the costs sum to at most ctas shares), and
+      // their cuts number at most cost / share + 1 each: below 2 * ctas in all
+      const int k = static_cast<int>((cost + cap - 1) / cap);
+      const int slot = atomicAdd(&n_slots, k), at_part = atomicAdd(&n_parts, k);
+      a.merge[atomicAdd(&n_merge, 1)] = MergeUnit{b.q0 + tok0, ntok, hk, slot, slot + 1, k};
+      for (int y = 0; y < k; ++y)
+        a.items[at_part + y] = ChunkItem{s, hk, tok0, static_cast<int>(static_cast<long long>(nb) * y / k),
+                                         static_cast<int>(static_cast<long long>(nb) * (y + 1) / k), slot + y};
+      it.seq = -1;
+    }
+    const int i = first_unit + at + x;
+    if (i < a.items_bound) a.items[i] = it;
+  };
   for (int s = tid; s < a.num_seqs; s += kListThreads) {
-    const int n = a.list_scratch[s];
-    if (n > 0) a.list_scratch[s] = atomicAdd(&bins[bin_of(bounds(a, s))], n);
-  }
-  __syncthreads();
-  for (int s = warp; s < a.num_seqs; s += kListThreads / 32) {
     const Bounds b = bounds(a, s);
-    const int units = ceil_div(b.nq, unit_tokens);
-    int at = a.list_scratch[s];
-    for (int u0 = 0; u0 < units; u0 += 32) {
-      const int u = units - 1 - u0 - lane;  // the last tokens first
-      const int tok0 = u * unit_tokens;
-      const int k = u >= 0 ? cuts(b, tok0) : 0;
-      int inc = k;
-#pragma unroll
-      for (int d = 1; d < 32; d <<= 1) {
-        const int x = __shfl_up_sync(0xffffffffu, inc, d);
-        if (lane >= d) inc += x;
-      }
-      const int mine = at + (inc - k) * a.heads_kv;
-      at += __shfl_sync(0xffffffffu, inc, 31) * a.heads_kv;
-      if (k == 0) continue;
-      const int nb = blocks(b, tok0), ntok = min(unit_tokens, b.nq - tok0);
-      for (int hk = 0; hk < a.heads_kv; ++hk) {
-        int slot = -1;
-        if (k > 1) {
-          // fewer than `ctas` units cost more than a share (their costs sum to at most ctas shares), and
-          // their cuts number at most cost / share + 1 each: below 2 * ctas in all
-          slot = atomicAdd(&n_slots, k);
-          const int x = atomicAdd(&n_merge, 1);
-          a.merge[x] = MergeUnit{b.q0 + tok0, ntok, hk, slot, slot + 1, k};
-        }
-        for (int x = 0; x < k; ++x) {
-          const int i = mine + hk * k + x;
-          if (i >= a.items_bound) break;
-          a.items[i] = ChunkItem{s, hk, tok0, static_cast<int>(static_cast<long long>(nb) * x / k),
-                                 static_cast<int>(static_cast<long long>(nb) * (x + 1) / k), slot < 0 ? -1 : slot + x};
-        }
+    if (b.nq == 0) continue;
+    const int units = ceil_div(b.nq, unit_tokens), n = units * a.heads_kv;
+    const int at = atomicAdd(&bins[bin_of(b)], n);
+    if (n > 16) {
+      const int x = atomicAdd(&n_large, 1);
+      if (x < kListThreads) {
+        large[x] = s;
+        large_at[x] = at;
+        continue;
       }
     }
+    for (int x = 0; x < n; ++x) write(s, b, units, at, x);
+  }
+  __syncthreads();
+  for (int y = warp; y < min(n_large, kListThreads); y += kListThreads / 32) {
+    const Bounds b = bounds(a, large[y]);
+    const int units = ceil_div(b.nq, unit_tokens);
+    for (int x = lane; x < units * a.heads_kv; x += 32) write(large[y], b, units, large_at[y], x);
   }
   __syncthreads();
   for (int x = tid; x < ctas; x += kListThreads)
     if (x >= n_merge) a.merge[x].n = 0;
   if (tid == 0) {
-    *a.n_items = min(total, a.items_bound);
-    *a.next_item = ctas;
+    a.list->n_parts = n_parts;
+    a.list->n_items = n_parts + min(total, a.items_bound - first_unit);
+    a.list->next = ctas;
   }
 }
 

@@ -18,6 +18,8 @@
 // the odd key blocks hide the chain S^T -> softmax -> O^T, as there.
 //
 // Warps: 0 work and TMA copies, 1 MMA issue, 4..7 and 8..11 softmax of stream 0 and 1.
+#include <cstddef>
+
 #include "kernels.h"
 #include "paged_common.cuh"
 #include "ptx_sm100.cuh"
@@ -53,13 +55,18 @@ struct Cfg {
 };
 
 struct Bars {
+  // one arrival
   uint64_t q_full[2], q_free[2];
   uint64_t k_full[6], k_empty[6], v_full[6], v_empty[6];
-  uint64_t s_full[2], p_full[2], o_full[2];
-  uint64_t o_free;    // a segment is over: its O has been read, its MMAs issued
-  uint64_t x_full[2];  // a stream's maxima and sums are in shared memory
-  uint64_t seg_full[kSegs], seg_empty[kSegs];
+  uint64_t s_full[2], o_full[2];
+  uint64_t seg_full[kSegs];
   uint64_t mma_done;
+  // four: a warpgroup's warps
+  uint64_t p_full[2];
+  uint64_t x_full[2];  // a stream's maxima and sums are in shared memory
+  // nine: eight softmax warps and the MMA thread
+  uint64_t seg_empty[kSegs];
+  uint64_t o_free;     // a segment is over: its O has been read, its MMAs issued (so neither side gets two ahead)
   uint32_t tmem_base;
   EvenStart even;
 };
@@ -154,28 +161,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   Bars* bar = reinterpret_cast<Bars*>(smem + C::OFF_BAR);
   const uint32_t warp = warp_id(), lane = lane_id();
 
-  if (threadIdx.x == 0) {
-    for (int s = 0; s < 2; ++s) {
-      mbar_init(&bar->q_full[s], 1);
-      mbar_init(&bar->q_free[s], 1);
-      mbar_init(&bar->s_full[s], 1);
-      mbar_init(&bar->p_full[s], 4);
-      mbar_init(&bar->o_full[s], 1);
-      mbar_init(&bar->x_full[s], 4);
-    }
-    for (int s = 0; s < 6; ++s) {
-      mbar_init(&bar->k_full[s], 1);
-      mbar_init(&bar->k_empty[s], 1);
-      mbar_init(&bar->v_full[s], 1);
-      mbar_init(&bar->v_empty[s], 1);
-    }
-    mbar_init(&bar->o_free, 9);  // eight softmax warps and the MMA thread, so that neither side gets two segments ahead
-    for (int s = 0; s < kSegs; ++s) {
-      mbar_init(&bar->seg_full[s], 1);
-      mbar_init(&bar->seg_empty[s], 9);  // the MMA thread and eight softmax warps
-    }
-    mbar_init(&bar->mma_done, 1);
+  constexpr int kOnes = offsetof(Bars, p_full) / 8, kFours = offsetof(Bars, seg_empty) / 8,
+                kAll = offsetof(Bars, tmem_base) / 8;
+  if (threadIdx.x >= 64 && threadIdx.x < 64 + kAll) {  // one thread per barrier
+    const int x = static_cast<int>(threadIdx.x) - 64;
+    mbar_init(reinterpret_cast<uint64_t*>(bar) + x, x < kOnes ? 1 : x < kFours ? 4 : 9);
     fence_barrier_init();
+  }
+  if (threadIdx.x == 0) {
     tma_prefetch_desc(&tmq);
     tma_prefetch_desc(&tmk);
     tma_prefetch_desc(&tmv);
@@ -197,98 +190,41 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (warp == 0) {
     // ===================== work and copies ==================================
-    const int np = a.page_size < BN ? BN >> a.page_shift : 1;  // pages (boxes along the keys) of a key block
-    const int box_rows = a.page_size < BN ? a.page_size : BN;
-    const int my_page = static_cast<int>(lane) % np, my_chunk = static_cast<int>(lane) / np;
     const uint32_t q_bytes = static_cast<uint32_t>(a.kv_group * a.q_box_tokens) * 128u * C::QCH;
-    uint32_t ck = 0, cv = 0, cq = 0, seg_i = 0;  // copies and segments so far
-    uint32_t cs0 = 0, cs1 = 0, phase = 0;
-    bool ok = true;
+    Ring<C::NQ> rq;
+    uint32_t cq = 0;
     EvenWalk walk;
     walk.begin(a, &bar->even);
-    Seg w = walk.next(a, &bar->even);
-    int page = w.more ? page_of(a, w, w.kt0, my_page) : 0;
-    for (;;) {
-      const int slot = static_cast<int>(seg_i % kSegs);
-      ok = mbar_wait_warp(&bar->seg_empty[slot], ((seg_i / kSegs) & 1u) ^ 1u, a.status, 0x4100);
-      if (!ok) break;
-      const int n = w.n0;
-      if (lane == 0) {
-        w.v0 = cv, w.s0 = cs0, w.s1 = cs1, w.phase = phase;
-        sSeg[slot] = w;
-        mbar_arrive(&bar->seg_full[slot]);
-      }
-      ++seg_i;
-      if (!w.more) break;
-      cs0 += (n + 1) / 2;
-      cs1 += n / 2;
-      phase ^= (n > 0 ? 1u : 0u) | (n > 1 ? 2u : 0u) | 4u;
-      // ---- its copies; the next segment and its first page are looked up behind the first few
-      Seg nw;
-      nw.more = 0;
-      int npage = 0;
-      if (n == 0) {
-        nw = walk.next(a, &bar->even);
-        npage = nw.more ? page_of(a, nw, nw.kt0, my_page) : 0;
-      }
-      for (int j = 0; j < n; ++j) {
-        const int next = j + 1 < n ? page_of(a, w, w.kt0 + j + 1, my_page) : 0;  // fetched ahead of the waits
-        const int row = a.page_size > BN ? ((w.kt0 + j) << 7) & (a.page_size - 1) : 0;
-        const uint32_t ks = ck % C::NK;
-        ok = mbar_wait_warp(&bar->k_empty[ks], ((ck / C::NK) & 1u) ^ 1u, a.status, 0x4110);
-        if (!ok) break;
-        if (lane == 0) mbar_arrive_expect_tx(&bar->k_full[ks], C::K_BYTES);
-        __syncwarp();
-        if (my_chunk < C::QCH)
-          tma_load_4d(sK + ks * C::K_BYTES + my_chunk * kChunk + my_page * box_rows * 128, &tmk, &bar->k_full[ks],
-                      my_chunk * 64, w.hk, row, page);
-        ++ck;
-        if (j == 0) {
-          const uint32_t qs = cq % C::NQ;
-          ok = mbar_wait_warp(&bar->q_free[qs], ((cq / C::NQ) & 1u) ^ 1u, a.status, 0x4120);
-          if (!ok) break;
-          if (lane == 0) mbar_arrive_expect_tx(&bar->q_full[qs], q_bytes);
+    const bool ok = copy_loop<C>(
+        a, bar, sSeg, sK, sV, &tmk, &tmv, 0x4100, [&] { return walk.next(a, &bar->even); },
+        [&](const Seg& w) {
+          if (!mbar_wait_warp(&bar->q_free[rq.slot], rq.phase ^ 1u, a.status, 0x4120)) return false;
+          if (lane == 0) mbar_arrive_expect_tx(&bar->q_full[rq.slot], q_bytes);
           __syncwarp();
           if (static_cast<int>(lane) < C::QCH)
-            tma_load_4d(sQ + qs * C::Q_BYTES + lane * C::Q_CHUNK, &tmq, &bar->q_full[qs], static_cast<int>(lane) * 64,
-                        w.hk * a.kv_group, w.q_row, 0);
+            tma_load_4d(sQ + rq.slot * C::Q_BYTES + lane * C::Q_CHUNK, &tmq, &bar->q_full[rq.slot],
+                        static_cast<int>(lane) * 64, w.hk * a.kv_group, w.q_row, 0);
+          rq.next();
           ++cq;
-        }
-        const uint32_t vs = cv % C::NV;
-        ok = mbar_wait_warp(&bar->v_empty[vs], ((cv / C::NV) & 1u) ^ 1u, a.status, 0x4130);
-        if (!ok) break;
-        if (lane == 0) mbar_arrive_expect_tx(&bar->v_full[vs], C::V_BYTES);
-        __syncwarp();
-        if (my_chunk < C::VCH)
-          tma_load_4d(sV + vs * C::V_BYTES + my_chunk * kChunk + my_page * box_rows * 128, &tmv, &bar->v_full[vs],
-                      my_chunk * 64, w.hk, row, page);
-        ++cv;
-        page = next;
-        if (j == min(n - 1, C::NK - 1)) {
-          nw = walk.next(a, &bar->even);
-          npage = nw.more ? page_of(a, nw, nw.kt0, my_page) : 0;
-        }
-      }
-      if (!ok) break;
-      w = nw;
-      page = npage;
-    }
+          return true;
+        });
     walk.finish(a);
-    if (!ok) {  // let the copies in flight land before the CTA exits
-      for (uint32_t u = 0; u < C::NK && u < ck; ++u)
-        mbar_wait(&bar->k_full[(ck - 1 - u) % C::NK], ((ck - 1 - u) / C::NK) & 1u, nullptr, 0);
-      for (uint32_t u = 0; u < C::NV && u < cv; ++u)
-        mbar_wait(&bar->v_full[(cv - 1 - u) % C::NV], ((cv - 1 - u) / C::NV) & 1u, nullptr, 0);
+    if (!ok)
       for (uint32_t u = 0; u < C::NQ && u < cq; ++u)
         mbar_wait(&bar->q_full[(cq - 1 - u) % C::NQ], ((cq - 1 - u) / C::NQ) & 1u, nullptr, 0);
-    }
   } else if (warp == 1) {
     if (lane == 0) {
       // ===================== MMA issue ======================================
       constexpr uint32_t idS = idesc_bf16_f32(BN, N, false, false);
       constexpr uint32_t idO = idesc_bf16_f32(C::M_O, N, true, false);
-      uint32_t ck = 0, cv = 0, cq = 0, seg_i = 0, cp[2] = {0, 0};
+      Ring<C::NK> rk;
+      Ring<C::NV> rv;
+      Ring<C::NQ> rq;
+      uint32_t seg_i = 0, pp = 0;  // pp: a bit per stream
       bool ok = true;
+      const uint64_t dk0 = smem_desc(smem_u32(sK), 16, 1024, SWZ_128B), dq0 = smem_desc(smem_u32(sQ), 16, 1024, SWZ_128B);
+      const uint64_t dv0 = smem_desc(smem_u32(sV), kChunk, 1024, SWZ_128B);
+      const uint64_t dp0 = smem_desc(smem_u32(smem + C::OFF_P), 16, 1024, SWZ_128B);
       for (;;) {
         const int slot = static_cast<int>(seg_i % kSegs);
         ok = mbar_wait(&bar->seg_full[slot], (seg_i / kSegs) & 1u, a.status, 0x4200);
@@ -299,46 +235,42 @@ __global__ void __launch_bounds__(kThreads, 1)
         // the previous segment's O has been read: before the first PV overwrites it
         auto wait_o = [&]() { return seg_i == 0 || mbar_wait(&bar->o_free, (seg_i - 1) & 1u, a.status, 0x4210); };
         if (n == 0) ok = wait_o();
-        const uint32_t qs = cq % C::NQ;
+        const uint64_t dq = desc_add(dq0, rq.slot * C::Q_BYTES);
         for (int j = 0; j <= n && n > 0 && ok; ++j) {
           if (j < n) {
-            ok = mbar_wait(&bar->k_full[ck % C::NK], (ck / C::NK) & 1u, a.status, 0x4220);
-            if (ok && j == 0) ok = mbar_wait(&bar->q_full[qs], (cq / C::NQ) & 1u, a.status, 0x4230);
+            ok = mbar_wait(&bar->k_full[rk.slot], rk.phase, a.status, 0x4220);
+            if (ok && j == 0) ok = mbar_wait(&bar->q_full[rq.slot], rq.phase, a.status, 0x4230);
             if (!ok) break;
             tc_fence_after();
-            const uint64_t dk = smem_desc(smem_u32(sK + (ck % C::NK) * C::K_BYTES), 16, 1024, SWZ_128B);
-            const uint64_t dq = smem_desc(smem_u32(sQ + qs * C::Q_BYTES), 16, 1024, SWZ_128B);
+            const uint64_t dk = desc_add(dk0, rk.slot * C::K_BYTES);
 #pragma unroll
             for (int kk = 0; kk < DQK / 16; ++kk)
               mma_ss(tbase + C::tS(j & 1), desc_add(dk, (kk / 4) * kChunk + (kk % 4) * 32),
                      desc_add(dq, (kk / 4) * C::Q_CHUNK + (kk % 4) * 32), idS, kk > 0 ? 1u : 0u);
-            mma_commit(&bar->s_full[j & 1]);
-            mma_commit(&bar->k_empty[ck % C::NK]);
-            ++ck;
-            if (j == n - 1) mma_commit(&bar->q_free[qs]);
+            mma_commit(&bar->s_full[j & 1]);  // (also says that K(j) and V(j - 2) have been read)
+            if (j == n - 1) mma_commit(&bar->q_free[rq.slot]);
+            rk.next();
           }
           if (j > 0) {
             const int i = (j - 1) & 1;
             if (j == 1) ok = wait_o();
-            ok = ok && mbar_wait(&bar->v_full[cv % C::NV], (cv / C::NV) & 1u, a.status, 0x4240) &&
-                 mbar_wait(&bar->p_full[i], cp[i] & 1u, a.status, 0x4250);
+            ok = ok && mbar_wait(&bar->v_full[rv.slot], rv.phase, a.status, 0x4240) &&
+                 mbar_wait(&bar->p_full[i], (pp >> i) & 1u, a.status, 0x4250);
             if (!ok) break;
             tc_fence_after();
-            ++cp[i];
-            const uint64_t dv = smem_desc(smem_u32(sV + (cv % C::NV) * C::V_BYTES), kChunk, 1024, SWZ_128B);
-            const uint64_t dp = smem_desc(smem_u32(smem + C::OFF_P + i * C::P_BYTES), 16, 1024, SWZ_128B);
+            pp ^= 1u << i;
+            const uint64_t dv = desc_add(dv0, rv.slot * C::V_BYTES), dp = desc_add(dp0, i * C::P_BYTES);
 #pragma unroll
             for (int kk = 0; kk < BN / 16; ++kk)  // 16 keys: 16 rows of V, 32 bytes of P's rows
               mma_ss(tbase + C::tO(i), desc_add(dv, kk * 2048),
                      desc_add(dp, (kk / 4) * C::P_CHUNK + (kk % 4) * 32), idO, (kk > 0 || j > 2) ? 1u : 0u);
-            mma_commit(&bar->v_empty[cv % C::NV]);
-            ++cv;
             if (j - 1 >= n - 2) mma_commit(&bar->o_full[i]);
+            rv.next();
           }
         }
         if (!ok) break;
         mbar_arrive(&bar->o_free);
-        if (n > 0) ++cq;
+        if (n > 0) rq.next();
         ++seg_i;
       }
       mma_commit(&bar->mma_done);
@@ -382,6 +314,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool here = pg_ok;
         if (j + 2 < n) pg_ok = page_ok(key + 2 * BN);  // fetched one block ahead
         ok = ok && mbar_wait_warp(&bar->s_full[i], s_phase & 1u, a.status, 0x4310 + i);
+        // a commit costs the MMA thread several hundred cycles, so the slots are released from here: S(j) of
+        // block j follows PV(j - 2) in issue order, so K(j) and V(j - 2) have been read
+        if (ok && quarter == 0 && lane == 0) {
+          mbar_arrive(&bar->k_empty[(w.v0 + j) % C::NK]);
+          if (j >= 2) mbar_arrive(&bar->v_empty[(w.v0 + j - 2) % C::NV]);
+        }
         tc_fence_after();
         uint32_t sr[N];
         tmem_ld_cols<N>(lane_base + C::tS(i), sr);
@@ -489,6 +427,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (ok && n > 1) ok = mbar_wait_warp(&bar->o_full[1], (w.phase >> 1) & 1u, a.status, 0x4341);
       if (ok) {
         tc_fence_after();
+        if (i == 0 && quarter == 0 && lane == 0) {  // the last two V blocks
+          if (n > 1) mbar_arrive(&bar->v_empty[(w.v0 + n - 2) % C::NV]);
+          if (n > 0) mbar_arrive(&bar->v_empty[(w.v0 + n - 1) % C::NV]);
+        }
         // this warpgroup writes rows [i N/2, (i + 1) N/2); lane u of each warp holds row i N/2 + u's weights
         const float* m_of = reinterpret_cast<const float*>(smem + C::OFF_M);
         const float* l_of = reinterpret_cast<const float*>(smem + C::OFF_W);

@@ -345,9 +345,13 @@ cudaError_t launch_kv_append(int d_qk, int d_v, const KvAppendArgs& a, cudaStrea
 struct MergeUnit {
   int q_row, ntok, hk, first, rest, n;
 };
-// One item of the chunks' list: 2 * tile_tokens tokens from tok0 on, key blocks [kt0, kt1).
+// One item of the chunks' list: 2 * tile_tokens tokens from tok0 on, key blocks [kt0, kt1); seq < 0: none.
 struct ChunkItem {
   int seq, hk, tok0, kt0, kt1, part;
+};
+// The list: n_parts items from items[0] on, then n_items - n_parts from items[2 * ctas] on; `next` to be taken.
+struct ChunkList {
+  int n_items, n_parts, next;
 };
 constexpr int kPagedMaxCtas = 152;    // one per SM
 constexpr int kPagedMinBlocks = 2;    // least key blocks of a CTA of the even split
@@ -376,12 +380,10 @@ struct PagedArgs {
   float* part_o;
   float* part_lse;
   MergeUnit* merge;  // [ctas]
-  // chunks only: the list, its bound and length, the next item to take, one int per request
+  // chunks only: the list, and the bound of its entries
   ChunkItem* items;
   int items_bound;
-  int* n_items;
-  int* next_item;
-  int* list_scratch;
+  ChunkList* list;
 };
 // Maps: q boxes of 64 columns x kv_group heads x q_box_tokens rows; k and v (caches as [pages, page_size, heads_kv, d])
 // of 64 columns x min(page_size, 128) rows. even: no request has more than one tile of rows; decode_rows > 0 (16, 32 or

@@ -13,6 +13,18 @@ constexpr int kChunk = BM * 128;     // bytes of one 64-column chunk of a 128-ro
 constexpr float kThreshold = 8.0f;   // log2 units
 constexpr int kSegs = 4;             // segment descriptors in flight
 
+// The same value in every lane (given that it is), known to be so by the compiler.
+__device__ __forceinline__ int warp_uniform(int x) { return __reduce_max_sync(0xffffffffu, x); }
+
+// Position in a ring of n slots: the slot and the parity of the pass over the ring.
+template <int n>
+struct Ring {
+  uint32_t slot = 0, phase = 0;
+  __device__ __forceinline__ void next() {
+    if (++slot == n) slot = 0, phase ^= 1u;
+  }
+};
+
 // One segment of work, written by warp 0 and read by every other warp. It carries
 // the pipeline's counters too (the warps' registers hold a row of S).
 struct Seg {
@@ -232,6 +244,105 @@ __device__ __forceinline__ int page_of(const PagedArgs& a, const Seg& w, int kt,
   if (key >= w.nk) return a.num_pages;
   const int pg = __ldg(a.block_table + w.seq * a.block_table_stride + (key >> a.page_shift));
   return pg < 0 || pg > a.num_pages ? a.num_pages : pg;
+}
+
+// Warp 0 of both kernels: publishes the segments that next_seg() gives and copies their K
+// and V blocks (and, by copy_q(w), Q) into the rings, one box per page and 64 columns, each
+// lane issuing one. K runs up to two blocks ahead of V, which is needed only a softmax
+// later: a K block that waited behind a V slot left the tensor cores idle for a copy's
+// latency (chunks of 24 requests: 604 us so, 4,080 cycles per pair of blocks where the
+// products take 2,048). The next segment and its first page are looked up behind the
+// first few copies. Returns false when a wait ran out; the copies in flight have landed then.
+template <typename C, typename B, typename NextSeg, typename CopyQ>
+__device__ __forceinline__ bool copy_loop(const PagedArgs& a, B* bar, Seg* sSeg, uint8_t* sK, uint8_t* sV,
+                                          const CUtensorMap* tmk, const CUtensorMap* tmv, uint32_t site,
+                                          NextSeg&& next_seg, CopyQ&& copy_q) {
+  const int lane = static_cast<int>(lane_id());
+  const int np = a.page_size < BN ? BN >> a.page_shift : 1;  // pages (boxes along the keys) of a key block
+  const int box_rows = a.page_size < BN ? a.page_size : BN;
+  const int my_page = lane % np, my_chunk = lane / np;
+  const uint32_t box_off = my_chunk * kChunk + my_page * box_rows * 128;
+  Ring<C::NK> rk;
+  Ring<C::NV> rv;
+  Ring<kSegs> rs;
+  uint32_t done = 0;  // key blocks of the segments so far
+  uint32_t cs0 = 0, cs1 = 0, phase = 0;
+  int jk = 0, jv = 0;
+  bool ok = true;
+  Seg w = next_seg();
+  int page = w.more ? page_of(a, w, w.kt0, my_page) : 0;
+  for (;;) {
+    ok = mbar_wait_warp(&bar->seg_empty[rs.slot], rs.phase ^ 1u, a.status, site);
+    if (!ok) break;
+    const int n = max(w.n0, w.n1);
+    if (lane == 0) {
+      w.v0 = done, w.s0 = cs0, w.s1 = cs1, w.phase = phase;
+      sSeg[rs.slot] = w;
+      mbar_arrive(&bar->seg_full[rs.slot]);
+    }
+    rs.next();
+    if (!w.more) break;
+    cs0 += w.dual ? (w.n0 + 1) / 2 : w.n0;
+    cs1 += w.dual ? w.n0 / 2 : w.n1;
+    phase ^= (w.n0 > 0 ? 1u : 0u) | ((w.dual ? w.n0 > 1 : w.n1 > 0) ? 2u : 0u) | (w.dual ? 4u : 0u);
+    Seg nw;
+    nw.more = 0;
+    int npage = 0;
+    if (n == 0) {
+      nw = next_seg();
+      npage = nw.more ? page_of(a, nw, nw.kt0, my_page) : 0;
+    }
+    auto row_of = [&](int j) { return a.page_size > BN ? ((w.kt0 + j) << 7) & (a.page_size - 1) : 0; };
+    int kp = page, vp = page;
+    for (jk = jv = 0; jv < n;) {
+      if (jk < n && jk - jv < 2) {
+        const int next = jk + 1 < n ? page_of(a, w, w.kt0 + jk + 1, my_page) : 0;  // fetched ahead of the wait
+        ok = mbar_wait_warp(&bar->k_empty[rk.slot], rk.phase ^ 1u, a.status, site + 1);
+        if (!ok) break;
+        if (lane == 0) mbar_arrive_expect_tx(&bar->k_full[rk.slot], C::K_BYTES);
+        __syncwarp();
+        if (my_chunk < C::QCH)
+          tma_load_4d(sK + rk.slot * C::K_BYTES + box_off, tmk, &bar->k_full[rk.slot], my_chunk * 64, w.hk, row_of(jk), kp);
+        rk.next();
+        if (jk == 0) {  // Q behind the first K: that slot may be free long before the previous Q is
+          ok = copy_q(w);
+          if (!ok) {
+            ++jk;
+            break;
+          }
+        }
+        kp = next;
+        ++jk;
+        if (jk == min(n, static_cast<int>(C::NK))) {
+          nw = next_seg();
+          npage = nw.more ? page_of(a, nw, nw.kt0, my_page) : 0;
+        }
+      } else {
+        const int next = jv + 1 < n ? page_of(a, w, w.kt0 + jv + 1, my_page) : 0;
+        ok = mbar_wait_warp(&bar->v_empty[rv.slot], rv.phase ^ 1u, a.status, site + 2);
+        if (!ok) break;
+        if (lane == 0) mbar_arrive_expect_tx(&bar->v_full[rv.slot], C::V_BYTES);
+        __syncwarp();
+        if (my_chunk < C::VCH)
+          tma_load_4d(sV + rv.slot * C::V_BYTES + box_off, tmv, &bar->v_full[rv.slot], my_chunk * 64, w.hk, row_of(jv), vp);
+        rv.next();
+        vp = next;
+        ++jv;
+      }
+    }
+    if (!ok) break;
+    done += static_cast<uint32_t>(n);
+    w = nw;
+    page = npage;
+  }
+  if (!ok) {
+    const uint32_t ck = done + static_cast<uint32_t>(jk), cv = done + static_cast<uint32_t>(jv);
+    for (uint32_t u = 0; u < C::NK && u < ck; ++u)
+      mbar_wait(&bar->k_full[(ck - 1 - u) % C::NK], ((ck - 1 - u) / C::NK) & 1u, nullptr, 0);
+    for (uint32_t u = 0; u < C::NV && u < cv; ++u)
+      mbar_wait(&bar->v_full[(cv - 1 - u) % C::NV], ((cv - 1 - u) / C::NV) & 1u, nullptr, 0);
+  }
+  return ok;
 }
 
 }  // namespace paged

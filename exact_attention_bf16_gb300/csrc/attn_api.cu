@@ -263,7 +263,7 @@ struct SparseSpec {
   int32_t lists_per_head = 0;
 };
 
-// Tile list of a packed variable-length launch (launch_tile_list): one
+// Tile list of a packed variable-length launch (launch_tile_lists): one
 // 32-byte entry per CTA of a grid bounded by heads * (total / R + sequences),
 // plus 8 bytes of scratch per sequence. Not built (the grid covers the longest
 // sequence for every sequence instead) when a sequence may exceed
@@ -457,7 +457,19 @@ attn_status_t run_fwd(const attn_fwd_params* p, bool varlen, cudaStream_t stream
   CUtensorMap tv16;
   ATTN_TRY(make_map(&tv16, v16, p->d_v, hkv, nk_rows, nb, v16_rows * hkv * p->d_v,
                     static_cast<int64_t>(hkv) * p->d_v, p->d_v, 128));
-  e = cudaMemsetAsync(flag, 0, sizeof(uint32_t), stream);
+  const ListPlan lp = fwd_list_plan(p, varlen);
+  if (lp.use) {  // longest sequences first, no CTA past a sequence's end; also zeroes the flag
+    uint8_t* lbase = static_cast<uint8_t*>(ws) + 256 + fwd_v16_bytes(p, varlen);
+    TileEntry* list = reinterpret_cast<TileEntry*>(lbase);
+    const TileListSpec spec{p->heads, 256, 0, 1, lp.max_nblk, list, lp.bound};
+    e = launch_tile_lists(p->cu_seqlens_q, p->cu_seqlens_k, p->num_seqs, &spec, 1,
+                          reinterpret_cast<int64_t*>(lbase + lp.list_bytes), flag, stream);
+    if (e != cudaSuccess) return cuda_fail(e, "fwd tile list");
+    a.tiles = list;
+    a.n_tiles = lp.bound;
+  } else {
+    e = cudaMemsetAsync(flag, 0, sizeof(uint32_t), stream);
+  }
   if (e == cudaSuccess && f8)  // exact: every E4M3 value is an fp16 value, the flag stays 0
     e = launch_v_e4m3_to_f16(p->v, varlen ? 0 : p->v_batch_stride, p->v_row_stride, p->v_head_stride, nb, nk_rows,
                              hkv, p->d_v, v16, stream);
@@ -466,17 +478,6 @@ attn_status_t run_fwd(const attn_fwd_params* p, bool varlen, cudaStream_t stream
                         hkv, p->d_v, v16, flag, stream);
   if (e != cudaSuccess) return cuda_fail(e, "fwd V conversion");
   a.v16_flag = flag;
-  const ListPlan lp = fwd_list_plan(p, varlen);
-  if (lp.use) {  // longest sequences first, no CTA past a sequence's end
-    uint8_t* lbase = static_cast<uint8_t*>(ws) + 256 + fwd_v16_bytes(p, varlen);
-    TileEntry* list = reinterpret_cast<TileEntry*>(lbase);
-    int64_t* scratch = reinterpret_cast<int64_t*>(lbase + lp.list_bytes);
-    e = launch_tile_list(p->cu_seqlens_q, p->cu_seqlens_k, p->num_seqs, p->heads, 256, false, true, lp.max_nblk, list,
-                         scratch, lp.bound, stream);
-    if (e != cudaSuccess) return cuda_fail(e, "fwd tile list");
-    a.tiles = list;
-    a.n_tiles = lp.bound;
-  }
   const SplitPlan spl = (sp.kv_count || p->cta_pair || f8) ? SplitPlan{} : fwd_split_plan(p, varlen);
   if (spl.splits > 1) {  // fp32 O and LSE of every key range, after the fp16 copy of V
     uint8_t* pbase = static_cast<uint8_t*>(ws) + 256 + fwd_v16_bytes(p, varlen);
@@ -570,7 +571,28 @@ size_t bwd_dq_split_bytes(const attn_bwd_params* p, const SplitPlan& sp) {
   const attn_fwd_params& f = p->fwd;
   return round256(static_cast<int64_t>(sp.splits) * f.batch * f.heads * f.seqlen_q * f.d_qk * 4);
 }
-// The workspace without the split-key dQ partials (the least a call accepts).
+// Split groups for the dK/dV kernel (shared K/V heads): when its grid of one CTA per key
+// block and K/V head would leave most SMs idle, a group's query heads are cut into parts,
+// one CTA each, writing fp32 partials that a merge kernel adds in order (7 packed sequences
+// of up to 500 tokens, 16 heads over 4, d = 64: 35 us in one part).
+int bwd_dkv_split(const attn_bwd_params* p, bool varlen) {
+  const attn_fwd_params& f = p->fwd;
+  if (f.heads < 1 || f.heads_kv < 0 || !shared_kv(&f) || f.heads % kv_heads(&f) != 0 || p->cta_pair || p->single_pass) return 1;
+  const int64_t units = varlen ? f.num_seqs : f.batch;
+  const int64_t max_k = varlen ? f.max_seqlen_k : f.seqlen_k;
+  if (units < 1 || max_k < 1) return 1;
+  const ListPlan kv = bwd_kv_plan(p, varlen);
+  const int64_t ctas = kv.use ? kv.bound : (max_k + 127) / 128 * units * kv_heads(&f);
+  if (ctas < 1 || ctas * 2 > kSplitTargetCtas) return 1;
+  return static_cast<int>(std::min<int64_t>(f.heads / kv_heads(&f), kSplitTargetCtas / ctas));
+}
+size_t bwd_dkv_split_bytes(const attn_bwd_params* p, bool varlen, int split) {
+  if (split < 2) return 0;
+  const attn_fwd_params& f = p->fwd;
+  const int64_t rows = varlen ? f.total_k : static_cast<int64_t>(f.batch) * f.seqlen_k;
+  return round256(split * rows * kv_heads(&f) * (f.d_qk + f.d_v) * 4);
+}
+// The workspace without the split-key dQ and split-group dK/dV partials (the least a call accepts).
 size_t bwd_workspace_bytes(const attn_bwd_params* p, bool varlen) {
   const size_t d = bwd_d_bytes(p, varlen);
   const size_t fused = bwd_dq_acc_bytes(p, varlen) + bwd_sem_bytes(p, varlen);
@@ -624,6 +646,10 @@ attn_status_t run_bwd(const attn_bwd_params* p, void* ws, size_t ws_bytes, bool 
   // split-key dQ (after the rest of the workspace) only when the caller's workspace holds its partials
   SplitPlan dqs = (sp.kv_count || nq_rows == 0 || nk_rows == 0) ? SplitPlan{} : bwd_dq_split_plan(p, varlen);
   if (dqs.splits > 1 && ws_bytes < need + bwd_dq_split_bytes(p, dqs)) dqs = SplitPlan{};
+  // split-group dK/dV (behind those) likewise
+  int dkv_split = (nq_rows == 0 || nk_rows == 0) ? 1 : bwd_dkv_split(p, varlen);
+  const size_t off_dkv = need + bwd_dq_split_bytes(p, dqs);
+  if (ws_bytes < off_dkv + bwd_dkv_split_bytes(p, varlen, dkv_split)) dkv_split = 1;
   if (nq_rows > 0 && nk_rows > 0 && f.score_mod == ATTN_SCORE_ALIBI) ATTN_TRY(check_lists_device(f.q, {f.alibi_slopes}));
   if (nq_rows > 0 && nk_rows > 0 && (ws == nullptr || ws_bytes < need || (reinterpret_cast<uintptr_t>(ws) & 15u)))
     return ATTN_ERR_WORKSPACE;
@@ -648,6 +674,8 @@ attn_status_t run_bwd(const attn_bwd_params* p, void* ws, size_t ws_bytes, bool 
   a.heads = f.heads;
   a.heads_kv = hkv;
   a.kv_group = f.heads / hkv;
+  a.dkv_split = dkv_split;
+  a.dkv_part = dkv_split > 1 ? reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + off_dkv) : nullptr;
   a.seqlen_q = nq_rows;
   a.seqlen_k = nk_rows;
   a.cu_q = varlen ? f.cu_seqlens_q : nullptr;
@@ -692,24 +720,26 @@ attn_status_t run_bwd(const attn_bwd_params* p, void* ws, size_t ws_bytes, bool 
     const ListPlan kv = bwd_kv_plan(p, varlen), qp = bwd_q_plan(p, varlen);
     uint8_t* lbase = static_cast<uint8_t*>(ws) + bwd_d_bytes(p, varlen);
     int64_t* scratch = reinterpret_cast<int64_t*>(lbase + (kv.use ? kv.list_bytes : 0) + (qp.use ? qp.list_bytes : 0));
+    TileListSpec specs[2];
+    int n = 0;
     if (kv.use) {
       TileEntry* list = reinterpret_cast<TileEntry*>(lbase);
       // the deterministic single pass launches key tiles in descending order (its adds' order)
       const bool desc = p->single_pass && p->deterministic;
-      e = launch_tile_list(f.cu_seqlens_q, f.cu_seqlens_k, f.num_seqs, hkv, 128, true, desc, kv.max_nblk, list,
-                           scratch, kv.bound, stream);
-      if (e != cudaSuccess) return cuda_fail(e, "bwd tile list");
+      specs[n++] = TileListSpec{hkv, 128, 1, desc ? 1 : 0, kv.max_nblk, list, kv.bound};
       a.tiles_kv = list;
       a.n_tiles_kv = kv.bound;
       lbase += kv.list_bytes;
     }
     if (qp.use) {
       TileEntry* list = reinterpret_cast<TileEntry*>(lbase);
-      e = launch_tile_list(f.cu_seqlens_q, f.cu_seqlens_k, f.num_seqs, f.heads, 128, false, true, qp.max_nblk, list,
-                           scratch, qp.bound, stream);
-      if (e != cudaSuccess) return cuda_fail(e, "bwd tile list");
+      specs[n++] = TileListSpec{f.heads, 128, 0, 1, qp.max_nblk, list, qp.bound};
       a.tiles_q = list;
       a.n_tiles_q = qp.bound;
+    }
+    if (n > 0) {
+      e = launch_tile_lists(f.cu_seqlens_q, f.cu_seqlens_k, f.num_seqs, specs, n, scratch, nullptr, stream);
+      if (e != cudaSuccess) return cuda_fail(e, "bwd tile lists");
     }
   }
 
@@ -760,6 +790,7 @@ attn_status_t run_bwd(const attn_bwd_params* p, void* ws, size_t ws_bytes, bool 
     e = launch_bwd_dkdv_pair(tq_r, tq2, tk, tv, tdo_r, tdo2, a, stream);
   } else {
     e = launch_bwd_dkdv(f.d_qk, f.d_v, tq2, tk, tv, tdo2, a, stream);
+    if (e == cudaSuccess && dkv_split > 1) e = launch_bwd_dkv_merge(a, f.d_qk, f.d_v, stream);
   }
   if (e == cudaSuccess) e = mark(1);
   if (e != cudaSuccess) return cuda_fail(e, "bwd dkdv launch");
@@ -1061,7 +1092,8 @@ attn_status_t attn_bwd_block_sparse(const attn_bwd_params* p, const int32_t* kv_
 size_t attn_bwd_workspace_size(const attn_bwd_params* p) {
   if (!p) return 0;
   const bool varlen = p->fwd.cu_seqlens_q != nullptr;
-  return bwd_workspace_bytes(p, varlen) + bwd_dq_split_bytes(p, bwd_dq_split_plan(p, varlen));
+  return bwd_workspace_bytes(p, varlen) + bwd_dq_split_bytes(p, bwd_dq_split_plan(p, varlen)) +
+         bwd_dkv_split_bytes(p, varlen, bwd_dkv_split(p, varlen));
 }
 
 attn_status_t attn_bwd(const attn_bwd_params* p, void* workspace, size_t workspace_bytes, attn_stream_t stream) {

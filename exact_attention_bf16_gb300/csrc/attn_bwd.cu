@@ -209,6 +209,49 @@ cudaError_t launch_bwd_dq_merge(const BwdArgs& a, int d_qk, cudaStream_t stream)
   return cudaGetLastError();
 }
 
+namespace bwd {
+
+// One thread per 8 elements of a (key row, K/V head): the parts added in ascending
+// order, so that every call gives the same bits. Rows behind the last sequence of a
+// packed batch are left alone, as the kernels leave them.
+__global__ void dkv_merge_kernel(const BwdArgs a, int d_qk, int d_v) {
+  const int width = d_qk + d_v, upr = width / 8;
+  const int64_t rows = static_cast<int64_t>(a.batch) * a.seqlen_k, units = rows * a.heads_kv * upr;
+  const int64_t last = a.cu_k != nullptr ? a.cu_k[a.num_units] : rows;
+  for (int64_t i = blockIdx.x * static_cast<int64_t>(blockDim.x) + threadIdx.x; i < units;
+       i += static_cast<int64_t>(gridDim.x) * blockDim.x) {
+    const int c = 8 * static_cast<int>(i % upr);
+    const int64_t rh = i / upr, row = rh / a.heads_kv;
+    const int h = static_cast<int>(rh % a.heads_kv);
+    if (row >= last) continue;
+    const float* src = a.dkv_part + rh * width + c;
+    float4 x = make_float4(0.f, 0.f, 0.f, 0.f), y = x;
+#pragma unroll 4
+    for (int r = 0; r < a.dkv_split; ++r) {
+      const float4* pr = reinterpret_cast<const float4*>(src + r * rows * a.heads_kv * width);
+      const float4 u = __ldg(pr), w = __ldg(pr + 1);
+      x = make_float4(x.x + u.x, x.y + u.y, x.z + u.z, x.w + u.w);
+      y = make_float4(y.x + w.x, y.y + w.y, y.z + w.z, y.w + w.w);
+    }
+    const float sc = c < d_qk ? a.scale : 1.f;
+    const int64_t b = row / a.seqlen_k, n = row % a.seqlen_k;
+    __nv_bfloat16* dst = c < d_qk ? static_cast<__nv_bfloat16*>(a.dk) + b * a.dk_sb + n * a.dk_sn + h * a.dk_sh + c
+                                  : static_cast<__nv_bfloat16*>(a.dv) + b * a.dv_sb + n * a.dv_sn + h * a.dv_sh + c - d_qk;
+    *reinterpret_cast<uint4*>(dst) = make_uint4(pack_bf16x2(x.x * sc, x.y * sc), pack_bf16x2(x.z * sc, x.w * sc),
+                                                pack_bf16x2(y.x * sc, y.y * sc), pack_bf16x2(y.z * sc, y.w * sc));
+  }
+}
+
+}  // namespace bwd
+
+cudaError_t launch_bwd_dkv_merge(const BwdArgs& a, int d_qk, int d_v, cudaStream_t stream) {
+  if (a.dkv_split < 2 || a.dkv_part == nullptr) return cudaErrorInvalidValue;
+  const int64_t units = static_cast<int64_t>(a.batch) * a.seqlen_k * a.heads_kv * ((d_qk + d_v) / 8);
+  const int64_t want = (units + 255) / 256;
+  bwd::dkv_merge_kernel<<<static_cast<unsigned>(want < 152 * 16 ? want : 152 * 16), 256, 0, stream>>>(a, d_qk, d_v);
+  return cudaGetLastError();
+}
+
 cudaError_t launch_bwd_zero(const BwdArgs& a, int d_qk, int d_v, bool zero_dq, bool zero_dkdv, cudaStream_t stream) {
   auto go = [&](void* p, int64_t sb, int64_t sn, int64_t sh, int nrows, int heads, int d) -> cudaError_t {
     const int64_t total = static_cast<int64_t>(a.batch) * nrows * heads;

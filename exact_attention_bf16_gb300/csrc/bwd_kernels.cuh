@@ -64,6 +64,29 @@ __device__ __forceinline__ void tile_row_to_tmem(const uint8_t* tile, int chunks
   }
 }
 
+// Split groups: one key row's fp32 dV or unscaled dK of part `part` (32-column groups from
+// TMEM, all lanes of the warp alike), into the row of d_qk + d_v floats at column col0;
+// dkv_merge_kernel adds the parts.
+__device__ __forceinline__ void store_dkv_part(const BwdArgs& a, const Unit& U, int h, int part, int kj, bool store,
+                                               bool any, int width, int col0, int groups, uint32_t taddr) {
+  const int64_t row = static_cast<int64_t>(U.b) * a.seqlen_k + U.k_start + kj;
+  float* dst = a.dkv_part +
+               ((static_cast<int64_t>(part) * a.batch * a.seqlen_k + row) * a.heads_kv + h) * width + col0;
+  for (int c = 0; c < groups; ++c) {
+    uint32_t v[32];
+    tmem_ld32(taddr + c * 32, v);
+    tmem_wait_ld();
+    if (store) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        reinterpret_cast<float4*>(dst + c * 32)[e] =
+            any ? make_float4(__uint_as_float(v[4 * e]), __uint_as_float(v[4 * e + 1]), __uint_as_float(v[4 * e + 2]),
+                              __uint_as_float(v[4 * e + 3]))
+                : make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+  }
+}
+
 // ===========================================================================
 // dK / dV kernel (key-stationary)
 // ===========================================================================
@@ -151,6 +174,9 @@ __device__ __forceinline__ bool sem_wait(const int* sem, int target, uint32_t* s
 // the loop runs over the query tiles of its a.kv_group query heads, one head
 // after another, so that the sums over them stay in the same TMEM accumulators:
 // K and V are read once for the whole group, and no partial gradient leaves the SM.
+// Where that makes too few CTAs (a.dkv_split > 1), a group's heads are cut into
+// dkv_split parts of consecutive heads, one CTA each (part fastest in the grid), whose
+// fp32 sums are added in part order by a second kernel.
 template <int DQK, int DV, bool SPARSE = false, int MOD = 0, bool FUSED = false, bool GQA = false>
 __global__ void __launch_bounds__(kThreads, 1)
     dkdv_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUtensorMap tmk,
@@ -173,7 +199,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   int h, n;
   // FUSED with semaphores: key tiles in descending order, the shortest (fewest
   // query tiles under the causal mask) first, matching the adds' order below
-  if (!bwd_work(a, a.tiles_kv, a.n_kblk, FUSED && a.dq_sem != nullptr, U, h, n, a.heads_kv, a.n_groups_kv)) return;
+  // GQA, split groups: part `part` of the K/V head's query heads
+  const int n_parts = GQA ? a.dkv_split : 1;
+  const int part = GQA ? static_cast<int>(blockIdx.x) % n_parts : 0;
+  if (!bwd_work(a, a.tiles_kv, a.n_kblk, FUSED && a.dq_sem != nullptr, U, h, n, a.heads_kv, a.n_groups_kv,
+                GQA ? static_cast<int>(blockIdx.x) / n_parts : -1))
+    return;
   const int k0 = n * KB;
   if (k0 >= U.nk) return;
   int m_begin = 0;
@@ -188,7 +219,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                                  : 0;
   if constexpr (SPARSE) T = __ldg(a.q_count + kv_list) * (256 / QB);
   const int T1 = T;  // GQA: steps of one query head
-  if constexpr (GQA) T *= a.kv_group;
+  const int hq_first = GQA ? h * a.kv_group + part * a.kv_group / n_parts : h;  // this CTA's query heads
+  if constexpr (GQA) T *= h * a.kv_group + (part + 1) * a.kv_group / n_parts - hq_first;
   // first query row of step t
   auto q_row = [&](int t) -> int {
     if constexpr (SPARSE) {
@@ -238,7 +270,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // of their own (the slot is recycled only after dV, dK of that tile ran).
     int issued = 0;
     bool ok = true;
-    int tt = 0, hq = GQA ? h * a.kv_group : h;  // step within the query head hq
+    int tt = 0, hq = hq_first;  // step within the query head hq
     for (int t = 0; t < T && ok; ++t) {
       const int st = t % C::NST;
       const uint32_t use = static_cast<uint32_t>(t / C::NST);
@@ -388,7 +420,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int i_vis = a.causal ? kj - (U.nk - U.nq) : -0x40000000;
     const bool key_ok = kj < U.nk;
     const float sl2 = a.scale_log2;
-    int tt = 0, hq = GQA ? h * a.kv_group : h;  // step within the query head hq
+    int tt = 0, hq = hq_first;  // step within the query head hq
     float alibi_slope = MOD == kModAlibi ? __ldg(a.alibi_slopes + hq) * a.inv_scale : 0.f;  // raw units
     const uint32_t my_cols = C::tS + 32 * wg;     // this warpgroup's S^T columns
     const uint32_t my_pds = C::tPdS + 32 * wg;    // its P^T (16) and dS^T (16) columns
@@ -549,7 +581,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
     const bool store = key_ok;
-    if (wg == 0) {
+    if (GQA && n_parts > 1) {
+      store_dkv_part(a, U, h, part, kj, store, T > 0, DQK + DV, wg == 0 ? DQK : 0, (wg == 0 ? DV : DQK) / 32,
+                     lane_base + (wg == 0 ? C::tdV : C::tdK));
+    } else if (wg == 0) {
       __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(a.dv) + U.b * a.dv_sb +
                            static_cast<int64_t>(U.k_start + kj) * a.dv_sn + h * a.dv_sh;
 #pragma unroll
@@ -663,7 +698,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   // same work order as dkdv_kernel: (unit, head) slow, key tile 0 (the heaviest under causal) first
   Unit U;
   int h, n;
-  if (!bwd_work(a, a.tiles_kv, a.n_kblk, false, U, h, n, a.heads_kv, a.n_groups_kv)) return;
+  // GQA, split groups: part `part` of the K/V head's query heads
+  const int n_parts = GQA ? a.dkv_split : 1;
+  const int part = GQA ? static_cast<int>(blockIdx.x) % n_parts : 0;
+  if (!bwd_work(a, a.tiles_kv, a.n_kblk, false, U, h, n, a.heads_kv, a.n_groups_kv,
+                GQA ? static_cast<int>(blockIdx.x) / n_parts : -1))
+    return;
   const int k0 = n * KB;
   if (k0 >= U.nk) return;
   int m_begin = 0;
@@ -678,7 +718,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                                  : 0;
   if constexpr (SPARSE) T = __ldg(a.q_count + kv_list) * (256 / QB);
   const int T1 = T;  // GQA: steps of one query head
-  if constexpr (GQA) T *= a.kv_group;
+  const int hq_first = GQA ? h * a.kv_group + part * a.kv_group / n_parts : h;  // this CTA's query heads
+  if constexpr (GQA) T *= h * a.kv_group + (part + 1) * a.kv_group / n_parts - hq_first;
   // first query row of step t
   auto q_row = [&](int t) -> int {
     if constexpr (SPARSE) {
@@ -733,7 +774,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // 128 (-LSE*log2e, -D) pairs into the vector ring and arrives on its barrier.
     int nq_issued = 0, ng_issued = 0;
     bool ok = true;
-    int tt = 0, hq = GQA ? h * a.kv_group : h;  // step within the query head hq
+    int tt = 0, hq = hq_first;  // step within the query head hq
     for (int t = 0; t < T && ok; ++t) {
       const int tile = q_row(GQA ? tt : t);
       const int row = U.q_start + tile;
@@ -895,7 +936,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const bool all_keys = kok[0][0] && kok[0][1] && kok[1][0] && kok[1][1];
     const int vis_max = max(max(vis[0][0], vis[0][1]), max(vis[1][0], vis[1][1]));
     const float2 sl2v = make_float2(a.scale_log2, a.scale_log2);
-    int tt = 0, hq = GQA ? h * a.kv_group : h;  // step within the query head hq
+    int tt = 0, hq = hq_first;  // step within the query head hq
     float alibi_slope = MOD == kModAlibi ? __ldg(a.alibi_slopes + hq) * a.inv_scale : 0.f;  // raw units
     auto lanes = [&](int lg) { return tbase + ((quarter * 32u + 16u * static_cast<uint32_t>(lg)) << 16); };
     bool ok = true;
@@ -1025,6 +1066,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int kj = k0 + static_cast<int>(quarter * 32 + lane);
     const uint32_t lane_base = tbase + ((quarter * 32u) << 16);
     const bool store = kj < U.nk;
+    if (GQA && n_parts > 1)
+      store_dkv_part(a, U, h, part, kj, store, T > 0, 2 * C::D, wg == 0 ? C::D : 0, C::D / 32,
+                     lane_base + (wg == 0 ? C::tdV : C::tdK));
     __nv_bfloat16* dst = wg == 0 ? static_cast<__nv_bfloat16*>(a.dv) + U.b * a.dv_sb +
                                        static_cast<int64_t>(U.k_start + kj) * a.dv_sn + h * a.dv_sh
                                  : static_cast<__nv_bfloat16*>(a.dk) + U.b * a.dk_sb +
@@ -1033,6 +1077,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const float mul = wg == 0 ? 1.f : a.scale;
 #pragma unroll
     for (int c = 0; c < C::D / 32; ++c) {
+      if (GQA && n_parts > 1) break;
       uint32_t v[32], w[16];
       if (T > 0) {
         tmem_ld32(lane_base + acc + c * 32, v);
@@ -1549,12 +1594,13 @@ template <int DQK, int DV, bool SPARSE, int MOD = 0, bool FUSED = false, bool GQ
 cudaError_t launch_dkdv_t(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const CUtensorMap& tdo,
                           const BwdArgs& a, cudaStream_t stream) {
   using C = DkdvCfg<DQK, DV, FUSED>;
-  if (GQA != (a.kv_group > 1)) return cudaErrorInvalidValue;
+  if (GQA != (a.kv_group > 1) || a.dkv_split < 1 || (a.dkv_split > 1 && (!GQA || a.dkv_part == nullptr)))
+    return cudaErrorInvalidValue;
   auto kern = dkdv_kernel<DQK, DV, SPARSE, MOD, FUSED, GQA>;
   static PerDeviceOnce once;
   cudaError_t e = once.run([&] { return set_smem(kern, C::SMEM); });
   if (e != cudaSuccess) return e;
-  const int64_t grid = a.tiles_kv ? a.n_tiles_kv : static_cast<int64_t>(a.n_kblk) * a.num_units * a.heads_kv;
+  const int64_t grid = (a.tiles_kv ? a.n_tiles_kv : static_cast<int64_t>(a.n_kblk) * a.num_units * a.heads_kv) * (GQA ? a.dkv_split : 1);
   if (grid <= 0) return cudaSuccess;
   if (grid > 0x7fffffff) return cudaErrorInvalidConfiguration;
   kern<<<static_cast<unsigned>(grid), kThreads, C::SMEM, stream>>>(tq, tk, tv, tdo, a);
@@ -1564,11 +1610,12 @@ cudaError_t launch_dkdv_t(const CUtensorMap& tq, const CUtensorMap& tk, const CU
 template <bool SPARSE, int MOD = 0, bool GQA = false>
 cudaError_t launch_dkdv_wide(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                              const CUtensorMap& tdo, const BwdArgs& a, cudaStream_t stream) {
-  if (GQA != (a.kv_group > 1)) return cudaErrorInvalidValue;
+  if (GQA != (a.kv_group > 1) || a.dkv_split < 1 || (a.dkv_split > 1 && (!GQA || a.dkv_part == nullptr)))
+    return cudaErrorInvalidValue;
   static PerDeviceOnce once;
   cudaError_t e = once.run([] { return set_smem(dkdv_wide_kernel<SPARSE, MOD, GQA>, DkdvWCfg::SMEM); });
   if (e != cudaSuccess) return e;
-  const int64_t grid = a.tiles_kv ? a.n_tiles_kv : static_cast<int64_t>(a.n_kblk) * a.num_units * a.heads_kv;
+  const int64_t grid = (a.tiles_kv ? a.n_tiles_kv : static_cast<int64_t>(a.n_kblk) * a.num_units * a.heads_kv) * (GQA ? a.dkv_split : 1);
   if (grid <= 0) return cudaSuccess;
   if (grid > 0x7fffffff) return cudaErrorInvalidConfiguration;
   dkdv_wide_kernel<SPARSE, MOD, GQA>

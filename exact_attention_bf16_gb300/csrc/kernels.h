@@ -50,7 +50,7 @@ class DeviceScope {
 };
 
 // One CTA's work in a packed variable-length launch (built by
-// launch_tile_list): the sequence's row ranges, the head and the block index
+// launch_tile_lists): the sequence's row ranges, the head and the block index
 // (of R rows: 256 queries forward, 128 keys dK/dV, 128 queries dQ). seq < 0:
 // an empty entry past the real ones; its CTA exits.
 struct TileEntry {
@@ -99,14 +99,19 @@ inline int group_count(int n_pairs, int64_t bytes_per_pair) {
   return static_cast<int>((n_pairs + g - 1) / g);
 }
 
-// Builds the list for num_seqs sequences (cu_q / cu_k offsets on the device):
+// Builds up to two lists for num_seqs sequences (cu_q / cu_k offsets on the device):
 // sequences with the most blocks first (by key blocks when by_keys), then
 // head by head, blocks of a head in descending or ascending order. Writes
-// `bound` entries (the real ones, then empty ones); seq_start is scratch of
-// num_seqs int64. max_nblk bounds every sequence's block count (<= kMaxListBlocks).
-cudaError_t launch_tile_list(const int* cu_q, const int* cu_k, int num_seqs, int heads, int rows_per_block,
-                             bool by_keys, bool descending, int max_nblk, TileEntry* out, int64_t* seq_start,
-                             int64_t bound, cudaStream_t stream);
+// `bound` entries (the real ones, then empty ones); scratch holds num_seqs
+// int64. max_nblk bounds every sequence's block count (<= kMaxListBlocks).
+// *zero_word (when given) is set to 0.
+struct TileListSpec {
+  int heads, rows_per_block, by_keys, descending, max_nblk;
+  TileEntry* out;
+  int64_t bound;
+};
+cudaError_t launch_tile_lists(const int* cu_q, const int* cu_k, int num_seqs, const TileListSpec* specs, int n,
+                              int64_t* scratch, uint32_t* zero_word, cudaStream_t stream);
 
 // Forward kernel arguments (passed by value; tensor maps go separately as
 // __grid_constant__ parameters).
@@ -273,6 +278,11 @@ struct BwdArgs {
   // dispatch groups of grid_slot.
   int kv_group, heads_kv;
   int n_groups_kv;
+  // Shared K/V heads, dkv_split > 1: the group's query heads are cut into dkv_split parts,
+  // one CTA each, whose unscaled fp32 dK and dV rows go to dkv_part[part][key row][K/V
+  // head][d_qk + d_v]; launch_bwd_dkv_merge adds them in order.
+  int dkv_split;
+  float* dkv_part;
 };
 
 // Single-pass backward (d_qk = d_v = 64): dK, dV and the fp32 dQ partials of
@@ -305,6 +315,8 @@ cudaError_t launch_bwd_dq(int d_qk, int d_v, const CUtensorMap& tq, const CUtens
                           const CUtensorMap& tdo, const BwdArgs& a, cudaStream_t stream);
 // dQ (bf16, strided) = scale * (sum over r < a.dq_split, in order, of a.dq_part's range r).
 cudaError_t launch_bwd_dq_merge(const BwdArgs& a, int d_qk, cudaStream_t stream);
+// dK = scale * sum, dV = sum (bf16, strided) over the parts r < a.dkv_split, in order.
+cudaError_t launch_bwd_dkv_merge(const BwdArgs& a, int d_qk, int d_v, cudaStream_t stream);
 // Zero-fills dQ, dK, dV rows of a problem with no keys or no queries.
 cudaError_t launch_bwd_zero(const BwdArgs& a, int d_qk, int d_v, bool zero_dq, bool zero_dkdv, cudaStream_t stream);
 

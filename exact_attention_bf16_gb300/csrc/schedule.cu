@@ -28,10 +28,20 @@ namespace gb300 {
 namespace sched {
 
 constexpr int kThreads = 1024;
+constexpr int kSharedSeqs = 1024;  // up to so many sequences need no scratch in global memory
 
+// Block b builds list b (a backward's two lists in one launch).
 __global__ void __launch_bounds__(kThreads, 1)
-    tile_list_kernel(const int* cu_q, const int* cu_k, int num_seqs, int heads, int rows_per_block, int by_keys,
-                     int descending, int max_nblk, TileEntry* out, int64_t* seq_start, int64_t bound) {
+    tile_list_kernel(const int* cu_q, const int* cu_k, int num_seqs, TileListSpec l0, TileListSpec l1,
+                     int64_t* scratch, uint32_t* zero_word) {
+  const TileListSpec& l = blockIdx.x == 0 ? l0 : l1;
+  const int heads = l.heads, rows_per_block = l.rows_per_block, by_keys = l.by_keys, descending = l.descending,
+            max_nblk = l.max_nblk;
+  TileEntry* out = l.out;
+  const int64_t bound = l.bound;
+  __shared__ int64_t shared_start[kSharedSeqs];
+  int64_t* seq_start = num_seqs <= kSharedSeqs ? shared_start : scratch;
+  if (zero_word != nullptr && blockIdx.x == 0 && threadIdx.x == 0) *zero_word = 0;
   __shared__ int bins[kMaxListBlocks + 1];          // sequences per block count, then cursors
   __shared__ long long bin_start[kMaxListBlocks + 1];  // first entry of each block count
   __shared__ long long warp_sum[kThreads / 32];
@@ -114,14 +124,21 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 }  // namespace sched
 
-cudaError_t launch_tile_list(const int* cu_q, const int* cu_k, int num_seqs, int heads, int rows_per_block,
-                             bool by_keys, bool descending, int max_nblk, TileEntry* out, int64_t* seq_start,
-                             int64_t bound, cudaStream_t stream) {
-  if (max_nblk < 0 || max_nblk > kMaxListBlocks || num_seqs < 0 || rows_per_block <= 0) return cudaErrorInvalidValue;
-  sched::tile_list_kernel<<<1, sched::kThreads, 0, stream>>>(cu_q, cu_k, num_seqs, heads, rows_per_block,
-                                                           by_keys ? 1 : 0, descending ? 1 : 0, max_nblk, out,
-                                                           seq_start, bound);
-  return cudaGetLastError();
+cudaError_t launch_tile_lists(const int* cu_q, const int* cu_k, int num_seqs, const TileListSpec* specs, int n,
+                              int64_t* scratch, uint32_t* zero_word, cudaStream_t stream) {
+  if (num_seqs < 0 || n < 0 || n > 2) return cudaErrorInvalidValue;
+  for (int i = 0; i < n; ++i)
+    if (specs[i].max_nblk < 0 || specs[i].max_nblk > kMaxListBlocks || specs[i].rows_per_block <= 0)
+      return cudaErrorInvalidValue;
+  // more sequences than shared memory holds starts for: one list after another in the scratch
+  const int per_launch = num_seqs <= sched::kSharedSeqs ? n : 1;
+  for (int i = 0; i < n; i += per_launch) {
+    sched::tile_list_kernel<<<per_launch, sched::kThreads, 0, stream>>>(cu_q, cu_k, num_seqs, specs[i],
+                                                                       specs[i + per_launch - 1], scratch, zero_word);
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
 }
 
 }  // namespace gb300

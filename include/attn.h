@@ -282,7 +282,13 @@ typedef struct attn_bwd_params {
  * second kernel (the same bits on every call; dK and dV are unchanged). The
  * size then adds s x batch x heads x seqlen_q x d_qk x 4 bytes, rounded up to
  * 256. A call given at least the size without those bytes (but less than the
- * full size) runs unsplit. The block-sparse backward never splits. */
+ * full size) runs unsplit. The block-sparse backward never splits.
+ * With shared K/V heads, a dK/dV grid of c = key blocks x K/V heads CTAs (dense,
+ * or the tile list's bound) with 2 c <= 148 cuts each group's query heads into
+ * s = min(heads / heads_kv, 148 / c) parts, one CTA each, whose fp32 dK and dV a
+ * second kernel adds in order (the same bits on every call); the size then adds
+ * s x key rows x heads_kv x (d_qk + d_v) x 4 bytes, rounded up to 256, and again
+ * a call given less runs unsplit. */
 size_t attn_fwd_workspace_size(const attn_fwd_params* p);
 size_t attn_bwd_workspace_size(const attn_bwd_params* p);
 

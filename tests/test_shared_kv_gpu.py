@@ -168,3 +168,55 @@ def test_refusals(ea):
         ea.attn_bwd(q, k2, k2, o, lse, o, single_pass=True)
     with pytest.raises(ValueError, match="dk"):
         ea.attn_bwd(q, k2, k2, o, lse, o, dk=torch.empty_like(q))
+
+
+@pytest.mark.parametrize("dims", [(64, 64), (128, 128)])
+def test_enough_blocks_for_whole_groups(ea, dims):
+    """Enough key blocks that every CTA of the dK/dV grid takes all query heads of its K/V head (the small cases above
+    cut the groups into parts)."""
+    lens = [1200, 900, 1401]
+    _check_packed(ea, _packed(lens, lens, 6, 3, dims, seed=91), lens, lens, True)
+
+
+def test_parts_of_groups_match_whole_groups(ea):
+    """The same call with a workspace too small for the parts' sums: dQ the same bits, dK and dV within rounding (each
+    is rounded to bf16 once, half a step of 2^-8 each side)."""
+    import ctypes
+    from exact_attention_bf16_gb300 import _abi
+    q, do = _draw(2, 200, 10, 64, seed=101), _draw(2, 200, 10, 64, seed=102)
+    k, v = _draw(2, 300, 2, 64, seed=103), _draw(2, 300, 2, 64, seed=104)
+    o, lse = ea.attn_fwd(q, k, v, causal=True)
+    want = ea.attn_bwd(q, k, v, o, lse, do, causal=True)
+    p = _abi.AttnBwdParams()
+    ea._fill_fwd(p.fwd, q, k, v, o, lse, ea._strides4, 64 ** -0.5, True)
+    p.fwd.batch, p.fwd.seqlen_q, p.fwd.seqlen_k = 2, 200, 300
+    got = [torch.empty_like(x) for x in (q, k, v)]
+    ea._fill_bwd(p, do, *got, ea._strides4, False)
+    lib = _abi.load()
+    full = lib.attn_bwd_workspace_size(ctypes.byref(p))
+    small = (4 * 2 * 10 * 200 + 255) // 256 * 256  # D only
+    assert full > small
+    ws = torch.empty(small, dtype=torch.uint8, device="cuda")
+    assert lib.attn_bwd(ctypes.byref(p), ctypes.c_void_p(ws.data_ptr()), small, None) == _abi.ATTN_OK
+    torch.cuda.synchronize()
+    assert torch.equal(got[0], want[0])
+    for a, b in zip(got[1:], want[1:]):
+        a, b = a.float(), b.float()
+        assert torch.all((a - b).abs() <= 2.0 ** -7 * torch.maximum(a.abs(), b.abs()) + 1e-5)
+
+
+def test_rows_behind_the_last_sequence_stay(ea):
+    """Packed tensors with rows behind the last offset, gradients into given buffers: those rows stay."""
+    lens = [100, 60]
+    q, k, v, do, cu, _ = _packed(lens + [20], lens + [20], 4, 2, (64, 64), seed=111)
+    cu = cu[:3].contiguous()
+    o = torch.full_like(q, 3.0)
+    lse = torch.full((4, 180), 7.0, device="cuda")
+    grads = [torch.full_like(x, 5.0) for x in (q, k, v)]
+    ea.attn_fwd_varlen(q, k, v, cu, cu, 100, 100, causal=True, out=o, lse=lse)
+    ea.attn_bwd_varlen(q, k, v, o, lse, do, cu, cu, 100, 100, causal=True, dq=grads[0], dk=grads[1], dv=grads[2])
+    torch.cuda.synchronize()
+    ea.attn_get_device_status()
+    assert torch.all(o[160:] == 3) and torch.all(lse[:, 160:] == 7)
+    for g in grads:
+        assert torch.all(g[160:] == 5) and not torch.any(g[:160] == 5)

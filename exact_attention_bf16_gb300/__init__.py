@@ -198,6 +198,27 @@ def _check_offsets(q, cu_seqlens_q, cu_seqlens_k):
         _check_int32("cu_seqlens_k", cu_seqlens_k, dev, cu_seqlens_q.shape[0])
 
 
+def _check_packed_kv(q, k, v, heads: int, d_qk: int, ks, vs) -> int:
+    """Packed k [total_k, Hkv, d_qk] and v [total_k, Hkv, d_v] against q's heads, Hkv a divisor of them; q's GPU."""
+    if ks[2] != d_qk or ks[0] != vs[0] or ks[1] != vs[1] or ks[1] < 1 or heads % ks[1] != 0:
+        _check_kv(q, k, v)
+    dev = q.get_device()
+    if k.get_device() != dev or v.get_device() != dev:
+        _check_kv(q, k, v)
+    return dev
+
+
+def _packed_grad(name: str, grad, like, stream):
+    """A gradient buffer for `like` (the given one, checked) and its strides."""
+    if grad is None:
+        grad = torch.empty(like.shape, dtype=_BF16, device=like.device) if like.is_contiguous() else torch.empty_like(like)
+        if stream is not None:
+            _used_on(stream, grad)
+    elif grad.shape != like.shape or grad.device != like.device:
+        raise ValueError(f"{name} must be {tuple(like.shape)} on {like.device}, got {tuple(grad.shape)} on {grad.device}")
+    return grad, _bf16_layout(name, grad, 3)[1]
+
+
 def _check_kv(q, k, v):
     """k and v of a call whose query heads may share K/V heads: q [..., H, d_qk], k [..., Hkv, d_qk] and
     v [..., Hkv, d_v] with Hkv a divisor of H, rows of k and v alike (dense: batches of q alike)."""
@@ -354,26 +375,32 @@ def attn_fwd_varlen(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqlen
                     v_descale: float = 1.0, cta_pair: bool = False,
                     stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
     """Packed variable-length forward. q [total_q, H, d_qk], k/v [total_k, Hkv, d] with Hkv a divisor of H
-    (query head h reads K/V head h // (H // Hkv)); cu_seqlens int32 on the device. Returns (O [total_q, H, d_v], LSE [H, total_q]). Score modifications and E4M3 inputs
-    as in :func:`attn_fwd`, positions counted within each sequence."""
-    f8 = _check_inputs(q, k, v, 3)
+    (query head h reads K/V head h // (H // Hkv)); cu_seqlens int32 on the device. Returns
+    (O [total_q, H, d_v], LSE [H, total_q]). Score modifications and E4M3 inputs as in :func:`attn_fwd`,
+    positions counted within each sequence."""
+    f8 = q.dtype is torch.float8_e4m3fn
+    if f8:
+        _check_inputs(q, k, v, 3)
+        (tq, H, dqk), sq, ks, sk, vs, sv = q.shape, q.stride(), k.shape, k.stride(), v.shape, v.stride()
+    else:
+        ((tq, H, dqk), sq), (ks, sk), (vs, sv) = (_bf16_layout("q", q, 3), _bf16_layout("k", k, 3),
+                                                  _bf16_layout("v", v, 3))
     _check_offsets(q, cu_seqlens_q, cu_seqlens_k)
-    tq, H, dqk = q.shape
-    tk, dv = k.shape[0], v.shape[-1]
-    _check_kv(q, k, v)
+    _check_packed_kv(q, k, v, H, dqk, ks, vs)
+    tk, dv = ks[0], vs[2]
     scale = float(softmax_scale) if softmax_scale is not None else 1.0 / math.sqrt(dqk)
     if out is None:
-        out = torch.empty((tq, H, dv), dtype=torch.bfloat16, device=q.device)
-        _used_on(stream, out)
-    _check_bf16("out", out, 3)
-    if out.shape != (tq, H, dv):
-        raise ValueError(f"out must be {(tq, H, dv)}, got {tuple(out.shape)}")
+        out, so = torch.empty((tq, H, dv), dtype=_BF16, device=q.device), (H * dv, dv)
+    else:
+        shape, so = _bf16_layout("out", out, 3)
+        if shape != (tq, H, dv):
+            raise ValueError(f"out must be {(tq, H, dv)}, got {tuple(shape)}")
     if lse is None:
-        lse = torch.empty((H, tq), dtype=torch.float32, device=q.device)
-        _used_on(stream, lse)
-    if lse.shape != (H, tq) or not lse.is_contiguous() or lse.dtype != torch.float32:
+        lse = torch.empty((H, tq), dtype=_F32, device=q.device)
+    elif lse.shape != (H, tq) or not lse.is_contiguous() or lse.dtype is not _F32:
         raise ValueError("lse must be a contiguous float32 [H, total_q] tensor")
-    sq, sk, sv, so = q.stride(), k.stride(), v.stride(), out.stride()
+    if stream is not None:
+        _used_on(stream, out, lse)
     mod, cap, slopes = _mod_fields(q, softcap, alibi_slopes)
     p = _pack_fwd(
         q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), lse.data_ptr(),
@@ -382,7 +409,7 @@ def attn_fwd_varlen(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqlen
         int(max_seqlen_q), int(max_seqlen_k), tq, tk, scale, 1 if causal else 0, int(exp2_emu_period),
         rescale_stats.data_ptr() if rescale_stats is not None else 0, mod, cap, slopes,
         _abi.INPUT_E4M3 if f8 else _abi.INPUT_BF16, float(q_descale), float(k_descale), float(v_descale),
-        1 if cta_pair else 0, k.shape[1])
+        1 if cta_pair else 0, ks[1])
     nbytes = _lib.attn_fwd_workspace_size(p)
     ws, ws_ptr = _workspace_ptr(nbytes, q, stream)
     status = _lib.attn_fwd_varlen(p, ws_ptr, nbytes, _stream_of(stream, q))
@@ -488,22 +515,27 @@ def attn_bwd_varlen(q, k, v, out, lse, dout, cu_seqlens_q, cu_seqlens_k, max_seq
                     alibi_slopes: Optional[torch.Tensor] = None, single_pass: bool = False):
     """Packed variable-length backward: returns (dQ, dK, dV) packed like q, k, v; where query heads share
     K/V heads (attn_fwd_varlen), dK and dV are the sums over them."""
-    for n, t in (("q", q), ("k", k), ("v", v), ("out", out), ("dout", dout)):
-        _check_bf16(n, t, 3)
-    tq, H, dqk = q.shape
-    _check_bwd(q, k, v, out, lse, dout, (H, tq), (dq, dk, dv))
+    ((tq, H, dqk), sq), (ks, sk), (vs, sv) = _bf16_layout("q", q, 3), _bf16_layout("k", k, 3), _bf16_layout("v", v, 3)
+    (os, so), (ds, sd) = _bf16_layout("out", out, 3), _bf16_layout("dout", dout, 3)
     _check_offsets(q, cu_seqlens_q, cu_seqlens_k)
+    dev = _check_packed_kv(q, k, v, H, dqk, ks, vs)
+    want = (tq, H, vs[2])
+    for n, t, shape in (("out", out, os), ("dout", dout, ds)):
+        if shape != want or t.get_device() != dev:
+            raise ValueError(f"{n} must be {want} on cuda:{dev}, got {tuple(shape)} on {t.device}")
+    if lse.shape != (H, tq) or not lse.is_contiguous() or lse.dtype is not _F32 or lse.get_device() != dev:
+        raise ValueError(f"lse must be a contiguous float32 tensor of shape {(H, tq)} on cuda:{dev}")
     scale = float(softmax_scale) if softmax_scale is not None else 1.0 / math.sqrt(dqk)
-    dq, dk, dv = _grad_buffers(stream, (dq, q), (dk, k), (dv, v))
-    sq, sk, sv, so, sd = q.stride(), k.stride(), v.stride(), out.stride(), dout.stride()
-    tdq, tdk, tdv = dq.stride(), dk.stride(), dv.stride()
+    dq, tdq = _packed_grad("dq", dq, q, stream)
+    dk, tdk = _packed_grad("dk", dk, k, stream)
+    dv, tdv = _packed_grad("dv", dv, v, stream)
     mod, cap, slopes = _mod_fields(q, softcap, alibi_slopes)
     p = _pack_bwd(
         q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), lse.data_ptr(),
         0, sq[0], sq[1], 0, sk[0], sk[1], 0, sv[0], sv[1], 0, so[0], so[1],
-        1, H, 0, 0, dqk, v.shape[2], cu_seqlens_q.data_ptr(), cu_seqlens_k.data_ptr(), cu_seqlens_q.shape[0] - 1,
-        int(max_seqlen_q), int(max_seqlen_k), tq, k.shape[0], scale, 1 if causal else 0, 0, 0, mod, cap, slopes,
-        0, 0.0, 0.0, 0.0, 0, k.shape[1],
+        1, H, 0, 0, dqk, vs[2], cu_seqlens_q.data_ptr(), cu_seqlens_k.data_ptr(), cu_seqlens_q.shape[0] - 1,
+        int(max_seqlen_q), int(max_seqlen_k), tq, ks[0], scale, 1 if causal else 0, 0, 0, mod, cap, slopes,
+        0, 0.0, 0.0, 0.0, 0, ks[1],
         dout.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(),
         0, sd[0], sd[1], 0, tdq[0], tdq[1], 0, tdk[0], tdk[1], 0, tdv[0], tdv[1],
         1 if deterministic else 0, 1 if cta_pair else 0, 0, 0, 0, 1 if single_pass else 0)

@@ -239,11 +239,12 @@ struct EvenWalk {
 
 // The page of key block kt that lane's box number my_page of a block's copies reads;
 // num_pages (whose boxes read zeros) past the last key and for entries outside the cache.
-__device__ __forceinline__ int page_of(const PagedArgs& a, const Seg& w, int kt, int my_page) {
-  const long long key = (static_cast<long long>(kt) << 7) + (static_cast<long long>(my_page) << a.page_shift);
-  if (key >= w.nk) return a.num_pages;
-  const int pg = __ldg(a.block_table + w.seq * a.block_table_stride + (key >> a.page_shift));
-  return pg < 0 || pg > a.num_pages ? a.num_pages : pg;
+// (Positions fit in 31 bits: max_keys.)
+__device__ __forceinline__ int page_of(const PagedArgs& a, const int* table, int nk, int kt, int my_page) {
+  const int key = (kt << 7) + (my_page << a.page_shift);
+  if (key >= nk) return a.num_pages;
+  const uint32_t pg = static_cast<uint32_t>(__ldg(table + (key >> a.page_shift)));
+  return static_cast<int>(min(pg, static_cast<uint32_t>(a.num_pages)));
 }
 
 // Warp 0 of both kernels: publishes the segments that next_seg() gives and copies their K
@@ -269,71 +270,80 @@ __device__ __forceinline__ bool copy_loop(const PagedArgs& a, B* bar, Seg* sSeg,
   uint32_t cs0 = 0, cs1 = 0, phase = 0;
   int jk = 0, jv = 0;
   bool ok = true;
-  Seg w = next_seg();
-  int page = w.more ? page_of(a, w, w.kt0, my_page) : 0;
+  Seg w, nw;          // this segment and the next
+  const int* table;   // block-table rows of both
+  const int* ntable = nullptr;
+  int npage = 0;
+  nw.more = 1;
+  bool first = true;
   for (;;) {
-    ok = mbar_wait_warp(&bar->seg_empty[rs.slot], rs.phase ^ 1u, a.status, site);
-    if (!ok) break;
-    const int n = max(w.n0, w.n1);
-    if (lane == 0) {
-      w.v0 = done, w.s0 = cs0, w.s1 = cs1, w.phase = phase;
-      sSeg[rs.slot] = w;
-      mbar_arrive(&bar->seg_full[rs.slot]);
-    }
-    rs.next();
-    if (!w.more) break;
-    cs0 += w.dual ? (w.n0 + 1) / 2 : w.n0;
-    cs1 += w.dual ? w.n0 / 2 : w.n1;
-    phase ^= (w.n0 > 0 ? 1u : 0u) | ((w.dual ? w.n0 > 1 : w.n1 > 0) ? 2u : 0u) | (w.dual ? 4u : 0u);
-    Seg nw;
-    nw.more = 0;
-    int npage = 0;
-    if (n == 0) {
+    // the next segment and its first page; at the start, then behind each segment's first few copies
+    auto look_ahead = [&]() {
       nw = next_seg();
-      npage = nw.more ? page_of(a, nw, nw.kt0, my_page) : 0;
+      if (nw.more) {
+        ntable = a.block_table + nw.seq * a.block_table_stride;
+        npage = page_of(a, ntable, nw.nk, nw.kt0, my_page);
+      }
+    };
+    int n = 0;
+    if (!first) {
+      w = nw;
+      table = ntable;
+      ok = mbar_wait_warp(&bar->seg_empty[rs.slot], rs.phase ^ 1u, a.status, site);
+      if (!ok) break;
+      n = max(w.n0, w.n1);
+      if (lane == 0) {
+        w.v0 = done, w.s0 = cs0, w.s1 = cs1, w.phase = phase;
+        sSeg[rs.slot] = w;
+        mbar_arrive(&bar->seg_full[rs.slot]);
+      }
+      rs.next();
+      if (!w.more) break;
+      cs0 += w.dual ? (w.n0 + 1) / 2 : w.n0;
+      cs1 += w.dual ? w.n0 / 2 : w.n1;
+      phase ^= (w.n0 > 0 ? 1u : 0u) | ((w.dual ? w.n0 > 1 : w.n1 > 0) ? 2u : 0u) | (w.dual ? 4u : 0u);
     }
-    auto row_of = [&](int j) { return a.page_size > BN ? ((w.kt0 + j) << 7) & (a.page_size - 1) : 0; };
-    int kp = page, vp = page;
-    for (jk = jv = 0; jv < n;) {
-      if (jk < n && jk - jv < 2) {
-        const int next = jk + 1 < n ? page_of(a, w, w.kt0 + jk + 1, my_page) : 0;  // fetched ahead of the wait
+    first = false;
+    int kp = npage, p1 = 0, p2 = 0;  // pages of K block jk, jk - 1 and jk - 2
+    const int ahead = min(n, static_cast<int>(C::NK));
+    bool looked = false;
+    for (jk = jv = 0;;) {
+      if (jk >= ahead && !looked) {
+        look_ahead();
+        looked = true;
+      }
+      if (jv >= n) break;
+      const bool is_k = jk < n && jk - jv < 2;
+      if (is_k) {
+        const int next = jk + 1 < n ? page_of(a, table, w.nk, w.kt0 + jk + 1, my_page) : 0;  // fetched ahead of the wait
         ok = mbar_wait_warp(&bar->k_empty[rk.slot], rk.phase ^ 1u, a.status, site + 1);
         if (!ok) break;
         if (lane == 0) mbar_arrive_expect_tx(&bar->k_full[rk.slot], C::K_BYTES);
         __syncwarp();
+        const int row = a.page_size > BN ? ((w.kt0 + jk) << 7) & (a.page_size - 1) : 0;
         if (my_chunk < C::QCH)
-          tma_load_4d(sK + rk.slot * C::K_BYTES + box_off, tmk, &bar->k_full[rk.slot], my_chunk * 64, w.hk, row_of(jk), kp);
+          tma_load_4d(sK + rk.slot * C::K_BYTES + box_off, tmk, &bar->k_full[rk.slot], my_chunk * 64, w.hk, row, kp);
         rk.next();
-        if (jk == 0) {  // Q behind the first K: that slot may be free long before the previous Q is
+        p2 = p1, p1 = kp, kp = next;
+        if (++jk == 1) {  // Q behind the first K: that slot may be free long before the previous Q is
           ok = copy_q(w);
-          if (!ok) {
-            ++jk;
-            break;
-          }
-        }
-        kp = next;
-        ++jk;
-        if (jk == min(n, static_cast<int>(C::NK))) {
-          nw = next_seg();
-          npage = nw.more ? page_of(a, nw, nw.kt0, my_page) : 0;
+          if (!ok) break;
         }
       } else {
-        const int next = jv + 1 < n ? page_of(a, w, w.kt0 + jv + 1, my_page) : 0;
         ok = mbar_wait_warp(&bar->v_empty[rv.slot], rv.phase ^ 1u, a.status, site + 2);
         if (!ok) break;
         if (lane == 0) mbar_arrive_expect_tx(&bar->v_full[rv.slot], C::V_BYTES);
         __syncwarp();
+        const int row = a.page_size > BN ? ((w.kt0 + jv) << 7) & (a.page_size - 1) : 0;
         if (my_chunk < C::VCH)
-          tma_load_4d(sV + rv.slot * C::V_BYTES + box_off, tmv, &bar->v_full[rv.slot], my_chunk * 64, w.hk, row_of(jv), vp);
+          tma_load_4d(sV + rv.slot * C::V_BYTES + box_off, tmv, &bar->v_full[rv.slot], my_chunk * 64, w.hk, row,
+                      jk - jv == 2 ? p2 : p1);
         rv.next();
-        vp = next;
         ++jv;
       }
     }
     if (!ok) break;
     done += static_cast<uint32_t>(n);
-    w = nw;
-    page = npage;
   }
   if (!ok) {
     const uint32_t ck = done + static_cast<uint32_t>(jk), cv = done + static_cast<uint32_t>(jv);

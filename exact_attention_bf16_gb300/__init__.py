@@ -782,6 +782,7 @@ def attention_varlen(q, k, v, cu_seqlens_q, cu_seqlens_k, max_seqlen_q: int, max
                      softmax_scale: Optional[float] = None, deterministic: bool = False,
                      softcap: Optional[float] = None, alibi_slopes: Optional[torch.Tensor] = None):
     """Autograd wrapper over attn_fwd_varlen / attn_bwd_varlen for packed bf16 tensors q [total_q, H, d_qk],
-    k [total_k, Hkv, d_qk] and v [total_k, Hkv, d_v]; ``softcap`` / ``alibi_slopes`` select a score modification."""
+    k [total_k, Hkv, d_qk] and v [total_k, Hkv, d_v]; ``softcap`` / ``alibi_slopes`` select a score modification.
+    The offsets cover every row: cu_seqlens[-1] is the total (of a buffer with spare rows, pass the used part)."""
     return _AttentionVarlen.apply(q, k, v, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, max_seqlen_k, causal,
                                   softmax_scale, deterministic, softcap, alibi_slopes)

@@ -96,7 +96,10 @@ typedef void* attn_stream_t;
  * cu_seqlens_k are device int32 arrays of num_seqs+1 non-decreasing offsets
  * starting at 0; total_q / total_k are the packed row counts (= last offset),
  * max_seqlen_q / max_seqlen_k bound every sequence's length; batch and the
- * batch strides are ignored. Work scheduling (the tile scheduler for
+ * batch strides are ignored. The last tile of a sequence also reads the rows
+ * behind its end, with weight zero, so an infinity or NaN in one sequence's
+ * rows can reach the sequence before it (0 x NaN is NaN); a buffer with spare
+ * rows is passed as its used part. Work scheduling (the tile scheduler for
  * variable-length balance of newton wiki "FlashAttention-4", 核心技術): when
  * max_seqlen_q <= 2047 x 256 (forward), or max_seqlen_q and max_seqlen_k <=
  * 2047 x 128 (backward, per kernel), the call first builds on the stream, in

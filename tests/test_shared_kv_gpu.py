@@ -220,3 +220,69 @@ def test_rows_behind_the_last_sequence_stay(ea):
     assert torch.all(o[160:] == 3) and torch.all(lse[:, 160:] == 7)
     for g in grads:
         assert torch.all(g[160:] == 5) and not torch.any(g[:160] == 5)
+
+
+@pytest.mark.parametrize("dims,heads", [((64, 64), (4, 2)), ((128, 128), (8, 1)), ((192, 128), (6, 2)), ((128, 128), (2, 2))])
+@pytest.mark.parametrize("keep", [False, True])
+def test_a_captured_step_follows_the_lengths(ea, dims, heads, keep):
+    """Forward and backward of packed sequences captured once and replayed with other offsets; keep: while the eager
+    graph of the same leaves is alive."""
+    total, n, max_len = 600, 4, 600
+    q, k, v, do, cu, _ = _packed([total], [total], *heads, dims, seed=141)
+    cu = torch.tensor([0, 100, 100, 333, total], dtype=torch.int32, device="cuda")
+    leaf = [x.requires_grad_() for x in (q, k, v)]
+
+    def step():
+        o = ea.attention_varlen(*leaf, cu, cu, max_len, max_len, causal=True, deterministic=True)
+        return o, torch.autograd.grad(o, leaf, do, retain_graph=keep)
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        eager = step()
+    torch.cuda.current_stream().wait_stream(side)
+    if not keep:
+        del eager
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = step()
+    for offs in ([0, 100, 100, 333, 600], [0, 600, 600, 600, 600], [0, 1, 130, 257, 600], [0, 0, 64, 128, 600]):
+        cu.copy_(torch.tensor(offs, dtype=torch.int32))
+        graph.replay()
+        want = step()
+        torch.cuda.synchronize()
+        ea.attn_get_device_status()
+        assert torch.equal(got[0], want[0])
+        for a, b in zip(got[1], want[1]):
+            assert torch.equal(a, b)
+    with torch.no_grad():
+        check = [x.detach() for x in leaf]
+    lens = np.diff(cu.tolist())
+    _check_packed(ea, (*check, do, cu, cu), [int(x) for x in lens], [int(x) for x in lens], True)
+
+
+def test_two_steps_at_once(ea):
+    """Packed forward and backward of shared heads on two streams, over and over: the same bits as alone."""
+    lens = [[300, 17, 512], [64] * 12]
+    t = [_packed(x, x, 8, 2, (128, 128), seed=151 + i) for i, x in enumerate(lens)]
+
+    def step(i):
+        q, k, v, do, cu, _ = t[i]
+        m = max(lens[i])
+        o, lse = ea.attn_fwd_varlen(q, k, v, cu, cu, m, m, causal=True)
+        return o, lse, *ea.attn_bwd_varlen(q, k, v, o, lse, do, cu, cu, m, m, causal=True, deterministic=True)
+
+    want = [step(i) for i in (0, 1)]
+    streams = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(10):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got[i].append(step(i))
+    torch.cuda.synchronize()
+    ea.attn_get_device_status()
+    for i in (0, 1):
+        for g in got[i]:
+            assert all(torch.equal(a, b) for a, b in zip(g, want[i]))

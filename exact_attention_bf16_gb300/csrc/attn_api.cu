@@ -369,7 +369,8 @@ attn_status_t run_fwd(const attn_fwd_params* p, bool varlen, cudaStream_t stream
   if (p->cta_pair && (p->d_qk != 128 || p->d_v != 128 || f8 || p->exp2_emu_period != 0 ||
                       p->score_mod != ATTN_SCORE_NONE || sp.kv_count != nullptr || diag_limit))
     return ATTN_ERR_UNSUPPORTED;
-  if (shared_kv(p) && (p->cta_pair || sp.kv_count != nullptr || diag_limit)) return ATTN_ERR_UNSUPPORTED;
+  if (shared_kv(p) && (p->cta_pair || sp.kv_count != nullptr || diag_limit || p->heads >= 65536))
+    return ATTN_ERR_UNSUPPORTED;  // heads: FwdArgs::kv_inv is exact below
   const int hkv = kv_heads(p);
   const int nq_rows = varlen ? p->total_q : p->seqlen_q;
   const int nk_rows = varlen ? p->total_k : p->seqlen_k;
@@ -395,6 +396,7 @@ attn_status_t run_fwd(const attn_fwd_params* p, bool varlen, cudaStream_t stream
   a.batch = varlen ? 1 : p->batch;
   a.heads = p->heads;
   a.kv_group = p->heads / hkv;
+  a.kv_inv = ((uint64_t{1} << 32) + static_cast<uint64_t>(a.kv_group) - 1) / static_cast<uint64_t>(a.kv_group);
   a.seqlen_q = varlen ? p->total_q : p->seqlen_q;
   a.seqlen_k = varlen ? p->total_k : p->seqlen_k;
   a.lse_sb = varlen ? 0 : static_cast<int64_t>(p->heads) * p->seqlen_q;
@@ -631,7 +633,8 @@ attn_status_t run_bwd(const attn_bwd_params* p, void* ws, size_t ws_bytes, bool 
   if (p->single_pass && (f.d_qk != 64 || f.d_v != 64 || sp.kv_count || f.score_mod != ATTN_SCORE_NONE ||
                          p->cta_pair))
     return ATTN_ERR_UNSUPPORTED;
-  if (shared_kv(&f) && (p->cta_pair || p->single_pass || sp.kv_count)) return ATTN_ERR_UNSUPPORTED;
+  if (shared_kv(&f) && (p->cta_pair || p->single_pass || sp.kv_count || f.heads >= 65536))
+    return ATTN_ERR_UNSUPPORTED;
   const int hkv = kv_heads(&f);
   const int nq_rows = varlen ? f.total_q : f.seqlen_q;
   const int nk_rows = varlen ? f.total_k : f.seqlen_k;

@@ -97,6 +97,9 @@ struct Bars {
 };
 
 __device__ __forceinline__ int ceil_div(int a, int b) { return (a + b - 1) / b; }
+__device__ __forceinline__ int kv_head(const FwdArgs& a, int h) {
+  return static_cast<int>((static_cast<uint64_t>(static_cast<uint32_t>(h)) * a.kv_inv) >> 32);
+}
 
 // V (and so P) in fp16 for this call: a copy was made and every value fit.
 __device__ __forceinline__ bool v_is_f16(const FwdArgs& a) { return a.v16_flag != nullptr && __ldg(a.v16_flag) == 0u; }
@@ -267,7 +270,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int kb0 = key_block(0);
           mbar_arrive_expect_tx(&bar->kv_full[0], C::K_BYTES);
           for (int c = 0; c < C::QCH; ++c)
-            tma_load_4d(sKV + c * kChunk, &tmk, &bar->kv_full[0], c * C::QX, h / a.kv_group, k_start + kb0 * BN, b);
+            tma_load_4d(sKV + c * kChunk, &tmk, &bar->kv_full[0], c * C::QX, kv_head(a, h), k_start + kb0 * BN, b);
         }
       }
     }
@@ -295,7 +298,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       tma_prefetch_desc(&tmk);
-      const int hk = h / a.kv_group;  // the K/V head of this query head
+      const int hk = kv_head(a, h);  // the K/V head of this query head
       // read while the Q copies fly: V from the fp16 copy, or the bf16 original
       const CUtensorMap* tmvv = v_is_f16(a) ? &tmv16 : &tmv;
       tma_prefetch_desc(tmvv);

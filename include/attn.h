@@ -195,7 +195,8 @@ typedef struct attn_fwd_params {
    * query heads that share them, accumulated in fp32 and rounded once. Shared
    * heads work with the dense and the variable-length forward and backward,
    * score modifications, E4M3 inputs and split keys; cta_pair, single_pass,
-   * the block-sparse pair and the diagnostic give ATTN_ERR_UNSUPPORTED. */
+   * the block-sparse pair, the diagnostic and 65536 or more heads give
+   * ATTN_ERR_UNSUPPORTED. */
   int32_t heads_kv;
 } attn_fwd_params;
 

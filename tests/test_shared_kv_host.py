@@ -90,3 +90,21 @@ def test_gradients_of_shared_heads_match_differences():
             num[i] = (up - loss(q, k, v)) / (2 * eps)
             x[i] = keep
         assert np.abs(num - got[name]).max() < 1e-8, name
+
+
+def test_too_many_heads_to_share_are_refused(abi):
+    lib = abi.load()
+    assert lib.attn_fwd(ctypes.byref(_params(abi, heads=65536, heads_kv=2)), None, 0, None) == UNSUPPORTED
+    assert lib.attn_bwd(ctypes.byref(_bwd(abi, heads=65536, heads_kv=2)), None, 0, None) == UNSUPPORTED
+
+
+def test_the_kv_head_by_multiplication_is_the_quotient():
+    """h * ceil(2^32 / g) >> 32 = h // g for every h < 65536 and group g <= 65535 (the forward's form of it): the
+    smallest and largest head of every quotient, where a product could first fall on the wrong side."""
+    import numpy as np
+    for g in list(range(1, 300)) + [511, 1000, 4095, 21845, 32767, 32768, 65535]:
+        inv = ((1 << 32) + g - 1) // g
+        q = np.arange(0, 65536 // g + 1, dtype=np.uint64)
+        for h in (q * np.uint64(g), q * np.uint64(g) + np.uint64(g - 1)):
+            h = h[h < 65536]
+            assert np.array_equal((h * np.uint64(inv)) >> np.uint64(32), h // np.uint64(g))

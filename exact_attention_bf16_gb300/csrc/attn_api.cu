@@ -767,7 +767,15 @@ attn_status_t run_bwd(const attn_bwd_params* p, void* ws, size_t ws_bytes, bool 
   auto mark = [&](int i) -> cudaError_t {
     return p->phase_events[i] ? cudaEventRecord(static_cast<cudaEvent_t>(p->phase_events[i]), stream) : cudaSuccess;
   };
-  e = launch_bwd_preprocess(f.d_v, a, stream);
+  if ((varlen ? f.max_seqlen_k : f.seqlen_k) <= kFewKeys && sp.kv_count == nullptr) {
+    auto bf = [](const void* x) { return static_cast<const __nv_bfloat16*>(x); };
+    const FewKeys t{bf(f.q), bf(f.k), bf(f.v), varlen ? 0 : f.q_batch_stride, f.q_row_stride, f.q_head_stride,
+                    varlen ? 0 : f.k_batch_stride, f.k_row_stride, f.k_head_stride,
+                    varlen ? 0 : f.v_batch_stride, f.v_row_stride, f.v_head_stride};
+    e = launch_bwd_few_keys_dsum(f.d_qk, f.d_v, a, t, stream);
+  } else {
+    e = launch_bwd_preprocess(f.d_v, a, stream);
+  }
   if (e == cudaSuccess && sp.kv_count) e = launch_bwd_transpose_lists(a, n_kb_sparse, stream);
   if (e == cudaSuccess) e = mark(0);
   if (e != cudaSuccess) return cuda_fail(e, "bwd preprocess launch");

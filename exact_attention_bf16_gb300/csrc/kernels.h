@@ -296,6 +296,13 @@ cudaError_t launch_bwd_single_pass(const CUtensorMap& tq, const CUtensorMap& tk,
 cudaError_t launch_bwd_dq_convert(const BwdArgs& a, int d, cudaStream_t stream);
 // D = rowsum(dO * O) into args.dsum.
 cudaError_t launch_bwd_preprocess(int d_v, const BwdArgs& a, cudaStream_t stream);
+// The same D from q, k, v, dO and the LSE, for calls whose rows see few keys (no block lists).
+constexpr int kFewKeys = 8;
+struct FewKeys {
+  const __nv_bfloat16 *q, *k, *v;
+  int64_t q_sb, q_sn, q_sh, k_sb, k_sn, k_sh, v_sb, v_sn, v_sh;
+};
+cudaError_t launch_bwd_few_keys_dsum(int d_qk, int d_v, const BwdArgs& a, const FewKeys& t, cudaStream_t stream);
 // dK, dV (KV-stationary) and dQ (Q-stationary). Maps: q, k, v, dO. With
 // a.kv_count set they walk the block-sparse lists (dense layout only).
 cudaError_t launch_bwd_dkdv(int d_qk, int d_v, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,

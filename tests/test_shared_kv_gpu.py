@@ -286,3 +286,48 @@ def test_two_steps_at_once(ea):
     for i in (0, 1):
         for g in got[i]:
             assert all(torch.equal(a, b) for a, b in zip(g, want[i]))
+
+
+@pytest.mark.parametrize("dims", [(64, 64), (128, 128), (192, 128)])
+@pytest.mark.parametrize("heads", [(4, 4), (8, 2)])
+@pytest.mark.parametrize("lens_q,lens_k", [([1, 2] * 20, [1, 2] * 20), ([2, 0, 1, 3] * 8, [1, 5, 8, 0] * 8),
+                                           ([8, 5, 1, 4] * 6, [8, 5, 1, 4] * 6)])
+@pytest.mark.parametrize("causal", [True, False])
+def test_gradients_of_short_sequences(ea, dims, heads, lens_q, lens_k, causal):
+    """Few keys a row: dS = P (dP - D) loses by cancellation what D is off by. With D in fp32, dQ and dK carry the
+    independent roundings of dS and of themselves to bf16, each at most 2^-8 of a value, evenly spread, so 2^-8 / sqrt(3)
+    of the norm: together sqrt(2) 2^-8 / sqrt(3) = 3.2e-3 at most; 5% on top for the spread of some thousands of
+    values. dV likewise from P and itself."""
+    q, k, v, do, cq, ck = _packed(lens_q, lens_k, *heads, dims, seed=161)
+    scale = dims[0] ** -0.5
+    o, lse = ea.attn_fwd_varlen(q, k, v, cq, ck, max(lens_q), max(lens_k), causal=causal)
+    grads = ea.attn_bwd_varlen(q, k, v, o, lse, do, cq, ck, max(lens_q), max(lens_k), causal=causal)
+    torch.cuda.synchronize()
+    ea.attn_get_device_status()
+    a = b = 0
+    ref = [np.zeros(x.shape) for x in (q, k, v)]
+    for lq, lk in zip(lens_q, lens_k):
+        if lq and lk:
+            x = [to64(t) for t in (q[a:a + lq], k[b:b + lk], v[b:b + lk], do[a:a + lq])]
+            r = shared_bwd(*x, scale, causal)
+            ref[0][a:a + lq], ref[1][b:b + lk], ref[2][b:b + lk] = r["dq"], r["dk"], r["dv"]
+        a, b = a + lq, b + lk
+    for name, g, want in zip(("dq", "dk", "dv"), grads, ref):
+        err = np.linalg.norm(to64(g) - want) / np.linalg.norm(want)
+        assert err <= 1.05 * np.sqrt(2 / 3) * 2.0 ** -8, (name, err)
+
+
+@pytest.mark.parametrize("mod", ["softcap", "alibi"])
+@pytest.mark.parametrize("nk", [1, 7, 8, 9])
+def test_dense_rows_of_few_keys(ea, mod, nk):
+    q, k, v, do = (_draw(2, n, h, 64, seed=171 + n + h) for n, h in ((40, 4), (nk, 2), (nk, 2), (40, 4)))
+    slopes = torch.tensor([0.4, 0.01, 0.1, 0.0], dtype=torch.float32, device="cuda")
+    kw = dict(softcap=2.0) if mod == "softcap" else dict(alibi_slopes=slopes)
+    score_mod = ("softcap", 2.0) if mod == "softcap" else ("alibi", slopes.double().cpu().numpy())
+    o, lse = ea.attn_fwd(q, k, v, causal=True, **kw)
+    grads = ea.attn_bwd(q, k, v, o, lse, do, causal=True, **kw)
+    torch.cuda.synchronize()
+    ea.attn_get_device_status()
+    refs = [shared_bwd(*(to64(x[i]) for x in (q, k, v, do)), 0.125, True, score_mod) for i in range(2)]
+    check_grads(dict(zip(("dq", "dk", "dv"), grads)), {n: np.stack([r[n] for r in refs]) for n in ("dq", "dk", "dv")},
+                f"{nk} keys")

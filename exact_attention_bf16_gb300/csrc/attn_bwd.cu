@@ -13,7 +13,7 @@ namespace bwd {
 // 16-byte boundaries, as the TMA tensor maps already require).
 // ===========================================================================
 template <int DV>
-__global__ void preprocess_kernel(const BwdArgs a) {
+__global__ void __launch_bounds__(256, 8) preprocess_kernel(const BwdArgs a) {
   constexpr int LPR = DV / 8;    // lanes per row
   constexpr int RPW = 32 / LPR;  // rows per warp
   const int64_t rows = static_cast<int64_t>(a.batch) * a.seqlen_q * a.heads;
@@ -47,47 +47,41 @@ __global__ void preprocess_kernel(const BwdArgs a) {
     for (int s = LPR / 2; s > 0; s >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, s);
     if (r < rows && l == 0) a.dsum[b * a.lse_sb + h * a.lse_sh + i] = acc;
   }
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // behind the tile lists' kernel: over before this one is
 }
 
 
 
-// D of a call whose rows see few keys, as sum_j P_ij (dO_i . v_j) with P from the LSE, all in fp32. The same number in
-// exact arithmetic, but O comes rounded to bf16, and its error d is the same in all dS_ij = P_ij (dO_i . v_j - D_i): dQ_i
-// is off by d sum_j P_ij k_j, up to 2^-9 |dO_i| |O_i| beside a dQ_i that shrinks as the keys' v_j differ less from their
-// mean O_i. Over sequences of one and two tokens dQ and dK came out 5.0e-3 from the exact ones (norms), now below 2.9e-3;
-// from 9 keys on it is at most 3.1e-3 from the rounded O, too. Latency-bound: 8 lanes share a row, one key each at a time.
+// D of packed sequences that all have few keys, as sum_j P_ij (dO_i . v_j) with P from the LSE, all in fp32. The same
+// number in exact arithmetic, but O comes rounded to bf16, and its error d is the same in all dS_ij =
+// P_ij (dO_i . v_j - D_i): dQ_i is off by d sum_j P_ij k_j, d up to 2^-9 |dO_i| |O_i|, beside a dQ_i that shrinks as the
+// v_j of its keys differ less from their mean O_i. Over sequences of one and two tokens dQ and dK came out 5.0e-3 from the
+// exact ones (norms), now below 2.9e-3; from 9 keys on it is at most 3.1e-3 from the rounded O, too. (A choice per
+// sequence, in the pass above, cost the rows of longer ones 40% of its time.) Latency-bound: 8 lanes share a row, one key
+// each at a time.
 template <int DQK, int DV, int MOD>
 __global__ void few_keys_dsum_kernel(const BwdArgs a, const FewKeys t) {
-  const int64_t rows = static_cast<int64_t>(a.batch) * a.seqlen_q * a.heads;
+  const int64_t rows = static_cast<int64_t>(a.seqlen_q) * a.heads;
   const int64_t r = (blockIdx.x * static_cast<int64_t>(blockDim.x) + threadIdx.x) >> 3;
   const int l = static_cast<int>(threadIdx.x & 7u);
   float acc = 0.f;
-  int h = 0, i = 0, b = 0;
+  const int i = static_cast<int>(r / a.heads), h = static_cast<int>(r % a.heads);
   bool mine = r < rows;
   if (mine) {
-    h = static_cast<int>(r % a.heads);
-    i = static_cast<int>((r / a.heads) % a.seqlen_q);
-    b = static_cast<int>(r / a.heads / a.seqlen_q);
-    int qi = i, nq = a.seqlen_q, nk = a.seqlen_k, k_start = 0;
-    if (a.cu_q != nullptr) {  // the sequence of row i: the last one that begins at or before it
-      int s = 0;
-      for (int e = a.num_units; s + 1 < e;) {
-        const int m = (s + e) / 2;
-        if (a.cu_q[m] <= i) s = m;
-        else e = m;
-      }
-      qi = i - a.cu_q[s];
-      nq = a.cu_q[s + 1] - a.cu_q[s];
-      k_start = a.cu_k[s];
-      nk = a.cu_k[s + 1] - k_start;
-      // rows of no sequence are not read later either; offsets past the tensors are not followed
-      mine = qi >= 0 && qi < nq && k_start >= 0 && k_start + nk <= a.seqlen_k;
+    int s = 0;  // the sequence of row i: the last one that begins at or before it
+    for (int e = a.num_units; s + 1 < e;) {
+      const int m = (s + e) / 2;
+      if (a.cu_q[m] <= i) s = m;
+      else e = m;
     }
-    const float lse = mine ? a.lse[b * a.lse_sb + h * a.lse_sh + i] : -INFINITY;
-    const int pos = qi + nk - nq;
+    const int q_end = a.cu_q[s + 1], k_start = a.cu_k[s], nk = a.cu_k[s + 1] - k_start;
+    // rows of no sequence are not read later either; offsets past the tensors are not followed
+    mine = i >= a.cu_q[s] && i < q_end && k_start >= 0 && k_start + nk <= a.seqlen_k;
+    const int pos = i - q_end + nk;  // the row's position among the keys
+    const float lse = mine ? a.lse[h * a.lse_sh + i] : -INFINITY;
     const int keys = lse == -INFINITY ? 0 : (a.causal ? min(nk, pos + 1) : nk);
-    const __nv_bfloat16* q = t.q + b * t.q_sb + i * t.q_sn + h * t.q_sh;
-    const __nv_bfloat16* g = static_cast<const __nv_bfloat16*>(a.dout) + b * a.do_sb + i * a.do_sn + h * a.do_sh;
+    const __nv_bfloat16* q = t.q + i * t.q_sn + h * t.q_sh;
+    const __nv_bfloat16* g = static_cast<const __nv_bfloat16*>(a.dout) + i * a.do_sn + h * a.do_sh;
     const int hk = h / a.kv_group;
     auto dot = [](const __nv_bfloat16* x, const __nv_bfloat16* y, int n) {
       float2 sum = make_float2(0.f, 0.f);
@@ -106,16 +100,17 @@ __global__ void few_keys_dsum_kernel(const BwdArgs a, const FewKeys t) {
     };
     for (int j = l; j < keys; j += 8) {
       const int64_t row = k_start + j;
-      float s = dot(q, t.k + b * t.k_sb + row * t.k_sn + hk * t.k_sh, DQK);
-      if (MOD == kModSoftcap) s = a.mod_b * tanh_scaled(s, a.mod_k2);
-      if (MOD == kModAlibi) s -= fabsf(a.alibi_slopes[h] * a.inv_scale * static_cast<float>(j - pos));
-      const float p = exp2f(fmaf(s, a.scale_log2, -lse * 1.4426950408889634f));
-      acc = fmaf(p, dot(g, t.v + b * t.v_sb + row * t.v_sn + hk * t.v_sh, DV), acc);
+      float x = dot(q, t.k + row * t.k_sn + hk * t.k_sh, DQK);
+      if (MOD == kModSoftcap) x = a.mod_b * tanh_scaled(x, a.mod_k2);
+      if (MOD == kModAlibi) x -= fabsf(a.alibi_slopes[h] * a.inv_scale * static_cast<float>(j - pos));
+      const float p = exp2f(fmaf(x, a.scale_log2, -lse * 1.4426950408889634f));
+      acc = fmaf(p, dot(g, t.v + row * t.v_sn + hk * t.v_sh, DV), acc);
     }
   }
 #pragma unroll
-  for (int s = 4; s > 0; s >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, s);
-  if (mine && l == 0) a.dsum[b * a.lse_sb + h * a.lse_sh + i] = acc;
+  for (int d = 4; d > 0; d >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, d);
+  if (mine && l == 0) a.dsum[h * a.lse_sh + i] = acc;
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // as in preprocess_kernel
 }
 
 // Zero rows: dQ (all queries) and/or dK, dV (all keys).
@@ -164,25 +159,28 @@ __global__ void transpose_lists_kernel(BwdArgs a, int n_kb, int n_sets) {
 
 }  // namespace bwd
 
-cudaError_t launch_bwd_preprocess(int d_v, const BwdArgs& a, cudaStream_t stream) {
+cudaError_t launch_bwd_preprocess(int d_v, const BwdArgs& a, bool early, cudaStream_t stream) {
   const int64_t rows = static_cast<int64_t>(a.batch) * a.seqlen_q * a.heads;
   if (rows == 0) return cudaSuccess;
   const int64_t per_block = 8 * (d_v == 64 ? 4 : 2);  // 8 warps, each 32 / (d_v / 8) rows per pass
   const int64_t want = (rows + per_block - 1) / per_block;
   const int64_t blocks = want < 16384 ? want : 16384;
-  if (d_v == 64) bwd::preprocess_kernel<64><<<static_cast<unsigned>(blocks), 256, 0, stream>>>(a);
-  else if (d_v == 128) bwd::preprocess_kernel<128><<<static_cast<unsigned>(blocks), 256, 0, stream>>>(a);
-  else return cudaErrorInvalidValue;
+  if (d_v != 64 && d_v != 128) return cudaErrorInvalidValue;
+  auto kern = d_v == 64 ? bwd::preprocess_kernel<64> : bwd::preprocess_kernel<128>;
+  if (early) return launch_early(kern, dim3(static_cast<unsigned>(blocks)), 256, 0, stream, a);
+  kern<<<static_cast<unsigned>(blocks), 256, 0, stream>>>(a);
   return cudaGetLastError();
 }
 
-cudaError_t launch_bwd_few_keys_dsum(int d_qk, int d_v, const BwdArgs& a, const FewKeys& t, cudaStream_t stream) {
-  const int64_t rows = static_cast<int64_t>(a.batch) * a.seqlen_q * a.heads;
+cudaError_t launch_bwd_few_keys_dsum(int d_qk, int d_v, const BwdArgs& a, const FewKeys& t, bool early,
+                                     cudaStream_t stream) {
+  const int64_t rows = static_cast<int64_t>(a.seqlen_q) * a.heads;
   if (rows == 0) return cudaSuccess;
   const int64_t blocks = (rows + 31) / 32;
   if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
   auto with_mod = [&](auto none, auto softcap, auto alibi) {
     auto k = a.score_mod == kModNone ? none : a.score_mod == kModSoftcap ? softcap : alibi;
+    if (early) return launch_early(k, dim3(static_cast<unsigned>(blocks)), 256, 0, stream, a, t);
     k<<<static_cast<unsigned>(blocks), 256, 0, stream>>>(a, t);
     return cudaGetLastError();
   };

@@ -152,6 +152,8 @@ __global__ void v_to_f16_kernel(const void* v, int64_t sb, int64_t sn, int64_t s
       dst[i] = make_uint4(o[0], o[1], o[2], o[3]);
     }
   }
+  // Behind a tile list's kernel, which zeroes the flag and whose lists the next kernel reads: over before this one is.
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   if (__any_sync(0xffffffffu, bad != 0) && lane == 0) atomicOr(flag, 1u);
 }
 
@@ -188,14 +190,15 @@ cudaError_t launch_fwd_diag_timeout(const CUtensorMap& tq, const CUtensorMap& tk
 }
 
 cudaError_t launch_v_to_f16(const void* v, int64_t sb, int64_t sn, int64_t sh, int nb, int nrows, int heads, int dv,
-                            void* out, uint32_t* flag, cudaStream_t stream) {
+                            void* out, uint32_t* flag, bool early, cudaStream_t stream) {
   const int64_t rows = static_cast<int64_t>(nb) * nrows;
   if (rows == 0) return cudaSuccess;
   const int64_t want = (rows + 7) / 8;  // 8 warps (rows) per block and pass
   const unsigned blocks = static_cast<unsigned>(want < 152 * 8 ? want : 152 * 8);
-  if (dv == 64) fwd::v_to_f16_kernel<64><<<blocks, 256, 0, stream>>>(v, sb, sn, sh, nb, nrows, heads, out, flag);
-  else if (dv == 128) fwd::v_to_f16_kernel<128><<<blocks, 256, 0, stream>>>(v, sb, sn, sh, nb, nrows, heads, out, flag);
-  else return cudaErrorInvalidValue;
+  if (dv != 64 && dv != 128) return cudaErrorInvalidValue;
+  auto kern = dv == 64 ? fwd::v_to_f16_kernel<64> : fwd::v_to_f16_kernel<128>;
+  if (early) return launch_early(kern, dim3(blocks), 256, 0, stream, v, sb, sn, sh, nb, nrows, heads, out, flag);
+  kern<<<blocks, 256, 0, stream>>>(v, sb, sn, sh, nb, nrows, heads, out, flag);
   return cudaGetLastError();
 }
 

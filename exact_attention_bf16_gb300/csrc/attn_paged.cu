@@ -751,24 +751,6 @@ __global__ void __launch_bounds__(kListThreads, 1) chunk_list_kernel(const Paged
   }
 }
 
-// A kernel that may be launched before the one ahead of it on the stream is over (it
-// waits with griddepcontrol.wait before it reads that kernel's results).
-template <typename K, typename... A>
-cudaError_t launch_early(K kern, dim3 grid, int threads, int smem, cudaStream_t stream, const A&... args) {
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3(threads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = stream;
-  cudaLaunchAttribute at{};
-  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &at;
-  cfg.numAttrs = 1;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, args...);
-  return e != cudaSuccess ? e : cudaGetLastError();
-}
-
 template <int DQK, int DV, int MOD, bool EVEN>
 cudaError_t launch_main(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const PagedArgs& a, int ctas,
                         cudaStream_t stream) {

@@ -99,6 +99,24 @@ inline int group_count(int n_pairs, int64_t bytes_per_pair) {
   return static_cast<int>((n_pairs + g - 1) / g);
 }
 
+// A kernel that may be launched before the one ahead of it on the stream is over (it
+// waits with griddepcontrol.wait before it reads that kernel's results).
+template <typename K, typename... A>
+cudaError_t launch_early(K kern, dim3 grid, int threads, int smem, cudaStream_t stream, const A&... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute at{};
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, args...);
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
 // Builds up to two lists for num_seqs sequences (cu_q / cu_k offsets on the device):
 // sequences with the most blocks first (by key blocks when by_keys), then
 // head by head, blocks of a head in descending or ascending order. Writes
@@ -192,8 +210,9 @@ cudaError_t launch_fwd_mod(int d_qk, int d_v, const CUtensorMap& tq, const CUten
 // fp16 copy of V (contiguous [nb, nrows, heads, dv]) for the forward's PV
 // product; ORs 1 into *flag (zeroed by the caller) if a finite value is out of
 // fp16's range.
+// early: behind launch_tile_lists, whose kernel it runs beside (it waits before it sets the flag and before it ends).
 cudaError_t launch_v_to_f16(const void* v, int64_t sb, int64_t sn, int64_t sh, int nb, int nrows, int heads, int dv,
-                            void* out, uint32_t* flag, cudaStream_t stream);
+                            void* out, uint32_t* flag, bool early, cudaStream_t stream);
 
 // Block-sparse forward (dense layout, cu_q == nullptr, emu_period == 0): the
 // same kernel walking a.kv_index's key blocks instead of 0 .. nkv-1.
@@ -294,15 +313,16 @@ struct BwdArgs {
 cudaError_t launch_bwd_single_pass(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                                    const CUtensorMap& tdo, const BwdArgs& a, cudaStream_t stream);
 cudaError_t launch_bwd_dq_convert(const BwdArgs& a, int d, cudaStream_t stream);
-// D = rowsum(dO * O) into args.dsum.
-cudaError_t launch_bwd_preprocess(int d_v, const BwdArgs& a, cudaStream_t stream);
-// The same D from q, k, v, dO and the LSE, for calls whose rows see few keys (no block lists).
+// D = rowsum(dO * O) into args.dsum. early: behind launch_tile_lists, whose kernel it runs beside.
+cudaError_t launch_bwd_preprocess(int d_v, const BwdArgs& a, bool early, cudaStream_t stream);
+// The same D from q, k, v, dO and the LSE, for packed sequences of at most kFewKeys keys.
 constexpr int kFewKeys = 8;
 struct FewKeys {
   const __nv_bfloat16 *q, *k, *v;
-  int64_t q_sb, q_sn, q_sh, k_sb, k_sn, k_sh, v_sb, v_sn, v_sh;
+  int64_t q_sn, q_sh, k_sn, k_sh, v_sn, v_sh;
 };
-cudaError_t launch_bwd_few_keys_dsum(int d_qk, int d_v, const BwdArgs& a, const FewKeys& t, cudaStream_t stream);
+cudaError_t launch_bwd_few_keys_dsum(int d_qk, int d_v, const BwdArgs& a, const FewKeys& t, bool early,
+                                     cudaStream_t stream);
 // dK, dV (KV-stationary) and dQ (Q-stationary). Maps: q, k, v, dO. With
 // a.kv_count set they walk the block-sparse lists (dense layout only).
 cudaError_t launch_bwd_dkdv(int d_qk, int d_v, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,

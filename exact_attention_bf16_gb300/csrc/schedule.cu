@@ -20,6 +20,7 @@
 // affects only scheduling, never a result.
 #include <cuda_runtime.h>
 
+#include <cstddef>
 #include <cstdint>
 
 #include "kernels.h"
@@ -34,6 +35,7 @@ constexpr int kSharedSeqs = 1024;  // up to so many sequences need no scratch in
 __global__ void __launch_bounds__(kThreads, 1)
     tile_list_kernel(const int* cu_q, const int* cu_k, int num_seqs, TileListSpec l0, TileListSpec l1,
                      int64_t* scratch, uint32_t* zero_word) {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the next kernel reads no list
   const TileListSpec& l = blockIdx.x == 0 ? l0 : l1;
   const int heads = l.heads, rows_per_block = l.rows_per_block, by_keys = l.by_keys, descending = l.descending,
             max_nblk = l.max_nblk;
@@ -96,29 +98,28 @@ __global__ void __launch_bounds__(kThreads, 1)
     seq_start[s] = n > 0 ? bin_start[n] + static_cast<long long>(atomicAdd(&bins[n], 1)) * n * heads : -1;
   }
   __syncthreads();
+  // few sequences: several warps each; two lanes per entry, 16 bytes each
+  constexpr int kWarps = kThreads / 32;
+  const int team = num_seqs < kWarps ? kWarps / max(num_seqs, 1) : 1;
   const int lane = tid & 31, warp = tid >> 5;
-  for (int s = warp; s < num_seqs; s += kThreads / 32) {
+  for (int s = warp / team; s < num_seqs; s += kWarps / team) {
     const long long st = seq_start[s];
     if (st < 0) continue;
     const int n = nblk_of(s);
-    TileEntry e;
-    e.q_start = cu_q[s];
-    e.nq = cu_q[s + 1] - e.q_start;
-    e.k_start = cu_k[s];
-    e.nk = cu_k[s + 1] - e.k_start;
-    e.seq = s;
-    e.pad = 0;
-    for (int i = lane; i < n * heads && st + i < bound; i += 32) {  // bound: offsets that overrun total rows
+    const int q_start = cu_q[s], k_start = cu_k[s];
+    const int4 rows = make_int4(q_start, cu_q[s + 1] - q_start, k_start, cu_k[s + 1] - k_start);
+    static_assert(offsetof(TileEntry, head) == 16 && offsetof(TileEntry, seq) == 24, "an entry's two halves");
+    for (int u = warp % team * 32 + lane; u < 2 * n * heads; u += team * 32) {
+      const int i = u >> 1;
+      if (st + i >= bound) break;  // offsets that overrun total rows
       const int h = i / n, k = i % n;
-      e.head = h;
-      e.blk = descending ? n - 1 - k : k;
-      out[st + i] = e;
+      reinterpret_cast<int4*>(out)[2 * (st + i) + (u & 1)] =
+          (u & 1) ? make_int4(h, descending ? n - 1 - k : k, s, 0) : rows;
     }
   }
   for (long long i = total + tid; i < bound; i += kThreads) {
-    TileEntry z{};
-    z.seq = -1;
-    out[i] = z;
+    reinterpret_cast<int4*>(out)[2 * i] = make_int4(0, 0, 0, 0);
+    reinterpret_cast<int4*>(out)[2 * i + 1] = make_int4(0, 0, -1, 0);
   }
 }
 

@@ -936,7 +936,8 @@ attn_status_t check_paged(const attn_paged_params* p) {
 struct PagedPlan {
   bool even = true;
   int tile_tokens = 0, part_rows = 0;
-  int decode_rows = 0, q_box_tokens = 0;
+  bool decode = false;
+  int q_box_tokens = 0;
   int64_t items = 0;
   size_t off_lse = 0, off_merge = 0, off_list = 0, off_items = 0, bytes = 0;
 };
@@ -945,11 +946,10 @@ PagedPlan paged_plan(const attn_paged_params* p) {
   const int group = p->heads / p->heads_kv;
   pl.tile_tokens = 128 / group;
   pl.even = p->max_seqlen_q <= pl.tile_tokens;  // one tile of rows holds any request's queries
-  // up to 64 rows per request and K/V head: rows in the columns of the products (attn_paged_decode.cu)
-  const int64_t rows_q = static_cast<int64_t>(p->max_seqlen_q) * group;
-  if (p->score_mod == ATTN_SCORE_NONE && rows_q <= 64) pl.decode_rows = rows_q <= 16 ? 16 : rows_q <= 32 ? 32 : 64;
-  pl.q_box_tokens = (pl.decode_rows ? pl.decode_rows : 128) / group;
-  pl.part_rows = pl.decode_rows ? pl.decode_rows : pl.even ? 128 : 256;
+  // few rows per request and K/V head: rows in the columns of the products (attn_paged_decode.cu, where both are measured)
+  pl.decode = p->score_mod == ATTN_SCORE_NONE && static_cast<int64_t>(p->max_seqlen_q) * group <= kDecodeRows;
+  pl.q_box_tokens = (pl.decode ? kDecodeRows : 128) / group;
+  pl.part_rows = pl.decode ? kDecodeRows : pl.even ? 128 : 256;
   const int64_t rows = 2ll * kPagedMaxCtas * pl.part_rows;
   pl.off_lse = round256(rows * p->d_v * 4);
   pl.off_merge = pl.off_lse + round256(rows * 4);
@@ -1020,7 +1020,7 @@ attn_status_t run_fwd_paged(const attn_paged_params* p, void* ws, size_t ws_byte
                     p->k_head_stride, box));
   ATTN_TRY(make_map(&tv, p->v_cache, p->d_v, p->heads_kv, p->page_size, p->num_pages, p->v_page_stride, p->v_row_stride,
                     p->v_head_stride, box));
-  e = launch_fwd_paged(p->d_qk, p->d_v, tq, tk, tv, a, pl.even, pl.decode_rows, std::min(sms, kPagedMaxCtas),
+  e = launch_fwd_paged(p->d_qk, p->d_v, tq, tk, tv, a, pl.even, pl.decode, std::min(sms, kPagedMaxCtas),
                        stream);
   return e == cudaSuccess ? ATTN_OK : cuda_fail(e, "paged fwd launch");
 }

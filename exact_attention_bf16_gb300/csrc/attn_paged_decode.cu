@@ -1,5 +1,5 @@
-// attn_fwd_paged for few rows per K/V head (decoding, a few proposed tokens): up to
-// N = 16, 32 or 64 rows (token, head of the group) per request.
+// attn_fwd_paged for few rows per K/V head (decoding): up to N = 16 rows (token, head of
+// the group) per request.
 //
 // The products are taken the other way round than in attn_paged.cu, with the long
 // side in the 128 lanes of an MMA:
@@ -14,7 +14,12 @@
 // sums stay per thread (per key lane) until the end.
 //
 // Bound by HBM: per 128 keys and K/V head at d = 128 64 KB against 16 MMAs of about
-// 50 cycles. Work is the even split of paged_common.cuh; two streams over the even and
+// 50 cycles. 64 requests of up to 32768 tokens, 32 heads over 8, d = 128: 307 us, 6.67 TB/s
+// (98% of a copy's), 321 us by paged_kernel; one of 4100 tokens 14.5 us against 15.5, its
+// launches, first copies and merge. d = 64 (8 heads of their own, 64 requests) reaches 4.1 TB/s
+// against 3.8: a 128-key block is half the bytes for the same waits. With 32 columns the same calls took 341 us where 16 took 323 and
+// paged_kernel 332 (64 requests, 8 heads, d = 128), with 64 columns 416, so 17 rows and more are
+// paged_kernel's. Work is the even split of paged_common.cuh; two streams over the even and
 // the odd key blocks hide the chain S^T -> softmax -> O^T, as there.
 //
 // Warps: 0 work and TMA copies, 1 MMA issue, 4..7 and 8..11 softmax of stream 0 and 1.
@@ -28,16 +33,18 @@ namespace gb300 {
 namespace paged {
 namespace decode {
 
-template <int DQK, int DV, int N>
+constexpr int N = kDecodeRows;
+
+template <int DQK, int DV>
 struct Cfg {
   static constexpr int QCH = DQK / 64, VCH = DV / 64;
   static constexpr int K_BYTES = QCH * kChunk, V_BYTES = VCH * kChunk;
   static constexpr int Q_CHUNK = N * 128, Q_BYTES = QCH * Q_CHUNK;  // 64 columns of N rows
   static constexpr int P_CHUNK = N * 128, P_BYTES = 2 * P_CHUNK;    // 64 keys of N rows; [N][128 keys]
-  static constexpr int NQ = N == 64 ? 1 : 2;  // 2: the next segment's Q is copied while this one's is used
+  static constexpr int NQ = 2;  // the next segment's Q is copied while this one's is used
   // ring slots: what 227 KB hold beside Q and P
   static constexpr int NK = DQK == 64 ? 6 : (DQK == 128 ? 3 : 2);
-  static constexpr int NV = DQK == 64 ? (N == 64 ? 5 : 6) : (DQK == 128 ? (N == 64 ? 2 : 3) : (N == 16 ? 3 : 2));
+  static constexpr int NV = DQK == 64 ? 6 : 3;
   static constexpr int OFF_V = NK * K_BYTES;
   static constexpr int OFF_Q = OFF_V + NV * V_BYTES;
   static constexpr int OFF_P = OFF_Q + NQ * Q_BYTES;
@@ -50,7 +57,7 @@ struct Cfg {
   // TMEM columns: S^T and O^T of the two streams
   static constexpr uint32_t tS(int i) { return N * i; }
   static constexpr uint32_t tO(int i) { return 2 * N + N * i; }
-  static constexpr uint32_t COLS = 4 * N;  // 64, 128 or 256: powers of two
+  static constexpr uint32_t COLS = 4 * N;  // a power of two
   static constexpr int M_O = DV;           // rows of O^T (DV = 64: an M = 64 MMA)
 };
 
@@ -90,65 +97,36 @@ __device__ __forceinline__ void group_sync(int id) {
   asm volatile("barrier.cta.sync.aligned %0, 128;" ::"r"(id) : "memory");
 }
 
-template <int N>
-__device__ __forceinline__ void tmem_ld_cols(uint32_t taddr, uint32_t (&r)[N]) {
-  if constexpr (N >= 32) {
-#pragma unroll
-    for (int c = 0; c < N / 32; ++c) tmem_ld32(taddr + 32 * c, *reinterpret_cast<uint32_t(*)[32]>(&r[32 * c]));
-  } else if constexpr (N == 16) {
-    tmem_ld16(taddr, r);
-  } else {
-    tmem_ld8(taddr, r);
-  }
-}
-template <int N>
-__device__ __forceinline__ void tmem_st_cols(uint32_t taddr, const uint32_t (&r)[N]) {
-  if constexpr (N >= 32) {
-#pragma unroll
-    for (int c = 0; c < N / 32; ++c) tmem_st32(taddr + 32 * c, *reinterpret_cast<const uint32_t(*)[32]>(&r[32 * c]));
-  } else {
-    tmem_st16(taddr, r);
-  }
-}
-
-// Reduces N values per lane over the warp, 32 (or 16) columns at a time, and writes the
-// results to out[0 .. N). At each step a lane keeps one half of its columns and hands over
-// the other: 32 columns cost 31 shuffles, not 160.
-template <int N, typename Op>
+// Reduces 16 values per lane over the warp and writes the results to out[0 .. 16). At each step
+// a lane keeps one half of its columns and hands over the other: 16 shuffles, not 80.
+template <typename Op>
 __device__ __forceinline__ void warp_reduce_cols(const float (&x)[N], uint32_t lane, float* out, Op op) {
-  constexpr int R = N < 32 ? N : 32;
+  static_assert(N == 16, "lanes 2c and 2c + 1 end with the halves of column c");
+  float v[N];
 #pragma unroll
-  for (int c0 = 0; c0 < N; c0 += R) {
-    float v[R];
+  for (int c = 0; c < N; ++c) v[c] = x[c];
 #pragma unroll
-    for (int c = 0; c < R; ++c) v[c] = x[c0 + c];
+  for (int st = 0; (N >> (st + 1)) > 0; ++st) {
+    const int half = N >> (st + 1);
+    const uint32_t bit = 16u >> st;
+    const bool up = (lane & bit) != 0;
 #pragma unroll
-    for (int st = 0; (R >> (st + 1)) > 0; ++st) {
-      const int half = R >> (st + 1);
-      const uint32_t bit = 16u >> st;
-      const bool up = (lane & bit) != 0;
-#pragma unroll
-      for (int c = 0; c < R / 2; ++c) {
-        if (c < half) {
-          const float send = up ? v[c] : v[c + half], keep = up ? v[c + half] : v[c];
-          v[c] = op(keep, __shfl_xor_sync(0xffffffffu, send, bit));
-        }
+    for (int c = 0; c < N / 2; ++c) {
+      if (c < half) {
+        const float send = up ? v[c] : v[c + half], keep = up ? v[c + half] : v[c];
+        v[c] = op(keep, __shfl_xor_sync(0xffffffffu, send, bit));
       }
     }
-    if constexpr (R == 16) {  // lanes 2c and 2c + 1 hold the halves of column c
-      v[0] = op(v[0], __shfl_xor_sync(0xffffffffu, v[0], 1));
-      if ((lane & 1u) == 0) out[lane >> 1] = v[0];
-    } else {
-      out[c0 + lane] = v[0];
-    }
   }
+  v[0] = op(v[0], __shfl_xor_sync(0xffffffffu, v[0], 1));
+  if ((lane & 1u) == 0) out[lane >> 1] = v[0];
 }
 
-template <int DQK, int DV, int N>
+template <int DQK, int DV>
 __global__ void __launch_bounds__(kThreads, 1)
     paged_decode_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUtensorMap tmk,
                         const __grid_constant__ CUtensorMap tmv, const PagedArgs a) {
-  using C = Cfg<DQK, DV, N>;
+  using C = Cfg<DQK, DV>;
   extern __shared__ __align__(1024) uint8_t smem[];
   if ((smem_u32(smem) & 1023u) != 0u) {  // the 128-byte-swizzled tiles need 1024-byte alignment
     if (threadIdx.x == 0) record_error(a.status, DEV_BAD_CONFIG, 0x4000);
@@ -322,7 +300,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         tc_fence_after();
         uint32_t sr[N];
-        tmem_ld_cols<N>(lane_base + C::tS(i), sr);
+        tmem_ld16(lane_base + C::tS(i), sr);
         tmem_wait_ld();
         float s[N];
 #pragma unroll
@@ -353,7 +331,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             ok = false;
             break;
           }
-          warp_reduce_cols<N>(s, lane, sW + quarter * N, [](float x, float y) { return fmaxf(x, y); });
+          warp_reduce_cols(s, lane, sW + quarter * N, [](float x, float y) { return fmaxf(x, y); });
           group_sync(bid);
           if (key_lane < N) {  // one thread per row: the maximum in use is replaced where the block exceeds it enough
             const int c = key_lane;
@@ -365,20 +343,16 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           group_sync(bid);
           if (!fresh) {
-            constexpr int STEP = 16;
+            uint32_t o[N];
+            tmem_ld16(lane_base + C::tO(i), o);
+            tmem_wait_ld();
 #pragma unroll
-            for (int c0 = 0; c0 < N; c0 += STEP) {
-              uint32_t o[STEP];
-              tmem_ld_cols<STEP>(lane_base + C::tO(i) + c0, o);
-              tmem_wait_ld();
-#pragma unroll
-              for (int c = 0; c < STEP; ++c) {
-                const float alpha = sW[c0 + c];
-                l[c0 + c] *= alpha;
-                o[c] = __float_as_uint(__uint_as_float(o[c]) * alpha);
-              }
-              tmem_st_cols<STEP>(lane_base + C::tO(i) + c0, o);
+            for (int c = 0; c < N; ++c) {
+              const float alpha = sW[c];
+              l[c] *= alpha;
+              o[c] = __float_as_uint(__uint_as_float(o[c]) * alpha);
             }
+            tmem_st16(lane_base + C::tO(i), o);
             tmem_wait_st();
           }
           group_sync(bid);
@@ -414,7 +388,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       // ---- output: sums over the key lanes, the two streams merged
       if (ok) {
-        warp_reduce_cols<N>(l, lane, sW + quarter * N, [](float x, float y) { return x + y; });
+        warp_reduce_cols(l, lane, sW + quarter * N, [](float x, float y) { return x + y; });
         __syncwarp();
         if (lane == 0) mbar_arrive(&bar->x_full[i]);
         const uint32_t xp = (w.phase >> 2) & 1u;
@@ -464,20 +438,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         // O^T: lane = column of O (d_v = 64: an M = 64 product, whose row m is in lane 32 (m / 16) + m % 16)
         const bool has_col = DV == 128 || lane < 16;
         const int col = DV == 128 ? key_lane : static_cast<int>(quarter * 16 + lane);
-        constexpr int STEP = HALF < 16 ? 8 : 16;
-#pragma unroll 1
-        for (int c0 = 0; c0 < HALF && i * HALF + c0 < rows; c0 += STEP) {
-          uint32_t o0[STEP], o1[STEP];
-          tmem_ld_cols<STEP>(lane_base + C::tO(0) + i * HALF + c0, o0);  // (columns never written are not used)
-          tmem_ld_cols<STEP>(lane_base + C::tO(1) + i * HALF + c0, o1);
+        if (i * HALF < rows) {
+          uint32_t o0[HALF], o1[HALF];
+          tmem_ld8(lane_base + C::tO(0) + i * HALF, o0);  // (columns never written are not used)
+          tmem_ld8(lane_base + C::tO(1) + i * HALF, o1);
           tmem_wait_ld();
-          int tok = (i * HALF + c0) / a.kv_group, hd = i * HALF + c0 - tok * a.kv_group;
+          int tok = i * HALF / a.kv_group, hd = i * HALF - tok * a.kv_group;
 #pragma unroll
-          for (int c = 0; c < STEP; ++c) {
-            const float x0 = __shfl_sync(0xffffffffu, w0, c0 + c), x1 = __shfl_sync(0xffffffffu, w1, c0 + c);
+          for (int c = 0; c < HALF; ++c) {
+            const float x0 = __shfl_sync(0xffffffffu, w0, c), x1 = __shfl_sync(0xffffffffu, w1, c);
             const float v0 = n > 0 ? __uint_as_float(o0[c]) * x0 : 0.f;
             const float v = n > 1 ? fmaf(__uint_as_float(o1[c]), x1, v0) : v0;
-            const int rw = i * HALF + c0 + c;
+            const int rw = i * HALF + c;
             if (rw < rows && has_col) {
               if (part >= 0)
                 a.part_o[(static_cast<int64_t>(part) * a.part_rows + rw) * DV + col] = v;
@@ -504,11 +476,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 1) tmem_dealloc(tbase, C::COLS);
 }
 
-template <int DQK, int DV, int N>
-cudaError_t launch_n(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const PagedArgs& a, int ctas,
+template <int DQK, int DV>
+cudaError_t launch_d(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const PagedArgs& a, int ctas,
                      cudaStream_t stream) {
-  using C = Cfg<DQK, DV, N>;
-  auto kern = paged_decode_kernel<DQK, DV, N>;
+  using C = Cfg<DQK, DV>;
+  auto kern = paged_decode_kernel<DQK, DV>;
   static PerDeviceOnce once;
   const cudaError_t e =
       once.run([&] { return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM); });
@@ -517,25 +489,14 @@ cudaError_t launch_n(const CUtensorMap& tq, const CUtensorMap& tk, const CUtenso
   return cudaGetLastError();
 }
 
-template <int DQK, int DV>
-cudaError_t launch_d(int n, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const PagedArgs& a,
-                     int ctas, cudaStream_t stream) {
-  switch (n) {
-    case 16: return launch_n<DQK, DV, 16>(tq, tk, tv, a, ctas, stream);
-    case 32: return launch_n<DQK, DV, 32>(tq, tk, tv, a, ctas, stream);
-    case 64: return launch_n<DQK, DV, 64>(tq, tk, tv, a, ctas, stream);
-    default: return cudaErrorInvalidValue;
-  }
-}
-
 }  // namespace decode
 }  // namespace paged
 
-cudaError_t launch_paged_decode(int d_qk, int d_v, int n, const CUtensorMap& tq, const CUtensorMap& tk,
-                                const CUtensorMap& tv, const PagedArgs& a, int ctas, cudaStream_t stream) {
-  if (d_qk == 64 && d_v == 64) return paged::decode::launch_d<64, 64>(n, tq, tk, tv, a, ctas, stream);
-  if (d_qk == 128 && d_v == 128) return paged::decode::launch_d<128, 128>(n, tq, tk, tv, a, ctas, stream);
-  if (d_qk == 192 && d_v == 128) return paged::decode::launch_d<192, 128>(n, tq, tk, tv, a, ctas, stream);
+cudaError_t launch_paged_decode(int d_qk, int d_v, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
+                                const PagedArgs& a, int ctas, cudaStream_t stream) {
+  if (d_qk == 64 && d_v == 64) return paged::decode::launch_d<64, 64>(tq, tk, tv, a, ctas, stream);
+  if (d_qk == 128 && d_v == 128) return paged::decode::launch_d<128, 128>(tq, tk, tv, a, ctas, stream);
+  if (d_qk == 192 && d_v == 128) return paged::decode::launch_d<192, 128>(tq, tk, tv, a, ctas, stream);
   return cudaErrorInvalidValue;
 }
 

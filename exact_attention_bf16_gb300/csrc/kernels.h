@@ -428,12 +428,13 @@ struct PagedArgs {
   ChunkList* list;
 };
 // Maps: q boxes of 64 columns x kv_group heads x q_box_tokens rows; k and v (caches as [pages, page_size, heads_kv, d])
-// of 64 columns x min(page_size, 128) rows. even: no request has more than one tile of rows; decode_rows > 0 (16, 32 or
-// 64): none has more than that, and launch_paged_decode's kernel takes the place of paged_kernel.
+// of 64 columns x min(page_size, 128) rows. even: no request has more than one tile of rows; decode: none has more than
+// kDecodeRows, and launch_paged_decode's kernel takes the place of paged_kernel.
+constexpr int kDecodeRows = 16;
 cudaError_t launch_fwd_paged(int d_qk, int d_v, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
-                             const PagedArgs& a, bool even, int decode_rows, int ctas, cudaStream_t stream);
-cudaError_t launch_paged_decode(int d_qk, int d_v, int n, const CUtensorMap& tq, const CUtensorMap& tk,
-                                const CUtensorMap& tv, const PagedArgs& a, int ctas, cudaStream_t stream);
+                             const PagedArgs& a, bool even, bool decode, int ctas, cudaStream_t stream);
+cudaError_t launch_paged_decode(int d_qk, int d_v, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
+                                const PagedArgs& a, int ctas, cudaStream_t stream);
 
 cudaError_t launch_exp2_eval(const float* x, float* y_poly, float* y_hw, int64_t n, cudaStream_t stream);
 

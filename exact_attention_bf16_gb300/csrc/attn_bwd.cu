@@ -54,7 +54,7 @@ __global__ void __launch_bounds__(256, 8) preprocess_kernel(const BwdArgs a) {
 
 // D of packed sequences that all have few keys, as sum_j P_ij (dO_i . v_j) with P from the LSE, all in fp32. The same
 // number in exact arithmetic, but O comes rounded to bf16, and its error d is the same in all dS_ij =
-// P_ij (dO_i . v_j - D_i): dQ_i is off by d sum_j P_ij k_j, d up to 2^-9 |dO_i| |O_i|, beside a dQ_i that shrinks as the
+// P_ij (dO_i . v_j - D_i): dQ_i is off by d sum_j P_ij k_j, d up to 2^-8 |dO_i| |O_i|, beside a dQ_i that shrinks as the
 // v_j of its keys differ less from their mean O_i. Over sequences of one and two tokens dQ and dK came out 5.0e-3 from the
 // exact ones (norms), now below 2.9e-3; from 9 keys on it is at most 3.1e-3 from the rounded O, too. (A choice per
 // sequence, in the pass above, cost the rows of longer ones 40% of its time.) Latency-bound: 8 lanes share a row, one key

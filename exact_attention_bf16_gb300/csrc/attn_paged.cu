@@ -24,15 +24,15 @@
 //     HBM (every K/V byte is read once and used for a handful of rows), so the
 //     key blocks of all (request, K/V head) units, laid end to end, are cut into
 //     equal ranges, one per CTA. A CTA finds its range from the lengths alone. 33 requests
-//     of 3..6 tokens, 16 heads over 1, d = 64, up to 16384 keys: 27.2 us (about five key
-//     blocks a CTA), 29.2 by the list below; 64 decoding requests 321 us against 393.
+//     of 3..6 tokens, 16 heads over 1, d = 64, up to 16384 keys: 26.4 us (about five key
+//     blocks a CTA), 28 by the list below; 64 decoding requests 321 us against 393.
 //   - longer chunks: bound by the tensor cores, and by L2 where concurrent CTAs
 //     read different keys, so units are taken one after another from a list
 //     that chunk_list_kernel builds, a request's units together, long requests
 //     and late units (the most keys under the causal mask) first. Only units
 //     longer than an equal share of the work are cut. 24 requests, chunks of 500..2048 tokens over
-//     up to 16384 keys, 32 heads over 8, d = 128: 527 us, 1154 TFLOP/s (the contiguous forward
-//     of like lengths: 1100..1350); the tensor pipe is active 53% of the time, the rest is the
+//     up to 16384 keys, 32 heads over 8, d = 128: 527 us, 1154 TFLOP/s (the contiguous
+//     causal forward: 1165 at 4096 keys, 1375 at 8192); the tensor pipe is active 53% of the time, the rest is the
 //     chain S -> softmax -> PV of the two tiles and the ends of the units.
 //
 // Warps: 0 work and TMA copies, 1 MMA issue, 4..7 and 8..11 softmax of tile or
@@ -41,10 +41,11 @@
 // key and entries outside the cache become a page index past the cache, whose
 // boxes read zeros.
 //
-// P enters the PV product in bf16, V's type in the cache (half a step is 2^-9 of
+// P enters the PV product in bf16, V's type in the cache (half a step is 2^-8 of
 // each weight): an fp16 copy of V, as the contiguous forward makes, would cost a
 // second pass over keys that a decoding step reads only once. Every sum is fp32.
 #include <cstddef>
+#include <type_traits>
 
 #include "kernels.h"
 #include "paged_common.cuh"
@@ -562,7 +563,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 // Merges the units that were cut, launched while paged_kernel still runs (it waits for
 // it below): with the segments' LSE_r in log2 units, M their
 // maximum, O = sum_r 2^(LSE_r - M) O_r / sum_r 2^(LSE_r - M), the segments in key
-// order within a warp and then warp after warp. Bound by latency: WPR warps share a row,
+// order within a warp and then warp after warp. Bound by latency (a segment's O is loaded beside its LSE: one request
+// of 4100 tokens 13.9 us, 14.6 with the loads one after the other): WPR warps share a row,
 // each taking every WPR-th segment (8 where rows are few, as in decoding, else 1); lane l
 // holds columns [DV/32 l, DV/32 (l + 1)).
 template <int DV, int WPR>
@@ -582,32 +584,38 @@ __global__ void __launch_bounds__(256) merge_kernel(const PagedArgs a) {
   auto at = [&](int r) -> int64_t {
     return static_cast<int64_t>(r == 0 ? m.first : m.rest + r - 1) * a.part_rows + row;
   };
-  float mx = -INFINITY;
-  for (int r = lane; r < m.n; r += 32) mx = fmaxf(mx, a.part_lse[at(r)]);
+  // the first segments' O, loaded beside their LSE
+  using Vec = std::conditional_t<CPL == 4, float4, float2>;
+  auto load_o = [&](int r) -> Vec { return *reinterpret_cast<const Vec*>(a.part_o + at(r) * DV + lane * CPL); };
+  constexpr int kAhead = 4;
+  Vec ahead[kAhead];
+#pragma unroll
+  for (int u = 0; u < kAhead; ++u)
+    if (part + u * WPR < m.n) ahead[u] = load_o(part + u * WPR);
+  const float lse0 = lane < m.n ? a.part_lse[at(lane)] : -INFINITY;  // segment `lane`'s
+  float mx = lse0;
+  for (int r = lane + 32; r < m.n; r += 32) mx = fmaxf(mx, a.part_lse[at(r)]);
 #pragma unroll
   for (int d = 16; d > 0; d >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
   float sum = 0.f, acc[CPL];
 #pragma unroll
   for (int c = 0; c < CPL; ++c) acc[c] = 0.f;
   if (mx != -INFINITY) {
-#pragma unroll 4
-    for (int r = part; r < m.n; r += WPR) {
-      const int64_t x = at(r);
-      const float wr = ex2_mufu(a.part_lse[x] - mx);
+    auto add = [&](int r, const Vec& v) {
+      const float wr = ex2_mufu((r < 32 ? __shfl_sync(0xffffffffu, lse0, r & 31) : a.part_lse[at(r)]) - mx);
       sum += wr;
-      const float* src = a.part_o + x * DV + lane * CPL;
+      acc[0] = fmaf(wr, v.x, acc[0]);
+      acc[1] = fmaf(wr, v.y, acc[1]);
       if constexpr (CPL == 4) {
-        const float4 v = *reinterpret_cast<const float4*>(src);
-        acc[0] = fmaf(wr, v.x, acc[0]);
-        acc[1] = fmaf(wr, v.y, acc[1]);
         acc[2] = fmaf(wr, v.z, acc[2]);
         acc[3] = fmaf(wr, v.w, acc[3]);
-      } else {
-        const float2 v = *reinterpret_cast<const float2*>(src);
-        acc[0] = fmaf(wr, v.x, acc[0]);
-        acc[1] = fmaf(wr, v.y, acc[1]);
       }
-    }
+    };
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u)
+      if (part + u * WPR < m.n) add(part + u * WPR, ahead[u]);
+#pragma unroll 4
+    for (int r = part + kAhead * WPR; r < m.n; r += WPR) add(r, load_o(r));
   }
   if constexpr (WPR > 1) {
 #pragma unroll
@@ -807,8 +815,8 @@ cudaError_t launch_d(const CUtensorMap& tq, const CUtensorMap& tk, const CUtenso
   }
   if (e != cudaSuccess) return e;
   const int rows = min(a.max_q, (even ? 1 : 2) * a.tile_tokens) * a.kv_group;
-  // up to 16 rows, whose blocks fit the GPU at once: a decoding request of 4100 tokens 14.6 us with eight warps per row,
-  // 17.8 with one
+  // up to 16 rows, whose blocks fit the GPU at once: a decoding request of 4100 tokens 13.9 us with eight warps per row,
+  // 17 with one
   if (rows <= 16)
     return launch_early(merge_kernel<DV, 8>, dim3(ctas, rows), 256, 0, stream, a);
   return launch_early(merge_kernel<DV, 1>, dim3(ctas, (rows + 7) / 8), 256, 0, stream, a);

@@ -15,7 +15,7 @@
 //
 // Bound by HBM: per 128 keys and K/V head at d = 128 64 KB against 16 MMAs of about
 // 50 cycles. 64 requests of up to 32768 tokens, 32 heads over 8, d = 128: 307 us, 6.67 TB/s
-// (98% of a copy's), 321 us by paged_kernel; one of 4100 tokens 14.5 us against 15.5, its
+// (98% of a copy's), 321 us by paged_kernel; one of 4100 tokens 13.9 us against 15, its
 // launches, first copies and merge. d = 64 (8 heads of their own, 64 requests) reaches 4.1 TB/s
 // against 3.8: a 128-key block is half the bytes for the same waits. With 32 columns the same calls took 341 us where 16 took 323 and
 // paged_kernel 332 (64 requests, 8 heads, d = 128), with 64 columns 416, so 17 rows and more are

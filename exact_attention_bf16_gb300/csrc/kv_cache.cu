@@ -4,6 +4,7 @@
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 
+#include <algorithm>
 #include <cstdint>
 
 #include "kernels.h"
@@ -23,13 +24,12 @@ namespace cg = cooperative_groups;
 // where stack is free_pages[0 .. c) followed by the ended requests' pages in
 // order, and token t belongs to the request s with cu_s <= t < cu_{s+1}.
 //
-// Bound by latency: a few KB to a few hundred KB of slots. Every CTA of one
-// cluster computes the sums itself (the lengths are a few KB in L2) into its
-// shared memory and then takes its share of tokens and pages, finding the
-// request of each by bisection. Nothing a CTA reads is written before the
-// cluster's barrier except places no other reads (table entries from have on,
-// stack entries from c on), so the in-place outputs (lengths, stack height)
-// are written after it.
+// Bound by latency: a few KB to a few hundred KB of slots. Every CTA computes the
+// sums itself (the lengths are a few KB in L2) into its shared memory and then
+// takes its share of tokens and pages, finding the request of each by bisection.
+// Nothing a CTA reads is written except places no other reads (table entries from
+// have on, stack entries from c on) and, in place, the lengths and the stack's
+// height: then the grid is one cluster, whose barrier stands before those.
 struct Sums {
   long long add, grow, back;
 };
@@ -62,7 +62,6 @@ __global__ void kv_plan_kernel(const KvPlanArgs a) {
   extern __shared__ int s_start[];  // cu[n + 1], grow[n + 1], back[n + 1]
   __shared__ Sums warp_sum[32];
   __shared__ int too_wide;
-  cg::cluster_group cluster = cg::this_cluster();
   const int n = a.num_seqs, tid = static_cast<int>(threadIdx.x), nthr = static_cast<int>(blockDim.x);
   const int lane = tid & 31, warp = tid >> 5, nwarps = nthr >> 5;
   int* s_cu = s_start;
@@ -127,8 +126,8 @@ __global__ void kv_plan_kernel(const KvPlanArgs a) {
   else if (count + total.back > kMost || count + total.back - total.grow > a.free_capacity) status = 4;
   const int height = count + static_cast<int>(min(total.back, kMost - count));  // of the stack, ended pages pushed
   const int grow = static_cast<int>(min(total.grow, kMost));
-  const int rank = static_cast<int>(cluster.block_rank());
-  const int all = nthr * static_cast<int>(cluster.num_blocks()), me = rank * nthr + tid;
+  const int rank = static_cast<int>(blockIdx.x), ctas = static_cast<int>(gridDim.x);
+  const int all = nthr * ctas, me = rank * nthr + tid;
   if (status == 0) {
     auto stack = [&](int i) -> int {
       if (i < count) return a.free_pages[i];
@@ -142,7 +141,7 @@ __global__ void kv_plan_kernel(const KvPlanArgs a) {
     }
     // ended requests' pages that stay on the stack: a warp copies a row, in order
     if (total.back > 0) {
-      for (int s = rank * nwarps + warp; s < n; s += nwarps * static_cast<int>(cluster.num_blocks())) {
+      for (int s = rank * nwarps + warp; s < n; s += nwarps * ctas) {
         const int len = s_back[s + 1] - s_back[s], keep = min(len, height - grow - count - s_back[s]);
         const int* row = a.block_table + s * a.block_table_stride;
         int* dst = a.free_pages + count + s_back[s];
@@ -190,8 +189,8 @@ __global__ void kv_plan_kernel(const KvPlanArgs a) {
   } else {
     for (int t = me; t < a.max_tokens; t += all) a.slot_mapping[t] = -1;
   }
-  // every read of the lengths, the stack's height and the old entries is done
-  cluster.sync();
+  // every read of the lengths and the stack's height is done (where they are updated in place, the grid is one cluster)
+  cg::this_cluster().sync();
   for (int s = me; s <= n; s += all) {
     a.cu_seqlens_q[s] = status == 0 ? s_cu[s] : 0;
     if (s < n) {
@@ -286,17 +285,22 @@ cudaError_t launch_kv_plan(const KvPlanArgs& a, cudaStream_t stream) {
     return cudaFuncSetAttribute(kv::kv_plan_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
   });
   if (e != cudaSuccess) return e;
-  // a small step is one CTA's work; more tokens are shared by a cluster of sixteen (1000 requests with
-  // 50,000 tokens: 11.2 us with eight CTAs)
+  // A small step is one CTA's work (1000 requests of one token each: 6.4 us). More tokens are shared by up to kPlanCtas
+  // (1000 requests with 48,420 tokens 8.3 us, 11.6 by half as many; 3000 with 150,394 tokens 8.3, 11.2 by 64), or where
+  // lengths or the stack's height are updated in place, and so must have been read by all first, by a cluster of sixteen,
+  // the most there are (12.3 us of the former; eight take 17.1).
+  constexpr int kPlanCtas = 148;
   const bool small = a.max_tokens <= 4096 && a.num_seqs <= 1024;
+  const bool in_place = a.seqlens_k == a.seqlens_old || a.free_count_out == a.free_count;
+  const int ctas = small ? 1 : in_place ? 16 : std::max(16, std::min(kPlanCtas, (a.max_tokens + 1023) / 1024));
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(small ? 1 : 16);
+  cfg.gridDim = dim3(ctas);
   cfg.blockDim = dim3(small && a.num_seqs <= 256 && a.max_tokens <= 1024 ? 256 : 1024);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cudaLaunchAttribute at{};
   at.id = cudaLaunchAttributeClusterDimension;
-  at.val.clusterDim.x = cfg.gridDim.x;
+  at.val.clusterDim.x = ctas <= 16 && (small || in_place) ? ctas : 1;
   at.val.clusterDim.y = at.val.clusterDim.z = 1;
   cfg.attrs = &at;
   cfg.numAttrs = 1;

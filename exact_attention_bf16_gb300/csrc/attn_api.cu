@@ -890,6 +890,12 @@ attn_status_t run_kv_append(const attn_kv_append_params* p, cudaStream_t stream)
   ATTN_TRY(check_tensor(p->v, 0, p->v_row_stride, p->v_head_stride, true, none));
   ATTN_TRY(check_cache(p->k_cache, p->k_cache_page_stride, p->k_cache_row_stride, p->k_cache_head_stride));
   ATTN_TRY(check_cache(p->v_cache, p->v_cache_page_stride, p->v_cache_row_stride, p->v_cache_head_stride));
+  auto overlaps = [&](int64_t page, int64_t row, int64_t head) {  // rows on top of one another, all written
+    return row == 0 || (page == 0 && p->num_pages > 1) || (head == 0 && p->heads_kv > 1);
+  };
+  if (overlaps(p->k_cache_page_stride, p->k_cache_row_stride, p->k_cache_head_stride) ||
+      overlaps(p->v_cache_page_stride, p->v_cache_row_stride, p->v_cache_head_stride))
+    return ATTN_ERR_INVALID_ARG;
   if (none) return ATTN_OK;
   if (!p->slot_mapping || (reinterpret_cast<uintptr_t>(p->slot_mapping) & 7u)) return ATTN_ERR_INVALID_ARG;
   ATTN_TRY(check_lists_device(p->k, {p->v, p->k_cache, p->v_cache, p->slot_mapping}));

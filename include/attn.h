@@ -428,7 +428,8 @@ attn_status_t attn_kv_plan(const attn_kv_plan_params* p, attn_stream_t stream);
  * slot_mapping[i] (page slot / page_size, row slot % page_size). A slot outside
  * [0, num_pages * page_size), as -1, writes nothing. Slots must differ; of rows
  * with the same slot any one may stay, in 16-byte pieces. The rest of the
- * caches is left as it was. (d_qk, d_v), bases and strides as for attn_fwd. */
+ * caches is left as it was. (d_qk, d_v), bases and strides as for attn_fwd; the
+ * caches' rows must not overlap (a stride of 0 is ATTN_ERR_INVALID_ARG). */
 typedef struct attn_kv_append_params {
   const void* k;
   const void* v;

@@ -128,3 +128,10 @@ def test_paged_workspace_of_bad_arguments_is_zero(abi):
     p.heads_kv = -1
     assert abi.load().attn_fwd_paged_workspace_size(ctypes.byref(p)) == 0
     assert abi.load().attn_fwd_paged_workspace_size(None) == 0
+
+
+@pytest.mark.parametrize("field", [f"{c}_cache_{s}_stride" for c in "kv" for s in ("page", "row", "head")])
+def test_append_refuses_caches_whose_rows_overlap(abi, field):
+    p = _append(abi)
+    setattr(p, field, 0)
+    assert abi.load().attn_kv_append(ctypes.byref(p), None) == INVALID

@@ -978,6 +978,7 @@ attn_status_t run_fwd_paged(const attn_paged_params* p, void* ws, size_t ws_byte
   DeviceScope scope;
   ATTN_TRY(bind_device(&scope, p->q));
   const PagedPlan pl = paged_plan(p);
+  if (pl.items > 0x7fffffff) return ATTN_ERR_UNSUPPORTED;
   if (ws == nullptr || ws_bytes < pl.bytes || (reinterpret_cast<uintptr_t>(ws) & 255u)) return ATTN_ERR_WORKSPACE;
   PagedArgs a{};
   a.o = static_cast<__nv_bfloat16*>(p->o);

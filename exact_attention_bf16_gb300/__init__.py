@@ -280,8 +280,9 @@ def attn_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, *, causal: bool 
     if lse is None:
         lse = torch.empty((B, H, Nq), dtype=torch.float32, device=q.device)
         _used_on(stream, lse)
-    if lse.shape != (B, H, Nq) or not lse.is_contiguous() or lse.dtype != torch.float32:
-        raise ValueError("lse must be a contiguous float32 [B, H, Nq] tensor")
+    if (lse.shape != (B, H, Nq) or not lse.is_contiguous() or lse.dtype != torch.float32 or lse.device != q.device or
+            out.device != q.device):
+        raise ValueError(f"out and lse (a contiguous float32 [B, H, Nq] tensor) must be on {q.device}")
     p = AttnFwdParams()
     _fill_fwd(p, q, k, v, out, lse, _strides4, scale, causal)
     p.batch, p.seqlen_q, p.seqlen_k = B, Nq, Nk
@@ -354,8 +355,9 @@ def attn_fwd_block_sparse(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, kv_
     _check_bf16("out", out, 4)
     if lse is None:
         lse = torch.empty((B, H, Nq), dtype=torch.float32, device=q.device)
-    if lse.shape != (B, H, Nq) or not lse.is_contiguous() or lse.dtype != torch.float32:
-        raise ValueError("lse must be a contiguous float32 [B, H, Nq] tensor")
+    if (lse.shape != (B, H, Nq) or not lse.is_contiguous() or lse.dtype != torch.float32 or lse.device != q.device or
+            out.device != q.device):
+        raise ValueError(f"out and lse (a contiguous float32 [B, H, Nq] tensor) must be on {q.device}")
     p = AttnFwdParams()
     _fill_fwd(p, q, k, v, out, lse, _strides4, scale, causal)
     p.batch, p.seqlen_q, p.seqlen_k = B, Nq, Nk
@@ -393,12 +395,12 @@ def attn_fwd_varlen(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqlen
         out, so = torch.empty((tq, H, dv), dtype=_BF16, device=q.device), (H * dv, dv)
     else:
         shape, so = _bf16_layout("out", out, 3)
-        if shape != (tq, H, dv):
-            raise ValueError(f"out must be {(tq, H, dv)}, got {tuple(shape)}")
+        if shape != (tq, H, dv) or out.device != q.device:
+            raise ValueError(f"out must be {(tq, H, dv)} on {q.device}, got {tuple(shape)} on {out.device}")
     if lse is None:
         lse = torch.empty((H, tq), dtype=_F32, device=q.device)
-    elif lse.shape != (H, tq) or not lse.is_contiguous() or lse.dtype is not _F32:
-        raise ValueError("lse must be a contiguous float32 [H, total_q] tensor")
+    elif lse.shape != (H, tq) or not lse.is_contiguous() or lse.dtype is not _F32 or lse.device != q.device:
+        raise ValueError(f"lse must be a contiguous float32 [H, total_q] tensor on {q.device}")
     if stream is not None:
         _used_on(stream, out, lse)
     mod, cap, slopes = _mod_fields(q, softcap, alibi_slopes)

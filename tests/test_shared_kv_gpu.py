@@ -331,3 +331,12 @@ def test_dense_rows_of_few_keys(ea, mod, nk):
     refs = [shared_bwd(*(to64(x[i]) for x in (q, k, v, do)), 0.125, True, score_mod) for i in range(2)]
     check_grads(dict(zip(("dq", "dk", "dv"), grads)), {n: np.stack([r[n] for r in refs]) for n in ("dq", "dk", "dv")},
                 f"{nk} keys")
+
+
+def test_outputs_elsewhere_are_refused(ea):
+    """An LSE in host memory is refused, not written to."""
+    q, k, v, _, cu, _ = _packed([40], [40], 4, 2, (64, 64), seed=181)
+    with pytest.raises(ValueError):
+        ea.attn_fwd_varlen(q, k, v, cu, cu, 40, 40, lse=torch.empty((4, 40)))
+    with pytest.raises(ValueError):
+        ea.attn_fwd(q[None], k[None], v[None], lse=torch.empty((1, 4, 40)))

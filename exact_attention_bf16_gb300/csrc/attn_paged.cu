@@ -31,8 +31,8 @@
 //     that chunk_list_kernel builds, a request's units together, long requests
 //     and late units (the most keys under the causal mask) first. Only units
 //     longer than an equal share of the work are cut. 24 requests, chunks of 500..2048 tokens over
-//     up to 16384 keys, 32 heads over 8, d = 128: 527 us, 1154 TFLOP/s (the contiguous
-//     causal forward: 1165 at 4096 keys, 1375 at 8192); the tensor pipe is active 53% of the time, the rest is the
+//     up to 16384 keys, 32 heads over 8, d = 128: 512 us, 1190 TFLOP/s (the contiguous
+//     causal forward: 1165 at 4096 keys, 1375 at 8192); the tensor pipe is active 55% of the time, the rest is the
 //     chain S -> softmax -> PV of the two tiles and the ends of the units.
 //
 // Warps: 0 work and TMA copies, 1 MMA issue, 4..7 and 8..11 softmax of tile or
@@ -243,14 +243,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         auto wait_o = [&]() { return seg_i == 0 || mbar_wait_warp(&bar->o_free, (seg_i - 1) & 1u, a.status, 0x3210); };
         if (n == 0) ok = wait_o();
         for (int j = 0; j <= n && n > 0 && ok; ++j) {
-          if (j < n) {
-            ok = mbar_wait_warp(&bar->k_full[rk.slot], rk.phase, a.status, 0x3220);
-            if (ok && j == 0) ok = mbar_wait_warp(&bar->q_full, cq & 1u, a.status, 0x3230);
-            if (!ok) break;
-            tc_fence_after();
-          }
           if (dual) {
             if (j < n) {
+              ok = mbar_wait_warp(&bar->k_full[rk.slot], rk.phase, a.status, 0x3220);
+              if (ok && j == 0) ok = mbar_wait_warp(&bar->q_full, cq & 1u, a.status, 0x3230);
+              if (!ok) break;
+              tc_fence_after();
               issue_s(j & 1, 0);
               rk.next();
               if (j == n - 1 && lane == 0) mma_commit(&bar->q_free);
@@ -268,18 +266,29 @@ __global__ void __launch_bounds__(kThreads, 1)
               if (j - 1 >= n - 2 && lane == 0) mma_commit(&bar->o_full[i]);
             }
           } else {
-            if (j > 0) {
-              if (j == 1) ok = wait_o();
-              ok = ok && mbar_wait_warp(&bar->v_full[rv.slot], rv.phase, a.status, 0x3240);
+            // What the step's first products need is tested together: this warp's instructions are the step's limit, and
+            // waits one after another cost 150 to 400 cycles each even where everything had arrived.
+            const bool pv0 = j > 0 && j - 1 < n0;
+            const bool k_in = j == n || mbar_test(&bar->k_full[rk.slot], rk.phase);
+            const bool v_in = j == 0 || mbar_test(&bar->v_full[rv.slot], rv.phase);
+            const bool p_in = !pv0 || mbar_test(&bar->p_full[0], pp & 1u);
+            if (j < 2 || !__all_sync(0xffffffffu, k_in && v_in && p_in)) {
+              ok = (j == n || mbar_wait_warp(&bar->k_full[rk.slot], rk.phase, a.status, 0x3220)) &&
+                   (j != 0 || mbar_wait_warp(&bar->q_full, cq & 1u, a.status, 0x3230)) && (j != 1 || wait_o()) &&
+                   (j == 0 || mbar_wait_warp(&bar->v_full[rv.slot], rv.phase, a.status, 0x3240)) &&
+                   (!pv0 || mbar_wait_warp(&bar->p_full[0], pp & 1u, a.status, 0x3250));
               if (!ok) break;
             }
-#pragma unroll
+            tc_fence_after();
+#pragma unroll 1  // (unrolled 552 us, so 512: the code no longer fits what the instruction caches keep for this warp)
             for (int i = 0; i < 2; ++i) {
               const int ni = i == 0 ? n0 : n1;
               if (j > 0 && j - 1 < ni) {
-                ok = mbar_wait_warp(&bar->p_full[i], (pp >> i) & 1u, a.status, 0x3250);
-                if (!ok) break;
-                tc_fence_after();
+                if (i == 1) {
+                  ok = mbar_wait_warp(&bar->p_full[1], (pp >> 1) & 1u, a.status, 0x3251);
+                  if (!ok) break;
+                  tc_fence_after();
+                }
                 pp ^= 1u << i;
                 issue_pv(i, j == 1);
                 if (j == ni && lane == 0) mma_commit(&bar->o_full[i]);

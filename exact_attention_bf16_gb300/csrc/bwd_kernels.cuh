@@ -369,7 +369,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       for (int t = 0; t < T && ok; ++t) {
         if (t + 1 < T) {  // next S^T, dP^T as soon as the softmax warps hold this tile's
-          ok = mbar_wait(&bar->sp_free, static_cast<uint32_t>(t) & 1u, a.status, 0x1215) && wait_stage(t + 1);
+          ok = mbar_wait_all(
+              a.status, {&bar->sp_free, static_cast<uint32_t>(t) & 1u, 0x1215},
+              {&bar->st_full[(t + 1) % C::NST], static_cast<uint32_t>((t + 1) / C::NST) & 1u, 0x1210});
           if (!ok) break;
           tc_fence_after();
           issue_s(t + 1);
@@ -872,13 +874,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       for (int t = 0; t < T && ok; ++t) {
         if (t + 1 < T) {  // S^T(t+1) into R'(t) once the softmax warps hold dP^T(t)
-          ok = mbar_wait(&bar->sp_free, static_cast<uint32_t>(t) & 1u, a.status, 0x1425) &&
-               mbar_wait(&bar->q_full[(t + 1) % C::NQ], static_cast<uint32_t>((t + 1) / C::NQ) & 1u, a.status, 0x1426);
+          ok = mbar_wait_all(
+              a.status, {&bar->sp_free, static_cast<uint32_t>(t) & 1u, 0x1425},
+              {&bar->q_full[(t + 1) % C::NQ], static_cast<uint32_t>((t + 1) / C::NQ) & 1u, 0x1426});
           if (!ok) break;
           tc_fence_after();
           issue_s(t + 1);
           mma_commit(&bar->s_full);
         }
+        // (dO(t+1), needed below, is looked for here, beside the wait)
+        const bool g_in = t + 1 < T && mbar_test(&bar->g_full[(t + 1) % C::NG], static_cast<uint32_t>((t + 1) / C::NG) & 1u);
         ok = mbar_wait(&bar->ds_full, static_cast<uint32_t>(t) & 1u, a.status, 0x1428);
         if (!ok) break;
         tc_fence_after();
@@ -901,7 +906,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         mma_commit(&bar->q_empty[t % C::NQ]);
         if (t + 1 < T) {  // dP^T(t+1) into R(t), after the reads above in issue order
-          ok = mbar_wait(&bar->g_full[(t + 1) % C::NG], static_cast<uint32_t>((t + 1) / C::NG) & 1u, a.status, 0x142a);
+          ok = g_in ||
+               mbar_wait(&bar->g_full[(t + 1) % C::NG], static_cast<uint32_t>((t + 1) / C::NG) & 1u, a.status, 0x142a);
           if (!ok) break;
           tc_fence_after();
           issue_dp(t + 1);
@@ -1401,7 +1407,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!ok) break;
         } else {
           if (t + 1 < T) {  // next S, dP as soon as the softmax warps hold this tile's
-            ok = mbar_wait(&bar->sp_free, static_cast<uint32_t>(t) & 1u, a.status, 0x2215) && wait_stage(t + 1);
+            ok = mbar_wait_all(
+                a.status, {&bar->sp_free, static_cast<uint32_t>(t) & 1u, 0x2215},
+                {&bar->k_full[(t + 1) % C::KST], static_cast<uint32_t>((t + 1) / C::KST) & 1u, 0x2210},
+                {&bar->v_full[(t + 1) % C::VST], static_cast<uint32_t>((t + 1) / C::VST) & 1u, 0x2211});
             if (!ok) break;
             issue_next();
           }

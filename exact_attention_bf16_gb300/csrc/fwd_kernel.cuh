@@ -382,10 +382,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int uK = 2 * j, uV = 2 * (j - 1) + 1;
         const int sK = ring_slot(uK), sV = ring_slot(haveV ? uV : 1);
         const uint32_t js = (static_cast<uint32_t>(j) & 0xFFFu) << 12;  // the step, in the site's bits 12..23
-        if (haveK) ok = mbar_wait(&bar->kv_full[sK], ring_use(uK) & 1u, a.status, 0x210 | js, poll_lim);
-        if (ok && haveV)
-          ok = mbar_wait(&bar->kv_full[sV], ring_use(uV) & 1u, a.status, 0x211 | js, poll_lim);
-        if (!ok) break;
+        // What the step's first products need is tested together: this thread's instructions limit the step, and waits
+        // one after another cost it 150 cycles each even where everything had arrived (d = 128, N = 8192: 1.42 -> 1.38 ms).
+        const bool pv0 = haveV && j - 1 < nkv[0];
+        const bool k_in = !haveK || mbar_test(&bar->kv_full[sK], ring_use(uK) & 1u);
+        const bool v_in = !haveV || mbar_test(&bar->kv_full[sV], ring_use(uV) & 1u);
+        const bool p_in = !pv0 || mbar_test(&bar->p_full[0], static_cast<uint32_t>(j - 1) & 1u);
+        if (!(k_in && v_in && p_in)) {
+          ok = (!haveK || mbar_wait(&bar->kv_full[sK], ring_use(uK) & 1u, a.status, 0x210 | js, poll_lim)) &&
+               (!haveV || mbar_wait(&bar->kv_full[sV], ring_use(uV) & 1u, a.status, 0x211 | js, poll_lim)) &&
+               (!pv0 || mbar_wait(&bar->p_full[0], static_cast<uint32_t>(j - 1) & 1u, a.status, 0x220u | js, poll_lim));
+          if (!ok) break;
+        }
         tc_fence_after();
         // descriptors built once per tile, advanced per k-step with one add
         const uint64_t dk = smem_desc(smem_u32(ring_addr(uK)), 16, 1024, SWZ_128B);
@@ -394,9 +402,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int i = 0; i < QT; ++i) {
           if (haveV && j - 1 < nkv[i]) {
             // O_i (+)= P_i(j-1) V_{j-1}: P from TMEM (aliasing S_i), V MN-major in shared memory
-            ok = mbar_wait(&bar->p_full[i], static_cast<uint32_t>(j - 1) & 1u, a.status, (0x220u + i) | js, poll_lim);
-            if (!ok) break;
-            tc_fence_after();
+            if (i > 0) {
+              ok = mbar_wait(&bar->p_full[i], static_cast<uint32_t>(j - 1) & 1u, a.status, (0x220u + i) | js, poll_lim);
+              if (!ok) break;
+              tc_fence_after();
+            }
             const uint32_t acc0 = j - 1 > 0 ? 1u : 0u;
 #pragma unroll
             for (int kk = 0; kk < BN / 16; ++kk) {

@@ -122,6 +122,23 @@ __device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
   return ok != 0;
 }
 
+// A barrier's phase to wait for, and the site to report.
+struct MbarPhase {
+  uint64_t* bar;
+  uint32_t parity, where;
+};
+// Waits for two or three phases (mbar_wait, one after another) after testing them together: the tests' latencies overlap,
+// where waits one after another cost a thread that issues MMAs some 150 cycles each even if everything has arrived.
+__device__ __forceinline__ bool mbar_wait_all(uint32_t* status, MbarPhase x, MbarPhase y) {
+  const bool a = mbar_test(x.bar, x.parity), b = mbar_test(y.bar, y.parity);
+  return (a && b) || (mbar_wait(x.bar, x.parity, status, x.where) && mbar_wait(y.bar, y.parity, status, y.where));
+}
+__device__ __forceinline__ bool mbar_wait_all(uint32_t* status, MbarPhase x, MbarPhase y, MbarPhase z) {
+  const bool a = mbar_test(x.bar, x.parity), b = mbar_test(y.bar, y.parity), c = mbar_test(z.bar, z.parity);
+  return (a && b && c) || (mbar_wait(x.bar, x.parity, status, x.where) && mbar_wait(y.bar, y.parity, status, y.where) &&
+                           mbar_wait(z.bar, z.parity, status, z.where));
+}
+
 // mbar_wait for code that all 32 lanes of a warp run together and that issues
 // warp-collective instructions (tcgen05.ld/st, votes) afterwards: if any lane's
 // wait failed, every lane sees false, so the warp leaves its loop as one.

@@ -201,3 +201,18 @@ def test_append_refusals(ea):
         ea.attn_kv_append(k.float(), k, cache, cache, slots)
     with pytest.raises(ea.AttnError):
         ea.attn_kv_append(k, k, cache[:, :12], cache[:, :12], slots)
+
+
+@pytest.mark.parametrize("n,lo,hi,page", [(400, 100, 700, 16), (1500, 1, 150, 64), (3, 40000, 60000, 128)])
+def test_plan_of_many_tokens(ea, n, lo, hi, page):
+    """Shared by as many CTAs as there are, or, in place, by one cluster."""
+    rng = random.Random(n + hi)
+    old = [rng.randrange(0, 2000) for _ in range(n)]
+    new = [-1 if i % 7 == 3 else rng.randint(lo, hi) for i in range(n)]
+    spare = sum(-(-max(x, 0) // page) + 1 for x in new)
+    table, free = _setting(old, page, (2000 + hi) // page + 3, spare, n)
+    tokens = sum(max(x, 0) for x in new) + 100
+    want = paged_ref.plan(old, new, table, free, spare, page, tokens, len(free))
+    assert want[-1] == 0
+    for in_place in (False, True):
+        _same(_run(ea, old, new, table, free, spare, page, tokens, in_place), want)

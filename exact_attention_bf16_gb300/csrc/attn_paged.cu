@@ -489,18 +489,19 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float2 y = sX[(1 - i) * BM + r];
         const float ma = i == 0 ? m_used : y.x, la = i == 0 ? l : y.y, mb = i == 0 ? y.x : m_used, lb = i == 0 ? y.y : l;
         const float mm = fmaxf(ma, mb);
-        const float ea = la > 0.f ? ex2_mufu(ma - mm) : 0.f, eb = lb > 0.f ? ex2_mufu(mb - mm) : 0.f;
+        // (a sum of 0 is a row without keys; a NaN sum is no such row, and stays NaN in O and LSE)
+        const float ea = la != 0.f ? ex2_mufu(ma - mm) : 0.f, eb = lb != 0.f ? ex2_mufu(mb - mm) : 0.f;
         const float lt = la * ea + lb * eb;
-        const float inv_l = lt > 0.f ? 1.f / lt : 0.f;
-        lse2 = lt > 0.f ? mm + log2f(lt) : -INFINITY;
+        const float inv_l = lt != 0.f ? 1.f / lt : 0.f;
+        lse2 = lt != 0.f ? mm + log2f(lt) : -INFINITY;
         w0 = ea * inv_l, w1 = eb * inv_l;
         // (the exchange above also says that the other warpgroup has left the segment before, so
         // that its O barrier is at most one phase behind)
         if (has0) ok = mbar_wait_warp(&bar->o_full[0], w.phase & 1u, a.status, 0x3340);
         if (ok && has1) ok = mbar_wait_warp(&bar->o_full[1], (w.phase >> 1) & 1u, a.status, 0x3341);
       } else {
-        w0 = l > 0.f ? 1.f / l : 0.f;
-        lse2 = l > 0.f ? m_used + log2f(l) : -INFINITY;
+        w0 = l != 0.f ? 1.f / l : 0.f;
+        lse2 = l != 0.f ? m_used + log2f(l) : -INFINITY;
         if (has0) ok = mbar_wait_warp(&bar->o_full[i], (w.phase >> i) & 1u, a.status, 0x3340 + i);
       }
       if (!ok) break;
@@ -603,9 +604,10 @@ __global__ void __launch_bounds__(256) merge_kernel(const PagedArgs a) {
     if (part + u * WPR < m.n) ahead[u] = load_o(part + u * WPR);
   const float lse0 = lane < m.n ? a.part_lse[at(lane)] : -INFINITY;  // segment `lane`'s
   float mx = lse0;
-  for (int r = lane + 32; r < m.n; r += 32) mx = fmaxf(mx, a.part_lse[at(r)]);
+  // (a segment's NaN is kept: dropped, the row would pass for one without keys, or for the other segments' alone)
+  for (int r = lane + 32; r < m.n; r += 32) mx = fmax_nan(mx, a.part_lse[at(r)]);
 #pragma unroll
-  for (int d = 16; d > 0; d >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
+  for (int d = 16; d > 0; d >>= 1) mx = fmax_nan(mx, __shfl_xor_sync(0xffffffffu, mx, d));
   float sum = 0.f, acc[CPL];
 #pragma unroll
   for (int c = 0; c < CPL; ++c) acc[c] = 0.f;
@@ -642,14 +644,14 @@ __global__ void __launch_bounds__(256) merge_kernel(const PagedArgs a) {
       for (int c = 0; c < CPL; ++c) acc[c] += s_acc[w][lane * CPL + c];
     }
   }
-  const float inv = sum > 0.f ? 1.f / sum : 0.f;
+  const float inv = sum != 0.f ? 1.f / sum : 0.f;
   const int64_t head = static_cast<int64_t>(m.hk) * a.kv_group + hd;
   __nv_bfloat16* o = a.o + static_cast<int64_t>(m.q_row + tok) * a.o_row + head * a.o_head + lane * CPL;
   if constexpr (CPL == 4)
     *reinterpret_cast<uint2*>(o) = make_uint2(pack_bf16x2(acc[0] * inv, acc[1] * inv), pack_bf16x2(acc[2] * inv, acc[3] * inv));
   else
     *reinterpret_cast<uint32_t*>(o) = pack_bf16x2(acc[0] * inv, acc[1] * inv);
-  if (lane == 0) a.lse[head * a.total_q + m.q_row + tok] = sum > 0.f ? (mx + log2f(sum)) * 0.69314718055994531f : -INFINITY;
+  if (lane == 0) a.lse[head * a.total_q + m.q_row + tok] = sum != 0.f ? (mx + log2f(sum)) * 0.69314718055994531f : -INFINITY;
 }
 
 // The list of paged_kernel<EVEN = false>: first the parts of the units (request, 2 *

@@ -421,11 +421,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           lb = (l_of[4 * N + row] + l_of[5 * N + row]) + (l_of[6 * N + row] + l_of[7 * N + row]);
         }
         const float mm = fmaxf(ma, mb);
-        const float ea = la > 0.f ? ex2_mufu(ma - mm) : 0.f, eb = lb > 0.f ? ex2_mufu(mb - mm) : 0.f;
+        // (a sum of 0 is a row without keys; a NaN sum is no such row, and stays NaN in O and LSE)
+        const float ea = la != 0.f ? ex2_mufu(ma - mm) : 0.f, eb = lb != 0.f ? ex2_mufu(mb - mm) : 0.f;
         const float lt = la * ea + lb * eb;
-        const float inv = lt > 0.f ? 1.f / lt : 0.f;
+        const float inv = lt != 0.f ? 1.f / lt : 0.f;
         const float w0 = ea * inv, w1 = eb * inv;
-        const float lse2 = lt > 0.f ? mm + log2f(lt) : -INFINITY;
+        const float lse2 = lt != 0.f ? mm + log2f(lt) : -INFINITY;
         const int q_row = w.q_row, head0 = w.hk * a.kv_group;
         if (quarter == 0 && static_cast<int>(lane) < HALF && row < rows) {
           const int tok = row / a.kv_group;

@@ -466,7 +466,8 @@ attn_status_t attn_kv_append(const attn_kv_append_params* p, attn_stream_t strea
  * anything, infinities and NaN included, and reach no result; a non-finite
  * value among a request's own visible keys or values reaches every query row
  * of that request whose 128-key block holds it, also rows that the causal mask
- * hides it from.
+ * hides it from. A row with a NaN or +infinite logit among its visible keys has a
+ * NaN LSE and O, split across SMs or not.
  * P enters the PV product in bf16 (V's type). Results depend on the batch only
  * through the order of additions (keys may be split across SMs and merged in
  * key order): the same call gives the same bits.

@@ -44,7 +44,7 @@ __global__ void combine_kv_splits_kernel(FwdArgs a) {
     const float lr = lane < a.kv_split ? a.lse_part[lane * a.part_rows + row] : -INFINITY;
     float m = lr;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    for (int o = 16; o > 0; o >>= 1) m = fmax_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
     const float w = (lr == -INFINITY) ? 0.f : expf(lr - m);
     float wsum = w;
 #pragma unroll
@@ -68,7 +68,7 @@ __global__ void combine_kv_splits_kernel(FwdArgs a) {
         acc[1] = fmaf(wr, v.y, acc[1]);
       }
     }
-    const float inv = wsum > 0.f ? 1.f / wsum : 0.f;
+    const float inv = wsum != 0.f ? 1.f / wsum : 0.f;
     const int64_t q = row % a.seqlen_q, bh = row / a.seqlen_q;
     const int64_t h = bh % a.heads, b = bh / a.heads;
     __nv_bfloat16* orow = static_cast<__nv_bfloat16*>(a.o) + b * a.o_sb + q * a.o_sn + h * a.o_sh + lane * CPL;
@@ -78,7 +78,7 @@ __global__ void combine_kv_splits_kernel(FwdArgs a) {
     } else {
       *reinterpret_cast<uint32_t*>(orow) = pack_bf16x2(acc[0] * inv, acc[1] * inv);
     }
-    if (lane == 0) a.lse[b * a.lse_sb + h * a.lse_sh + q] = wsum > 0.f ? m + logf(wsum) : -INFINITY;
+    if (lane == 0) a.lse[b * a.lse_sb + h * a.lse_sh + q] = wsum != 0.f ? m + logf(wsum) : -INFINITY;
   }
 }
 

@@ -320,7 +320,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       ok = wait_c_warp(&bar->o_full[i], 0, a.status, 0x1960 + i);
       tc_fence_after();
     }
-    const float inv_l = (l > 0.f) ? 1.f / l : 0.f;
+    const float inv_l = (l != 0.f) ? 1.f / l : 0.f;
     __nv_bfloat16* orow = static_cast<__nv_bfloat16*>(a.o) + static_cast<int64_t>(b) * a.o_sb +
                           static_cast<int64_t>(q_start + row) * a.o_sn + static_cast<int64_t>(h) * a.o_sh;
     const bool store = row < nq;
@@ -345,7 +345,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       }
     }
     if (store) {
-      const float lse = (l > 0.f) ? (m_used + log2f(l)) * 0.69314718055994531f : -INFINITY;
+      const float lse = (l != 0.f) ? (m_used + log2f(l)) * 0.69314718055994531f : -INFINITY;
       a.lse[static_cast<int64_t>(b) * a.lse_sb + static_cast<int64_t>(h) * a.lse_sh + q_start + row] = lse;
     }
   }

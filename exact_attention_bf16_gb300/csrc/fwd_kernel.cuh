@@ -573,7 +573,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       ok = mbar_wait_warp(&bar->o_full[i], 0, a.status, 0x310 + i, poll_lim);
       tc_fence_after();
     }
-    float inv_l = (l > 0.f) ? 1.f / l : 0.f;
+    // (a sum of 0 is a row without keys; a NaN sum is no such row, and stays NaN in O and LSE)
+    float inv_l = (l != 0.f) ? 1.f / l : 0.f;
     if constexpr (F8) inv_l *= a.v_descale;
     const bool store = row < nq;
     if constexpr (SPLITKV) {
@@ -598,7 +599,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                         __uint_as_float(o[4 * t + 2]) * inv_l, __uint_as_float(o[4 * t + 3]) * inv_l);
         }
       }
-      if (store) a.lse_part[prow] = (l > 0.f) ? (m_used + log2f(l)) * 0.69314718055994531f : -INFINITY;
+      if (store) a.lse_part[prow] = (l != 0.f) ? (m_used + log2f(l)) * 0.69314718055994531f : -INFINITY;
     } else {
     __nv_bfloat16* orow = static_cast<__nv_bfloat16*>(a.o) + static_cast<int64_t>(b) * a.o_sb +
                           static_cast<int64_t>(q_start + row) * a.o_sn + static_cast<int64_t>(h) * a.o_sh;
@@ -619,7 +620,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (store) store_row64(orow + c * 32, w);
     }
     if (store) {
-      const float lse = (l > 0.f) ? (m_used + log2f(l)) * 0.69314718055994531f : -INFINITY;
+      const float lse = (l != 0.f) ? (m_used + log2f(l)) * 0.69314718055994531f : -INFINITY;
       a.lse[static_cast<int64_t>(b) * a.lse_sb + static_cast<int64_t>(h) * a.lse_sh + q_start + row] = lse;
     }
     }

@@ -19,7 +19,8 @@
  * Visibility. Key j (of a sequence of Nk keys) is visible to query i (of Nq
  * queries) iff j < Nk and, when causal != 0, j <= i + (Nk - Nq) (causal mask
  * aligned to the bottom-right corner; equals j <= i when Nq == Nk). A query
- * row that sees no key gets O = 0, LSE = -inf and zero gradient.
+ * row that sees no key gets O = 0, LSE = -inf and zero gradient. A row with a
+ * NaN or +infinite logit among its visible keys has a NaN LSE and O.
  *
  * Layouts (all element counts, not bytes). Dense tensors are 4-D
  * [batch, seqlen, heads, head_dim] addressed as

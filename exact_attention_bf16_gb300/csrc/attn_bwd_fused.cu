@@ -26,8 +26,10 @@ __global__ void dq_convert_kernel(const BwdArgs a) {
     const int h = static_cast<int>(bh % a.heads), b = static_cast<int>(bh / a.heads);
     const float4* src = reinterpret_cast<const float4*>(a.dq_acc + rh * D + 8 * c);
     const float4 x = src[0], y = src[1];
-    const uint4 w = make_uint4(pack_bf16x2(x.x * a.scale, x.y * a.scale), pack_bf16x2(x.z * a.scale, x.w * a.scale),
-                               pack_bf16x2(y.x * a.scale, y.y * a.scale), pack_bf16x2(y.z * a.scale, y.w * a.scale));
+    uint4 w = make_uint4(pack_bf16x2(x.x * a.scale, x.y * a.scale), pack_bf16x2(x.z * a.scale, x.w * a.scale),
+                         pack_bf16x2(y.x * a.scale, y.y * a.scale), pack_bf16x2(y.z * a.scale, y.w * a.scale));
+    // a row that sees no key: 0, also beside keys that are not finite (0 x NaN)
+    if (__ldg(a.lse + b * a.lse_sb + h * a.lse_sh + row) == -INFINITY) w = make_uint4(0, 0, 0, 0);
     __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(a.dq) + b * a.dq_sb + static_cast<int64_t>(row) * a.dq_sn +
                          h * a.dq_sh + 8 * c;
     *reinterpret_cast<uint4*>(dst) = w;

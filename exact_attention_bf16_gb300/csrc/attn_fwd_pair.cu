@@ -321,6 +321,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       tc_fence_after();
     }
     const float inv_l = (l != 0.f) ? 1.f / l : 0.f;
+    const bool any = nkv[i] > 0 && l != 0.f;  // else O = 0, also beside values that are not finite (0 x NaN)
     __nv_bfloat16* orow = static_cast<__nv_bfloat16*>(a.o) + static_cast<int64_t>(b) * a.o_sb +
                           static_cast<int64_t>(q_start + row) * a.o_sn + static_cast<int64_t>(h) * a.o_sh;
     const bool store = row < nq;
@@ -334,8 +335,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       uint32_t w[16];
 #pragma unroll
       for (int t = 0; t < 16; ++t) {
-        const float v0 = nkv[i] > 0 ? __uint_as_float(o[2 * t]) * inv_l : 0.f;
-        const float v1 = nkv[i] > 0 ? __uint_as_float(o[2 * t + 1]) * inv_l : 0.f;
+        const float v0 = any ? __uint_as_float(o[2 * t]) * inv_l : 0.f;
+        const float v1 = any ? __uint_as_float(o[2 * t + 1]) * inv_l : 0.f;
         w[t] = pack_bf16x2(v0, v1);
       }
       if (store) {

@@ -479,7 +479,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!ok) break;
       const int r = static_cast<int>(quarter * 32 + lane);
       float lse2;      // the row's LSE in log2 units
-      float w0, w1 = 0.f;  // weights of O_0 (or this tile's O) and, dual, of O_1
+      // Weights of O_0 (or this tile's O) and, dual, of O_1; kNoKeys where the row saw no key: nothing is added then, also
+      // beside values that are not finite (0 x NaN). (A flag beside each weight cost the chunks spills and 3%.)
+      constexpr float kNoKeys = -0.f;
+      float w0, w1 = kNoKeys;
       if (dual) {
         sX[i * BM + r] = make_float2(m_used, l);
         __syncwarp();
@@ -494,13 +497,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float lt = la * ea + lb * eb;
         const float inv_l = lt != 0.f ? 1.f / lt : 0.f;
         lse2 = lt != 0.f ? mm + log2f(lt) : -INFINITY;
-        w0 = ea * inv_l, w1 = eb * inv_l;
+        w0 = la != 0.f ? ea * inv_l : kNoKeys, w1 = lb != 0.f ? eb * inv_l : kNoKeys;
         // (the exchange above also says that the other warpgroup has left the segment before, so
         // that its O barrier is at most one phase behind)
         if (has0) ok = mbar_wait_warp(&bar->o_full[0], w.phase & 1u, a.status, 0x3340);
         if (ok && has1) ok = mbar_wait_warp(&bar->o_full[1], (w.phase >> 1) & 1u, a.status, 0x3341);
       } else {
-        w0 = l != 0.f ? 1.f / l : 0.f;
+        w0 = l != 0.f ? 1.f / l : kNoKeys;
         lse2 = l != 0.f ? m_used + log2f(l) : -INFINITY;
         if (has0) ok = mbar_wait_warp(&bar->o_full[i], (w.phase >> i) & 1u, a.status, 0x3340 + i);
       }
@@ -517,6 +520,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int c_lo = dual ? i * (DV / 64) : 0, c_hi = dual ? (i + 1) * (DV / 64) : DV / 32;  // 32-column groups
         const int64_t prow = static_cast<int64_t>(part) * a.part_rows + (dual ? 0 : i * BM) + r;
         __nv_bfloat16* orow = a.o + static_cast<int64_t>(w.q_row + tok) * a.o_row + static_cast<int64_t>(head) * a.o_head;
+        auto keys = [](float weight) { return __float_as_uint(weight) != __float_as_uint(kNoKeys); };
 #pragma unroll 1
         for (int c = c_lo; c < c_hi; ++c) {
           uint32_t o[32];  // (columns never written are read too, but not used)
@@ -527,13 +531,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             tmem_wait_ld();
 #pragma unroll
             for (int t = 0; t < 32; ++t) {
-              const float x0 = has0 ? __uint_as_float(o[t]) * w0 : 0.f;
-              o[t] = __float_as_uint(has1 ? fmaf(__uint_as_float(o1[t]), w1, x0) : x0);
+              const float x0 = keys(w0) ? __uint_as_float(o[t]) * w0 : 0.f;
+              o[t] = __float_as_uint(keys(w1) ? fmaf(__uint_as_float(o1[t]), w1, x0) : x0);
             }
           } else {
             tmem_wait_ld();
 #pragma unroll
-            for (int t = 0; t < 32; ++t) o[t] = __float_as_uint(has0 ? __uint_as_float(o[t]) * w0 : 0.f);
+            for (int t = 0; t < 32; ++t) o[t] = __float_as_uint(keys(w0) ? __uint_as_float(o[t]) * w0 : 0.f);
           }
           if (valid) {
             if (part >= 0) {

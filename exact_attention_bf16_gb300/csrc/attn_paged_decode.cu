@@ -427,6 +427,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float inv = lt != 0.f ? 1.f / lt : 0.f;
         const float w0 = ea * inv, w1 = eb * inv;
         const float lse2 = lt != 0.f ? mm + log2f(lt) : -INFINITY;
+        // A stream in which the row saw no key (or that has no block) adds nothing, also where its values are not finite
+        // (0 x NaN).
+        const uint32_t keys0 = __ballot_sync(0xffffffffu, la != 0.f), keys1 = __ballot_sync(0xffffffffu, lb != 0.f);
         const int q_row = w.q_row, head0 = w.hk * a.kv_group;
         if (quarter == 0 && static_cast<int>(lane) < HALF && row < rows) {
           const int tok = row / a.kv_group;
@@ -448,8 +451,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int c = 0; c < HALF; ++c) {
             const float x0 = __shfl_sync(0xffffffffu, w0, c), x1 = __shfl_sync(0xffffffffu, w1, c);
-            const float v0 = n > 0 ? __uint_as_float(o0[c]) * x0 : 0.f;
-            const float v = n > 1 ? fmaf(__uint_as_float(o1[c]), x1, v0) : v0;
+            const float v0 = (keys0 >> c) & 1u ? __uint_as_float(o0[c]) * x0 : 0.f;
+            const float v = (keys1 >> c) & 1u ? fmaf(__uint_as_float(o1[c]), x1, v0) : v0;
             const int rw = i * HALF + c;
             if (rw < rows && has_col) {
               if (part >= 0)

@@ -1557,6 +1557,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(a.dq) + U.b * a.dq_sb +
                          static_cast<int64_t>(U.q_start + i) * a.dq_sn + h * a.dq_sh;
     constexpr int CPW = DQK / 2;  // dQ columns per warpgroup (32, 64 or 96)
+    const bool any = T > 0 && lse2 != INFINITY;  // else dQ = 0, also beside keys that are not finite (0 x NaN)
     // split keys: this range's unscaled fp32 dQ row (zero when the range sees no key)
     float* part = split ? a.dq_part + ((static_cast<int64_t>(range) * a.batch + U.b) * a.heads + h) *
                                           static_cast<int64_t>(a.seqlen_q) * DQK +
@@ -1575,7 +1576,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           float4* pv = reinterpret_cast<float4*>(part + col0);
 #pragma unroll
           for (int e = 0; e < 8; ++e)
-            pv[e] = T > 0 ? make_float4(__uint_as_float(v[4 * e]), __uint_as_float(v[4 * e + 1]),
+            pv[e] = any ? make_float4(__uint_as_float(v[4 * e]), __uint_as_float(v[4 * e + 1]),
                                         __uint_as_float(v[4 * e + 2]), __uint_as_float(v[4 * e + 3]))
                           : make_float4(0.f, 0.f, 0.f, 0.f);
         }
@@ -1583,7 +1584,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
 #pragma unroll
       for (int e = 0; e < 16; ++e)
-        w[e] = T > 0 ? pack_bf16x2(__uint_as_float(v[2 * e]) * a.scale, __uint_as_float(v[2 * e + 1]) * a.scale) : 0u;
+        w[e] = any ? pack_bf16x2(__uint_as_float(v[2 * e]) * a.scale, __uint_as_float(v[2 * e + 1]) * a.scale) : 0u;
       if (i < U.nq) store_row_bf16(dst + col0, w);
     }
   }

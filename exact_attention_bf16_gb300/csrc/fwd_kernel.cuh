@@ -576,6 +576,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // (a sum of 0 is a row without keys; a NaN sum is no such row, and stays NaN in O and LSE)
     float inv_l = (l != 0.f) ? 1.f / l : 0.f;
     if constexpr (F8) inv_l *= a.v_descale;
+    const bool any = nkv[i] > 0 && l != 0.f;  // else O = 0, also beside values that are not finite (0 x NaN)
     const bool store = row < nq;
     if constexpr (SPLITKV) {
       // this range's O (normalised over its keys, fp32) and LSE; -inf where it has no key
@@ -613,8 +614,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t w[16];
 #pragma unroll
       for (int t = 0; t < 16; ++t) {
-        const float v0 = nkv[i] > 0 ? __uint_as_float(o[2 * t]) * inv_l : 0.f;
-        const float v1 = nkv[i] > 0 ? __uint_as_float(o[2 * t + 1]) * inv_l : 0.f;
+        const float v0 = any ? __uint_as_float(o[2 * t]) * inv_l : 0.f;
+        const float v1 = any ? __uint_as_float(o[2 * t + 1]) * inv_l : 0.f;
         w[t] = pack_bf16x2(v0, v1);
       }
       if (store) store_row64(orow + c * 32, w);

@@ -19,7 +19,8 @@
  * Visibility. Key j (of a sequence of Nk keys) is visible to query i (of Nq
  * queries) iff j < Nk and, when causal != 0, j <= i + (Nk - Nq) (causal mask
  * aligned to the bottom-right corner; equals j <= i when Nq == Nk). A query
- * row that sees no key gets O = 0, LSE = -inf and zero gradient. A row with a
+ * row that sees no key gets O = 0, LSE = -inf and dQ = 0, whatever the keys and
+ * values beside it hold. A row with a
  * NaN or +infinite logit among its visible keys has a NaN LSE and O.
  *
  * Layouts (all element counts, not bytes). Dense tensors are 4-D
@@ -458,7 +459,8 @@ attn_status_t attn_kv_append(const attn_kv_append_params* p, attn_stream_t strea
  * of nq sees key j <= i + seqlens_k[s] - nq (aligned to the last key); else all
  * keys. o [total_q, heads, d_v] (bf16) and lse [heads, total_q] (fp32,
  * contiguous) as for attn_fwd_varlen, score modifications too; a row that sees
- * no key gets O = 0 and LSE = -inf. Rows of o and lse behind the last request
+ * no key gets O = 0 and LSE = -inf, whatever the keys and values beside it hold.
+ * Rows of o and lse behind the last request
  * are left as they were.
  * Lengths are clamped: seqlens_k to [0, max_pages * page_size], the offsets of
  * q to [0, total_q] and each request's queries to max_seqlen_q (a bound the
@@ -466,8 +468,8 @@ attn_status_t attn_kv_append(const attn_kv_append_params* p, attn_stream_t strea
  * outside [0, num_pages) are masked. Cache rows past seqlens_k may hold
  * anything, infinities and NaN included, and reach no result; a non-finite
  * value among a request's own visible keys or values reaches every query row
- * of that request whose 128-key block holds it, also rows that the causal mask
- * hides it from. A row with a NaN or +infinite logit among its visible keys has a
+ * of that request that sees a key of the 128-key block that holds it, also rows
+ * that the causal mask hides it from. A row with a NaN or +infinite logit among its visible keys has a
  * NaN LSE and O, split across SMs or not.
  * P enters the PV product in bf16 (V's type). Results depend on the batch only
  * through the order of additions (keys may be split across SMs and merged in

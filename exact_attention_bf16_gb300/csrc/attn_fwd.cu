@@ -122,10 +122,18 @@ cudaError_t launch_t(const CUtensorMap& tq, const CUtensorMap& tk, const CUtenso
 // V -> fp16 copy for the PV product (contiguous [rows, heads, d_v], rows = B * N
 // dense or total varlen). One warp per token row: its heads x d_v values are
 // HEADS x DV / 8 units of 16 bytes, a warp-wide unit index split by constant
-// shifts, the (batch, row) division done once per row. Sets *flag when a
-// finite value lies outside fp16's range (|v| >= 65536, which would become
-// inf); inf and NaN convert to themselves.
-template <int DV>
+// shifts, the (batch, row) division done once per row. HBM-bound for long rows: four
+// units per lane in flight where a row has them (8 x 16384 rows of 16 heads of 128:
+// the whole call 347 us, 371 with one), one where it has at most 32 (64 x 500 rows of
+// 3 heads of 64: 26.7 us, 28.6 with four).
+// Sets *flag when a finite value lies above fp16's range (|v| >= 65536, which would
+// become inf), or where fp16 would lose what a row holds: a head's row that is not
+// zero but has no value in fp16's normal range (all |v| < 2^-14). (bf16 values of
+// 2^-17 and more are exact in fp16, its smallest step being 2^-24, smaller ones off by
+// at most 2^-25: 2^-11 of a row's largest value otherwise. Zero rows, and small values
+// beside larger ones, do not set it: P then keeps its 11 bits.) inf and NaN convert to
+// themselves.
+template <int DV, int AHEAD>
 __global__ void v_to_f16_kernel(const void* v, int64_t sb, int64_t sn, int64_t sh, int nb, int nrows, int heads,
                                 void* out, uint32_t* flag) {
   constexpr int UPH = DV / 8;  // 16-byte units per (row, head)
@@ -138,18 +146,35 @@ __global__ void v_to_f16_kernel(const void* v, int64_t sb, int64_t sn, int64_t s
     const int b = static_cast<int>(r / nrows), n = static_cast<int>(r % nrows);
     const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(v) + b * sb + n * sn;
     uint4* dst = static_cast<uint4*>(out) + r * upr;
-#pragma unroll 4
-    for (int i = lane; i < upr; i += 32) {
-      const uint4 x = *reinterpret_cast<const uint4*>(src + (i / UPH) * sh + 8 * (i % UPH));
-      const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-      uint32_t o[4];
+    for (int i0 = lane; i0 - lane < upr; i0 += 32 * AHEAD) {
+      uint4 xs[AHEAD];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const uint32_t lo = w[e] & 0x7FFFu, hi = (w[e] >> 16) & 0x7FFFu;
-        bad |= static_cast<uint32_t>(lo >= 0x4780u && lo < 0x7F80u) | static_cast<uint32_t>(hi >= 0x4780u && hi < 0x7F80u);
-        o[e] = pack_f16x2(__uint_as_float(w[e] << 16), __uint_as_float(w[e] & 0xFFFF0000u));
+      for (int u = 0; u < AHEAD; ++u) {
+        const int i = i0 + 32 * u;
+        xs[u] = i < upr ? *reinterpret_cast<const uint4*>(src + (i / UPH) * sh + 8 * (i % UPH)) : make_uint4(0, 0, 0, 0);
       }
-      dst[i] = make_uint4(o[0], o[1], o[2], o[3]);
+#pragma unroll
+      for (int u = 0; u < AHEAD; ++u) {
+        const int i = i0 + 32 * u;
+        if (i - lane >= upr) break;
+        const uint4 x = xs[u];
+        const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+        uint32_t o[4];
+        const uint32_t m2 = __vmaxu2(__vmaxu2(x.x & 0x7FFF7FFFu, x.y & 0x7FFF7FFFu),
+                                     __vmaxu2(x.z & 0x7FFF7FFFu, x.w & 0x7FFF7FFFu));
+        const uint32_t largest = max(m2 >> 16, m2 & 0xFFFFu);  // of this lane's eight; UPH lanes hold a head's row
+        const uint32_t some = __ballot_sync(0xffffffffu, largest != 0);
+        const uint32_t normal = __ballot_sync(0xffffffffu, largest >= 0x3880u);  // 2^-14
+        const uint32_t row = ((1u << UPH) - 1u) << (lane & ~(UPH - 1));
+        bad |= static_cast<uint32_t>((some & row) != 0 && (normal & row) == 0);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const uint32_t lo = w[e] & 0x7FFFu, hi = (w[e] >> 16) & 0x7FFFu;
+          bad |= static_cast<uint32_t>(lo >= 0x4780u && lo < 0x7F80u) | static_cast<uint32_t>(hi >= 0x4780u && hi < 0x7F80u);
+          o[e] = pack_f16x2(__uint_as_float(w[e] << 16), __uint_as_float(w[e] & 0xFFFF0000u));
+        }
+        if (i < upr) dst[i] = make_uint4(o[0], o[1], o[2], o[3]);
+      }
     }
   }
   // Behind a tile list's kernel, which zeroes the flag and whose lists the next kernel reads: over before this one is.
@@ -196,7 +221,9 @@ cudaError_t launch_v_to_f16(const void* v, int64_t sb, int64_t sn, int64_t sh, i
   const int64_t want = (rows + 7) / 8;  // 8 warps (rows) per block and pass
   const unsigned blocks = static_cast<unsigned>(want < 152 * 8 ? want : 152 * 8);
   if (dv != 64 && dv != 128) return cudaErrorInvalidValue;
-  auto kern = dv == 64 ? fwd::v_to_f16_kernel<64> : fwd::v_to_f16_kernel<128>;
+  const bool one = heads * (dv / 8) <= 32;
+  auto kern = dv == 64 ? (one ? fwd::v_to_f16_kernel<64, 1> : fwd::v_to_f16_kernel<64, 4>)
+                       : (one ? fwd::v_to_f16_kernel<128, 1> : fwd::v_to_f16_kernel<128, 4>);
   if (early) return launch_early(kern, dim3(blocks), 256, 0, stream, v, sb, sn, sh, nb, nrows, heads, out, flag);
   kern<<<blocks, 256, 0, stream>>>(v, sb, sn, sh, nb, nrows, heads, out, flag);
   return cudaGetLastError();

@@ -25,9 +25,10 @@
 // under a stale max a row's largest weights reach 2^8 and carry their own
 // rounding, which with bf16 moves O by up to ~2e-2 on rows that concentrate on
 // a few keys. The MMA takes A and B of one type, so V is read from an fp16 copy
-// made by v_to_f16_kernel before the launch (exact for |v| < 65536). When that
-// pass found a finite value outside fp16's range (a.v16_flag != 0), or no copy
-// was made (a.v16_flag == nullptr), V and P stay bf16 for the whole call.
+// made by v_to_f16_kernel before the launch (exact for 2^-17 <= |v| < 65536). When
+// that pass found a finite value above fp16's range or a row that fp16 cannot hold
+// (a.v16_flag != 0), or no copy was made (a.v16_flag == nullptr), V and P stay bf16
+// for the whole call.
 //
 // This header holds the kernel template and its launch template; the
 // translation units that instantiate it are attn_fwd.cu (no score

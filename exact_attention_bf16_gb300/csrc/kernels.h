@@ -208,8 +208,8 @@ cudaError_t launch_fwd_mod(int d_qk, int d_v, const CUtensorMap& tq, const CUten
                            const CUtensorMap& tv16, const FwdArgs& a, cudaStream_t stream);
 
 // fp16 copy of V (contiguous [nb, nrows, heads, dv]) for the forward's PV
-// product; ORs 1 into *flag (zeroed by the caller) if a finite value is out of
-// fp16's range.
+// product; ORs 1 into *flag (zeroed by the caller) if a finite value is above
+// fp16's range, or a head's row holds only values that it loses bits of.
 // early: behind launch_tile_lists, whose kernel it runs beside (it waits before it sets the flag and before it ends).
 cudaError_t launch_v_to_f16(const void* v, int64_t sb, int64_t sn, int64_t sh, int nb, int nrows, int heads, int dv,
                             void* out, uint32_t* flag, bool early, cudaStream_t stream);

@@ -260,8 +260,9 @@ typedef struct attn_bwd_params {
  * which keeps O within 1e-2 of the exact result where a few keys dominate a
  * row. Its size is 256 + 2 * (keys x heads x d_v) bytes, rounded up to 256;
  * it must be 256-byte aligned. When V holds a finite value with |v| >= 65536
- * (outside fp16's range), that call computes the PV product in bf16
- * instead. A variable-length forward that builds its tile list adds, each
+ * (above fp16's range), or a head's row that is not zero but all below 2^-14
+ * (where fp16 loses bits of bf16 values), that call computes the PV product in
+ * bf16 instead. A variable-length forward that builds its tile list adds, each
  * rounded up to 256, 32 x heads x (total_q / 256 + num_seqs) bytes for the
  * list and 8 x num_seqs bytes of scratch.
  * A dense forward (bf16, d_qk = d_v = 64 or 128, exp2_emu_period 0, no score

@@ -412,7 +412,7 @@ def attn_fwd_varlen(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqlen
         rescale_stats.data_ptr() if rescale_stats is not None else 0, mod, cap, slopes,
         _abi.INPUT_E4M3 if f8 else _abi.INPUT_BF16, float(q_descale), float(k_descale), float(v_descale),
         1 if cta_pair else 0, ks[1])
-    nbytes = _lib.attn_fwd_workspace_size(p)
+    nbytes = _lib.attn_fwd_varlen_workspace_size(p)
     ws, ws_ptr = _workspace_ptr(nbytes, q, stream)
     status = _lib.attn_fwd_varlen(p, ws_ptr, nbytes, _stream_of(stream, q))
     if status:
@@ -541,7 +541,7 @@ def attn_bwd_varlen(q, k, v, out, lse, dout, cu_seqlens_q, cu_seqlens_k, max_seq
         dout.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(),
         0, sd[0], sd[1], 0, tdq[0], tdq[1], 0, tdk[0], tdk[1], 0, tdv[0], tdv[1],
         1 if deterministic else 0, 1 if cta_pair else 0, 0, 0, 0, 1 if single_pass else 0)
-    nbytes = _lib.attn_bwd_workspace_size(p)
+    nbytes = _lib.attn_bwd_varlen_workspace_size(p)
     ws, ws_ptr = _workspace_ptr(nbytes, q, stream)
     status = _lib.attn_bwd_varlen(p, ws_ptr, nbytes, _stream_of(stream, q))
     if status:
@@ -785,6 +785,7 @@ def attention_varlen(q, k, v, cu_seqlens_q, cu_seqlens_k, max_seqlen_q: int, max
                      softcap: Optional[float] = None, alibi_slopes: Optional[torch.Tensor] = None):
     """Autograd wrapper over attn_fwd_varlen / attn_bwd_varlen for packed bf16 tensors q [total_q, H, d_qk],
     k [total_k, Hkv, d_qk] and v [total_k, Hkv, d_v]; ``softcap`` / ``alibi_slopes`` select a score modification.
-    The offsets cover every row: cu_seqlens[-1] is the total (of a buffer with spare rows, pass the used part)."""
+    The offsets cover every row: cu_seqlens[-1] is the total (of a buffer with spare rows, pass the used part: O and the
+    gradients of rows behind the last offset are not written)."""
     return _AttentionVarlen.apply(q, k, v, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, max_seqlen_k, causal,
                                   softmax_scale, deterministic, softcap, alibi_slopes)

@@ -11,7 +11,7 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libattn_gb300.so")
 HEADER_PATH = os.path.join(os.path.dirname(HERE), "include", "attn.h")
 
-ABI_VERSION = 6
+ABI_VERSION = 7
 BWD_NOALLOC_SCRATCH_BYTES = 8 << 20  # ATTN_BWD_NOALLOC_SCRATCH_BYTES
 
 STATUS = {
@@ -140,6 +140,8 @@ def load(path: str = LIB_PATH):
     sig = {
         "attn_fwd_workspace_size": (ctypes.c_size_t, [c_vp]),
         "attn_bwd_workspace_size": (ctypes.c_size_t, [c_vp]),
+        "attn_fwd_varlen_workspace_size": (ctypes.c_size_t, [c_vp]),
+        "attn_bwd_varlen_workspace_size": (ctypes.c_size_t, [c_vp]),
         "attn_fwd": (ctypes.c_int, [c_vp, c_vp, ctypes.c_size_t, c_vp]),
         "attn_fwd_varlen": (ctypes.c_int, [c_vp, c_vp, ctypes.c_size_t, c_vp]),
         "attn_fwd_block_sparse": (ctypes.c_int, [c_vp, c_vp, c_vp, ctypes.c_int32, ctypes.c_int32, c_vp,

@@ -344,6 +344,15 @@ size_t fwd_workspace_bytes(const attn_fwd_params* p, bool varlen) {
          fwd_split_bytes(p, fwd_split_plan(p, varlen));
 }
 
+// The sequences' tensor maps of a packed call, behind the rest of its workspace: used where the caller gives as much.
+size_t fwd_seq_map_bytes(const attn_fwd_params* p) {
+  return round256(2 * static_cast<int64_t>(p->num_seqs) * static_cast<int64_t>(sizeof(CUtensorMap)));
+}
+size_t bwd_seq_map_bytes(const attn_bwd_params* p) {
+  const int64_t n = p->cta_pair ? 6 : 4;
+  return round256(n * p->fwd.num_seqs * static_cast<int64_t>(sizeof(CUtensorMap)));
+}
+
 // diag_limit != 0: the diagnostic launch of attn_diag_wait_timeout instead of the forward.
 attn_status_t run_fwd(const attn_fwd_params* p, bool varlen, cudaStream_t stream, void* ws, size_t ws_bytes,
                       const SparseSpec& sp = {}, uint32_t diag_limit = 0) {
@@ -460,17 +469,28 @@ attn_status_t run_fwd(const attn_fwd_params* p, bool varlen, cudaStream_t stream
   ATTN_TRY(make_map(&tv16, v16, p->d_v, hkv, nk_rows, nb, v16_rows * hkv * p->d_v,
                     static_cast<int64_t>(hkv) * p->d_v, p->d_v, 128));
   const ListPlan lp = fwd_list_plan(p, varlen);
+  SeqMaps maps{};
+  if (varlen && ws_bytes >= need_ws + fwd_seq_map_bytes(p)) {  // V of each sequence, apart from the next one's
+    maps.base[0] = tv, maps.base[1] = tv16;
+    maps.by_keys[0] = maps.by_keys[1] = 1;
+    maps.n = 2;
+    maps.rows_q = p->total_q, maps.rows_k = p->total_k;
+    maps.out = reinterpret_cast<CUtensorMap*>(static_cast<uint8_t*>(ws) + need_ws);
+    a.seq_maps = maps.out;
+  }
   if (lp.use) {  // longest sequences first, no CTA past a sequence's end; also zeroes the flag
     uint8_t* lbase = static_cast<uint8_t*>(ws) + 256 + fwd_v16_bytes(p, varlen);
     TileEntry* list = reinterpret_cast<TileEntry*>(lbase);
     const TileListSpec spec{p->heads, 256, 0, 1, lp.max_nblk, list, lp.bound};
     e = launch_tile_lists(p->cu_seqlens_q, p->cu_seqlens_k, p->num_seqs, &spec, 1,
-                          reinterpret_cast<int64_t*>(lbase + lp.list_bytes), flag, stream);
+                          reinterpret_cast<int64_t*>(lbase + lp.list_bytes), flag, maps, stream);
     if (e != cudaSuccess) return cuda_fail(e, "fwd tile list");
     a.tiles = list;
     a.n_tiles = lp.bound;
   } else {
     e = cudaMemsetAsync(flag, 0, sizeof(uint32_t), stream);
+    if (e == cudaSuccess && maps.n > 0)
+      e = launch_tile_lists(p->cu_seqlens_q, p->cu_seqlens_k, p->num_seqs, nullptr, 0, nullptr, nullptr, maps, stream);
   }
   if (e == cudaSuccess && f8)  // exact: every E4M3 value is an fp16 value, the flag stays 0
     e = launch_v_e4m3_to_f16(p->v, varlen ? 0 : p->v_batch_stride, p->v_row_stride, p->v_head_stride, nb, nk_rows,
@@ -719,6 +739,28 @@ attn_status_t run_bwd(const attn_bwd_params* p, void* ws, size_t ws_bytes, bool 
   cudaError_t e = status_ptr(&a.status);
   if (e != cudaSuccess) return cuda_fail(e, "status word");
 
+  const int nb = varlen ? 1 : f.batch;
+  const int qrows = bwd_dkdv_rows(f.d_qk);
+  CUtensorMap tq, tk, tv, tdo, tq2, tdo2, tq_r, tdo_r;
+  if (nq_rows > 0 && nk_rows > 0) {
+    auto q_map = [&](CUtensorMap* m, int rows) {
+      return make_map(m, f.q, f.d_qk, f.heads, nq_rows, nb, f.q_batch_stride, f.q_row_stride, f.q_head_stride, rows);
+    };
+    auto do_map = [&](CUtensorMap* m, int rows) {
+      return make_map(m, p->dout, f.d_v, f.heads, nq_rows, nb, p->do_batch_stride, p->do_row_stride, p->do_head_stride, rows);
+    };
+    ATTN_TRY(q_map(&tq, 128));
+    ATTN_TRY(do_map(&tdo, 128));
+    ATTN_TRY(q_map(&tq2, qrows));
+    ATTN_TRY(do_map(&tdo2, qrows));
+    if (p->cta_pair) {  // 64-row boxes of the two-SM kernel
+      ATTN_TRY(q_map(&tq_r, 64));
+      ATTN_TRY(do_map(&tdo_r, 64));
+    }
+    ATTN_TRY(make_map(&tk, f.k, f.d_qk, hkv, nk_rows, nb, f.k_batch_stride, f.k_row_stride, f.k_head_stride, 128));
+    ATTN_TRY(make_map(&tv, f.v, f.d_v, hkv, nk_rows, nb, f.v_batch_stride, f.v_row_stride, f.v_head_stride, 128));
+  }
+
   if (nq_rows > 0 && nk_rows > 0 && varlen) {  // tile lists: longest sequences first, no CTA past an end
     const ListPlan kv = bwd_kv_plan(p, varlen), qp = bwd_q_plan(p, varlen);
     uint8_t* lbase = static_cast<uint8_t*>(ws) + bwd_d_bytes(p, varlen);
@@ -740,8 +782,24 @@ attn_status_t run_bwd(const attn_bwd_params* p, void* ws, size_t ws_bytes, bool 
       a.tiles_q = list;
       a.n_tiles_q = qp.bound;
     }
-    if (n > 0) {
-      e = launch_tile_lists(f.cu_seqlens_q, f.cu_seqlens_k, f.num_seqs, specs, n, scratch, nullptr, stream);
+    SeqMaps maps{};
+    const size_t off_maps = off_dkv + bwd_dkv_split_bytes(p, varlen, dkv_split);
+    uint8_t* at = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(ws) + off_maps + 127) & ~uintptr_t(127));
+    if (static_cast<uint8_t*>(ws) + ws_bytes >= at + bwd_seq_map_bytes(p)) {  // each sequence's rows, apart from the next one's
+      maps.base[kMapQ] = tq2, maps.base[kMapDO] = tdo2, maps.base[kMapK] = tk, maps.base[kMapV] = tv;
+      maps.by_keys[kMapK] = maps.by_keys[kMapV] = 1;
+      maps.n = 4;
+      if (p->cta_pair) {
+        maps.base[kMapQr] = tq_r, maps.base[kMapDOr] = tdo_r;
+        maps.n = 6;
+      }
+      maps.rows_q = f.total_q, maps.rows_k = f.total_k;
+      maps.out = reinterpret_cast<CUtensorMap*>(at);
+      a.seq_maps = maps.out;
+      a.n_seq_maps = maps.n;
+    }
+    if (n > 0 || maps.n > 0) {
+      e = launch_tile_lists(f.cu_seqlens_q, f.cu_seqlens_k, f.num_seqs, specs, n, scratch, nullptr, maps, stream);
       if (e != cudaSuccess) return cuda_fail(e, "bwd tile lists");
     }
   }
@@ -752,18 +810,6 @@ attn_status_t run_bwd(const attn_bwd_params* p, void* ws, size_t ws_bytes, bool 
     return e == cudaSuccess ? ATTN_OK : cuda_fail(e, "bwd zero launch");
   }
 
-  const int nb = varlen ? 1 : f.batch;
-  const int qrows = bwd_dkdv_rows(f.d_qk);
-  CUtensorMap tq, tk, tv, tdo, tq2, tdo2;
-  ATTN_TRY(make_map(&tq, f.q, f.d_qk, f.heads, nq_rows, nb, f.q_batch_stride, f.q_row_stride, f.q_head_stride, 128));
-  ATTN_TRY(make_map(&tk, f.k, f.d_qk, hkv, nk_rows, nb, f.k_batch_stride, f.k_row_stride, f.k_head_stride, 128));
-  ATTN_TRY(make_map(&tv, f.v, f.d_v, hkv, nk_rows, nb, f.v_batch_stride, f.v_row_stride, f.v_head_stride, 128));
-  ATTN_TRY(make_map(&tdo, p->dout, f.d_v, f.heads, nq_rows, nb, p->do_batch_stride, p->do_row_stride,
-                    p->do_head_stride, 128));
-  ATTN_TRY(make_map(&tq2, f.q, f.d_qk, f.heads, nq_rows, nb, f.q_batch_stride, f.q_row_stride, f.q_head_stride,
-                    qrows));
-  ATTN_TRY(make_map(&tdo2, p->dout, f.d_v, f.heads, nq_rows, nb, p->do_batch_stride, p->do_row_stride,
-                    p->do_head_stride, qrows));
   auto mark = [&](int i) -> cudaError_t {
     return p->phase_events[i] ? cudaEventRecord(static_cast<cudaEvent_t>(p->phase_events[i]), stream) : cudaSuccess;
   };
@@ -793,11 +839,6 @@ attn_status_t run_bwd(const attn_bwd_params* p, void* ws, size_t ws_bytes, bool 
     return e == cudaSuccess ? ATTN_OK : cuda_fail(e, "bwd single-pass launch");
   }
   if (p->cta_pair) {  // the two-SM kernel (d = 128, no block lists; checked before any launch)
-    CUtensorMap tq_r, tdo_r;
-    ATTN_TRY(make_map(&tq_r, f.q, f.d_qk, f.heads, nq_rows, nb, f.q_batch_stride, f.q_row_stride, f.q_head_stride,
-                      64));
-    ATTN_TRY(make_map(&tdo_r, p->dout, f.d_v, f.heads, nq_rows, nb, p->do_batch_stride, p->do_row_stride,
-                      p->do_head_stride, 64));
     e = launch_bwd_dkdv_pair(tq_r, tq2, tk, tv, tdo_r, tdo2, a, stream);
   } else {
     e = launch_bwd_dkdv(f.d_qk, f.d_v, tq2, tk, tv, tdo2, a, stream);
@@ -1105,6 +1146,18 @@ attn_status_t attn_bwd_block_sparse(const attn_bwd_params* p, const int32_t* kv_
   SparseSpec sp;
   ATTN_TRY(check_block_lists(&p->fwd, kv_count, kv_index, max_kv, lists_per_head, true, &sp));
   return run_bwd(p, workspace, workspace_bytes, false, static_cast<cudaStream_t>(stream), sp);
+}
+
+size_t attn_fwd_varlen_workspace_size(const attn_fwd_params* p) {
+  if (!p || p->cu_seqlens_q == nullptr || p->num_seqs < 1) return 0;
+  const size_t n = fwd_workspace_bytes(p, true);
+  return n ? n + fwd_seq_map_bytes(p) : 0;
+}
+
+size_t attn_bwd_varlen_workspace_size(const attn_bwd_params* p) {
+  if (!p || p->fwd.cu_seqlens_q == nullptr || p->fwd.num_seqs < 1) return 0;
+  const size_t n = attn_bwd_workspace_size(p);
+  return n ? n + 128 + bwd_seq_map_bytes(p) : 0;  // 128: the maps' alignment in a workspace that is only 16-byte aligned
 }
 
 size_t attn_bwd_workspace_size(const attn_bwd_params* p) {

@@ -137,6 +137,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             tma_load_4d(sQ + i * C::Q_BYTES + c * kChunk, &tmq, &bar->q_full[i], c * 64, h, q_start + own_row0(i), b);
         }
         const CUtensorMap* tmvv = f16 ? &tmv16 : &tmv;
+        if (a.seq_maps != nullptr) {  // that of the sequence, whose rows end with it
+          tmvv = a.seq_maps + (2 * static_cast<int64_t>(unit) + (f16 ? 1 : 0));
+          tensormap_acquire(tmvv);
+        }
         int issued = 0;
         bool ok = true;
         for (int j = 0; j < nkv_max && ok; ++j) {

@@ -30,7 +30,7 @@
 #include "kernels.h"
 
 namespace gb300 {
-// The backward's workspace without the optional split-key dQ partials.
+// The backward's workspace without its optional parts.
 size_t bwd_workspace_min_size(const attn_bwd_params* p);
 }  // namespace gb300
 
@@ -66,7 +66,7 @@ extern "C" attn_status_t attn_bwd_noalloc(const attn_bwd_params* p, attn_stream_
   // for the scratch (the workspace size is 0 for it).
   if (f.heads < 1 || (varlen ? (f.total_q < 0 || f.total_k < 0) : (f.batch < 1 || f.seqlen_q < 0 || f.seqlen_k < 0)))
     return ATTN_ERR_INVALID_ARG;
-  // the workspace without the optional split-key dQ partials, which the
+  // the workspace without its optional parts (partials, tensor maps), which the
   // backward uses only when the scratch also holds them
   const size_t need = gb300::bwd_workspace_min_size(p);
   if (need > ATTN_BWD_NOALLOC_SCRATCH_BYTES) return ATTN_ERR_WORKSPACE;  // problem too large for the fixed scratch

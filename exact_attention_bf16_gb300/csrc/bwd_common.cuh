@@ -36,6 +36,11 @@ __device__ __forceinline__ Unit unit_bounds(const BwdArgs& a, int unit) {
   return u;
 }
 
+// Map `which` of the unit's sequence (a.seq_maps != nullptr).
+__device__ __forceinline__ const CUtensorMap* seq_map(const BwdArgs& a, const Unit& U, SeqMapBwd which) {
+  return a.seq_maps + (static_cast<int64_t>(U.unit) * a.n_seq_maps + which);
+}
+
 // A backward CTA's work: from the tile list of a packed variable-length
 // launch (`tiles` non-null), else from the block index over nblk blocks per
 // (unit, head), blocks in descending (dQ: the last query blocks are the

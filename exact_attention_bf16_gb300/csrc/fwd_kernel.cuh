@@ -301,7 +301,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       tma_prefetch_desc(&tmk);
       const int hk = kv_head(a, h);  // the K/V head of this query head
       // read while the Q copies fly: V from the fp16 copy, or the bf16 original
-      const CUtensorMap* tmvv = v_is_f16(a) ? &tmv16 : &tmv;
+      const bool vf16 = v_is_f16(a);
+      const CUtensorMap* tmvv = vf16 ? &tmv16 : &tmv;
+      if (a.seq_maps != nullptr) {  // that of the sequence, whose rows end with it (looked up anew, not kept in a register)
+        const int seq = LIST ? __ldg(&a.tiles[blockIdx.x].seq)
+                             : grid_slot(static_cast<int>(blockIdx.x), a.num_units * a.heads, a.n_mblk, a.n_groups).pair / a.heads;
+        tmvv = a.seq_maps + (2 * static_cast<int64_t>(seq) + (vf16 ? 1 : 0));
+        tensormap_acquire(tmvv);
+      }
       tma_prefetch_desc(tmvv);
       if constexpr (C::SPLIT) {
         // Split rings: K0, then K(j+1) before V(j), since a K slot frees a step

@@ -128,8 +128,21 @@ struct TileListSpec {
   TileEntry* out;
   int64_t bound;
 };
+// Beside them, in blocks of their own, the sequences' tensor maps (when given): map m of sequence s,
+// out[s * n + m], is base[m] with its rows ending where the sequence's queries or keys do, so that
+// the rows behind them, which belong to the next sequence, read as zeros in the tile that the
+// sequence ends in (0 x NaN is NaN: an infinity or NaN there would reach this sequence through its
+// zero weights). A kernel only takes its copies' maps from there.
+constexpr int kMaxSeqMaps = 6;
+struct SeqMaps {
+  CUtensorMap base[kMaxSeqMaps];
+  int by_keys[kMaxSeqMaps];  // 1: rows are keys, 0: queries
+  int n = 0;
+  int rows_q = 0, rows_k = 0;  // of the packed tensors
+  CUtensorMap* out = nullptr;
+};
 cudaError_t launch_tile_lists(const int* cu_q, const int* cu_k, int num_seqs, const TileListSpec* specs, int n,
-                              int64_t* scratch, uint32_t* zero_word, cudaStream_t stream);
+                              int64_t* scratch, uint32_t* zero_word, const SeqMaps& maps, cudaStream_t stream);
 
 // Forward kernel arguments (passed by value; tensor maps go separately as
 // __grid_constant__ parameters).
@@ -188,6 +201,8 @@ struct FwdArgs {
   // < 2^32. (The two divisions themselves cost the dense kernel 1%.)
   int kv_group;
   uint64_t kv_inv;
+  // Packed variable-length only (or nullptr): sequence s's maps of V (2 s) and of its fp16 copy (2 s + 1), SeqMaps.
+  const CUtensorMap* seq_maps;
 };
 
 cudaError_t launch_fwd(int d_qk, int d_v, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
@@ -305,7 +320,13 @@ struct BwdArgs {
   // head][d_qk + d_v]; launch_bwd_dkv_merge adds them in order.
   int dkv_split;
   float* dkv_part;
+  // Packed variable-length only (or nullptr): sequence s's maps, from seq_maps + s * n_seq_maps on, in the order of
+  // SeqMapBwd (SeqMaps).
+  const CUtensorMap* seq_maps;
+  int n_seq_maps;
 };
+// Q and dO as the dK/dV kernels copy them, K and V, and (the two-SM kernel) Q and dO with 64-row boxes.
+enum SeqMapBwd : int { kMapQ = 0, kMapDO, kMapK, kMapV, kMapQr, kMapDOr };
 
 // Single-pass backward (d_qk = d_v = 64): dK, dV and the fp32 dQ partials of
 // the dK/dV kernel (a.dq_acc, ordered by a.dq_sem when set), then

@@ -163,6 +163,24 @@ __device__ __forceinline__ void tma_load_4d(void* dst, const void* tmap, uint64_
       : "memory");
 }
 
+// Tensor maps made on the device: the extent of dimension 2 of a map in shared memory is
+// replaced, the whole warp copies the map to global memory (128 bytes, 128-byte aligned), and a
+// later kernel's thread acquires it there before its first copy with it.
+__device__ __forceinline__ void tensormap_set_dim2(void* map, uint32_t extent) {
+  asm volatile("tensormap.replace.tile.global_dim.shared::cta.b1024.b32 [%0], 2, %1;" ::"r"(smem_u32(map)), "r"(extent)
+               : "memory");
+}
+__device__ __forceinline__ void tensormap_publish(void* dst, const void* map) {
+  asm volatile(
+      "tensormap.cp_fenceproxy.global.shared::cta.tensormap::generic.release.gpu.sync.aligned [%0], [%1], 128;" ::"l"(
+          __cvta_generic_to_global(dst)),
+      "r"(smem_u32(map))
+      : "memory");
+}
+__device__ __forceinline__ void tensormap_acquire(const void* map) {
+  asm volatile("fence.proxy.tensormap::generic.acquire.gpu [%0], 128;" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
+}
+
 // ---------------------------------------------------------------------------
 // Tensor Memory
 // ---------------------------------------------------------------------------

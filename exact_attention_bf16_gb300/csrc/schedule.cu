@@ -18,12 +18,16 @@
 // then one warp per sequence writes its entries. Sequences with the same
 // block count are placed in arrival order of an atomic counter; the order
 // affects only scheduling, never a result.
+//
+// The same launch makes the sequences' tensor maps (SeqMaps), a warp per map.
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cstddef>
 #include <cstdint>
 
 #include "kernels.h"
+#include "ptx_sm100.cuh"
 
 namespace gb300 {
 namespace sched {
@@ -31,11 +35,30 @@ namespace sched {
 constexpr int kThreads = 1024;
 constexpr int kSharedSeqs = 1024;  // up to so many sequences need no scratch in global memory
 
-// Block b builds list b (a backward's two lists in one launch).
+// Block b < n_lists builds list b (a backward's two lists in one launch), the blocks behind them the tensor maps.
 __global__ void __launch_bounds__(kThreads, 1)
-    tile_list_kernel(const int* cu_q, const int* cu_k, int num_seqs, TileListSpec l0, TileListSpec l1,
-                     int64_t* scratch, uint32_t* zero_word) {
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the next kernel reads no list
+    tile_list_kernel(const int* cu_q, const int* cu_k, int num_seqs, TileListSpec l0, TileListSpec l1, int n_lists,
+                     int64_t* scratch, uint32_t* zero_word, const __grid_constant__ SeqMaps maps) {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the next kernel reads no list and no map
+  if (static_cast<int>(blockIdx.x) >= n_lists) {
+    __shared__ alignas(128) uint32_t s_map[kThreads / 32][32];
+    const int ln = static_cast<int>(threadIdx.x & 31u), wp = static_cast<int>(threadIdx.x >> 5);
+    const int64_t count = static_cast<int64_t>(num_seqs) * maps.n;
+    for (int64_t x = (static_cast<int64_t>(blockIdx.x) - n_lists) * (kThreads / 32) + wp; x < count;
+         x += (static_cast<int64_t>(gridDim.x) - n_lists) * (kThreads / 32)) {
+      const int s = static_cast<int>(x / maps.n), m = static_cast<int>(x - static_cast<int64_t>(s) * maps.n);
+      s_map[wp][ln] = reinterpret_cast<const uint32_t*>(&maps.base[m])[ln];
+      __syncwarp();
+      if (ln == 0) {
+        const int end = maps.by_keys[m] ? min(cu_k[s + 1], maps.rows_k) : min(cu_q[s + 1], maps.rows_q);
+        tensormap_set_dim2(s_map[wp], static_cast<uint32_t>(max(end, 1)));
+      }
+      __syncwarp();
+      tensormap_publish(maps.out + x, s_map[wp]);
+      __syncwarp();
+    }
+    return;
+  }
   const TileListSpec& l = blockIdx.x == 0 ? l0 : l1;
   const int heads = l.heads, rows_per_block = l.rows_per_block, by_keys = l.by_keys, descending = l.descending,
             max_nblk = l.max_nblk;
@@ -126,19 +149,29 @@ __global__ void __launch_bounds__(kThreads, 1)
 }  // namespace sched
 
 cudaError_t launch_tile_lists(const int* cu_q, const int* cu_k, int num_seqs, const TileListSpec* specs, int n,
-                              int64_t* scratch, uint32_t* zero_word, cudaStream_t stream) {
-  if (num_seqs < 0 || n < 0 || n > 2) return cudaErrorInvalidValue;
+                              int64_t* scratch, uint32_t* zero_word, const SeqMaps& maps, cudaStream_t stream) {
+  static_assert(sizeof(CUtensorMap) == 128, "a warp copies a map, four bytes a lane");
+  if (num_seqs < 0 || n < 0 || n > 2 || maps.n < 0 || maps.n > kMaxSeqMaps || (maps.n > 0 && maps.out == nullptr) ||
+      (reinterpret_cast<uintptr_t>(maps.out) & 127u))
+    return cudaErrorInvalidValue;
   for (int i = 0; i < n; ++i)
     if (specs[i].max_nblk < 0 || specs[i].max_nblk > kMaxListBlocks || specs[i].rows_per_block <= 0)
       return cudaErrorInvalidValue;
   // more sequences than shared memory holds starts for: one list after another in the scratch
-  const int per_launch = num_seqs <= sched::kSharedSeqs ? n : 1;
-  for (int i = 0; i < n; i += per_launch) {
-    sched::tile_list_kernel<<<per_launch, sched::kThreads, 0, stream>>>(cu_q, cu_k, num_seqs, specs[i],
-                                                                       specs[i + per_launch - 1], scratch, zero_word);
+  const int per_launch = num_seqs <= sched::kSharedSeqs ? n : std::min(n, 1);
+  const int64_t map_warps = static_cast<int64_t>(num_seqs) * maps.n;
+  const int map_blocks = static_cast<int>(std::min<int64_t>((map_warps + sched::kThreads / 32 - 1) / (sched::kThreads / 32), 152));
+  int i = 0;
+  do {
+    const int blocks = per_launch + (i == 0 ? map_blocks : 0);
+    if (blocks == 0) break;
+    const TileListSpec l0 = n > 0 ? specs[i] : TileListSpec{}, l1 = n > 0 ? specs[i + per_launch - 1] : TileListSpec{};
+    sched::tile_list_kernel<<<blocks, sched::kThreads, 0, stream>>>(cu_q, cu_k, num_seqs, l0, l1, per_launch, scratch,
+                                                                   zero_word, maps);
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-  }
+    i += per_launch;
+  } while (i < n);
   return cudaSuccess;
 }
 

@@ -65,7 +65,7 @@
 extern "C" {
 #endif
 
-#define ATTN_ABI_VERSION 6
+#define ATTN_ABI_VERSION 7
 
 typedef enum {
   ATTN_OK = 0,
@@ -98,10 +98,12 @@ typedef void* attn_stream_t;
  * cu_seqlens_k are device int32 arrays of num_seqs+1 non-decreasing offsets
  * starting at 0; total_q / total_k are the packed row counts (= last offset),
  * max_seqlen_q / max_seqlen_k bound every sequence's length; batch and the
- * batch strides are ignored. The last tile of a sequence also reads the rows
- * behind its end, with weight zero, so an infinity or NaN in one sequence's
- * rows can reach the sequence before it (0 x NaN is NaN); a buffer with spare
- * rows is passed as its used part. Work scheduling (the tile scheduler for
+ * batch strides are ignored. Sequences do not reach one another, whatever their
+ * rows or spare rows behind the last offset hold, in a call that is given
+ * attn_fwd_varlen_workspace_size (attn_bwd_varlen_workspace_size) bytes of
+ * workspace; given less, the last tile of a sequence reads the rows behind its
+ * end with weight zero, and an infinity or NaN there makes results of the
+ * sequence NaN (0 x NaN is NaN). Work scheduling (the tile scheduler for
  * variable-length balance of newton wiki "FlashAttention-4", 核心技術): when
  * max_seqlen_q <= 2047 x 256 (forward), or max_seqlen_q and max_seqlen_k <=
  * 2047 x 128 (backward, per kernel), the call first builds on the stream, in
@@ -300,6 +302,12 @@ typedef struct attn_bwd_params {
  * a call given less runs unsplit. */
 size_t attn_fwd_workspace_size(const attn_fwd_params* p);
 size_t attn_bwd_workspace_size(const attn_bwd_params* p);
+/* The workspace of a variable-length call that keeps its sequences apart
+ * (attn_fwd_params): the above and behind it the sequences' tensor maps, 2 x 128
+ * bytes per sequence forward, 4 x 128 (6 x 128 with cta_pair) backward, rounded up
+ * to 256, and 128 more backward. 0 for other calls. */
+size_t attn_fwd_varlen_workspace_size(const attn_fwd_params* p);
+size_t attn_bwd_varlen_workspace_size(const attn_bwd_params* p);
 
 /* Dense forward: O, LSE from Q, K, V. */
 attn_status_t attn_fwd(const attn_fwd_params* p, void* workspace, size_t workspace_bytes, attn_stream_t stream);
@@ -357,8 +365,9 @@ attn_status_t attn_bwd_block_sparse(const attn_bwd_params* p, const int32_t* kv_
  * ATTN_BWD_NOALLOC_SCRATCH_BYTES bytes per GPU that loads the library, held
  * until process exit. The attention method has no counterpart to this entry
  * point; it exists only for these callers. Limit: the workspace that
- * attn_bwd would need, without the split-key dQ partials (which it uses only
- * when the array also holds them), must not exceed
+ * attn_bwd would need, without the split-key dQ and split-group dK/dV partials
+ * and the sequences' tensor maps (which it uses only where the array also holds
+ * them), must not exceed
  * ATTN_BWD_NOALLOC_SCRATCH_BYTES (4 bytes per batch x head x
  * query row, so up to 2,097,152 such rows dense; variable length adds the
  * tile lists), else ATTN_ERR_WORKSPACE and

@@ -74,7 +74,7 @@ struct Cfg {
   static constexpr int OFF_X = OFF_V + NV * V_BYTES;  // the streams' (m, l): [2 streams][128] float2
   static constexpr int OFF_SEG = OFF_X + 2 * BM * 8;
   static constexpr int OFF_BAR = OFF_SEG + kSegs * 64;
-  static constexpr int SMEM = OFF_BAR + 512;  // the base is 1024-byte aligned (checked)
+  static constexpr int SMEM = OFF_BAR + 640;  // the base is 1024-byte aligned (checked)
   static_assert(SMEM <= 232448, "shared memory budget");
   static constexpr uint32_t REG_LO = 96, REG_HI = 200;
   static constexpr int REG_BUDGET = 128 * REG_LO + 256 * REG_HI;
@@ -96,7 +96,7 @@ struct Bars {
   uint32_t tmem_base;
   EvenStart even;
 };
-static_assert(sizeof(Bars) <= 512, "barriers must fit their reserved bytes");
+static_assert(sizeof(Bars) <= 640, "barriers must fit their reserved bytes");
 
 // EVEN: the even split of all units' key blocks (at most one tile of rows per
 // request); else the list of chunk_list_kernel.

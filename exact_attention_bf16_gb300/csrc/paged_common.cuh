@@ -46,21 +46,23 @@ static_assert(sizeof(Seg) == 64, "OFF_SEG");
 
 __device__ __forceinline__ int ceil_div(int a, int b) { return (a + b - 1) / b; }
 
-// Bounds of request s: rows of q (clamped to the rows there are and to max_q) and keys.
+// Bounds of request s: its rows of q (clamped to the rows there are), those that are computed (the first max_q of
+// them) and its keys. The causal mask aligns the last of all rows with the last key.
 struct Bounds {
-  int q0, nq, nk;
+  int q0, n, nq, nk;
 };
 __device__ __forceinline__ Bounds bounds(const PagedArgs& a, int s) {
   const int c0 = __ldg(a.cu_q + s), c1 = __ldg(a.cu_q + s + 1), k = __ldg(a.seqlens_k + s);
   Bounds b;
   b.q0 = max(0, min(c0, a.total_q));
-  b.nq = max(0, min(min(c1, a.total_q) - b.q0, a.max_q));
+  b.n = max(0, min(c1, a.total_q) - b.q0);
+  b.nq = min(b.n, a.max_q);
   b.nk = max(0, min(k, a.max_keys));
   return b;
 }
 // Keys that tokens up to `last` (0-based in the request) see.
 __device__ __forceinline__ int keys_seen(const PagedArgs& a, const Bounds& b, int last) {
-  return a.causal ? max(0, min(b.nk, last + b.nk - b.nq + 1)) : b.nk;
+  return a.causal ? max(0, min(b.nk, last + b.nk - b.n + 1)) : b.nk;
 }
 // Key blocks that a unit of a request costs; a unit whose rows see no key still writes them.
 __device__ __forceinline__ int unit_blocks(const PagedArgs& a, const Bounds& b, int last) {
@@ -75,7 +77,7 @@ __device__ __forceinline__ Seg make_seg(const PagedArgs& a, const Bounds& b, int
   g.seq = s, g.hk = hk;
   g.q_row = b.q0 + tok0;
   g.ntok = ntok;
-  g.pos0 = tok0 + b.nk - b.nq;
+  g.pos0 = tok0 + b.nk - b.n;
   g.nk = b.nk;
   g.kt0 = kt0;
   g.dual = ntok <= a.tile_tokens ? 1 : 0;
@@ -122,7 +124,7 @@ __device__ __forceinline__ void even_split(const PagedArgs& a, EvenStart* e) {
     for (int s0 = 0; s0 < a.num_seqs; s0 += kThreads) {
       const int s = s0 + tid;
       int n = 0;
-      Bounds b{0, 0, 0};
+      Bounds b{0, 0, 0, 0};
       if (s < a.num_seqs) {
         b = bounds(a, s);
         n = b.nq > 0 ? unit_blocks(a, b, b.nq - 1) : 0;
@@ -180,7 +182,7 @@ __device__ __forceinline__ void even_split(const PagedArgs& a, EvenStart* e) {
 // run by one warp, all lanes alike.
 struct EvenWalk {
   int s = 0, hk = 0, kt = 0, unit = 0;
-  Bounds b{0, 0, 0}, b_next{0, 0, 0};  // request s and, fetched ahead, s + 1
+  Bounds b{0, 0, 0, 0}, b_next{0, 0, 0, 0};  // request s and, fetched ahead, s + 1
   long long g = 0, range1 = 0;
   bool merged = false;  // a unit begins in this range and ends beyond it: at most one
 

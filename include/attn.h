@@ -473,8 +473,9 @@ attn_status_t attn_kv_append(const attn_kv_append_params* p, attn_stream_t strea
  * Rows of o and lse behind the last request
  * are left as they were.
  * Lengths are clamped: seqlens_k to [0, max_pages * page_size], the offsets of
- * q to [0, total_q] and each request's queries to max_seqlen_q (a bound the
- * caller gives; it sizes the launch). Keys on a page whose table entry is
+ * q to [0, total_q]. max_seqlen_q is a bound the caller gives; it sizes the
+ * launch: of a request with more queries the first max_seqlen_q are computed,
+ * as they are with a larger bound, and the rows of the others left as they were. Keys on a page whose table entry is
  * outside [0, num_pages) are masked. Cache rows past seqlens_k may hold
  * anything, infinities and NaN included, and reach no result; a non-finite
  * value among a request's own visible keys or values reaches every query row

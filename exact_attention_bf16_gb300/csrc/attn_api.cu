@@ -814,13 +814,15 @@ attn_status_t run_bwd(const attn_bwd_params* p, void* ws, size_t ws_bytes, bool 
     return p->phase_events[i] ? cudaEventRecord(static_cast<cudaEvent_t>(p->phase_events[i]), stream) : cudaSuccess;
   };
   const bool lists = a.tiles_kv != nullptr || a.tiles_q != nullptr;
-  if (varlen && f.max_seqlen_k <= kFewKeys) {
+  const bool all_few = max_k <= kFewKeys;  // no row sees more keys
+  if (!all_few) e = launch_bwd_preprocess(f.d_v, a, lists, stream);
+  if (e == cudaSuccess && (all_few || varlen)) {  // (packed: some sequences may be as short)
     auto bf = [](const void* x) { return static_cast<const __nv_bfloat16*>(x); };
-    const FewKeys t{bf(f.q), bf(f.k), bf(f.v), f.q_row_stride, f.q_head_stride, f.k_row_stride, f.k_head_stride,
-                    f.v_row_stride, f.v_head_stride};
-    e = launch_bwd_few_keys_dsum(f.d_qk, f.d_v, a, t, lists, stream);
-  } else {
-    e = launch_bwd_preprocess(f.d_v, a, lists, stream);
+    const bool b = !varlen;
+    const FewKeys t{bf(f.q), bf(f.k), bf(f.v), b ? f.q_batch_stride : 0, f.q_row_stride, f.q_head_stride,
+                    b ? f.k_batch_stride : 0, f.k_row_stride, f.k_head_stride, b ? f.v_batch_stride : 0, f.v_row_stride,
+                    f.v_head_stride};
+    e = launch_bwd_few_keys_dsum(f.d_qk, f.d_v, a, t, lists || !all_few, stream);
   }
   if (e == cudaSuccess && sp.kv_count) e = launch_bwd_transpose_lists(a, n_kb_sparse, stream);
   if (e == cudaSuccess) e = mark(0);

@@ -16,6 +16,7 @@ template <int DV>
 __global__ void __launch_bounds__(256, 8) preprocess_kernel(const BwdArgs a) {
   constexpr int LPR = DV / 8;    // lanes per row
   constexpr int RPW = 32 / LPR;  // rows per warp
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // few_keys_dsum_kernel, where it follows
   const int64_t rows = static_cast<int64_t>(a.batch) * a.seqlen_q * a.heads;
   const int64_t warp0 = (blockIdx.x * static_cast<int64_t>(blockDim.x) + threadIdx.x) >> 5;
   const int64_t nwarps = (static_cast<int64_t>(gridDim.x) * blockDim.x) >> 5;
@@ -52,65 +53,71 @@ __global__ void __launch_bounds__(256, 8) preprocess_kernel(const BwdArgs a) {
 
 
 
-// D of packed sequences that all have few keys, as sum_j P_ij (dO_i . v_j) with P from the LSE, all in fp32. The same
-// number in exact arithmetic, but O comes rounded to bf16, and its error d is the same in all dS_ij =
+// D of the rows of sequences (dense: calls) of at most kFewKeys keys, as sum_j P_ij (dO_i . v_j) with P from the LSE, all
+// in fp32. The same number in exact arithmetic, but O comes rounded to bf16, and its error d is the same in all dS_ij =
 // P_ij (dO_i . v_j - D_i): dQ_i is off by d sum_j P_ij k_j, d up to 2^-8 |dO_i| |O_i|, beside a dQ_i that shrinks as the
 // v_j of its keys differ less from their mean O_i. Over sequences of one and two tokens dQ and dK came out 5.0e-3 from the
-// exact ones (norms), now below 2.9e-3; from 9 keys on it is at most 3.1e-3 from the rounded O, too. (A choice per
-// sequence, in the pass above, cost the rows of longer ones 40% of its time.) Latency-bound: 8 lanes share a row, one key
-// each at a time.
+// exact ones (norms), now below 2.9e-3; from 9 keys on it is at most 3.1e-3 from the rounded O, too. Which rows are taken
+// depends on their sequence alone, so that a sequence has the same gradients in every batch. Where a packed batch may hold
+// longer sequences this runs behind the pass above, beside its end, and replaces its D. (A choice per sequence in that
+// pass cost the rows of longer ones 40% of its time.) Latency-bound: 8 lanes share a row, one key each.
+// Block x takes units x, x + gridDim.x, ..., its rows shared by the blocks along y.
 template <int DQK, int DV, int MOD>
-__global__ void few_keys_dsum_kernel(const BwdArgs a, const FewKeys t) {
-  const int64_t rows = static_cast<int64_t>(a.seqlen_q) * a.heads;
-  const int64_t r = (blockIdx.x * static_cast<int64_t>(blockDim.x) + threadIdx.x) >> 3;
+__global__ void __launch_bounds__(256) few_keys_dsum_kernel(const BwdArgs a, const FewKeys t) {
   const int l = static_cast<int>(threadIdx.x & 7u);
-  float acc = 0.f;
-  const int i = static_cast<int>(r / a.heads), h = static_cast<int>(r % a.heads);
-  bool mine = r < rows;
-  if (mine) {
-    int s = 0;  // the sequence of row i: the last one that begins at or before it
-    for (int e = a.num_units; s + 1 < e;) {
-      const int m = (s + e) / 2;
-      if (a.cu_q[m] <= i) s = m;
-      else e = m;
-    }
-    const int q_end = a.cu_q[s + 1], k_start = a.cu_k[s], nk = a.cu_k[s + 1] - k_start;
-    // rows of no sequence are not read later either; offsets past the tensors are not followed
-    mine = i >= a.cu_q[s] && i < q_end && k_start >= 0 && k_start + nk <= a.seqlen_k;
-    const int pos = i - q_end + nk;  // the row's position among the keys
-    const float lse = mine ? a.lse[h * a.lse_sh + i] : -INFINITY;
-    const int keys = lse == -INFINITY ? 0 : (a.causal ? min(nk, pos + 1) : nk);
-    const __nv_bfloat16* q = t.q + i * t.q_sn + h * t.q_sh;
-    const __nv_bfloat16* g = static_cast<const __nv_bfloat16*>(a.dout) + i * a.do_sn + h * a.do_sh;
-    const int hk = h / a.kv_group;
-    auto dot = [](const __nv_bfloat16* x, const __nv_bfloat16* y, int n) {
-      float2 sum = make_float2(0.f, 0.f);
-      for (int c = 0; c < n; c += 8) {
-        const uint4 xv = *reinterpret_cast<const uint4*>(x + c), yv = *reinterpret_cast<const uint4*>(y + c);
-        const uint32_t xw[4] = {xv.x, xv.y, xv.z, xv.w}, yw[4] = {yv.x, yv.y, yv.z, yv.w};
+  for (int unit = static_cast<int>(blockIdx.x); unit < a.num_units; unit += static_cast<int>(gridDim.x)) {
+    const Unit U = unit_bounds(a, unit);
+    // offsets past the tensors are not followed
+    if (U.nk < 1 || U.nk > kFewKeys || U.q_start < 0 || U.k_start < 0 || U.q_start + U.nq > a.seqlen_q ||
+        U.k_start + U.nk > a.seqlen_k)
+      continue;
+    const int64_t rows = static_cast<int64_t>(U.nq) * a.heads;
+    for (int64_t r0 = blockIdx.y * 32 + (threadIdx.x >> 5) * 4; r0 < rows; r0 += gridDim.y * 32) {  // four rows a warp
+      const int64_t r = r0 + ((threadIdx.x >> 3) & 3u);
+      const bool mine = r < rows;
+      const int i = static_cast<int>(r / a.heads), h = static_cast<int>(r % a.heads);
+      const int64_t at = U.b * a.lse_sb + h * a.lse_sh + U.q_start + i;
+      float acc = 0.f;
+      if (mine) {
+        const int pos = i - U.nq + U.nk;  // the row's position among the keys
+        const float lse = a.lse[at];
+        const int keys = lse == -INFINITY ? 0 : (a.causal ? min(U.nk, pos + 1) : U.nk);
+        const int64_t row = U.q_start + i;
+        const __nv_bfloat16* q = t.q + U.b * t.q_sb + row * t.q_sn + h * t.q_sh;
+        const __nv_bfloat16* g = static_cast<const __nv_bfloat16*>(a.dout) + U.b * a.do_sb + row * a.do_sn + h * a.do_sh;
+        const int hk = h / a.kv_group;
+        auto dot = [](const __nv_bfloat16* x, const __nv_bfloat16* y, int n) {
+          float2 sum = make_float2(0.f, 0.f);
+          for (int c = 0; c < n; c += 8) {
+            const uint4 xv = *reinterpret_cast<const uint4*>(x + c), yv = *reinterpret_cast<const uint4*>(y + c);
+            const uint32_t xw[4] = {xv.x, xv.y, xv.z, xv.w}, yw[4] = {yv.x, yv.y, yv.z, yv.w};
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float2 xf = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&xw[e]));
-          const float2 yf = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&yw[e]));
-          sum.x = fmaf(xf.x, yf.x, sum.x);
-          sum.y = fmaf(xf.y, yf.y, sum.y);
+            for (int e = 0; e < 4; ++e) {
+              const float2 xf = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&xw[e]));
+              const float2 yf = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&yw[e]));
+              sum.x = fmaf(xf.x, yf.x, sum.x);
+              sum.y = fmaf(xf.y, yf.y, sum.y);
+            }
+          }
+          return sum.x + sum.y;
+        };
+        static_assert(kFewKeys <= 8, "a key per lane");
+        if (l < keys) {
+          const int64_t kr = U.k_start + l;
+          float x = dot(q, t.k + U.b * t.k_sb + kr * t.k_sn + hk * t.k_sh, DQK);
+          if (MOD == kModSoftcap) x = a.mod_b * tanh_scaled(x, a.mod_k2);
+          if (MOD == kModAlibi) x -= fabsf(a.alibi_slopes[h] * a.inv_scale * static_cast<float>(l - pos));
+          const float p = exp2f(fmaf(x, a.scale_log2, -lse * 1.4426950408889634f));
+          acc = p * dot(g, t.v + U.b * t.v_sb + kr * t.v_sn + hk * t.v_sh, DV);
         }
       }
-      return sum.x + sum.y;
-    };
-    for (int j = l; j < keys; j += 8) {
-      const int64_t row = k_start + j;
-      float x = dot(q, t.k + row * t.k_sn + hk * t.k_sh, DQK);
-      if (MOD == kModSoftcap) x = a.mod_b * tanh_scaled(x, a.mod_k2);
-      if (MOD == kModAlibi) x -= fabsf(a.alibi_slopes[h] * a.inv_scale * static_cast<float>(j - pos));
-      const float p = exp2f(fmaf(x, a.scale_log2, -lse * 1.4426950408889634f));
-      acc = fmaf(p, dot(g, t.v + row * t.v_sn + hk * t.v_sh, DV), acc);
+#pragma unroll
+      for (int d = 4; d > 0; d >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, d);
+      asm volatile("griddepcontrol.wait;" ::: "memory");  // behind the pass above, which writes these D too
+      if (mine && l == 0) a.dsum[at] = acc;
     }
   }
-#pragma unroll
-  for (int d = 4; d > 0; d >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, d);
-  if (mine && l == 0) a.dsum[h * a.lse_sh + i] = acc;
-  asm volatile("griddepcontrol.wait;" ::: "memory");  // as in preprocess_kernel
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // the kernel ahead is over before this one is
 }
 
 // Zero rows: dQ (all queries) and/or dK, dV (all keys).
@@ -174,14 +181,14 @@ cudaError_t launch_bwd_preprocess(int d_v, const BwdArgs& a, bool early, cudaStr
 
 cudaError_t launch_bwd_few_keys_dsum(int d_qk, int d_v, const BwdArgs& a, const FewKeys& t, bool early,
                                      cudaStream_t stream) {
-  const int64_t rows = static_cast<int64_t>(a.seqlen_q) * a.heads;
-  if (rows == 0) return cudaSuccess;
-  const int64_t blocks = (rows + 31) / 32;
-  if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
+  if (a.num_units < 1 || a.seqlen_q < 1) return cudaSuccess;
+  constexpr int kBlocks = 152 * 4;
+  const int gx = a.num_units < kBlocks ? a.num_units : kBlocks;
+  const dim3 grid(static_cast<unsigned>(gx), static_cast<unsigned>(kBlocks / gx));
   auto with_mod = [&](auto none, auto softcap, auto alibi) {
     auto k = a.score_mod == kModNone ? none : a.score_mod == kModSoftcap ? softcap : alibi;
-    if (early) return launch_early(k, dim3(static_cast<unsigned>(blocks)), 256, 0, stream, a, t);
-    k<<<static_cast<unsigned>(blocks), 256, 0, stream>>>(a, t);
+    if (early) return launch_early(k, grid, 256, 0, stream, a, t);
+    k<<<grid, 256, 0, stream>>>(a, t);
     return cudaGetLastError();
   };
   using namespace bwd;

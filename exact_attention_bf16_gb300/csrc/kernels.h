@@ -336,11 +336,12 @@ cudaError_t launch_bwd_single_pass(const CUtensorMap& tq, const CUtensorMap& tk,
 cudaError_t launch_bwd_dq_convert(const BwdArgs& a, int d, cudaStream_t stream);
 // D = rowsum(dO * O) into args.dsum. early: behind launch_tile_lists, whose kernel it runs beside.
 cudaError_t launch_bwd_preprocess(int d_v, const BwdArgs& a, bool early, cudaStream_t stream);
-// The same D from q, k, v, dO and the LSE, for packed sequences of at most kFewKeys keys.
+// The same D from q, k, v, dO and the LSE, for the rows of sequences (dense: a call) of at most kFewKeys keys; the others'
+// are left as they are. early: behind launch_bwd_preprocess or launch_tile_lists.
 constexpr int kFewKeys = 8;
 struct FewKeys {
   const __nv_bfloat16 *q, *k, *v;
-  int64_t q_sn, q_sh, k_sn, k_sh, v_sn, v_sh;
+  int64_t q_sb, q_sn, q_sh, k_sb, k_sn, k_sh, v_sb, v_sn, v_sh;
 };
 cudaError_t launch_bwd_few_keys_dsum(int d_qk, int d_v, const BwdArgs& a, const FewKeys& t, bool early,
                                      cudaStream_t stream);

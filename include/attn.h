@@ -277,9 +277,9 @@ typedef struct attn_bwd_params {
  * x (4 x d_v + 4) bytes (the two parts each rounded up to 256). The result
  * equals the unsplit one within rounding and is the same bits on every call
  * with the same shapes. The block-sparse forward never splits.
- * The backward's workspace holds D = rowsum(dO * O) (variable length with
- * max_seqlen_k <= 8: computed without O, whose rounding would show in dQ and dK
- * of so few keys): 4 x heads x query rows
+ * The backward's workspace holds D = rowsum(dO * O) (for sequences of at most 8
+ * keys computed without O, whose rounding would show in dQ and dK of so few
+ * keys): 4 x heads x query rows
  * bytes, rounded up to 256, 16-byte aligned; a variable-length backward adds
  * its tile lists, 32 x heads x (total_k / 128 + num_seqs) bytes for dK/dV
  * (none with cta_pair) and 32 x heads x (total_q / 128 + num_seqs) for dQ, and

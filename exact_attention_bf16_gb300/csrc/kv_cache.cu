@@ -57,6 +57,8 @@ __device__ __forceinline__ int owner(const int* start, int n, int x) {
 }
 
 constexpr long long kMost = 0x7fffffff;
+constexpr int kPlanCtas = 148;  // the most that share a step
+static_assert(kMost + 4ll * 1024 * kPlanCtas <= 0xffffffffll, "32-bit token indices do not wrap");
 
 __global__ void kv_plan_kernel(const KvPlanArgs a) {
   extern __shared__ int s_start[];  // cu[n + 1], grow[n + 1], back[n + 1]
@@ -134,7 +136,8 @@ __global__ void kv_plan_kernel(const KvPlanArgs a) {
       const int e = owner(s_back, n, i - count);
       return a.block_table[e * a.block_table_stride + (i - count - s_back[e])];
     };
-    for (int i = me; i < grow; i += all) {
+    for (uint32_t j = me; j < static_cast<uint32_t>(grow); j += all) {  // (unsigned: as the tokens below)
+      const int i = static_cast<int>(j);
       const int s = owner(s_grow, n, i);
       const long long have = pages(max(0, a.seqlens_old[s]));
       a.block_table[s * a.block_table_stride + have + (i - s_grow[s])] = stack(height - 1 - i);
@@ -158,9 +161,11 @@ __global__ void kv_plan_kernel(const KvPlanArgs a) {
     const int tokens = static_cast<int>(total.add);
     // four tokens in a row per thread where there are more tokens than threads: the request and the page are
     // looked up again only where they change
-    const int run = a.max_tokens <= all ? 1 : 4;
-    for (int t0 = run * me; t0 < a.max_tokens; t0 += run * all) {
-      const int t1 = min(t0 + run, a.max_tokens);
+    // (unsigned: the count is below 2^31, and a step past it, at most 4 x 1024 x kPlanCtas, stays below 2^32)
+    const uint32_t max_tokens = static_cast<uint32_t>(a.max_tokens);
+    const uint32_t run = max_tokens <= static_cast<uint32_t>(all) ? 1 : 4;
+    for (uint32_t first = run * me; first < max_tokens; first += run * all) {
+      const int t0 = static_cast<int>(first), t1 = static_cast<int>(min(first + run, max_tokens));
       long long slot = -1;
       int left = 0, end = t0;  // tokens left on the page; first token of the next request
       int s = 0, pos = 0;
@@ -187,7 +192,7 @@ __global__ void kv_plan_kernel(const KvPlanArgs a) {
       }
     }
   } else {
-    for (int t = me; t < a.max_tokens; t += all) a.slot_mapping[t] = -1;
+    for (uint32_t t = me; t < static_cast<uint32_t>(a.max_tokens); t += all) a.slot_mapping[t] = -1;
   }
   // every read of the lengths and the stack's height is done (where they are updated in place, the grid is one cluster)
   cg::this_cluster().sync();
@@ -289,10 +294,10 @@ cudaError_t launch_kv_plan(const KvPlanArgs& a, cudaStream_t stream) {
   // (1000 requests with 48,420 tokens 8.3 us, 11.6 by half as many; 3000 with 150,394 tokens 8.3, 11.2 by 64), or where
   // lengths or the stack's height are updated in place, and so must have been read by all first, by a cluster of sixteen,
   // the most there are (12.3 us of the former; eight take 17.1).
-  constexpr int kPlanCtas = 148;
   const bool small = a.max_tokens <= 4096 && a.num_seqs <= 1024;
   const bool in_place = a.seqlens_k == a.seqlens_old || a.free_count_out == a.free_count;
-  const int ctas = small ? 1 : in_place ? 16 : std::max(16, std::min(kPlanCtas, (a.max_tokens + 1023) / 1024));
+  const int shares = static_cast<int>(std::min<int64_t>(kv::kPlanCtas, (static_cast<int64_t>(a.max_tokens) + 1023) / 1024));
+  const int ctas = small ? 1 : in_place ? 16 : std::max(16, shares);
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(ctas);
   cfg.blockDim = dim3(small && a.num_seqs <= 256 && a.max_tokens <= 1024 ? 256 : 1024);

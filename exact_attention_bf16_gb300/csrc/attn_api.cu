@@ -12,6 +12,7 @@
 #include <cstdio>
 #include <cstring>
 #include <initializer_list>
+#include <iterator>
 #include <mutex>
 
 #include "../../include/attn.h"
@@ -881,6 +882,36 @@ attn_status_t bind_device(DeviceScope* scope, const void* ptr) {
   return e == cudaErrorInvalidDevicePointer ? ATTN_ERR_INVALID_ARG : cuda_fail(e, "device");
 }
 
+// Whether an array that attn_kv_plan writes lies on another of its arrays, but for the two pairs that may be the same.
+bool plan_arrays_overlap(const attn_kv_plan_params* p) {
+  const int64_t n = p->num_seqs;
+  struct Range {
+    uintptr_t at;
+    int64_t bytes;
+    bool written;
+  };
+  auto of = [](const void* x, int64_t bytes, bool written) { return Range{reinterpret_cast<uintptr_t>(x), bytes, written}; };
+  const Range r[] = {of(p->seqlens_old, 4 * n, false), of(p->seqlens_new, 4 * n, false), of(p->free_count, 4, false),
+                     of(p->free_pages, 4ll * p->free_capacity, true), of(p->free_count_out, 4, true),
+                     of(p->cu_seqlens_q, 4 * (n + 1), true), of(p->seqlens_k, 4 * n, true),
+                     of(p->slot_mapping, 8ll * p->max_tokens, true), of(p->status, 4, true)};
+  for (const Range& x : r) {
+    for (const Range* y = &x + 1; y != std::end(r); ++y) {
+      if (!(x.written || y->written) || x.bytes == 0 || y->bytes == 0) continue;
+      const bool same = x.at == y->at && ((&x == &r[0] && y == &r[6]) || (&x == &r[2] && y == &r[4]));  // updated in place
+      if (!same && x.at < y->at + y->bytes && y->at < x.at + x.bytes) return true;
+    }
+    // the table's rows: an array may lie between them
+    const int64_t stride = 4 * p->block_table_stride, row = 4ll * p->max_pages;
+    const int64_t from = static_cast<int64_t>(x.at - reinterpret_cast<uintptr_t>(p->block_table)), to = from + x.bytes;
+    if (x.bytes > 0 && to > 0 && from < (n - 1) * stride + row) {
+      const int64_t first = std::max<int64_t>(from, 0), s = first / stride;  // the row at or before it
+      if (first - s * stride < row || (s + 1 < n && to > (s + 1) * stride)) return true;
+    }
+  }
+  return false;
+}
+
 attn_status_t run_kv_plan(const attn_kv_plan_params* p, cudaStream_t stream) {
   if (!p) return ATTN_ERR_INVALID_ARG;
   KvPlanArgs a{};
@@ -896,6 +927,7 @@ attn_status_t run_kv_plan(const attn_kv_plan_params* p, cudaStream_t stream) {
   if (p->max_tokens > 0 && (!p->slot_mapping || (reinterpret_cast<uintptr_t>(p->slot_mapping) & 7u)))
     return ATTN_ERR_INVALID_ARG;
   if (p->num_seqs > kMaxPlanSeqs) return ATTN_ERR_UNSUPPORTED;
+  if (plan_arrays_overlap(p)) return ATTN_ERR_INVALID_ARG;
   ATTN_TRY(check_lists_device(p->seqlens_old, {p->seqlens_new, p->block_table, p->free_capacity ? p->free_pages : nullptr,
                                                p->free_count, p->free_count_out, p->cu_seqlens_q, p->seqlens_k,
                                                p->max_tokens ? p->slot_mapping : nullptr, p->status}));

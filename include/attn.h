@@ -413,7 +413,7 @@ attn_status_t attn_bwd_noalloc(const attn_bwd_params* p, attn_stream_t stream);
  * 0 throughout, slot_mapping -1, seqlens_k = seqlens_old and *free_count_out =
  * *free_count, so that the step's other calls do nothing. seqlens_k may be
  * seqlens_old and free_count_out may be free_count (updated in place); no
- * other arrays may overlap. The result is the same bits on every call.
+ * other array may lie on one that is written (ATTN_ERR_INVALID_ARG). The result is the same bits on every call.
  * num_seqs is 1 to 16384 (more: ATTN_ERR_UNSUPPORTED). */
 typedef struct attn_kv_plan_params {
   const int32_t* seqlens_old;

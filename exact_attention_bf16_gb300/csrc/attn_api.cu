@@ -498,7 +498,7 @@ attn_status_t run_fwd(const attn_fwd_params* p, bool varlen, cudaStream_t stream
                              hkv, p->d_v, v16, stream);
   else if (e == cudaSuccess)
     e = launch_v_to_f16(p->v, varlen ? 0 : p->v_batch_stride, p->v_row_stride, p->v_head_stride, nb, nk_rows,
-                        hkv, p->d_v, v16, flag, lp.use, stream);
+                        hkv, p->d_v, v16, flag, varlen ? p->cu_seqlens_k + p->num_seqs : nullptr, lp.use, stream);
   if (e != cudaSuccess) return cuda_fail(e, "fwd V conversion");
   a.v16_flag = flag;
   const SplitPlan spl = (sp.kv_count || p->cta_pair || f8) ? SplitPlan{} : fwd_split_plan(p, varlen);
@@ -815,16 +815,11 @@ attn_status_t run_bwd(const attn_bwd_params* p, void* ws, size_t ws_bytes, bool 
     return p->phase_events[i] ? cudaEventRecord(static_cast<cudaEvent_t>(p->phase_events[i]), stream) : cudaSuccess;
   };
   const bool lists = a.tiles_kv != nullptr || a.tiles_q != nullptr;
-  const bool all_few = max_k <= kFewKeys;  // no row sees more keys
-  if (!all_few) e = launch_bwd_preprocess(f.d_v, a, lists, stream);
-  if (e == cudaSuccess && (all_few || varlen)) {  // (packed: some sequences may be as short)
-    auto bf = [](const void* x) { return static_cast<const __nv_bfloat16*>(x); };
-    const bool b = !varlen;
-    const FewKeys t{bf(f.q), bf(f.k), bf(f.v), b ? f.q_batch_stride : 0, f.q_row_stride, f.q_head_stride,
-                    b ? f.k_batch_stride : 0, f.k_row_stride, f.k_head_stride, b ? f.v_batch_stride : 0, f.v_row_stride,
-                    f.v_head_stride};
-    e = launch_bwd_few_keys_dsum(f.d_qk, f.d_v, a, t, lists || !all_few, stream);
-  }
+  auto bf = [](const void* x) { return static_cast<const __nv_bfloat16*>(x); };
+  FewKeys few{bf(f.q), bf(f.k), bf(f.v), f.q_batch_stride, f.q_row_stride, f.q_head_stride, f.k_batch_stride, f.k_row_stride,
+              f.k_head_stride, f.v_batch_stride, f.v_row_stride, f.v_head_stride, f.d_qk, f.d_v};
+  if (varlen) few.q_sb = few.k_sb = few.v_sb = 0;
+  e = max_k <= kFewKeys ? launch_bwd_few_keys_dsum(a, few, lists, stream) : launch_bwd_preprocess(f.d_v, a, few, lists, stream);
   if (e == cudaSuccess && sp.kv_count) e = launch_bwd_transpose_lists(a, n_kb_sparse, stream);
   if (e == cudaSuccess) e = mark(0);
   if (e != cudaSuccess) return cuda_fail(e, "bwd preprocess launch");

@@ -7,22 +7,97 @@
 namespace gb300 {
 namespace bwd {
 
+// D of a row of a sequence (dense: a call) of at most kFewKeys keys, as sum_j P_ij (dO_i . v_j) with P from the LSE, all
+// in fp32. The same number as dO_i . O_i in exact arithmetic, but O comes rounded to bf16, and its error d is the same in
+// all dS_ij = P_ij (dO_i . v_j - D_i): dQ_i is off by d sum_j P_ij k_j, d up to 2^-8 |dO_i| |O_i|, beside a dQ_i that
+// shrinks as the v_j of its keys differ less from their mean O_i. Over sequences of one and two tokens dQ and dK came out
+// 5.0e-3 from the exact ones (norms), now below 2.9e-3; from 9 keys on it is at most 3.1e-3 from the rounded O, too. Which
+// rows are taken depends on their sequence alone, so that a sequence has the same gradients in every batch.
+// Run by the eight lanes l = 0 .. 7 of the row, each with an eighth of the columns (one key each instead left seven lanes
+// idle where there is one key, and took 37 us for 29,000 rows); all rows of a warp are of the same unit. Row i (of the
+// unit), head h; every lane returns the sum.
+__device__ __forceinline__ float few_keys_d(const BwdArgs& a, const FewKeys& t, const Unit& U, int i, int h, int l) {
+  auto dot8 = [](const __nv_bfloat16* x, const __nv_bfloat16* y, float sum) {
+    const uint4 xv = *reinterpret_cast<const uint4*>(x), yv = *reinterpret_cast<const uint4*>(y);
+    const uint32_t xw[4] = {xv.x, xv.y, xv.z, xv.w}, yw[4] = {yv.x, yv.y, yv.z, yv.w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float2 xf = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&xw[e]));
+      const float2 yf = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&yw[e]));
+      sum = fmaf(xf.x, yf.x, sum);
+      sum = fmaf(xf.y, yf.y, sum);
+    }
+    return sum;
+  };
+  const int64_t row = U.q_start + i;
+  const int pos = i - U.nq + U.nk, hk = h / a.kv_group;  // the row's position among the keys
+  const float lse = a.lse[U.b * a.lse_sb + h * a.lse_sh + row];
+  const int keys = lse == -INFINITY ? 0 : (a.causal ? min(U.nk, pos + 1) : U.nk);
+  const __nv_bfloat16* q = t.q + U.b * t.q_sb + row * t.q_sn + h * t.q_sh;
+  const __nv_bfloat16* g = static_cast<const __nv_bfloat16*>(a.dout) + U.b * a.do_sb + row * a.do_sn + h * a.do_sh;
+  float acc = 0.f;
+  for (int j = 0; j < U.nk; ++j) {
+    const __nv_bfloat16* k = t.k + U.b * t.k_sb + static_cast<int64_t>(U.k_start + j) * t.k_sn + hk * t.k_sh;
+    const __nv_bfloat16* v = t.v + U.b * t.v_sb + static_cast<int64_t>(U.k_start + j) * t.v_sn + hk * t.v_sh;
+    float x = 0.f, y = 0.f;
+    for (int c = 8 * l; c < t.d_qk; c += 64) x = dot8(q + c, k + c, x);
+    for (int c = 8 * l; c < t.d_v; c += 64) y = dot8(g + c, v + c, y);
+#pragma unroll
+    for (int d = 4; d > 0; d >>= 1) x += __shfl_xor_sync(0xffffffffu, x, d);
+    if (a.score_mod == kModSoftcap) x = a.mod_b * tanh_scaled(x, a.mod_k2);
+    if (a.score_mod == kModAlibi) x -= fabsf(a.alibi_slopes[h] * a.inv_scale * static_cast<float>(j - pos));
+    if (j < keys) acc = fmaf(exp2f(fmaf(x, a.scale_log2, -lse * 1.4426950408889634f)), y, acc);
+  }
+#pragma unroll
+  for (int d = 4; d > 0; d >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, d);
+  return acc;
+}
+
+// Whether few_keys_d is for this unit (offsets past the tensors are not followed).
+__device__ __forceinline__ bool few_keys(const BwdArgs& a, const Unit& U) {
+  return U.nk >= 1 && U.nk <= kFewKeys && U.q_start >= 0 && U.k_start >= 0 && U.q_start + U.nq <= a.seqlen_q &&
+         U.k_start + U.nk <= a.seqlen_k;
+}
+
+// D of calls whose rows all see few keys. Latency-bound: four rows a warp. Block x takes units x, x + gridDim.x, ..., its
+// rows shared by the blocks along y.
+__global__ void __launch_bounds__(256) few_keys_dsum_kernel(const BwdArgs a, const FewKeys t) {
+  const int l = static_cast<int>(threadIdx.x & 7u);
+  for (int unit = static_cast<int>(blockIdx.x); unit < a.num_units; unit += static_cast<int>(gridDim.x)) {
+    const Unit U = unit_bounds(a, unit);
+    if (!few_keys(a, U)) continue;
+    const int64_t rows = static_cast<int64_t>(U.nq) * a.heads;
+    for (int64_t r0 = blockIdx.y * 32 + (threadIdx.x >> 5) * 4; r0 < rows; r0 += gridDim.y * 32) {
+      const int64_t r = r0 + ((threadIdx.x >> 3) & 3u), at = min(r, rows - 1);
+      const int i = static_cast<int>(at / a.heads), h = static_cast<int>(at % a.heads);
+      const float d = few_keys_d(a, t, U, i, h, l);
+      if (r < rows && l == 0) a.dsum[U.b * a.lse_sb + h * a.lse_sh + U.q_start + i] = d;
+    }
+  }
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // behind the tile lists' kernel: over before this one is
+}
+
 // ===========================================================================
 // Preprocess: D = rowsum(dO * O). HBM-bound: DV / 8 lanes share a row, each
 // loading 16 bytes of O and of dO per access (rows and head slices start on
 // 16-byte boundaries, as the TMA tensor maps already require).
 // ===========================================================================
-template <int DV>
-__global__ void __launch_bounds__(256, 8) preprocess_kernel(const BwdArgs a) {
+// PACKED: a block takes `chunk` rows side by side and then, where sequences of few keys
+// lie in them, replaces those sequences' D by few_keys_d's. (A choice per row in the
+// loop cost the rows of longer sequences 40% of its time, a pass of its own behind this
+// one 1 us of every call.)
+constexpr int kPackedBlocks = 6;  // per SM: at 8 few_keys_d spills (3000 sequences of 1 to 30 tokens, the backward: 1557 us, 1616)
+template <int DV, bool PACKED>
+__global__ void __launch_bounds__(256, PACKED ? kPackedBlocks : 8) preprocess_kernel(const BwdArgs a, const __grid_constant__ FewKeys t, int64_t chunk) {
   constexpr int LPR = DV / 8;    // lanes per row
   constexpr int RPW = 32 / LPR;  // rows per warp
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // few_keys_dsum_kernel, where it follows
-  const int64_t rows = static_cast<int64_t>(a.batch) * a.seqlen_q * a.heads;
-  const int64_t warp0 = (blockIdx.x * static_cast<int64_t>(blockDim.x) + threadIdx.x) >> 5;
-  const int64_t nwarps = (static_cast<int64_t>(gridDim.x) * blockDim.x) >> 5;
+  const int64_t all = static_cast<int64_t>(a.batch) * a.seqlen_q * a.heads;
   const int lane = threadIdx.x & 31;
   const int sub = lane / LPR, l = lane % LPR;
-  for (int64_t r0 = warp0 * RPW; r0 < rows; r0 += nwarps * RPW) {
+  const int64_t begin = PACKED ? blockIdx.x * chunk : 0, rows = PACKED ? min(all, begin + chunk) : all;
+  const int64_t warp0 = PACKED ? threadIdx.x >> 5 : (blockIdx.x * static_cast<int64_t>(blockDim.x) + threadIdx.x) >> 5;
+  const int64_t nwarps = PACKED ? 8 : (static_cast<int64_t>(gridDim.x) * blockDim.x) >> 5;
+  for (int64_t r0 = begin + warp0 * RPW; r0 < rows; r0 += nwarps * RPW) {
     const int64_t r = r0 + sub;
     float acc = 0.f;
     int h = 0, i = 0, b = 0;
@@ -48,76 +123,28 @@ __global__ void __launch_bounds__(256, 8) preprocess_kernel(const BwdArgs a) {
     for (int s = LPR / 2; s > 0; s >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, s);
     if (r < rows && l == 0) a.dsum[b * a.lse_sb + h * a.lse_sh + i] = acc;
   }
-  asm volatile("griddepcontrol.wait;" ::: "memory");  // behind the tile lists' kernel: over before this one is
-}
-
-
-
-// D of the rows of sequences (dense: calls) of at most kFewKeys keys, as sum_j P_ij (dO_i . v_j) with P from the LSE, all
-// in fp32. The same number in exact arithmetic, but O comes rounded to bf16, and its error d is the same in all dS_ij =
-// P_ij (dO_i . v_j - D_i): dQ_i is off by d sum_j P_ij k_j, d up to 2^-8 |dO_i| |O_i|, beside a dQ_i that shrinks as the
-// v_j of its keys differ less from their mean O_i. Over sequences of one and two tokens dQ and dK came out 5.0e-3 from the
-// exact ones (norms), now below 2.9e-3; from 9 keys on it is at most 3.1e-3 from the rounded O, too. Which rows are taken
-// depends on their sequence alone, so that a sequence has the same gradients in every batch. Where a packed batch may hold
-// longer sequences this runs behind the pass above, beside its end, and replaces its D. (A choice per sequence in that
-// pass cost the rows of longer ones 40% of its time.) Latency-bound: 8 lanes share a row, one key each.
-// Block x takes units x, x + gridDim.x, ..., its rows shared by the blocks along y.
-template <int DQK, int DV, int MOD>
-__global__ void __launch_bounds__(256) few_keys_dsum_kernel(const BwdArgs a, const FewKeys t) {
-  const int l = static_cast<int>(threadIdx.x & 7u);
-  for (int unit = static_cast<int>(blockIdx.x); unit < a.num_units; unit += static_cast<int>(gridDim.x)) {
-    const Unit U = unit_bounds(a, unit);
-    // offsets past the tensors are not followed
-    if (U.nk < 1 || U.nk > kFewKeys || U.q_start < 0 || U.k_start < 0 || U.q_start + U.nq > a.seqlen_q ||
-        U.k_start + U.nk > a.seqlen_k)
-      continue;
-    const int64_t rows = static_cast<int64_t>(U.nq) * a.heads;
-    for (int64_t r0 = blockIdx.y * 32 + (threadIdx.x >> 5) * 4; r0 < rows; r0 += gridDim.y * 32) {  // four rows a warp
-      const int64_t r = r0 + ((threadIdx.x >> 3) & 3u);
-      const bool mine = r < rows;
-      const int i = static_cast<int>(r / a.heads), h = static_cast<int>(r % a.heads);
-      const int64_t at = U.b * a.lse_sb + h * a.lse_sh + U.q_start + i;
-      float acc = 0.f;
-      if (mine) {
-        const int pos = i - U.nq + U.nk;  // the row's position among the keys
-        const float lse = a.lse[at];
-        const int keys = lse == -INFINITY ? 0 : (a.causal ? min(U.nk, pos + 1) : U.nk);
-        const int64_t row = U.q_start + i;
-        const __nv_bfloat16* q = t.q + U.b * t.q_sb + row * t.q_sn + h * t.q_sh;
-        const __nv_bfloat16* g = static_cast<const __nv_bfloat16*>(a.dout) + U.b * a.do_sb + row * a.do_sn + h * a.do_sh;
-        const int hk = h / a.kv_group;
-        auto dot = [](const __nv_bfloat16* x, const __nv_bfloat16* y, int n) {
-          float2 sum = make_float2(0.f, 0.f);
-          for (int c = 0; c < n; c += 8) {
-            const uint4 xv = *reinterpret_cast<const uint4*>(x + c), yv = *reinterpret_cast<const uint4*>(y + c);
-            const uint32_t xw[4] = {xv.x, xv.y, xv.z, xv.w}, yw[4] = {yv.x, yv.y, yv.z, yv.w};
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const float2 xf = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&xw[e]));
-              const float2 yf = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&yw[e]));
-              sum.x = fmaf(xf.x, yf.x, sum.x);
-              sum.y = fmaf(xf.y, yf.y, sum.y);
-            }
-          }
-          return sum.x + sum.y;
-        };
-        static_assert(kFewKeys <= 8, "a key per lane");
-        if (l < keys) {
-          const int64_t kr = U.k_start + l;
-          float x = dot(q, t.k + U.b * t.k_sb + kr * t.k_sn + hk * t.k_sh, DQK);
-          if (MOD == kModSoftcap) x = a.mod_b * tanh_scaled(x, a.mod_k2);
-          if (MOD == kModAlibi) x -= fabsf(a.alibi_slopes[h] * a.inv_scale * static_cast<float>(l - pos));
-          const float p = exp2f(fmaf(x, a.scale_log2, -lse * 1.4426950408889634f));
-          acc = p * dot(g, t.v + U.b * t.v_sb + kr * t.v_sn + hk * t.v_sh, DV);
-        }
+  if constexpr (PACKED) {
+    __syncthreads();  // the D above are written
+    const int first = static_cast<int>(begin / a.heads), last = static_cast<int>((rows - 1) / a.heads);  // tokens
+    int unit = 0;  // the last sequence that begins at or before `first`
+    for (int e = a.num_units; unit + 1 < e;) {
+      const int m = (unit + e) / 2;
+      if (__ldg(a.cu_q + m) <= first) unit = m;
+      else e = m;
+    }
+    for (; unit < a.num_units && __ldg(a.cu_q + unit) <= last; ++unit) {
+      const Unit U = unit_bounds(a, unit);
+      if (!few_keys(a, U)) continue;
+      const int64_t r_end = min(rows, static_cast<int64_t>(U.q_start + U.nq) * a.heads);
+      for (int64_t r0 = max(begin, static_cast<int64_t>(U.q_start) * a.heads) + (threadIdx.x >> 5) * 4; r0 < r_end; r0 += 32) {
+        const int64_t r = r0 + (lane >> 3), at = min(r, r_end - 1);
+        const int i = static_cast<int>(at / a.heads), h = static_cast<int>(at % a.heads);
+        const float d = few_keys_d(a, t, U, i - U.q_start, h, lane & 7);
+        if (r < r_end && (lane & 7) == 0) a.dsum[h * a.lse_sh + i] = d;
       }
-#pragma unroll
-      for (int d = 4; d > 0; d >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, d);
-      asm volatile("griddepcontrol.wait;" ::: "memory");  // behind the pass above, which writes these D too
-      if (mine && l == 0) a.dsum[at] = acc;
     }
   }
-  asm volatile("griddepcontrol.wait;" ::: "memory");  // the kernel ahead is over before this one is
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // behind the tile lists' kernel: over before this one is
 }
 
 // Zero rows: dQ (all queries) and/or dK, dV (all keys).
@@ -166,42 +193,34 @@ __global__ void transpose_lists_kernel(BwdArgs a, int n_kb, int n_sets) {
 
 }  // namespace bwd
 
-cudaError_t launch_bwd_preprocess(int d_v, const BwdArgs& a, bool early, cudaStream_t stream) {
+cudaError_t launch_bwd_preprocess(int d_v, const BwdArgs& a, const FewKeys& t, bool early, cudaStream_t stream) {
   const int64_t rows = static_cast<int64_t>(a.batch) * a.seqlen_q * a.heads;
   if (rows == 0) return cudaSuccess;
-  const int64_t per_block = 8 * (d_v == 64 ? 4 : 2);  // 8 warps, each 32 / (d_v / 8) rows per pass
-  const int64_t want = (rows + per_block - 1) / per_block;
-  const int64_t blocks = want < 16384 ? want : 16384;
   if (d_v != 64 && d_v != 128) return cudaErrorInvalidValue;
-  auto kern = d_v == 64 ? bwd::preprocess_kernel<64> : bwd::preprocess_kernel<128>;
-  if (early) return launch_early(kern, dim3(static_cast<unsigned>(blocks)), 256, 0, stream, a);
-  kern<<<static_cast<unsigned>(blocks), 256, 0, stream>>>(a);
+  const int64_t per_block = 8 * (d_v == 64 ? 4 : 2);  // 8 warps, each 32 / (d_v / 8) rows per pass
+  const int64_t passes = (rows + per_block - 1) / per_block;
+  if (a.cu_q != nullptr) {  // one wave of blocks
+    const int64_t chunk = (passes + 152 * bwd::kPackedBlocks - 1) / (152 * bwd::kPackedBlocks) * per_block;
+    const unsigned blocks = static_cast<unsigned>((rows + chunk - 1) / chunk);
+    auto kern = d_v == 64 ? bwd::preprocess_kernel<64, true> : bwd::preprocess_kernel<128, true>;
+    if (early) return launch_early(kern, dim3(blocks), 256, 0, stream, a, t, chunk);
+    kern<<<blocks, 256, 0, stream>>>(a, t, chunk);
+    return cudaGetLastError();
+  }
+  const unsigned blocks = static_cast<unsigned>(passes < 16384 ? passes : 16384);
+  auto kern = d_v == 64 ? bwd::preprocess_kernel<64, false> : bwd::preprocess_kernel<128, false>;
+  kern<<<blocks, 256, 0, stream>>>(a, t, int64_t{0});
   return cudaGetLastError();
 }
 
-cudaError_t launch_bwd_few_keys_dsum(int d_qk, int d_v, const BwdArgs& a, const FewKeys& t, bool early,
-                                     cudaStream_t stream) {
+cudaError_t launch_bwd_few_keys_dsum(const BwdArgs& a, const FewKeys& t, bool early, cudaStream_t stream) {
   if (a.num_units < 1 || a.seqlen_q < 1) return cudaSuccess;
   constexpr int kBlocks = 152 * 4;
   const int gx = a.num_units < kBlocks ? a.num_units : kBlocks;
   const dim3 grid(static_cast<unsigned>(gx), static_cast<unsigned>(kBlocks / gx));
-  auto with_mod = [&](auto none, auto softcap, auto alibi) {
-    auto k = a.score_mod == kModNone ? none : a.score_mod == kModSoftcap ? softcap : alibi;
-    if (early) return launch_early(k, grid, 256, 0, stream, a, t);
-    k<<<grid, 256, 0, stream>>>(a, t);
-    return cudaGetLastError();
-  };
-  using namespace bwd;
-  if (d_qk == 64 && d_v == 64)
-    return with_mod(few_keys_dsum_kernel<64, 64, kModNone>, few_keys_dsum_kernel<64, 64, kModSoftcap>,
-                    few_keys_dsum_kernel<64, 64, kModAlibi>);
-  if (d_qk == 128 && d_v == 128)
-    return with_mod(few_keys_dsum_kernel<128, 128, kModNone>, few_keys_dsum_kernel<128, 128, kModSoftcap>,
-                    few_keys_dsum_kernel<128, 128, kModAlibi>);
-  if (d_qk == 192 && d_v == 128)
-    return with_mod(few_keys_dsum_kernel<192, 128, kModNone>, few_keys_dsum_kernel<192, 128, kModSoftcap>,
-                    few_keys_dsum_kernel<192, 128, kModAlibi>);
-  return cudaErrorInvalidValue;
+  if (early) return launch_early(bwd::few_keys_dsum_kernel, grid, 256, 0, stream, a, t);
+  bwd::few_keys_dsum_kernel<<<grid, 256, 0, stream>>>(a, t);
+  return cudaGetLastError();
 }
 
 cudaError_t launch_bwd_dkdv(int d_qk, int d_v, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,

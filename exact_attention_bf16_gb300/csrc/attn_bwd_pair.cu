@@ -153,14 +153,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     int nq_issued = 0, ng_issued = 0;
     bool ok = true;
     const int rh = 64 * static_cast<int>(rank);  // this CTA's row half and column half
-    const CUtensorMap *mq_r = &tmq_r, *mq_c = &tmq_c, *mdo_r = &tmdo_r, *mdo_c = &tmdo_c;
-    if (a.seq_maps != nullptr) {  // the sequence's, whose rows end with it
-      mq_r = seq_map(a, U, kMapQr), mq_c = seq_map(a, U, kMapQ), mdo_r = seq_map(a, U, kMapDOr), mdo_c = seq_map(a, U, kMapDO);
-      for (const CUtensorMap* m : {mq_r, mq_c, mdo_r, mdo_c}) tensormap_acquire(m);
-    }
+    const TailMaps tails_r(a, U, kMapQr, kMapDOr, true), tails_c(a, U, kMapQ, kMapDO, true);
     for (int t = 0; t < T && ok; ++t) {
       const int tile = q_row(t);
       const int row = U.q_start + tile;
+      const bool tail = tile + QB > U.nq;
       float nl[QB / 32], nd[QB / 32];
 #pragma unroll
       for (int u = 0; u < QB / 32; ++u) {
@@ -180,8 +177,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       if (lane == 0) {
         uint8_t* dst = sQ + qs * C::SLOT;
         mbar_arrive_expect_tx(&bar->q_full[qs], C::SLOT);
-        for (int c = 0; c < 2; ++c) tma_load_4d(dst + c * (C::ROWH / 2), mq_r, &bar->q_full[qs], c * 64, h, row + rh, U.b);
-        tma_load_4d(dst + C::ROWH, mq_c, &bar->q_full[qs], rh, h, row, U.b);
+        for (int c = 0; c < 2; ++c) tma_load_4d(dst + c * (C::ROWH / 2), tails_r.x(&tmq_r, tail), &bar->q_full[qs], c * 64, h, row + rh, U.b);
+        tma_load_4d(dst + C::ROWH, tails_c.x(&tmq_c, tail), &bar->q_full[qs], rh, h, row, U.b);
       }
       ++nq_issued;
       ok = mbar_wait_cluster(&bar->g_empty[gs], (static_cast<uint32_t>(t / C::NG) & 1u) ^ 1u, a.status, 0x1808 + gs);
@@ -190,8 +187,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         uint8_t* dst = sG + gs * C::SLOT;
         mbar_arrive_expect_tx(&bar->g_full[gs], C::SLOT);
         for (int c = 0; c < 2; ++c)
-          tma_load_4d(dst + c * (C::ROWH / 2), mdo_r, &bar->g_full[gs], c * 64, h, row + rh, U.b);
-        tma_load_4d(dst + C::ROWH, mdo_c, &bar->g_full[gs], rh, h, row, U.b);
+          tma_load_4d(dst + c * (C::ROWH / 2), tails_r.y(&tmdo_r, tail), &bar->g_full[gs], c * 64, h, row + rh, U.b);
+        tma_load_4d(dst + C::ROWH, tails_c.y(&tmdo_c, tail), &bar->g_full[gs], rh, h, row, U.b);
       }
       ++ng_issued;
       ok = mbar_wait(&bar->v_empty[vs], (static_cast<uint32_t>(t / C::NVEC) & 1u) ^ 1u, a.status, 0x1810 + vs);

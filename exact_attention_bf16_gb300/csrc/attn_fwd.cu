@@ -132,17 +132,20 @@ cudaError_t launch_t(const CUtensorMap& tq, const CUtensorMap& tk, const CUtenso
 // 2^-17 and more are exact in fp16, its smallest step being 2^-24, smaller ones off by
 // at most 2^-25: 2^-11 of a row's largest value otherwise. Zero rows, and small values
 // beside larger ones, do not set it: P then keeps its 11 bits.) inf and NaN convert to
-// themselves.
+// themselves. Whatever is not finite in the copy sets its second bit: packed sequences
+// are then kept apart.
 template <int DV, int AHEAD>
 __global__ void v_to_f16_kernel(const void* v, int64_t sb, int64_t sn, int64_t sh, int nb, int nrows, int heads,
-                                void* out, uint32_t* flag) {
+                                void* out, uint32_t* flag, const int* used) {
   constexpr int UPH = DV / 8;  // 16-byte units per (row, head)
   const int upr = heads * UPH;  // per row
   const int64_t rows = static_cast<int64_t>(nb) * nrows;
   const int lane = static_cast<int>(threadIdx.x & 31u);
   const int64_t nwarps = (static_cast<int64_t>(gridDim.x) * blockDim.x) >> 5;
+  const int64_t last = used != nullptr ? *used : rows;  // rows behind it belong to no sequence: only whether they are finite matters
   uint32_t bad = 0;
   for (int64_t r = (blockIdx.x * static_cast<int64_t>(blockDim.x) + threadIdx.x) >> 5; r < rows; r += nwarps) {
+    uint32_t of_row = 0;
     const int b = static_cast<int>(r / nrows), n = static_cast<int>(r % nrows);
     const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(v) + b * sb + n * sn;
     uint4* dst = static_cast<uint4*>(out) + r * upr;
@@ -166,20 +169,23 @@ __global__ void v_to_f16_kernel(const void* v, int64_t sb, int64_t sn, int64_t s
         const uint32_t some = __ballot_sync(0xffffffffu, largest != 0);
         const uint32_t normal = __ballot_sync(0xffffffffu, largest >= 0x3880u);  // 2^-14
         const uint32_t row = ((1u << UPH) - 1u) << (lane & ~(UPH - 1));
-        bad |= static_cast<uint32_t>((some & row) != 0 && (normal & row) == 0);
+        of_row |= static_cast<uint32_t>((some & row) != 0 && (normal & row) == 0);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const uint32_t lo = w[e] & 0x7FFFu, hi = (w[e] >> 16) & 0x7FFFu;
-          bad |= static_cast<uint32_t>(lo >= 0x4780u && lo < 0x7F80u) | static_cast<uint32_t>(hi >= 0x4780u && hi < 0x7F80u);
+          of_row |= static_cast<uint32_t>(lo >= 0x4780u && lo < 0x7F80u) | static_cast<uint32_t>(hi >= 0x4780u && hi < 0x7F80u);
+          of_row |= lo >= 0x4780u || hi >= 0x4780u ? 2u : 0u;
           o[e] = pack_f16x2(__uint_as_float(w[e] << 16), __uint_as_float(w[e] & 0xFFFF0000u));
         }
         if (i < upr) dst[i] = make_uint4(o[0], o[1], o[2], o[3]);
       }
     }
+    bad |= of_row & (r < last ? 3u : 2u);
   }
   // Behind a tile list's kernel, which zeroes the flag and whose lists the next kernel reads: over before this one is.
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  if (__any_sync(0xffffffffu, bad != 0) && lane == 0) atomicOr(flag, 1u);
+  bad = __reduce_or_sync(0xffffffffu, bad);
+  if (bad != 0 && lane == 0) atomicOr(flag, bad);
 }
 
 }  // namespace fwd
@@ -215,7 +221,7 @@ cudaError_t launch_fwd_diag_timeout(const CUtensorMap& tq, const CUtensorMap& tk
 }
 
 cudaError_t launch_v_to_f16(const void* v, int64_t sb, int64_t sn, int64_t sh, int nb, int nrows, int heads, int dv,
-                            void* out, uint32_t* flag, bool early, cudaStream_t stream) {
+                            void* out, uint32_t* flag, const int* used, bool early, cudaStream_t stream) {
   const int64_t rows = static_cast<int64_t>(nb) * nrows;
   if (rows == 0) return cudaSuccess;
   const int64_t want = (rows + 7) / 8;  // 8 warps (rows) per block and pass
@@ -224,8 +230,8 @@ cudaError_t launch_v_to_f16(const void* v, int64_t sb, int64_t sn, int64_t sh, i
   const bool one = heads * (dv / 8) <= 32;
   auto kern = dv == 64 ? (one ? fwd::v_to_f16_kernel<64, 1> : fwd::v_to_f16_kernel<64, 4>)
                        : (one ? fwd::v_to_f16_kernel<128, 1> : fwd::v_to_f16_kernel<128, 4>);
-  if (early) return launch_early(kern, dim3(blocks), 256, 0, stream, v, sb, sn, sh, nb, nrows, heads, out, flag);
-  kern<<<blocks, 256, 0, stream>>>(v, sb, sn, sh, nb, nrows, heads, out, flag);
+  if (early) return launch_early(kern, dim3(blocks), 256, 0, stream, v, sb, sn, sh, nb, nrows, heads, out, flag, used);
+  kern<<<blocks, 256, 0, stream>>>(v, sb, sn, sh, nb, nrows, heads, out, flag, used);
   return cudaGetLastError();
 }
 

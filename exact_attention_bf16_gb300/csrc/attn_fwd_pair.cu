@@ -137,9 +137,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             tma_load_4d(sQ + i * C::Q_BYTES + c * kChunk, &tmq, &bar->q_full[i], c * 64, h, q_start + own_row0(i), b);
         }
         const CUtensorMap* tmvv = f16 ? &tmv16 : &tmv;
-        if (a.seq_maps != nullptr) {  // that of the sequence, whose rows end with it
-          tmvv = a.seq_maps + (2 * static_cast<int64_t>(unit) + (f16 ? 1 : 0));
-          tensormap_acquire(tmvv);
+        // of the block that a packed sequence ends in, where V or its copy is not all finite: its own, whose rows end with it
+        const CUtensorMap* tmv_tail = tmvv;
+        if (a.seq_maps != nullptr && (__ldg(a.v16_flag) & 2u) != 0u) {
+          tmv_tail = a.seq_maps + (2 * static_cast<int64_t>(unit) + (f16 ? 1 : 0));
+          tensormap_acquire(tmv_tail);
         }
         int issued = 0;
         bool ok = true;
@@ -157,7 +159,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                             k_start + j * BN + 64 * static_cast<int>(rank), b);
             } else {  // all 128 keys, columns [64 r, +64)
               mbar_arrive_expect_tx(&bar->kv_full[slot], C::VH_BYTES);
-              tma_load_4d(dst, tmvv, &bar->kv_full[slot], 64 * static_cast<int>(rank), h, k_start + j * BN, b);
+              tma_load_4d(dst, (j + 1) * BN > nk ? tmv_tail : tmvv, &bar->kv_full[slot], 64 * static_cast<int>(rank), h, k_start + j * BN, b);
             }
             ++issued;
           }

@@ -41,6 +41,20 @@ __device__ __forceinline__ const CUtensorMap* seq_map(const BwdArgs& a, const Un
   return a.seq_maps + (static_cast<int64_t>(U.unit) * a.n_seq_maps + which);
 }
 
+// The two maps of its sequence that a copying thread takes for tiles that the sequence ends in (`use`: at all); the
+// parameters' otherwise, which every SM holds already: a map of its own costs a CTA its fetch, about 0.5 us.
+struct TailMaps {
+  const CUtensorMap *mx = nullptr, *my = nullptr;
+  __device__ __forceinline__ TailMaps(const BwdArgs& a, const Unit& U, SeqMapBwd x, SeqMapBwd y, bool use) {
+    if (!use || a.seq_maps == nullptr) return;
+    mx = seq_map(a, U, x), my = seq_map(a, U, y);
+    tensormap_acquire(mx);
+    tensormap_acquire(my);
+  }
+  __device__ __forceinline__ const CUtensorMap* x(const CUtensorMap* all, bool tail) const { return tail && mx != nullptr ? mx : all; }
+  __device__ __forceinline__ const CUtensorMap* y(const CUtensorMap* all, bool tail) const { return tail && my != nullptr ? my : all; }
+};
+
 // A backward CTA's work: from the tile list of a packed variable-length
 // launch (`tiles` non-null), else from the block index over nblk blocks per
 // (unit, head), blocks in descending (dQ: the last query blocks are the

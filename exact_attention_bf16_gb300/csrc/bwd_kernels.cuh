@@ -258,12 +258,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (warp == kTmaWarp) {
     if (lane == 0) {
-      const CUtensorMap *mk = &tmk, *mv = &tmv;
-      if (FUSED && a.seq_maps != nullptr) {  // (dQ's partials sum over the keys of the tile)
-        mk = seq_map(a, U, kMapK), mv = seq_map(a, U, kMapV);
-        tensormap_acquire(mk);
-        tensormap_acquire(mv);
-      }
+      const TailMaps tails(a, U, kMapK, kMapV, FUSED && k0 + KB > U.nk);  // (dQ's partials sum over the keys of the tile)
+      const CUtensorMap *mk = tails.x(&tmk, true), *mv = tails.y(&tmv, true);
       mbar_arrive_expect_tx(&bar->kv_full, C::K_BYTES + C::V_BYTES);
       for (int c = 0; c < C::QCH; ++c)
         tma_load_4d(sK + c * KB * 128, mk, &bar->kv_full, c * 64, h, U.k_start + k0, U.b);
@@ -276,12 +272,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // of their own (the slot is recycled only after dV, dK of that tile ran).
     int issued = 0;
     bool ok = true;
-    const CUtensorMap *mq = &tmq, *mdo = &tmdo;
-    if (!SPARSE && a.seq_maps != nullptr) {  // the sequence's, whose rows end with it
-      mq = seq_map(a, U, kMapQ), mdo = seq_map(a, U, kMapDO);
-      tensormap_acquire(mq);
-      tensormap_acquire(mdo);
-    }
+    const TailMaps tails(a, U, kMapQ, kMapDO, !SPARSE);
     int tt = 0, hq = hq_first;  // step within the query head hq
     for (int t = 0; t < T && ok; ++t) {
       const int st = t % C::NST;
@@ -307,6 +298,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint8_t* dst = sST + st * C::STAGE;
         const int row = U.q_start + tile;
         mbar_arrive_expect_tx(&bar->st_full[st], C::STAGE);
+        const CUtensorMap* mq = tails.x(&tmq, tile + QB > U.nq);
+        const CUtensorMap* mdo = tails.y(&tmdo, tile + QB > U.nq);
         for (int c = 0; c < C::QCH; ++c) tma_load_4d(dst + c * QB * 128, mq, &bar->st_full[st], c * 64, hq, row, U.b);
         for (int c = 0; c < C::VCH; ++c)
           tma_load_4d(dst + C::QT_BYTES + c * QB * 128, mdo, &bar->st_full[st], c * 64, hq, row, U.b);
@@ -788,12 +781,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // 128 (-LSE*log2e, -D) pairs into the vector ring and arrives on its barrier.
     int nq_issued = 0, ng_issued = 0;
     bool ok = true;
-    const CUtensorMap *mq = &tmq, *mdo = &tmdo;
-    if (!SPARSE && a.seq_maps != nullptr) {  // the sequence's, whose rows end with it
-      mq = seq_map(a, U, kMapQ), mdo = seq_map(a, U, kMapDO);
-      tensormap_acquire(mq);
-      tensormap_acquire(mdo);
-    }
+    const TailMaps tails(a, U, kMapQ, kMapDO, !SPARSE);
     int tt = 0, hq = hq_first;  // step within the query head hq
     for (int t = 0; t < T && ok; ++t) {
       const int tile = q_row(GQA ? tt : t);
@@ -817,7 +805,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lane == 0) {
         mbar_arrive_expect_tx(&bar->q_full[qs], C::TILE);
         for (int c = 0; c < 2; ++c)
-          tma_load_4d(sQ + qs * C::TILE + c * QB * 128, mq, &bar->q_full[qs], c * 64, hq, row, U.b);
+          tma_load_4d(sQ + qs * C::TILE + c * QB * 128, tails.x(&tmq, tile + QB > U.nq), &bar->q_full[qs], c * 64, hq, row, U.b);
       }
       ++nq_issued;
       ok = mbar_wait(&bar->g_empty[gs], (static_cast<uint32_t>(t / C::NG) & 1u) ^ 1u, a.status, 0x1408 + gs);
@@ -825,7 +813,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lane == 0) {
         mbar_arrive_expect_tx(&bar->g_full[gs], C::TILE);
         for (int c = 0; c < 2; ++c)
-          tma_load_4d(sG + gs * C::TILE + c * QB * 128, mdo, &bar->g_full[gs], c * 64, hq, row, U.b);
+          tma_load_4d(sG + gs * C::TILE + c * QB * 128, tails.y(&tmdo, tile + QB > U.nq), &bar->g_full[gs], c * 64, hq, row, U.b);
       }
       ++ng_issued;
       ok = mbar_wait(&bar->v_empty[vs], (static_cast<uint32_t>(t / C::NVEC) & 1u) ^ 1u, a.status, 0x1410 + vs);
@@ -1275,28 +1263,24 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int c = 0; c < C::VCH; ++c)
         tma_load_4d(sdO + c * MB * 128, &tmdo, &bar->q_full, c * 64, h, U.q_start + q0, U.b);
       const int hk = h / a.kv_group;  // the K/V head of this query head
-      const CUtensorMap *mk = &tmk, *mv = &tmv;
-      if (!SPARSE && a.seq_maps != nullptr) {  // the sequence's, whose rows end with it
-        mk = seq_map(a, U, kMapK), mv = seq_map(a, U, kMapV);
-        tensormap_acquire(mk);
-        tensormap_acquire(mv);
-      }
+      const TailMaps tails(a, U, kMapK, kMapV, !SPARSE);
       int nk_issued = 0, nv_issued = 0;
       bool ok = true;
       for (int t = 0; t < T && ok; ++t) {
         const int row = U.k_start + key_block(t) * KB;
+        const bool tail = row + KB > U.k_start + U.nk;
         const int ks = t % C::KST, vs = t % C::VST;
         ok = mbar_wait(&bar->k_empty[ks], (static_cast<uint32_t>(t / C::KST) & 1u) ^ 1u, a.status, 0x2100 + ks);
         if (!ok) break;
         mbar_arrive_expect_tx(&bar->k_full[ks], C::K_BYTES);
         for (int c = 0; c < C::QCH; ++c)
-          tma_load_4d(sKr + ks * C::K_BYTES + c * KB * 128, mk, &bar->k_full[ks], c * 64, hk, row, U.b);
+          tma_load_4d(sKr + ks * C::K_BYTES + c * KB * 128, tails.x(&tmk, tail), &bar->k_full[ks], c * 64, hk, row, U.b);
         ++nk_issued;
         ok = mbar_wait(&bar->v_empty[vs], (static_cast<uint32_t>(t / C::VST) & 1u) ^ 1u, a.status, 0x2108 + vs);
         if (!ok) break;
         mbar_arrive_expect_tx(&bar->v_full[vs], C::V_BYTES);
         for (int c = 0; c < C::VCH; ++c)
-          tma_load_4d(sVr + vs * C::V_BYTES + c * KB * 128, mv, &bar->v_full[vs], c * 64, hk, row, U.b);
+          tma_load_4d(sVr + vs * C::V_BYTES + c * KB * 128, tails.y(&tmv, tail), &bar->v_full[vs], c * 64, hk, row, U.b);
         ++nv_issued;
       }
       if (!ok) {  // let the copies in flight land before the CTA exits

@@ -27,7 +27,7 @@
 // a few keys. The MMA takes A and B of one type, so V is read from an fp16 copy
 // made by v_to_f16_kernel before the launch (exact for 2^-17 <= |v| < 65536). When
 // that pass found a finite value above fp16's range or a row that fp16 cannot hold
-// (a.v16_flag != 0), or no copy was made (a.v16_flag == nullptr), V and P stay bf16
+// (bit 0 of *a.v16_flag), or no copy was made (a.v16_flag == nullptr), V and P stay bf16
 // for the whole call.
 //
 // This header holds the kernel template and its launch template; the
@@ -103,7 +103,7 @@ __device__ __forceinline__ int kv_head(const FwdArgs& a, int h) {
 }
 
 // V (and so P) in fp16 for this call: a copy was made and every value fit.
-__device__ __forceinline__ bool v_is_f16(const FwdArgs& a) { return a.v16_flag != nullptr && __ldg(a.v16_flag) == 0u; }
+__device__ __forceinline__ bool v_is_f16(const FwdArgs& a) { return a.v16_flag != nullptr && (__ldg(a.v16_flag) & 1u) == 0u; }
 
 // Number of visible keys of query row `row` (0-based within its sequence).
 __device__ __forceinline__ int key_limit(int row, int nq, int nk, int causal) {
@@ -303,13 +303,17 @@ __global__ void __launch_bounds__(kThreads, 1)
       // read while the Q copies fly: V from the fp16 copy, or the bf16 original
       const bool vf16 = v_is_f16(a);
       const CUtensorMap* tmvv = vf16 ? &tmv16 : &tmv;
-      if (a.seq_maps != nullptr) {  // that of the sequence, whose rows end with it (looked up anew, not kept in a register)
+      tma_prefetch_desc(tmvv);
+      // V of the block that a packed sequence ends in, where V or its copy is not all finite: by the sequence's own map, whose rows
+      // end with it (a map of its own costs a CTA its fetch, about 0.5 us).
+      const CUtensorMap* tmv_tail = tmvv;
+      if (a.seq_maps != nullptr && (F8 || (__ldg(a.v16_flag) & 2u) != 0u)) {
         const int seq = LIST ? __ldg(&a.tiles[blockIdx.x].seq)
                              : grid_slot(static_cast<int>(blockIdx.x), a.num_units * a.heads, a.n_mblk, a.n_groups).pair / a.heads;
-        tmvv = a.seq_maps + (2 * static_cast<int64_t>(seq) + (vf16 ? 1 : 0));
-        tensormap_acquire(tmvv);
+        tmv_tail = a.seq_maps + (2 * static_cast<int64_t>(seq) + (vf16 ? 1 : 0));
+        tensormap_acquire(tmv_tail);
       }
-      tma_prefetch_desc(tmvv);
+      auto v_map = [&](int kb) { return (kb + 1) * BN > nk ? tmv_tail : tmvv; };
       if constexpr (C::SPLIT) {
         // Split rings: K0, then K(j+1) before V(j), since a K slot frees a step
         // before the V slot does.
@@ -334,7 +338,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           } else {
             mbar_arrive_expect_tx(&bar->kv_full[slot], C::V_BYTES);
             for (int c = 0; c < C::VCH; ++c)
-              tma_load_4d(dst + c * kChunk, tmvv, &bar->kv_full[slot], c * 64, hk, k_start + kb * BN, b);
+              tma_load_4d(dst + c * kChunk, v_map(kb), &bar->kv_full[slot], c * 64, hk, k_start + kb * BN, b);
           }
           last_use[slot] = static_cast<int>(use);
         }
@@ -363,7 +367,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             } else {
               mbar_arrive_expect_tx(&bar->kv_full[slot], C::V_BYTES);
               for (int c = 0; c < C::VCH; ++c)
-                tma_load_4d(dst + c * kChunk, tmvv, &bar->kv_full[slot], c * 64, hk, k_start + kb * BN, b);
+                tma_load_4d(dst + c * kChunk, v_map(kb), &bar->kv_full[slot], c * 64, hk, k_start + kb * BN, b);
             }
             ++issued;
           }

@@ -167,9 +167,9 @@ struct FwdArgs {
   const int* kv_index;
   int max_kv;
   uint32_t spin_limit;       // diagnostic launches only: poll limit of every wait
-  // Device word written by v_to_f16 before the launch: 0 = V is read from the
-  // fp16 copy (map tv16) and P is packed in fp16; nonzero, or a null pointer,
-  // = V and P in bf16.
+  // Device word written by v_to_f16 before the launch: bit 0 clear = V is read from
+  // the fp16 copy (map tv16) and P is packed in fp16; set, or a null pointer, = V and
+  // P in bf16. Bit 1: V or its copy is not all finite.
   const uint32_t* v16_flag;
   // Packed variable-length only (nullptr otherwise): one entry per CTA, and
   // the number of entries (the grid).
@@ -224,10 +224,12 @@ cudaError_t launch_fwd_mod(int d_qk, int d_v, const CUtensorMap& tq, const CUten
 
 // fp16 copy of V (contiguous [nb, nrows, heads, dv]) for the forward's PV
 // product; ORs 1 into *flag (zeroed by the caller) if a finite value is above
-// fp16's range, or a head's row holds only values that it loses bits of.
+// fp16's range, or a head's row holds only values that it loses bits of, and 2 if a
+// value of the copy is not finite. used (packed): the device word that counts the rows that
+// belong to a sequence; those behind them set only the latter.
 // early: behind launch_tile_lists, whose kernel it runs beside (it waits before it sets the flag and before it ends).
 cudaError_t launch_v_to_f16(const void* v, int64_t sb, int64_t sn, int64_t sh, int nb, int nrows, int heads, int dv,
-                            void* out, uint32_t* flag, bool early, cudaStream_t stream);
+                            void* out, uint32_t* flag, const int* used, bool early, cudaStream_t stream);
 
 // Block-sparse forward (dense layout, cu_q == nullptr, emu_period == 0): the
 // same kernel walking a.kv_index's key blocks instead of 0 .. nkv-1.
@@ -334,17 +336,17 @@ enum SeqMapBwd : int { kMapQ = 0, kMapDO, kMapK, kMapV, kMapQr, kMapDOr };
 cudaError_t launch_bwd_single_pass(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                                    const CUtensorMap& tdo, const BwdArgs& a, cudaStream_t stream);
 cudaError_t launch_bwd_dq_convert(const BwdArgs& a, int d, cudaStream_t stream);
-// D = rowsum(dO * O) into args.dsum. early: behind launch_tile_lists, whose kernel it runs beside.
-cudaError_t launch_bwd_preprocess(int d_v, const BwdArgs& a, bool early, cudaStream_t stream);
-// The same D from q, k, v, dO and the LSE, for the rows of sequences (dense: a call) of at most kFewKeys keys; the others'
-// are left as they are. early: behind launch_bwd_preprocess or launch_tile_lists.
+// D = rowsum(dO * O) into args.dsum, for the rows of packed sequences of at most kFewKeys keys from q, k, v, dO and the
+// LSE. early: behind launch_tile_lists, whose kernel it runs beside.
 constexpr int kFewKeys = 8;
 struct FewKeys {
   const __nv_bfloat16 *q, *k, *v;
   int64_t q_sb, q_sn, q_sh, k_sb, k_sn, k_sh, v_sb, v_sn, v_sh;
+  int d_qk, d_v;
 };
-cudaError_t launch_bwd_few_keys_dsum(int d_qk, int d_v, const BwdArgs& a, const FewKeys& t, bool early,
-                                     cudaStream_t stream);
+cudaError_t launch_bwd_preprocess(int d_v, const BwdArgs& a, const FewKeys& t, bool early, cudaStream_t stream);
+// The latter alone, for a call in which no row sees more keys.
+cudaError_t launch_bwd_few_keys_dsum(const BwdArgs& a, const FewKeys& t, bool early, cudaStream_t stream);
 // dK, dV (KV-stationary) and dQ (Q-stationary). Maps: q, k, v, dO. With
 // a.kv_count set they walk the block-sparse lists (dense layout only).
 cudaError_t launch_bwd_dkdv(int d_qk, int d_v, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,

@@ -42,7 +42,8 @@ def _short_rows_error(t, grads, lens_q, lens_k, scale, causal, mod=None):
                 diff[i] += np.sum((to64(got[i]) - r[n]) ** 2)
                 norm[i] += np.sum(r[n] ** 2)
         a, b = a + lq, b + lk
-    return np.sqrt(diff / norm)
+    with np.errstate(divide="ignore"):  # a gradient that is 0 in exact arithmetic (one key)
+        return np.sqrt(diff / norm)
 
 
 MIXES = [([1, 2] * 20 + [9], [1, 2] * 20 + [9]), ([1, 2, 300, 1, 3] * 8, [1, 2, 300, 8, 5] * 8),

@@ -88,3 +88,15 @@ def test_gradients_of_small_values(ea):
     torch.cuda.synchronize()
     ref = shared_bwd(*(to64(x[0]) for x in (q, k, v, do)), 128 ** -0.5, True)
     check_grads({n: x[0] for n, x in zip(("dq", "dk", "dv"), g)}, ref, "small values")
+
+
+def test_spare_rows_do_not_choose_the_type(ea):
+    """Rows behind the last sequence, whatever they hold, leave the results the same bits."""
+    q, k, v = (_rand(240, 2, 64, seed=s).to(torch.bfloat16).cuda() for s in (14, 15, 16))
+    cu = torch.tensor([0, 70, 200], dtype=torch.int32, device="cuda")
+    want = ea.attn_fwd_varlen(q, k, v, cu, cu, 130, 130, causal=True)
+    for value in (1e-30, 1e30, float("nan")):
+        v[200:] = value
+        got = ea.attn_fwd_varlen(q, k, v, cu, cu, 130, 130, causal=True)
+        torch.cuda.synchronize()
+        assert torch.equal(got[0][:200], want[0][:200]) and torch.equal(got[1][:, :200], want[1][:, :200])

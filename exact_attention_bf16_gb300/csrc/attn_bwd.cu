@@ -132,15 +132,25 @@ __global__ void __launch_bounds__(256, PACKED ? kPackedBlocks : 8) preprocess_ke
       if (__ldg(a.cu_q + m) <= first) unit = m;
       else e = m;
     }
-    for (; unit < a.num_units && __ldg(a.cu_q + unit) <= last; ++unit) {
-      const Unit U = unit_bounds(a, unit);
-      if (!few_keys(a, U)) continue;
-      const int64_t r_end = min(rows, static_cast<int64_t>(U.q_start + U.nq) * a.heads);
-      for (int64_t r0 = max(begin, static_cast<int64_t>(U.q_start) * a.heads) + (threadIdx.x >> 5) * 4; r0 < r_end; r0 += 32) {
-        const int64_t r = r0 + (lane >> 3), at = min(r, r_end - 1);
-        const int i = static_cast<int>(at / a.heads), h = static_cast<int>(at % a.heads);
-        const float d = few_keys_d(a, t, U, i - U.q_start, h, lane & 7);
-        if (r < r_end && (lane & 7) == 0) a.dsum[h * a.lse_sh + i] = d;
+    // 32 sequences are looked at together (a step captured for many has a run of empty ones), by every warp alike
+    for (bool more = true; more; unit += 32) {
+      const int mine = unit + lane;
+      const bool in = mine < a.num_units && __ldg(a.cu_q + mine) <= last;
+      bool few = false;
+      if (in) {
+        const Unit U = unit_bounds(a, mine);
+        few = U.nq > 0 && few_keys(a, U);
+      }
+      more = __all_sync(0xffffffffu, in);
+      for (uint32_t left = __ballot_sync(0xffffffffu, few); left != 0; left &= left - 1) {
+        const Unit U = unit_bounds(a, unit + __ffs(left) - 1);
+        const int64_t r_end = min(rows, static_cast<int64_t>(U.q_start + U.nq) * a.heads);
+        for (int64_t r0 = max(begin, static_cast<int64_t>(U.q_start) * a.heads) + (threadIdx.x >> 5) * 4; r0 < r_end; r0 += 32) {
+          const int64_t r = r0 + (lane >> 3), at = min(r, r_end - 1);
+          const int i = static_cast<int>(at / a.heads), h = static_cast<int>(at % a.heads);
+          const float d = few_keys_d(a, t, U, i - U.q_start, h, lane & 7);
+          if (r < r_end && (lane & 7) == 0) a.dsum[h * a.lse_sh + i] = d;
+        }
       }
     }
   }

@@ -137,3 +137,20 @@ def test_dense(ea, dims, nk, causal):
     torch.cuda.synchronize()
     for x, y in zip(packed, flat[4:]):
         assert torch.equal(x, y)
+
+
+@pytest.mark.parametrize("heads", [(4, 2), (33, 11)])
+def test_runs_of_empty_sequences(ea, heads):
+    """A step captured for many sequences: runs of empty ones between and behind the others, spare rows, and sequences of
+    many queries over few keys beside short ones."""
+    lens_q = [3] + [0] * 700 + [2, 900, 1] + [0] * 45 + [40, 6] + [0] * 1000
+    lens_k = [3] + [0] * 350 + [4] + [0] * 349 + [2, 5, 1] + [0] * 45 + [300, 6] + [0] * 1000
+    q, do = _rand(sum(lens_q) + 60, heads[0], 64, seed=31), _rand(sum(lens_q) + 60, heads[0], 64, seed=32)
+    k, v = _rand(sum(lens_k) + 60, heads[1], 64, seed=33), _rand(sum(lens_k) + 60, heads[1], 64, seed=34)
+    cq, ck = _cu(lens_q), _cu(lens_k)
+    o, lse = ea.attn_fwd_varlen(q, k, v, cq, ck, 960, 360)
+    g = ea.attn_bwd_varlen(q, k, v, o, lse, do, cq, ck, 960, 360)
+    torch.cuda.synchronize()
+    ea.attn_get_device_status()
+    err = _short_rows_error((q, k, v, do), g, lens_q, lens_k, 0.125, False)
+    assert np.all(err <= TOL), err

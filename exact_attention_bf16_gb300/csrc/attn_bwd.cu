@@ -85,43 +85,79 @@ __global__ void __launch_bounds__(256) few_keys_dsum_kernel(const BwdArgs a, con
 // PACKED: a block takes `chunk` rows side by side and then, where sequences of few keys
 // lie in them, replaces those sequences' D by few_keys_d's. (A choice per row in the
 // loop cost the rows of longer sequences 40% of its time, a pass of its own behind this
-// one 1 us of every call.)
-constexpr int kPackedBlocks = 6;  // per SM: at 8 few_keys_d spills (3000 sequences of 1 to 30 tokens, the backward: 1557 us, 1616)
+// one 1 us of every call.) A row's token and head are stepped from pass to pass: with
+// two divisions a row the pass was bound by its instructions (8 sequences of 2048, 32
+// heads, d = 128, the backward: 938 us, 922 so).
+constexpr int kPackedBlocks = 6;  // per SM: at 8 few_keys_d spills (3000 sequences of 1 to 30 tokens, the backward: 1550 us, 1621)
 template <int DV, bool PACKED>
 __global__ void __launch_bounds__(256, PACKED ? kPackedBlocks : 8) preprocess_kernel(const BwdArgs a, const __grid_constant__ FewKeys t, int64_t chunk) {
   constexpr int LPR = DV / 8;    // lanes per row
   constexpr int RPW = 32 / LPR;  // rows per warp
-  const int64_t all = static_cast<int64_t>(a.batch) * a.seqlen_q * a.heads;
   const int lane = threadIdx.x & 31;
   const int sub = lane / LPR, l = lane % LPR;
-  const int64_t begin = PACKED ? blockIdx.x * chunk : 0, rows = PACKED ? min(all, begin + chunk) : all;
-  const int64_t warp0 = PACKED ? threadIdx.x >> 5 : (blockIdx.x * static_cast<int64_t>(blockDim.x) + threadIdx.x) >> 5;
-  const int64_t nwarps = PACKED ? 8 : (static_cast<int64_t>(gridDim.x) * blockDim.x) >> 5;
-  for (int64_t r0 = begin + warp0 * RPW; r0 < rows; r0 += nwarps * RPW) {
-    const int64_t r = r0 + sub;
+  auto dot8 = [](const uint4& x, const uint4& y) {
+    const uint32_t xw[4] = {x.x, x.y, x.z, x.w}, yw[4] = {y.x, y.y, y.z, y.w};
     float acc = 0.f;
-    int h = 0, i = 0, b = 0;
-    if (r < rows) {
-      h = static_cast<int>(r % a.heads);
-      const int64_t bi = r / a.heads;
-      i = static_cast<int>(bi % a.seqlen_q);
-      b = static_cast<int>(bi / a.seqlen_q);
-      const __nv_bfloat16* o = static_cast<const __nv_bfloat16*>(a.o) + b * a.o_sb + i * a.o_sn + h * a.o_sh;
-      const __nv_bfloat16* g = static_cast<const __nv_bfloat16*>(a.dout) + b * a.do_sb + i * a.do_sn + h * a.do_sh;
-      const uint4 ov = *reinterpret_cast<const uint4*>(o + 8 * l);
-      const uint4 gv = *reinterpret_cast<const uint4*>(g + 8 * l);
-      const uint32_t ow[4] = {ov.x, ov.y, ov.z, ov.w}, gw[4] = {gv.x, gv.y, gv.z, gv.w};
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const float2 of = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&ow[e]));
-        const float2 gf = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&gw[e]));
-        acc = fmaf(of.x, gf.x, acc);
-        acc = fmaf(of.y, gf.y, acc);
-      }
+    for (int e = 0; e < 4; ++e) {
+      const float2 xf = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&xw[e]));
+      const float2 yf = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&yw[e]));
+      acc = fmaf(xf.x, yf.x, acc);
+      acc = fmaf(xf.y, yf.y, acc);
     }
 #pragma unroll
     for (int s = LPR / 2; s > 0; s >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, s);
-    if (r < rows && l == 0) a.dsum[b * a.lse_sb + h * a.lse_sh + i] = acc;
+    return acc;
+  };
+  const __nv_bfloat16* o = static_cast<const __nv_bfloat16*>(a.o) + 8 * l;
+  const __nv_bfloat16* g = static_cast<const __nv_bfloat16*>(a.dout) + 8 * l;
+  const int64_t all = static_cast<int64_t>(a.batch) * a.seqlen_q * a.heads;
+  const int64_t begin = PACKED ? blockIdx.x * chunk : 0, rows = PACKED ? min(all, begin + chunk) : all;
+  if constexpr (PACKED) {
+    // two rows in flight
+    constexpr int STEP = 8 * RPW;
+    const int di = STEP / a.heads, dh = STEP - di * a.heads;
+    int64_t r = begin + (threadIdx.x >> 5) * RPW + sub;
+    int i = static_cast<int>(r / a.heads), h = static_cast<int>(r - static_cast<int64_t>(i) * a.heads);
+    for (int64_t r0 = r - sub; r0 < rows; r0 += 2 * STEP) {
+      uint4 ov[2], gv[2];
+      int64_t at[2];
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        at[u] = -1;
+        ov[u] = gv[u] = make_uint4(0, 0, 0, 0);
+        if (r < rows) {
+          at[u] = h * a.lse_sh + i;
+          ov[u] = *reinterpret_cast<const uint4*>(o + i * a.o_sn + h * a.o_sh);
+          gv[u] = *reinterpret_cast<const uint4*>(g + i * a.do_sn + h * a.do_sh);
+        }
+        r += STEP, i += di, h += dh;
+        if (h >= a.heads) h -= a.heads, ++i;
+      }
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const float d = dot8(ov[u], gv[u]);
+        if (at[u] >= 0 && l == 0) a.dsum[at[u]] = d;
+      }
+    }
+  } else {
+    const int64_t warp0 = (blockIdx.x * static_cast<int64_t>(blockDim.x) + threadIdx.x) >> 5;
+    const int64_t nwarps = (static_cast<int64_t>(gridDim.x) * blockDim.x) >> 5;
+    for (int64_t r0 = warp0 * RPW; r0 < rows; r0 += nwarps * RPW) {
+      const int64_t r = r0 + sub;
+      uint4 ov = make_uint4(0, 0, 0, 0), gv = ov;
+      int h = 0, i = 0, b = 0;
+      if (r < rows) {
+        h = static_cast<int>(r % a.heads);
+        const int64_t bi = r / a.heads;
+        i = static_cast<int>(bi % a.seqlen_q);
+        b = static_cast<int>(bi / a.seqlen_q);
+        ov = *reinterpret_cast<const uint4*>(o + b * a.o_sb + i * a.o_sn + h * a.o_sh);
+        gv = *reinterpret_cast<const uint4*>(g + b * a.do_sb + i * a.do_sn + h * a.do_sh);
+      }
+      const float d = dot8(ov, gv);
+      if (r < rows && l == 0) a.dsum[b * a.lse_sb + h * a.lse_sh + i] = d;
+    }
   }
   if constexpr (PACKED) {
     __syncthreads();  // the D above are written

@@ -54,9 +54,9 @@ KERNEL_SOURCES = {
                         "kernels.h"),
 }
 KERNEL_TRAFFIC_NCU = {
-    "dkdv_wide_kernel": {"source_sha": "0e5c13170f822e3d", "bytes_per_launch": 2 * (270.638848e6 + 107.483392e6)},
-    "dq_kernel": {"source_sha": "0e5c13170f822e3d", "bytes_per_launch": 2 * (270.719488e6 + 50.029568e6)},
-    "attn_fwd_kernel": {"source_sha": "3484d0e8f058a718", "bytes_per_launch": 2 * (201.458944e6 + 49.052160e6)},
+    "dkdv_wide_kernel": {"source_sha": "b4c969d031f96807", "bytes_per_launch": 2 * (270.599424e6 + 108.157696e6)},
+    "dq_kernel": {"source_sha": "b4c969d031f96807", "bytes_per_launch": 2 * (270.853888e6 + 50.331136e6)},
+    "attn_fwd_kernel": {"source_sha": "b73c8f1eaec16b08", "bytes_per_launch": 2 * (201.449472e6 + 48.839424e6)},
 }
 
 

@@ -1059,7 +1059,6 @@ attn_status_t run_fwd_paged(const attn_paged_params* p, void* ws, size_t ws_byte
   a.cu_q = p->cu_seqlens_q;
   a.seqlens_k = p->seqlens_k;
   a.num_seqs = p->num_seqs;
-  a.heads = p->heads;
   a.heads_kv = p->heads_kv;
   a.kv_group = p->heads / p->heads_kv;
   a.page_size = p->page_size;

@@ -31,9 +31,10 @@
 //     that chunk_list_kernel builds, a request's units together, long requests
 //     and late units (the most keys under the causal mask) first. Only units
 //     longer than an equal share of the work are cut. 24 requests, chunks of 500..2048 tokens over
-//     up to 16384 keys, 32 heads over 8, d = 128: 512 us, 1190 TFLOP/s (the contiguous
-//     causal forward: 1165 at 4096 keys, 1375 at 8192); the tensor pipe is active 55% of the time, the rest is the
-//     chain S -> softmax -> PV of the two tiles and the ends of the units.
+//     up to 16384 keys, 32 heads over 8, d = 128: 512 us, 1190 TFLOP/s; four times the work over
+//     like lengths 1360 (the contiguous causal forward: 1230 at 4096 keys, 1450 at 8192, 1590 at 32768). The tensor
+//     pipe is active 55% of the time. A pair of blocks takes some 3,760 cycles: the chain S -> softmax -> PV of the two
+//     tiles 2,900, the rest is the units' ends, single tokens that share the list, the list itself and the merge.
 //
 // Warps: 0 work and TMA copies, 1 MMA issue, 4..7 and 8..11 softmax of tile or
 // stream 0 and 1. K and V have rings of their own; a copy is one box per page
@@ -830,8 +831,9 @@ cudaError_t launch_d(const CUtensorMap& tq, const CUtensorMap& tk, const CUtenso
   }
   if (e != cudaSuccess) return e;
   const int rows = min(a.max_q, (even ? 1 : 2) * a.tile_tokens) * a.kv_group;
-  // up to 16 rows, whose blocks fit the GPU at once: a decoding request of 4100 tokens 13.9 us with eight warps per row,
-  // 17 with one
+  // Up to 16 rows, whose blocks fit the GPU at once, eight warps share a row: 16 rows over 16000 keys 13.0 us, with one warp
+  // 22.8, over 1000 11.4 and 10.2. (32 rows: over 16000 16.3 and 25.2, over 1000 13.4 and 10.8; 33 requests of 3 to 6 tokens
+  // 36.9 and 29.5. The segments decide, which the host does not know.)
   if (rows <= 16)
     return launch_early(merge_kernel<DV, 8>, dim3(ctas, rows), 256, 0, stream, a);
   return launch_early(merge_kernel<DV, 1>, dim3(ctas, (rows + 7) / 8), 256, 0, stream, a);

@@ -16,11 +16,14 @@
 // Bound by HBM: per 128 keys and K/V head at d = 128 64 KB against 16 MMAs of about
 // 50 cycles. 64 requests of up to 32768 tokens, 32 heads over 8, d = 128: 307 us, 6.67 TB/s
 // (98% of a copy's), 321 us by paged_kernel; one of 4100 tokens 13.9 us against 15, its
-// launches, first copies and merge. d = 64 (8 heads of their own, 64 requests) reaches 4.1 TB/s
-// against 3.8: a 128-key block is half the bytes for the same waits. With 32 columns the same calls took 341 us where 16 took 323 and
-// paged_kernel 332 (64 requests, 8 heads, d = 128), with 64 columns 416, so 17 rows and more are
-// paged_kernel's. Work is the even split of paged_common.cuh; two streams over the even and
-// the odd key blocks hide the chain S^T -> softmax -> O^T, as there.
+// launches, first copies and merge. d = 64 (8 heads of their own, 64 requests) reaches 4.2 TB/s
+// against 3.8: a 128-key block is half the bytes for the same waits. (192, 128): 6.3 TB/s.
+// With 32 columns the same calls took 341 us where 16 took 323 and paged_kernel 332 (64
+// requests, 8 heads, d = 128), with 64 columns 416, so 17 rows and more are paged_kernel's. Up
+// to 16 rows of the other head sizes, here and there: d = 64, 8 requests of 8000 tokens 33.4 us
+// and 37.7, one of 4100 13.7 both (16 rows 15.2 and 15.0); (192, 128), one 14.1 and 15.4, 64
+// requests 479 and 484. Work is the even split of paged_common.cuh; two streams over the even
+// and the odd key blocks hide the chain S^T -> softmax -> O^T, as there.
 //
 // Warps: 0 work and TMA copies, 1 MMA issue, 4..7 and 8..11 softmax of stream 0 and 1.
 #include <cstddef>

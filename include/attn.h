@@ -20,8 +20,8 @@
  * queries) iff j < Nk and, when causal != 0, j <= i + (Nk - Nq) (causal mask
  * aligned to the bottom-right corner; equals j <= i when Nq == Nk). A query
  * row that sees no key gets O = 0, LSE = -inf and dQ = 0, whatever the keys and
- * values beside it hold. A row with a
- * NaN or +infinite logit among its visible keys has a NaN LSE and O.
+ * values beside it hold. A row with a NaN or +infinite logit among its visible
+ * keys has a NaN LSE and O.
  *
  * Layouts (all element counts, not bytes). Dense tensors are 4-D
  * [batch, seqlen, heads, head_dim] addressed as
@@ -277,11 +277,10 @@ typedef struct attn_bwd_params {
  * x (4 x d_v + 4) bytes (the two parts each rounded up to 256). The result
  * equals the unsplit one within rounding and is the same bits on every call
  * with the same shapes. The block-sparse forward never splits.
- * The backward's workspace holds D = rowsum(dO * O) (for sequences of at most 8
- * keys computed without O, whose rounding would show in dQ and dK of so few
- * keys): 4 x heads x query rows
- * bytes, rounded up to 256, 16-byte aligned; a variable-length backward adds
- * its tile lists, 32 x heads x (total_k / 128 + num_seqs) bytes for dK/dV
+ * The backward's workspace holds D = rowsum(dO * O) (for sequences, or dense
+ * calls, of at most 8 keys computed without O, whose rounding would show in dQ and
+ * dK of so few keys): 4 x heads x query rows bytes, rounded up to 256, 16-byte
+ * aligned; a variable-length backward adds its tile lists, 32 x heads x (total_k / 128 + num_seqs) bytes for dK/dV
  * (none with cta_pair) and 32 x heads x (total_q / 128 + num_seqs) for dQ, and
  * 8 x num_seqs bytes of scratch, each rounded up to 256.
  * A dense two-kernel backward (bf16, single_pass 0, any supported head size,
@@ -470,18 +469,18 @@ attn_status_t attn_kv_append(const attn_kv_append_params* p, attn_stream_t strea
  * keys. o [total_q, heads, d_v] (bf16) and lse [heads, total_q] (fp32,
  * contiguous) as for attn_fwd_varlen, score modifications too; a row that sees
  * no key gets O = 0 and LSE = -inf, whatever the keys and values beside it hold.
- * Rows of o and lse behind the last request
- * are left as they were.
+ * Rows of o and lse behind the last request are left as they were.
  * Lengths are clamped: seqlens_k to [0, max_pages * page_size], the offsets of
  * q to [0, total_q]. max_seqlen_q is a bound the caller gives; it sizes the
- * launch: of a request with more queries the first max_seqlen_q are computed,
- * as they are with a larger bound, and the rows of the others left as they were. Keys on a page whose table entry is
- * outside [0, num_pages) are masked. Cache rows past seqlens_k may hold
- * anything, infinities and NaN included, and reach no result; a non-finite
- * value among a request's own visible keys or values reaches every query row
- * of that request that sees a key of the 128-key block that holds it, also rows
- * that the causal mask hides it from. A row with a NaN or +infinite logit among its visible keys has a
- * NaN LSE and O, split across SMs or not.
+ * launch: of a request with more queries the first max_seqlen_q are computed, as
+ * they are with a larger bound, and the rows of the others left as they were.
+ * Keys on a page whose table entry is outside [0, num_pages) are masked. Cache
+ * rows past seqlens_k may hold anything, infinities and NaN included, and reach
+ * no result; a non-finite value among a request's own visible keys or values
+ * reaches every query row of that request that sees a key of the 128-key block
+ * that holds it, also rows that the causal mask hides it from. A row with a NaN
+ * or +infinite logit among its visible keys has a NaN LSE and O, split across
+ * SMs or not.
  * P enters the PV product in bf16 (V's type). Results depend on the batch only
  * through the order of additions (keys may be split across SMs and merged in
  * key order): the same call gives the same bits.

@@ -377,7 +377,8 @@ def attn_fwd_varlen(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqlen
                     v_descale: float = 1.0, cta_pair: bool = False,
                     stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
     """Packed variable-length forward. q [total_q, H, d_qk], k/v [total_k, Hkv, d] with Hkv a divisor of H
-    (query head h reads K/V head h // (H // Hkv)); cu_seqlens int32 on the device. Returns
+    (query head h reads K/V head h // (H // Hkv)); cu_seqlens int32 on the device. Sequences do not reach one another,
+    whatever their rows, or spare rows behind the last offset, hold. Returns
     (O [total_q, H, d_v], LSE [H, total_q]). Score modifications and E4M3 inputs as in :func:`attn_fwd`,
     positions counted within each sequence."""
     f8 = q.dtype is torch.float8_e4m3fn
@@ -660,7 +661,8 @@ def attn_fwd_paged(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor
     ``block_table`` [requests, max_pages], the new ones among them, in k_cache [pages, page_size, Hkv, d_qk] and
     v_cache [pages, page_size, Hkv, d_v]; Hkv divides H. With ``causal`` (the default) query i of n sees the keys up
     to position i + seqlens_k[s] - n. cu_seqlens_q [requests + 1], seqlens_k [requests] and the table are int32 on
-    q's GPU; ``max_seqlen_q`` bounds the queries of a request. Score modifications as in :func:`attn_fwd`.
+    q's GPU; ``max_seqlen_q`` bounds the queries of a request (of one with more the first are computed). Score
+    modifications as in :func:`attn_fwd`.
     Returns (O [total_q, H, d_v] bf16, LSE [H, total_q] fp32); rows behind the last request are not written."""
     (tq, H, dqk), sq = _bf16_layout("q", q, 3)
     dev = q.get_device()

@@ -206,3 +206,61 @@ def test_the_least_workspace_gives_the_same_bits(ea):
     ea.attn_get_device_status()
     for x, y in zip((o, lse, *got), (*want, *grads)):
         assert torch.equal(x, y)
+
+
+def test_a_captured_step_with_other_offsets(ea):
+    """Captured on finite rows, replayed with offsets that move and other sequences not finite: the maps and the choice
+    between them are made anew by every replay."""
+    total, H, Hk, d = 700, 4, 2, 128
+    base = [_rand(total, h, d, seed=21 + i) for i, h in enumerate((H, Hk, Hk, H))]
+    t = [x.clone() for x in base]
+    cu = _cu([130, 40, 257, 5, 200])
+    m = 600
+
+    def step(q, k, v, do, cu):
+        o, lse = ea.attn_fwd_varlen(q, k, v, cu, cu, m, m, causal=True)
+        return o, lse.T, *ea.attn_bwd_varlen(q, k, v, o, lse, do, cu, cu, m, m, causal=True, deterministic=True)
+
+    step(*t, cu)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = step(*t, cu)
+    for lens in ([130, 40, 257, 5, 200], [1, 127, 130, 300, 90], [64, 64, 64, 64, 64], [300, 1, 1, 1, 1]):
+        cu.copy_(_cu(lens))
+        want = step(*base, _cu(lens))
+        for value in (float("nan"), float("inf"), None):
+            for x, b in zip(t, base):
+                x.copy_(b if value is None else _spoil(b, lens, value))
+            graph.replay()
+            torch.cuda.synchronize()
+            ea.attn_get_device_status()
+            for g, w in zip(got, want):
+                assert torch.equal(g[_rows(lens)], w[_rows(lens)])
+
+
+def test_two_steps_at_once(ea):
+    """Two streams, sequences that are not finite on both, over and over."""
+    sets = [LENS[0][0], [60, 3, 200, 30, 64]]
+    t = [[_rand(sum(x) + 40, h, 64, seed=31 + 7 * i + j) for j, h in enumerate((2, 2, 2, 2))] for i, x in enumerate(sets)]
+
+    def step(q, k, v, do, lens):
+        cu, m = _cu(lens), max(lens)
+        o, lse = ea.attn_fwd_varlen(q, k, v, cu, cu, m, m, causal=True)
+        return o, *ea.attn_bwd_varlen(q, k, v, o, lse, do, cu, cu, m, m, causal=True, deterministic=True)
+
+    want = [step(*x, lens) for x, lens in zip(t, sets)]
+    bad = [[_spoil(x, lens, float("nan")) for x in xs] for xs, lens in zip(t, sets)]
+    streams = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(10):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got[i].append(step(*bad[i], sets[i]))
+    torch.cuda.synchronize()
+    ea.attn_get_device_status()
+    for i, lens in enumerate(sets):
+        for g in got[i]:
+            for x, w in zip(g, want[i]):
+                assert torch.equal(x[_rows(lens)], w[_rows(lens)])

@@ -154,3 +154,35 @@ def test_runs_of_empty_sequences(ea, heads):
     ea.attn_get_device_status()
     err = _short_rows_error((q, k, v, do), g, lens_q, lens_k, 0.125, False)
     assert np.all(err <= TOL), err
+
+
+def test_block_sparse_of_few_keys(ea):
+    """Lists over a single short key block: query rows whose list is empty see no key."""
+    nq, nk = 300, 5
+    q, k, v, do = _rand(2, nq, 2, 64, seed=41), _rand(2, nk, 2, 64, seed=42), _rand(2, nk, 2, 64, seed=43), _rand(2, nq, 2, 64, seed=44)
+    count = torch.tensor([1, 0], dtype=torch.int32, device="cuda")
+    index = torch.zeros((2, 1), dtype=torch.int32, device="cuda")
+    o, lse = ea.attn_fwd_block_sparse(q, k, v, count, index)
+    dq, dk, dv = ea.attn_bwd_block_sparse(q, k, v, o, lse, do, count, index)
+    torch.cuda.synchronize()
+    ea.attn_get_device_status()
+    assert torch.all(dq[:, 256:] == 0)
+    flat = [x[:, :256].reshape(-1, *x.shape[2:]) for x in (q, k, v, do, dq, dk, dv)]
+    err = _short_rows_error(flat[:4], flat[4:], [256] * 2, [nk] * 2, 0.125, False)
+    assert np.all(err <= TOL), err
+
+
+def test_strided_dense_rows_of_few_keys(ea):
+    """K and V as views of one fused buffer, Q and dO with spare columns: the same bits as contiguous ones."""
+    qd, kv = _rand(3, 20, 4, 256, seed=45), _rand(3, 6, 2, 256, seed=46)
+    views = qd[..., :128], kv[..., :128], kv[..., 128:], qd[..., 128:]
+    dense = [x.contiguous() for x in views]
+
+    def grads(q, k, v, do):
+        o, lse = ea.attn_fwd(q, k, v, causal=True)
+        return ea.attn_bwd(q, k, v, o, lse, do, causal=True)
+
+    a, b = grads(*views), grads(*dense)
+    torch.cuda.synchronize()
+    for x, y in zip(a, b):
+        assert torch.equal(x, y)

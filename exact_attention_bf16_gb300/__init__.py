@@ -17,8 +17,8 @@ from typing import Optional, Tuple, Union
 import torch
 
 from . import _abi
-from ._abi import (AttnBwdParams, AttnError, AttnFwdParams, AttnKvAppendParams, AttnKvPlanParams,  # noqa: F401
-                   AttnPagedParams)
+from ._abi import (AttnBwdParams, AttnError, AttnFwdParams, AttnKvAppendParams, AttnKvAppendRotaryParams,  # noqa: F401
+                   AttnKvPlanParams, AttnPagedParams, AttnRotaryParams)
 
 _lib = _abi.load()
 
@@ -27,7 +27,8 @@ SUPPORTED_HEAD_DIMS = ((64, 64), (128, 128), (192, 128))
 __all__ = [
     "attn_fwd", "attn_fwd_block_sparse", "attn_fwd_varlen", "attn_bwd", "attn_bwd_block_sparse",
     "block_lists_from_mask", "attn_bwd_varlen", "attn_exp2_eval",
-    "attn_kv_plan", "attn_kv_append", "attn_fwd_paged", "attn_get_device_status", "attention", "attention_varlen", "AttnError", "SUPPORTED_HEAD_DIMS", "library_path",
+    "attn_kv_plan", "attn_kv_append", "attn_kv_append_rotary", "attn_fwd_paged", "attn_rotary", "attn_get_device_status",
+    "attention", "attention_varlen", "rotary", "AttnError", "SUPPORTED_HEAD_DIMS", "library_path",
 ]
 
 
@@ -39,6 +40,7 @@ _BF16, _I32, _I64, _F32 = torch.bfloat16, torch.int32, torch.int64, torch.float3
 _pack_fwd, _pack_bwd = _abi.packer(AttnFwdParams), _abi.packer(AttnBwdParams)
 _pack_plan, _pack_append, _pack_paged = (_abi.packer(AttnKvPlanParams), _abi.packer(AttnKvAppendParams),
                                          _abi.packer(AttnPagedParams))
+_pack_rotary, _pack_append_rotary = _abi.packer(AttnRotaryParams), _abi.packer(AttnKvAppendRotaryParams)
 _raw_stream = torch._C._cuda_getCurrentRawStream
 
 
@@ -567,13 +569,14 @@ def attn_kv_plan(seqlens_old: torch.Tensor, seqlens_new: torch.Tensor, block_tab
                  free_pages: torch.Tensor, free_count: torch.Tensor, page_size: int,
                  slot_mapping: Union[torch.Tensor, int], *, cu_seqlens_q: Optional[torch.Tensor] = None,
                  seqlens_k: Optional[torch.Tensor] = None, free_count_out: Optional[torch.Tensor] = None,
-                 status: Optional[torch.Tensor] = None, stream=None):
+                 status: Optional[torch.Tensor] = None, positions: Optional[torch.Tensor] = None, stream=None):
     """Plans one step of a paged KV cache on the GPU (include/attn.h, attn_kv_plan): pages for every request's
     new tokens, and their slots. Request s holds ``seqlens_old[s]`` tokens and adds ``seqlens_new[s]`` (negative:
     it ends and returns its pages); its pages are listed in row s of ``block_table`` [requests, max_pages], and free
     ones on the stack ``free_pages[:free_count]``. The table, the stack and ``free_count`` (or ``free_count_out``,
     when given) are updated. ``slot_mapping`` is an int64 tensor, or the number of entries of one to make; entries
-    past the step's tokens become -1. All other arrays are int32.
+    past the step's tokens become -1. All other arrays are int32; ``positions``, when given, has as many entries as
+    ``slot_mapping`` and gets each new token's position in its request (for :func:`attn_kv_append_rotary`), then -1.
     Returns (cu_seqlens_q [requests + 1], seqlens_k [requests], slot_mapping, status [1]): status 0, or 1 (too few
     free pages), 2 (a row of the table is too short), 3 (slot_mapping is), 4 (free_pages is), and then nothing is
     changed and the step holds no tokens."""
@@ -605,10 +608,13 @@ def attn_kv_plan(seqlens_old: torch.Tensor, seqlens_new: torch.Tensor, block_tab
     elif slot_mapping.dtype is not _I64 or slot_mapping.dim() != 1 or not slot_mapping.is_contiguous() or \
             not slot_mapping.is_cuda or slot_mapping.get_device() != dev:
         raise ValueError(f"slot_mapping must be a contiguous int64 tensor [max_tokens] on cuda:{dev}")
+    if positions is not None:
+        _check_int32("positions", positions, dev, slot_mapping.shape[0])
     p = _pack_plan(seqlens_old.data_ptr(), seqlens_new.data_ptr(), block_table.data_ptr(), table_stride,
                    free_pages.data_ptr(), free_count.data_ptr(), free_count_out.data_ptr(), cu_seqlens_q.data_ptr(),
                    seqlens_k.data_ptr(), slot_mapping.data_ptr(), status.data_ptr(),
-                   n, block_table.shape[1], int(page_size), free_pages.shape[0], slot_mapping.shape[0])
+                   n, block_table.shape[1], int(page_size), free_pages.shape[0], slot_mapping.shape[0],
+                   0 if positions is None else positions.data_ptr())
     st = _lib.attn_kv_plan(p, _stream_of(stream, seqlens_old))
     if st:
         _abi.check(st, "attn_kv_plan")
@@ -632,6 +638,14 @@ def attn_kv_append(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_ca
     page_size, Hkv, d_qk] and v_cache [pages, page_size, Hkv, d_v] (bf16, any strides with contiguous d): row i goes
     to slot ``slot_mapping[i]`` (int64; page slot // page_size, row slot % page_size). Slots outside the cache, as -1,
     write nothing; slots must differ."""
+    p, _ = _append_fields(k, v, k_cache, v_cache, slot_mapping)
+    st = _lib.attn_kv_append(_pack_append(*p), _stream_of(stream, k))
+    if st:
+        _abi.check(st, "attn_kv_append")
+
+
+def _append_fields(k, v, k_cache, v_cache, slot_mapping):
+    """The fields of a checked append (attn_kv_append_params), and k's shape."""
     (ks, kt), (vs, vt) = _bf16_layout("k", k, 3), _bf16_layout("v", v, 3)
     dev = k.get_device()
     kcs, kct, vcs, vct = _cache_layout(k_cache, v_cache, dev)
@@ -642,12 +656,122 @@ def attn_kv_append(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_ca
     if slot_mapping.dtype is not _I64 or slot_mapping.dim() != 1 or slot_mapping.shape[0] != ks[0] or \
             not slot_mapping.is_contiguous() or not slot_mapping.is_cuda or slot_mapping.get_device() != dev:
         raise ValueError(f"slot_mapping must be a contiguous int64 tensor [{ks[0]}] on cuda:{dev}")
-    p = _pack_append(k.data_ptr(), v.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), kt[0], kt[1], vt[0], vt[1],
-                     kct[0], kct[1], kct[2], vct[0], vct[1], vct[2], slot_mapping.data_ptr(),
-                     ks[0], ks[1], ks[2], vs[2], kcs[1], kcs[0])
-    st = _lib.attn_kv_append(p, _stream_of(stream, k))
+    return (k.data_ptr(), v.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), kt[0], kt[1], vt[0], vt[1],
+            kct[0], kct[1], kct[2], vct[0], vct[1], vct[2], slot_mapping.data_ptr(),
+            ks[0], ks[1], ks[2], vs[2], kcs[1], kcs[0]), ks
+
+
+def _check_rotation(cos, sin, device: int, rotary_offset: int):
+    """The checked tables' fields: pointers, row stride, positions, rotary_dim."""
+    for n, t in (("cos", cos), ("sin", sin)):
+        if not isinstance(t, torch.Tensor) or t.dtype is not _F32 or not t.is_cuda or t.dim() != 2 or \
+                (t.stride(1) != 1 and t.shape[1] > 1):
+            raise ValueError(f"{n} must be a float32 CUDA tensor [positions, rotary_dim / 2] with contiguous rows")
+        if t.get_device() != device:
+            raise ValueError(f"{n} is on {t.device} but the call is on cuda:{device}")
+        if t.requires_grad and torch.is_grad_enabled():
+            raise ValueError(f"{n} has no gradient here: pass it detached")
+    n, half = cos.shape
+    if sin.shape != cos.shape or (n > 1 and sin.stride(0) != cos.stride(0)):
+        raise ValueError(f"cos {tuple(cos.shape)} and sin {tuple(sin.shape)} must be alike, strides too")
+    if half < 8 or half % 8 or rotary_offset < 0 or rotary_offset % 8:
+        raise ValueError(f"rotary_dim {2 * half} must be a multiple of 16 and rotary_offset {rotary_offset} of 8")
+    return cos.data_ptr(), sin.data_ptr(), cos.stride(0) if n > 1 else half, n, 2 * half
+
+
+def attn_kv_append_rotary(q: Optional[torch.Tensor], k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor,
+                          v_cache: torch.Tensor, slot_mapping: torch.Tensor, positions: torch.Tensor, cos: torch.Tensor,
+                          sin: torch.Tensor, *, rotary_offset: int = 0, interleaved: bool = False,
+                          q_out: Optional[torch.Tensor] = None, stream=None) -> Optional[torch.Tensor]:
+    """:func:`attn_kv_append` with the rotation of :func:`attn_rotary` on the way: k's row i, rotated by
+    ``positions[i]`` (int32 [tokens], as :func:`attn_kv_plan` writes it), and v's go to slot ``slot_mapping[i]``, and q
+    [tokens, H, d_qk], unless None, is rotated into ``q_out`` (which may be q; made when not given). A token whose
+    position lies outside the tables writes nothing, one whose slot is outside the cache only its row of q_out.
+    Returns q_out (None without q)."""
+    append, ks = _append_fields(k, v, k_cache, v_cache, slot_mapping)
+    dev = k.get_device()
+    _check_int32("positions", positions, dev, ks[0])
+    cos_ptr, sin_ptr, row, n, dim = _check_rotation(cos, sin, dev, rotary_offset)
+    if rotary_offset + dim > ks[2]:
+        raise ValueError(f"columns {rotary_offset} .. {rotary_offset + dim - 1} are not all of a head of {ks[2]}")
+    heads, qt, qo, q_ptr, out_ptr = 0, (0, 0), (0, 0), 0, 0
+    if q is not None:
+        qs, qt = _bf16_layout("q", q, 3)
+        if qs[0] != ks[0] or qs[2] != ks[2] or q.get_device() != dev:
+            raise ValueError(f"q {tuple(qs)} does not match k {tuple(ks)} on cuda:{dev}")
+        q_out, qo = _rotated("q_out", q_out, q, stream)
+        heads, q_ptr, out_ptr = qs[1], q.data_ptr(), q_out.data_ptr()
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    p = _pack_append_rotary(*append, q_ptr, out_ptr, qt[0], qt[1], qo[0], qo[1], positions.data_ptr(), cos_ptr, sin_ptr, row,
+                            heads, dim, rotary_offset, 1 if interleaved else 0, n)
+    st = _lib.attn_kv_append_rotary(p, _stream_of(stream, k))
     if st:
-        _abi.check(st, "attn_kv_append")
+        _abi.check(st, "attn_kv_append_rotary")
+    return q_out
+
+
+def _rotated(name: str, out, like, stream):
+    """An output buffer for the rotated `like` (the given one, checked) and its strides."""
+    if out is None:
+        out = torch.empty(like.shape, dtype=_BF16, device=like.device)
+        if stream is not None:
+            _used_on(stream, out)
+    elif out.shape != like.shape or out.device != like.device:
+        raise ValueError(f"{name} must be {tuple(like.shape)} on {like.device}, got {tuple(out.shape)} on {out.device}")
+    return out, _bf16_layout(name, out, like.dim())[1]
+
+
+def attn_rotary(q: torch.Tensor, k: Optional[torch.Tensor], cos: torch.Tensor, sin: torch.Tensor,
+                positions: Optional[torch.Tensor] = None, *, rotary_offset: int = 0, interleaved: bool = False,
+                inverse: bool = False, q_out: Optional[torch.Tensor] = None, k_out: Optional[torch.Tensor] = None,
+                stream=None) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
+    """Rotary position encoding of q [B, N, H, d_qk] and, unless None, k [B, N, Hkv, d_qk] (or packed, [total, H, d_qk];
+    bf16): pairs of columns of ``rotary_offset .. rotary_offset + rotary_dim - 1`` of every head turn by their row's
+    position p, (x, y) -> (x c - y s, x s + y c) with c = cos[p, f] and s = sin[p, f] (float32 [positions,
+    rotary_dim / 2]); pair f is columns f and f + rotary_dim / 2, or with ``interleaved`` 2f and 2f + 1. ``positions``
+    is int32 [B, N] or [N] ([total]); without it a row's position is its index. ``inverse`` turns back: of the
+    gradients of the outputs it gives those of the inputs. q_out and k_out may be q and k. Rows whose position lies
+    outside the tables are not written. Returns (q_out, k_out)."""
+    dim = q.dim() if isinstance(q, torch.Tensor) and q.dim() == 3 else 4
+    qs, qt = _bf16_layout("q", q, dim)
+    dev = q.get_device()
+    batch, n = (qs[0], qs[1]) if dim == 4 else (1, qs[0])
+    cos_ptr, sin_ptr, row, n_pos, rot = _check_rotation(cos, sin, dev, rotary_offset)
+    if rotary_offset + rot > qs[-1]:
+        raise ValueError(f"columns {rotary_offset} .. {rotary_offset + rot - 1} are not all of a head of {qs[-1]}")
+    ks = kt = ko = None
+    if k is not None:
+        ks, kt = _bf16_layout("k", k, dim)
+        if ks[:-2] != qs[:-2] or ks[-1] != qs[-1] or k.get_device() != dev:
+            raise ValueError(f"k {tuple(ks)} does not match q {tuple(qs)} on cuda:{dev}")
+        k_out, ko = _rotated("k_out", k_out, k, stream)
+    elif k_out is not None:
+        raise ValueError("k_out without k")
+    q_out, qo = _rotated("q_out", q_out, q, stream)
+    pos_ptr, pos_batch = 0, 0
+    if positions is not None:
+        if dim == 4 and positions.dim() == 2:
+            if positions.shape != (batch, n):
+                raise ValueError(f"positions must be [{batch}, {n}] or [{n}], got {tuple(positions.shape)}")
+            _check_int32("positions", positions.reshape(-1) if positions.is_contiguous() else positions, dev, batch * n)
+            pos_batch = n
+        else:
+            _check_int32("positions", positions, dev, n)
+        pos_ptr = positions.data_ptr()
+    elif n > n_pos:
+        raise ValueError(f"{n} rows but the tables hold {n_pos} positions")
+    four = lambda s: (0, s[0], s[1]) if dim == 3 else s[:3]  # noqa: E731
+    none = (0, 0, 0)
+    p = _pack_rotary(q.data_ptr(), k.data_ptr() if k is not None else 0, q_out.data_ptr(),
+                     k_out.data_ptr() if k is not None else 0, *four(qt), *(four(kt) if k is not None else none), *four(qo),
+                     *(four(ko) if k is not None else none), pos_ptr, pos_batch, cos_ptr, sin_ptr, row, batch, n, qs[-2],
+                     ks[-2] if k is not None else 0, qs[-1], rot, rotary_offset, 1 if interleaved else 0, 1 if inverse else 0,
+                     n_pos)
+    st = _lib.attn_rotary(p, _stream_of(stream, q))
+    if st:
+        _abi.check(st, "attn_rotary")
+    return q_out, k_out
 
 
 def attn_fwd_paged(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, block_table: torch.Tensor,
@@ -791,3 +915,25 @@ def attention_varlen(q, k, v, cu_seqlens_q, cu_seqlens_k, max_seqlen_q: int, max
     gradients of rows behind the last offset are not written)."""
     return _AttentionVarlen.apply(q, k, v, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, max_seqlen_k, causal,
                                   softmax_scale, deterministic, softcap, alibi_slopes)
+
+
+class _Rotary(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, q, k, cos, sin, positions, rotary_offset, interleaved):
+        ctx.save_for_backward(cos, sin, positions)
+        ctx.how = dict(rotary_offset=rotary_offset, interleaved=interleaved)
+        out = attn_rotary(q, k, cos, sin, positions, **ctx.how)
+        return out if k is not None else out[0]
+
+    @staticmethod
+    def backward(ctx, dq, dk=None):
+        cos, sin, positions = ctx.saved_tensors
+        dq, dk = attn_rotary(dq.contiguous(), dk.contiguous() if dk is not None else None, cos, sin, positions, inverse=True,
+                             **ctx.how)
+        return dq, dk, None, None, None, None, None
+
+
+def rotary(q, k, cos, sin, positions: Optional[torch.Tensor] = None, rotary_offset: int = 0, interleaved: bool = False):
+    """Autograd wrapper over attn_rotary: (q, k) rotated, or q alone where k is None. Every row needs a position inside
+    the tables (rows without one are not written)."""
+    return _Rotary.apply(q, k, cos, sin, positions, rotary_offset, interleaved)

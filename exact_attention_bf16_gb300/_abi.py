@@ -11,7 +11,7 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libattn_gb300.so")
 HEADER_PATH = os.path.join(os.path.dirname(HERE), "include", "attn.h")
 
-ABI_VERSION = 7
+ABI_VERSION = 8
 BWD_NOALLOC_SCRATCH_BYTES = 8 << 20  # ATTN_BWD_NOALLOC_SCRATCH_BYTES
 
 STATUS = {
@@ -69,7 +69,7 @@ class AttnKvPlanParams(ctypes.Structure):
         ("free_pages", c_vp), ("free_count", c_vp), ("free_count_out", c_vp), ("cu_seqlens_q", c_vp),
         ("seqlens_k", c_vp), ("slot_mapping", c_vp), ("status", c_vp),
         ("num_seqs", c_i32), ("max_pages", c_i32), ("page_size", c_i32), ("free_capacity", c_i32),
-        ("max_tokens", c_i32),
+        ("max_tokens", c_i32), ("positions", c_vp),
     ]
 
 
@@ -95,6 +95,32 @@ class AttnPagedParams(ctypes.Structure):
         ("num_seqs", c_i32), ("heads", c_i32), ("heads_kv", c_i32), ("d_qk", c_i32), ("d_v", c_i32),
         ("page_size", c_i32), ("num_pages", c_i32), ("max_pages", c_i32), ("total_q", c_i32), ("max_seqlen_q", c_i32),
         ("softmax_scale", c_f32), ("causal", c_i32), ("score_mod", c_i32), ("softcap", c_f32), ("alibi_slopes", c_vp),
+    ]
+
+
+class AttnRotaryParams(ctypes.Structure):
+    _fields_ = [
+        ("q", c_vp), ("k", c_vp), ("q_out", c_vp), ("k_out", c_vp),
+        ("q_batch_stride", c_i64), ("q_row_stride", c_i64), ("q_head_stride", c_i64),
+        ("k_batch_stride", c_i64), ("k_row_stride", c_i64), ("k_head_stride", c_i64),
+        ("q_out_batch_stride", c_i64), ("q_out_row_stride", c_i64), ("q_out_head_stride", c_i64),
+        ("k_out_batch_stride", c_i64), ("k_out_row_stride", c_i64), ("k_out_head_stride", c_i64),
+        ("positions", c_vp), ("positions_batch_stride", c_i64),
+        ("cos_table", c_vp), ("sin_table", c_vp), ("table_row_stride", c_i64),
+        ("batch", c_i32), ("seqlen", c_i32), ("heads", c_i32), ("heads_kv", c_i32), ("d_qk", c_i32),
+        ("rotary_dim", c_i32), ("rotary_offset", c_i32), ("interleaved", c_i32), ("inverse", c_i32),
+        ("num_positions", c_i32),
+    ]
+
+
+class AttnKvAppendRotaryParams(ctypes.Structure):
+    _fields_ = [
+        ("append", AttnKvAppendParams),
+        ("q", c_vp), ("q_out", c_vp),
+        ("q_row_stride", c_i64), ("q_head_stride", c_i64), ("q_out_row_stride", c_i64), ("q_out_head_stride", c_i64),
+        ("positions", c_vp), ("cos_table", c_vp), ("sin_table", c_vp), ("table_row_stride", c_i64),
+        ("heads", c_i32), ("rotary_dim", c_i32), ("rotary_offset", c_i32), ("interleaved", c_i32),
+        ("num_positions", c_i32),
     ]
 
 
@@ -154,11 +180,15 @@ def load(path: str = LIB_PATH):
         "attn_bwd_noalloc": (ctypes.c_int, [c_vp, c_vp]),
         "attn_kv_plan": (ctypes.c_int, [c_vp, c_vp]),
         "attn_kv_append": (ctypes.c_int, [c_vp, c_vp]),
+        "attn_rotary": (ctypes.c_int, [c_vp, c_vp]),
+        "attn_kv_append_rotary": (ctypes.c_int, [c_vp, c_vp]),
         "attn_fwd_paged_workspace_size": (ctypes.c_size_t, [c_vp]),
         "attn_fwd_paged": (ctypes.c_int, [c_vp, c_vp, ctypes.c_size_t, c_vp]),
         "attn_kv_plan_params_size": (ctypes.c_size_t, []),
         "attn_kv_append_params_size": (ctypes.c_size_t, []),
         "attn_paged_params_size": (ctypes.c_size_t, []),
+        "attn_rotary_params_size": (ctypes.c_size_t, []),
+        "attn_kv_append_rotary_params_size": (ctypes.c_size_t, []),
         "attn_exp2_eval": (ctypes.c_int, [c_vp, c_vp, c_vp, c_i64, c_vp]),
         "attn_diag_wait_timeout": (ctypes.c_int, [c_vp, ctypes.c_uint32, c_vp]),
         "attn_get_device_status": (ctypes.c_int, [c_vp, P(ctypes.c_uint32)]),
@@ -178,7 +208,9 @@ def load(path: str = LIB_PATH):
             lib.attn_bwd_params_size() != ctypes.sizeof(AttnBwdParams) or \
             lib.attn_kv_plan_params_size() != ctypes.sizeof(AttnKvPlanParams) or \
             lib.attn_kv_append_params_size() != ctypes.sizeof(AttnKvAppendParams) or \
-            lib.attn_paged_params_size() != ctypes.sizeof(AttnPagedParams):
+            lib.attn_paged_params_size() != ctypes.sizeof(AttnPagedParams) or \
+            lib.attn_rotary_params_size() != ctypes.sizeof(AttnRotaryParams) or \
+            lib.attn_kv_append_rotary_params_size() != ctypes.sizeof(AttnKvAppendRotaryParams):
         raise ImportError("libattn_gb300.so parameter-struct layout differs from the binding")
     _lib = lib
     return lib

@@ -2,7 +2,7 @@
 // argument validation, TMA tensor-map encoding, workspace accounting and
 // kernel launches. All compute runs in the CUDA kernels (fwd_kernel.cuh and
 // bwd_kernels.cuh with the translation units that instantiate them, the pair
-// kernels, attn_paged.cu, attn_paged_decode.cu, kv_cache.cu, schedule.cu); this file holds host logic only.
+// kernels, attn_paged.cu, attn_paged_decode.cu, kv_cache.cu, rotary.cu, schedule.cu); this file holds host logic only.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <cuda_runtime.h>
@@ -889,7 +889,8 @@ bool plan_arrays_overlap(const attn_kv_plan_params* p) {
   const Range r[] = {of(p->seqlens_old, 4 * n, false), of(p->seqlens_new, 4 * n, false), of(p->free_count, 4, false),
                      of(p->free_pages, 4ll * p->free_capacity, true), of(p->free_count_out, 4, true),
                      of(p->cu_seqlens_q, 4 * (n + 1), true), of(p->seqlens_k, 4 * n, true),
-                     of(p->slot_mapping, 8ll * p->max_tokens, true), of(p->status, 4, true)};
+                     of(p->slot_mapping, 8ll * p->max_tokens, true), of(p->status, 4, true),
+                     of(p->positions, p->positions ? 4ll * p->max_tokens : 0, true)};
   for (const Range& x : r) {
     for (const Range* y = &x + 1; y != std::end(r); ++y) {
       if (!(x.written || y->written) || x.bytes == 0 || y->bytes == 0) continue;
@@ -921,11 +922,13 @@ attn_status_t run_kv_plan(const attn_kv_plan_params* p, cudaStream_t stream) {
   if (p->free_capacity > 0 && !aligned4(p->free_pages)) return ATTN_ERR_INVALID_ARG;
   if (p->max_tokens > 0 && (!p->slot_mapping || (reinterpret_cast<uintptr_t>(p->slot_mapping) & 7u)))
     return ATTN_ERR_INVALID_ARG;
+  if (reinterpret_cast<uintptr_t>(p->positions) & 3u) return ATTN_ERR_INVALID_ARG;
   if (p->num_seqs > kMaxPlanSeqs) return ATTN_ERR_UNSUPPORTED;
   if (plan_arrays_overlap(p)) return ATTN_ERR_INVALID_ARG;
   ATTN_TRY(check_lists_device(p->seqlens_old, {p->seqlens_new, p->block_table, p->free_capacity ? p->free_pages : nullptr,
                                                p->free_count, p->free_count_out, p->cu_seqlens_q, p->seqlens_k,
-                                               p->max_tokens ? p->slot_mapping : nullptr, p->status}));
+                                               p->max_tokens ? p->slot_mapping : nullptr, p->status,
+                                               p->max_tokens ? p->positions : nullptr}));
   DeviceScope scope;
   ATTN_TRY(bind_device(&scope, p->seqlens_old));
   a.seqlens_old = p->seqlens_old;
@@ -944,17 +947,16 @@ attn_status_t run_kv_plan(const attn_kv_plan_params* p, cudaStream_t stream) {
   a.page_size = p->page_size;
   a.free_capacity = p->free_capacity;
   a.max_tokens = p->max_tokens;
+  a.positions = p->max_tokens ? p->positions : nullptr;
   const cudaError_t e = launch_kv_plan(a, stream);
   return e == cudaSuccess ? ATTN_OK : cuda_fail(e, "kv plan launch");
 }
 
-attn_status_t run_kv_append(const attn_kv_append_params* p, cudaStream_t stream) {
-  if (!p) return ATTN_ERR_INVALID_ARG;
+// The checks of an append that need no GPU.
+attn_status_t check_append(const attn_kv_append_params* p) {
   if (!supported_dims(p->d_qk, p->d_v))
     return p->d_qk <= 0 || p->d_v <= 0 ? ATTN_ERR_INVALID_ARG : ATTN_ERR_UNSUPPORTED;
-  KvAppendArgs a{};
-  a.page_shift = page_shift(p->page_size);
-  if (a.page_shift < 0 || p->num_pages < 1 || p->heads_kv < 1 || p->tokens < 0) return ATTN_ERR_INVALID_ARG;
+  if (page_shift(p->page_size) < 0 || p->num_pages < 1 || p->heads_kv < 1 || p->tokens < 0) return ATTN_ERR_INVALID_ARG;
   const bool none = p->tokens == 0;
   ATTN_TRY(check_tensor(p->k, 0, p->k_row_stride, p->k_head_stride, true, none));
   ATTN_TRY(check_tensor(p->v, 0, p->v_row_stride, p->v_head_stride, true, none));
@@ -966,11 +968,19 @@ attn_status_t run_kv_append(const attn_kv_append_params* p, cudaStream_t stream)
   if (overlaps(p->k_cache_page_stride, p->k_cache_row_stride, p->k_cache_head_stride) ||
       overlaps(p->v_cache_page_stride, p->v_cache_row_stride, p->v_cache_head_stride))
     return ATTN_ERR_INVALID_ARG;
-  if (none) return ATTN_OK;
-  if (!p->slot_mapping || (reinterpret_cast<uintptr_t>(p->slot_mapping) & 7u)) return ATTN_ERR_INVALID_ARG;
+  if (!none && (!p->slot_mapping || (reinterpret_cast<uintptr_t>(p->slot_mapping) & 7u))) return ATTN_ERR_INVALID_ARG;
+  return ATTN_OK;
+}
+
+attn_status_t run_kv_append(const attn_kv_append_params* p, cudaStream_t stream) {
+  if (!p) return ATTN_ERR_INVALID_ARG;
+  ATTN_TRY(check_append(p));
+  if (p->tokens == 0) return ATTN_OK;
   ATTN_TRY(check_lists_device(p->k, {p->v, p->k_cache, p->v_cache, p->slot_mapping}));
   DeviceScope scope;
   ATTN_TRY(bind_device(&scope, p->k));
+  KvAppendArgs a{};
+  a.page_shift = page_shift(p->page_size);
   a.k = static_cast<const __nv_bfloat16*>(p->k);
   a.v = static_cast<const __nv_bfloat16*>(p->v);
   a.k_cache = static_cast<__nv_bfloat16*>(p->k_cache);
@@ -985,6 +995,128 @@ attn_status_t run_kv_append(const attn_kv_append_params* p, cudaStream_t stream)
   a.page_size = p->page_size;
   a.num_pages = p->num_pages;
   const cudaError_t e = launch_kv_append(p->d_qk, p->d_v, a, stream);
+  return e == cudaSuccess ? ATTN_OK : cuda_fail(e, "kv append launch");
+}
+
+// ---- rotation ---------------------------------------------------------------
+attn_status_t check_rotation(int32_t d_qk, int32_t rotary_dim, int32_t rotary_offset, const float* cos_table,
+                             const float* sin_table, int64_t table_row_stride, int32_t num_positions) {
+  if (d_qk != 64 && d_qk != 128 && d_qk != 192) return d_qk <= 0 ? ATTN_ERR_INVALID_ARG : ATTN_ERR_UNSUPPORTED;
+  if (rotary_dim < 16 || rotary_dim % 16 || rotary_offset < 0 || rotary_offset % 8 || rotary_dim > d_qk ||
+      rotary_offset > d_qk - rotary_dim)
+    return ATTN_ERR_INVALID_ARG;
+  if (num_positions < 0 || table_row_stride < rotary_dim / 2 || table_row_stride % 4 || table_row_stride >= (int64_t(1) << 38))
+    return ATTN_ERR_INVALID_ARG;
+  if (num_positions > 0 && (!cos_table || !sin_table || !aligned16(cos_table) || !aligned16(sin_table)))
+    return ATTN_ERR_INVALID_ARG;
+  return ATTN_OK;
+}
+
+// An output of a rotation: its rows must not lie on one another, and it may be its input only as a whole.
+attn_status_t check_turned(const void* x, int64_t xb, int64_t xn, int64_t xh, const void* y, int64_t yb, int64_t yn, int64_t yh,
+                           int64_t batch, int64_t rows, int64_t heads, bool empty) {
+  ATTN_TRY(check_tensor(x, xb, xn, xh, batch == 1, empty));
+  ATTN_TRY(check_tensor(y, yb, yn, yh, batch == 1, empty));
+  if ((yh == 0 && heads > 1) || (yn == 0 && rows > 1) || (yb == 0 && batch > 1)) return ATTN_ERR_INVALID_ARG;
+  if (x == y && ((heads > 1 && xh != yh) || (rows > 1 && xn != yn) || (batch > 1 && xb != yb))) return ATTN_ERR_INVALID_ARG;
+  return ATTN_OK;
+}
+
+attn_status_t run_rotary(const attn_rotary_params* p, cudaStream_t stream) {
+  if (!p) return ATTN_ERR_INVALID_ARG;
+  ATTN_TRY(check_rotation(p->d_qk, p->rotary_dim, p->rotary_offset, p->cos_table, p->sin_table, p->table_row_stride,
+                          p->num_positions));
+  if (p->batch < 1 || p->seqlen < 0 || p->heads < 1) return ATTN_ERR_INVALID_ARG;
+  const bool none = p->seqlen == 0, with_k = p->k != nullptr || p->k_out != nullptr;
+  ATTN_TRY(check_turned(p->q, p->q_batch_stride, p->q_row_stride, p->q_head_stride, p->q_out, p->q_out_batch_stride,
+                        p->q_out_row_stride, p->q_out_head_stride, p->batch, p->seqlen, p->heads, none));
+  if (with_k) {
+    if (p->heads_kv < 1) return ATTN_ERR_INVALID_ARG;
+    ATTN_TRY(check_turned(p->k, p->k_batch_stride, p->k_row_stride, p->k_head_stride, p->k_out, p->k_out_batch_stride,
+                          p->k_out_row_stride, p->k_out_head_stride, p->batch, p->seqlen, p->heads_kv, none));
+  }
+  if (p->positions ? (reinterpret_cast<uintptr_t>(p->positions) & 3u) != 0 || p->positions_batch_stride < 0
+                   : p->seqlen > p->num_positions)
+    return ATTN_ERR_INVALID_ARG;
+  if (none) return ATTN_OK;
+  const int64_t tokens = static_cast<int64_t>(p->batch) * p->seqlen;
+  const int64_t heads = static_cast<int64_t>(p->heads) + (with_k ? p->heads_kv : 0);
+  if (tokens > 0x7fffffff || heads > (1 << 24)) return ATTN_ERR_UNSUPPORTED;
+  if (p->num_positions == 0) return ATTN_OK;  // every row is left as it was
+  ATTN_TRY(check_lists_device(p->q, {p->q_out, p->k, p->k_out, p->positions, p->cos_table, p->sin_table}));
+  DeviceScope scope;
+  ATTN_TRY(bind_device(&scope, p->q));
+  RotaryArgs a{};
+  a.q = static_cast<const __nv_bfloat16*>(p->q);
+  a.q_out = static_cast<__nv_bfloat16*>(p->q_out);
+  a.q_b = p->q_batch_stride, a.q_row = p->q_row_stride, a.q_head = p->q_head_stride;
+  a.qo_b = p->q_out_batch_stride, a.qo_row = p->q_out_row_stride, a.qo_head = p->q_out_head_stride;
+  a.heads = p->heads;
+  if (with_k) {
+    a.k = static_cast<const __nv_bfloat16*>(p->k);
+    a.k_out = static_cast<__nv_bfloat16*>(p->k_out);
+    a.k_b = p->k_batch_stride, a.k_row = p->k_row_stride, a.k_head = p->k_head_stride;
+    a.ko_b = p->k_out_batch_stride, a.ko_row = p->k_out_row_stride, a.ko_head = p->k_out_head_stride;
+    a.heads_kv = p->heads_kv;
+  }
+  a.positions = p->positions;
+  a.pos_b = p->positions_batch_stride;
+  a.cos = p->cos_table, a.sin = p->sin_table, a.table_row = p->table_row_stride;
+  a.tokens = static_cast<uint32_t>(tokens);
+  a.seqlen = p->seqlen;
+  a.rot = p->rotary_dim, a.first = p->rotary_offset, a.num_positions = p->num_positions;
+  a.inverse = p->inverse ? 1 : 0;
+  a.interleaved = p->interleaved ? 1 : 0;
+  const cudaError_t e = launch_rotary(p->d_qk, a, stream);
+  return e == cudaSuccess ? ATTN_OK : cuda_fail(e, "rotary launch");
+}
+
+attn_status_t run_kv_append_rotary(const attn_kv_append_rotary_params* p, cudaStream_t stream) {
+  if (!p) return ATTN_ERR_INVALID_ARG;
+  const attn_kv_append_params& w = p->append;
+  ATTN_TRY(check_append(&w));
+  ATTN_TRY(check_rotation(w.d_qk, p->rotary_dim, p->rotary_offset, p->cos_table, p->sin_table, p->table_row_stride,
+                          p->num_positions));
+  const bool none = w.tokens == 0, with_q = p->q != nullptr || p->q_out != nullptr;
+  if (with_q) {
+    if (p->heads < 1) return ATTN_ERR_INVALID_ARG;
+    ATTN_TRY(check_turned(p->q, 0, p->q_row_stride, p->q_head_stride, p->q_out, 0, p->q_out_row_stride, p->q_out_head_stride, 1,
+                          w.tokens, p->heads, none));
+  }
+  if (none) return ATTN_OK;
+  if (!aligned4(p->positions)) return ATTN_ERR_INVALID_ARG;
+  if (static_cast<int64_t>(w.heads_kv) + (with_q ? p->heads : 0) > (1 << 24)) return ATTN_ERR_UNSUPPORTED;
+  if (p->num_positions == 0) return ATTN_OK;  // no token has a position
+  ATTN_TRY(check_lists_device(w.k, {w.v, w.k_cache, w.v_cache, w.slot_mapping, p->q, p->q_out, p->positions, p->cos_table,
+                                    p->sin_table}));
+  DeviceScope scope;
+  ATTN_TRY(bind_device(&scope, w.k));
+  RotaryArgs a{};
+  if (with_q) {
+    a.q = static_cast<const __nv_bfloat16*>(p->q);
+    a.q_out = static_cast<__nv_bfloat16*>(p->q_out);
+    a.q_row = p->q_row_stride, a.q_head = p->q_head_stride;
+    a.qo_row = p->q_out_row_stride, a.qo_head = p->q_out_head_stride;
+    a.heads = p->heads;
+  }
+  a.k = static_cast<const __nv_bfloat16*>(w.k);
+  a.v = static_cast<const __nv_bfloat16*>(w.v);
+  a.k_out = static_cast<__nv_bfloat16*>(w.k_cache);
+  a.v_out = static_cast<__nv_bfloat16*>(w.v_cache);
+  a.k_row = w.k_row_stride, a.k_head = w.k_head_stride;
+  a.v_row = w.v_row_stride, a.v_head = w.v_head_stride;
+  a.ko_b = w.k_cache_page_stride, a.ko_row = w.k_cache_row_stride, a.ko_head = w.k_cache_head_stride;
+  a.vo_page = w.v_cache_page_stride, a.vo_row = w.v_cache_row_stride, a.vo_head = w.v_cache_head_stride;
+  a.slots = w.slot_mapping;
+  a.positions = p->positions;
+  a.cos = p->cos_table, a.sin = p->sin_table, a.table_row = p->table_row_stride;
+  a.tokens = a.seqlen = w.tokens;
+  a.heads_kv = w.heads_kv;
+  a.d_v = w.d_v;
+  a.rot = p->rotary_dim, a.first = p->rotary_offset, a.num_positions = p->num_positions;
+  a.interleaved = p->interleaved ? 1 : 0;
+  a.page_size = w.page_size, a.page_shift = page_shift(w.page_size), a.num_pages = w.num_pages;
+  const cudaError_t e = launch_rotary(w.d_qk, a, stream);
   return e == cudaSuccess ? ATTN_OK : cuda_fail(e, "kv append launch");
 }
 
@@ -1212,6 +1344,14 @@ attn_status_t attn_kv_append(const attn_kv_append_params* p, attn_stream_t strea
   return run_kv_append(p, static_cast<cudaStream_t>(stream));
 }
 
+attn_status_t attn_rotary(const attn_rotary_params* p, attn_stream_t stream) {
+  return run_rotary(p, static_cast<cudaStream_t>(stream));
+}
+
+attn_status_t attn_kv_append_rotary(const attn_kv_append_rotary_params* p, attn_stream_t stream) {
+  return run_kv_append_rotary(p, static_cast<cudaStream_t>(stream));
+}
+
 size_t attn_fwd_paged_workspace_size(const attn_paged_params* p) {
   if (check_paged(p) != ATTN_OK || p->total_q == 0 || p->max_seqlen_q == 0) return 0;
   return paged_plan(p).bytes;
@@ -1280,5 +1420,7 @@ size_t attn_bwd_params_size(void) { return sizeof(attn_bwd_params); }
 size_t attn_kv_plan_params_size(void) { return sizeof(attn_kv_plan_params); }
 size_t attn_kv_append_params_size(void) { return sizeof(attn_kv_append_params); }
 size_t attn_paged_params_size(void) { return sizeof(attn_paged_params); }
+size_t attn_rotary_params_size(void) { return sizeof(attn_rotary_params); }
+size_t attn_kv_append_rotary_params_size(void) { return sizeof(attn_kv_append_rotary_params); }
 
 }  // extern "C"

@@ -390,6 +390,7 @@ struct KvPlanArgs {
   int64_t* slot_mapping;
   int* status;
   int num_seqs, max_pages, page_size, page_shift, free_capacity, max_tokens;
+  int* positions;  // or nullptr
 };
 cudaError_t launch_kv_plan(const KvPlanArgs& a, cudaStream_t stream);
 
@@ -404,6 +405,29 @@ struct KvAppendArgs {
   int tokens, heads_kv, page_size, page_shift, num_pages;
 };
 cudaError_t launch_kv_append(int d_qk, int d_v, const KvAppendArgs& a, cudaStream_t stream);
+
+// Rotation (rotary.cu); fields as in include/attn.h. Rows t = b * seqlen + n of q and k; heads = 0 without q, heads_kv = 0
+// without k. slots != nullptr: k goes to slot slots[t] of the cache k_out (ko_b: its page stride), and v, when given, to
+// that of v_out.
+struct RotaryArgs {
+  const __nv_bfloat16* q;
+  const __nv_bfloat16* k;
+  const __nv_bfloat16* v;
+  __nv_bfloat16* q_out;
+  __nv_bfloat16* k_out;
+  __nv_bfloat16* v_out;
+  int64_t q_b, q_row, q_head, k_b, k_row, k_head, v_row, v_head;  // element strides
+  int64_t qo_b, qo_row, qo_head, ko_b, ko_row, ko_head, vo_page, vo_row, vo_head;
+  const int64_t* slots;
+  const int* positions;  // nullptr: n
+  int64_t pos_b;
+  const float* cos;
+  const float* sin;
+  int64_t table_row;
+  uint32_t tokens, seqlen, heads, heads_kv, d_v, rot, first, num_positions;
+  int inverse, interleaved, page_size, page_shift, num_pages;
+};
+cudaError_t launch_rotary(int d_qk, const RotaryArgs& a, cudaStream_t stream);
 
 // A unit of attn_fwd_paged whose keys were cut into n segments (n < 1: none): its
 // first token's row of q, its tokens, K/V head, the partial slot of segment 0

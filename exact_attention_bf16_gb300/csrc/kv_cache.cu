@@ -189,10 +189,14 @@ __global__ void kv_plan_kernel(const KvPlanArgs a) {
           left = a.page_size - 1 - (pos & (a.page_size - 1));
         }
         a.slot_mapping[t] = slot;
+        if (a.positions != nullptr) a.positions[t] = t < tokens ? pos : -1;
       }
     }
   } else {
-    for (uint32_t t = me; t < static_cast<uint32_t>(a.max_tokens); t += all) a.slot_mapping[t] = -1;
+    for (uint32_t t = me; t < static_cast<uint32_t>(a.max_tokens); t += all) {
+      a.slot_mapping[t] = -1;
+      if (a.positions != nullptr) a.positions[t] = -1;
+    }
   }
   // every read of the lengths and the stack's height is done (where they are updated in place, the grid is one cluster)
   cg::this_cluster().sync();

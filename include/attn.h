@@ -65,7 +65,7 @@
 extern "C" {
 #endif
 
-#define ATTN_ABI_VERSION 7
+#define ATTN_ABI_VERSION 8
 
 typedef enum {
   ATTN_OK = 0,
@@ -431,6 +431,10 @@ typedef struct attn_kv_plan_params {
   int32_t page_size;
   int32_t free_capacity;
   int32_t max_tokens;
+  /* Optional (may be NULL): int32 [max_tokens], written like slot_mapping with the
+   * position of each new token in its request (old length and up), then -1; for
+   * attn_kv_append_rotary. */
+  int32_t* positions;
 } attn_kv_plan_params;
 attn_status_t attn_kv_plan(const attn_kv_plan_params* p, attn_stream_t stream);
 
@@ -459,6 +463,74 @@ typedef struct attn_kv_append_params {
   int32_t num_pages;
 } attn_kv_append_params;
 attn_status_t attn_kv_append(const attn_kv_append_params* p, attn_stream_t stream);
+
+/* Rotary position encoding. Columns rotary_offset .. rotary_offset + rotary_dim - 1 of
+ * every head's row are turned pair by pair; the others are copied. Pair f (f <
+ * rotary_dim / 2) is the columns f and f + rotary_dim / 2 of the range, or, with
+ * interleaved != 0, 2f and 2f + 1. With position p of the row,
+ *   (x, y) -> (x c - y s, x s + y c),  c = cos_table[p][f], s = sin_table[p][f],
+ * in fp32, rounded once. The tables are fp32 [num_positions, rotary_dim / 2] on q's GPU,
+ * rows table_row_stride elements apart (a multiple of 4), 16-byte aligned. rotary_dim is
+ * a multiple of 16, rotary_offset of 8, d_qk 64, 128 or 192.
+ *
+ * attn_rotary rotates q [batch, seqlen, heads, d_qk] and, when given, k [batch, seqlen,
+ * heads_kv, d_qk] (bf16; packed tensors are batch 1) into q_out and k_out, which may be
+ * q and k themselves (same base and strides) but must not overlap them otherwise.
+ * inverse != 0 turns by the negative angle: applied to dQ and dK of the rotated tensors,
+ * it gives the gradients of the ones before. positions (int32, row b at
+ * b * positions_batch_stride) may be NULL: a row's position is then its index in seqlen,
+ * at most num_positions. Rows whose position lies outside [0, num_positions) are left as
+ * they were in the outputs. No workspace. */
+typedef struct attn_rotary_params {
+  const void* q;
+  const void* k; /* may be NULL */
+  void* q_out;
+  void* k_out;
+  int64_t q_batch_stride, q_row_stride, q_head_stride;
+  int64_t k_batch_stride, k_row_stride, k_head_stride;
+  int64_t q_out_batch_stride, q_out_row_stride, q_out_head_stride;
+  int64_t k_out_batch_stride, k_out_row_stride, k_out_head_stride;
+  const int32_t* positions;
+  int64_t positions_batch_stride;
+  const float* cos_table;
+  const float* sin_table;
+  int64_t table_row_stride;
+  int32_t batch;
+  int32_t seqlen;
+  int32_t heads;
+  int32_t heads_kv;
+  int32_t d_qk;
+  int32_t rotary_dim;
+  int32_t rotary_offset;
+  int32_t interleaved;
+  int32_t inverse;
+  int32_t num_positions;
+} attn_rotary_params;
+attn_status_t attn_rotary(const attn_rotary_params* p, attn_stream_t stream);
+
+/* attn_kv_append with the rotation on the way: K rows are rotated by positions[i] as they
+ * go to their slots, V rows copied, and, when q is given (q [tokens, heads, d_qk]), q is
+ * rotated into q_out (which may be q). `append` and its rules are attn_kv_append's; the
+ * rotation's are attn_rotary's, positions is required (int32 [tokens], as attn_kv_plan
+ * writes it). A token whose position lies outside [0, num_positions) writes nothing, one
+ * whose slot does writes its q_out alone. */
+typedef struct attn_kv_append_rotary_params {
+  attn_kv_append_params append;
+  const void* q; /* may be NULL */
+  void* q_out;
+  int64_t q_row_stride, q_head_stride;
+  int64_t q_out_row_stride, q_out_head_stride;
+  const int32_t* positions;
+  const float* cos_table;
+  const float* sin_table;
+  int64_t table_row_stride;
+  int32_t heads;
+  int32_t rotary_dim;
+  int32_t rotary_offset;
+  int32_t interleaved;
+  int32_t num_positions;
+} attn_kv_append_rotary_params;
+attn_status_t attn_kv_append_rotary(const attn_kv_append_rotary_params* p, attn_stream_t stream);
 
 /* Attention of packed new tokens over the paged cache. Request s's queries are
  * rows cu_seqlens_q[s] .. cu_seqlens_q[s+1]-1 of q [total_q, heads, d_qk] (none,
@@ -557,6 +629,8 @@ size_t attn_bwd_params_size(void);
 size_t attn_kv_plan_params_size(void);
 size_t attn_kv_append_params_size(void);
 size_t attn_paged_params_size(void);
+size_t attn_rotary_params_size(void);
+size_t attn_kv_append_rotary_params_size(void);
 
 #ifdef __cplusplus
 }

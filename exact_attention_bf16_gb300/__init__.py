@@ -64,13 +64,17 @@ def _bf16_layout(name: str, t, ndim: int):
     return shape, stride
 
 
-def _mod_fields(q, softcap, alibi_slopes):
-    """score_mod, softcap and alibi_slopes of a call (attn_fwd)."""
-    if softcap is None and alibi_slopes is None:
-        return 0, 0.0, 0
+_NO_REL = (0, 0, 0, 0, 0)
+
+
+def _mod_fields(q, softcap, alibi_slopes, rel_bias=None, rel_max_distance=128, rel_bidirectional=True):
+    """(score_mod, softcap, alibi_slopes) and the bias's fields (rel_bias .. rel_bidirectional) of a call (attn_fwd)."""
+    if softcap is None and alibi_slopes is None and rel_bias is None:
+        return (0, 0.0, 0), _NO_REL
     p = AttnFwdParams()
-    _set_score_mod(p, q, softcap, alibi_slopes)
-    return p.score_mod, p.softcap, p.alibi_slopes or 0
+    _set_score_mod(p, q, softcap, alibi_slopes, rel_bias, rel_max_distance, rel_bidirectional)
+    return ((p.score_mod, p.softcap, p.alibi_slopes or 0),
+            (p.rel_bias or 0, p.rel_bias_dtype, p.rel_buckets, p.rel_max_distance, p.rel_bidirectional))
 
 
 def _check_int32(name: str, t, device: int, n: int):
@@ -147,12 +151,25 @@ def _fill_fwd(p: AttnFwdParams, q, k, v, o, lse, strides, scale, causal):
     p.causal = 1 if causal else 0
 
 
-def _set_score_mod(p: AttnFwdParams, q: torch.Tensor, softcap, alibi_slopes):
+def _set_score_mod(p: AttnFwdParams, q: torch.Tensor, softcap, alibi_slopes, rel_bias=None, rel_max_distance=128,
+                   rel_bidirectional=True):
     """Score modification: logits soft-capped at ``softcap`` (a' = c tanh(a / c)), or ALiBi with one
-    slope per head (``alibi_slopes`` float32 [H] on q's GPU, each >= 0)."""
-    if softcap is not None and alibi_slopes is not None:
-        raise ValueError("choose one score modification: softcap or alibi_slopes")
-    if softcap is not None:
+    slope per head (``alibi_slopes`` float32 [H] on q's GPU, each >= 0), or a learned bias by buckets of relative
+    position (``rel_bias`` [buckets, H], bf16 or float32, on q's GPU)."""
+    if (softcap is not None) + (alibi_slopes is not None) + (rel_bias is not None) > 1:
+        raise ValueError("choose one score modification: softcap, alibi_slopes or rel_bias")
+    if rel_bias is not None:
+        t = rel_bias
+        if not isinstance(t, torch.Tensor) or t.dtype not in (_BF16, _F32) or not t.is_cuda or not t.is_contiguous() or \
+                t.dim() != 2 or t.shape[1] != q.shape[-2]:
+            raise ValueError(f"rel_bias must be a contiguous bfloat16 or float32 CUDA tensor [buckets, {q.shape[-2]}]")
+        if t.device != q.device:
+            raise ValueError(f"rel_bias is on {t.device} but q is on {q.device}")
+        p.score_mod, p.rel_bias = _abi.SCORE_RELBIAS, _ptr(t)
+        p.rel_bias_dtype = _abi.TABLE_F32 if t.dtype is _F32 else _abi.TABLE_BF16
+        p.rel_buckets, p.rel_max_distance = t.shape[0], int(rel_max_distance)
+        p.rel_bidirectional = 1 if rel_bidirectional else 0
+    elif softcap is not None:
         p.score_mod, p.softcap = _abi.SCORE_SOFTCAP, float(softcap)
     elif alibi_slopes is not None:
         t = alibi_slopes
@@ -260,12 +277,16 @@ def attn_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, *, causal: bool 
              lse: Optional[torch.Tensor] = None, rescale_stats: Optional[torch.Tensor] = None,
              exp2_emu_period: int = 0, softcap: Optional[float] = None,
              alibi_slopes: Optional[torch.Tensor] = None, q_descale: float = 1.0, k_descale: float = 1.0,
-             v_descale: float = 1.0, cta_pair: bool = False, stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
+             v_descale: float = 1.0, cta_pair: bool = False, rel_bias: Optional[torch.Tensor] = None, rel_max_distance: int = 128,
+             rel_bidirectional: bool = True, stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
     """Dense forward. q [B, Nq, H, d_qk], k [B, Nk, Hkv, d_qk], v [B, Nk, Hkv, d_v] (bf16, CUDA); Hkv
     divides H, and query head h reads K/V head h // (H // Hkv).
     Returns (O [B, Nq, H, d_v] bf16, LSE [B, H, Nq] fp32, natural log). ``exp2_emu_period`` (0, 4, 8)
-    sends one column in that many of every row's exp2 to the FMA-pipe polynomial. ``softcap`` or
-    ``alibi_slopes`` select a score modification (include/attn.h, attn_fwd_params.score_mod).
+    sends one column in that many of every row's exp2 to the FMA-pipe polynomial. ``softcap``,
+    ``alibi_slopes`` or ``rel_bias`` select a score modification (include/attn.h, attn_fwd_params.score_mod):
+    ``rel_bias`` [buckets, H] (bf16 or float32, up to 128 buckets) adds a learned bias by the bucket of the key's position
+    relative to the query's, both sides apart with ``rel_bidirectional`` (else all keys behind the query share bucket 0),
+    whole distances first and then logarithmic up to ``rel_max_distance`` (attn_fwd_params.rel_bias).
     q, k, v may instead all be torch.float8_e4m3fn (d = 128), standing for their values times
     ``q_descale``, ``k_descale``, ``v_descale``. ``cta_pair`` runs the two-SM forward (d = 128)."""
     f8 = _check_inputs(q, k, v, 4)
@@ -290,7 +311,7 @@ def attn_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, *, causal: bool 
     p.batch, p.seqlen_q, p.seqlen_k = B, Nq, Nk
     p.rescale_stats = _ptr(rescale_stats)
     p.exp2_emu_period = int(exp2_emu_period)
-    _set_score_mod(p, q, softcap, alibi_slopes)
+    _set_score_mod(p, q, softcap, alibi_slopes, rel_bias, rel_max_distance, rel_bidirectional)
     _set_input_dtype(p, f8, q_descale, k_descale, v_descale)
     p.cta_pair = 1 if cta_pair else 0
     ws, nbytes = _workspace(_lib.attn_fwd_workspace_size(ctypes.byref(p)), q.device, stream)
@@ -376,7 +397,8 @@ def attn_fwd_varlen(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqlen
                     lse: Optional[torch.Tensor] = None, rescale_stats: Optional[torch.Tensor] = None,
                     exp2_emu_period: int = 0, softcap: Optional[float] = None,
                     alibi_slopes: Optional[torch.Tensor] = None, q_descale: float = 1.0, k_descale: float = 1.0,
-                    v_descale: float = 1.0, cta_pair: bool = False,
+                    v_descale: float = 1.0, cta_pair: bool = False, rel_bias: Optional[torch.Tensor] = None, rel_max_distance: int = 128,
+                    rel_bidirectional: bool = True,
                     stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
     """Packed variable-length forward. q [total_q, H, d_qk], k/v [total_k, Hkv, d] with Hkv a divisor of H
     (query head h reads K/V head h // (H // Hkv)); cu_seqlens int32 on the device. Sequences do not reach one another,
@@ -406,15 +428,15 @@ def attn_fwd_varlen(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqlen
         raise ValueError(f"lse must be a contiguous float32 [H, total_q] tensor on {q.device}")
     if stream is not None:
         _used_on(stream, out, lse)
-    mod, cap, slopes = _mod_fields(q, softcap, alibi_slopes)
+    mod, rel = _mod_fields(q, softcap, alibi_slopes, rel_bias, rel_max_distance, rel_bidirectional)
     p = _pack_fwd(
         q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), lse.data_ptr(),
         0, sq[0], sq[1], 0, sk[0], sk[1], 0, sv[0], sv[1], 0, so[0], so[1],
         1, H, 0, 0, dqk, dv, cu_seqlens_q.data_ptr(), cu_seqlens_k.data_ptr(), cu_seqlens_q.shape[0] - 1,
         int(max_seqlen_q), int(max_seqlen_k), tq, tk, scale, 1 if causal else 0, int(exp2_emu_period),
-        rescale_stats.data_ptr() if rescale_stats is not None else 0, mod, cap, slopes,
+        rescale_stats.data_ptr() if rescale_stats is not None else 0, *mod,
         _abi.INPUT_E4M3 if f8 else _abi.INPUT_BF16, float(q_descale), float(k_descale), float(v_descale),
-        1 if cta_pair else 0, ks[1])
+        1 if cta_pair else 0, ks[1], *rel)
     nbytes = _lib.attn_fwd_varlen_workspace_size(p)
     ws, ws_ptr = _workspace_ptr(nbytes, q, stream)
     status = _lib.attn_fwd_varlen(p, ws_ptr, nbytes, _stream_of(stream, q))
@@ -432,6 +454,21 @@ def _fill_bwd(p: AttnBwdParams, do, dq, dk, dv, strides, deterministic, cta_pair
     p.deterministic = 1 if deterministic else 0
     p.cta_pair = 1 if cta_pair else 0
     p.single_pass = 1 if single_pass else 0
+
+
+def _rel_grad(drel_bias, rel_bias, wanted: bool, stream):
+    """The buffer for rel_bias's gradient (the given one, checked), or None."""
+    if rel_bias is None or not wanted:
+        if drel_bias is not None:
+            raise ValueError("drel_bias without rel_bias, or without rel_bias_grad")
+        return None
+    if drel_bias is None:
+        drel_bias = torch.empty_like(rel_bias)
+        _used_on(stream, drel_bias)
+    elif drel_bias.shape != rel_bias.shape or drel_bias.dtype is not rel_bias.dtype or drel_bias.device != rel_bias.device or \
+            not drel_bias.is_contiguous():
+        raise ValueError(f"drel_bias must be a contiguous {rel_bias.dtype} tensor {tuple(rel_bias.shape)} on {rel_bias.device}")
+    return drel_bias
 
 
 def _grad_buffers(stream, *pairs):
@@ -461,13 +498,15 @@ def _event_handles(events):
 def attn_bwd(q, k, v, out, lse, dout, *, causal: bool = False, softmax_scale: Optional[float] = None,
              deterministic: bool = False, dq=None, dk=None, dv=None, stream=None, phase_events=None,
              cta_pair: bool = False, softcap: Optional[float] = None, alibi_slopes: Optional[torch.Tensor] = None,
-             single_pass: bool = False):
+             single_pass: bool = False, rel_bias: Optional[torch.Tensor] = None, rel_max_distance: int = 128,
+             rel_bidirectional: bool = True, drel_bias: Optional[torch.Tensor] = None, rel_bias_grad: bool = True):
     """Dense backward: returns (dQ, dK, dV) bf16 for the loss <O, dO>; where query heads share K/V heads
     (attn_fwd), dK and dV are the sums over them. ``phase_events`` (optional, three
     torch.cuda.Event) are recorded after the D pass, the dK/dV kernel and the dQ kernel. ``cta_pair``
     selects the two-SM (cta_group::2) dK/dV kernel (d = 128); ``single_pass`` the one-kernel backward
     whose dQ partials are reduced across CTAs (d = 64; ordered by key tile when ``deterministic``).
-    The score modification must be the forward's."""
+    The score modification must be the forward's. With ``rel_bias`` a fourth value is returned, its gradient in
+    its type (into ``drel_bias`` when given; None, and not computed, without ``rel_bias_grad``)."""
     for n, t in (("q", q), ("k", k), ("v", v), ("out", out), ("dout", dout)):
         _check_bf16(n, t, 4)
     B, Nq, H, dqk = q.shape
@@ -479,14 +518,16 @@ def attn_bwd(q, k, v, out, lse, dout, *, causal: bool = False, softmax_scale: Op
     _fill_fwd(p.fwd, q, k, v, out, lse, _strides4, scale, causal)
     p.fwd.batch, p.fwd.seqlen_q, p.fwd.seqlen_k = B, Nq, Nk
     _fill_bwd(p, dout, dq, dk, dv, _strides4, deterministic, cta_pair, single_pass)
-    _set_score_mod(p.fwd, q, softcap, alibi_slopes)
+    _set_score_mod(p.fwd, q, softcap, alibi_slopes, rel_bias, rel_max_distance, rel_bidirectional)
+    drel_bias = _rel_grad(drel_bias, rel_bias, rel_bias_grad, stream)
+    p.drel_bias = _ptr(drel_bias)
     handles = _event_handles(phase_events)
     if handles is not None:
         for i, h in enumerate(handles):
             p.phase_events[i] = h
     ws, nbytes = _workspace(_lib.attn_bwd_workspace_size(ctypes.byref(p)), q.device, stream)
     _abi.check(_lib.attn_bwd(ctypes.byref(p), _ptr(ws), nbytes, _stream(stream, q.device)), "attn_bwd")
-    return dq, dk, dv
+    return (dq, dk, dv) if rel_bias is None else (dq, dk, dv, drel_bias)
 
 
 def attn_bwd_block_sparse(q, k, v, out, lse, dout, kv_count, kv_index, *, causal: bool = False,
@@ -517,9 +558,11 @@ def attn_bwd_block_sparse(q, k, v, out, lse, dout, kv_count, kv_index, *, causal
 def attn_bwd_varlen(q, k, v, out, lse, dout, cu_seqlens_q, cu_seqlens_k, max_seqlen_q: int, max_seqlen_k: int, *,
                     causal: bool = False, softmax_scale: Optional[float] = None, deterministic: bool = False,
                     dq=None, dk=None, dv=None, stream=None, cta_pair: bool = False, softcap: Optional[float] = None,
-                    alibi_slopes: Optional[torch.Tensor] = None, single_pass: bool = False):
+                    alibi_slopes: Optional[torch.Tensor] = None, single_pass: bool = False,
+                    rel_bias: Optional[torch.Tensor] = None, rel_max_distance: int = 128,
+                    rel_bidirectional: bool = True, drel_bias: Optional[torch.Tensor] = None, rel_bias_grad: bool = True):
     """Packed variable-length backward: returns (dQ, dK, dV) packed like q, k, v; where query heads share
-    K/V heads (attn_fwd_varlen), dK and dV are the sums over them."""
+    K/V heads (attn_fwd_varlen), dK and dV are the sums over them. ``rel_bias`` and its gradient as in :func:`attn_bwd`."""
     ((tq, H, dqk), sq), (ks, sk), (vs, sv) = _bf16_layout("q", q, 3), _bf16_layout("k", k, 3), _bf16_layout("v", v, 3)
     (os, so), (ds, sd) = _bf16_layout("out", out, 3), _bf16_layout("dout", dout, 3)
     _check_offsets(q, cu_seqlens_q, cu_seqlens_k)
@@ -534,22 +577,24 @@ def attn_bwd_varlen(q, k, v, out, lse, dout, cu_seqlens_q, cu_seqlens_k, max_seq
     dq, tdq = _packed_grad("dq", dq, q, stream)
     dk, tdk = _packed_grad("dk", dk, k, stream)
     dv, tdv = _packed_grad("dv", dv, v, stream)
-    mod, cap, slopes = _mod_fields(q, softcap, alibi_slopes)
+    drel_bias = _rel_grad(drel_bias, rel_bias, rel_bias_grad, stream)
+    mod, rel = _mod_fields(q, softcap, alibi_slopes, rel_bias, rel_max_distance, rel_bidirectional)
     p = _pack_bwd(
         q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), lse.data_ptr(),
         0, sq[0], sq[1], 0, sk[0], sk[1], 0, sv[0], sv[1], 0, so[0], so[1],
         1, H, 0, 0, dqk, vs[2], cu_seqlens_q.data_ptr(), cu_seqlens_k.data_ptr(), cu_seqlens_q.shape[0] - 1,
-        int(max_seqlen_q), int(max_seqlen_k), tq, ks[0], scale, 1 if causal else 0, 0, 0, mod, cap, slopes,
-        0, 0.0, 0.0, 0.0, 0, ks[1],
+        int(max_seqlen_q), int(max_seqlen_k), tq, ks[0], scale, 1 if causal else 0, 0, 0, *mod,
+        0, 0.0, 0.0, 0.0, 0, ks[1], *rel,
         dout.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(),
         0, sd[0], sd[1], 0, tdq[0], tdq[1], 0, tdk[0], tdk[1], 0, tdv[0], tdv[1],
-        1 if deterministic else 0, 1 if cta_pair else 0, 0, 0, 0, 1 if single_pass else 0)
+        1 if deterministic else 0, 1 if cta_pair else 0, 0, 0, 0, 1 if single_pass else 0,
+        drel_bias.data_ptr() if drel_bias is not None else 0)
     nbytes = _lib.attn_bwd_varlen_workspace_size(p)
     ws, ws_ptr = _workspace_ptr(nbytes, q, stream)
     status = _lib.attn_bwd_varlen(p, ws_ptr, nbytes, _stream_of(stream, q))
     if status:
         _abi.check(status, "attn_bwd_varlen")
-    return dq, dk, dv
+    return (dq, dk, dv) if rel_bias is None else (dq, dk, dv, drel_bias)
 
 
 def _check_table(t, device: int, num_seqs: int) -> int:
@@ -778,7 +823,8 @@ def attn_fwd_paged(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor
                    cu_seqlens_q: torch.Tensor, seqlens_k: torch.Tensor, max_seqlen_q: int, *, causal: bool = True,
                    softmax_scale: Optional[float] = None, softcap: Optional[float] = None,
                    alibi_slopes: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
-                   lse: Optional[torch.Tensor] = None, stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
+                   lse: Optional[torch.Tensor] = None, rel_bias: Optional[torch.Tensor] = None, rel_max_distance: int = 128,
+                   rel_bidirectional: bool = True, stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
     """Attention of new tokens over a paged KV cache (include/attn.h, attn_fwd_paged). q [total_q, H, d_qk] (bf16)
     packs the requests' new tokens, request s's in rows cu_seqlens_q[s] .. cu_seqlens_q[s + 1] - 1 (one for a decoding
     request, a chunk for a prompt, or none); its keys are the first seqlens_k[s] tokens on the pages of row s of
@@ -811,13 +857,13 @@ def attn_fwd_paged(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor
         lse = torch.empty((H, tq), dtype=_F32, device=q.device)
     elif lse.shape != (H, tq) or not lse.is_contiguous() or lse.dtype is not _F32 or lse.device != q.device:
         raise ValueError(f"lse must be a contiguous float32 [H, total_q] tensor on cuda:{dev}")
-    mod, cap, slopes = _mod_fields(q, softcap, alibi_slopes)
+    mod, rel = _mod_fields(q, softcap, alibi_slopes, rel_bias, rel_max_distance, rel_bidirectional)
     p = _pack_paged(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), out.data_ptr(), lse.data_ptr(),
                     sq[0], sq[1], so[0], so[1], kt[0], kt[1], kt[2], vt[0], vt[1], vt[2],
                     block_table.data_ptr(), table_stride, cu_seqlens_q.data_ptr(), seqlens_k.data_ptr(),
                     n, H, hk, dqk, dv, ks[1], ks[0], block_table.shape[1], tq, int(max_seqlen_q),
                     float(softmax_scale) if softmax_scale is not None else 1.0 / math.sqrt(dqk),
-                    1 if causal else 0, mod, cap, slopes)
+                    1 if causal else 0, *mod, *rel)
     nbytes = _lib.attn_fwd_paged_workspace_size(p)
     ws, ws_ptr = _workspace_ptr(nbytes, q, stream)
     if stream is not None:
@@ -848,73 +894,83 @@ def attn_get_device_status(stream=None) -> int:
 
 class _Attention(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, q, k, v, causal, softmax_scale, deterministic, kv_count, kv_index, softcap, alibi_slopes):
-        mod = dict(softcap=softcap, alibi_slopes=alibi_slopes)
+    def forward(ctx, q, k, v, rel_bias, causal, softmax_scale, deterministic, kv_count, kv_index, mod, rel):
         if kv_count is None:
-            o, lse = attn_fwd(q, k, v, causal=causal, softmax_scale=softmax_scale, **mod)
+            o, lse = attn_fwd(q, k, v, causal=causal, softmax_scale=softmax_scale, rel_bias=rel_bias, **mod, **rel)
         else:
+            if rel_bias is not None:
+                raise ValueError("block_mask and rel_bias do not go together")
             o, lse = attn_fwd_block_sparse(q, k, v, kv_count, kv_index, causal=causal, softmax_scale=softmax_scale,
                                            **mod)
-        ctx.save_for_backward(q, k, v, o, lse)
+        ctx.save_for_backward(q, k, v, o, lse, rel_bias)
         ctx.causal, ctx.scale, ctx.det = causal, softmax_scale, deterministic
         ctx.lists = (kv_count, kv_index)
-        ctx.mod = mod
+        ctx.mod, ctx.rel = mod, rel
         return o
 
     @staticmethod
     def backward(ctx, do):
-        q, k, v, o, lse = ctx.saved_tensors
+        q, k, v, o, lse, rel_bias = ctx.saved_tensors
         kv_count, kv_index = ctx.lists
         if kv_count is None:
-            dq, dk, dv = attn_bwd(q, k, v, o, lse, do.contiguous(), causal=ctx.causal, softmax_scale=ctx.scale,
-                                  deterministic=ctx.det, **ctx.mod)
+            grads = attn_bwd(q, k, v, o, lse, do.contiguous(), causal=ctx.causal, softmax_scale=ctx.scale,
+                             deterministic=ctx.det, rel_bias=rel_bias, rel_bias_grad=ctx.needs_input_grad[3], **ctx.mod,
+                             **ctx.rel)
         else:
-            dq, dk, dv = attn_bwd_block_sparse(q, k, v, o, lse, do.contiguous(), kv_count, kv_index,
-                                               causal=ctx.causal, softmax_scale=ctx.scale, deterministic=ctx.det,
-                                               **ctx.mod)
-        return dq, dk, dv, None, None, None, None, None, None, None
+            grads = attn_bwd_block_sparse(q, k, v, o, lse, do.contiguous(), kv_count, kv_index,
+                                          causal=ctx.causal, softmax_scale=ctx.scale, deterministic=ctx.det,
+                                          **ctx.mod)
+        return (*grads, *(None,) * (11 - len(grads)))
 
 
 def attention(q, k, v, causal: bool = False, softmax_scale: Optional[float] = None, deterministic: bool = False,
               block_mask: Optional[Tuple[torch.Tensor, torch.Tensor]] = None, softcap: Optional[float] = None,
-              alibi_slopes: Optional[torch.Tensor] = None):
+              alibi_slopes: Optional[torch.Tensor] = None, rel_bias: Optional[torch.Tensor] = None, rel_max_distance: int = 128,
+              rel_bidirectional: bool = True):
     """Autograd wrapper over attn_fwd / attn_bwd for [B, N, H, d] bf16 tensors; k and v may have fewer
     heads, a divisor of H, shared among the query heads as in attn_fwd. ``block_mask``
     = (kv_count, kv_index) selects the block-sparse pair attn_fwd_block_sparse / attn_bwd_block_sparse;
-    ``softcap`` / ``alibi_slopes`` a score modification."""
+    ``softcap`` / ``alibi_slopes`` / ``rel_bias`` (which gets a gradient; not with block_mask) a score modification."""
     kv_count, kv_index = block_mask if block_mask is not None else (None, None)
-    return _Attention.apply(q, k, v, causal, softmax_scale, deterministic, kv_count, kv_index, softcap, alibi_slopes)
+    return _Attention.apply(q, k, v, rel_bias, causal, softmax_scale, deterministic, kv_count, kv_index,
+                            dict(softcap=softcap, alibi_slopes=alibi_slopes),
+                            dict(rel_max_distance=rel_max_distance, rel_bidirectional=rel_bidirectional))
 
 
 class _AttentionVarlen(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, q, k, v, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, max_seqlen_k, causal, softmax_scale,
-                deterministic, softcap, alibi_slopes):
-        mod = dict(softcap=softcap, alibi_slopes=alibi_slopes)
+    def forward(ctx, q, k, v, rel_bias, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, max_seqlen_k, causal, softmax_scale,
+                deterministic, mod):
         o, lse = attn_fwd_varlen(q, k, v, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, max_seqlen_k, causal=causal,
-                                 softmax_scale=softmax_scale, **mod)
-        ctx.save_for_backward(q, k, v, o, lse, cu_seqlens_q, cu_seqlens_k)
+                                 softmax_scale=softmax_scale, rel_bias=rel_bias, **mod)
+        ctx.save_for_backward(q, k, v, o, lse, rel_bias, cu_seqlens_q, cu_seqlens_k)
         ctx.lengths = (max_seqlen_q, max_seqlen_k)
         ctx.causal, ctx.scale, ctx.det, ctx.mod = causal, softmax_scale, deterministic, mod
         return o
 
     @staticmethod
     def backward(ctx, do):
-        q, k, v, o, lse, cu_q, cu_k = ctx.saved_tensors
+        q, k, v, o, lse, rel_bias, cu_q, cu_k = ctx.saved_tensors
         grads = attn_bwd_varlen(q, k, v, o, lse, do.contiguous(), cu_q, cu_k, *ctx.lengths, causal=ctx.causal,
-                                softmax_scale=ctx.scale, deterministic=ctx.det, **ctx.mod)
-        return (*grads, *(None,) * 9)
+                                softmax_scale=ctx.scale, deterministic=ctx.det, rel_bias=rel_bias,
+                                rel_bias_grad=ctx.needs_input_grad[3], **ctx.mod)
+        return (*grads, *(None,) * (12 - len(grads)))
 
 
 def attention_varlen(q, k, v, cu_seqlens_q, cu_seqlens_k, max_seqlen_q: int, max_seqlen_k: int, causal: bool = False,
                      softmax_scale: Optional[float] = None, deterministic: bool = False,
-                     softcap: Optional[float] = None, alibi_slopes: Optional[torch.Tensor] = None):
+                     softcap: Optional[float] = None, alibi_slopes: Optional[torch.Tensor] = None,
+                     rel_bias: Optional[torch.Tensor] = None, rel_max_distance: int = 128,
+                     rel_bidirectional: bool = True):
     """Autograd wrapper over attn_fwd_varlen / attn_bwd_varlen for packed bf16 tensors q [total_q, H, d_qk],
-    k [total_k, Hkv, d_qk] and v [total_k, Hkv, d_v]; ``softcap`` / ``alibi_slopes`` select a score modification.
+    k [total_k, Hkv, d_qk] and v [total_k, Hkv, d_v]; ``softcap`` / ``alibi_slopes`` / ``rel_bias`` (which gets a gradient)
+    select a score modification.
     The offsets cover every row: cu_seqlens[-1] is the total (of a buffer with spare rows, pass the used part: O and the
     gradients of rows behind the last offset are not written)."""
-    return _AttentionVarlen.apply(q, k, v, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, max_seqlen_k, causal,
-                                  softmax_scale, deterministic, softcap, alibi_slopes)
+    return _AttentionVarlen.apply(q, k, v, rel_bias, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, max_seqlen_k, causal,
+                                  softmax_scale, deterministic,
+                                  dict(softcap=softcap, alibi_slopes=alibi_slopes, rel_max_distance=rel_max_distance,
+                                       rel_bidirectional=rel_bidirectional))
 
 
 class _Rotary(torch.autograd.Function):

@@ -11,7 +11,7 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libattn_gb300.so")
 HEADER_PATH = os.path.join(os.path.dirname(HERE), "include", "attn.h")
 
-ABI_VERSION = 8
+ABI_VERSION = 9
 BWD_NOALLOC_SCRATCH_BYTES = 8 << 20  # ATTN_BWD_NOALLOC_SCRATCH_BYTES
 
 STATUS = {
@@ -23,10 +23,15 @@ STATUS = {
     5: "ATTN_ERR_WORKSPACE",
 }
 ATTN_OK, ATTN_ERR_INVALID_ARG, ATTN_ERR_UNSUPPORTED, ATTN_ERR_CUDA, ATTN_ERR_TIMEOUT, ATTN_ERR_WORKSPACE = range(6)
-SCORE_NONE, SCORE_SOFTCAP, SCORE_ALIBI = range(3)  # attn_score_mod_t
+SCORE_NONE, SCORE_SOFTCAP, SCORE_ALIBI, SCORE_RELBIAS = range(4)  # attn_score_mod_t
+TABLE_BF16, TABLE_F32 = range(2)  # attn_table_dtype_t
 INPUT_BF16, INPUT_E4M3 = range(2)  # attn_input_dtype_t
 
 c_i32, c_i64, c_f32, c_vp = ctypes.c_int32, ctypes.c_int64, ctypes.c_float, ctypes.c_void_p
+
+
+_REL_BIAS = [("rel_bias", c_vp), ("rel_bias_dtype", c_i32), ("rel_buckets", c_i32), ("rel_max_distance", c_i32),
+             ("rel_bidirectional", c_i32)]
 
 
 class AttnFwdParams(ctypes.Structure):
@@ -46,7 +51,7 @@ class AttnFwdParams(ctypes.Structure):
         ("score_mod", c_i32), ("softcap", ctypes.c_float), ("alibi_slopes", c_vp),
         ("input_dtype", c_i32), ("q_descale", ctypes.c_float), ("k_descale", ctypes.c_float),
         ("v_descale", ctypes.c_float), ("cta_pair", c_i32), ("heads_kv", c_i32),
-    ]
+    ] + _REL_BIAS
 
 
 class AttnBwdParams(ctypes.Structure):
@@ -59,7 +64,7 @@ class AttnBwdParams(ctypes.Structure):
         ("dv_batch_stride", c_i64), ("dv_row_stride", c_i64), ("dv_head_stride", c_i64),
         ("deterministic", c_i32), ("cta_pair", c_i32),
         ("phase_events", c_vp * 3),
-        ("single_pass", c_i32),
+        ("single_pass", c_i32), ("drel_bias", c_vp),
     ]
 
 
@@ -95,7 +100,7 @@ class AttnPagedParams(ctypes.Structure):
         ("num_seqs", c_i32), ("heads", c_i32), ("heads_kv", c_i32), ("d_qk", c_i32), ("d_v", c_i32),
         ("page_size", c_i32), ("num_pages", c_i32), ("max_pages", c_i32), ("total_q", c_i32), ("max_seqlen_q", c_i32),
         ("softmax_scale", c_f32), ("causal", c_i32), ("score_mod", c_i32), ("softcap", c_f32), ("alibi_slopes", c_vp),
-    ]
+    ] + _REL_BIAS
 
 
 class AttnRotaryParams(ctypes.Structure):

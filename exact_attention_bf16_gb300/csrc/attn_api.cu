@@ -152,6 +152,7 @@ DeviceScope::~DeviceScope() {
 
 namespace {
 
+size_t round256(int64_t b) { return static_cast<size_t>((b + 255) / 256 * 256); }
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 bool stride_ok(int64_t s) { return s >= 0 && (s % 8) == 0 && s < (int64_t(1) << 38); }
 
@@ -165,6 +166,92 @@ bool shared_kv(const attn_fwd_params* p) { return kv_heads(p) != p->heads; }
 
 bool scale_ok(float scale) { return std::isfinite(scale) && scale > 0.f; }
 
+// ---- relative position bias --------------------------------------------------
+// a[0..] of base 2^32, times x; more than any power below needs (65536^64 * 64^64).
+struct BigNum {
+  static constexpr int kLimbs = 64;
+  uint32_t d[kLimbs] = {1};
+  int n = 1;
+  void times(uint32_t x) {
+    uint64_t carry = 0;
+    for (int i = 0; i < n; ++i) {
+      carry += static_cast<uint64_t>(d[i]) * x;
+      d[i] = static_cast<uint32_t>(carry);
+      carry >>= 32;
+    }
+    if (carry && n < kLimbs) d[n++] = static_cast<uint32_t>(carry);
+  }
+  void times_power(uint32_t x, int k) {
+    for (int i = 0; i < k; ++i) times(x);
+  }
+  bool at_least(const BigNum& o) const {
+    if (n != o.n) return n > o.n;
+    for (int i = n - 1; i >= 0; --i)
+      if (d[i] != o.d[i]) return d[i] > o.d[i];
+    return true;
+  }
+};
+
+// First distances of the n_b buckets of a side (include/attn.h); returns the last one, at least 1. Bucket m + k begins at the
+// least n with (n / m)^w >= (far / m)^k, w = n_b - m: a root that is no whole number by floating point, one that may be in
+// whole numbers, n^w m^k >= far^k m^w.
+int rel_borders(int n_b, int far, int* start) {
+  const int m = n_b / 2, w = n_b - m;
+  for (int k = 0; k <= m && k < n_b; ++k) start[k] = k;
+  for (int k = 1; k < w && m > 0; ++k) {
+    const double x = m * std::pow(static_cast<double>(far) / m, static_cast<double>(k) / w);
+    const double near = std::floor(x + 0.5);
+    int n = static_cast<int>(std::ceil(x));
+    if (std::fabs(x - near) <= 1e-9 * x) {
+      n = static_cast<int>(near);
+      BigNum lhs, rhs;
+      lhs.times_power(static_cast<uint32_t>(n), w);
+      lhs.times_power(static_cast<uint32_t>(m), k);
+      rhs.times_power(static_cast<uint32_t>(far), k);
+      rhs.times_power(static_cast<uint32_t>(m), w);
+      if (!lhs.at_least(rhs)) ++n;
+    }
+    start[m + k] = n;
+  }
+  return std::max(1, start[n_b - 1]);
+}
+
+template <typename P>  // attn_fwd_params or attn_paged_params
+attn_status_t check_rel(const P* p) {
+  const uintptr_t low = p->rel_bias_dtype == ATTN_TABLE_F32 ? 3u : 1u;
+  if (!p->rel_bias || (p->rel_bias_dtype != ATTN_TABLE_BF16 && p->rel_bias_dtype != ATTN_TABLE_F32) ||
+      (reinterpret_cast<uintptr_t>(p->rel_bias) & low))
+    return ATTN_ERR_INVALID_ARG;
+  if (p->rel_buckets < 1 || p->rel_buckets > kRelMaxBuckets || (p->rel_bidirectional && p->rel_buckets % 2))
+    return ATTN_ERR_INVALID_ARG;
+  const int side = p->rel_bidirectional ? p->rel_buckets / 2 : p->rel_buckets;
+  return p->rel_max_distance > side / 2 && p->rel_max_distance <= 65536 ? ATTN_OK : ATTN_ERR_INVALID_ARG;
+}
+
+// The table's layout for calls whose queries and keys are at most `longest` apart, and its room in a workspace.
+struct RelPlan {
+  RelTable table{};
+  size_t place_bytes = 0, bucket_bytes = 0, range_bytes = 0;
+};
+template <typename P>
+RelPlan rel_plan(const P* p, int64_t longest) {
+  RelPlan r;
+  if (p->score_mod != ATTN_SCORE_RELBIAS || p->heads < 1 || check_rel(p) != ATTN_OK) return r;
+  RelTable& t = r.table;
+  t.table = p->rel_bias;
+  t.f32 = p->rel_bias_dtype == ATTN_TABLE_F32;
+  t.heads = p->heads;
+  t.buckets = p->rel_buckets;
+  t.two_sided = p->rel_bidirectional ? 1 : 0;
+  t.side = t.two_sided ? t.buckets / 2 : t.buckets;
+  t.reach = static_cast<int>(std::min<int64_t>(rel_borders(t.side, p->rel_max_distance, t.start), std::max<int64_t>(longest, 1)));
+  const int64_t width = 2 * t.reach + 2 * kRelPad;
+  r.place_bytes = round256(t.heads * width * 4);
+  r.bucket_bytes = round256(width);
+  r.range_bytes = kRelMaxBuckets * sizeof(int2);
+  return r;
+}
+
 attn_status_t check_scores(float scale, int32_t score_mod, float softcap, const float* alibi_slopes) {
   if (!scale_ok(scale)) return ATTN_ERR_INVALID_ARG;
   switch (score_mod) {
@@ -173,6 +260,7 @@ attn_status_t check_scores(float scale, int32_t score_mod, float softcap, const 
       return std::isfinite(softcap) && softcap > 0.f && std::isfinite(softcap / scale) ? ATTN_OK : ATTN_ERR_INVALID_ARG;
     case ATTN_SCORE_ALIBI:
       return alibi_slopes && !(reinterpret_cast<uintptr_t>(alibi_slopes) & 3u) ? ATTN_OK : ATTN_ERR_INVALID_ARG;
+    case ATTN_SCORE_RELBIAS: return ATTN_OK;  // check_rel
     default: return ATTN_ERR_INVALID_ARG;
   }
 }
@@ -224,6 +312,7 @@ attn_status_t check_fwd(const attn_fwd_params* p, bool varlen) {
   ATTN_TRY(check_tensor(p->v, p->v_batch_stride, p->v_row_stride, p->v_head_stride, varlen, ek));
   ATTN_TRY(check_tensor(p->o, p->o_batch_stride, p->o_row_stride, p->o_head_stride, varlen, eq));
   if ((!p->lse && !eq) || (reinterpret_cast<uintptr_t>(p->lse) & 3u)) return ATTN_ERR_INVALID_ARG;
+  if (p->score_mod == ATTN_SCORE_RELBIAS) ATTN_TRY(check_rel(p));
   return check_scores(p->softmax_scale, p->score_mod, p->softcap, p->alibi_slopes);
 }
 
@@ -275,7 +364,6 @@ struct ListPlan {
   int64_t bound = 0;
   size_t list_bytes = 0;
 };
-size_t round256(int64_t b) { return static_cast<size_t>((b + 255) / 256 * 256); }
 ListPlan list_plan(int64_t total_rows, int num_seqs, int heads, int64_t max_len, int rows_per_block) {
   ListPlan lp;
   const int64_t max_nblk = (max_len + rows_per_block - 1) / rows_per_block;
@@ -337,11 +425,15 @@ size_t fwd_split_bytes(const attn_fwd_params* p, const SplitPlan& sp) {
   const int64_t rows = static_cast<int64_t>(p->batch) * p->heads * p->seqlen_q;
   return round256(sp.splits * rows * p->d_v * 4) + round256(sp.splits * rows * 4);
 }
+// The bias's layout of a forward or backward call.
+RelPlan call_rel_plan(const attn_fwd_params* p, bool varlen) {
+  return rel_plan(p, varlen ? std::max(p->max_seqlen_q, p->max_seqlen_k) : std::max(p->seqlen_q, p->seqlen_k));
+}
 size_t fwd_workspace_bytes(const attn_fwd_params* p, bool varlen) {
   const size_t v16 = fwd_v16_bytes(p, varlen);
   if (!v16) return 0;
   const ListPlan lp = fwd_list_plan(p, varlen);
-  return 256 + v16 + (lp.use ? lp.list_bytes + seq_scratch_bytes(p->num_seqs) : 0) +
+  return 256 + v16 + call_rel_plan(p, varlen).place_bytes + (lp.use ? lp.list_bytes + seq_scratch_bytes(p->num_seqs) : 0) +
          fwd_split_bytes(p, fwd_split_plan(p, varlen));
 }
 
@@ -360,6 +452,7 @@ attn_status_t run_fwd(const attn_fwd_params* p, bool varlen, cudaStream_t stream
   ATTN_TRY(check_fwd(p, varlen));
   if (p->exp2_emu_period != 0 && p->exp2_emu_period != 4 && p->exp2_emu_period != 8) return ATTN_ERR_INVALID_ARG;
   if (p->score_mod != ATTN_SCORE_NONE && (p->exp2_emu_period != 0 || diag_limit)) return ATTN_ERR_UNSUPPORTED;
+  if (p->score_mod == ATTN_SCORE_RELBIAS && sp.kv_count != nullptr) return ATTN_ERR_UNSUPPORTED;
   const bool f8 = p->input_dtype == ATTN_INPUT_E4M3;
   if (f8) {
     if (p->d_qk != 128 || p->d_v != 128 || p->exp2_emu_period != 0 || p->score_mod != ATTN_SCORE_NONE ||
@@ -388,6 +481,7 @@ attn_status_t run_fwd(const attn_fwd_params* p, bool varlen, cudaStream_t stream
   const int max_q = varlen ? p->max_seqlen_q : p->seqlen_q;
   if (nq_rows == 0 || max_q == 0) return ATTN_OK;
   if (nk_rows > 0 && p->score_mod == ATTN_SCORE_ALIBI) ATTN_TRY(check_lists_device(p->q, {p->alibi_slopes}));
+  if (nk_rows > 0 && p->score_mod == ATTN_SCORE_RELBIAS) ATTN_TRY(check_lists_device(p->q, {p->rel_bias}));
   const size_t need_ws = diag_limit ? 0 : fwd_workspace_bytes(p, varlen);
   if (nk_rows > 0 && need_ws > 0 && (ws == nullptr || ws_bytes < need_ws || (reinterpret_cast<uintptr_t>(ws) & 255u)))
     return ATTN_ERR_WORKSPACE;
@@ -470,6 +564,14 @@ attn_status_t run_fwd(const attn_fwd_params* p, bool varlen, cudaStream_t stream
   ATTN_TRY(make_map(&tv16, v16, p->d_v, hkv, nk_rows, nb, v16_rows * hkv * p->d_v,
                     static_cast<int64_t>(hkv) * p->d_v, p->d_v, 128));
   const ListPlan lp = fwd_list_plan(p, varlen);
+  if (p->score_mod == ATTN_SCORE_RELBIAS) {  // ahead of the lists, whose kernel others run beside
+    const RelPlan rp = call_rel_plan(p, varlen);
+    a.rel.by_place = reinterpret_cast<const float*>(static_cast<uint8_t*>(ws) + need_ws - rp.place_bytes);
+    a.rel.reach = rp.table.reach;
+    a.rel.buckets = rp.table.buckets;
+    e = launch_rel_layout(rp.table, a.rel, nullptr, 0, stream);
+    if (e != cudaSuccess) return cuda_fail(e, "bias layout");
+  }
   SeqMaps maps{};
   if (varlen && ws_bytes >= need_ws + fwd_seq_map_bytes(p)) {  // V of each sequence, apart from the next one's
     maps.base[0] = tv, maps.base[1] = tv16;
@@ -615,8 +717,21 @@ size_t bwd_dkv_split_bytes(const attn_bwd_params* p, bool varlen, int split) {
   const int64_t rows = varlen ? f.total_k : static_cast<int64_t>(f.batch) * f.seqlen_k;
   return round256(split * rows * kv_heads(&f) * (f.d_qk + f.d_v) * 4);
 }
-// The workspace without the split-key dQ and split-group dK/dV partials (the least a call accepts).
-size_t bwd_workspace_bytes(const attn_bwd_params* p, bool varlen) {
+// The bias's layout and its gradient's parts: eight rows of buckets per head and CTA of the dQ kernel.
+int64_t bwd_rel_part_rows(const attn_bwd_params* p, bool varlen, int splits) {
+  const attn_fwd_params& f = p->fwd;
+  if (varlen) return 8 * (static_cast<int64_t>(f.total_q) / 128 + f.num_seqs);
+  return 8 * static_cast<int64_t>(f.batch) * ((static_cast<int64_t>(f.seqlen_q) + 127) / 128) * splits;
+}
+size_t bwd_rel_bytes(const attn_bwd_params* p, bool varlen) {
+  const attn_fwd_params& f = p->fwd;
+  const RelPlan rp = call_rel_plan(&f, varlen);
+  if (!rp.place_bytes || (varlen ? f.total_q < 0 || f.num_seqs < 0 : f.batch < 0 || f.seqlen_q < 0)) return 0;
+  const int64_t rows = p->drel_bias ? bwd_rel_part_rows(p, varlen, bwd_dq_split_plan(p, varlen).splits) : 0;
+  return rp.place_bytes + rp.bucket_bytes + rp.range_bytes + round256(f.heads * rows * f.rel_buckets * 4);
+}
+// The workspace without the split-key dQ and split-group dK/dV partials (the least a call accepts), and without the bias.
+size_t bwd_base_bytes(const attn_bwd_params* p, bool varlen) {
   const size_t d = bwd_d_bytes(p, varlen);
   const size_t fused = bwd_dq_acc_bytes(p, varlen) + bwd_sem_bytes(p, varlen);
   if (!varlen) return d + fused;
@@ -624,6 +739,7 @@ size_t bwd_workspace_bytes(const attn_bwd_params* p, bool varlen) {
   const size_t lists = (kv.use ? kv.list_bytes : 0) + (q.use ? q.list_bytes : 0);
   return d + lists + (lists ? seq_scratch_bytes(p->fwd.num_seqs) : 0) + fused;
 }
+size_t bwd_workspace_bytes(const attn_bwd_params* p, bool varlen) { return bwd_base_bytes(p, varlen) + bwd_rel_bytes(p, varlen); }
 
 // Extra workspace of the block-sparse backward: the transposed lists
 // (int32 q_count[sets][n_kb], then q_index[sets][n_kb][n_qb256]) after the D
@@ -656,14 +772,26 @@ attn_status_t run_bwd(const attn_bwd_params* p, void* ws, size_t ws_bytes, bool 
     return ATTN_ERR_UNSUPPORTED;
   if (shared_kv(&f) && (p->cta_pair || p->single_pass || sp.kv_count || f.heads >= 65536))
     return ATTN_ERR_UNSUPPORTED;
+  const bool rel = f.score_mod == ATTN_SCORE_RELBIAS;
+  if (rel && sp.kv_count) return ATTN_ERR_UNSUPPORTED;
+  if (p->drel_bias && (!rel || (reinterpret_cast<uintptr_t>(p->drel_bias) & (f.rel_bias_dtype == ATTN_TABLE_F32 ? 3u : 1u))))
+    return ATTN_ERR_INVALID_ARG;
   const int hkv = kv_heads(&f);
   const int nq_rows = varlen ? f.total_q : f.seqlen_q;
   const int nk_rows = varlen ? f.total_k : f.seqlen_k;
-  if (nq_rows == 0 && nk_rows == 0) return ATTN_OK;
+  const bool none = nq_rows == 0 && nk_rows == 0;
+  if (none && !p->drel_bias) return ATTN_OK;
   DeviceScope scope;
   {
-    cudaError_t be = scope.bind(nq_rows ? f.q : f.k);
+    cudaError_t be = scope.bind(none ? p->drel_bias : nq_rows ? f.q : f.k);
     if (be != cudaSuccess) return be == cudaErrorInvalidDevicePointer ? ATTN_ERR_INVALID_ARG : cuda_fail(be, "device");
+  }
+  if (rel) ATTN_TRY(check_lists_device(none ? p->drel_bias : nq_rows ? f.q : f.k, {f.rel_bias, p->drel_bias}));
+  if (p->drel_bias && (nq_rows == 0 || nk_rows == 0)) {  // no pairs
+    const cudaError_t ze = cudaMemsetAsync(
+        p->drel_bias, 0, static_cast<size_t>(f.rel_buckets) * f.heads * (f.rel_bias_dtype == ATTN_TABLE_F32 ? 4 : 2), stream);
+    if (ze != cudaSuccess) return cuda_fail(ze, "bias gradient");
+    if (none) return ATTN_OK;
   }
   const size_t need_d = bwd_workspace_bytes(p, varlen);
   const size_t need = need_d + (sp.kv_count ? bwd_sparse_extra_bytes(f, sp.lists_per_head) : 0);
@@ -762,6 +890,23 @@ attn_status_t run_bwd(const attn_bwd_params* p, void* ws, size_t ws_bytes, bool 
     ATTN_TRY(make_map(&tv, f.v, f.d_v, hkv, nk_rows, nb, f.v_batch_stride, f.v_row_stride, f.v_head_stride, 128));
   }
 
+  if (nq_rows > 0 && nk_rows > 0 && rel) {  // the bias by place (ahead of the lists, whose kernel others run beside)
+    const RelPlan rp = call_rel_plan(&f, varlen);
+    uint8_t* at = static_cast<uint8_t*>(ws) + bwd_base_bytes(p, varlen);
+    a.rel.by_place = reinterpret_cast<const float*>(at);
+    a.rel.bucket = at + rp.place_bytes;
+    a.rel.range = reinterpret_cast<const int2*>(at + rp.place_bytes + rp.bucket_bytes);
+    a.rel.reach = rp.table.reach;
+    a.rel.buckets = rp.table.buckets;
+    if (p->drel_bias) {
+      a.rel.parts = reinterpret_cast<float*>(at + rp.place_bytes + rp.bucket_bytes + rp.range_bytes);
+      a.rel.part_rows = bwd_rel_part_rows(p, varlen, dqs.splits);
+    }
+    const int64_t n_parts = varlen ? f.heads * a.rel.part_rows * f.rel_buckets : 0;  // (dense: every CTA writes its own)
+    e = launch_rel_layout(rp.table, a.rel, a.rel.parts, n_parts, stream);
+    if (e != cudaSuccess) return cuda_fail(e, "bias layout");
+  }
+
   if (nq_rows > 0 && nk_rows > 0 && varlen) {  // tile lists: longest sequences first, no CTA past an end
     const ListPlan kv = bwd_kv_plan(p, varlen), qp = bwd_q_plan(p, varlen);
     uint8_t* lbase = static_cast<uint8_t*>(ws) + bwd_d_bytes(p, varlen);
@@ -851,6 +996,9 @@ attn_status_t run_bwd(const attn_bwd_params* p, void* ws, size_t ws_bytes, bool 
   }
   e = launch_bwd_dq(f.d_qk, f.d_v, tq, tk, tv, tdo, a, stream);
   if (e == cudaSuccess && dqs.splits > 1) e = launch_bwd_dq_merge(a, f.d_qk, stream);
+  if (e == cudaSuccess && p->drel_bias)
+    e = launch_rel_sum(a.rel.parts, a.rel.part_rows, f.rel_buckets, f.heads, p->drel_bias, f.rel_bias_dtype == ATTN_TABLE_F32,
+                       stream);
   if (e == cudaSuccess) e = mark(2);
   if (e != cudaSuccess) return cuda_fail(e, "bwd dq launch");
   return ATTN_OK;
@@ -1137,6 +1285,7 @@ attn_status_t check_paged(const attn_paged_params* p) {
   ATTN_TRY(check_cache(p->v_cache, p->v_page_stride, p->v_row_stride, p->v_head_stride));
   if (!none && !aligned4(p->lse)) return ATTN_ERR_INVALID_ARG;
   if (!aligned4(p->block_table) || !aligned4(p->cu_seqlens_q) || !aligned4(p->seqlens_k)) return ATTN_ERR_INVALID_ARG;
+  if (p->score_mod == ATTN_SCORE_RELBIAS) ATTN_TRY(check_rel(p));
   return check_scores(p->softmax_scale, p->score_mod, p->softcap, p->alibi_slopes);
 }
 
@@ -1147,7 +1296,8 @@ struct PagedPlan {
   bool decode = false;
   int q_box_tokens = 0;
   int64_t items = 0;
-  size_t off_lse = 0, off_merge = 0, off_list = 0, off_items = 0, bytes = 0;
+  size_t off_lse = 0, off_merge = 0, off_list = 0, off_items = 0, off_rel = 0, bytes = 0;
+  RelPlan rel;
 };
 PagedPlan paged_plan(const attn_paged_params* p) {
   PagedPlan pl;
@@ -1169,6 +1319,9 @@ PagedPlan paged_plan(const attn_paged_params* p) {
     pl.off_items = pl.off_list + 256;
     pl.bytes = pl.off_items + round256(pl.items * static_cast<int64_t>(sizeof(ChunkItem)));
   }
+  pl.rel = rel_plan(p, std::max<int64_t>(static_cast<int64_t>(p->max_pages) * p->page_size, p->max_seqlen_q));
+  pl.off_rel = pl.bytes;
+  pl.bytes += pl.rel.place_bytes;
   return pl;
 }
 
@@ -1176,7 +1329,8 @@ attn_status_t run_fwd_paged(const attn_paged_params* p, void* ws, size_t ws_byte
   ATTN_TRY(check_paged(p));
   if (p->total_q == 0 || p->max_seqlen_q == 0) return ATTN_OK;
   ATTN_TRY(check_lists_device(p->q, {p->k_cache, p->v_cache, p->o, p->lse, p->block_table, p->cu_seqlens_q, p->seqlens_k,
-                                     p->score_mod == ATTN_SCORE_ALIBI ? p->alibi_slopes : nullptr}));
+                                     p->score_mod == ATTN_SCORE_ALIBI ? p->alibi_slopes : nullptr,
+                                     p->score_mod == ATTN_SCORE_RELBIAS ? p->rel_bias : nullptr}));
   DeviceScope scope;
   ATTN_TRY(bind_device(&scope, p->q));
   const PagedPlan pl = paged_plan(p);
@@ -1215,6 +1369,13 @@ attn_status_t run_fwd_paged(const attn_paged_params* p, void* ws, size_t ws_byte
     a.list = reinterpret_cast<ChunkList*>(base + pl.off_list);
     a.items = reinterpret_cast<ChunkItem*>(base + pl.off_items);
     a.items_bound = static_cast<int>(pl.items);
+  }
+  if (p->score_mod == ATTN_SCORE_RELBIAS) {
+    a.rel.by_place = reinterpret_cast<const float*>(base + pl.off_rel);
+    a.rel.reach = pl.rel.table.reach;
+    a.rel.buckets = pl.rel.table.buckets;
+    e = launch_rel_layout(pl.rel.table, a.rel, nullptr, 0, stream);
+    if (e != cudaSuccess) return cuda_fail(e, "bias layout");
   }
   int dev = 0, sms = 0;
   e = cudaGetDevice(&dev);

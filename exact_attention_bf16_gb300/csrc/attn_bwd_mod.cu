@@ -43,6 +43,7 @@ cudaError_t launch_bwd_dkdv_mod(int d_qk, int d_v, const CUtensorMap& tq, const 
     case kModAlibi:
       return sp ? bwd::dkdv_m<kModAlibi, true>(d_qk, d_v, tq, tk, tv, tdo, a, stream)
                 : bwd::dkdv_m<kModAlibi, false>(d_qk, d_v, tq, tk, tv, tdo, a, stream);
+    case kModRelBias: return sp ? cudaErrorInvalidValue : launch_bwd_dkdv_rel(d_qk, d_v, tq, tk, tv, tdo, a, stream);
     default: return cudaErrorInvalidValue;
   }
 }
@@ -57,6 +58,7 @@ cudaError_t launch_bwd_dq_mod(int d_qk, int d_v, const CUtensorMap& tq, const CU
     case kModAlibi:
       return sp ? bwd::dq_m<kModAlibi, true>(d_qk, d_v, tq, tk, tv, tdo, a, stream)
                 : bwd::dq_m<kModAlibi, false>(d_qk, d_v, tq, tk, tv, tdo, a, stream);
+    case kModRelBias: return sp ? cudaErrorInvalidValue : launch_bwd_dq_rel(d_qk, d_v, tq, tk, tv, tdo, a, stream);
     default: return cudaErrorInvalidValue;
   }
 }

@@ -31,6 +31,7 @@ cudaError_t launch_fwd_mod(int d_qk, int d_v, const CUtensorMap& tq, const CUten
   switch (a.score_mod) {
     case kModSoftcap: return fwd::launch_d<kModSoftcap>(d_qk, d_v, tq, tk, tv, tv16, a, stream);
     case kModAlibi: return fwd::launch_d<kModAlibi>(d_qk, d_v, tq, tk, tv, tv16, a, stream);
+    case kModRelBias: return launch_fwd_rel(d_qk, d_v, tq, tk, tv, tv16, a, stream);
     default: return cudaErrorInvalidValue;
   }
 }

@@ -51,6 +51,7 @@
 #include "kernels.h"
 #include "paged_common.cuh"
 #include "ptx_sm100.cuh"
+#include "rel_bias.cuh"
 #include "score_mod.cuh"
 
 namespace gb300 {
@@ -346,6 +347,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (MOD == kModAlibi && valid)
           slope = fabsf(__ldg(a.alibi_slopes + w.hk * a.kv_group + static_cast<int>(quarter * 32 + lane) % a.kv_group) *
                         a.inv_scale);
+        RelRow rel{};
+        if constexpr (MOD == kModRelBias) rel = rel_row(a.rel, w.hk * a.kv_group + static_cast<int>(quarter * 32 + lane) % a.kv_group);
         // whether this lane's page of key block kt holds keys (one lane per page of a block)
         auto page_ok = [&](int kt) -> bool {
           const int np = a.page_size < BN ? BN >> a.page_shift : 1;
@@ -389,7 +392,22 @@ __global__ void __launch_bounds__(kThreads, 1)
               for (int c = 0; c < BN; ++c)
                 s[c] = __float_as_uint(__uint_as_float(s[c]) - fabsf(fmaf(slope, static_cast<float>(c), base)));
             }
+            const float sl2 = a.scale_log2;
+            // relative position bias: logits in log2 units, s * mul + add, where each row's bias is one number; else taken so
+            // here, and mul = 1 (a warp's tokens are at most 32 in a row; rows without one take any places)
+            float mul = sl2, add = 0.f;
+            if constexpr (MOD == kModRelBias) {
+              const int r0 = valid ? kt * BN - pos : 0;
+              const bool far = rel_far(rel, r0, r0 + BN - 1, add) || !valid;
+              if (!__all_sync(0xffffffffu, far)) {
+                const float* at = rel.centre + r0;
+#pragma unroll
+                for (int c = 0; c < BN; ++c) s[c] = __float_as_uint(fmaf(__uint_as_float(s[c]), sl2, __ldg(at + c)));
+                mul = 1.f, add = 0.f;
+              }
+            }
             const int cnt = klim - kt * BN;  // visible keys of this row in the block
+            if (MOD == kModRelBias && cnt <= 0) add = 0.f;
             if (cnt < BN) {
 #pragma unroll
               for (int c = 0; c < BN; ++c)
@@ -412,8 +430,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
               for (int z = 0; z < 8; ++z) mp[z] = fmax3(mp[z], __uint_as_float(s[c + z]), __uint_as_float(s[c + 8 + z]));
             const float mx = fmax3(fmax3(mp[0], mp[1], mp[2]), fmax3(mp[3], mp[4], mp[5]), fmaxf(mp[6], mp[7]));
-            const float sl2 = a.scale_log2;
-            const float m_tile = mx * sl2;
+            const float m_tile = MOD == kModRelBias ? fmaf(mx, mul, add) : mx * sl2;
             const bool need = valid && m_tile > m_used + kThreshold;
             float alpha = 1.f;
             if (need) {
@@ -424,7 +441,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             const float mu = (m_used == -INFINITY) ? 0.f : m_used;
             uint32_t pk[BN / 2];
             float2 rs[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-            const float2 sl2v = make_float2(sl2, sl2), negmu = make_float2(-mu, -mu);
+            const float off = MOD == kModRelBias ? add - mu : -mu;
+            const float2 sl2v = MOD == kModRelBias ? make_float2(mul, mul) : make_float2(sl2, sl2), negmu = make_float2(off, off);
 #pragma unroll
             for (int c = 0; c < BN / 2; ++c) {
               const float2 x = ffma2(make_float2(__uint_as_float(s[2 * c]), __uint_as_float(s[2 * c + 1])), sl2v, negmu);
@@ -826,6 +844,10 @@ cudaError_t launch_d(const CUtensorMap& tq, const CUtensorMap& tk, const CUtenso
     case kModAlibi:
       e = even ? launch_main<DQK, DV, kModAlibi, true>(tq, tk, tv, a, ctas, stream)
                : launch_main<DQK, DV, kModAlibi, false>(tq, tk, tv, a, ctas, stream);
+      break;
+    case kModRelBias:
+      e = even ? launch_main<DQK, DV, kModRelBias, true>(tq, tk, tv, a, ctas, stream)
+               : launch_main<DQK, DV, kModRelBias, false>(tq, tk, tv, a, ctas, stream);
       break;
     default: return cudaErrorInvalidValue;
   }

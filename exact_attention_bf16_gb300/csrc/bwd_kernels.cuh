@@ -34,6 +34,7 @@
 #include "bwd_common.cuh"
 #include "kernels.h"
 #include "ptx_sm100.cuh"
+#include "rel_bias.cuh"
 #include "score_mod.cuh"
 
 namespace gb300 {
@@ -429,6 +430,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const float sl2 = a.scale_log2;
     int tt = 0, hq = hq_first;  // step within the query head hq
     float alibi_slope = MOD == kModAlibi ? __ldg(a.alibi_slopes + hq) * a.inv_scale : 0.f;  // raw units
+    RelRow rel{};
+    if constexpr (MOD == kModRelBias) rel = rel_row(a.rel, hq);
     const uint32_t my_cols = C::tS + 32 * wg;     // this warpgroup's S^T columns
     const uint32_t my_pds = C::tPdS + 32 * wg;    // its P^T (16) and dS^T (16) columns
     bool ok = mbar_wait_warp(&bar->kv_full, 0, a.status, 0x1301);
@@ -501,7 +504,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t pw[16], dw[16];
       // ALiBi: slope * (kj - qpos) of this warpgroup's first query column
       const float abase = alibi_slope * static_cast<float>(kj - q0 - 32 * wg - (U.nk - U.nq));
-      auto pair = [&](int e, float2 nl, float2 nd, bool mask) {
+      // relative position bias: the place of this thread's key at its first query column, and where the warp's places
+      // (32 keys, 32 queries) have one bias, that
+      const int r0 = kj - q0 - 32 * wg - (U.nk - U.nq);
+      float radd = 0.f;
+      const bool near = MOD == kModRelBias && !rel_far(rel, r0 - static_cast<int>(lane) - 31, r0 - static_cast<int>(lane) + 31, radd);
+      auto pair = [&](int e, float2 nl, float2 nd, bool mask, bool by_place) {
         const int col = 32 * wg + e;
         float s0 = __uint_as_float(s[e]), s1 = __uint_as_float(s[e + 1]);
         float2 f = make_float2(1.f, 1.f);  // derivative of the score modification
@@ -514,30 +522,37 @@ __global__ void __launch_bounds__(kThreads, 1)
           s0 -= fabsf(fmaf(-alibi_slope, static_cast<float>(e), abase));
           s1 -= fabsf(fmaf(-alibi_slope, static_cast<float>(e + 1), abase));
         }
+        if constexpr (MOD == kModRelBias) {
+          if (by_place) nl = fadd2(nl, make_float2(__ldg(rel.centre + (r0 - e)), __ldg(rel.centre + (r0 - e - 1))));
+          else nl = fadd2(nl, make_float2(radd, radd));
+        }
         const float2 x = ffma2(make_float2(s0, s1), sl2v, nl);
         float2 p = make_float2(ex2_mufu(x.x), ex2_mufu(x.y));
         if (mask) {
-          if (!(key_ok && q0 + col >= i_vis)) p.x = 0.f;
-          if (!(key_ok && q0 + col + 1 >= i_vis)) p.y = 0.f;
+          // (with a bias also the queries past the end: it may be a NaN at places that no query has)
+          const bool in0 = MOD != kModRelBias || q0 + col < U.nq, in1 = MOD != kModRelBias || q0 + col + 1 < U.nq;
+          if (!(key_ok && q0 + col >= i_vis && in0)) p.x = 0.f;
+          if (!(key_ok && q0 + col + 1 >= i_vis && in1)) p.y = 0.f;
         }
         float2 ds = fmul2(p, fadd2(make_float2(__uint_as_float(dp[e]), __uint_as_float(dp[e + 1])), nd));
         if constexpr (MOD == kModSoftcap) ds = fmul2(ds, f);
         pw[e / 2] = pack_bf16x2(p.x, p.y);
         dw[e / 2] = pack_bf16x2(ds.x, ds.y);
       };
-      auto row = [&](bool mask) {
+      auto row = [&](bool mask, bool by_place) {
 #pragma unroll
         for (int e = 0; e < 32; e += 4) {
           const float4 nl = *reinterpret_cast<const float4*>(vL + e);
           const float4 nd = *reinterpret_cast<const float4*>(vD + e);
-          pair(e, make_float2(nl.x, nl.y), make_float2(nd.x, nd.y), mask);
-          pair(e + 2, make_float2(nl.z, nl.w), make_float2(nd.z, nd.w), mask);
+          pair(e, make_float2(nl.x, nl.y), make_float2(nd.x, nd.y), mask, by_place);
+          pair(e + 2, make_float2(nl.z, nl.w), make_float2(nd.z, nd.w), mask, by_place);
         }
       };
       // Queries past the end already give P = 0 through -LSE*log2e = -inf, so only
       // the causal boundary and a key row past the end need the per-element test.
-      if (key_ok && q0 + 32 * wg >= i_vis) row(false);
-      else row(true);
+      if (MOD == kModRelBias && near) row(true, true);
+      else if (key_ok && q0 + 32 * wg >= i_vis && (MOD != kModRelBias || q0 + 32 * wg + 32 <= U.nq)) row(false, false);
+      else row(true, false);
       if (t > 0) {  // dV(t-1), dK(t-1) (and dQ(t-1)) must have read the previous P^T, dS^T
         ok = mbar_wait_warp(&bar->pds_free, static_cast<uint32_t>(t - 1) & 1u, a.status, 0x1305);
         if (!ok) break;
@@ -568,6 +583,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (++tt == T1) {
           tt = 0, ++hq;
           if (MOD == kModAlibi && t + 1 < T) alibi_slope = __ldg(a.alibi_slopes + hq) * a.inv_scale;
+          if (MOD == kModRelBias && t + 1 < T) rel = rel_row(a.rel, hq);
         }
       }
       if constexpr (FUSED) {
@@ -950,6 +966,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const float2 sl2v = make_float2(a.scale_log2, a.scale_log2);
     int tt = 0, hq = hq_first;  // step within the query head hq
     float alibi_slope = MOD == kModAlibi ? __ldg(a.alibi_slopes + hq) * a.inv_scale : 0.f;  // raw units
+    RelRow rel{};
+    if constexpr (MOD == kModRelBias) rel = rel_row(a.rel, hq);
     auto lanes = [&](int lg) { return tbase + ((quarter * 32u + 16u * static_cast<uint32_t>(lg)) << 16); };
     bool ok = true;
     for (int t = 0; t < T && ok; ++t) {
@@ -962,13 +980,26 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_fence_after();
       const float4* vL = reinterpret_cast<const float4*>(sVec + (t % C::NVEC) * 2 * QB + 64 * wg) + c;
       const float4* vD = vL + QB / 4;
-      const bool full = all_keys && q0 >= vis_max;  // every (key, query) cell of this thread is visible
+      // every (key, query) cell of this thread is visible (with a relative position bias, which may be a NaN at places that no
+      // query has: also a query's)
+      const bool full = all_keys && q0 >= vis_max && (MOD != kModRelBias || q0 + 64 <= U.nq);
       float2 nlv[8];  // -LSE*log2e of this thread's 16 queries (the same for both lane groups)
 #pragma unroll
       for (int r = 0; r < 4; ++r) {  // queries 8r + 2c, +1 and 8(r + 4) + 2c, +1 in one 16-byte load
         const float4 x = vL[4 * r];
         nlv[r] = make_float2(x.x, x.y);
         nlv[r + 4] = make_float2(x.z, x.w);
+      }
+      // relative position bias: the place of key row g of lane group 0 at query column 2c; where all places of the warp (32
+      // keys, 64 queries) have one bias, it goes into the queries' offsets
+      const int r0 = k0 + static_cast<int>(quarter) * 32 + g - q0 - 2 * c - (U.nk - U.nq);
+      bool near = false;
+      if constexpr (MOD == kModRelBias) {
+        float add;
+        const int rw = r0 - g + 2 * c;  // the warp's first key at its first query
+        near = !rel_far(rel, rw - 63, rw + 31, add);
+#pragma unroll
+        for (int r = 0; r < 8; ++r) nlv[r] = fadd2(nlv[r], make_float2(add, add));
       }
       float p[2][32];
 #pragma unroll
@@ -1000,8 +1031,16 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             sm[u] = sx;
           }
-          const float2 x0 = ffma2(make_float2(sm[0], sm[1]), sl2v, nl);
-          const float2 x1 = ffma2(make_float2(sm[2], sm[3]), sl2v, nl);
+          float2 nl0 = nl, nl1 = nl;
+          if constexpr (MOD == kModRelBias) {
+            if (near) {
+              const float* at = rel.centre + (r0 + 16 * lg - 8 * r);
+              nl0 = fadd2(nl, make_float2(__ldg(at), __ldg(at - 1)));
+              nl1 = fadd2(nl, make_float2(__ldg(at + 8), __ldg(at + 7)));
+            }
+          }
+          const float2 x0 = ffma2(make_float2(sm[0], sm[1]), sl2v, nl0);
+          const float2 x1 = ffma2(make_float2(sm[2], sm[3]), sl2v, nl1);
           float* pp = &p[lg][4 * r];
           pp[0] = ex2_mufu(x0.x);
           pp[1] = ex2_mufu(x0.y);
@@ -1011,7 +1050,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int u = 0; u < 4; ++u) {
               const int qi = q0 + 8 * r + 2 * c + (u & 1);
-              if (!(kok[lg][u >> 1] && qi >= vis[lg][u >> 1])) pp[u] = 0.f;
+              if (!(kok[lg][u >> 1] && qi >= vis[lg][u >> 1] && (MOD != kModRelBias || qi < U.nq))) pp[u] = 0.f;
             }
           }
           pw[2 * r] = pack_bf16x2(pp[0], pp[1]);
@@ -1067,6 +1106,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (++tt == T1) {
           tt = 0, ++hq;
           if (MOD == kModAlibi && t + 1 < T) alibi_slope = __ldg(a.alibi_slopes + hq) * a.inv_scale;
+          if (MOD == kModRelBias && t + 1 < T) rel = rel_row(a.rel, hq);
         }
       }
     }
@@ -1447,6 +1487,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     const float sl2 = a.scale_log2;
     const float alibi_slope = MOD == kModAlibi ? __ldg(a.alibi_slopes + h) * a.inv_scale : 0.f;  // raw units
+    // relative position bias: its row, the buckets' gradient (bucket lane + 32 k), and the sums of dS beyond the reach
+    RelRow rel{};
+    float bsum[4] = {0.f, 0.f, 0.f, 0.f};
+    float2 fsum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+    bool rows_ok = true;  // every row of the warp has keys
+    if constexpr (MOD == kModRelBias) {
+      rel = rel_row(a.rel, h);
+      rows_ok = __all_sync(0xffffffffu, lse2 != INFINITY);
+    }
     bool ok = mbar_wait_warp(&bar->q_full, 0, a.status, 0x2301);
     // dO rows into TMEM as the A operand of dP, where it fits
     if (ok && wg == 1) {
@@ -1465,8 +1514,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t s[64], dp[64], dw[32];
       // ALiBi: slope * (key - qpos) of this warpgroup's first key column
       const float abase = alibi_slope * static_cast<float>(key_block(t) * KB + wg * 64 - i - (U.nk - U.nq));
+      // the place of this row at this warpgroup's first column; where the warp's places (32 rows, 64 columns) have one bias, that
+      const int r0 = key_block(t) * KB + wg * 64 - i - (U.nk - U.nq), r00 = r0 + static_cast<int>(lane);
+      float radd = 0.f;
+      const bool near = MOD == kModRelBias && !rel_far(rel, r00 - 31, r00 + 63, radd);
+      const float2 nla = make_float2(radd - lse2, radd - lse2);
       // P of columns e, e + 1 (zero where masked) and the score modification's derivative f there
-      auto prob2 = [&](int e, bool mask, float2& f) -> float2 {
+      auto prob2 = [&](int e, bool mask, float2& f, bool by_place) -> float2 {
         const int col = wg * 64 + e;
         float s0 = __uint_as_float(s[e]), s1 = __uint_as_float(s[e + 1]);
         f = make_float2(1.f, 1.f);
@@ -1479,13 +1533,24 @@ __global__ void __launch_bounds__(kThreads, 1)
           s0 -= fabsf(fmaf(alibi_slope, static_cast<float>(e), abase));
           s1 -= fabsf(fmaf(alibi_slope, static_cast<float>(e + 1), abase));
         }
-        const float2 x = ffma2(make_float2(s0, s1), sl2v, nl);
+        float2 off = nl;
+        if constexpr (MOD == kModRelBias)
+          off = by_place ? fadd2(nl, make_float2(__ldg(rel.centre + (r0 + e)), __ldg(rel.centre + (r0 + e + 1)))) : nla;
+        const float2 x = ffma2(make_float2(s0, s1), sl2v, off);
         float2 p = make_float2(ex2_mufu(x.x), ex2_mufu(x.y));
         if (mask) {
           if (col >= cnt) p.x = 0.f;
           if (col + 1 >= cnt) p.y = 0.f;
         }
         return p;
+      };
+      // dS in fp32 for the bias's gradient: in place of S, or (one bucket) added up
+      const bool right = r00 - 31 >= rel.reach;
+      float2 tsum = make_float2(0.f, 0.f);
+      auto keep_ds = [&](int e, const float2& ds) {
+        s[e] = __float_as_uint(ds.x);
+        s[e + 1] = __float_as_uint(ds.y);
+        tsum = fadd2(tsum, ds);
       };
       const bool full = cnt >= wg * 64 + 64;  // every key of this warpgroup's half is visible
       if constexpr (C::SPLIT_SDP) {
@@ -1497,18 +1562,19 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(&bar->s_free);
         // P times f, in place of S, while dP(t) runs
-        auto prob = [&](bool mask) {
+        auto prob = [&](bool mask, bool by_place) {
 #pragma unroll
           for (int e = 0; e < 64; e += 2) {
             float2 f;
-            float2 p = prob2(e, mask, f);
+            float2 p = prob2(e, mask, f, by_place);
             if constexpr (MOD == kModSoftcap) p = fmul2(p, f);
             s[e] = __float_as_uint(p.x);
             s[e + 1] = __float_as_uint(p.y);
           }
         };
-        if (full) prob(false);
-        else prob(true);
+        if (MOD == kModRelBias && near) prob(true, true);
+        else if (full) prob(false, false);
+        else prob(true, false);
         ok = mbar_wait_warp(&bar->dp_full, static_cast<uint32_t>(t) & 1u, a.status, 0x2302);
         if (!ok) break;
         tc_fence_after();
@@ -1523,6 +1589,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const float2 ds = fmul2(make_float2(__uint_as_float(s[e]), __uint_as_float(s[e + 1])),
                                   fadd2(make_float2(__uint_as_float(dp[e]), __uint_as_float(dp[e + 1])), nd));
           dw[e / 2] = pack_bf16x2(ds.x, ds.y);
+          if constexpr (MOD == kModRelBias) keep_ds(e, ds);
         }
       } else {
         // this warpgroup's 64 columns of S and dP out of TMEM, then both released
@@ -1534,18 +1601,20 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&bar->sp_free);
-        auto row = [&](bool mask) {  // dS = P (dP - D) f
+        auto row = [&](bool mask, bool by_place) {  // dS = P (dP - D) f
 #pragma unroll
           for (int e = 0; e < 64; e += 2) {
             float2 f;
-            const float2 p = prob2(e, mask, f);
+            const float2 p = prob2(e, mask, f, by_place);
             float2 ds = fmul2(p, fadd2(make_float2(__uint_as_float(dp[e]), __uint_as_float(dp[e + 1])), nd));
             if constexpr (MOD == kModSoftcap) ds = fmul2(ds, f);
             dw[e / 2] = pack_bf16x2(ds.x, ds.y);
+            if constexpr (MOD == kModRelBias) keep_ds(e, ds);
           }
         };
-        if (full) row(false);
-        else row(true);
+        if (MOD == kModRelBias && near) row(true, true);
+        else if (full) row(false, false);
+        else row(true, false);
       }
       if (t > 0) {  // dQ(t-1) must have read the previous dS
         ok = mbar_wait_warp(&bar->ds_free, static_cast<uint32_t>(t - 1) & 1u, a.status, 0x2305);
@@ -1557,6 +1626,45 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&bar->ds_full);
+      if constexpr (MOD == kModRelBias) {  // while the tensor core takes dS
+        if (!near) {
+          if (right) fsum[1] = fadd2(fsum[1], tsum);
+          else fsum[0] = fadd2(fsum[0], tsum);
+        } else if (a.rel.parts != nullptr) {
+          float x[64], diag[3];
+#pragma unroll
+          for (int e = 0; e < 64; ++e) x[e] = __uint_as_float(s[e]);
+          if (!rows_ok) {  // rows without keys, and those past the end: 0 x NaN
+#pragma unroll
+            for (int e = 0; e < 64; ++e) x[e] = lse2 != INFINITY ? x[e] : 0.f;
+          }
+          diagonal_sums(x, diag);
+          bucket_sums(a.rel, diag, r00, bsum);
+        }
+      }
+    }
+    if constexpr (MOD == kModRelBias) {
+      if (a.rel.parts != nullptr) {
+        const int64_t place = a.cu_q != nullptr ? static_cast<int64_t>(U.q_start) / MB + U.unit + m
+                                                : (static_cast<int64_t>(U.b) * a.n_qblk + m) * (split ? a.dq_split : 1) + range;
+        const bool alive = lse2 != INFINITY;
+#pragma unroll
+        for (int z = 0; z < 2; ++z) {
+          float x = alive ? fsum[z].x + fsum[z].y : 0.f;
+#pragma unroll
+          for (int d = 16; d > 0; d >>= 1) x += __shfl_xor_sync(0xffffffffu, x, d);
+          const int id = __ldg(a.rel.bucket + kRelPad + (z == 0 ? 0 : 2 * a.rel.reach));
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            if (id == static_cast<int>(lane) + 32 * k) bsum[k] += x;
+        }
+        if (place >= 0 && 8 * place + 8 <= a.rel.part_rows) {
+          float* dst = a.rel.parts + ((static_cast<int64_t>(h) * a.rel.part_rows) + 8 * place + warp) * a.rel.buckets;
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            if (static_cast<int>(lane) + 32 * k < a.rel.buckets) dst[lane + 32 * k] = bsum[k];
+        }
+      }
     }
     if (ok && T > 0) {
       ok = mbar_wait_warp(&bar->acc_full, 0, a.status, 0x2310);

@@ -42,6 +42,7 @@
 #include "exp2_emu.cuh"
 #include "kernels.h"
 #include "ptx_sm100.cuh"
+#include "rel_bias.cuh"
 #include "score_mod.cuh"
 
 namespace gb300 {
@@ -471,6 +472,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int klim = key_limit(row, nq, nk, a.causal) - (SPLITKV ? kb_lo * BN : 0);
     const float alibi_slope = MOD == kModAlibi ? __ldg(a.alibi_slopes + h) * a.inv_scale : 0.f;  // raw units
     const int qpos = row + (nk - nq);  // the row's position among the keys (bottom-right aligned)
+    RelRow rel{};
+    if constexpr (MOD == kModRelBias) rel = rel_row(a.rel, h);
     const uint32_t lane_base = tbase + ((quarter * 32u) << 16);
     const float sl2 = a.scale_log2;
     const bool f16 = v_is_f16(a);  // P packed as fp16 (V's copy) or bf16
@@ -500,7 +503,20 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int c = 0; c < BN; ++c)
           s[c] = __float_as_uint(__uint_as_float(s[c]) - fabsf(fmaf(alibi_slope, static_cast<float>(c), base)));
       }
+      // relative position bias: logits in log2 units, s * mul + add, where the tile's bias is one number per warp; else
+      // taken so here, and mul = 1 (kb * BN - qpos: this row's place of column 0; a warp's rows are 32 in a row)
+      float mul = sl2, add = 0.f;
+      if constexpr (MOD == kModRelBias) {
+        const int r0 = kb * BN - qpos, r_top = r0 + static_cast<int>(lane);
+        if (!rel_far(rel, r_top - 31, r_top + BN - 1, add)) {
+          const float* at = rel.centre + r0;
+#pragma unroll
+          for (int c = 0; c < BN; ++c) s[c] = __float_as_uint(fmaf(__uint_as_float(s[c]), sl2, __ldg(at + c)));
+          mul = 1.f;
+        }
+      }
       const int cnt = klim - kb * BN;  // visible keys of this row inside the tile
+      if (MOD == kModRelBias && cnt <= 0) add = 0.f;  // (whatever the bias of places that no key is visible at)
       if (cnt < BN) {
 #pragma unroll
         for (int c = 0; c < BN; ++c)
@@ -515,7 +531,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int z = 0; z < 8; ++z) mp[z] = fmax3(mp[z], __uint_as_float(s[c + z]), __uint_as_float(s[c + 8 + z]));
       const float mx = fmax3(fmax3(mp[0], mp[1], mp[2]), fmax3(mp[3], mp[4], mp[5]), fmaxf(mp[6], mp[7]));
-      const float m_tile = mx * sl2;
+      const float m_tile = MOD == kModRelBias ? fmaf(mx, mul, add) : mx * sl2;
       const bool need = m_tile > m_used + kThreshold;
       float alpha = 1.f;
       if (need) {
@@ -531,7 +547,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       // p = 2^(s * scale * log2e - m_used), packed to fp16 (or bf16) pairs in place
       uint32_t pk[BN / 2];
       float2 rs[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};  // partial row sums (packed pairs)
-      const float2 sl2v = make_float2(sl2, sl2), negmu = make_float2(-mu, -mu);
+      const float off = MOD == kModRelBias ? add - mu : -mu;
+      const float2 sl2v = MOD == kModRelBias ? make_float2(mul, mul) : make_float2(sl2, sl2), negmu = make_float2(off, off);
       auto exp_row = [&](auto f16_tag) {
         constexpr bool F16 = decltype(f16_tag)::value;
 #pragma unroll

@@ -144,6 +144,29 @@ struct SeqMaps {
 cudaError_t launch_tile_lists(const int* cu_q, const int* cu_k, int num_seqs, const TileListSpec* specs, int n,
                               int64_t* scratch, uint32_t* zero_word, const SeqMaps& maps, cudaStream_t stream);
 
+// Relative position bias (rel_bias.cuh). The caller's table and its buckets: bucket k of a side holds the distances from
+// start[k] on, up to start[k + 1] or without end.
+constexpr int kRelPad = 256;  // places a tile of 128 x 128 can reach past the row's bounds
+constexpr int kRelMaxBuckets = 128;
+struct RelTable {
+  const void* table;  // [buckets, heads], bf16 or fp32
+  int f32, heads, buckets, side, two_sided, reach;
+  int start[kRelMaxBuckets];
+};
+// Laid out by place, and for the gradient each place's bucket, each bucket's first and last place, and the parts' room:
+// [heads][part_rows][buckets], eight rows (one per softmax warp) per CTA of the dQ kernel.
+struct RelBias {
+  const float* by_place;
+  const uint8_t* bucket;
+  const int2* range;
+  float* parts;
+  int64_t part_rows;
+  int reach, buckets;
+};
+// zero: n_zero floats to clear along the way (a multiple of 4, 16-byte aligned).
+cudaError_t launch_rel_layout(const RelTable& t, const RelBias& b, float* zero, int64_t n_zero, cudaStream_t stream);
+cudaError_t launch_rel_sum(const float* parts, int64_t rows, int buckets, int heads, void* out, int f32, cudaStream_t stream);
+
 // Forward kernel arguments (passed by value; tensor maps go separately as
 // __grid_constant__ parameters).
 struct FwdArgs {
@@ -203,6 +226,7 @@ struct FwdArgs {
   uint64_t kv_inv;
   // Packed variable-length only (or nullptr): sequence s's maps of V (2 s) and of its fp16 copy (2 s + 1), SeqMaps.
   const CUtensorMap* seq_maps;
+  RelBias rel;  // score_mod kModRelBias
 };
 
 cudaError_t launch_fwd(int d_qk, int d_v, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
@@ -218,8 +242,10 @@ cudaError_t launch_fwd_e4m3(const CUtensorMap& tq, const CUtensorMap& tk, const 
 cudaError_t launch_v_e4m3_to_f16(const void* v, int64_t sb, int64_t sn, int64_t sh, int nb, int nrows, int heads,
                                  int dv, void* out, cudaStream_t stream);
 // The forward with a score modification (a.score_mod != 0, emu_period 0):
-// dense, tile list (a.tiles) or block-sparse (a.kv_count), by the arguments.
+// dense, tile list (a.tiles) or (not kModRelBias) block-sparse (a.kv_count), by the arguments.
 cudaError_t launch_fwd_mod(int d_qk, int d_v, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
+                           const CUtensorMap& tv16, const FwdArgs& a, cudaStream_t stream);
+cudaError_t launch_fwd_rel(int d_qk, int d_v, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                            const CUtensorMap& tv16, const FwdArgs& a, cudaStream_t stream);
 
 // fp16 copy of V (contiguous [nb, nrows, heads, dv]) for the forward's PV
@@ -326,6 +352,7 @@ struct BwdArgs {
   // SeqMapBwd (SeqMaps).
   const CUtensorMap* seq_maps;
   int n_seq_maps;
+  RelBias rel;  // score_mod kModRelBias
 };
 // Q and dO as the dK/dV kernels copy them, K and V, and (the two-SM kernel) Q and dO with 64-row boxes.
 enum SeqMapBwd : int { kMapQ = 0, kMapDO, kMapK, kMapV, kMapQr, kMapDOr };
@@ -356,6 +383,11 @@ cudaError_t launch_bwd_dkdv(int d_qk, int d_v, const CUtensorMap& tq, const CUte
 cudaError_t launch_bwd_dkdv_mod(int d_qk, int d_v, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                                 const CUtensorMap& tdo, const BwdArgs& a, cudaStream_t stream);
 cudaError_t launch_bwd_dq_mod(int d_qk, int d_v, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
+                              const CUtensorMap& tdo, const BwdArgs& a, cudaStream_t stream);
+// with a relative position bias
+cudaError_t launch_bwd_dkdv_rel(int d_qk, int d_v, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
+                                const CUtensorMap& tdo, const BwdArgs& a, cudaStream_t stream);
+cudaError_t launch_bwd_dq_rel(int d_qk, int d_v, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                               const CUtensorMap& tdo, const BwdArgs& a, cudaStream_t stream);
 // dK, dV for d_qk = d_v = 128 over CTA pairs (dense or varlen, no block
 // lists): maps q and dO with 64-row boxes (_r) and 128-row boxes (_c), k, v.
@@ -468,6 +500,7 @@ struct PagedArgs {
   int score_mod;  // as in FwdArgs
   float mod_k2, mod_b, inv_scale;
   const float* alibi_slopes;
+  RelBias rel;
   int tile_tokens;   // tokens of a 128-row tile: 128 / kv_group
   int q_box_tokens;  // tokens of a box of the q map
   // partial results, 2 * ctas slots of part_rows rows: fp32 O normalised over its keys, LSE in log2 units

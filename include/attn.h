@@ -65,7 +65,7 @@
 extern "C" {
 #endif
 
-#define ATTN_ABI_VERSION 8
+#define ATTN_ABI_VERSION 9
 
 typedef enum {
   ATTN_OK = 0,
@@ -80,8 +80,15 @@ typedef enum {
 typedef enum {
   ATTN_SCORE_NONE = 0,
   ATTN_SCORE_SOFTCAP = 1,  /* a' = softcap * tanh(a / softcap) */
-  ATTN_SCORE_ALIBI = 2     /* a' = a - m_h * |j - (i + Nk - Nq)| */
+  ATTN_SCORE_ALIBI = 2,    /* a' = a - m_h * |j - (i + Nk - Nq)| */
+  ATTN_SCORE_RELBIAS = 3   /* a' = a + rel_bias[bucket(j - (i + Nk - Nq))][h] */
 } attn_score_mod_t;
+
+/* Element type of a learned table (attn_fwd_params.rel_bias_dtype). */
+typedef enum {
+  ATTN_TABLE_BF16 = 0,
+  ATTN_TABLE_F32 = 1
+} attn_table_dtype_t;
 
 /* Element type of q, k, v (attn_fwd_params.input_dtype). */
 typedef enum {
@@ -202,6 +209,28 @@ typedef struct attn_fwd_params {
    * the block-sparse pair, the diagnostic and 65536 or more heads give
    * ATTN_ERR_UNSUPPORTED. */
   int32_t heads_kv;
+  /* Learned relative position bias (ATTN_SCORE_RELBIAS; ignored otherwise): a device
+   * table [rel_buckets, heads], contiguous, of bf16 or fp32 (rel_bias_dtype,
+   * attn_table_dtype_t) on q's GPU. The scaled logit of query i and key j gets
+   * rel_bias[bucket(j - (i + Nk - Nq))][h], i and j counted within the sequence and
+   * the query's position aligned to the last key, like the causal mask. Buckets of a
+   * relative position r: with rel_bidirectional != 0 (rel_buckets even) each side has
+   * n_b = rel_buckets / 2, keys behind the query (r > 0) the upper half, and the
+   * distance is |r|; otherwise n_b = rel_buckets and the distance max(-r, 0). With
+   * m = n_b / 2 (integer), a distance n < m is bucket n, a longer one
+   *   min(n_b - 1, m + floor((n_b - m) log(n / m) / log(rel_max_distance / m))),
+   * borders that fall on a whole distance decided exactly; n_b = 1 is one bucket for
+   * all. rel_buckets is 1 to 128, rel_max_distance m + 1 to 65536 (else
+   * ATTN_ERR_INVALID_ARG). An entry of -inf masks its bucket; a row left without keys
+   * by that has O = 0, LSE = -inf and dQ = 0. The bias works with the dense and the
+   * variable-length forward and backward and attn_fwd_paged, with shared K/V heads;
+   * the block-sparse pair gives ATTN_ERR_UNSUPPORTED. The workspaces then hold, in
+   * addition, the bias by distance, and in the backward its gradient's partial sums. */
+  const void* rel_bias;
+  int32_t rel_bias_dtype;
+  int32_t rel_buckets;
+  int32_t rel_max_distance;
+  int32_t rel_bidirectional;
 } attn_fwd_params;
 
 /* Backward parameters. `fwd` holds q, k, v, the forward's outputs o and lse
@@ -253,6 +282,12 @@ typedef struct attn_bwd_params {
    * 4 x heads x query rows x 64 bytes for the fp32 dQ and, deterministic
    * only, 4 x (batch or num_seqs) x heads x ceil(max query length / 64). */
   int32_t single_pass;
+  /* Optional (may be NULL), ATTN_SCORE_RELBIAS only: the gradient of rel_bias, written
+   * [rel_buckets, heads] in its type: the sums of dS over the (query, key) pairs of each
+   * bucket and all sequences, added in fp32 in a fixed order and rounded once (buckets
+   * that no pair falls in get 0). Its accuracy is that of dS, whose D comes from O
+   * rounded to bf16. */
+  void* drel_bias;
 } attn_bwd_params;
 
 /* Bytes of device workspace the matching call needs (0 means none: pass NULL).
@@ -587,6 +622,11 @@ typedef struct attn_paged_params {
   int32_t score_mod;
   float softcap;
   const float* alibi_slopes;
+  const void* rel_bias; /* as in attn_fwd_params */
+  int32_t rel_bias_dtype;
+  int32_t rel_buckets;
+  int32_t rel_max_distance;
+  int32_t rel_bidirectional;
 } attn_paged_params;
 size_t attn_fwd_paged_workspace_size(const attn_paged_params* p);
 attn_status_t attn_fwd_paged(const attn_paged_params* p, void* workspace, size_t workspace_bytes,

@@ -225,6 +225,7 @@ attn_status_t check_rel(const P* p) {
   if (p->rel_buckets < 1 || p->rel_buckets > kRelMaxBuckets || (p->rel_bidirectional && p->rel_buckets % 2))
     return ATTN_ERR_INVALID_ARG;
   const int side = p->rel_bidirectional ? p->rel_buckets / 2 : p->rel_buckets;
+  if (!std::isfinite(1.f / p->softmax_scale)) return ATTN_ERR_INVALID_ARG;  // the bias is taken over the scale
   return p->rel_max_distance > side / 2 && p->rel_max_distance <= 65536 ? ATTN_OK : ATTN_ERR_INVALID_ARG;
 }
 
@@ -239,6 +240,7 @@ RelPlan rel_plan(const P* p, int64_t longest) {
   if (p->score_mod != ATTN_SCORE_RELBIAS || p->heads < 1 || check_rel(p) != ATTN_OK) return r;
   RelTable& t = r.table;
   t.table = p->rel_bias;
+  t.inv_scale = 1.f / p->softmax_scale;
   t.f32 = p->rel_bias_dtype == ATTN_TABLE_F32;
   t.heads = p->heads;
   t.buckets = p->rel_buckets;
@@ -564,12 +566,17 @@ attn_status_t run_fwd(const attn_fwd_params* p, bool varlen, cudaStream_t stream
   ATTN_TRY(make_map(&tv16, v16, p->d_v, hkv, nk_rows, nb, v16_rows * hkv * p->d_v,
                     static_cast<int64_t>(hkv) * p->d_v, p->d_v, 128));
   const ListPlan lp = fwd_list_plan(p, varlen);
-  if (p->score_mod == ATTN_SCORE_RELBIAS) {  // ahead of the lists, whose kernel others run beside
+  // the bias by place, beside which the lists are built and V is copied
+  const bool rel = p->score_mod == ATTN_SCORE_RELBIAS;
+  auto lay_out_bias = [&]() -> cudaError_t {
     const RelPlan rp = call_rel_plan(p, varlen);
     a.rel.by_place = reinterpret_cast<const float*>(static_cast<uint8_t*>(ws) + need_ws - rp.place_bytes);
     a.rel.reach = rp.table.reach;
     a.rel.buckets = rp.table.buckets;
-    e = launch_rel_layout(rp.table, a.rel, nullptr, 0, stream);
+    return launch_rel_layout(rp.table, a.rel, nullptr, 0, stream);
+  };
+  if (rel && lp.use) {
+    e = lay_out_bias();
     if (e != cudaSuccess) return cuda_fail(e, "bias layout");
   }
   SeqMaps maps{};
@@ -586,21 +593,22 @@ attn_status_t run_fwd(const attn_fwd_params* p, bool varlen, cudaStream_t stream
     TileEntry* list = reinterpret_cast<TileEntry*>(lbase);
     const TileListSpec spec{p->heads, 256, 0, 1, lp.max_nblk, list, lp.bound};
     e = launch_tile_lists(p->cu_seqlens_q, p->cu_seqlens_k, p->num_seqs, &spec, 1,
-                          reinterpret_cast<int64_t*>(lbase + lp.list_bytes), flag, maps, stream);
+                          reinterpret_cast<int64_t*>(lbase + lp.list_bytes), flag, maps, rel, stream);
     if (e != cudaSuccess) return cuda_fail(e, "fwd tile list");
     a.tiles = list;
     a.n_tiles = lp.bound;
   } else {
     e = cudaMemsetAsync(flag, 0, sizeof(uint32_t), stream);
     if (e == cudaSuccess && maps.n > 0)
-      e = launch_tile_lists(p->cu_seqlens_q, p->cu_seqlens_k, p->num_seqs, nullptr, 0, nullptr, nullptr, maps, stream);
+      e = launch_tile_lists(p->cu_seqlens_q, p->cu_seqlens_k, p->num_seqs, nullptr, 0, nullptr, nullptr, maps, false, stream);
+    if (e == cudaSuccess && rel) e = lay_out_bias();
   }
   if (e == cudaSuccess && f8)  // exact: every E4M3 value is an fp16 value, the flag stays 0
     e = launch_v_e4m3_to_f16(p->v, varlen ? 0 : p->v_batch_stride, p->v_row_stride, p->v_head_stride, nb, nk_rows,
                              hkv, p->d_v, v16, stream);
   else if (e == cudaSuccess)
     e = launch_v_to_f16(p->v, varlen ? 0 : p->v_batch_stride, p->v_row_stride, p->v_head_stride, nb, nk_rows,
-                        hkv, p->d_v, v16, flag, varlen ? p->cu_seqlens_k + p->num_seqs : nullptr, lp.use, stream);
+                        hkv, p->d_v, v16, flag, varlen ? p->cu_seqlens_k + p->num_seqs : nullptr, lp.use || rel, stream);
   if (e != cudaSuccess) return cuda_fail(e, "fwd V conversion");
   a.v16_flag = flag;
   const SplitPlan spl = (sp.kv_count || p->cta_pair || f8) ? SplitPlan{} : fwd_split_plan(p, varlen);
@@ -717,11 +725,11 @@ size_t bwd_dkv_split_bytes(const attn_bwd_params* p, bool varlen, int split) {
   const int64_t rows = varlen ? f.total_k : static_cast<int64_t>(f.batch) * f.seqlen_k;
   return round256(split * rows * kv_heads(&f) * (f.d_qk + f.d_v) * 4);
 }
-// The bias's layout and its gradient's parts: eight rows of buckets per head and CTA of the dQ kernel.
+// The bias's layout and its gradient's parts: a row of buckets per head and CTA of the dQ kernel.
 int64_t bwd_rel_part_rows(const attn_bwd_params* p, bool varlen, int splits) {
   const attn_fwd_params& f = p->fwd;
-  if (varlen) return 8 * (static_cast<int64_t>(f.total_q) / 128 + f.num_seqs);
-  return 8 * static_cast<int64_t>(f.batch) * ((static_cast<int64_t>(f.seqlen_q) + 127) / 128) * splits;
+  if (varlen) return static_cast<int64_t>(f.total_q) / 128 + f.num_seqs;
+  return static_cast<int64_t>(f.batch) * ((static_cast<int64_t>(f.seqlen_q) + 127) / 128) * splits;
 }
 size_t bwd_rel_bytes(const attn_bwd_params* p, bool varlen) {
   const attn_fwd_params& f = p->fwd;
@@ -898,11 +906,14 @@ attn_status_t run_bwd(const attn_bwd_params* p, void* ws, size_t ws_bytes, bool 
     a.rel.range = reinterpret_cast<const int2*>(at + rp.place_bytes + rp.bucket_bytes);
     a.rel.reach = rp.table.reach;
     a.rel.buckets = rp.table.buckets;
+    a.rel.left = rp.table.side - 1;
+    a.rel.right = rp.table.two_sided ? rp.table.buckets - 1 : 0;
     if (p->drel_bias) {
       a.rel.parts = reinterpret_cast<float*>(at + rp.place_bytes + rp.bucket_bytes + rp.range_bytes);
       a.rel.part_rows = bwd_rel_part_rows(p, varlen, dqs.splits);
     }
-    const int64_t n_parts = varlen ? f.heads * a.rel.part_rows * f.rel_buckets : 0;  // (dense: every CTA writes its own)
+    // (dense: every CTA writes its own)
+    const int64_t n_parts = varlen ? (f.heads * a.rel.part_rows * f.rel_buckets + 3) / 4 * 4 : 0;
     e = launch_rel_layout(rp.table, a.rel, a.rel.parts, n_parts, stream);
     if (e != cudaSuccess) return cuda_fail(e, "bias layout");
   }
@@ -945,7 +956,7 @@ attn_status_t run_bwd(const attn_bwd_params* p, void* ws, size_t ws_bytes, bool 
       a.n_seq_maps = maps.n;
     }
     if (n > 0 || maps.n > 0) {
-      e = launch_tile_lists(f.cu_seqlens_q, f.cu_seqlens_k, f.num_seqs, specs, n, scratch, nullptr, maps, stream);
+      e = launch_tile_lists(f.cu_seqlens_q, f.cu_seqlens_k, f.num_seqs, specs, n, scratch, nullptr, maps, rel, stream);
       if (e != cudaSuccess) return cuda_fail(e, "bwd tile lists");
     }
   }
@@ -959,7 +970,8 @@ attn_status_t run_bwd(const attn_bwd_params* p, void* ws, size_t ws_bytes, bool 
   auto mark = [&](int i) -> cudaError_t {
     return p->phase_events[i] ? cudaEventRecord(static_cast<cudaEvent_t>(p->phase_events[i]), stream) : cudaSuccess;
   };
-  const bool lists = a.tiles_kv != nullptr || a.tiles_q != nullptr;
+  // behind kernels that the D pass runs beside: the lists', or alone the bias's layout
+  const bool lists = a.tiles_kv != nullptr || a.tiles_q != nullptr || rel;
   auto bf = [](const void* x) { return static_cast<const __nv_bfloat16*>(x); };
   FewKeys few{bf(f.q), bf(f.k), bf(f.v), f.q_batch_stride, f.q_row_stride, f.q_head_stride, f.k_batch_stride, f.k_row_stride,
               f.k_head_stride, f.v_batch_stride, f.v_row_stride, f.v_head_stride, f.d_qk, f.d_v};
@@ -1305,7 +1317,8 @@ PagedPlan paged_plan(const attn_paged_params* p) {
   pl.tile_tokens = 128 / group;
   pl.even = p->max_seqlen_q <= pl.tile_tokens;  // one tile of rows holds any request's queries
   // few rows per request and K/V head: rows in the columns of the products (attn_paged_decode.cu, where both are measured)
-  pl.decode = p->score_mod == ATTN_SCORE_NONE && static_cast<int64_t>(p->max_seqlen_q) * group <= kDecodeRows;
+  pl.decode = (p->score_mod == ATTN_SCORE_NONE || p->score_mod == ATTN_SCORE_RELBIAS) &&
+              static_cast<int64_t>(p->max_seqlen_q) * group <= kDecodeRows;
   pl.q_box_tokens = (pl.decode ? kDecodeRows : 128) / group;
   pl.part_rows = pl.decode ? kDecodeRows : pl.even ? 128 : 256;
   const int64_t rows = 2ll * kPagedMaxCtas * pl.part_rows;

@@ -46,9 +46,8 @@ __device__ __forceinline__ float few_keys_d(const BwdArgs& a, const FewKeys& t, 
     for (int d = 4; d > 0; d >>= 1) x += __shfl_xor_sync(0xffffffffu, x, d);
     if (a.score_mod == kModSoftcap) x = a.mod_b * tanh_scaled(x, a.mod_k2);
     if (a.score_mod == kModAlibi) x -= fabsf(a.alibi_slopes[h] * a.inv_scale * static_cast<float>(j - pos));
-    float bias = 0.f;  // log2 units
-    if (a.score_mod == kModRelBias && j < keys) bias = rel_row(a.rel, h).centre[max(-a.rel.reach, min(a.rel.reach, j - pos))];
-    if (j < keys) acc = fmaf(exp2f(fmaf(x, a.scale_log2, bias - lse * 1.4426950408889634f)), y, acc);
+    if (a.score_mod == kModRelBias && j < keys) x += RelRow<kRelPad>{a.rel, 0, h}.one(max(-a.rel.reach, min(a.rel.reach, j - pos)));
+    if (j < keys) acc = fmaf(exp2f(fmaf(x, a.scale_log2, -lse * 1.4426950408889634f)), y, acc);
   }
 #pragma unroll
   for (int d = 4; d > 0; d >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, d);
@@ -65,6 +64,7 @@ __device__ __forceinline__ bool few_keys(const BwdArgs& a, const Unit& U) {
 // rows shared by the blocks along y.
 __global__ void __launch_bounds__(256) few_keys_dsum_kernel(const BwdArgs a, const FewKeys t) {
   const int l = static_cast<int>(threadIdx.x & 7u);
+  if (a.score_mod == kModRelBias) asm volatile("griddepcontrol.wait;" ::: "memory");  // the bias's layout
   for (int unit = static_cast<int>(blockIdx.x); unit < a.num_units; unit += static_cast<int>(gridDim.x)) {
     const Unit U = unit_bounds(a, unit);
     if (!few_keys(a, U)) continue;
@@ -162,6 +162,7 @@ __global__ void __launch_bounds__(256, PACKED ? kPackedBlocks : 8) preprocess_ke
     }
   }
   if constexpr (PACKED) {
+    if (a.score_mod == kModRelBias) asm volatile("griddepcontrol.wait;" ::: "memory");  // the bias's layout
     __syncthreads();  // the D above are written
     const int first = static_cast<int>(begin / a.heads), last = static_cast<int>((rows - 1) / a.heads);  // tokens
     int unit = 0;  // the last sequence that begins at or before `first`
@@ -257,6 +258,7 @@ cudaError_t launch_bwd_preprocess(int d_v, const BwdArgs& a, const FewKeys& t, b
   }
   const unsigned blocks = static_cast<unsigned>(passes < 16384 ? passes : 16384);
   auto kern = d_v == 64 ? bwd::preprocess_kernel<64, false> : bwd::preprocess_kernel<128, false>;
+  if (early) return launch_early(kern, dim3(blocks), 256, 0, stream, a, t, int64_t{0});
   kern<<<blocks, 256, 0, stream>>>(a, t, int64_t{0});
   return cudaGetLastError();
 }

@@ -142,8 +142,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_after();
   const uint32_t tbase = bar->tmem_base;
   // merge_kernel may be launched (its blocks fit only as these CTAs leave), and this kernel's own
-  // reads of chunk_list_kernel's list begin
-  if constexpr (!EVEN) asm volatile("griddepcontrol.wait;" ::: "memory");
+  // reads of chunk_list_kernel's list, and of the relative position bias's layout, begin
+  if constexpr (!EVEN || MOD == kModRelBias) asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
   if (warp < 4) {
@@ -347,8 +347,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (MOD == kModAlibi && valid)
           slope = fabsf(__ldg(a.alibi_slopes + w.hk * a.kv_group + static_cast<int>(quarter * 32 + lane) % a.kv_group) *
                         a.inv_scale);
-        RelRow rel{};
-        if constexpr (MOD == kModRelBias) rel = rel_row(a.rel, w.hk * a.kv_group + static_cast<int>(quarter * 32 + lane) % a.kv_group);
+        const RelRow<kRelPad> rel{a.rel, 0, MOD == kModRelBias ? w.hk * a.kv_group + static_cast<int>(quarter * 32 + lane) % a.kv_group : 0};
         // whether this lane's page of key block kt holds keys (one lane per page of a block)
         auto page_ok = [&](int kt) -> bool {
           const int np = a.page_size < BN ? BN >> a.page_shift : 1;
@@ -393,18 +392,20 @@ __global__ void __launch_bounds__(kThreads, 1)
                 s[c] = __float_as_uint(__uint_as_float(s[c]) - fabsf(fmaf(slope, static_cast<float>(c), base)));
             }
             const float sl2 = a.scale_log2;
-            // relative position bias: logits in log2 units, s * mul + add, where each row's bias is one number; else taken so
-            // here, and mul = 1 (a warp's tokens are at most 32 in a row; rows without one take any places)
-            float mul = sl2, add = 0.f;
+            // relative position bias: one number per row, which goes into the softmax's offsets (add, log2 units), or a number per
+            // logit (a warp's tokens are at most 32 in a row; rows without one take any places)
+            float add = 0.f;
             if constexpr (MOD == kModRelBias) {
               const int r0 = valid ? kt * BN - pos : 0;
-              const bool far = rel_far(rel, r0, r0 + BN - 1, add) || !valid;
+              const bool far = rel.far(r0, r0 + BN - 1, add) || !valid;
               if (!__all_sync(0xffffffffu, far)) {
-                const float* at = rel.centre + r0;
+                rel.at(r0, [&](auto bias) {
 #pragma unroll
-                for (int c = 0; c < BN; ++c) s[c] = __float_as_uint(fmaf(__uint_as_float(s[c]), sl2, __ldg(at + c)));
-                mul = 1.f, add = 0.f;
+                  for (int c = 0; c < BN; ++c) s[c] = __float_as_uint(__uint_as_float(s[c]) + bias(c));
+                });
+                add = 0.f;
               }
+              add *= sl2;
             }
             const int cnt = klim - kt * BN;  // visible keys of this row in the block
             if (MOD == kModRelBias && cnt <= 0) add = 0.f;
@@ -430,7 +431,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
               for (int z = 0; z < 8; ++z) mp[z] = fmax3(mp[z], __uint_as_float(s[c + z]), __uint_as_float(s[c + 8 + z]));
             const float mx = fmax3(fmax3(mp[0], mp[1], mp[2]), fmax3(mp[3], mp[4], mp[5]), fmaxf(mp[6], mp[7]));
-            const float m_tile = MOD == kModRelBias ? fmaf(mx, mul, add) : mx * sl2;
+            const float m_tile = MOD == kModRelBias ? fmaf(mx, sl2, add) : mx * sl2;
             const bool need = valid && m_tile > m_used + kThreshold;
             float alpha = 1.f;
             if (need) {
@@ -442,7 +443,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint32_t pk[BN / 2];
             float2 rs[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
             const float off = MOD == kModRelBias ? add - mu : -mu;
-            const float2 sl2v = MOD == kModRelBias ? make_float2(mul, mul) : make_float2(sl2, sl2), negmu = make_float2(off, off);
+            const float2 sl2v = make_float2(sl2, sl2), negmu = make_float2(off, off);
 #pragma unroll
             for (int c = 0; c < BN / 2; ++c) {
               const float2 x = ffma2(make_float2(__uint_as_float(s[2 * c]), __uint_as_float(s[2 * c + 1])), sl2v, negmu);
@@ -796,6 +797,7 @@ __global__ void __launch_bounds__(kListThreads, 1) chunk_list_kernel(const Paged
     a.list->n_items = n_parts + min(total, a.items_bound - first_unit);
     a.list->next = ctas;
   }
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // behind the bias's layout: over before this one is
 }
 
 template <int DQK, int DV, int MOD, bool EVEN>
@@ -814,11 +816,11 @@ cudaError_t launch_main(const CUtensorMap& tq, const CUtensorMap& tk, const CUte
     return fa.numRegs * kThreads < C::REG_BUDGET ? cudaErrorInvalidConfiguration : cudaSuccess;
   });
   if (e != cudaSuccess) return e;
-  if constexpr (EVEN) {
+  if constexpr (EVEN && MOD != kModRelBias) {
     kern<<<ctas, kThreads, C::SMEM, stream>>>(tq, tk, tv, a);
     return cudaGetLastError();
   }
-  return launch_early(kern, dim3(ctas), kThreads, C::SMEM, stream, tq, tk, tv, a);  // behind chunk_list_kernel
+  return launch_early(kern, dim3(ctas), kThreads, C::SMEM, stream, tq, tk, tv, a);  // behind chunk_list_kernel or the bias's layout
 }
 
 template <int DQK, int DV>
@@ -826,8 +828,12 @@ cudaError_t launch_d(const CUtensorMap& tq, const CUtensorMap& tk, const CUtenso
                      bool decode, int ctas, cudaStream_t stream) {
   cudaError_t e = cudaSuccess;
   if (!even) {
-    chunk_list_kernel<<<1, kListThreads, 0, stream>>>(a, ctas);
-    e = cudaGetLastError();
+    if (a.score_mod == kModRelBias) {
+      e = launch_early(chunk_list_kernel, dim3(1), kListThreads, 0, stream, a, ctas);
+    } else {
+      chunk_list_kernel<<<1, kListThreads, 0, stream>>>(a, ctas);
+      e = cudaGetLastError();
+    }
     if (e != cudaSuccess) return e;
   }
   if (decode) {

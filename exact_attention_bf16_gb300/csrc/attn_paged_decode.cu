@@ -31,6 +31,8 @@
 #include "kernels.h"
 #include "paged_common.cuh"
 #include "ptx_sm100.cuh"
+#include "rel_bias.cuh"
+#include "score_mod.cuh"
 
 namespace gb300 {
 namespace paged {
@@ -125,7 +127,8 @@ __device__ __forceinline__ void warp_reduce_cols(const float (&x)[N], uint32_t l
   if ((lane & 1u) == 0) out[lane >> 1] = v[0];
 }
 
-template <int DQK, int DV>
+// MOD: kModNone or kModRelBias.
+template <int DQK, int DV, int MOD>
 __global__ void __launch_bounds__(kThreads, 1)
     paged_decode_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUtensorMap tmk,
                         const __grid_constant__ CUtensorMap tmv, const PagedArgs a) {
@@ -167,6 +170,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tbase = bar->tmem_base;
+  if constexpr (MOD == kModRelBias) asm volatile("griddepcontrol.wait;" ::: "memory");  // the bias's layout
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // merge_kernel, as SMs become free
 
   if (warp == 0) {
@@ -294,6 +298,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int key = (kt0 + j) * BN + key_lane;
         const bool here = pg_ok;
         if (j + 2 < n) pg_ok = page_ok(key + 2 * BN);  // fetched one block ahead
+        // relative position bias of this key to each column's query (a load per column, the same for all lanes beyond the reach)
+        float bias[N];
+        if constexpr (MOD == kModRelBias) {
+          const int width = 2 * a.rel.reach + 2 * kRelPad;
+          const float* row = a.rel.by_place + static_cast<int64_t>(w.hk) * a.kv_group * width + a.rel.reach + kRelPad;
+          int r = key - pos0, hd = 0;
+#pragma unroll
+          for (int c = 0; c < N; ++c) {
+            bias[c] = __ldg(row + static_cast<int64_t>(hd) * width + max(-a.rel.reach, min(a.rel.reach, r)));
+            if (++hd == a.kv_group) hd = 0, --r;
+          }
+        }
         ok = ok && mbar_wait_warp(&bar->s_full[i], s_phase & 1u, a.status, 0x4310 + i);
         // a commit costs the MMA thread several hundred cycles, so the slots are released from here: S(j) of
         // block j follows PV(j - 2) in issue order, so K(j) and V(j - 2) have been read
@@ -307,7 +323,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_wait_ld();
         float s[N];
 #pragma unroll
-        for (int c = 0; c < N; ++c) s[c] = __uint_as_float(sr[c]) * sl2;
+        for (int c = 0; c < N; ++c)
+          s[c] = (MOD == kModRelBias ? __uint_as_float(sr[c]) + bias[c] : __uint_as_float(sr[c])) * sl2;
         if (!here || key >= full) {  // keys that no row or not every row sees
           int tok = 0, left = a.kv_group;  // of column c
 #pragma unroll
@@ -483,17 +500,25 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 1) tmem_dealloc(tbase, C::COLS);
 }
 
-template <int DQK, int DV>
-cudaError_t launch_d(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const PagedArgs& a, int ctas,
+template <int DQK, int DV, int MOD>
+cudaError_t launch_m(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const PagedArgs& a, int ctas,
                      cudaStream_t stream) {
   using C = Cfg<DQK, DV>;
-  auto kern = paged_decode_kernel<DQK, DV>;
+  auto kern = paged_decode_kernel<DQK, DV, MOD>;
   static PerDeviceOnce once;
   const cudaError_t e =
       once.run([&] { return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM); });
   if (e != cudaSuccess) return e;
+  if constexpr (MOD == kModRelBias) return launch_early(kern, dim3(ctas), kThreads, C::SMEM, stream, tq, tk, tv, a);
   kern<<<ctas, kThreads, C::SMEM, stream>>>(tq, tk, tv, a);
   return cudaGetLastError();
+}
+
+template <int DQK, int DV>
+cudaError_t launch_d(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const PagedArgs& a, int ctas,
+                     cudaStream_t stream) {
+  return a.score_mod == kModRelBias ? launch_m<DQK, DV, kModRelBias>(tq, tk, tv, a, ctas, stream)
+                                    : launch_m<DQK, DV, kModNone>(tq, tk, tv, a, ctas, stream);
 }
 
 }  // namespace decode

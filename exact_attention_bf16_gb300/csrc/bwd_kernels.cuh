@@ -430,8 +430,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const float sl2 = a.scale_log2;
     int tt = 0, hq = hq_first;  // step within the query head hq
     float alibi_slope = MOD == kModAlibi ? __ldg(a.alibi_slopes + hq) * a.inv_scale : 0.f;  // raw units
-    RelRow rel{};
-    if constexpr (MOD == kModRelBias) rel = rel_row(a.rel, hq);
+    RelRow<kRelPad> rel{a.rel, 0, hq};
+    float2 rel_far = MOD == kModRelBias ? rel.both() : make_float2(0.f, 0.f);  // the bias beyond the reach, left and right
     const uint32_t my_cols = C::tS + 32 * wg;     // this warpgroup's S^T columns
     const uint32_t my_pds = C::tPdS + 32 * wg;    // its P^T (16) and dS^T (16) columns
     bool ok = mbar_wait_warp(&bar->kv_full, 0, a.status, 0x1301);
@@ -508,7 +508,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       // (32 keys, 32 queries) have one bias, that
       const int r0 = kj - q0 - 32 * wg - (U.nk - U.nq);
       float radd = 0.f;
-      const bool near = MOD == kModRelBias && !rel_far(rel, r0 - static_cast<int>(lane) - 31, r0 - static_cast<int>(lane) + 31, radd);
+      const bool near = MOD == kModRelBias && !rel.far(r0 - static_cast<int>(lane) - 31, r0 - static_cast<int>(lane) + 31, rel_far, radd);
+      radd *= sl2;
+      const float* rel_at = MOD == kModRelBias ? rel.global() + r0 : nullptr;
       auto pair = [&](int e, float2 nl, float2 nd, bool mask, bool by_place) {
         const int col = 32 * wg + e;
         float s0 = __uint_as_float(s[e]), s1 = __uint_as_float(s[e + 1]);
@@ -523,7 +525,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           s1 -= fabsf(fmaf(-alibi_slope, static_cast<float>(e + 1), abase));
         }
         if constexpr (MOD == kModRelBias) {
-          if (by_place) nl = fadd2(nl, make_float2(__ldg(rel.centre + (r0 - e)), __ldg(rel.centre + (r0 - e - 1))));
+          if (by_place) s0 += __ldg(rel_at - e), s1 += __ldg(rel_at - e - 1);
           else nl = fadd2(nl, make_float2(radd, radd));
         }
         const float2 x = ffma2(make_float2(s0, s1), sl2v, nl);
@@ -583,7 +585,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (++tt == T1) {
           tt = 0, ++hq;
           if (MOD == kModAlibi && t + 1 < T) alibi_slope = __ldg(a.alibi_slopes + hq) * a.inv_scale;
-          if (MOD == kModRelBias && t + 1 < T) rel = rel_row(a.rel, hq);
+          rel.h = hq;
+          if (MOD == kModRelBias && t + 1 < T) rel_far = rel.both();
         }
       }
       if constexpr (FUSED) {
@@ -966,8 +969,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const float2 sl2v = make_float2(a.scale_log2, a.scale_log2);
     int tt = 0, hq = hq_first;  // step within the query head hq
     float alibi_slope = MOD == kModAlibi ? __ldg(a.alibi_slopes + hq) * a.inv_scale : 0.f;  // raw units
-    RelRow rel{};
-    if constexpr (MOD == kModRelBias) rel = rel_row(a.rel, hq);
+    RelRow<kRelPad> rel{a.rel, 0, hq};
+    float2 rel_far = MOD == kModRelBias ? rel.both() : make_float2(0.f, 0.f);  // the bias beyond the reach, left and right
     auto lanes = [&](int lg) { return tbase + ((quarter * 32u + 16u * static_cast<uint32_t>(lg)) << 16); };
     bool ok = true;
     for (int t = 0; t < T && ok; ++t) {
@@ -997,11 +1000,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       if constexpr (MOD == kModRelBias) {
         float add;
         const int rw = r0 - g + 2 * c;  // the warp's first key at its first query
-        near = !rel_far(rel, rw - 63, rw + 31, add);
+        near = !rel.far(rw - 63, rw + 31, rel_far, add);
+        add *= a.scale_log2;
 #pragma unroll
         for (int r = 0; r < 8; ++r) nlv[r] = fadd2(nlv[r], make_float2(add, add));
       }
       float p[2][32];
+      auto phase_a = [&](auto by_place) {
 #pragma unroll
       for (int lg = 0; lg < 2; ++lg) {
         uint32_t sv[32], pw[16];
@@ -1031,16 +1036,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             sm[u] = sx;
           }
-          float2 nl0 = nl, nl1 = nl;
-          if constexpr (MOD == kModRelBias) {
-            if (near) {
-              const float* at = rel.centre + (r0 + 16 * lg - 8 * r);
-              nl0 = fadd2(nl, make_float2(__ldg(at), __ldg(at - 1)));
-              nl1 = fadd2(nl, make_float2(__ldg(at + 8), __ldg(at + 7)));
-            }
+          if constexpr (decltype(by_place)::value) {
+            const float* at = rel.global() + (r0 + 16 * lg - 8 * r);
+            sm[0] += __ldg(at), sm[1] += __ldg(at - 1);
+            sm[2] += __ldg(at + 8), sm[3] += __ldg(at + 7);
           }
-          const float2 x0 = ffma2(make_float2(sm[0], sm[1]), sl2v, nl0);
-          const float2 x1 = ffma2(make_float2(sm[2], sm[3]), sl2v, nl1);
+          const float2 x0 = ffma2(make_float2(sm[0], sm[1]), sl2v, nl);
+          const float2 x1 = ffma2(make_float2(sm[2], sm[3]), sl2v, nl);
           float* pp = &p[lg][4 * r];
           pp[0] = ex2_mufu(x0.x);
           pp[1] = ex2_mufu(x0.y);
@@ -1062,6 +1064,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         tmem_st16x128b_x8(lanes(lg) + col, pw);
       }
+      };
+      if (MOD == kModRelBias && near) phase_a(std::integral_constant<bool, MOD == kModRelBias>{});
+      else phase_a(std::false_type{});
       // ---- phase B: dS = P (dP - D) from dP^T(t), written next to P^T
       ok = mbar_wait_warp(&bar->dp_full, static_cast<uint32_t>(t) & 1u, a.status, 0x1432);
       if (!ok) break;
@@ -1106,7 +1111,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (++tt == T1) {
           tt = 0, ++hq;
           if (MOD == kModAlibi && t + 1 < T) alibi_slope = __ldg(a.alibi_slopes + hq) * a.inv_scale;
-          if (MOD == kModRelBias && t + 1 < T) rel = rel_row(a.rel, hq);
+          rel.h = hq;
+          if (MOD == kModRelBias && t + 1 < T) rel_far = rel.both();
         }
       }
     }
@@ -1156,6 +1162,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 // dS does not overwrite S, the next tile's S and dP are issued as soon as the
 // softmax warps have copied this tile's out of TMEM. dO sits in TMEM as the A
 // operand of dP where it fits (d_qk <= 128); Q is read from shared memory.
+constexpr int kDqRelPad = 96;  // places that a warp's 32 rows and 64 keys can reach past a relative position bias's reach
 template <int DQK, int DV>
 struct DqCfg {
   static constexpr bool DO_TMEM = DQK <= 128;
@@ -1487,13 +1494,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     const float sl2 = a.scale_log2;
     const float alibi_slope = MOD == kModAlibi ? __ldg(a.alibi_slopes + h) * a.inv_scale : 0.f;  // raw units
-    // relative position bias: its row, the buckets' gradient (bucket lane + 32 k), and the sums of dS beyond the reach
-    RelRow rel{};
-    float bsum[4] = {0.f, 0.f, 0.f, 0.f};
-    float2 fsum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+    // relative position bias: its row and the buckets' gradient, in dO's room where that is in TMEM. Beyond the reach on the right dS is added up
+    // per row. On the left it is not: a row's dS sum to zero over its keys, so the CTA's sum there is minus all the others'
+    // (adding them up cost the kernel 8%; the D that comes from the rounded O also shows less so, P of the few keys within the reach
+    // instead of the many beyond it). Only where such tiles were passed over, and not with split keys, whose CTAs do not see whole
+    // rows.
+    const RelGrad<kDqRelPad> rel_grad{a.rel, smem_u32(C::DO_TMEM ? sdO : smem + C::OFF_BAR + 256)};
+    const RelRow<kDqRelPad> rel{a.rel, rel_grad.row(), h};
+    float right_sum = 0.f;
+    bool left_out = false;
     bool rows_ok = true;  // every row of the warp has keys
     if constexpr (MOD == kModRelBias) {
-      rel = rel_row(a.rel, h);
       rows_ok = __all_sync(0xffffffffu, lse2 != INFINITY);
     }
     bool ok = mbar_wait_warp(&bar->q_full, 0, a.status, 0x2301);
@@ -1505,8 +1516,22 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_before();
     __syncwarp();
     if (lane == 0) mbar_arrive(&bar->qd_tmem);
+    if constexpr (MOD == kModRelBias) {
+      if constexpr (C::DO_TMEM) named_barrier_sync(1, kSoftThreads);  // every warp has taken its dO
+      rel_grad.load(static_cast<int>(threadIdx.x), kSoftThreads);
+      if (a.rel.in_smem) rel.load(static_cast<int>(threadIdx.x), kSoftThreads);
+      named_barrier_sync(1, kSoftThreads);
+    }
     const float2 sl2v = make_float2(sl2, sl2), nl = make_float2(-lse2, -lse2), nd = make_float2(-dsum, -dsum);
     for (int t = 0; t < T && ok; ++t) {
+      // relative position bias: one number for the warp (32 rows, 64 columns), in the row's offset, or a number per logit (r0: the
+      // place of this row at its first column, r00: of the warp's first)
+      const int r0 = key_block(t) * KB + wg * 64 - i - (U.nk - U.nq), r00 = r0 + static_cast<int>(lane);
+      float radd = 0.f;
+      const bool near = MOD == kModRelBias && !rel.far(r00 - 31, r00 + 63, radd);
+      const bool grad = near && a.rel.parts != nullptr;
+      const float offset = fmaf(radd, sl2, -lse2);
+      const float2 off = MOD == kModRelBias ? make_float2(offset, offset) : nl;
       ok = mbar_wait_warp(&bar->s_full, static_cast<uint32_t>(t) & 1u, a.status, 0x2300);
       if (!ok) break;
       tc_fence_after();
@@ -1514,13 +1539,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t s[64], dp[64], dw[32];
       // ALiBi: slope * (key - qpos) of this warpgroup's first key column
       const float abase = alibi_slope * static_cast<float>(key_block(t) * KB + wg * 64 - i - (U.nk - U.nq));
-      // the place of this row at this warpgroup's first column; where the warp's places (32 rows, 64 columns) have one bias, that
-      const int r0 = key_block(t) * KB + wg * 64 - i - (U.nk - U.nq), r00 = r0 + static_cast<int>(lane);
-      float radd = 0.f;
-      const bool near = MOD == kModRelBias && !rel_far(rel, r00 - 31, r00 + 63, radd);
-      const float2 nla = make_float2(radd - lse2, radd - lse2);
       // P of columns e, e + 1 (zero where masked) and the score modification's derivative f there
-      auto prob2 = [&](int e, bool mask, float2& f, bool by_place) -> float2 {
+      auto by_place = [&] {
+        rel.at(r0, [&](auto bias) {
+#pragma unroll
+          for (int e = 0; e < 64; ++e) s[e] = __float_as_uint(__uint_as_float(s[e]) + bias(e));
+        });
+      };
+      auto prob2 = [&](int e, bool mask, float2& f) -> float2 {
         const int col = wg * 64 + e;
         float s0 = __uint_as_float(s[e]), s1 = __uint_as_float(s[e + 1]);
         f = make_float2(1.f, 1.f);
@@ -1533,9 +1559,6 @@ __global__ void __launch_bounds__(kThreads, 1)
           s0 -= fabsf(fmaf(alibi_slope, static_cast<float>(e), abase));
           s1 -= fabsf(fmaf(alibi_slope, static_cast<float>(e + 1), abase));
         }
-        float2 off = nl;
-        if constexpr (MOD == kModRelBias)
-          off = by_place ? fadd2(nl, make_float2(__ldg(rel.centre + (r0 + e)), __ldg(rel.centre + (r0 + e + 1)))) : nla;
         const float2 x = ffma2(make_float2(s0, s1), sl2v, off);
         float2 p = make_float2(ex2_mufu(x.x), ex2_mufu(x.y));
         if (mask) {
@@ -1543,14 +1566,6 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (col + 1 >= cnt) p.y = 0.f;
         }
         return p;
-      };
-      // dS in fp32 for the bias's gradient: in place of S, or (one bucket) added up
-      const bool right = r00 - 31 >= rel.reach;
-      float2 tsum = make_float2(0.f, 0.f);
-      auto keep_ds = [&](int e, const float2& ds) {
-        s[e] = __float_as_uint(ds.x);
-        s[e + 1] = __float_as_uint(ds.y);
-        tsum = fadd2(tsum, ds);
       };
       const bool full = cnt >= wg * 64 + 64;  // every key of this warpgroup's half is visible
       if constexpr (C::SPLIT_SDP) {
@@ -1562,19 +1577,19 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(&bar->s_free);
         // P times f, in place of S, while dP(t) runs
-        auto prob = [&](bool mask, bool by_place) {
+        if (MOD == kModRelBias && near) by_place();
+        auto prob = [&](bool mask) {
 #pragma unroll
           for (int e = 0; e < 64; e += 2) {
             float2 f;
-            float2 p = prob2(e, mask, f, by_place);
+            float2 p = prob2(e, mask, f);
             if constexpr (MOD == kModSoftcap) p = fmul2(p, f);
             s[e] = __float_as_uint(p.x);
             s[e + 1] = __float_as_uint(p.y);
           }
         };
-        if (MOD == kModRelBias && near) prob(true, true);
-        else if (full) prob(false, false);
-        else prob(true, false);
+        if (full) prob(false);
+        else prob(true);
         ok = mbar_wait_warp(&bar->dp_full, static_cast<uint32_t>(t) & 1u, a.status, 0x2302);
         if (!ok) break;
         tc_fence_after();
@@ -1589,7 +1604,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const float2 ds = fmul2(make_float2(__uint_as_float(s[e]), __uint_as_float(s[e + 1])),
                                   fadd2(make_float2(__uint_as_float(dp[e]), __uint_as_float(dp[e + 1])), nd));
           dw[e / 2] = pack_bf16x2(ds.x, ds.y);
-          if constexpr (MOD == kModRelBias) keep_ds(e, ds);
+          if constexpr (MOD == kModRelBias) s[e] = __float_as_uint(ds.x), s[e + 1] = __float_as_uint(ds.y);
         }
       } else {
         // this warpgroup's 64 columns of S and dP out of TMEM, then both released
@@ -1601,20 +1616,20 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&bar->sp_free);
-        auto row = [&](bool mask, bool by_place) {  // dS = P (dP - D) f
+        if (MOD == kModRelBias && near) by_place();
+        auto row = [&](bool mask) {  // dS = P (dP - D) f
 #pragma unroll
           for (int e = 0; e < 64; e += 2) {
             float2 f;
-            const float2 p = prob2(e, mask, f, by_place);
+            const float2 p = prob2(e, mask, f);
             float2 ds = fmul2(p, fadd2(make_float2(__uint_as_float(dp[e]), __uint_as_float(dp[e + 1])), nd));
             if constexpr (MOD == kModSoftcap) ds = fmul2(ds, f);
             dw[e / 2] = pack_bf16x2(ds.x, ds.y);
-            if constexpr (MOD == kModRelBias) keep_ds(e, ds);
+            if constexpr (MOD == kModRelBias) s[e] = __float_as_uint(ds.x), s[e + 1] = __float_as_uint(ds.y);  // for the gradient
           }
         };
-        if (MOD == kModRelBias && near) row(true, true);
-        else if (full) row(false, false);
-        else row(true, false);
+        if (full) row(false);
+        else row(true);
       }
       if (t > 0) {  // dQ(t-1) must have read the previous dS
         ok = mbar_wait_warp(&bar->ds_free, static_cast<uint32_t>(t - 1) & 1u, a.status, 0x2305);
@@ -1628,9 +1643,19 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lane == 0) mbar_arrive(&bar->ds_full);
       if constexpr (MOD == kModRelBias) {  // while the tensor core takes dS
         if (!near) {
-          if (right) fsum[1] = fadd2(fsum[1], tsum);
-          else fsum[0] = fadd2(fsum[0], tsum);
-        } else if (a.rel.parts != nullptr) {
+          const bool right = r00 - 31 >= a.rel.reach;
+          if (right || split) {
+            float2 t2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+            for (int e = 0; e < 64; e += 2)
+              t2[(e / 2) & 1] = fadd2(t2[(e / 2) & 1], make_float2(__uint_as_float(s[e]), __uint_as_float(s[e + 1])));
+            float x = (t2[0].x + t2[0].y) + (t2[1].x + t2[1].y);
+            if (right) right_sum += x;
+            else rel_grad.add(static_cast<int>(warp), a.rel.left, lse2 != INFINITY ? x : 0.f);
+          } else {
+            left_out = left_out || radd > -INFINITY;
+          }
+        } else if (grad) {
           float x[64], diag[3];
 #pragma unroll
           for (int e = 0; e < 64; ++e) x[e] = __uint_as_float(s[e]);
@@ -1639,30 +1664,33 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int e = 0; e < 64; ++e) x[e] = lse2 != INFINITY ? x[e] : 0.f;
           }
           diagonal_sums(x, diag);
-          bucket_sums(a.rel, diag, r00, bsum);
+          rel_grad.add(static_cast<int>(warp), diag, r00);
         }
       }
     }
     if constexpr (MOD == kModRelBias) {
       if (a.rel.parts != nullptr) {
+        rel_grad.add(static_cast<int>(warp), a.rel.right, lse2 != INFINITY ? right_sum : 0.f);
+        const bool any = named_barrier_or(1, kSoftThreads, left_out);
         const int64_t place = a.cu_q != nullptr ? static_cast<int64_t>(U.q_start) / MB + U.unit + m
                                                 : (static_cast<int64_t>(U.b) * a.n_qblk + m) * (split ? a.dq_split : 1) + range;
-        const bool alive = lse2 != INFINITY;
+        if (warp == 0 && place >= 0 && place < a.rel.part_rows) {  // (else offsets overrun total_q)
+          float sum[4], all = 0.f;  // of bucket lane + 32 k, the warps' sums in order
 #pragma unroll
-        for (int z = 0; z < 2; ++z) {
-          float x = alive ? fsum[z].x + fsum[z].y : 0.f;
+          for (int k = 0; k < 4; ++k) {
+            sum[k] = 0.f;
 #pragma unroll
-          for (int d = 16; d > 0; d >>= 1) x += __shfl_xor_sync(0xffffffffu, x, d);
-          const int id = __ldg(a.rel.bucket + kRelPad + (z == 0 ? 0 : 2 * a.rel.reach));
+            for (int y = 0; y < kSoftThreads / 32; ++y) sum[k] += ld_shared_f32(rel_grad.sum(y, static_cast<int>(lane) + 32 * k));
+            all += sum[k];
+          }
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
-            if (id == static_cast<int>(lane) + 32 * k) bsum[k] += x;
-        }
-        if (place >= 0 && 8 * place + 8 <= a.rel.part_rows) {
-          float* dst = a.rel.parts + ((static_cast<int64_t>(h) * a.rel.part_rows) + 8 * place + warp) * a.rel.buckets;
+          for (int d = 16; d > 0; d >>= 1) all += __shfl_xor_sync(0xffffffffu, all, d);
+          float* dst = a.rel.parts + (static_cast<int64_t>(h) * a.rel.part_rows + place) * a.rel.buckets;
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
-            if (static_cast<int>(lane) + 32 * k < a.rel.buckets) dst[lane + 32 * k] = bsum[k];
+          for (int k = 0; k < 4; ++k) {
+            const int b = static_cast<int>(lane) + 32 * k;
+            if (b < a.rel.buckets) dst[b] = sum[k] - (any && b == a.rel.left ? all : 0.f);
+          }
         }
       }
     }
@@ -1755,7 +1783,7 @@ cudaError_t launch_dq_t(const CUtensorMap& tq, const CUtensorMap& tk, const CUte
   using C = DqCfg<DQK, DV>;
   auto kern = dq_kernel<DQK, DV, SPARSE, MOD>;
   static PerDeviceOnce once;
-  cudaError_t e = once.run([&] { return set_smem(kern, C::SMEM); });
+  cudaError_t e = once.run([&] { return set_smem(kern, MOD == kModRelBias ? 232448 : C::SMEM); });
   if (e != cudaSuccess) return e;
   const int split = (!SPARSE && a.dq_split > 1) ? a.dq_split : 1;
   if (split > 1 && (a.tiles_q != nullptr || a.dq_part == nullptr || a.dq_kb_per_split < 1))
@@ -1763,6 +1791,15 @@ cudaError_t launch_dq_t(const CUtensorMap& tq, const CUtensorMap& tk, const CUte
   const int64_t grid = (a.tiles_q ? a.n_tiles_q : static_cast<int64_t>(a.n_qblk) * a.num_units * a.heads) * split;
   if (grid <= 0) return cudaSuccess;
   if (grid > 0x7fffffff) return cudaErrorInvalidConfiguration;
+  if constexpr (MOD == kModRelBias) {
+    BwdArgs b = a;
+    // dO's room, where that goes to TMEM, or else what is left of shared memory
+    constexpr int kRoom = C::DO_TMEM ? C::DO_BYTES : 232448 - C::SMEM;
+    static_assert(kRoom >= kRelSums + kRelRange, "the gradient's sums");
+    b.rel.in_smem = RelGrad<kDqRelPad>::bytes(a.rel.reach) <= kRoom;
+    kern<<<static_cast<unsigned>(grid), kThreads, C::DO_TMEM ? C::SMEM : 232448, stream>>>(tq, tk, tv, tdo, b);
+    return cudaGetLastError();
+  }
   kern<<<static_cast<unsigned>(grid), kThreads, C::SMEM, stream>>>(tq, tk, tv, tdo, a);
   return cudaGetLastError();
 }

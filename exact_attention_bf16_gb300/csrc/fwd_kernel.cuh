@@ -54,6 +54,7 @@ constexpr int QT = 2;           // query tiles per CTA
 constexpr int kThreads = 384;   // 12 warps
 constexpr int kChunk = BM * 128;  // bytes of one 64-column (128-byte) swizzled chunk of a 128-row tile
 constexpr float kThreshold = 8.0f;  // log2 units (factor 256)
+constexpr int kMaxSmem = 232448;    // shared memory of a CTA
 
 
 // TMEM column map (512 columns allocated): S/P for tile i at tS(i), O at tO(i).
@@ -78,7 +79,7 @@ struct Cfg {
   static constexpr int NSLOT = SPLIT ? 3 : (DQK <= 64 ? 8 : 4);
   static constexpr int BAR_OFF = QT * Q_BYTES + (SPLIT ? 2 * K_BYTES + V_BYTES : NSLOT * SLOT);
   static constexpr int SMEM = BAR_OFF + 256 + 1024;  // barriers + alignment slack
-  static_assert(SMEM <= 232448, "shared memory budget");
+  static_assert(SMEM <= kMaxSmem, "shared memory budget");
   // Register split: warpgroup 0 (TMA, MMA, two idle warps) gives registers to
   // the two softmax warpgroups. 128*REG_LO + 256*REG_HI must fit in the
   // 384 * (launch registers per thread) the CTA starts with (checked on the host).
@@ -242,10 +243,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   const PollLimit poll_lim = DIAG ? PollLimit{a.spin_limit} : kNoPollLimit;  // of the waits below
 
   // Early copies by thread 0 for dense d_qk <= 128 without a score
-  // modification. Otherwise (d_qk = 192: measured faster; block-sparse and
-  // score modifications: fewer spills) the producer copies Q first, then the
-  // K/V ring, after the block barrier.
-  constexpr bool kEarlyQ = DQK <= 128 && !SPARSE && MOD == kModNone, kEarlyK = kEarlyQ;
+  // modification, or with a relative position bias (B32 H16 N512 d64: 101 us, 99 so). Otherwise (d_qk = 192: measured
+  // faster; block-sparse and the other modifications: fewer spills) the producer copies Q first, then the K/V ring, after
+  // the block barrier.
+  constexpr bool kEarlyQ = DQK <= 128 && !SPARSE && (MOD == kModNone || MOD == kModRelBias), kEarlyK = kEarlyQ;
   const uint32_t warp = warp_id(), lane = lane_id();
   if (threadIdx.x == 0) {
     for (int i = 0; i < QT; ++i) {
@@ -398,8 +399,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         // What the step's first products need is tested together: this thread's instructions limit the step, and waits
         // one after another cost it 150 cycles each even where everything had arrived (d = 128, N = 8192: 1.42 -> 1.38 ms).
         // Not where the softmax limits it, which then has to share its issue slots with the tests (ALiBi 1.70 -> 1.74 ms,
-        // E4M3 1.23 -> 1.26).
-        constexpr bool kTogether = MOD == 0 && !F8;
+        // E4M3 1.23 -> 1.26; with a relative position bias d = 128 gains, B2 H16 over 4 N8192 404 -> 390 us, and d = 64 loses, B1 H8
+        // N16001 713 -> 756).
+        constexpr bool kTogether = (MOD == 0 || (MOD == kModRelBias && DQK == 128)) && !F8;
         const bool pv0 = kTogether && haveV && j - 1 < nkv[0];
         const bool k_in = kTogether && (!haveK || mbar_test(&bar->kv_full[sK], ring_use(uK) & 1u));
         const bool v_in = kTogether && (!haveV || mbar_test(&bar->kv_full[sV], ring_use(uV) & 1u));
@@ -472,8 +474,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int klim = key_limit(row, nq, nk, a.causal) - (SPLITKV ? kb_lo * BN : 0);
     const float alibi_slope = MOD == kModAlibi ? __ldg(a.alibi_slopes + h) * a.inv_scale : 0.f;  // raw units
     const int qpos = row + (nk - nq);  // the row's position among the keys (bottom-right aligned)
-    RelRow rel{};
-    if constexpr (MOD == kModRelBias) rel = rel_row(a.rel, h);
+    const RelRow<kRelPad> rel{a.rel, smem_u32(smem + C::BAR_OFF + 256), h};
+    if (MOD == kModRelBias && a.rel.in_smem) {
+      rel.load(static_cast<int>(threadIdx.x) - 128, 256);
+      named_barrier_sync(1, 256);
+    }
     const uint32_t lane_base = tbase + ((quarter * 32u) << 16);
     const float sl2 = a.scale_log2;
     const bool f16 = v_is_f16(a);  // P packed as fp16 (V's copy) or bf16
@@ -483,6 +488,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true;
     for (int j = 0; j < nkv[i]; ++j) {
       const int kb = SPLITKV ? j : key_block(j);  // read before the wait, off the critical path
+      // relative position bias: one number for the warp (32 rows in a row; r0 is this one's place at column 0), which goes into
+      // the softmax's offsets (add, log2 units), or a number per logit, added below
+      const int r0 = kb * BN - qpos;
+      float add = 0.f;
+      const bool near = MOD == kModRelBias && !rel.far(r0 + static_cast<int>(lane) - 31, r0 + static_cast<int>(lane) + BN - 1, add);
+      add *= sl2;
       // site: 0x300 + tile, the step in bits 12..23 (a timeout then says where it stopped)
       ok = mbar_wait_warp(&bar->s_full[i], static_cast<uint32_t>(j) & 1u, a.status,
                           0x300u + i + ((static_cast<uint32_t>(j) & 0xFFFu) << 12), poll_lim);
@@ -503,16 +514,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int c = 0; c < BN; ++c)
           s[c] = __float_as_uint(__uint_as_float(s[c]) - fabsf(fmaf(alibi_slope, static_cast<float>(c), base)));
       }
-      // relative position bias: logits in log2 units, s * mul + add, where the tile's bias is one number per warp; else
-      // taken so here, and mul = 1 (kb * BN - qpos: this row's place of column 0; a warp's rows are 32 in a row)
-      float mul = sl2, add = 0.f;
       if constexpr (MOD == kModRelBias) {
-        const int r0 = kb * BN - qpos, r_top = r0 + static_cast<int>(lane);
-        if (!rel_far(rel, r_top - 31, r_top + BN - 1, add)) {
-          const float* at = rel.centre + r0;
+        if (near) {
+          rel.at(r0, [&](auto bias) {
 #pragma unroll
-          for (int c = 0; c < BN; ++c) s[c] = __float_as_uint(fmaf(__uint_as_float(s[c]), sl2, __ldg(at + c)));
-          mul = 1.f;
+            for (int c = 0; c < BN; ++c) s[c] = __float_as_uint(__uint_as_float(s[c]) + bias(c));
+          });
         }
       }
       const int cnt = klim - kb * BN;  // visible keys of this row inside the tile
@@ -531,7 +538,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int z = 0; z < 8; ++z) mp[z] = fmax3(mp[z], __uint_as_float(s[c + z]), __uint_as_float(s[c + 8 + z]));
       const float mx = fmax3(fmax3(mp[0], mp[1], mp[2]), fmax3(mp[3], mp[4], mp[5]), fmaxf(mp[6], mp[7]));
-      const float m_tile = MOD == kModRelBias ? fmaf(mx, mul, add) : mx * sl2;
+      const float m_tile = MOD == kModRelBias ? fmaf(mx, sl2, add) : mx * sl2;
       const bool need = m_tile > m_used + kThreshold;
       float alpha = 1.f;
       if (need) {
@@ -548,7 +555,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t pk[BN / 2];
       float2 rs[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};  // partial row sums (packed pairs)
       const float off = MOD == kModRelBias ? add - mu : -mu;
-      const float2 sl2v = MOD == kModRelBias ? make_float2(mul, mul) : make_float2(sl2, sl2), negmu = make_float2(off, off);
+      const float2 sl2v = make_float2(sl2, sl2), negmu = make_float2(off, off);
       auto exp_row = [&](auto f16_tag) {
         constexpr bool F16 = decltype(f16_tag)::value;
 #pragma unroll
@@ -671,7 +678,8 @@ cudaError_t launch_e(const CUtensorMap& tq, const CUtensorMap& tk, const CUtenso
   auto kern = attn_fwd_kernel<DQK, DV, EMU, SPARSE, DIAG, LIST, MOD, F8, SPLITKV>;
   static PerDeviceOnce once;
   cudaError_t e = once.run([&]() -> cudaError_t {
-    cudaError_t r = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+    cudaError_t r = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         MOD == kModRelBias ? kMaxSmem : C::SMEM);
     if (r != cudaSuccess) return r;
     cudaFuncAttributes fa{};
     r = cudaFuncGetAttributes(&fa, kern);
@@ -689,6 +697,13 @@ cudaError_t launch_e(const CUtensorMap& tq, const CUtensorMap& tk, const CUtenso
   if (grid <= 0) return cudaSuccess;
   if (grid > 0x7fffffff || (SPLITKV && a.kv_split > 65535)) return cudaErrorInvalidConfiguration;
   const dim3 g3(static_cast<unsigned>(grid), SPLITKV ? static_cast<unsigned>(a.kv_split) : 1u);
+  if constexpr (MOD == kModRelBias) {
+    FwdArgs b = a;
+    const int row = 2 * (a.rel.reach + kRelPad) * 4;
+    b.rel.in_smem = row <= kMaxSmem - C::SMEM;
+    kern<<<g3, kThreads, C::SMEM + (b.rel.in_smem ? row : 0), stream>>>(tq, tk, tv, tv16, b);
+    return cudaGetLastError();
+  }
   kern<<<g3, kThreads, C::SMEM, stream>>>(tq, tk, tv, tv16, a);
   return cudaGetLastError();
 }

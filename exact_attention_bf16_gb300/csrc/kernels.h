@@ -122,7 +122,7 @@ cudaError_t launch_early(K kern, dim3 grid, int threads, int smem, cudaStream_t 
 // head by head, blocks of a head in descending or ascending order. Writes
 // `bound` entries (the real ones, then empty ones); scratch holds num_seqs
 // int64. max_nblk bounds every sequence's block count (<= kMaxListBlocks).
-// *zero_word (when given) is set to 0.
+// *zero_word (when given) is set to 0. early: behind launch_rel_layout, whose kernel it runs beside.
 struct TileListSpec {
   int heads, rows_per_block, by_keys, descending, max_nblk;
   TileEntry* out;
@@ -142,28 +142,31 @@ struct SeqMaps {
   CUtensorMap* out = nullptr;
 };
 cudaError_t launch_tile_lists(const int* cu_q, const int* cu_k, int num_seqs, const TileListSpec* specs, int n,
-                              int64_t* scratch, uint32_t* zero_word, const SeqMaps& maps, cudaStream_t stream);
+                              int64_t* scratch, uint32_t* zero_word, const SeqMaps& maps, bool early, cudaStream_t stream);
 
 // Relative position bias (rel_bias.cuh). The caller's table and its buckets: bucket k of a side holds the distances from
 // start[k] on, up to start[k + 1] or without end.
-constexpr int kRelPad = 256;  // places a tile of 128 x 128 can reach past the row's bounds
+constexpr int kRelPad = 160;  // places that a warp's logits (32 rows, 128 keys) can reach past the reach
 constexpr int kRelMaxBuckets = 128;
 struct RelTable {
   const void* table;  // [buckets, heads], bf16 or fp32
+  float inv_scale;    // 1 / softmax_scale
   int f32, heads, buckets, side, two_sided, reach;
   int start[kRelMaxBuckets];
 };
-// Laid out by place, and for the gradient each place's bucket, each bucket's first and last place, and the parts' room:
-// [heads][part_rows][buckets], eight rows (one per softmax warp) per CTA of the dQ kernel.
+// Laid out by place, and for the gradient each place's bucket, each bucket's first and last place, the buckets beyond the
+// reach, and the parts' room: [heads][part_rows][buckets], a row per CTA of the dQ kernel.
 struct RelBias {
   const float* by_place;
   const uint8_t* bucket;
   const int2* range;
   float* parts;
   int64_t part_rows;
-  int reach, buckets;
+  int reach, buckets, left, right;
+  int in_smem;  // the kernel holds its head's row in shared memory (set by its launch, where that fits)
 };
-// zero: n_zero floats to clear along the way (a multiple of 4, 16-byte aligned).
+// zero: n_zero floats to clear along the way (a multiple of 4, 16-byte aligned). The next kernel may be launched early: it
+// waits before it reads the bias and before it ends.
 cudaError_t launch_rel_layout(const RelTable& t, const RelBias& b, float* zero, int64_t n_zero, cudaStream_t stream);
 cudaError_t launch_rel_sum(const float* parts, int64_t rows, int buckets, int heads, void* out, int f32, cudaStream_t stream);
 

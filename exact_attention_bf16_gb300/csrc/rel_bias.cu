@@ -26,6 +26,7 @@ __device__ __forceinline__ int bucket_of(const RelTable& t, int r) {
 // gradient's parts, which not every CTA of a packed backward writes. A few hundred KB at most: bound by its launch.
 __global__ void __launch_bounds__(kThreads) layout_kernel(const __grid_constant__ RelTable t, float* by_place, uint8_t* bucket,
                                                           int2* range, float4* zero, int64_t n_zero) {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int width = 2 * t.reach + 2 * kRelPad;
   const int x = static_cast<int>(blockIdx.x * kThreads + threadIdx.x);
   if (x < width) {
@@ -34,7 +35,7 @@ __global__ void __launch_bounds__(kThreads) layout_kernel(const __grid_constant_
       const int64_t at = static_cast<int64_t>(b) * t.heads + h;
       const float v = t.f32 ? __ldg(static_cast<const float*>(t.table) + at)
                             : __bfloat162float(static_cast<const __nv_bfloat16*>(t.table)[at]);
-      by_place[static_cast<int64_t>(h) * width + x] = v * 1.4426950408889634f;
+      by_place[static_cast<int64_t>(h) * width + x] = v * t.inv_scale;
     }
     if (bucket != nullptr && blockIdx.y == 0) bucket[x] = static_cast<uint8_t>(b);
   }
@@ -58,6 +59,7 @@ __global__ void __launch_bounds__(1024) sum_parts_kernel(const float* parts, int
   const int h = static_cast<int>(blockIdx.x), lanes = static_cast<int>(blockDim.x) / buckets;
   const int b = static_cast<int>(threadIdx.x) % buckets, y = static_cast<int>(threadIdx.x) / buckets;
   float sum = 0.f;
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // launched before the parts' kernel is over
   if (y < lanes) {
     const float* p = parts + (static_cast<int64_t>(h) * rows) * buckets + b;
 #pragma unroll 8
@@ -86,8 +88,8 @@ cudaError_t launch_rel_layout(const RelTable& t, const RelBias& b, float* zero, 
 }
 
 cudaError_t launch_rel_sum(const float* parts, int64_t rows, int buckets, int heads, void* out, int f32, cudaStream_t stream) {
-  rel::sum_parts_kernel<<<static_cast<unsigned>(heads), 1024, 0, stream>>>(parts, rows, buckets, heads, out, f32);
-  return cudaGetLastError();
+  return launch_early(rel::sum_parts_kernel, dim3(static_cast<unsigned>(heads)), 1024, 0, stream, parts, rows, buckets, heads, out,
+                      f32);
 }
 
 }  // namespace gb300

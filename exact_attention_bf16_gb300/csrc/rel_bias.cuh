@@ -2,7 +2,7 @@
 // a (query, key) pair depends on the head and on r = key - query's position
 // alone, and beyond a reach R on r's sign alone: the bucket borders lie within
 // |r| <= R. A call first lays it out by r (rel_bias.cu): one row of fp32 per
-// head, times log2(e), of r = -R - kRelPad .. R + kRelPad - 1. A tile of logits that lies beyond the reach as a whole then
+// head, over the softmax scale (in units of the raw logits q . k), of r = -R - kRelPad .. R + kRelPad - 1. A tile of logits that lies beyond the reach as a whole then
 // takes one number, added for free to the softmax's own offset; any other takes
 // one load per logit, neighbouring lanes neighbouring addresses (the row in L1: 3 KB
 // at R = 128), from a row wide enough that no index needs a test.
@@ -12,22 +12,122 @@
 
 namespace gb300 {
 
-// A head's row.
+// A head's row: in shared memory from r = -reach - pad on (b.in_smem; smem is its address), where a warp's loads from any place take one
+// pass, else in L1 (two lines). Nothing of it lives in registers between tiles.
+template <int PAD>
 struct RelRow {
-  const float* centre;  // centre[r], -reach - kRelPad <= r < reach + kRelPad
-  float left, right;    // of r <= -reach and r >= reach
-  int reach;
+  const RelBias& b;
+  uint32_t smem;
+  int h;
+  __device__ __forceinline__ const float* global() const {  // of r = 0
+    return b.by_place + static_cast<int64_t>(h) * (2 * b.reach + 2 * kRelPad) + b.reach + kRelPad;
+  }
+  __device__ __forceinline__ uint32_t shared() const { return smem + 4 * (b.reach + PAD); }
+  // Copied by n threads, which then have to meet.
+  __device__ __forceinline__ void load(int thread, int n) const {
+    const float* src = global() - b.reach - PAD;
+    for (int x = thread; x < 2 * (b.reach + PAD); x += n) st_shared_f32(smem + 4 * x, __ldg(src + x));
+  }
+  __device__ __forceinline__ float one(int r) const { return b.in_smem ? ld_shared_f32(shared() + 4 * r) : __ldg(global() + r); }
+  // Whether places r_min .. r_max all have one bias, `add`.
+  __device__ __forceinline__ bool far(int r_min, int r_max, float& add) const {
+    const bool l = r_max <= -b.reach, r = r_min >= b.reach;
+    add = 0.f;
+    if (l || r) add = one(l ? -b.reach : b.reach);
+    return l || r;
+  }
+  // The same with the two numbers in registers (left of and right of the reach).
+  __device__ __forceinline__ float2 both() const { return make_float2(one(-b.reach), one(b.reach)); }
+  __device__ __forceinline__ bool far(int r_min, int r_max, const float2& lr, float& add) const {
+    const bool l = r_max <= -b.reach, r = r_min >= b.reach;
+    add = l ? lr.x : r ? lr.y : 0.f;
+    return l || r;
+  }
+  // f(load) with load(c) the bias of place r + c.
+  template <typename F>
+  __device__ __forceinline__ void at(int r, F&& f) const {
+    if (b.in_smem) {
+      const uint32_t from = shared() + 4 * r;
+      f([from](int c) { return ld_shared_f32(from + 4 * c); });
+    } else {
+      const float* from = global() + r;
+      f([from](int c) { return __ldg(from + c); });
+    }
+  }
 };
-__device__ __forceinline__ RelRow rel_row(const RelBias& b, int h) {
-  const float* row = b.by_place + static_cast<int64_t>(h) * (2 * b.reach + 2 * kRelPad);
-  return RelRow{row + b.reach + kRelPad, __ldg(row + kRelPad), __ldg(row + 2 * b.reach + kRelPad), b.reach};
-}
-// Whether places r_min .. r_max all have one bias, `add`.
-__device__ __forceinline__ bool rel_far(const RelRow& w, int r_min, int r_max, float& add) {
-  const bool l = r_max <= -w.reach, r = r_min >= w.reach;
-  add = l ? w.left : r ? w.right : 0.f;
-  return l || r;
-}
+
+// What the dQ kernel holds of the gradient in shared memory: each warp's sums by bucket, and behind them, where the row is there
+// too (b.in_smem), the buckets' first and last places, the row and its places' buckets.
+constexpr int kRelSums = 8 * kRelMaxBuckets * 4, kRelRange = kRelMaxBuckets * 8;  // bytes
+template <int PAD>
+struct RelGrad {
+  const RelBias& b;
+  uint32_t smem;
+  static constexpr int bytes(int reach) { return kRelSums + kRelRange + 5 * 2 * (reach + PAD); }  // with the row
+  __device__ __forceinline__ uint32_t row() const { return smem + kRelSums + kRelRange; }
+  __device__ __forceinline__ uint32_t sum(int warp, int bucket) const { return smem + 4 * (warp * kRelMaxBuckets + bucket); }
+  // By n threads, which then have to meet.
+  __device__ __forceinline__ void load(int thread, int n) const {
+    for (int x = thread; x < 8 * kRelMaxBuckets; x += n) st_shared_f32(smem + 4 * x, 0.f);
+    if (!b.in_smem || b.parts == nullptr) return;
+    const int width = 2 * (b.reach + PAD);
+    for (int x = thread; x < b.buckets; x += n) {
+      const int2 r = __ldg(b.range + x);
+      st_shared_f32(smem + kRelSums + 8 * x, __int_as_float(r.x));
+      st_shared_f32(smem + kRelSums + 8 * x + 4, __int_as_float(r.y));
+    }
+    for (int x = thread; x < width; x += n) st_shared_u8(row() + 4 * width + x, __ldg(b.bucket + kRelPad - PAD + x));
+  }
+  __device__ __forceinline__ int bucket(int r) const {
+    return b.in_smem ? ld_shared_u8(row() + 4 * 2 * (b.reach + PAD) + b.reach + PAD + r) : __ldg(b.bucket + kRelPad + b.reach + r);
+  }
+  __device__ __forceinline__ int2 range(int bucket) const {
+    if (!b.in_smem) return __ldg(b.range + bucket);
+    return make_int2(__float_as_int(ld_shared_f32(smem + kRelSums + 8 * bucket)),
+                     __float_as_int(ld_shared_f32(smem + kRelSums + 8 * bucket + 4)));
+  }
+  // Adds the sum of x over the warp to a bucket.
+  __device__ __forceinline__ void add(int warp, int bucket, float x) const {
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) x += __shfl_xor_sync(0xffffffffu, x, d);
+    if (bucket % 32 == static_cast<int>(lane_id())) st_shared_f32(sum(warp, bucket), ld_shared_f32(sum(warp, bucket)) + x);
+  }
+  // Adds the diagonals' sums t of a block (diagonal_sums), whose place at row 0, column 0 is r00. Each window of 32 places is
+  // summed by bucket along the lanes (a bucket's places lie side by side), and the lane that bucket lane + 32 k belongs to takes
+  // the sum from the last of them.
+  __device__ __forceinline__ void add(int warp, const float (&t)[3], int r00) const {
+    const int lane = static_cast<int>(lane_id());
+    float x[3];
+    int start[3];  // first lane of this one's bucket
+#pragma unroll
+    for (int q = 0; q < 3; ++q) {
+      const int id = bucket(r00 + 32 * q - lane), before = __shfl_up_sync(0xffffffffu, id, 1);
+      const uint32_t heads = __ballot_sync(0xffffffffu, lane == 0 || id != before);
+      start[q] = 31 - __clz(heads & (0xffffffffu >> (31 - lane)));
+      x[q] = t[q];
+    }
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+#pragma unroll
+      for (int q = 0; q < 3; ++q) {
+        const float y = __shfl_up_sync(0xffffffffu, x[q], d);
+        if (lane - d >= start[q]) x[q] += y;
+      }
+    }
+    for (int k = 0; 32 * k < b.buckets; ++k) {
+      const bool mine = lane + 32 * k < b.buckets;
+      const int2 places = mine ? range(lane + 32 * k) : make_int2(1, 0);
+      float all = 0.f;
+#pragma unroll
+      for (int q = 0; q < 3; ++q) {  // places top .. top - 31
+        const int top = r00 + 32 * q, low = max(places.x, top - 31);
+        const float y = __shfl_sync(0xffffffffu, x[q], (top - low) & 31);
+        if (low <= min(places.y, top)) all += y;
+      }
+      if (mine) st_shared_f32(sum(warp, lane + 32 * k), ld_shared_f32(sum(warp, lane + 32 * k)) + all);
+    }
+  }
+};
 
 // Sums along the diagonals of a warp's 32 x 64 block, lane l's row in x[0 .. 63]: t[q] of lane l becomes
 // sum_i x_i[d + i], d = 32 q - l, over the lanes i with 0 <= d + i < 64. Five rounds, in each of which two lanes a power of
@@ -57,35 +157,6 @@ __device__ __forceinline__ void diagonal_sums(float (&x)[64], float (&t)[3]) {
   round(std::integral_constant<int, 9>{}, 8);
   round(std::integral_constant<int, 5>{}, 16);
   t[0] = x[0], t[1] = x[1], t[2] = x[2];
-}
-
-// Adds the diagonals' sums t of a block (diagonal_sums), whose place at row 0, column 0 is r00, to the buckets' sums: bucket
-// lane + 32 k in acc[k]. Each window of 32 places is summed by bucket along the lanes (a bucket's places lie side by side), and
-// the bucket's lane takes the sum from the last of them.
-__device__ __forceinline__ void bucket_sums(const RelBias& b, const float (&t)[3], int r00, float (&acc)[4]) {
-  const int lane = static_cast<int>(lane_id());
-#pragma unroll
-  for (int q = 0; q < 3; ++q) {
-    const int top = r00 + 32 * q, r = top - lane;  // places top .. top - 31
-    const int id = __ldg(b.bucket + r + b.reach + kRelPad);
-    const int before = __shfl_up_sync(0xffffffffu, id, 1);
-    const uint32_t heads = __ballot_sync(0xffffffffu, lane == 0 || id != before);
-    const int start = 31 - __clz(heads & (0xffffffffu >> (31 - lane)));
-    float x = t[q];
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-      const float y = __shfl_up_sync(0xffffffffu, x, d);
-      if (lane - d >= start) x += y;
-    }
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      if (32 * k >= b.buckets) break;
-      const int2 range = lane + 32 * k < b.buckets ? __ldg(b.range + lane + 32 * k) : make_int2(1, 0);
-      const int low = max(range.x, top - 31);
-      const float y = __shfl_sync(0xffffffffu, x, (top - low) & 31);
-      if (low <= min(range.y, top)) acc[k] += y;
-    }
-  }
 }
 
 }  // namespace gb300

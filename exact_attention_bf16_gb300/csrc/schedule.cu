@@ -36,10 +36,9 @@ constexpr int kThreads = 1024;
 constexpr int kSharedSeqs = 1024;  // up to so many sequences need no scratch in global memory
 
 // Block b < n_lists builds list b (a backward's two lists in one launch), the blocks behind them the tensor maps.
-__global__ void __launch_bounds__(kThreads, 1)
-    tile_list_kernel(const int* cu_q, const int* cu_k, int num_seqs, TileListSpec l0, TileListSpec l1, int n_lists,
-                     int64_t* scratch, uint32_t* zero_word, const __grid_constant__ SeqMaps maps) {
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the next kernel reads no list and no map
+__device__ __forceinline__ void tile_lists(const int* cu_q, const int* cu_k, int num_seqs, const TileListSpec& l0,
+                                           const TileListSpec& l1, int n_lists, int64_t* scratch, uint32_t* zero_word,
+                                           const SeqMaps& maps) {
   if (static_cast<int>(blockIdx.x) >= n_lists) {
     __shared__ alignas(128) uint32_t s_map[kThreads / 32][32];
     const int ln = static_cast<int>(threadIdx.x & 31u), wp = static_cast<int>(threadIdx.x >> 5);
@@ -146,10 +145,18 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
+__global__ void __launch_bounds__(kThreads, 1)
+    tile_list_kernel(const int* cu_q, const int* cu_k, int num_seqs, TileListSpec l0, TileListSpec l1, int n_lists,
+                     int64_t* scratch, uint32_t* zero_word, const __grid_constant__ SeqMaps maps) {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the next kernel reads no list and no map
+  tile_lists(cu_q, cu_k, num_seqs, l0, l1, n_lists, scratch, zero_word, maps);
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // behind the bias's layout: over before this one is
+}
+
 }  // namespace sched
 
 cudaError_t launch_tile_lists(const int* cu_q, const int* cu_k, int num_seqs, const TileListSpec* specs, int n,
-                              int64_t* scratch, uint32_t* zero_word, const SeqMaps& maps, cudaStream_t stream) {
+                              int64_t* scratch, uint32_t* zero_word, const SeqMaps& maps, bool early, cudaStream_t stream) {
   static_assert(sizeof(CUtensorMap) == 128, "a warp copies a map, four bytes a lane");
   if (num_seqs < 0 || n < 0 || n > 2 || maps.n < 0 || maps.n > kMaxSeqMaps || (maps.n > 0 && maps.out == nullptr) ||
       (reinterpret_cast<uintptr_t>(maps.out) & 127u))
@@ -166,9 +173,15 @@ cudaError_t launch_tile_lists(const int* cu_q, const int* cu_k, int num_seqs, co
     const int blocks = per_launch + (i == 0 ? map_blocks : 0);
     if (blocks == 0) break;
     const TileListSpec l0 = n > 0 ? specs[i] : TileListSpec{}, l1 = n > 0 ? specs[i + per_launch - 1] : TileListSpec{};
-    sched::tile_list_kernel<<<blocks, sched::kThreads, 0, stream>>>(cu_q, cu_k, num_seqs, l0, l1, per_launch, scratch,
-                                                                   zero_word, maps);
-    const cudaError_t e = cudaGetLastError();
+    cudaError_t e;
+    if (early && i == 0) {
+      e = launch_early(sched::tile_list_kernel, dim3(blocks), sched::kThreads, 0, stream, cu_q, cu_k, num_seqs, l0, l1, per_launch,
+                       scratch, zero_word, maps);
+    } else {
+      sched::tile_list_kernel<<<blocks, sched::kThreads, 0, stream>>>(cu_q, cu_k, num_seqs, l0, l1, per_launch, scratch,
+                                                                     zero_word, maps);
+      e = cudaGetLastError();
+    }
     if (e != cudaSuccess) return e;
     i += per_launch;
   } while (i < n);

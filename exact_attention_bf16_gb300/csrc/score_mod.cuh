@@ -10,8 +10,8 @@
 //   kModAlibi:   a' = a - m_h |j - (i + Nk - Nq)|, so s' = s - |slope (j - qpos)|
 //                with slope = m_h / scale and qpos = i + Nk - Nq (the query's
 //                position, aligned bottom-right like the causal mask).
-//   kModRelBias: a' = a + a learned bias of (head, j - qpos): rel_bias.cuh (in log2
-//                units, added where the kernels scale s).
+//   kModRelBias: a' = a + a learned bias of (head, j - qpos): rel_bias.cuh (over
+//                the scale, added to s).
 // tanh is evaluated as 1 - 2 / (1 + e^(2x)): one hardware exp2 (relative error
 // about 2^-22) and one hardware reciprocal, exact to a few fp32 ulps of 1.
 #pragma once

@@ -68,6 +68,11 @@ def attention64(q, k, v, table, far, two_sided, scale, causal, do=None):
         for z in range(table.shape[0]):
             out["dtable"][z, x] = (ds * (which == z)).sum()
             out["slack"][z, x] = (off * (which == z)).sum()
+    if do is not None:
+        # the bucket of the keys far ahead of their query may come as minus the sum of the others (a row's dS sum to zero), and is
+        # then off by what all of them are
+        left = (table.shape[0] // 2 if two_sided else table.shape[0]) - 1
+        out["slack"][left] = out["slack"].sum(0)
     return out
 
 

@@ -104,13 +104,13 @@ def test_workspaces_hold_the_bias(abi):
     _fill(p, abi)
     with_bias = lib.attn_fwd_workspace_size(ctypes.byref(p))
     p.score_mod = 0
-    # 4 heads x (2 x reach + 512) places, the reach the last border, 91 for 16 buckets a side up to 128
+    # 4 heads x (2 x reach + 320) places, the reach the last border, 91 for 16 buckets a side up to 128
     assert bucket(16, 128, 90) == 14 and bucket(16, 128, 91) == 15
-    assert with_bias - lib.attn_fwd_workspace_size(ctypes.byref(p)) == -(-4 * (2 * 91 + 512) * 4 // 256) * 256
+    assert with_bias - lib.attn_fwd_workspace_size(ctypes.byref(p)) == -(-4 * (2 * 91 + 320) * 4 // 256) * 256
     b = abi.AttnBwdParams()
     _fill(b.fwd, abi)
     b.fwd.seqlen_q = b.fwd.seqlen_k = 50  # reach 50
-    width = 2 * 50 + 512
+    width = 2 * 50 + 320
     left_out = lib.attn_bwd_workspace_size(ctypes.byref(b))
     b.drel_bias = FAKE
     whole = lib.attn_bwd_workspace_size(ctypes.byref(b))
@@ -118,4 +118,4 @@ def test_workspaces_hold_the_bias(abi):
     plain = lib.attn_bwd_workspace_size(ctypes.byref(b))
     up = lambda x: -(-x // 256) * 256  # noqa: E731
     assert left_out - plain == up(4 * width * 4) + up(width) + 128 * 8
-    assert whole - left_out == up(4 * 8 * 2 * 32 * 4)  # 8 warps, 2 sequences of one block, 32 buckets, 4 heads
+    assert whole - left_out == up(4 * 2 * 32 * 4)  # 2 sequences of one block, 32 buckets, 4 heads

@@ -69,12 +69,24 @@ _NO_REL = (0, 0, 0, 0, 0)
 
 def _mod_fields(q, softcap, alibi_slopes, rel_bias=None, rel_max_distance=128, rel_bidirectional=True):
     """(score_mod, softcap, alibi_slopes) and the bias's fields (rel_bias .. rel_bidirectional) of a call (attn_fwd)."""
-    if softcap is None and alibi_slopes is None and rel_bias is None:
-        return (0, 0.0, 0), _NO_REL
+    if softcap is None and alibi_slopes is None:
+        if rel_bias is None:
+            return (0, 0.0, 0), _NO_REL
+        return (_abi.SCORE_RELBIAS, 0.0, 0), _rel_fields(q, rel_bias, rel_max_distance, rel_bidirectional)
     p = AttnFwdParams()
-    _set_score_mod(p, q, softcap, alibi_slopes, rel_bias, rel_max_distance, rel_bidirectional)
-    return ((p.score_mod, p.softcap, p.alibi_slopes or 0),
-            (p.rel_bias or 0, p.rel_bias_dtype, p.rel_buckets, p.rel_max_distance, p.rel_bidirectional))
+    _set_score_mod(p, q, softcap, alibi_slopes, rel_bias)
+    return (p.score_mod, p.softcap, p.alibi_slopes or 0), _NO_REL
+
+
+def _rel_fields(q, t, rel_max_distance, rel_bidirectional):
+    """rel_bias .. rel_bidirectional of a checked table."""
+    if not isinstance(t, torch.Tensor) or t.dtype not in (_BF16, _F32) or not t.is_cuda or not t.is_contiguous() or \
+            t.dim() != 2 or t.shape[1] != q.shape[-2]:
+        raise ValueError(f"rel_bias must be a contiguous bfloat16 or float32 CUDA tensor [buckets, {q.shape[-2]}]")
+    if t.get_device() != q.get_device():
+        raise ValueError(f"rel_bias is on {t.device} but q is on {q.device}")
+    return (t.data_ptr(), _abi.TABLE_F32 if t.dtype is _F32 else _abi.TABLE_BF16, t.shape[0], int(rel_max_distance),
+            1 if rel_bidirectional else 0)
 
 
 def _check_int32(name: str, t, device: int, n: int):
@@ -159,16 +171,9 @@ def _set_score_mod(p: AttnFwdParams, q: torch.Tensor, softcap, alibi_slopes, rel
     if (softcap is not None) + (alibi_slopes is not None) + (rel_bias is not None) > 1:
         raise ValueError("choose one score modification: softcap, alibi_slopes or rel_bias")
     if rel_bias is not None:
-        t = rel_bias
-        if not isinstance(t, torch.Tensor) or t.dtype not in (_BF16, _F32) or not t.is_cuda or not t.is_contiguous() or \
-                t.dim() != 2 or t.shape[1] != q.shape[-2]:
-            raise ValueError(f"rel_bias must be a contiguous bfloat16 or float32 CUDA tensor [buckets, {q.shape[-2]}]")
-        if t.device != q.device:
-            raise ValueError(f"rel_bias is on {t.device} but q is on {q.device}")
-        p.score_mod, p.rel_bias = _abi.SCORE_RELBIAS, _ptr(t)
-        p.rel_bias_dtype = _abi.TABLE_F32 if t.dtype is _F32 else _abi.TABLE_BF16
-        p.rel_buckets, p.rel_max_distance = t.shape[0], int(rel_max_distance)
-        p.rel_bidirectional = 1 if rel_bidirectional else 0
+        p.score_mod = _abi.SCORE_RELBIAS
+        (p.rel_bias, p.rel_bias_dtype, p.rel_buckets, p.rel_max_distance, p.rel_bidirectional) = _rel_fields(
+            q, rel_bias, rel_max_distance, rel_bidirectional)
     elif softcap is not None:
         p.score_mod, p.softcap = _abi.SCORE_SOFTCAP, float(softcap)
     elif alibi_slopes is not None:
@@ -706,22 +711,23 @@ def _append_fields(k, v, k_cache, v_cache, slot_mapping):
             ks[0], ks[1], ks[2], vs[2], kcs[1], kcs[0]), ks
 
 
-def _check_rotation(cos, sin, device: int, rotary_offset: int):
+def _check_rotation(cos, sin, device: int, rotary_offset: int, head: int):
     """The checked tables' fields: pointers, row stride, positions, rotary_dim."""
-    for n, t in (("cos", cos), ("sin", sin)):
-        if not isinstance(t, torch.Tensor) or t.dtype is not _F32 or not t.is_cuda or t.dim() != 2 or \
-                (t.stride(1) != 1 and t.shape[1] > 1):
-            raise ValueError(f"{n} must be a float32 CUDA tensor [positions, rotary_dim / 2] with contiguous rows")
+    for name, t in (("cos", cos), ("sin", sin)):
+        if not isinstance(t, torch.Tensor) or t.dtype is not _F32 or not t.is_cuda or t.dim() != 2:
+            raise ValueError(f"{name} must be a float32 CUDA tensor [positions, rotary_dim / 2] with contiguous rows")
         if t.get_device() != device:
-            raise ValueError(f"{n} is on {t.device} but the call is on cuda:{device}")
+            raise ValueError(f"{name} is on {t.device} but the call is on cuda:{device}")
         if t.requires_grad and torch.is_grad_enabled():
-            raise ValueError(f"{n} has no gradient here: pass it detached")
-    n, half = cos.shape
-    if sin.shape != cos.shape or (n > 1 and sin.stride(0) != cos.stride(0)):
-        raise ValueError(f"cos {tuple(cos.shape)} and sin {tuple(sin.shape)} must be alike, strides too")
+            raise ValueError(f"{name} has no gradient here: pass it detached")
+    (n, half), (row, col) = cos.shape, cos.stride()
+    if sin.shape != cos.shape or (n > 1 and sin.stride() != (row, col)) or col != 1 or sin.stride(1) != 1:
+        raise ValueError(f"cos {tuple(cos.shape)} and sin {tuple(sin.shape)} must be alike, strides too, with contiguous rows")
     if half < 8 or half % 8 or rotary_offset < 0 or rotary_offset % 8:
         raise ValueError(f"rotary_dim {2 * half} must be a multiple of 16 and rotary_offset {rotary_offset} of 8")
-    return cos.data_ptr(), sin.data_ptr(), cos.stride(0) if n > 1 else half, n, 2 * half
+    if rotary_offset + 2 * half > head:
+        raise ValueError(f"columns {rotary_offset} .. {rotary_offset + 2 * half - 1} are not all of a head of {head}")
+    return cos.data_ptr(), sin.data_ptr(), row if n > 1 else half, n, 2 * half
 
 
 def attn_kv_append_rotary(q: Optional[torch.Tensor], k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor,
@@ -736,15 +742,13 @@ def attn_kv_append_rotary(q: Optional[torch.Tensor], k: torch.Tensor, v: torch.T
     append, ks = _append_fields(k, v, k_cache, v_cache, slot_mapping)
     dev = k.get_device()
     _check_int32("positions", positions, dev, ks[0])
-    cos_ptr, sin_ptr, row, n, dim = _check_rotation(cos, sin, dev, rotary_offset)
-    if rotary_offset + dim > ks[2]:
-        raise ValueError(f"columns {rotary_offset} .. {rotary_offset + dim - 1} are not all of a head of {ks[2]}")
+    cos_ptr, sin_ptr, row, n, dim = _check_rotation(cos, sin, dev, rotary_offset, ks[2])
     heads, qt, qo, q_ptr, out_ptr = 0, (0, 0), (0, 0), 0, 0
     if q is not None:
         qs, qt = _bf16_layout("q", q, 3)
         if qs[0] != ks[0] or qs[2] != ks[2] or q.get_device() != dev:
             raise ValueError(f"q {tuple(qs)} does not match k {tuple(ks)} on cuda:{dev}")
-        q_out, qo = _rotated("q_out", q_out, q, stream)
+        q_out, qo = _rotated("q_out", q_out, q, qs, stream)
         heads, q_ptr, out_ptr = qs[1], q.data_ptr(), q_out.data_ptr()
     elif q_out is not None:
         raise ValueError("q_out without q")
@@ -756,15 +760,17 @@ def attn_kv_append_rotary(q: Optional[torch.Tensor], k: torch.Tensor, v: torch.T
     return q_out
 
 
-def _rotated(name: str, out, like, stream):
-    """An output buffer for the rotated `like` (the given one, checked) and its strides."""
+def _rotated(name: str, out, like, shape, stream):
+    """An output buffer for the rotated `like` (the given one, checked) and its strides, the last one left out."""
     if out is None:
-        out = torch.empty(like.shape, dtype=_BF16, device=like.device)
+        out = torch.empty(shape, dtype=_BF16, device=like.device)
         if stream is not None:
             _used_on(stream, out)
-    elif out.shape != like.shape or out.device != like.device:
-        raise ValueError(f"{name} must be {tuple(like.shape)} on {like.device}, got {tuple(out.shape)} on {out.device}")
-    return out, _bf16_layout(name, out, like.dim())[1]
+        row = shape[-2] * shape[-1]
+        return out, (row, shape[-1]) if len(shape) == 3 else (shape[1] * row, row, shape[-1])
+    if out.shape != shape or out.get_device() != like.get_device():
+        raise ValueError(f"{name} must be {tuple(shape)} on {like.device}, got {tuple(out.shape)} on {out.device}")
+    return out, _bf16_layout(name, out, len(shape))[1][:-1]
 
 
 def attn_rotary(q: torch.Tensor, k: Optional[torch.Tensor], cos: torch.Tensor, sin: torch.Tensor,
@@ -778,41 +784,42 @@ def attn_rotary(q: torch.Tensor, k: Optional[torch.Tensor], cos: torch.Tensor, s
     is int32 [B, N] or [N] ([total]); without it a row's position is its index. ``inverse`` turns back: of the
     gradients of the outputs it gives those of the inputs. q_out and k_out may be q and k. Rows whose position lies
     outside the tables are not written. Returns (q_out, k_out)."""
-    dim = q.dim() if isinstance(q, torch.Tensor) and q.dim() == 3 else 4
+    dim = 3 if isinstance(q, torch.Tensor) and q.dim() == 3 else 4
     qs, qt = _bf16_layout("q", q, dim)
     dev = q.get_device()
-    batch, n = (qs[0], qs[1]) if dim == 4 else (1, qs[0])
-    cos_ptr, sin_ptr, row, n_pos, rot = _check_rotation(cos, sin, dev, rotary_offset)
-    if rotary_offset + rot > qs[-1]:
-        raise ValueError(f"columns {rotary_offset} .. {rotary_offset + rot - 1} are not all of a head of {qs[-1]}")
-    ks = kt = ko = None
+    cos_ptr, sin_ptr, row, n_pos, rot = _check_rotation(cos, sin, dev, rotary_offset, qs[-1])
+    heads_kv = k_ptr = ko_ptr = 0
     if k is not None:
         ks, kt = _bf16_layout("k", k, dim)
         if ks[:-2] != qs[:-2] or ks[-1] != qs[-1] or k.get_device() != dev:
             raise ValueError(f"k {tuple(ks)} does not match q {tuple(qs)} on cuda:{dev}")
-        k_out, ko = _rotated("k_out", k_out, k, stream)
+        k_out, ko = _rotated("k_out", k_out, k, ks, stream)
+        heads_kv, k_ptr, ko_ptr = ks[-2], k.data_ptr(), k_out.data_ptr()
     elif k_out is not None:
         raise ValueError("k_out without k")
-    q_out, qo = _rotated("q_out", q_out, q, stream)
-    pos_ptr, pos_batch = 0, 0
+    else:
+        kt = ko = (0, 0, 0)
+    q_out, qo = _rotated("q_out", q_out, q, qs, stream)
+    if dim == 4:
+        batch, n = qs[0], qs[1]
+        strides = (*qt[:3], *kt[:3], *qo, *ko)
+    else:
+        batch, n = 1, qs[0]
+        strides = (0, qt[0], qt[1], 0, kt[0], kt[1], 0, qo[0], qo[1], 0, ko[0], ko[1])
+    pos_ptr = pos_batch = 0
     if positions is not None:
         if dim == 4 and positions.dim() == 2:
             if positions.shape != (batch, n):
                 raise ValueError(f"positions must be [{batch}, {n}] or [{n}], got {tuple(positions.shape)}")
-            _check_int32("positions", positions.reshape(-1) if positions.is_contiguous() else positions, dev, batch * n)
+            _check_int32("positions", positions.view(-1) if positions.is_contiguous() else positions, dev, batch * n)
             pos_batch = n
         else:
             _check_int32("positions", positions, dev, n)
         pos_ptr = positions.data_ptr()
     elif n > n_pos:
         raise ValueError(f"{n} rows but the tables hold {n_pos} positions")
-    four = lambda s: (0, s[0], s[1]) if dim == 3 else s[:3]  # noqa: E731
-    none = (0, 0, 0)
-    p = _pack_rotary(q.data_ptr(), k.data_ptr() if k is not None else 0, q_out.data_ptr(),
-                     k_out.data_ptr() if k is not None else 0, *four(qt), *(four(kt) if k is not None else none), *four(qo),
-                     *(four(ko) if k is not None else none), pos_ptr, pos_batch, cos_ptr, sin_ptr, row, batch, n, qs[-2],
-                     ks[-2] if k is not None else 0, qs[-1], rot, rotary_offset, 1 if interleaved else 0, 1 if inverse else 0,
-                     n_pos)
+    p = _pack_rotary(q.data_ptr(), k_ptr, q_out.data_ptr(), ko_ptr, *strides, pos_ptr, pos_batch, cos_ptr, sin_ptr, row, batch,
+                     n, qs[-2], heads_kv, qs[-1], rot, rotary_offset, 1 if interleaved else 0, 1 if inverse else 0, n_pos)
     st = _lib.attn_rotary(p, _stream_of(stream, q))
     if st:
         _abi.check(st, "attn_rotary")

@@ -192,28 +192,26 @@ struct BigNum {
   }
 };
 
-// First distances of the n_b buckets of a side (include/attn.h); returns the last one, at least 1. Bucket m + k begins at the
-// least n with (n / m)^w >= (far / m)^k, w = n_b - m: a root that is no whole number by floating point, one that may be in
-// whole numbers, n^w m^k >= far^k m^w.
-int rel_borders(int n_b, int far, int* start) {
+// First distance of bucket m + k, m = n_b / 2, of a side's n_b: the least n with (n / m)^w >= (far / m)^k, w = n_b - m. A root that
+// is no whole number is found by floating point, one that may be in whole numbers, n^w m^k >= far^k m^w.
+int rel_border(int n_b, int far, int k) {
   const int m = n_b / 2, w = n_b - m;
-  for (int k = 0; k <= m && k < n_b; ++k) start[k] = k;
-  for (int k = 1; k < w && m > 0; ++k) {
-    const double x = m * std::pow(static_cast<double>(far) / m, static_cast<double>(k) / w);
-    const double near = std::floor(x + 0.5);
-    int n = static_cast<int>(std::ceil(x));
-    if (std::fabs(x - near) <= 1e-9 * x) {
-      n = static_cast<int>(near);
-      BigNum lhs, rhs;
-      lhs.times_power(static_cast<uint32_t>(n), w);
-      lhs.times_power(static_cast<uint32_t>(m), k);
-      rhs.times_power(static_cast<uint32_t>(far), k);
-      rhs.times_power(static_cast<uint32_t>(m), w);
-      if (!lhs.at_least(rhs)) ++n;
-    }
-    start[m + k] = n;
-  }
-  return std::max(1, start[n_b - 1]);
+  if (m == 0 || k == 0) return m;
+  const double x = m * std::pow(static_cast<double>(far) / m, static_cast<double>(k) / w);
+  const double near = std::floor(x + 0.5);
+  if (std::fabs(x - near) > 1e-9 * x) return static_cast<int>(std::ceil(x));
+  const int n = static_cast<int>(near);
+  BigNum lhs, rhs;
+  lhs.times_power(static_cast<uint32_t>(n), w);
+  lhs.times_power(static_cast<uint32_t>(m), k);
+  rhs.times_power(static_cast<uint32_t>(far), k);
+  rhs.times_power(static_cast<uint32_t>(m), w);
+  return lhs.at_least(rhs) ? n : n + 1;
+}
+// Beyond the last border (at least 1), or farther than any pair, the bias is one number to each side.
+int rel_reach(int n_b, int far, int64_t longest) {
+  const int last = std::max(1, rel_border(n_b, far, n_b - n_b / 2 - 1));
+  return static_cast<int>(std::min<int64_t>(last, std::max<int64_t>(longest, 1)));
 }
 
 template <typename P>  // attn_fwd_params or attn_paged_params
@@ -229,29 +227,38 @@ attn_status_t check_rel(const P* p) {
   return p->rel_max_distance > side / 2 && p->rel_max_distance <= 65536 ? ATTN_OK : ATTN_ERR_INVALID_ARG;
 }
 
-// The table's layout for calls whose queries and keys are at most `longest` apart, and its room in a workspace.
+// The layout of a call's table, whose queries and keys are at most `longest` apart: its reach (0: no bias) and room in a workspace.
 struct RelPlan {
-  RelTable table{};
+  int reach = 0;
   size_t place_bytes = 0, bucket_bytes = 0, range_bytes = 0;
 };
 template <typename P>
 RelPlan rel_plan(const P* p, int64_t longest) {
   RelPlan r;
   if (p->score_mod != ATTN_SCORE_RELBIAS || p->heads < 1 || check_rel(p) != ATTN_OK) return r;
-  RelTable& t = r.table;
+  r.reach = rel_reach(p->rel_bidirectional ? p->rel_buckets / 2 : p->rel_buckets, p->rel_max_distance, longest);
+  const int64_t width = 2 * static_cast<int64_t>(r.reach) + 2 * kRelPad;
+  r.place_bytes = round256(p->heads * width * 4);
+  r.bucket_bytes = round256(width);
+  r.range_bytes = kRelMaxBuckets * sizeof(int2);
+  return r;
+}
+// The table's layout, launched (b's arrays are set), and the rest of b.
+template <typename P>
+cudaError_t lay_out_rel(const P* p, const RelPlan& plan, RelBias* b, float* zero, int64_t n_zero, cudaStream_t stream) {
+  RelTable t{};
   t.table = p->rel_bias;
   t.inv_scale = 1.f / p->softmax_scale;
   t.f32 = p->rel_bias_dtype == ATTN_TABLE_F32;
   t.heads = p->heads;
-  t.buckets = p->rel_buckets;
+  t.buckets = b->buckets = p->rel_buckets;
   t.two_sided = p->rel_bidirectional ? 1 : 0;
   t.side = t.two_sided ? t.buckets / 2 : t.buckets;
-  t.reach = static_cast<int>(std::min<int64_t>(rel_borders(t.side, p->rel_max_distance, t.start), std::max<int64_t>(longest, 1)));
-  const int64_t width = 2 * t.reach + 2 * kRelPad;
-  r.place_bytes = round256(t.heads * width * 4);
-  r.bucket_bytes = round256(width);
-  r.range_bytes = kRelMaxBuckets * sizeof(int2);
-  return r;
+  t.reach = b->reach = plan.reach;
+  b->left = t.side - 1;
+  b->right = t.two_sided ? t.buckets - 1 : 0;
+  for (int k = 0; k < t.side; ++k) t.start[k] = k < t.side / 2 ? k : rel_border(t.side, p->rel_max_distance, k - t.side / 2);
+  return launch_rel_layout(t, *b, zero, n_zero, stream);
 }
 
 attn_status_t check_scores(float scale, int32_t score_mod, float softcap, const float* alibi_slopes) {
@@ -571,9 +578,7 @@ attn_status_t run_fwd(const attn_fwd_params* p, bool varlen, cudaStream_t stream
   auto lay_out_bias = [&]() -> cudaError_t {
     const RelPlan rp = call_rel_plan(p, varlen);
     a.rel.by_place = reinterpret_cast<const float*>(static_cast<uint8_t*>(ws) + need_ws - rp.place_bytes);
-    a.rel.reach = rp.table.reach;
-    a.rel.buckets = rp.table.buckets;
-    return launch_rel_layout(rp.table, a.rel, nullptr, 0, stream);
+    return lay_out_rel(p, rp, &a.rel, nullptr, 0, stream);
   };
   if (rel && lp.use) {
     e = lay_out_bias();
@@ -904,17 +909,13 @@ attn_status_t run_bwd(const attn_bwd_params* p, void* ws, size_t ws_bytes, bool 
     a.rel.by_place = reinterpret_cast<const float*>(at);
     a.rel.bucket = at + rp.place_bytes;
     a.rel.range = reinterpret_cast<const int2*>(at + rp.place_bytes + rp.bucket_bytes);
-    a.rel.reach = rp.table.reach;
-    a.rel.buckets = rp.table.buckets;
-    a.rel.left = rp.table.side - 1;
-    a.rel.right = rp.table.two_sided ? rp.table.buckets - 1 : 0;
     if (p->drel_bias) {
       a.rel.parts = reinterpret_cast<float*>(at + rp.place_bytes + rp.bucket_bytes + rp.range_bytes);
       a.rel.part_rows = bwd_rel_part_rows(p, varlen, dqs.splits);
     }
     // (dense: every CTA writes its own)
     const int64_t n_parts = varlen ? (f.heads * a.rel.part_rows * f.rel_buckets + 3) / 4 * 4 : 0;
-    e = launch_rel_layout(rp.table, a.rel, a.rel.parts, n_parts, stream);
+    e = lay_out_rel(&f, rp, &a.rel, a.rel.parts, n_parts, stream);
     if (e != cudaSuccess) return cuda_fail(e, "bias layout");
   }
 
@@ -1385,9 +1386,7 @@ attn_status_t run_fwd_paged(const attn_paged_params* p, void* ws, size_t ws_byte
   }
   if (p->score_mod == ATTN_SCORE_RELBIAS) {
     a.rel.by_place = reinterpret_cast<const float*>(base + pl.off_rel);
-    a.rel.reach = pl.rel.table.reach;
-    a.rel.buckets = pl.rel.table.buckets;
-    e = launch_rel_layout(pl.rel.table, a.rel, nullptr, 0, stream);
+    e = lay_out_rel(p, pl.rel, &a.rel, nullptr, 0, stream);
     if (e != cudaSuccess) return cuda_fail(e, "bias layout");
   }
   int dev = 0, sms = 0;

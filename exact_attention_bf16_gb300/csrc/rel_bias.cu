@@ -52,7 +52,7 @@ __global__ void __launch_bounds__(kThreads) layout_kernel(const __grid_constant_
 }
 
 // Table entry (bucket, head) = the sum of the head's parts, [rows][buckets]: a block per head, its threads' rows a stride
-// apart, then the threads' sums in order.
+// apart, then the threads' sums pair by pair.
 __global__ void __launch_bounds__(1024) sum_parts_kernel(const float* parts, int64_t rows, int buckets, int heads, void* out,
                                                          int f32) {
   __shared__ float s[1024];
@@ -67,8 +67,12 @@ __global__ void __launch_bounds__(1024) sum_parts_kernel(const float* parts, int
   }
   s[threadIdx.x] = sum;
   __syncthreads();
+  for (int n = lanes; n > 1; n = (n + 1) / 2) {  // the upper half onto the lower one
+    if (y < n / 2) s[threadIdx.x] += s[(y + (n + 1) / 2) * buckets + b];
+    __syncthreads();
+  }
   if (y == 0) {
-    for (int i = 1; i < lanes; ++i) sum += s[i * buckets + b];
+    sum = s[b];
     const int64_t at = static_cast<int64_t>(b) * heads + h;
     if (f32) static_cast<float*>(out)[at] = sum;
     else static_cast<__nv_bfloat16*>(out)[at] = __float2bfloat16_rn(sum);

@@ -82,6 +82,58 @@ def test_few_queries_over_long_keys_split(ea):
         _dense(ea, nq, 1, 2, 1, nq, 4100, 64, 64, False, True, 32, 900)
 
 
+@pytest.mark.parametrize("d,dv", [(64, 64), (128, 128), (192, 128)])
+@pytest.mark.parametrize("causal", [False, True])
+def test_reach_longer_than_shared_memory_holds(ea, d, dv, causal):
+    """The bias read from global memory: the dQ kernel's row from about 1000 (d = 64), 2600 and 1200 on."""
+    _dense(ea, d, 1, 1, 1, 2700, 2900, d, dv, causal, not causal, 32, 65536)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_reach_longer_than_shared_memory_holds_forward(ea, d):
+    """The forward's row from about 8200 (d = 64) and 4100 on."""
+    n = 9000 if d == 64 else 5000
+    _dense(ea, d, 1, 1, 1, 300, n, d, d, False, True, 16, 65536, backward=False)
+
+
+def test_backward_without_an_allocation_and_from_odd_workspaces(ea):
+    """attn_bwd_noalloc, and attn_bwd from a workspace that is only 16-byte aligned and no larger than needed."""
+    import ctypes
+    rng = np.random.default_rng(31)
+    q, k, v, do = (_t(rng, 1, 300, 2, 64) for _ in range(4))
+    table = log_table(rng, 32, 2, torch.float32)
+    kw = dict(rel_bias=table, rel_max_distance=60, softmax_scale=0.125)
+    o, lse = ea.attn_fwd(q, k, v, **kw)
+    want = ea.attn_bwd(q, k, v, o, lse, do, **kw)
+    lib, seen = ea._lib, {}
+
+    class Spy:  # the call's parameter struct
+        def __getattr__(self, name):
+            f = getattr(lib, name)
+            if name != "attn_bwd":
+                return f
+            return lambda p, *rest: seen.setdefault("p", p) and f(p, *rest)
+
+    ea._lib = Spy()
+    try:
+        got = ea.attn_bwd(q, k, v, o, lse, do, **kw)
+    finally:
+        ea._lib = lib
+    p, stream = seen["p"], ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+    size = lib.attn_bwd_workspace_size(p)
+    room = torch.full((size + 4096,), 0xff, dtype=torch.uint8, device="cuda")
+    base = -(-room.data_ptr() // 256) * 256 + 16
+    for call in (lambda: lib.attn_bwd_noalloc(p, stream), lambda: lib.attn_bwd(p, ctypes.c_void_p(base), size, stream)):
+        for t in got:
+            t.fill_(5.0)
+        assert call() == 0
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+    end = base - room.data_ptr() + size
+    assert (room[end:] == 0xff).all()
+    assert lib.attn_bwd(p, ctypes.c_void_p(base), size - 1, stream) != 0
+
+
 def test_masked_buckets(ea):
     """-inf masks a bucket; rows that it leaves without keys give 0 and -inf."""
     def far_only(table, clean):

@@ -1505,6 +1505,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool left_out = false;
     bool rows_ok = true;  // every row of the warp has keys
     if constexpr (MOD == kModRelBias) {
+      rel_grad.prefetch(rel.global() - a.rel.reach - kDqRelPad, static_cast<int>(threadIdx.x), kSoftThreads);
       rows_ok = __all_sync(0xffffffffu, lse2 != INFINITY);
     }
     bool ok = mbar_wait_warp(&bar->q_full, 0, a.status, 0x2301);

@@ -79,6 +79,11 @@ __device__ __forceinline__ float ld_shared_f32(uint32_t addr) {
   asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
   return v;
 }
+// A load of the byte at p whose value nothing waits for: it brings p's line into L1.
+__device__ __forceinline__ void touch_global(const void* p) {
+  uint32_t v;
+  asm volatile("ld.global.nc.u8 %0, [%1];" : "=r"(v) : "l"(p));
+}
 __device__ __forceinline__ int ld_shared_u8(uint32_t addr) {
   int v;
   asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");

@@ -487,6 +487,21 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     for (int t = 0; t < T && ok; ++t) {
       const int q0 = q_row(GQA ? tt : t);
+      // relative position bias of this thread's logits: one number where the warp's places (32 keys, 32 queries) have one, else a
+      // load each, on its way while the logits are (r0: the place of the thread's key at its first query column)
+      float bias[32];
+      if constexpr (MOD == kModRelBias) {
+        const int r0 = kj - q0 - 32 * wg - (U.nk - U.nq);
+        float add;
+        if (rel.far(r0 - static_cast<int>(lane) - 31, r0 - static_cast<int>(lane) + 31, rel_far, add)) {
+#pragma unroll
+          for (int e = 0; e < 32; ++e) bias[e] = add;
+        } else {
+          const float* at = rel.global() + r0;
+#pragma unroll
+          for (int e = 0; e < 32; ++e) bias[e] = __ldg(at - e);
+        }
+      }
       ok = mbar_wait_warp(&bar->s_full, static_cast<uint32_t>(t) & 1u, a.status, 0x1300);
       // this tile's (-LSE*log2e, -D) vectors, written by the loader lanes
       if (ok) ok = mbar_wait_warp(&bar->st_full[t % C::NST], static_cast<uint32_t>(t / C::NST) & 1u, a.status, 0x1302);
@@ -504,14 +519,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t pw[16], dw[16];
       // ALiBi: slope * (kj - qpos) of this warpgroup's first query column
       const float abase = alibi_slope * static_cast<float>(kj - q0 - 32 * wg - (U.nk - U.nq));
-      // relative position bias: the place of this thread's key at its first query column, and where the warp's places
-      // (32 keys, 32 queries) have one bias, that
-      const int r0 = kj - q0 - 32 * wg - (U.nk - U.nq);
-      float radd = 0.f;
-      const bool near = MOD == kModRelBias && !rel.far(r0 - static_cast<int>(lane) - 31, r0 - static_cast<int>(lane) + 31, rel_far, radd);
-      radd *= sl2;
-      const float* rel_at = MOD == kModRelBias ? rel.global() + r0 : nullptr;
-      auto pair = [&](int e, float2 nl, float2 nd, bool mask, bool by_place) {
+      if constexpr (MOD == kModRelBias) {
+#pragma unroll
+        for (int e = 0; e < 32; ++e) s[e] = __float_as_uint(__uint_as_float(s[e]) + bias[e]);
+      }
+      auto pair = [&](int e, float2 nl, float2 nd, bool mask) {
         const int col = 32 * wg + e;
         float s0 = __uint_as_float(s[e]), s1 = __uint_as_float(s[e + 1]);
         float2 f = make_float2(1.f, 1.f);  // derivative of the score modification
@@ -523,10 +535,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         } else if constexpr (MOD == kModAlibi) {
           s0 -= fabsf(fmaf(-alibi_slope, static_cast<float>(e), abase));
           s1 -= fabsf(fmaf(-alibi_slope, static_cast<float>(e + 1), abase));
-        }
-        if constexpr (MOD == kModRelBias) {
-          if (by_place) s0 += __ldg(rel_at - e), s1 += __ldg(rel_at - e - 1);
-          else nl = fadd2(nl, make_float2(radd, radd));
         }
         const float2 x = ffma2(make_float2(s0, s1), sl2v, nl);
         float2 p = make_float2(ex2_mufu(x.x), ex2_mufu(x.y));
@@ -541,20 +549,19 @@ __global__ void __launch_bounds__(kThreads, 1)
         pw[e / 2] = pack_bf16x2(p.x, p.y);
         dw[e / 2] = pack_bf16x2(ds.x, ds.y);
       };
-      auto row = [&](bool mask, bool by_place) {
+      auto row = [&](bool mask) {
 #pragma unroll
         for (int e = 0; e < 32; e += 4) {
           const float4 nl = *reinterpret_cast<const float4*>(vL + e);
           const float4 nd = *reinterpret_cast<const float4*>(vD + e);
-          pair(e, make_float2(nl.x, nl.y), make_float2(nd.x, nd.y), mask, by_place);
-          pair(e + 2, make_float2(nl.z, nl.w), make_float2(nd.z, nd.w), mask, by_place);
+          pair(e, make_float2(nl.x, nl.y), make_float2(nd.x, nd.y), mask);
+          pair(e + 2, make_float2(nl.z, nl.w), make_float2(nd.z, nd.w), mask);
         }
       };
       // Queries past the end already give P = 0 through -LSE*log2e = -inf, so only
       // the causal boundary and a key row past the end need the per-element test.
-      if (MOD == kModRelBias && near) row(true, true);
-      else if (key_ok && q0 + 32 * wg >= i_vis && (MOD != kModRelBias || q0 + 32 * wg + 32 <= U.nq)) row(false, false);
-      else row(true, false);
+      if (key_ok && q0 + 32 * wg >= i_vis && (MOD != kModRelBias || q0 + 32 * wg + 32 <= U.nq)) row(false);
+      else row(true);
       if (t > 0) {  // dV(t-1), dK(t-1) (and dQ(t-1)) must have read the previous P^T, dS^T
         ok = mbar_wait_warp(&bar->pds_free, static_cast<uint32_t>(t - 1) & 1u, a.status, 0x1305);
         if (!ok) break;

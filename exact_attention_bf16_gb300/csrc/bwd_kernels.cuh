@@ -983,6 +983,22 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int t = 0; t < T && ok; ++t) {
       const int q0 = q_row(GQA ? tt : t) + 64 * wg;  // this warpgroup's first query
       const uint32_t col = region(t) + 64 * wg;
+      // relative position bias, loaded while the logits are on their way: where all places of the warp (32 keys, 64 queries) have
+      // one, it goes into the queries' offsets (radd); else the thread's 64 logits lie on 22 diagonals, two by two: bias[i] of the
+      // places 24 - 8 i and 23 - 8 i from its key row g of lane group 0 at query column 2c
+      float radd = 0.f;
+      bool near = false;
+      float2 bias[11];
+      if constexpr (MOD == kModRelBias) {
+        const int rw = k0 + static_cast<int>(quarter) * 32 - q0 - (U.nk - U.nq);  // the warp's first key at its first query
+        near = !rel.far(rw - 63, rw + 31, rel_far, radd);
+        radd *= a.scale_log2;
+        if (near) {
+          const float* at = rel.global() + (rw + g - 2 * c);
+#pragma unroll
+          for (int i = 0; i < 11; ++i) bias[i] = make_float2(__ldg(at + 24 - 8 * i), __ldg(at + 23 - 8 * i));
+        }
+      }
       // ---- phase A: P from S^T(t), written over S^T(t) as bf16 P^T
       ok = mbar_wait_warp(&bar->s_full, static_cast<uint32_t>(t) & 1u, a.status, 0x1430) &&
            mbar_wait_warp(&bar->v_full[t % C::NVEC], static_cast<uint32_t>(t / C::NVEC) & 1u, a.status, 0x1431);
@@ -1000,77 +1016,69 @@ __global__ void __launch_bounds__(kThreads, 1)
         nlv[r] = make_float2(x.x, x.y);
         nlv[r + 4] = make_float2(x.z, x.w);
       }
-      // relative position bias: the place of key row g of lane group 0 at query column 2c; where all places of the warp (32
-      // keys, 64 queries) have one bias, it goes into the queries' offsets
-      const int r0 = k0 + static_cast<int>(quarter) * 32 + g - q0 - 2 * c - (U.nk - U.nq);
-      bool near = false;
       if constexpr (MOD == kModRelBias) {
-        float add;
-        const int rw = r0 - g + 2 * c;  // the warp's first key at its first query
-        near = !rel.far(rw - 63, rw + 31, rel_far, add);
-        add *= a.scale_log2;
 #pragma unroll
-        for (int r = 0; r < 8; ++r) nlv[r] = fadd2(nlv[r], make_float2(add, add));
+        for (int r = 0; r < 8; ++r) nlv[r] = fadd2(nlv[r], make_float2(radd, radd));
       }
       float p[2][32];
       auto phase_a = [&](auto by_place) {
 #pragma unroll
-      for (int lg = 0; lg < 2; ++lg) {
-        uint32_t sv[32], pw[16];
-        tmem_ld16x256b_x8(lanes(lg) + col, sv);
-        tmem_wait_ld();
-        // ALiBi: slope * (kj - qpos) of key rows g, g + 8 at query column 2c
-        float abase[2];
+        for (int lg = 0; lg < 2; ++lg) {
+          uint32_t sv[32], pw[16];
+          tmem_ld16x256b_x8(lanes(lg) + col, sv);
+          tmem_wait_ld();
+          // ALiBi: slope * (kj - qpos) of key rows g, g + 8 at query column 2c
+          float abase[2];
 #pragma unroll
-        for (int hh = 0; hh < 2; ++hh) {
-          const int kj = k0 + static_cast<int>(quarter) * 32 + 16 * lg + 8 * hh + g;
-          abase[hh] = alibi_slope * static_cast<float>(kj - q0 - 2 * c - (U.nk - U.nq));
-        }
-#pragma unroll
-        for (int r = 0; r < 8; ++r) {
-          const float2 nl = nlv[r];
-          float sm[4], fz[4];  // modified logits and the modification's derivative
-#pragma unroll
-          for (int u = 0; u < 4; ++u) {
-            float sx = __uint_as_float(sv[4 * r + u]);
-            fz[u] = 1.f;
-            if constexpr (MOD == kModSoftcap) {
-              const float tt = tanh_scaled(sx, a.mod_k2);
-              sx = a.mod_b * tt;
-              fz[u] = fmaf(-tt, tt, 1.f);
-            } else if constexpr (MOD == kModAlibi) {
-              sx -= fabsf(fmaf(-alibi_slope, static_cast<float>(8 * r + (u & 1)), abase[u >> 1]));
-            }
-            sm[u] = sx;
+          for (int hh = 0; hh < 2; ++hh) {
+            const int kj = k0 + static_cast<int>(quarter) * 32 + 16 * lg + 8 * hh + g;
+            abase[hh] = alibi_slope * static_cast<float>(kj - q0 - 2 * c - (U.nk - U.nq));
           }
-          if constexpr (decltype(by_place)::value) {
-            const float* at = rel.global() + (r0 + 16 * lg - 8 * r);
-            sm[0] += __ldg(at), sm[1] += __ldg(at - 1);
-            sm[2] += __ldg(at + 8), sm[3] += __ldg(at + 7);
-          }
-          const float2 x0 = ffma2(make_float2(sm[0], sm[1]), sl2v, nl);
-          const float2 x1 = ffma2(make_float2(sm[2], sm[3]), sl2v, nl);
-          float* pp = &p[lg][4 * r];
-          pp[0] = ex2_mufu(x0.x);
-          pp[1] = ex2_mufu(x0.y);
-          pp[2] = ex2_mufu(x1.x);
-          pp[3] = ex2_mufu(x1.y);
-          if (!full) {
+#pragma unroll
+          for (int r = 0; r < 8; ++r) {
+            const float2 nl = nlv[r];
+            float sm[4], fz[4];  // modified logits and the modification's derivative
 #pragma unroll
             for (int u = 0; u < 4; ++u) {
-              const int qi = q0 + 8 * r + 2 * c + (u & 1);
-              if (!(kok[lg][u >> 1] && qi >= vis[lg][u >> 1] && (MOD != kModRelBias || qi < U.nq))) pp[u] = 0.f;
+              float sx = __uint_as_float(sv[4 * r + u]);
+              fz[u] = 1.f;
+              if constexpr (MOD == kModSoftcap) {
+                const float tt = tanh_scaled(sx, a.mod_k2);
+                sx = a.mod_b * tt;
+                fz[u] = fmaf(-tt, tt, 1.f);
+              } else if constexpr (MOD == kModAlibi) {
+                sx -= fabsf(fmaf(-alibi_slope, static_cast<float>(8 * r + (u & 1)), abase[u >> 1]));
+              }
+              sm[u] = sx;
+            }
+            if constexpr (decltype(by_place)::value) {
+              const float2 b0 = bias[3 - 2 * lg + r], b1 = bias[2 - 2 * lg + r];
+              sm[0] += b0.x, sm[1] += b0.y;
+              sm[2] += b1.x, sm[3] += b1.y;
+            }
+            const float2 x0 = ffma2(make_float2(sm[0], sm[1]), sl2v, nl);
+            const float2 x1 = ffma2(make_float2(sm[2], sm[3]), sl2v, nl);
+            float* pp = &p[lg][4 * r];
+            pp[0] = ex2_mufu(x0.x);
+            pp[1] = ex2_mufu(x0.y);
+            pp[2] = ex2_mufu(x1.x);
+            pp[3] = ex2_mufu(x1.y);
+            if (!full) {
+#pragma unroll
+              for (int u = 0; u < 4; ++u) {
+                const int qi = q0 + 8 * r + 2 * c + (u & 1);
+                if (!(kok[lg][u >> 1] && qi >= vis[lg][u >> 1] && (MOD != kModRelBias || qi < U.nq))) pp[u] = 0.f;
+              }
+            }
+            pw[2 * r] = pack_bf16x2(pp[0], pp[1]);
+            pw[2 * r + 1] = pack_bf16x2(pp[2], pp[3]);
+            if constexpr (MOD == kModSoftcap) {  // phase B then computes dS = P f (dP - D)
+#pragma unroll
+              for (int u = 0; u < 4; ++u) pp[u] *= fz[u];
             }
           }
-          pw[2 * r] = pack_bf16x2(pp[0], pp[1]);
-          pw[2 * r + 1] = pack_bf16x2(pp[2], pp[3]);
-          if constexpr (MOD == kModSoftcap) {  // phase B then computes dS = P f (dP - D)
-#pragma unroll
-            for (int u = 0; u < 4; ++u) pp[u] *= fz[u];
-          }
+          tmem_st16x128b_x8(lanes(lg) + col, pw);
         }
-        tmem_st16x128b_x8(lanes(lg) + col, pw);
-      }
       };
       if (MOD == kModRelBias && near) phase_a(std::integral_constant<bool, MOD == kModRelBias>{});
       else phase_a(std::false_type{});

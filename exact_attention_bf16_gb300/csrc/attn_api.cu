@@ -258,6 +258,12 @@ cudaError_t lay_out_rel(const P* p, const RelPlan& plan, RelBias* b, float* zero
   b->left = t.side - 1;
   b->right = t.two_sided ? t.buckets - 1 : 0;
   for (int k = 0; k < t.side; ++k) t.start[k] = k < t.side / 2 ? k : rel_border(t.side, p->rel_max_distance, k - t.side / 2);
+  // Up to `reach`, that is, which no pair exceeds. (The kernels for wide buckets ask every tile within the reach whether it lies in
+  // one: B4 H16 N4096 d64, 32 buckets up to 8192, forward and backward 2530 -> 1960 us; up to 128, 1676 -> 1697.)
+  for (int k = 0; k < t.side; ++k) {
+    const int end = std::min(k + 1 < t.side ? t.start[k + 1] : plan.reach, plan.reach);
+    if (end - t.start[k] > kRelWide) b->wide = 1;
+  }
   return launch_rel_layout(t, *b, zero, n_zero, stream);
 }
 
@@ -442,7 +448,8 @@ size_t fwd_workspace_bytes(const attn_fwd_params* p, bool varlen) {
   const size_t v16 = fwd_v16_bytes(p, varlen);
   if (!v16) return 0;
   const ListPlan lp = fwd_list_plan(p, varlen);
-  return 256 + v16 + call_rel_plan(p, varlen).place_bytes + (lp.use ? lp.list_bytes + seq_scratch_bytes(p->num_seqs) : 0) +
+  const RelPlan rp = call_rel_plan(p, varlen);
+  return 256 + v16 + rp.place_bytes + rp.bucket_bytes + (lp.use ? lp.list_bytes + seq_scratch_bytes(p->num_seqs) : 0) +
          fwd_split_bytes(p, fwd_split_plan(p, varlen));
 }
 
@@ -577,7 +584,8 @@ attn_status_t run_fwd(const attn_fwd_params* p, bool varlen, cudaStream_t stream
   const bool rel = p->score_mod == ATTN_SCORE_RELBIAS;
   auto lay_out_bias = [&]() -> cudaError_t {
     const RelPlan rp = call_rel_plan(p, varlen);
-    a.rel.by_place = reinterpret_cast<const float*>(static_cast<uint8_t*>(ws) + need_ws - rp.place_bytes);
+    a.rel.bucket = static_cast<uint8_t*>(ws) + need_ws - rp.bucket_bytes;
+    a.rel.by_place = reinterpret_cast<const float*>(a.rel.bucket - rp.place_bytes);
     return lay_out_rel(p, rp, &a.rel, nullptr, 0, stream);
   };
   if (rel && lp.use) {
@@ -1335,7 +1343,7 @@ PagedPlan paged_plan(const attn_paged_params* p) {
   }
   pl.rel = rel_plan(p, std::max<int64_t>(static_cast<int64_t>(p->max_pages) * p->page_size, p->max_seqlen_q));
   pl.off_rel = pl.bytes;
-  pl.bytes += pl.rel.place_bytes;
+  pl.bytes += pl.rel.place_bytes + pl.rel.bucket_bytes;
   return pl;
 }
 
@@ -1386,6 +1394,7 @@ attn_status_t run_fwd_paged(const attn_paged_params* p, void* ws, size_t ws_byte
   }
   if (p->score_mod == ATTN_SCORE_RELBIAS) {
     a.rel.by_place = reinterpret_cast<const float*>(base + pl.off_rel);
+    a.rel.bucket = base + pl.off_rel + pl.rel.place_bytes;
     e = lay_out_rel(p, pl.rel, &a.rel, nullptr, 0, stream);
     if (e != cudaSuccess) return cuda_fail(e, "bias layout");
   }

@@ -1,26 +1,13 @@
 // Forward variants with a learned relative position bias (rel_bias.cuh): the
 // kernel of fwd_kernel.cuh, dense and tile-list (packed variable length).
-#include "fwd_kernel.cuh"
+#include "attn_fwd_rel.cuh"
 
 namespace gb300 {
-namespace fwd {
-
-template <int DQK, int DV>
-cudaError_t launch_r(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const CUtensorMap& tv16,
-                     const FwdArgs& a, cudaStream_t stream) {
-  if (a.tiles != nullptr) return launch_e<DQK, DV, 0, false, false, true, kModRelBias>(tq, tk, tv, tv16, a, stream);
-  return launch_e<DQK, DV, 0, false, false, false, kModRelBias>(tq, tk, tv, tv16, a, stream);
-}
-
-}  // namespace fwd
 
 cudaError_t launch_fwd_rel(int d_qk, int d_v, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                            const CUtensorMap& tv16, const FwdArgs& a, cudaStream_t stream) {
-  if (a.emu_period != 0 || a.kv_count != nullptr || a.rel.by_place == nullptr) return cudaErrorInvalidValue;
-  if (d_qk == 64 && d_v == 64) return fwd::launch_r<64, 64>(tq, tk, tv, tv16, a, stream);
-  if (d_qk == 128 && d_v == 128) return fwd::launch_r<128, 128>(tq, tk, tv, tv16, a, stream);
-  if (d_qk == 192 && d_v == 128) return fwd::launch_r<192, 128>(tq, tk, tv, tv16, a, stream);
-  return cudaErrorInvalidValue;
+  return a.rel.wide ? launch_fwd_rel_wide(d_qk, d_v, tq, tk, tv, tv16, a, stream)
+                    : fwd::launch_rel<kModRelBias>(d_qk, d_v, tq, tk, tv, tv16, a, stream);
 }
 
 }  // namespace gb300

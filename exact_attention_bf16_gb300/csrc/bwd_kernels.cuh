@@ -431,7 +431,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     int tt = 0, hq = hq_first;  // step within the query head hq
     float alibi_slope = MOD == kModAlibi ? __ldg(a.alibi_slopes + hq) * a.inv_scale : 0.f;  // raw units
     RelRow<kRelPad> rel{a.rel, 0, hq};
-    float2 rel_far = MOD == kModRelBias ? rel.both() : make_float2(0.f, 0.f);  // the bias beyond the reach, left and right
+    float2 rel_far = is_rel(MOD) ? rel.both() : make_float2(0.f, 0.f);  // the bias beyond the reach, left and right
     const uint32_t my_cols = C::tS + 32 * wg;     // this warpgroup's S^T columns
     const uint32_t my_pds = C::tPdS + 32 * wg;    // its P^T (16) and dS^T (16) columns
     bool ok = mbar_wait_warp(&bar->kv_full, 0, a.status, 0x1301);
@@ -490,10 +490,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       // relative position bias of this thread's logits: one number where the warp's places (32 keys, 32 queries) have one, else a
       // load each, on its way while the logits are (r0: the place of the thread's key at its first query column)
       float bias[32];
-      if constexpr (MOD == kModRelBias) {
+      if constexpr (is_rel(MOD)) {
         const int r0 = kj - q0 - 32 * wg - (U.nk - U.nq);
+        const int low = r0 - static_cast<int>(lane) - 31;
         float add;
-        if (rel.far(r0 - static_cast<int>(lane) - 31, r0 - static_cast<int>(lane) + 31, rel_far, add)) {
+        int id;
+        bool same = rel.far(low, low + 62, rel_far, add);
+        if constexpr (MOD == kModRelWide) same = same || rel.far_or_one(low, low + 62, add, id);
+        if (same) {
 #pragma unroll
           for (int e = 0; e < 32; ++e) bias[e] = add;
         } else {
@@ -519,7 +523,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t pw[16], dw[16];
       // ALiBi: slope * (kj - qpos) of this warpgroup's first query column
       const float abase = alibi_slope * static_cast<float>(kj - q0 - 32 * wg - (U.nk - U.nq));
-      if constexpr (MOD == kModRelBias) {
+      if constexpr (is_rel(MOD)) {
 #pragma unroll
         for (int e = 0; e < 32; ++e) s[e] = __float_as_uint(__uint_as_float(s[e]) + bias[e]);
       }
@@ -540,7 +544,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         float2 p = make_float2(ex2_mufu(x.x), ex2_mufu(x.y));
         if (mask) {
           // (with a bias also the queries past the end: it may be a NaN at places that no query has)
-          const bool in0 = MOD != kModRelBias || q0 + col < U.nq, in1 = MOD != kModRelBias || q0 + col + 1 < U.nq;
+          const bool in0 = !is_rel(MOD) || q0 + col < U.nq, in1 = !is_rel(MOD) || q0 + col + 1 < U.nq;
           if (!(key_ok && q0 + col >= i_vis && in0)) p.x = 0.f;
           if (!(key_ok && q0 + col + 1 >= i_vis && in1)) p.y = 0.f;
         }
@@ -560,7 +564,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       };
       // Queries past the end already give P = 0 through -LSE*log2e = -inf, so only
       // the causal boundary and a key row past the end need the per-element test.
-      if (key_ok && q0 + 32 * wg >= i_vis && (MOD != kModRelBias || q0 + 32 * wg + 32 <= U.nq)) row(false);
+      if (key_ok && q0 + 32 * wg >= i_vis && (!is_rel(MOD) || q0 + 32 * wg + 32 <= U.nq)) row(false);
       else row(true);
       if (t > 0) {  // dV(t-1), dK(t-1) (and dQ(t-1)) must have read the previous P^T, dS^T
         ok = mbar_wait_warp(&bar->pds_free, static_cast<uint32_t>(t - 1) & 1u, a.status, 0x1305);
@@ -593,7 +597,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           tt = 0, ++hq;
           if (MOD == kModAlibi && t + 1 < T) alibi_slope = __ldg(a.alibi_slopes + hq) * a.inv_scale;
           rel.h = hq;
-          if (MOD == kModRelBias && t + 1 < T) rel_far = rel.both();
+          if (is_rel(MOD) && t + 1 < T) rel_far = rel.both();
         }
       }
       if constexpr (FUSED) {
@@ -977,7 +981,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     int tt = 0, hq = hq_first;  // step within the query head hq
     float alibi_slope = MOD == kModAlibi ? __ldg(a.alibi_slopes + hq) * a.inv_scale : 0.f;  // raw units
     RelRow<kRelPad> rel{a.rel, 0, hq};
-    float2 rel_far = MOD == kModRelBias ? rel.both() : make_float2(0.f, 0.f);  // the bias beyond the reach, left and right
+    float2 rel_far = is_rel(MOD) ? rel.both() : make_float2(0.f, 0.f);  // the bias beyond the reach, left and right
     auto lanes = [&](int lg) { return tbase + ((quarter * 32u + 16u * static_cast<uint32_t>(lg)) << 16); };
     bool ok = true;
     for (int t = 0; t < T && ok; ++t) {
@@ -989,9 +993,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       float radd = 0.f;
       bool near = false;
       float2 bias[11];
-      if constexpr (MOD == kModRelBias) {
+      if constexpr (is_rel(MOD)) {
         const int rw = k0 + static_cast<int>(quarter) * 32 - q0 - (U.nk - U.nq);  // the warp's first key at its first query
+        int id;
         near = !rel.far(rw - 63, rw + 31, rel_far, radd);
+        if constexpr (MOD == kModRelWide) near = near && !rel.far_or_one(rw - 63, rw + 31, radd, id);
         radd *= a.scale_log2;
         if (near) {
           const float* at = rel.global() + (rw + g - 2 * c);
@@ -1008,7 +1014,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const float4* vD = vL + QB / 4;
       // every (key, query) cell of this thread is visible (with a relative position bias, which may be a NaN at places that no
       // query has: also a query's)
-      const bool full = all_keys && q0 >= vis_max && (MOD != kModRelBias || q0 + 64 <= U.nq);
+      const bool full = all_keys && q0 >= vis_max && (!is_rel(MOD) || q0 + 64 <= U.nq);
       float2 nlv[8];  // -LSE*log2e of this thread's 16 queries (the same for both lane groups)
 #pragma unroll
       for (int r = 0; r < 4; ++r) {  // queries 8r + 2c, +1 and 8(r + 4) + 2c, +1 in one 16-byte load
@@ -1016,7 +1022,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         nlv[r] = make_float2(x.x, x.y);
         nlv[r + 4] = make_float2(x.z, x.w);
       }
-      if constexpr (MOD == kModRelBias) {
+      if constexpr (is_rel(MOD)) {
 #pragma unroll
         for (int r = 0; r < 8; ++r) nlv[r] = fadd2(nlv[r], make_float2(radd, radd));
       }
@@ -1067,7 +1073,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
               for (int u = 0; u < 4; ++u) {
                 const int qi = q0 + 8 * r + 2 * c + (u & 1);
-                if (!(kok[lg][u >> 1] && qi >= vis[lg][u >> 1] && (MOD != kModRelBias || qi < U.nq))) pp[u] = 0.f;
+                if (!(kok[lg][u >> 1] && qi >= vis[lg][u >> 1] && (!is_rel(MOD) || qi < U.nq))) pp[u] = 0.f;
               }
             }
             pw[2 * r] = pack_bf16x2(pp[0], pp[1]);
@@ -1080,7 +1086,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           tmem_st16x128b_x8(lanes(lg) + col, pw);
         }
       };
-      if (MOD == kModRelBias && near) phase_a(std::integral_constant<bool, MOD == kModRelBias>{});
+      if (is_rel(MOD) && near) phase_a(std::integral_constant<bool, is_rel(MOD)>{});
       else phase_a(std::false_type{});
       // ---- phase B: dS = P (dP - D) from dP^T(t), written next to P^T
       ok = mbar_wait_warp(&bar->dp_full, static_cast<uint32_t>(t) & 1u, a.status, 0x1432);
@@ -1127,7 +1133,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           tt = 0, ++hq;
           if (MOD == kModAlibi && t + 1 < T) alibi_slope = __ldg(a.alibi_slopes + hq) * a.inv_scale;
           rel.h = hq;
-          if (MOD == kModRelBias && t + 1 < T) rel_far = rel.both();
+          if (is_rel(MOD) && t + 1 < T) rel_far = rel.both();
         }
       }
     }
@@ -1519,7 +1525,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     float right_sum = 0.f;
     bool left_out = false;
     bool rows_ok = true;  // every row of the warp has keys
-    if constexpr (MOD == kModRelBias) {
+    if constexpr (is_rel(MOD)) {
       rel_grad.prefetch(rel.global() - a.rel.reach - kDqRelPad, static_cast<int>(threadIdx.x), kSoftThreads);
       rows_ok = __all_sync(0xffffffffu, lse2 != INFINITY);
     }
@@ -1532,10 +1538,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_before();
     __syncwarp();
     if (lane == 0) mbar_arrive(&bar->qd_tmem);
-    if constexpr (MOD == kModRelBias) {
+    if constexpr (is_rel(MOD)) {
       if constexpr (C::DO_TMEM) named_barrier_sync(1, kSoftThreads);  // every warp has taken its dO
       rel_grad.load(static_cast<int>(threadIdx.x), kSoftThreads);
-      if (a.rel.in_smem) rel.load(static_cast<int>(threadIdx.x), kSoftThreads);
+      if (a.rel.in_smem) {
+        rel.load(static_cast<int>(threadIdx.x), kSoftThreads);
+        if constexpr (MOD == kModRelWide) rel.load_buckets(static_cast<int>(threadIdx.x), kSoftThreads);
+      }
       named_barrier_sync(1, kSoftThreads);
     }
     const float2 sl2v = make_float2(sl2, sl2), nl = make_float2(-lse2, -lse2), nd = make_float2(-dsum, -dsum);
@@ -1544,10 +1553,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       // place of this row at its first column, r00: of the warp's first)
       const int r0 = key_block(t) * KB + wg * 64 - i - (U.nk - U.nq), r00 = r0 + static_cast<int>(lane);
       float radd = 0.f;
-      const bool near = MOD == kModRelBias && !rel.far(r00 - 31, r00 + 63, radd);
+      int one_bucket = -1;  // within the reach, where all places are in it
+      bool near = false;
+      if constexpr (MOD == kModRelWide) near = !rel.far_or_one(r00 - 31, r00 + 63, radd, one_bucket);
+      else if constexpr (MOD == kModRelBias) near = !rel.far(r00 - 31, r00 + 63, radd);
       const bool grad = near && a.rel.parts != nullptr;
       const float offset = fmaf(radd, sl2, -lse2);
-      const float2 off = MOD == kModRelBias ? make_float2(offset, offset) : nl;
+      const float2 off = is_rel(MOD) ? make_float2(offset, offset) : nl;
       ok = mbar_wait_warp(&bar->s_full, static_cast<uint32_t>(t) & 1u, a.status, 0x2300);
       if (!ok) break;
       tc_fence_after();
@@ -1593,7 +1605,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(&bar->s_free);
         // P times f, in place of S, while dP(t) runs
-        if (MOD == kModRelBias && near) by_place();
+        if (is_rel(MOD) && near) by_place();
         auto prob = [&](bool mask) {
 #pragma unroll
           for (int e = 0; e < 64; e += 2) {
@@ -1620,7 +1632,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const float2 ds = fmul2(make_float2(__uint_as_float(s[e]), __uint_as_float(s[e + 1])),
                                   fadd2(make_float2(__uint_as_float(dp[e]), __uint_as_float(dp[e + 1])), nd));
           dw[e / 2] = pack_bf16x2(ds.x, ds.y);
-          if constexpr (MOD == kModRelBias) s[e] = __float_as_uint(ds.x), s[e + 1] = __float_as_uint(ds.y);
+          if constexpr (is_rel(MOD)) s[e] = __float_as_uint(ds.x), s[e + 1] = __float_as_uint(ds.y);
         }
       } else {
         // this warpgroup's 64 columns of S and dP out of TMEM, then both released
@@ -1632,7 +1644,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&bar->sp_free);
-        if (MOD == kModRelBias && near) by_place();
+        if (is_rel(MOD) && near) by_place();
         auto row = [&](bool mask) {  // dS = P (dP - D) f
 #pragma unroll
           for (int e = 0; e < 64; e += 2) {
@@ -1641,7 +1653,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             float2 ds = fmul2(p, fadd2(make_float2(__uint_as_float(dp[e]), __uint_as_float(dp[e + 1])), nd));
             if constexpr (MOD == kModSoftcap) ds = fmul2(ds, f);
             dw[e / 2] = pack_bf16x2(ds.x, ds.y);
-            if constexpr (MOD == kModRelBias) s[e] = __float_as_uint(ds.x), s[e + 1] = __float_as_uint(ds.y);  // for the gradient
+            if constexpr (is_rel(MOD)) s[e] = __float_as_uint(ds.x), s[e + 1] = __float_as_uint(ds.y);  // for the gradient
           }
         };
         if (full) row(false);
@@ -1657,17 +1669,17 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&bar->ds_full);
-      if constexpr (MOD == kModRelBias) {  // while the tensor core takes dS
+      if constexpr (is_rel(MOD)) {  // while the tensor core takes dS
         if (!near) {
           const bool right = r00 - 31 >= a.rel.reach;
-          if (right || split) {
+          if (right || split || (MOD == kModRelWide && one_bucket >= 0)) {
             float2 t2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
             for (int e = 0; e < 64; e += 2)
               t2[(e / 2) & 1] = fadd2(t2[(e / 2) & 1], make_float2(__uint_as_float(s[e]), __uint_as_float(s[e + 1])));
             float x = (t2[0].x + t2[0].y) + (t2[1].x + t2[1].y);
             if (right) right_sum += x;
-            else rel_grad.add(static_cast<int>(warp), a.rel.left, lse2 != INFINITY ? x : 0.f);
+            else rel_grad.add(static_cast<int>(warp), MOD == kModRelWide && one_bucket >= 0 ? one_bucket : a.rel.left, lse2 != INFINITY ? x : 0.f);
           } else {
             left_out = left_out || radd > -INFINITY;
           }
@@ -1684,7 +1696,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
     }
-    if constexpr (MOD == kModRelBias) {
+    if constexpr (is_rel(MOD)) {
       if (a.rel.parts != nullptr) {
         rel_grad.add(static_cast<int>(warp), a.rel.right, lse2 != INFINITY ? right_sum : 0.f);
         const bool any = named_barrier_or(1, kSoftThreads, left_out);
@@ -1799,7 +1811,7 @@ cudaError_t launch_dq_t(const CUtensorMap& tq, const CUtensorMap& tk, const CUte
   using C = DqCfg<DQK, DV>;
   auto kern = dq_kernel<DQK, DV, SPARSE, MOD>;
   static PerDeviceOnce once;
-  cudaError_t e = once.run([&] { return set_smem(kern, MOD == kModRelBias ? 232448 : C::SMEM); });
+  cudaError_t e = once.run([&] { return set_smem(kern, is_rel(MOD) ? 232448 : C::SMEM); });
   if (e != cudaSuccess) return e;
   const int split = (!SPARSE && a.dq_split > 1) ? a.dq_split : 1;
   if (split > 1 && (a.tiles_q != nullptr || a.dq_part == nullptr || a.dq_kb_per_split < 1))
@@ -1807,7 +1819,7 @@ cudaError_t launch_dq_t(const CUtensorMap& tq, const CUtensorMap& tk, const CUte
   const int64_t grid = (a.tiles_q ? a.n_tiles_q : static_cast<int64_t>(a.n_qblk) * a.num_units * a.heads) * split;
   if (grid <= 0) return cudaSuccess;
   if (grid > 0x7fffffff) return cudaErrorInvalidConfiguration;
-  if constexpr (MOD == kModRelBias) {
+  if constexpr (is_rel(MOD)) {
     BwdArgs b = a;
     // dO's room, where that goes to TMEM, or else what is left of shared memory
     constexpr int kRoom = C::DO_TMEM ? C::DO_BYTES : 232448 - C::SMEM;

@@ -246,7 +246,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   // modification, or with a relative position bias (B32 H16 N512 d64: 101 us, 99 so). Otherwise (d_qk = 192: measured
   // faster; block-sparse and the other modifications: fewer spills) the producer copies Q first, then the K/V ring, after
   // the block barrier.
-  constexpr bool kEarlyQ = DQK <= 128 && !SPARSE && (MOD == kModNone || MOD == kModRelBias), kEarlyK = kEarlyQ;
+  constexpr bool kEarlyQ = DQK <= 128 && !SPARSE && (MOD == kModNone || is_rel(MOD)), kEarlyK = kEarlyQ;
   const uint32_t warp = warp_id(), lane = lane_id();
   if (threadIdx.x == 0) {
     for (int i = 0; i < QT; ++i) {
@@ -401,7 +401,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // Not where the softmax limits it, which then has to share its issue slots with the tests (ALiBi 1.70 -> 1.74 ms,
         // E4M3 1.23 -> 1.26; with a relative position bias d = 128 gains, B2 H16 over 4 N8192 404 -> 390 us, and d = 64 loses, B1 H8
         // N16001 713 -> 756).
-        constexpr bool kTogether = (MOD == 0 || (MOD == kModRelBias && DQK == 128)) && !F8;
+        constexpr bool kTogether = (MOD == 0 || (is_rel(MOD) && DQK == 128)) && !F8;
         const bool pv0 = kTogether && haveV && j - 1 < nkv[0];
         const bool k_in = kTogether && (!haveK || mbar_test(&bar->kv_full[sK], ring_use(uK) & 1u));
         const bool v_in = kTogether && (!haveV || mbar_test(&bar->kv_full[sV], ring_use(uV) & 1u));
@@ -475,8 +475,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     const float alibi_slope = MOD == kModAlibi ? __ldg(a.alibi_slopes + h) * a.inv_scale : 0.f;  // raw units
     const int qpos = row + (nk - nq);  // the row's position among the keys (bottom-right aligned)
     const RelRow<kRelPad> rel{a.rel, smem_u32(smem + C::BAR_OFF + 256), h};
-    if (MOD == kModRelBias && a.rel.in_smem) {
+    if (is_rel(MOD) && a.rel.in_smem) {
       rel.load(static_cast<int>(threadIdx.x) - 128, 256);
+      if constexpr (MOD == kModRelWide) rel.load_buckets(static_cast<int>(threadIdx.x) - 128, 256);
       named_barrier_sync(1, 256);
     }
     const uint32_t lane_base = tbase + ((quarter * 32u) << 16);
@@ -492,7 +493,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       // the softmax's offsets (add, log2 units), or a number per logit, added below
       const int r0 = kb * BN - qpos;
       float add = 0.f;
-      const bool near = MOD == kModRelBias && !rel.far(r0 + static_cast<int>(lane) - 31, r0 + static_cast<int>(lane) + BN - 1, add);
+      bool near = false;
+      if constexpr (is_rel(MOD)) {
+        const int low = r0 + static_cast<int>(lane) - 31, high = low + 30 + BN;
+        int id;
+        if constexpr (MOD == kModRelWide) near = !rel.far_or_one(low, high, add, id);
+        else near = !rel.far(low, high, add);
+      }
       add *= sl2;
       // site: 0x300 + tile, the step in bits 12..23 (a timeout then says where it stopped)
       ok = mbar_wait_warp(&bar->s_full[i], static_cast<uint32_t>(j) & 1u, a.status,
@@ -514,7 +521,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int c = 0; c < BN; ++c)
           s[c] = __float_as_uint(__uint_as_float(s[c]) - fabsf(fmaf(alibi_slope, static_cast<float>(c), base)));
       }
-      if constexpr (MOD == kModRelBias) {
+      if constexpr (is_rel(MOD)) {
         if (near) {
           rel.at(r0, [&](auto bias) {
 #pragma unroll
@@ -523,7 +530,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       const int cnt = klim - kb * BN;  // visible keys of this row inside the tile
-      if (MOD == kModRelBias && cnt <= 0) add = 0.f;  // (whatever the bias of places that no key is visible at)
+      if (is_rel(MOD) && cnt <= 0) add = 0.f;  // (whatever the bias of places that no key is visible at)
       if (cnt < BN) {
 #pragma unroll
         for (int c = 0; c < BN; ++c)
@@ -538,7 +545,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int z = 0; z < 8; ++z) mp[z] = fmax3(mp[z], __uint_as_float(s[c + z]), __uint_as_float(s[c + 8 + z]));
       const float mx = fmax3(fmax3(mp[0], mp[1], mp[2]), fmax3(mp[3], mp[4], mp[5]), fmaxf(mp[6], mp[7]));
-      const float m_tile = MOD == kModRelBias ? fmaf(mx, sl2, add) : mx * sl2;
+      const float m_tile = is_rel(MOD) ? fmaf(mx, sl2, add) : mx * sl2;
       const bool need = m_tile > m_used + kThreshold;
       float alpha = 1.f;
       if (need) {
@@ -554,7 +561,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // p = 2^(s * scale * log2e - m_used), packed to fp16 (or bf16) pairs in place
       uint32_t pk[BN / 2];
       float2 rs[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};  // partial row sums (packed pairs)
-      const float off = MOD == kModRelBias ? add - mu : -mu;
+      const float off = is_rel(MOD) ? add - mu : -mu;
       const float2 sl2v = make_float2(sl2, sl2), negmu = make_float2(off, off);
       auto exp_row = [&](auto f16_tag) {
         constexpr bool F16 = decltype(f16_tag)::value;
@@ -679,7 +686,7 @@ cudaError_t launch_e(const CUtensorMap& tq, const CUtensorMap& tk, const CUtenso
   static PerDeviceOnce once;
   cudaError_t e = once.run([&]() -> cudaError_t {
     cudaError_t r = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         MOD == kModRelBias ? kMaxSmem : C::SMEM);
+                                         is_rel(MOD) ? kMaxSmem : C::SMEM);
     if (r != cudaSuccess) return r;
     cudaFuncAttributes fa{};
     r = cudaFuncGetAttributes(&fa, kern);
@@ -688,7 +695,7 @@ cudaError_t launch_e(const CUtensorMap& tq, const CUtensorMap& tk, const CUtenso
     return fa.numRegs * kThreads < C::REG_BUDGET ? cudaErrorInvalidConfiguration : cudaSuccess;
   });
   if (e != cudaSuccess) return e;
-  if (LIST != (a.tiles != nullptr) || MOD != a.score_mod || SPARSE != (a.kv_count != nullptr) ||
+  if (LIST != (a.tiles != nullptr) || (is_rel(MOD) ? kModRelBias : MOD) != a.score_mod || SPARSE != (a.kv_count != nullptr) ||
       F8 != (a.input_e4m3 != 0) || SPLITKV != (a.kv_split > 1))
     return cudaErrorInvalidValue;
   if (SPLITKV && (a.o_part == nullptr || a.lse_part == nullptr || a.kv_blocks_per_split < 1 || LIST || SPARSE))
@@ -697,9 +704,9 @@ cudaError_t launch_e(const CUtensorMap& tq, const CUtensorMap& tk, const CUtenso
   if (grid <= 0) return cudaSuccess;
   if (grid > 0x7fffffff || (SPLITKV && a.kv_split > 65535)) return cudaErrorInvalidConfiguration;
   const dim3 g3(static_cast<unsigned>(grid), SPLITKV ? static_cast<unsigned>(a.kv_split) : 1u);
-  if constexpr (MOD == kModRelBias) {
+  if constexpr (is_rel(MOD)) {
     FwdArgs b = a;
-    const int row = 2 * (a.rel.reach + kRelPad) * 4;
+    const int row = RelRow<kRelPad>::bytes(a.rel.reach);
     b.rel.in_smem = row <= kMaxSmem - C::SMEM;
     kern<<<g3, kThreads, C::SMEM + (b.rel.in_smem ? row : 0), stream>>>(tq, tk, tv, tv16, b);
     return cudaGetLastError();

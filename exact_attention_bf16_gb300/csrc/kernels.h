@@ -148,13 +148,14 @@ cudaError_t launch_tile_lists(const int* cu_q, const int* cu_k, int num_seqs, co
 // start[k] on, up to start[k + 1] or without end.
 constexpr int kRelPad = 160;  // places that a warp's logits (32 rows, 128 keys) can reach past the reach
 constexpr int kRelMaxBuckets = 128;
+constexpr int kRelWide = 190;  // places: a warp's 32 rows and 64 keys span 95
 struct RelTable {
   const void* table;  // [buckets, heads], bf16 or fp32
   float inv_scale;    // 1 / softmax_scale
   int f32, heads, buckets, side, two_sided, reach;
   int start[kRelMaxBuckets];
 };
-// Laid out by place, and for the gradient each place's bucket, each bucket's first and last place, the buckets beyond the
+// Laid out by place, with each place's bucket, and for the gradient each bucket's first and last place, the buckets beyond the
 // reach, and the parts' room: [heads][part_rows][buckets], a row per CTA of the dQ kernel.
 struct RelBias {
   const float* by_place;
@@ -163,6 +164,7 @@ struct RelBias {
   float* parts;
   int64_t part_rows;
   int reach, buckets, left, right;
+  int wide;     // a bucket within the reach is wider than kRelWide
   int in_smem;  // the kernel holds its head's row in shared memory (set by its launch, where that fits)
 };
 // zero: n_zero floats to clear along the way (a multiple of 4, 16-byte aligned). The next kernel may be launched early: it
@@ -249,6 +251,8 @@ cudaError_t launch_v_e4m3_to_f16(const void* v, int64_t sb, int64_t sn, int64_t 
 cudaError_t launch_fwd_mod(int d_qk, int d_v, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                            const CUtensorMap& tv16, const FwdArgs& a, cudaStream_t stream);
 cudaError_t launch_fwd_rel(int d_qk, int d_v, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
+                           const CUtensorMap& tv16, const FwdArgs& a, cudaStream_t stream);
+cudaError_t launch_fwd_rel_wide(int d_qk, int d_v, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                            const CUtensorMap& tv16, const FwdArgs& a, cudaStream_t stream);
 
 // fp16 copy of V (contiguous [nb, nrows, heads, dv]) for the forward's PV
@@ -390,7 +394,11 @@ cudaError_t launch_bwd_dq_mod(int d_qk, int d_v, const CUtensorMap& tq, const CU
 // with a relative position bias
 cudaError_t launch_bwd_dkdv_rel(int d_qk, int d_v, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                                 const CUtensorMap& tdo, const BwdArgs& a, cudaStream_t stream);
+cudaError_t launch_bwd_dkdv_rel_wide(int d_qk, int d_v, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
+                                const CUtensorMap& tdo, const BwdArgs& a, cudaStream_t stream);
 cudaError_t launch_bwd_dq_rel(int d_qk, int d_v, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
+                              const CUtensorMap& tdo, const BwdArgs& a, cudaStream_t stream);
+cudaError_t launch_bwd_dq_rel_wide(int d_qk, int d_v, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                               const CUtensorMap& tdo, const BwdArgs& a, cudaStream_t stream);
 // dK, dV for d_qk = d_v = 128 over CTA pairs (dense or varlen, no block
 // lists): maps q and dO with 64-row boxes (_r) and 128-row boxes (_c), k, v.

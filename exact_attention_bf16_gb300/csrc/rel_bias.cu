@@ -37,9 +37,9 @@ __global__ void __launch_bounds__(kThreads) layout_kernel(const __grid_constant_
                             : __bfloat162float(static_cast<const __nv_bfloat16*>(t.table)[at]);
       by_place[static_cast<int64_t>(h) * width + x] = v * t.inv_scale;
     }
-    if (bucket != nullptr && blockIdx.y == 0) bucket[x] = static_cast<uint8_t>(b);
+    if (blockIdx.y == 0) bucket[x] = static_cast<uint8_t>(b);
   }
-  if (bucket != nullptr && blockIdx.x == 0 && blockIdx.y == 0 && static_cast<int>(threadIdx.x) < t.buckets) {
+  if (range != nullptr && blockIdx.x == 0 && blockIdx.y == 0 && static_cast<int>(threadIdx.x) < t.buckets) {
     constexpr int kFar = 0x40000000;
     const int b = static_cast<int>(threadIdx.x), k = b % t.side;
     const int from = t.start[k], to = k + 1 < t.side ? t.start[k + 1] - 1 : kFar;  // distances

@@ -43,6 +43,25 @@ struct RelRow {
     add = l ? lr.x : r ? lr.y : 0.f;
     return l || r;
   }
+  // The buckets of its places lie behind the row in shared memory, if they are asked for.
+  static constexpr int bytes(int reach) { return 5 * 2 * (reach + PAD); }
+  __device__ __forceinline__ void load_buckets(int thread, int n) const {
+    const int width = 2 * (b.reach + PAD);
+    for (int x = thread; x < width; x += n) st_shared_u8(smem + 4 * width + x, __ldg(b.bucket + kRelPad - PAD + x));
+  }
+  __device__ __forceinline__ int bucket(int r) const {
+    return b.in_smem ? ld_shared_u8(smem + 4 * 2 * (b.reach + PAD) + b.reach + PAD + r) : __ldg(b.bucket + kRelPad + b.reach + r);
+  }
+  // Whether places r_min .. r_max all lie beyond the reach or (id: it, else -1) in one bucket within it.
+  __device__ __forceinline__ bool far_or_one(int r_min, int r_max, float& add, int& id) const {
+    id = -1;
+    if (far(r_min, r_max, add)) return true;
+    if (r_min < -b.reach || r_max > b.reach) return false;  // in two
+    id = bucket(r_min);
+    if (id != bucket(r_max)) id = -1;
+    if (id >= 0) add = one(r_min);
+    return id >= 0;
+  }
   // f(load) with load(c) the bias of place r + c.
   template <typename F>
   __device__ __forceinline__ void at(int r, F&& f) const {

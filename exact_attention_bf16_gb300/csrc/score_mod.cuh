@@ -19,7 +19,10 @@
 
 namespace gb300 {
 
-enum : int { kModNone = 0, kModSoftcap = 1, kModAlibi = 2, kModRelBias = 3 };
+enum : int { kModNone = 0, kModSoftcap = 1, kModAlibi = 2, kModRelBias = 3, kModRelWide = 4 };
+
+// Kernels of kModRelBias: kModRelWide is theirs for tables with a bucket within the reach that is wider than a warp's places.
+__host__ __device__ constexpr bool is_rel(int mod) { return mod == kModRelBias || mod == kModRelWide; }
 
 __device__ __forceinline__ float rcp_mufu(float x) {
   float y;

@@ -69,6 +69,14 @@ def test_buckets(ea, two_sided, buckets, far, d, dv):
     _dense(ea, buckets + far, 1, 2, 2, 450, 600, d, dv, not two_sided, two_sided, buckets, far, torch.float32)
 
 
+@pytest.mark.parametrize("d,dv", [(64, 64), (128, 128), (192, 128)])
+@pytest.mark.parametrize("causal,two_sided", [(False, True), (True, False), (False, False), (True, True)])
+@pytest.mark.parametrize("buckets,far", [(2, 600), (4, 1900), (12, 1500), (32, 4000)])
+def test_wide_buckets(ea, d, dv, causal, two_sided, buckets, far):
+    """Tiles that lie in one bucket within the reach."""
+    _dense(ea, buckets + d, 1, 2, 1, 1500, 1900, d, dv, causal, two_sided, buckets, far)
+
+
 @pytest.mark.parametrize("d", [64, 128])
 @pytest.mark.parametrize("causal", [False, True])
 def test_many_tiles_beyond_the_reach(ea, d, causal):
@@ -277,10 +285,12 @@ def test_same_bits_every_time_also_from_captured_and_concurrent_calls(ea):
     assert torch.equal(captured[0], want[0]) and not torch.equal(want[0], o)
 
 
-def test_workspaces_full_of_nan_and_the_gradient_left_out(ea):
+@pytest.mark.parametrize("d,dv", [(64, 64), (128, 128), (192, 128)])
+@pytest.mark.parametrize("buckets,far", [(32, 128), (8, 2000)])
+def test_workspaces_full_of_nan_and_the_gradient_left_out(ea, d, dv, buckets, far):
     """Nothing depends on what a workspace held, and without the table's gradient the others are the same."""
-    lens = [130, 70]
-    q, k, v, o, lse, do, args, kw, grads = _packed(ea, 6, lens, lens, 2, 2, 128, 128, True, False, 32, 128)
+    lens = [1300, 70]
+    q, k, v, o, lse, do, args, kw, grads = _packed(ea, 6, lens, lens, 2, 2, d, dv, True, False, buckets, far)
     junk = [torch.full((1 << 22,), float("nan"), device="cuda") for _ in range(4)]
     del junk
     out = torch.full_like(kw["rel_bias"], 9.0)

@@ -104,9 +104,9 @@ def test_workspaces_hold_the_bias(abi):
     _fill(p, abi)
     with_bias = lib.attn_fwd_workspace_size(ctypes.byref(p))
     p.score_mod = 0
-    # 4 heads x (2 x reach + 320) places, the reach the last border, 91 for 16 buckets a side up to 128
+    # 4 heads x (2 x reach + 320) places and their buckets, the reach the last border, 91 for 16 buckets a side up to 128
     assert bucket(16, 128, 90) == 14 and bucket(16, 128, 91) == 15
-    assert with_bias - lib.attn_fwd_workspace_size(ctypes.byref(p)) == -(-4 * (2 * 91 + 320) * 4 // 256) * 256
+    assert with_bias - lib.attn_fwd_workspace_size(ctypes.byref(p)) == -(-4 * (2 * 91 + 320) * 4 // 256) * 256 + 512
     b = abi.AttnBwdParams()
     _fill(b.fwd, abi)
     b.fwd.seqlen_q = b.fwd.seqlen_k = 50  # reach 50

@@ -259,7 +259,7 @@ cudaError_t lay_out_rel(const P* p, const RelPlan& plan, RelBias* b, float* zero
   b->right = t.two_sided ? t.buckets - 1 : 0;
   for (int k = 0; k < t.side; ++k) t.start[k] = k < t.side / 2 ? k : rel_border(t.side, p->rel_max_distance, k - t.side / 2);
   // Up to `reach`, that is, which no pair exceeds. (The kernels for wide buckets ask every tile within the reach whether it lies in
-  // one: B4 H16 N4096 d64, 32 buckets up to 8192, forward and backward 2530 -> 1960 us; up to 128, 1676 -> 1697.)
+  // one: B4 H16 N4096 d64, 32 buckets up to 8192, forward and backward 2530 -> 2064 us; up to 128, 1671 -> 1697.)
   for (int k = 0; k < t.side; ++k) {
     const int end = std::min(k + 1 < t.side ? t.start[k + 1] : plan.reach, plan.reach);
     if (end - t.start[k] > kRelWide) b->wide = 1;
@@ -1203,6 +1203,7 @@ attn_status_t run_rotary(const attn_rotary_params* p, cudaStream_t stream) {
     if (p->heads_kv < 1) return ATTN_ERR_INVALID_ARG;
     ATTN_TRY(check_turned(p->k, p->k_batch_stride, p->k_row_stride, p->k_head_stride, p->k_out, p->k_out_batch_stride,
                           p->k_out_row_stride, p->k_out_head_stride, p->batch, p->seqlen, p->heads_kv, none));
+    if (!none && p->q_out == p->k_out) return ATTN_ERR_INVALID_ARG;
   }
   if (p->positions ? (reinterpret_cast<uintptr_t>(p->positions) & 3u) != 0 || p->positions_batch_stride < 0
                    : p->seqlen > p->num_positions)

@@ -46,7 +46,7 @@ __device__ __forceinline__ float few_keys_d(const BwdArgs& a, const FewKeys& t, 
     for (int d = 4; d > 0; d >>= 1) x += __shfl_xor_sync(0xffffffffu, x, d);
     if (a.score_mod == kModSoftcap) x = a.mod_b * tanh_scaled(x, a.mod_k2);
     if (a.score_mod == kModAlibi) x -= fabsf(a.alibi_slopes[h] * a.inv_scale * static_cast<float>(j - pos));
-    if (a.score_mod == kModRelBias && j < keys) x += RelRow<kRelPad>{a.rel, 0, h}.one(max(-a.rel.reach, min(a.rel.reach, j - pos)));
+    if (a.score_mod == kModRelBias && j < keys) x += RelRow<kRelPad, false>{a.rel, 0, h}.one(max(-a.rel.reach, min(a.rel.reach, j - pos)));
     if (j < keys) acc = fmaf(exp2f(fmaf(x, a.scale_log2, -lse * 1.4426950408889634f)), y, acc);
   }
 #pragma unroll

@@ -347,7 +347,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (MOD == kModAlibi && valid)
           slope = fabsf(__ldg(a.alibi_slopes + w.hk * a.kv_group + static_cast<int>(quarter * 32 + lane) % a.kv_group) *
                         a.inv_scale);
-        const RelRow<kRelPad> rel{a.rel, 0, MOD == kModRelBias ? w.hk * a.kv_group + static_cast<int>(quarter * 32 + lane) % a.kv_group : 0};
+        const RelRow<kRelPad, false> rel{a.rel, 0, MOD == kModRelBias ? w.hk * a.kv_group + static_cast<int>(quarter * 32 + lane) % a.kv_group : 0};
         // whether this lane's page of key block kt holds keys (one lane per page of a block)
         auto page_ok = [&](int kt) -> bool {
           const int np = a.page_size < BN ? BN >> a.page_shift : 1;

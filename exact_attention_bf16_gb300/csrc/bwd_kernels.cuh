@@ -430,7 +430,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const float sl2 = a.scale_log2;
     int tt = 0, hq = hq_first;  // step within the query head hq
     float alibi_slope = MOD == kModAlibi ? __ldg(a.alibi_slopes + hq) * a.inv_scale : 0.f;  // raw units
-    RelRow<kRelPad> rel{a.rel, 0, hq};
+    RelRow<kRelPad, false> rel{a.rel, 0, hq};
     float2 rel_far = is_rel(MOD) ? rel.both() : make_float2(0.f, 0.f);  // the bias beyond the reach, left and right
     const uint32_t my_cols = C::tS + 32 * wg;     // this warpgroup's S^T columns
     const uint32_t my_pds = C::tPdS + 32 * wg;    // its P^T (16) and dS^T (16) columns
@@ -980,7 +980,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const float2 sl2v = make_float2(a.scale_log2, a.scale_log2);
     int tt = 0, hq = hq_first;  // step within the query head hq
     float alibi_slope = MOD == kModAlibi ? __ldg(a.alibi_slopes + hq) * a.inv_scale : 0.f;  // raw units
-    RelRow<kRelPad> rel{a.rel, 0, hq};
+    RelRow<kRelPad, false> rel{a.rel, 0, hq};
     float2 rel_far = is_rel(MOD) ? rel.both() : make_float2(0.f, 0.f);  // the bias beyond the reach, left and right
     auto lanes = [&](int lg) { return tbase + ((quarter * 32u + 16u * static_cast<uint32_t>(lg)) << 16); };
     bool ok = true;

@@ -12,13 +12,14 @@
 
 namespace gb300 {
 
-// A head's row: in shared memory from r = -reach - pad on (b.in_smem; smem is its address), where a warp's loads from any place take one
-// pass, else in L1 (two lines). Nothing of it lives in registers between tiles.
-template <int PAD>
+// A head's row: in shared memory from r = -reach - PAD on (SMEM: kernels that keep it there where it fits, b.in_smem; smem is its
+// address), or in L1. Nothing of it lives in registers between tiles.
+template <int PAD, bool SMEM = true>
 struct RelRow {
   const RelBias& b;
   uint32_t smem;
   int h;
+  __device__ __forceinline__ bool in_smem() const { return SMEM && b.in_smem; }
   __device__ __forceinline__ const float* global() const {  // of r = 0
     return b.by_place + static_cast<int64_t>(h) * (2 * b.reach + 2 * kRelPad) + b.reach + kRelPad;
   }
@@ -28,7 +29,7 @@ struct RelRow {
     const float* src = global() - b.reach - PAD;
     for (int x = thread; x < 2 * (b.reach + PAD); x += n) st_shared_f32(smem + 4 * x, __ldg(src + x));
   }
-  __device__ __forceinline__ float one(int r) const { return b.in_smem ? ld_shared_f32(shared() + 4 * r) : __ldg(global() + r); }
+  __device__ __forceinline__ float one(int r) const { return in_smem() ? ld_shared_f32(shared() + 4 * r) : __ldg(global() + r); }
   // Whether places r_min .. r_max all have one bias, `add`.
   __device__ __forceinline__ bool far(int r_min, int r_max, float& add) const {
     const bool l = r_max <= -b.reach, r = r_min >= b.reach;
@@ -50,7 +51,7 @@ struct RelRow {
     for (int x = thread; x < width; x += n) st_shared_u8(smem + 4 * width + x, __ldg(b.bucket + kRelPad - PAD + x));
   }
   __device__ __forceinline__ int bucket(int r) const {
-    return b.in_smem ? ld_shared_u8(smem + 4 * 2 * (b.reach + PAD) + b.reach + PAD + r) : __ldg(b.bucket + kRelPad + b.reach + r);
+    return in_smem() ? ld_shared_u8(smem + 4 * 2 * (b.reach + PAD) + b.reach + PAD + r) : __ldg(b.bucket + kRelPad + b.reach + r);
   }
   // Whether places r_min .. r_max all lie beyond the reach or (id: it, else -1) in one bucket within it.
   __device__ __forceinline__ bool far_or_one(int r_min, int r_max, float& add, int& id) const {
@@ -65,7 +66,7 @@ struct RelRow {
   // f(load) with load(c) the bias of place r + c.
   template <typename F>
   __device__ __forceinline__ void at(int r, F&& f) const {
-    if (b.in_smem) {
+    if (in_smem()) {
       const uint32_t from = shared() + 4 * r;
       f([from](int c) { return ld_shared_f32(from + 4 * c); });
     } else {

@@ -15,7 +15,9 @@ def abi():
 
 def _rotary(abi):
     p = abi.AttnRotaryParams()
-    p.q = p.k = p.q_out = p.k_out = p.positions = p.cos_table = p.sin_table = FAKE
+    p.q = p.q_out = FAKE
+    p.k = p.k_out = FAKE + 0x10000
+    p.positions = p.cos_table = p.sin_table = FAKE
     for n in ("q", "k", "q_out", "k_out"):
         for s, x in (("batch", 1280), ("row", 128), ("head", 64)):
             setattr(p, f"{n}_{s}_stride", x)
@@ -28,7 +30,7 @@ def _rotary(abi):
 BAD_ROTARY = [
     ("batch", 0, INVALID), ("seqlen", -1, INVALID), ("heads", 0, INVALID), ("heads_kv", 0, INVALID), ("d_qk", 0, INVALID),
     ("d_qk", 96, UNSUPPORTED), ("q", None, INVALID), ("q", FAKE + 8, INVALID), ("q_out", None, INVALID),
-    ("k_out", None, INVALID), ("k", None, INVALID), ("q_row_stride", 4, INVALID), ("q_out_head_stride", 0, INVALID),
+    ("k_out", None, INVALID), ("k", None, INVALID), ("k_out", FAKE, INVALID), ("q_row_stride", 4, INVALID), ("q_out_head_stride", 0, INVALID),
     ("q_out_row_stride", 0, INVALID), ("k_out_batch_stride", 0, INVALID), ("q_out_row_stride", 256, INVALID),
     ("k_batch_stride", 2560, INVALID), ("k_head_stride", -64, INVALID), ("positions", FAKE + 2, INVALID),
     ("positions_batch_stride", -1, INVALID), ("cos_table", None, INVALID), ("sin_table", FAKE + 4, INVALID),

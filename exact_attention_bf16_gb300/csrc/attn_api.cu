@@ -985,7 +985,8 @@ attn_status_t run_bwd(const attn_bwd_params* p, void* ws, size_t ws_bytes, bool 
   FewKeys few{bf(f.q), bf(f.k), bf(f.v), f.q_batch_stride, f.q_row_stride, f.q_head_stride, f.k_batch_stride, f.k_row_stride,
               f.k_head_stride, f.v_batch_stride, f.v_row_stride, f.v_head_stride, f.d_qk, f.d_v};
   if (varlen) few.q_sb = few.k_sb = few.v_sb = 0;
-  e = max_k <= kFewKeys ? launch_bwd_few_keys_dsum(a, few, lists, stream) : launch_bwd_preprocess(f.d_v, a, few, lists, stream);
+  e = max_k <= kFewKeys && !rel ? launch_bwd_few_keys_dsum(a, few, lists, stream)
+                                : launch_bwd_preprocess(f.d_v, a, few, lists, stream);
   if (e == cudaSuccess && sp.kv_count) e = launch_bwd_transpose_lists(a, n_kb_sparse, stream);
   if (e == cudaSuccess) e = mark(0);
   if (e != cudaSuccess) return cuda_fail(e, "bwd preprocess launch");
@@ -1002,14 +1003,20 @@ attn_status_t run_bwd(const attn_bwd_params* p, void* ws, size_t ws_bytes, bool 
     if (e == cudaSuccess) e = mark(2);
     return e == cudaSuccess ? ATTN_OK : cuda_fail(e, "bwd single-pass launch");
   }
-  if (p->cta_pair) {  // the two-SM kernel (d = 128, no block lists; checked before any launch)
-    e = launch_bwd_dkdv_pair(tq_r, tq2, tk, tv, tdo_r, tdo2, a, stream);
-  } else {
-    e = launch_bwd_dkdv(f.d_qk, f.d_v, tq2, tk, tv, tdo2, a, stream);
-    if (e == cudaSuccess && dkv_split > 1) e = launch_bwd_dkv_merge(a, f.d_qk, f.d_v, stream);
+  auto dkdv = [&]() -> cudaError_t {
+    cudaError_t de;
+    if (p->cta_pair) {  // the two-SM kernel (d = 128, no block lists; checked before any launch)
+      de = launch_bwd_dkdv_pair(tq_r, tq2, tk, tv, tdo_r, tdo2, a, stream);
+    } else {
+      de = launch_bwd_dkdv(f.d_qk, f.d_v, tq2, tk, tv, tdo2, a, stream);
+      if (de == cudaSuccess && dkv_split > 1) de = launch_bwd_dkv_merge(a, f.d_qk, f.d_v, stream);
+    }
+    return de == cudaSuccess ? mark(1) : de;
+  };
+  if (!rel) {
+    e = dkdv();
+    if (e != cudaSuccess) return cuda_fail(e, "bwd dkdv launch");
   }
-  if (e == cudaSuccess) e = mark(1);
-  if (e != cudaSuccess) return cuda_fail(e, "bwd dkdv launch");
   if (dqs.splits > 1) {
     a.dq_split = dqs.splits;
     a.dq_kb_per_split = dqs.per;
@@ -1017,11 +1024,15 @@ attn_status_t run_bwd(const attn_bwd_params* p, void* ws, size_t ws_bytes, bool 
   }
   e = launch_bwd_dq(f.d_qk, f.d_v, tq, tk, tv, tdo, a, stream);
   if (e == cudaSuccess && dqs.splits > 1) e = launch_bwd_dq_merge(a, f.d_qk, stream);
-  if (e == cudaSuccess && p->drel_bias)
-    e = launch_rel_sum(a.rel.parts, a.rel.part_rows, f.rel_buckets, f.heads, p->drel_bias, f.rel_bias_dtype == ATTN_TABLE_F32,
-                       stream);
   if (e == cudaSuccess) e = mark(2);
   if (e != cudaSuccess) return cuda_fail(e, "bwd dq launch");
+  if (rel) {  // behind the dQ kernel, which corrects D
+    e = dkdv();
+    if (e == cudaSuccess && p->drel_bias)
+      e = launch_rel_sum(a.rel.parts, a.rel.part_rows, f.rel_buckets, f.heads, p->drel_bias, f.rel_bias_dtype == ATTN_TABLE_F32,
+                         stream);
+    if (e != cudaSuccess) return cuda_fail(e, "bwd dkdv launch");
+  }
   return ATTN_OK;
 }
 

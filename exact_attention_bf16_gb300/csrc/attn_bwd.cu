@@ -46,7 +46,6 @@ __device__ __forceinline__ float few_keys_d(const BwdArgs& a, const FewKeys& t, 
     for (int d = 4; d > 0; d >>= 1) x += __shfl_xor_sync(0xffffffffu, x, d);
     if (a.score_mod == kModSoftcap) x = a.mod_b * tanh_scaled(x, a.mod_k2);
     if (a.score_mod == kModAlibi) x -= fabsf(a.alibi_slopes[h] * a.inv_scale * static_cast<float>(j - pos));
-    if (a.score_mod == kModRelBias && j < keys) x += RelRow<kRelPad, false>{a.rel, 0, h}.one(max(-a.rel.reach, min(a.rel.reach, j - pos)));
     if (j < keys) acc = fmaf(exp2f(fmaf(x, a.scale_log2, -lse * 1.4426950408889634f)), y, acc);
   }
 #pragma unroll
@@ -54,9 +53,10 @@ __device__ __forceinline__ float few_keys_d(const BwdArgs& a, const FewKeys& t, 
   return acc;
 }
 
-// Whether few_keys_d is for this unit (offsets past the tensors are not followed).
+// Whether few_keys_d is for this unit (offsets past the tensors are not followed). Not with a relative position bias, whose dQ
+// kernel takes D from P and dP itself.
 __device__ __forceinline__ bool few_keys(const BwdArgs& a, const Unit& U) {
-  return U.nk >= 1 && U.nk <= kFewKeys && U.q_start >= 0 && U.k_start >= 0 && U.q_start + U.nq <= a.seqlen_q &&
+  return a.score_mod != kModRelBias && U.nk >= 1 && U.nk <= kFewKeys && U.q_start >= 0 && U.k_start >= 0 && U.q_start + U.nq <= a.seqlen_q &&
          U.k_start + U.nk <= a.seqlen_k;
 }
 
@@ -64,7 +64,6 @@ __device__ __forceinline__ bool few_keys(const BwdArgs& a, const Unit& U) {
 // rows shared by the blocks along y.
 __global__ void __launch_bounds__(256) few_keys_dsum_kernel(const BwdArgs a, const FewKeys t) {
   const int l = static_cast<int>(threadIdx.x & 7u);
-  if (a.score_mod == kModRelBias) asm volatile("griddepcontrol.wait;" ::: "memory");  // the bias's layout
   for (int unit = static_cast<int>(blockIdx.x); unit < a.num_units; unit += static_cast<int>(gridDim.x)) {
     const Unit U = unit_bounds(a, unit);
     if (!few_keys(a, U)) continue;
@@ -162,7 +161,6 @@ __global__ void __launch_bounds__(256, PACKED ? kPackedBlocks : 8) preprocess_ke
     }
   }
   if constexpr (PACKED) {
-    if (a.score_mod == kModRelBias) asm volatile("griddepcontrol.wait;" ::: "memory");  // the bias's layout
     __syncthreads();  // the D above are written
     const int first = static_cast<int>(begin / a.heads), last = static_cast<int>((rows - 1) / a.heads);  // tokens
     int unit = 0;  // the last sequence that begins at or before `first`

@@ -1547,6 +1547,37 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       named_barrier_sync(1, kSoftThreads);
     }
+    // Where a row's keys are all in one tile, D = sum_j P_j dP_j anew, in fp32, here and for the dK/dV kernel behind this one: the D
+    // from O carries O's rounding, which shows in the gradients of rows with few keys (few_keys_d says how; of 9 to 32 keys dQ
+    // and dK came out 2.5e-3 to 3.2e-3 from the exact ones and the bias's gradient up to 4.7e-3, now 2.4e-3 and 2.2e-3).
+    if (is_rel(MOD) && T == 1 && !split) {
+      bool in = mbar_wait_warp(&bar->s_full, 0, a.status, 0x2300);
+      if constexpr (C::SPLIT_SDP) in = mbar_wait_warp(&bar->dp_full, 0, a.status, 0x2302) && in;
+      float more = 0.f;  // what D lacks: the sum of dS
+      if (in) {
+        tc_fence_after();
+        const int r0 = wg * 64 - i - (U.nk - U.nq);
+#pragma unroll 1
+        for (int c = 0; c < 64; c += 16) {
+          uint32_t s[16], dp[16];
+          tmem_ld16(lane_base + C::tS + wg * 64 + c, s);
+          tmem_ld16(lane_base + C::tdP + wg * 64 + c, dp);
+          tmem_wait_ld();
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            const float bias = rel.one(max(-a.rel.reach, min(a.rel.reach, r0 + c + e)));
+            const float p = ex2_mufu(fmaf(__uint_as_float(s[e]) + bias, sl2, -lse2));
+            if (wg * 64 + c + e < lim && lse2 != INFINITY) more = fmaf(p, __uint_as_float(dp[e]) - dsum, more);
+          }
+        }
+        tc_fence_before();
+      }
+      st_shared_f32(rel_grad.row_sum(wg, r), more);
+      named_barrier_sync(1, kSoftThreads);  // (every warp gets here, also those whose waits ran out)
+      dsum += more + ld_shared_f32(rel_grad.row_sum(1 - wg, r));
+      if (wg == 0 && i < U.nq) a.dsum[U.b * a.lse_sb + h * a.lse_sh + U.q_start + i] = dsum;
+      ok = ok && in;
+    }
     const float2 sl2v = make_float2(sl2, sl2), nl = make_float2(-lse2, -lse2), nd = make_float2(-dsum, -dsum);
     for (int t = 0; t < T && ok; ++t) {
       // relative position bias: one number for the warp (32 rows, 64 columns), in the row's offset, or a number per logit (r0: the

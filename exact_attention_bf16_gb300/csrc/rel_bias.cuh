@@ -76,15 +76,16 @@ struct RelRow {
   }
 };
 
-// What the dQ kernel holds of the gradient in shared memory: each warp's sums by bucket, and behind them, where the row is there
-// too (b.in_smem), the buckets' first and last places, the row and its places' buckets.
-constexpr int kRelSums = 8 * kRelMaxBuckets * 4, kRelRange = kRelMaxBuckets * 8;  // bytes
+// What the dQ kernel holds of the gradient in shared memory: each warp's sums by bucket, the halves' sums of a row, and behind
+// them, where the row is there too (b.in_smem), the buckets' first and last places, the row and its places' buckets.
+constexpr int kRelRowSums = 2 * 128 * 4, kRelSums = 8 * kRelMaxBuckets * 4 + kRelRowSums, kRelRange = kRelMaxBuckets * 8;  // bytes
 template <int PAD>
 struct RelGrad {
   const RelBias& b;
   uint32_t smem;
   static constexpr int bytes(int reach) { return kRelSums + kRelRange + 5 * 2 * (reach + PAD); }  // with the row
   __device__ __forceinline__ uint32_t row() const { return smem + kRelSums + kRelRange; }
+  __device__ __forceinline__ uint32_t row_sum(int half, int row) const { return smem + kRelSums - kRelRowSums + 4 * (128 * half + row); }
   __device__ __forceinline__ uint32_t sum(int warp, int bucket) const { return smem + 4 * (warp * kRelMaxBuckets + bucket); }
   // Brings what load() and RelRow::load() read into L1 (their latency was a third of a microsecond of every CTA).
   __device__ __forceinline__ void prefetch(const float* row, int thread, int n) const {

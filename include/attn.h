@@ -265,7 +265,8 @@ typedef struct attn_bwd_params {
   int32_t cta_pair;
   /* Optional (each may be NULL): CUDA events (cudaEvent_t) recorded on the
    * stream after the D = rowsum(dO * O) pass [0], after the dK/dV kernel [1]
-   * and after the dQ kernel [2], for timing the phases. */
+   * and after the dQ kernel [2], for timing the phases. (With ATTN_SCORE_RELBIAS the
+   * dQ kernel runs before the dK/dV kernel.) */
   void* phase_events[3];
   /* single_pass != 0: the backward of wittx "FlashAttention-4", 反向传播的优化:
    * one key-stationary kernel computes dK, dV and, per 64-query step, the dQ

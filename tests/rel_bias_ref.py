@@ -62,9 +62,14 @@ def attention64(q, k, v, table, far, two_sided, scale, causal, do=None):
         out["dq"][:, x] = scale * ds @ f(k[:, y])
         out["dk"][:, y] += scale * ds.T @ f(q[:, x])
         out["dv"][:, y] += p.T @ g
-        # D from O rounded to bf16 (half a step, 2^-8); P and dP in fp32: the logits' steps of at most 2^-24 of 100 and
-        # the LSE's 1e-4 leave 2e-4 of P; dP's sum of 64 or 128 products 1e-5 of its terms
-        off = p * (2.0 ** -8 * (g.abs() * o.abs()).sum(1, keepdim=True) + 1e-5 * (g.abs() @ f(v[:, y]).abs().T)) + 2e-4 * ds.abs()
+        # P and dP in fp32: the logits' steps of at most 2^-24 of 100 and the LSE's 1e-4 leave 2e-4 of P, and dP's sum of 64 or
+        # 128 products 1e-5 of its terms; so, too, in D = sum P dP of rows whose keys are all in one tile of 128. Longer rows' D is
+        # that of O rounded to bf16, half a step (2^-8) of each term.
+        terms = g.abs() @ f(v[:, y]).abs().T
+        d_off = (p * (2e-4 * dp.abs() + 1e-5 * terms)).sum(1, keepdim=True)
+        if nk > 128:
+            d_off = d_off + 2.0 ** -8 * (g.abs() * o.abs()).sum(1, keepdim=True)
+        off = p * (d_off + 1e-5 * terms) + 2e-4 * ds.abs()
         for z in range(table.shape[0]):
             out["dtable"][z, x] = (ds * (which == z)).sum()
             out["slack"][z, x] = (off * (which == z)).sum()

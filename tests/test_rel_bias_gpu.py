@@ -83,6 +83,15 @@ def test_many_tiles_beyond_the_reach(ea, d, causal):
     _dense(ea, d, 1, 2, 1, 2111, 2500, d, d, causal, not causal, 32, 128)
 
 
+@pytest.mark.parametrize("d,dv", [(64, 64), (128, 128), (192, 128)])
+@pytest.mark.parametrize("n", [2, 9, 16, 33, 100, 128])
+def test_rows_of_one_tile_of_keys(ea, d, dv, n):
+    """D from P and dP: the table's gradient is as good as fp32 (rel_bias_ref's slack without O's rounding)."""
+    for causal in (False, True):
+        _dense(ea, n + d, 3, 4, 2, n, n, d, dv, causal, not causal, 16, 40, torch.float32)
+        _dense(ea, n + d, 1, 2, 2, 300, n, d, dv, causal, True, 16, 40, torch.float32)
+
+
 def test_few_queries_over_long_keys_split(ea):
     """The dQ kernel's split keys."""
     for nq in (1, 100, 130):

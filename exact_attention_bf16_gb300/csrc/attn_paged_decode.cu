@@ -25,6 +25,9 @@
 // requests 479 and 484. Work is the even split of paged_common.cuh; two streams over the even
 // and the odd key blocks hide the chain S^T -> softmax -> O^T, as there.
 //
+// A relative position bias is 16 loads a key lane and block, ahead of the block's logits: 64 requests of 300 to 16384 tokens, 32
+// heads over 8, d = 128: 206 us, 200 without a bias, 256 by paged_kernel with one.
+//
 // Warps: 0 work and TMA copies, 1 MMA issue, 4..7 and 8..11 softmax of stream 0 and 1.
 #include <cstddef>
 

@@ -84,7 +84,9 @@ __global__ void __launch_bounds__(1024) sum_parts_kernel(const float* parts, int
 cudaError_t launch_rel_layout(const RelTable& t, const RelBias& b, float* zero, int64_t n_zero, cudaStream_t stream) {
   const int width = 2 * t.reach + 2 * kRelPad;
   const unsigned gx = static_cast<unsigned>((width + rel::kThreads - 1) / rel::kThreads);
-  const unsigned gy = static_cast<unsigned>(std::min(t.heads, 65535));
+  // (rows of blocks beyond the heads only clear: a packed backward of thousands of sequences has tens of MB of parts)
+  const int64_t clear = std::min<int64_t>(n_zero / (4 * rel::kThreads), 152 * 8) / gx;
+  const unsigned gy = static_cast<unsigned>(std::min<int64_t>(std::max<int64_t>(t.heads, clear), 65535));
   rel::layout_kernel<<<dim3(gx, gy), rel::kThreads, 0, stream>>>(t, const_cast<float*>(b.by_place), const_cast<uint8_t*>(b.bucket),
                                                                  const_cast<int2*>(b.range), reinterpret_cast<float4*>(zero),
                                                                  n_zero / 4);

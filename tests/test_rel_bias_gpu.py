@@ -397,6 +397,68 @@ def test_paged(ea, d, dv, h, hk, page, new):
             assert float((lse[:, a:b].double() - ref["lse"]).abs().max()) <= 1e-4
 
 
+@pytest.mark.parametrize("h,hk,chunk", [(4, 4, 1), (16, 1, 2), (8, 2, 70)])
+def test_paged_captured_and_at_once(ea, h, hk, chunk):
+    """One captured call replayed as lengths change, and calls on three streams, with workspaces of their own."""
+    rng = np.random.default_rng(chunk)
+    d, page, n, cap = 64, 32, 3, 20
+    kc, vc, q = _t(rng, n * cap, page, hk, d), _t(rng, n * cap, page, hk, d), _t(rng, n * chunk, h, d)
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    pages, cu, lens = i32(rng.permutation(n * cap).reshape(n, cap).tolist()), i32([chunk * i for i in range(n + 1)]), i32([chunk] * n)
+    how = dict(rel_bias=log_table(rng, 32, h, torch.bfloat16), rel_max_distance=100, rel_bidirectional=False)
+    call = lambda **kw: ea.attn_fwd_paged(q, kc, vc, pages, cu, lens, chunk, **how, **kw)  # noqa: E731
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        call()
+    side.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        o, lse = call()
+    for now in ([640, 100, chunk], [chunk, 640, 333], [500, 0, 400]):
+        lens.copy_(i32(now))
+        o.fill_(3.0)
+        graph.replay()
+        want, want_lse = call()
+        torch.cuda.synchronize()
+        assert torch.equal(o, want) and torch.equal(lse, want_lse)
+        streams = [torch.cuda.Stream() for _ in range(3)]
+        for s in streams:
+            s.wait_stream(torch.cuda.current_stream())
+        many = [call(stream=s) for s in streams for _ in range(2)]
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, want) and torch.equal(b, want_lse) for a, b in many)
+        for s in range(n):
+            if now[s] < chunk:
+                continue
+            keys, values = (torch.tensor(paged_ref.gather(c, pages[s].tolist(), now[s]), device="cuda") for c in (kc, vc))
+            ref = attention64(q[s * chunk:(s + 1) * chunk], keys, values, how["rel_bias"], 100, False, d ** -0.5, True)
+            assert float((lse[:, s * chunk:(s + 1) * chunk].double() - ref["lse"]).abs().max()) <= 1e-4
+            assert float((o[s * chunk:(s + 1) * chunk].double() - ref["o"]).abs().max()) <= 2.0 ** -6 * float(values.abs().max())
+
+
+def test_thousands_of_sequences(ea):
+    """The gradient's parts of thousands of sequences, most of them with no rows."""
+    rng = np.random.default_rng(40)
+    lens = np.where(rng.random(3500) < 0.02, rng.integers(1, 200, 3500), 0)
+    lens[17] = 300
+    h, d = 4, 64
+    total = int(lens.sum())
+    q, k, v, do = (_t(rng, total, h, d) for _ in range(4))
+    cu = torch.tensor([0, *np.cumsum(lens)], dtype=torch.int32, device="cuda")
+    table = log_table(rng, 32, h, torch.float32)
+    args, kw = (cu, cu, 300, 300), dict(rel_bias=table, rel_max_distance=60)
+    junk = [torch.full((1 << 24,), float("nan"), device="cuda") for _ in range(2)]
+    del junk
+    o, lse = ea.attn_fwd_varlen(q, k, v, *args, **kw)
+    dt = ea.attn_bwd_varlen(q, k, v, o, lse, do, *args, **kw)[3]
+    total, slack, a = 0.0, 0.0, 0
+    for n in lens[lens > 0].tolist():
+        ref = attention64(q[a:a + n], k[a:a + n], v[a:a + n], table, 60, True, d ** -0.5, False, do[a:a + n])
+        total, slack, a = total + ref["dtable"], slack + ref["slack"], a + n
+    check_table(dt, total, slack)
+
+
 def test_paged_steps_end_where_the_whole_prompt_does(ea):
     """Token by token over a paged cache, against the packed forward of the whole sequence with the same table."""
     rng = np.random.default_rng(20)

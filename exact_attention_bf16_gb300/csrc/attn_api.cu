@@ -243,10 +243,11 @@ RelPlan rel_plan(const P* p, int64_t longest) {
   r.range_bytes = kRelMaxBuckets * sizeof(int2);
   return r;
 }
-// The table's layout, launched (b's arrays are set), and the rest of b.
+// The layout of the call's table, to be launched (b's arrays are set), and the rest of b.
 template <typename P>
-cudaError_t lay_out_rel(const P* p, const RelPlan& plan, RelBias* b, float* zero, int64_t n_zero, cudaStream_t stream) {
-  RelTable t{};
+RelLayout rel_layout_of(const P* p, const RelPlan& plan, RelBias* b, int64_t n_zero, uint32_t* zero_word) {
+  RelLayout l{};
+  RelTable& t = l.table;
   t.table = p->rel_bias;
   t.inv_scale = 1.f / p->softmax_scale;
   t.f32 = p->rel_bias_dtype == ATTN_TABLE_F32;
@@ -264,7 +265,13 @@ cudaError_t lay_out_rel(const P* p, const RelPlan& plan, RelBias* b, float* zero
     const int end = std::min(k + 1 < t.side ? t.start[k + 1] : plan.reach, plan.reach);
     if (end - t.start[k] > kRelWide) b->wide = 1;
   }
-  return launch_rel_layout(t, *b, zero, n_zero, stream);
+  l.by_place = const_cast<float*>(b->by_place);
+  l.bucket = const_cast<uint8_t*>(b->bucket);
+  l.range = const_cast<int2*>(b->range);
+  l.zero = reinterpret_cast<float4*>(b->parts);
+  l.n_zero = n_zero;
+  l.zero_word = zero_word;
+  return l;
 }
 
 attn_status_t check_scores(float scale, int32_t score_mod, float softcap, const float* alibi_slopes) {
@@ -580,17 +587,14 @@ attn_status_t run_fwd(const attn_fwd_params* p, bool varlen, cudaStream_t stream
   ATTN_TRY(make_map(&tv16, v16, p->d_v, hkv, nk_rows, nb, v16_rows * hkv * p->d_v,
                     static_cast<int64_t>(hkv) * p->d_v, p->d_v, 128));
   const ListPlan lp = fwd_list_plan(p, varlen);
-  // the bias by place, beside which the lists are built and V is copied
+  // the bias by place: beside the lists, or ahead of the copy of V, which runs beside it
   const bool rel = p->score_mod == ATTN_SCORE_RELBIAS;
-  auto lay_out_bias = [&]() -> cudaError_t {
+  RelLayout layout{};
+  if (rel) {
     const RelPlan rp = call_rel_plan(p, varlen);
     a.rel.bucket = static_cast<uint8_t*>(ws) + need_ws - rp.bucket_bytes;
     a.rel.by_place = reinterpret_cast<const float*>(a.rel.bucket - rp.place_bytes);
-    return lay_out_rel(p, rp, &a.rel, nullptr, 0, stream);
-  };
-  if (rel && lp.use) {
-    e = lay_out_bias();
-    if (e != cudaSuccess) return cuda_fail(e, "bias layout");
+    layout = rel_layout_of(p, rp, &a.rel, 0, lp.use ? nullptr : flag);
   }
   SeqMaps maps{};
   if (varlen && ws_bytes >= need_ws + fwd_seq_map_bytes(p)) {  // V of each sequence, apart from the next one's
@@ -606,15 +610,15 @@ attn_status_t run_fwd(const attn_fwd_params* p, bool varlen, cudaStream_t stream
     TileEntry* list = reinterpret_cast<TileEntry*>(lbase);
     const TileListSpec spec{p->heads, 256, 0, 1, lp.max_nblk, list, lp.bound};
     e = launch_tile_lists(p->cu_seqlens_q, p->cu_seqlens_k, p->num_seqs, &spec, 1,
-                          reinterpret_cast<int64_t*>(lbase + lp.list_bytes), flag, maps, rel, stream);
+                          reinterpret_cast<int64_t*>(lbase + lp.list_bytes), flag, maps, rel ? &layout : nullptr, stream);
     if (e != cudaSuccess) return cuda_fail(e, "fwd tile list");
     a.tiles = list;
     a.n_tiles = lp.bound;
   } else {
-    e = cudaMemsetAsync(flag, 0, sizeof(uint32_t), stream);
-    if (e == cudaSuccess && maps.n > 0)
-      e = launch_tile_lists(p->cu_seqlens_q, p->cu_seqlens_k, p->num_seqs, nullptr, 0, nullptr, nullptr, maps, false, stream);
-    if (e == cudaSuccess && rel) e = lay_out_bias();
+    // (the sequences' maps first, whose kernel nothing then runs beside)
+    if (maps.n > 0)
+      e = launch_tile_lists(p->cu_seqlens_q, p->cu_seqlens_k, p->num_seqs, nullptr, 0, nullptr, nullptr, maps, nullptr, stream);
+    if (e == cudaSuccess) e = rel ? launch_rel_layout(layout, stream) : cudaMemsetAsync(flag, 0, sizeof(uint32_t), stream);
   }
   if (e == cudaSuccess && f8)  // exact: every E4M3 value is an fp16 value, the flag stays 0
     e = launch_v_e4m3_to_f16(p->v, varlen ? 0 : p->v_batch_stride, p->v_row_stride, p->v_head_stride, nb, nk_rows,
@@ -911,7 +915,8 @@ attn_status_t run_bwd(const attn_bwd_params* p, void* ws, size_t ws_bytes, bool 
     ATTN_TRY(make_map(&tv, f.v, f.d_v, hkv, nk_rows, nb, f.v_batch_stride, f.v_row_stride, f.v_head_stride, 128));
   }
 
-  if (nq_rows > 0 && nk_rows > 0 && rel) {  // the bias by place (ahead of the lists, whose kernel others run beside)
+  RelLayout layout{};
+  if (nq_rows > 0 && nk_rows > 0 && rel) {  // the bias by place: beside the lists, or ahead of the D pass, which runs beside it
     const RelPlan rp = call_rel_plan(&f, varlen);
     uint8_t* at = static_cast<uint8_t*>(ws) + bwd_base_bytes(p, varlen);
     a.rel.by_place = reinterpret_cast<const float*>(at);
@@ -921,10 +926,13 @@ attn_status_t run_bwd(const attn_bwd_params* p, void* ws, size_t ws_bytes, bool 
       a.rel.parts = reinterpret_cast<float*>(at + rp.place_bytes + rp.bucket_bytes + rp.range_bytes);
       a.rel.part_rows = bwd_rel_part_rows(p, varlen, dqs.splits);
     }
-    // (dense: every CTA writes its own)
-    const int64_t n_parts = varlen ? (f.heads * a.rel.part_rows * f.rel_buckets + 3) / 4 * 4 : 0;
-    e = lay_out_rel(&f, rp, &a.rel, a.rel.parts, n_parts, stream);
-    if (e != cudaSuccess) return cuda_fail(e, "bias layout");
+    // (dense: every CTA of the dQ kernel writes its own)
+    const int64_t n_parts = varlen ? (f.heads * a.rel.part_rows * f.rel_buckets + 3) / 4 : 0;
+    layout = rel_layout_of(&f, rp, &a.rel, n_parts, nullptr);
+    if (!varlen) {
+      e = launch_rel_layout(layout, stream);
+      if (e != cudaSuccess) return cuda_fail(e, "bias layout");
+    }
   }
 
   if (nq_rows > 0 && nk_rows > 0 && varlen) {  // tile lists: longest sequences first, no CTA past an end
@@ -965,8 +973,12 @@ attn_status_t run_bwd(const attn_bwd_params* p, void* ws, size_t ws_bytes, bool 
       a.n_seq_maps = maps.n;
     }
     if (n > 0 || maps.n > 0) {
-      e = launch_tile_lists(f.cu_seqlens_q, f.cu_seqlens_k, f.num_seqs, specs, n, scratch, nullptr, maps, rel, stream);
+      e = launch_tile_lists(f.cu_seqlens_q, f.cu_seqlens_k, f.num_seqs, specs, n, scratch, nullptr, maps, rel ? &layout : nullptr,
+                            stream);
       if (e != cudaSuccess) return cuda_fail(e, "bwd tile lists");
+    } else if (rel) {
+      e = launch_rel_layout(layout, stream);
+      if (e != cudaSuccess) return cuda_fail(e, "bias layout");
     }
   }
 
@@ -1407,7 +1419,7 @@ attn_status_t run_fwd_paged(const attn_paged_params* p, void* ws, size_t ws_byte
   if (p->score_mod == ATTN_SCORE_RELBIAS) {
     a.rel.by_place = reinterpret_cast<const float*>(base + pl.off_rel);
     a.rel.bucket = base + pl.off_rel + pl.rel.place_bytes;
-    e = lay_out_rel(p, pl.rel, &a.rel, nullptr, 0, stream);
+    e = launch_rel_layout(rel_layout_of(p, pl.rel, &a.rel, 0, nullptr), stream);
     if (e != cudaSuccess) return cuda_fail(e, "bias layout");
   }
   int dev = 0, sms = 0;

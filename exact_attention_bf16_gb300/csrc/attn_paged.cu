@@ -20,7 +20,7 @@
 // merge_kernel adds them with the weights 2^(LSE_r - LSE), in key order.
 // One persistent CTA per SM (shared memory and Tensor Memory are taken whole):
 //   - up to 128 rows per request (a few proposed tokens; up to 16 rows without a score
-//     modification run in attn_paged_decode.cu instead): bound by
+//     modification, or with a relative position bias, run in attn_paged_decode.cu instead): bound by
 //     HBM (every K/V byte is read once and used for a handful of rows), so the
 //     key blocks of all (request, K/V head) units, laid end to end, are cut into
 //     equal ranges, one per CTA. A CTA finds its range from the lengths alone. 33 requests

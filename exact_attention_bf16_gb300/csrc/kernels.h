@@ -117,33 +117,6 @@ cudaError_t launch_early(K kern, dim3 grid, int threads, int smem, cudaStream_t 
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
-// Builds up to two lists for num_seqs sequences (cu_q / cu_k offsets on the device):
-// sequences with the most blocks first (by key blocks when by_keys), then
-// head by head, blocks of a head in descending or ascending order. Writes
-// `bound` entries (the real ones, then empty ones); scratch holds num_seqs
-// int64. max_nblk bounds every sequence's block count (<= kMaxListBlocks).
-// *zero_word (when given) is set to 0. early: behind launch_rel_layout, whose kernel it runs beside.
-struct TileListSpec {
-  int heads, rows_per_block, by_keys, descending, max_nblk;
-  TileEntry* out;
-  int64_t bound;
-};
-// Beside them, in blocks of their own, the sequences' tensor maps (when given): map m of sequence s,
-// out[s * n + m], is base[m] with its rows ending where the sequence's queries or keys do, so that
-// the rows behind them, which belong to the next sequence, read as zeros in the tile that the
-// sequence ends in (0 x NaN is NaN: an infinity or NaN there would reach this sequence through its
-// zero weights). A kernel only takes its copies' maps from there.
-constexpr int kMaxSeqMaps = 6;
-struct SeqMaps {
-  CUtensorMap base[kMaxSeqMaps];
-  int by_keys[kMaxSeqMaps];  // 1: rows are keys, 0: queries
-  int n = 0;
-  int rows_q = 0, rows_k = 0;  // of the packed tensors
-  CUtensorMap* out = nullptr;
-};
-cudaError_t launch_tile_lists(const int* cu_q, const int* cu_k, int num_seqs, const TileListSpec* specs, int n,
-                              int64_t* scratch, uint32_t* zero_word, const SeqMaps& maps, bool early, cudaStream_t stream);
-
 // Relative position bias (rel_bias.cuh). The caller's table and its buckets: bucket k of a side holds the distances from
 // start[k] on, up to start[k + 1] or without end.
 constexpr int kRelPad = 160;  // places that a warp's logits (32 rows, 128 keys) can reach past the reach
@@ -167,10 +140,48 @@ struct RelBias {
   int wide;     // a bucket within the reach is wider than kRelWide
   int in_smem;  // the kernel holds its head's row in shared memory (set by its launch, where that fits)
 };
-// zero: n_zero floats to clear along the way (a multiple of 4, 16-byte aligned). The next kernel may be launched early: it
-// waits before it reads the bias and before it ends.
-cudaError_t launch_rel_layout(const RelTable& t, const RelBias& b, float* zero, int64_t n_zero, cudaStream_t stream);
+// One layout (rel_layout.cuh): the table, where it goes, and what is cleared along the way: n_zero float4 of the gradient's parts
+// and a word.
+struct RelLayout {
+  RelTable table;
+  float* by_place;
+  uint8_t* bucket;
+  int2* range;  // gradient only, or nullptr
+  float4* zero;
+  int64_t n_zero;
+  uint32_t* zero_word;  // or nullptr
+};
+int rel_layout_blocks(const RelLayout& l, int threads, int most);
+// The next kernel may be launched early: it waits before it reads the bias and before it ends.
+cudaError_t launch_rel_layout(const RelLayout& l, cudaStream_t stream);
 cudaError_t launch_rel_sum(const float* parts, int64_t rows, int buckets, int heads, void* out, int f32, cudaStream_t stream);
+
+// Builds up to two lists for num_seqs sequences (cu_q / cu_k offsets on the device):
+// sequences with the most blocks first (by key blocks when by_keys), then
+// head by head, blocks of a head in descending or ascending order. Writes
+// `bound` entries (the real ones, then empty ones); scratch holds num_seqs
+// int64. max_nblk bounds every sequence's block count (<= kMaxListBlocks).
+// *zero_word (when given) is set to 0. rel (when given): a bias's layout, by blocks of its own.
+struct TileListSpec {
+  int heads, rows_per_block, by_keys, descending, max_nblk;
+  TileEntry* out;
+  int64_t bound;
+};
+// Beside them, in blocks of their own, the sequences' tensor maps (when given): map m of sequence s,
+// out[s * n + m], is base[m] with its rows ending where the sequence's queries or keys do, so that
+// the rows behind them, which belong to the next sequence, read as zeros in the tile that the
+// sequence ends in (0 x NaN is NaN: an infinity or NaN there would reach this sequence through its
+// zero weights). A kernel only takes its copies' maps from there.
+constexpr int kMaxSeqMaps = 6;
+struct SeqMaps {
+  CUtensorMap base[kMaxSeqMaps];
+  int by_keys[kMaxSeqMaps];  // 1: rows are keys, 0: queries
+  int n = 0;
+  int rows_q = 0, rows_k = 0;  // of the packed tensors
+  CUtensorMap* out = nullptr;
+};
+cudaError_t launch_tile_lists(const int* cu_q, const int* cu_k, int num_seqs, const TileListSpec* specs, int n,
+                              int64_t* scratch, uint32_t* zero_word, const SeqMaps& maps, const RelLayout* rel, cudaStream_t stream);
 
 // Forward kernel arguments (passed by value; tensor maps go separately as
 // __grid_constant__ parameters).

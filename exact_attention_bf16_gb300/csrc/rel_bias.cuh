@@ -1,7 +1,7 @@
 // Learned relative position bias by buckets, as the kernels read it. The bias of
 // a (query, key) pair depends on the head and on r = key - query's position
 // alone, and beyond a reach R on r's sign alone: the bucket borders lie within
-// |r| <= R. A call first lays it out by r (rel_bias.cu): one row of fp32 per
+// |r| <= R. A call first lays it out by r (rel_layout.cuh): one row of fp32 per
 // head, over the softmax scale (in units of the raw logits q . k), of
 // r = -R - kRelPad .. R + kRelPad - 1. A tile of logits that lies beyond the reach
 // as a whole then takes one number, added to the softmax's own offset; any other
@@ -10,7 +10,7 @@
 //
 // What it costs: at N = 8192 (B2, 16 heads over 4, d = 128, causal, 32 buckets up to 128) the forward 391 us against
 // 363 without a bias and the backward 1450 against 1385; at N = 512 (B32, 16 heads, d = 64, both sides, half of the warps'
-// tiles within the reach) 93 against 84 and 325 against 283, 27 of them for the table's gradient.
+// tiles within the reach) 89 against 84 and 325 against 283, 27 of them for the table's gradient.
 #pragma once
 #include "kernels.h"
 #include "ptx_sm100.cuh"

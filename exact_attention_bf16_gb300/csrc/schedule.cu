@@ -28,6 +28,7 @@
 
 #include "kernels.h"
 #include "ptx_sm100.cuh"
+#include "rel_layout.cuh"
 
 namespace gb300 {
 namespace sched {
@@ -37,14 +38,14 @@ constexpr int kSharedSeqs = 1024;  // up to so many sequences need no scratch in
 
 // Block b < n_lists builds list b (a backward's two lists in one launch), the blocks behind them the tensor maps.
 __device__ __forceinline__ void tile_lists(const int* cu_q, const int* cu_k, int num_seqs, const TileListSpec& l0,
-                                           const TileListSpec& l1, int n_lists, int64_t* scratch, uint32_t* zero_word,
+                                           const TileListSpec& l1, int n_lists, int blocks, int64_t* scratch, uint32_t* zero_word,
                                            const SeqMaps& maps) {
   if (static_cast<int>(blockIdx.x) >= n_lists) {
     __shared__ alignas(128) uint32_t s_map[kThreads / 32][32];
     const int ln = static_cast<int>(threadIdx.x & 31u), wp = static_cast<int>(threadIdx.x >> 5);
     const int64_t count = static_cast<int64_t>(num_seqs) * maps.n;
     for (int64_t x = (static_cast<int64_t>(blockIdx.x) - n_lists) * (kThreads / 32) + wp; x < count;
-         x += (static_cast<int64_t>(gridDim.x) - n_lists) * (kThreads / 32)) {
+         x += (static_cast<int64_t>(blocks) - n_lists) * (kThreads / 32)) {
       const int s = static_cast<int>(x / maps.n), m = static_cast<int>(x - static_cast<int64_t>(s) * maps.n);
       s_map[wp][ln] = reinterpret_cast<const uint32_t*>(&maps.base[m])[ln];
       __syncwarp();
@@ -149,14 +150,25 @@ __global__ void __launch_bounds__(kThreads, 1)
     tile_list_kernel(const int* cu_q, const int* cu_k, int num_seqs, TileListSpec l0, TileListSpec l1, int n_lists,
                      int64_t* scratch, uint32_t* zero_word, const __grid_constant__ SeqMaps maps) {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the next kernel reads no list and no map
-  tile_lists(cu_q, cu_k, num_seqs, l0, l1, n_lists, scratch, zero_word, maps);
-  asm volatile("griddepcontrol.wait;" ::: "memory");  // behind the bias's layout: over before this one is
+  tile_lists(cu_q, cu_k, num_seqs, l0, l1, n_lists, static_cast<int>(gridDim.x), scratch, zero_word, maps);
+}
+
+// The same, with a bias's layout in the last rel_blocks blocks: with a launch of its own, which this one ran beside, a packed pass of
+// 7 sequences, forward and backward, took 58 us, 57 so.
+__global__ void __launch_bounds__(kThreads, 1)
+    tile_list_rel_kernel(const int* cu_q, const int* cu_k, int num_seqs, TileListSpec l0, TileListSpec l1, int n_lists,
+                         int64_t* scratch, uint32_t* zero_word, const __grid_constant__ SeqMaps maps,
+                         const __grid_constant__ RelLayout rel, int rel_blocks) {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int blocks = static_cast<int>(gridDim.x) - rel_blocks;
+  if (static_cast<int>(blockIdx.x) >= blocks) rel_layout(rel, static_cast<int>(blockIdx.x) - blocks, rel_blocks);
+  else tile_lists(cu_q, cu_k, num_seqs, l0, l1, n_lists, blocks, scratch, zero_word, maps);
 }
 
 }  // namespace sched
 
 cudaError_t launch_tile_lists(const int* cu_q, const int* cu_k, int num_seqs, const TileListSpec* specs, int n,
-                              int64_t* scratch, uint32_t* zero_word, const SeqMaps& maps, bool early, cudaStream_t stream) {
+                              int64_t* scratch, uint32_t* zero_word, const SeqMaps& maps, const RelLayout* rel, cudaStream_t stream) {
   static_assert(sizeof(CUtensorMap) == 128, "a warp copies a map, four bytes a lane");
   if (num_seqs < 0 || n < 0 || n > 2 || maps.n < 0 || maps.n > kMaxSeqMaps || (maps.n > 0 && maps.out == nullptr) ||
       (reinterpret_cast<uintptr_t>(maps.out) & 127u))
@@ -171,17 +183,17 @@ cudaError_t launch_tile_lists(const int* cu_q, const int* cu_k, int num_seqs, co
   int i = 0;
   do {
     const int blocks = per_launch + (i == 0 ? map_blocks : 0);
-    if (blocks == 0) break;
+    if (blocks == 0 && rel == nullptr) break;
     const TileListSpec l0 = n > 0 ? specs[i] : TileListSpec{}, l1 = n > 0 ? specs[i + per_launch - 1] : TileListSpec{};
-    cudaError_t e;
-    if (early && i == 0) {
-      e = launch_early(sched::tile_list_kernel, dim3(blocks), sched::kThreads, 0, stream, cu_q, cu_k, num_seqs, l0, l1, per_launch,
-                       scratch, zero_word, maps);
+    if (rel != nullptr && i == 0) {
+      const int more = rel_layout_blocks(*rel, sched::kThreads, 152);
+      sched::tile_list_rel_kernel<<<blocks + more, sched::kThreads, 0, stream>>>(cu_q, cu_k, num_seqs, l0, l1, per_launch, scratch,
+                                                                                zero_word, maps, *rel, more);
     } else {
       sched::tile_list_kernel<<<blocks, sched::kThreads, 0, stream>>>(cu_q, cu_k, num_seqs, l0, l1, per_launch, scratch,
                                                                      zero_word, maps);
-      e = cudaGetLastError();
     }
+    const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     i += per_launch;
   } while (i < n);

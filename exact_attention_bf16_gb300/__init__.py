@@ -85,6 +85,8 @@ def _rel_fields(q, t, rel_max_distance, rel_bidirectional):
         raise ValueError(f"rel_bias must be a contiguous bfloat16 or float32 CUDA tensor [buckets, {q.shape[-2]}]")
     if t.get_device() != q.get_device():
         raise ValueError(f"rel_bias is on {t.device} but q is on {q.device}")
+    if not 0 < rel_max_distance < 2 ** 31:
+        raise ValueError(f"rel_max_distance {rel_max_distance} must be a positive 32-bit number")
     return (t.data_ptr(), _abi.TABLE_F32 if t.dtype is _F32 else _abi.TABLE_BF16, t.shape[0], int(rel_max_distance),
             1 if rel_bidirectional else 0)
 

@@ -505,3 +505,73 @@ def test_refusals(ea, bad):
     with pytest.raises((ValueError, ea.AttnError)):
         o, lse = ea.attn_fwd(q, q, q, **kw)
         ea.attn_bwd(q, q, q, o, lse, q, **kw, **bw)
+
+
+@pytest.mark.parametrize("far", [2 ** 32 + 128, -2 ** 32 + 128])
+def test_a_distance_past_32_bits_is_refused(ea, far):
+    q = torch.zeros(4, 2, 64, device="cuda").bfloat16()
+    cu = torch.tensor([0, 4], dtype=torch.int32, device="cuda")
+    kw = dict(rel_bias=torch.zeros(8, 2, device="cuda"), rel_max_distance=far)
+    with pytest.raises(ValueError):
+        ea.attn_fwd(q[None], q[None], q[None], **kw)
+    with pytest.raises(ValueError):
+        ea.attn_fwd_varlen(q, q, q, cu, cu, 4, 4, **kw)
+
+
+@pytest.mark.parametrize("packed", [False, True])
+@pytest.mark.parametrize("keep", [False, True])
+def test_a_captured_training_step_of_rotation_and_bias(ea, packed, keep):
+    """rotary, attention with a learned table and both gradients, captured once and replayed with other inputs; keep: while the
+    eager graph of the same leaves is alive."""
+    rng = np.random.default_rng(33)
+    n, h, hk, d = 300, 4, 2, 64
+    q, k, v, do = _t(rng, 1, n, h, d), _t(rng, 1, n, hk, d), _t(rng, 1, n, hk, d), _t(rng, 1, n, h, d)
+    table = log_table(rng, 32, h, torch.float32)
+    angle = torch.arange(n, device="cuda", dtype=torch.float64)[:, None] * 0.9 ** torch.arange(16, device="cuda", dtype=torch.float64)
+    cos, sin = angle.cos().float(), angle.sin().float()
+    cu = torch.tensor([0, 100, 100, 233, n], dtype=torch.int32, device="cuda")
+    leaf = [x.requires_grad_() for x in (q, k, v, table)]
+    how = dict(causal=True, rel_bias=table, rel_max_distance=64, rel_bidirectional=False)
+
+    def step():
+        qr, kr = ea.rotary(q, k, cos, sin)
+        if packed:
+            o = ea.attention_varlen(qr[0], kr[0], v[0], cu, cu, n, n, **how)[None]
+        else:
+            o = ea.attention(qr, kr, v, **how)
+        return o, torch.autograd.grad(o, leaf, do, retain_graph=keep)
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        eager = step()
+    torch.cuda.current_stream().wait_stream(side)
+    if not keep:
+        del eager
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = step()
+    for lens in ([100, 0, 133, 67], [300, 0, 0, 0], [1, 9, 30, 260]):
+        cu.copy_(torch.tensor([0, *np.cumsum(lens)], dtype=torch.int32))
+        with torch.no_grad():
+            for x in (q, k, v, do):
+                x.copy_(_t(rng, *x.shape))
+            table.copy_(log_table(rng, 32, h, torch.float32))
+        graph.replay()
+        want = step()
+        torch.cuda.synchronize()
+        ea.attn_get_device_status()
+        assert torch.equal(got[0], want[0])
+        assert all(torch.equal(a, b) for a, b in zip(got[1], want[1]))
+    with torch.no_grad():
+        qr, kr = ea.rotary(q, k, cos, sin)
+    at = 0
+    dtable, slack = 0.0, 0.0
+    for m in lens if packed else [n]:
+        part = slice(at, at + m)
+        ref = attention64(qr[0, part], kr[0, part], v.detach()[0, part], table.detach(), 64, False, d ** -0.5, True, do[0, part])
+        # half a step each of P and of O, whose weights sum to one
+        assert float((got[0].detach()[0, part].double() - ref["o"]).abs().max()) <= 2 * 2.0 ** -8 * float(v.detach().abs().max())
+        dtable, slack, at = dtable + ref["dtable"], slack + ref["slack"], at + m
+    check_table(got[1][3], dtable, slack)

@@ -233,25 +233,27 @@ struct RelPlan {
   size_t place_bytes = 0, bucket_bytes = 0, range_bytes = 0;
 };
 template <typename P>
-RelPlan rel_plan(const P* p, int64_t longest) {
+RelPlan rel_plan(const P* p, int64_t longest, int64_t rows) {
   RelPlan r;
   if (p->score_mod != ATTN_SCORE_RELBIAS || p->heads < 1 || check_rel(p) != ATTN_OK) return r;
   r.reach = rel_reach(p->rel_bidirectional ? p->rel_buckets / 2 : p->rel_buckets, p->rel_max_distance, longest);
   const int64_t width = 2 * static_cast<int64_t>(r.reach) + 2 * kRelPad;
-  r.place_bytes = round256(p->heads * width * 4);
+  r.place_bytes = round256(rows * width * 4);
   r.bucket_bytes = round256(width);
   r.range_bytes = kRelMaxBuckets * sizeof(int2);
   return r;
 }
 // The layout of the call's table, to be launched (b's arrays are set), and the rest of b.
 template <typename P>
-RelLayout rel_layout_of(const P* p, const RelPlan& plan, RelBias* b, int64_t n_zero, uint32_t* zero_word) {
+RelLayout rel_layout_of(const P* p, const RelPlan& plan, RelBias* b, int64_t n_zero, uint32_t* zero_word, int group = 1) {
   RelLayout l{};
   RelTable& t = l.table;
   t.table = p->rel_bias;
   t.inv_scale = 1.f / p->softmax_scale;
   t.f32 = p->rel_bias_dtype == ATTN_TABLE_F32;
   t.heads = p->heads;
+  t.group = group;
+  t.fours = group > 1 ? (group + 3) / 4 : 0;
   t.buckets = b->buckets = p->rel_buckets;
   t.two_sided = p->rel_bidirectional ? 1 : 0;
   t.side = t.two_sided ? t.buckets / 2 : t.buckets;
@@ -449,7 +451,7 @@ size_t fwd_split_bytes(const attn_fwd_params* p, const SplitPlan& sp) {
 }
 // The bias's layout of a forward or backward call.
 RelPlan call_rel_plan(const attn_fwd_params* p, bool varlen) {
-  return rel_plan(p, varlen ? std::max(p->max_seqlen_q, p->max_seqlen_k) : std::max(p->seqlen_q, p->seqlen_k));
+  return rel_plan(p, varlen ? std::max(p->max_seqlen_q, p->max_seqlen_k) : std::max(p->seqlen_q, p->seqlen_k), p->heads);
 }
 size_t fwd_workspace_bytes(const attn_fwd_params* p, bool varlen) {
   const size_t v16 = fwd_v16_bytes(p, varlen);
@@ -1339,7 +1341,7 @@ struct PagedPlan {
   bool even = true;
   int tile_tokens = 0, part_rows = 0;
   bool decode = false;
-  int q_box_tokens = 0;
+  int q_box_tokens = 0, rel_group = 1;
   int64_t items = 0;
   size_t off_lse = 0, off_merge = 0, off_list = 0, off_items = 0, off_rel = 0, bytes = 0;
   RelPlan rel;
@@ -1365,7 +1367,9 @@ PagedPlan paged_plan(const attn_paged_params* p) {
     pl.off_items = pl.off_list + 256;
     pl.bytes = pl.off_items + round256(pl.items * static_cast<int64_t>(sizeof(ChunkItem)));
   }
-  pl.rel = rel_plan(p, std::max<int64_t>(static_cast<int64_t>(p->max_pages) * p->page_size, p->max_seqlen_q));
+  pl.rel_group = pl.even ? 1 : group;  // RelPaged
+  pl.rel = rel_plan(p, std::max<int64_t>(static_cast<int64_t>(p->max_pages) * p->page_size, p->max_seqlen_q),
+                    pl.rel_group > 1 ? static_cast<int64_t>(p->heads_kv) * ((group + 3) / 4 * 4) : p->heads);
   pl.off_rel = pl.bytes;
   pl.bytes += pl.rel.place_bytes + pl.rel.bucket_bytes;
   return pl;
@@ -1419,7 +1423,7 @@ attn_status_t run_fwd_paged(const attn_paged_params* p, void* ws, size_t ws_byte
   if (p->score_mod == ATTN_SCORE_RELBIAS) {
     a.rel.by_place = reinterpret_cast<const float*>(base + pl.off_rel);
     a.rel.bucket = base + pl.off_rel + pl.rel.place_bytes;
-    e = launch_rel_layout(rel_layout_of(p, pl.rel, &a.rel, 0, nullptr), stream);
+    e = launch_rel_layout(rel_layout_of(p, pl.rel, &a.rel, 0, nullptr, pl.rel_group), stream);
     if (e != cudaSuccess) return cuda_fail(e, "bias layout");
   }
   int dev = 0, sms = 0;

@@ -347,7 +347,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (MOD == kModAlibi && valid)
           slope = fabsf(__ldg(a.alibi_slopes + w.hk * a.kv_group + static_cast<int>(quarter * 32 + lane) % a.kv_group) *
                         a.inv_scale);
-        const RelRow<kRelPad, false> rel{a.rel, 0, MOD == kModRelBias ? w.hk * a.kv_group + static_cast<int>(quarter * 32 + lane) % a.kv_group : 0};
+        const RelPaged<!EVEN> rel(a.rel, w.hk, a.kv_group, static_cast<int>(quarter * 32 + lane) % a.kv_group);
         // whether this lane's page of key block kt holds keys (one lane per page of a block)
         auto page_ok = [&](int kt) -> bool {
           const int np = a.page_size < BN ? BN >> a.page_shift : 1;
@@ -365,6 +365,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (; kt < kt_end; kt += step, ++s_phase, first = false) {
           const uint32_t pages = __ballot_sync(0xffffffffu, pg_ok);
           if (kt + step < kt_end) pg_ok = page_ok(kt + step);  // fetched one block ahead
+          // relative position bias: one number per row, which goes into the softmax's offsets (add, log2 units; on its way while the
+          // logits are), or a number per logit (near; a warp's tokens are at most 32 in a row, and rows without one take any places)
+          const int r0 = valid ? kt * BN - pos : 0;
+          float add = 0.f;
+          bool near = false;
+          if constexpr (MOD == kModRelBias) {
+            const bool far = rel.far(r0, r0 + BN - 1, add) || !valid;
+            near = !__all_sync(0xffffffffu, far);
+            add = near || klim <= kt * BN ? 0.f : add * a.scale_log2;
+          }
           ok = mbar_wait_warp(&bar->s_full[i], s_phase & 1u, a.status, 0x3310 + i);
           if (!ok) break;
           // K of this block has been read, and V of the stream's block before (not dual: by tile 1's S, which is
@@ -392,23 +402,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                 s[c] = __float_as_uint(__uint_as_float(s[c]) - fabsf(fmaf(slope, static_cast<float>(c), base)));
             }
             const float sl2 = a.scale_log2;
-            // relative position bias: one number per row, which goes into the softmax's offsets (add, log2 units), or a number per
-            // logit (a warp's tokens are at most 32 in a row; rows without one take any places)
-            float add = 0.f;
-            if constexpr (MOD == kModRelBias) {
-              const int r0 = valid ? kt * BN - pos : 0;
-              const bool far = rel.far(r0, r0 + BN - 1, add) || !valid;
-              if (!__all_sync(0xffffffffu, far)) {
-                rel.at(r0, [&](auto bias) {
+            if (MOD == kModRelBias && near) {
+              rel.at(r0, [&](auto bias) {
 #pragma unroll
-                  for (int c = 0; c < BN; ++c) s[c] = __float_as_uint(__uint_as_float(s[c]) + bias(c));
-                });
-                add = 0.f;
-              }
-              add *= sl2;
+                for (int c = 0; c < BN; ++c) s[c] = __float_as_uint(__uint_as_float(s[c]) + bias(c));
+              });
             }
             const int cnt = klim - kt * BN;  // visible keys of this row in the block
-            if (MOD == kModRelBias && cnt <= 0) add = 0.f;
             if (cnt < BN) {
 #pragma unroll
               for (int c = 0; c < BN; ++c)

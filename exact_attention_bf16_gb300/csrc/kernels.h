@@ -126,6 +126,7 @@ struct RelTable {
   const void* table;  // [buckets, heads], bf16 or fp32
   float inv_scale;    // 1 / softmax_scale
   int f32, heads, buckets, side, two_sided, reach;
+  int group, fours;  // fours > 0: the group query heads of a K/V head by fours, their rows place by place; 0: a row behind the other
   int start[kRelMaxBuckets];
 };
 // Laid out by place, with each place's bucket, and for the gradient each bucket's first and last place, the buckets beyond the
@@ -151,6 +152,9 @@ struct RelLayout {
   int64_t n_zero;
   uint32_t* zero_word;  // or nullptr
 };
+__host__ __device__ inline int64_t rel_rows(const RelTable& t) {
+  return t.fours > 0 ? static_cast<int64_t>(t.heads / t.group) * t.fours * 4 : t.heads;
+}
 int rel_layout_blocks(const RelLayout& l, int threads, int most);
 // The next kernel may be launched early: it waits before it reads the bias and before it ends.
 cudaError_t launch_rel_layout(const RelLayout& l, cudaStream_t stream);

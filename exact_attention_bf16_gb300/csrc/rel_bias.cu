@@ -48,7 +48,7 @@ __global__ void __launch_bounds__(1024) sum_parts_kernel(const float* parts, int
 }  // namespace rel
 
 int rel_layout_blocks(const RelLayout& l, int threads, int most) {
-  const int64_t items = std::max<int64_t>(static_cast<int64_t>(2 * l.table.reach + 2 * kRelPad) * l.table.heads, l.n_zero);
+  const int64_t items = std::max<int64_t>((2 * l.table.reach + 2 * kRelPad) * rel_rows(l.table), l.n_zero);
   return static_cast<int>(std::min<int64_t>((items + threads - 1) / threads, most));
 }
 

@@ -81,6 +81,40 @@ struct RelRow {
   }
 };
 
+// A head's row in L1 as paged_kernel reads it: by itself, or (FOURS, heads that share a K/V head) place by place among four of
+// them (RelTable::fours): a warp's rows are a few tokens of all these heads, and a load takes a step per line. Chunks of 300 to 1500
+// tokens over up to 8192 keys, 16 heads over 4, 2 and 1, by themselves 118, 108 and 110 us, in fours 114, 102 and 100 (all heads
+// of the group side by side, a stride known at run time: 126 for 127, but 16 over 16 156 for 148). Not where one tile of rows
+// holds any request's tokens (16 requests of 20: 56.3 us so, 55.0).
+template <bool FOURS>
+struct RelPaged {
+  const RelBias& b;
+  const float* at0;  // of place 0
+  bool fours;
+  __device__ __forceinline__ RelPaged(const RelBias& bias, int hk, int group, int h) : b(bias), fours(FOURS && group > 1) {
+    const int64_t width = 2 * bias.reach + 2 * kRelPad, zero = bias.reach + kRelPad;
+    at0 = fours ? bias.by_place + 4 * ((static_cast<int64_t>(hk) * ((group + 3) / 4) + h / 4) * width + zero) + h % 4
+                : bias.by_place + (static_cast<int64_t>(hk) * group + h) * width + zero;
+  }
+  __device__ __forceinline__ bool far(int r_min, int r_max, float& add) const {
+    const bool l = r_max <= -b.reach, r = r_min >= b.reach;
+    const int at = l ? -b.reach : b.reach;
+    add = l || r ? __ldg(at0 + (fours ? 4 * at : at)) : 0.f;
+    return l || r;
+  }
+  // f(load) with load(c) the bias of place r + c.
+  template <typename F>
+  __device__ __forceinline__ void at(int r, F&& f) const {
+    if (fours) {
+      const float* from = at0 + 4 * r;
+      f([from](int c) { return __ldg(from + 4 * c); });
+    } else {
+      const float* from = at0 + r;
+      f([from](int c) { return __ldg(from + c); });
+    }
+  }
+};
+
 // What the dQ kernel holds of the gradient in shared memory: each warp's sums by bucket, the halves' sums of a row, and behind
 // them, where the row is there too (b.in_smem), the buckets' first and last places, the row and its places' buckets.
 constexpr int kRelRowSums = 2 * 128 * 4, kRelSums = 8 * kRelMaxBuckets * 4 + kRelRowSums, kRelRange = kRelMaxBuckets * 8;  // bytes

@@ -23,10 +23,17 @@ __device__ __forceinline__ int rel_bucket(const RelTable& t, int r) {
 __device__ __forceinline__ void rel_layout(const RelLayout& l, int block, int blocks) {
   const RelTable& t = l.table;
   const int width = 2 * t.reach + 2 * kRelPad;
-  const int64_t all = static_cast<int64_t>(width) * t.heads, step = static_cast<int64_t>(blocks) * blockDim.x;
+  const int64_t all = static_cast<int64_t>(width) * rel_rows(t), step = static_cast<int64_t>(blocks) * blockDim.x;
   const int64_t me = static_cast<int64_t>(block) * blockDim.x + threadIdx.x;
   for (int64_t i = me; i < all; i += step) {
-    const int h = static_cast<int>(i / width), x = static_cast<int>(i - static_cast<int64_t>(h) * width);
+    const int64_t y = t.fours > 0 ? i >> 2 : i;
+    int h = static_cast<int>(y / width);
+    const int x = static_cast<int>(y - static_cast<int64_t>(h) * width);
+    if (t.fours > 0) {
+      const int hk = h / t.fours, g = 4 * (h - hk * t.fours) + static_cast<int>(i & 3);
+      if (g >= t.group) continue;
+      h = hk * t.group + g;
+    }
     const int b = rel_bucket(t, x - t.reach - kRelPad);
     const int64_t at = static_cast<int64_t>(b) * t.heads + h;
     const float v = t.f32 ? __ldg(static_cast<const float*>(t.table) + at)

@@ -397,6 +397,12 @@ def test_paged(ea, d, dv, h, hk, page, new):
             assert float((lse[:, a:b].double() - ref["lse"]).abs().max()) <= 1e-4
 
 
+@pytest.mark.parametrize("h,hk", [(6, 2), (10, 2), (9, 3), (8, 4), (24, 2), (128, 1)])
+@pytest.mark.parametrize("new", [[1, 300, 3, 1, 70], [20, 2, 0, 1, 17]])
+def test_paged_chunks_of_heads_in_fours_and_others(ea, h, hk, new):
+    test_paged(ea, 64, 64, h, hk, 32, new)
+
+
 @pytest.mark.parametrize("h,hk,chunk", [(4, 4, 1), (16, 1, 2), (8, 2, 70)])
 def test_paged_captured_and_at_once(ea, h, hk, chunk):
     """One captured call replayed as lengths change, and calls on three streams, with workspaces of their own."""

@@ -185,6 +185,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const __grid_constant__ CUtensorMap tmv, const __grid_constant__ CUtensorMap tmdo, const BwdArgs a) {
   using C = DkdvCfg<DQK, DV, FUSED>;
   constexpr int QB = C::QB;
+  // the sum of a bias's gradient, whose parts the kernel ahead of this one has written, takes the SMs that this one leaves
+  if constexpr (is_rel(MOD)) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* sK = smem;
@@ -721,6 +723,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                      const __grid_constant__ CUtensorMap tmv, const __grid_constant__ CUtensorMap tmdo, const BwdArgs a) {
   using C = DkdvWCfg;
   constexpr int QB = C::QB;
+  if constexpr (is_rel(MOD)) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // as in dkdv_kernel
   extern __shared__ __align__(1024) uint8_t smem_w[];
   if ((smem_u32(smem_w) & 1023u) != 0u) {  // the 128-byte-swizzled tiles need 1024-byte alignment
     if (threadIdx.x == 0) record_error(a.status, DEV_BAD_CONFIG, 0x1400);

@@ -25,7 +25,6 @@ __global__ void __launch_bounds__(1024) sum_parts_kernel(const float* parts, int
   const int h = static_cast<int>(blockIdx.x), lanes = static_cast<int>(blockDim.x) / buckets;
   const int b = static_cast<int>(threadIdx.x) % buckets, y = static_cast<int>(threadIdx.x) / buckets;
   float sum = 0.f;
-  asm volatile("griddepcontrol.wait;" ::: "memory");  // launched before the parts' kernel is over
   if (y < lanes) {
     const float* p = parts + (static_cast<int64_t>(h) * rows) * buckets + b;
 #pragma unroll 8
@@ -43,6 +42,9 @@ __global__ void __launch_bounds__(1024) sum_parts_kernel(const float* parts, int
     if (f32) static_cast<float*>(out)[at] = sum;
     else static_cast<__nv_bfloat16*>(out)[at] = __float2bfloat16_rn(sum);
   }
+  // Beside the dK/dV kernel, behind the parts' kernel: over before this one is. (Behind both, the backward of
+  // 7 packed sequences of up to 500 took 39.4 us, 38.1 so; of 32 x 512, 16 heads, 327 and 324.)
+  asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
 }  // namespace rel

@@ -581,3 +581,18 @@ def test_a_captured_training_step_of_rotation_and_bias(ea, packed, keep):
         assert float((got[0].detach()[0, part].double() - ref["o"]).abs().max()) <= 2 * 2.0 ** -8 * float(v.detach().abs().max())
         dtable, slack, at = dtable + ref["dtable"], slack + ref["slack"], at + m
     check_table(got[1][3], dtable, slack)
+
+
+def test_packed_in_a_buffer_too_long_for_a_tile_list(ea):
+    """max_seqlen bounds the lengths; past what a list of tiles holds (2047 of 128 or 256 rows) the kernels run without one, with
+    the same results."""
+    lens, m = [300, 0, 7, 129], 2048 * 256
+    q, k, v, o, lse, do, args, kw, grads = _packed(ea, 41, lens, lens, 1, 1, 64, 64, False, True, 32, 128, spare=m)
+    cu, n = args[0], sum(lens)
+    for longest in (2048 * 128, m):
+        o2, lse2 = ea.attn_fwd_varlen(q, k, v, cu, cu, longest, longest, **kw)
+        again = ea.attn_bwd_varlen(q, k, v, o, lse, do, cu, cu, longest, longest, **kw)
+        torch.cuda.synchronize()
+        ea.attn_get_device_status()
+        assert torch.equal(o[:n], o2[:n]) and torch.equal(lse[:, :n], lse2[:, :n])
+        assert all(torch.equal(a[:n], b[:n]) for a, b in zip(again, grads))

@@ -1519,15 +1519,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     const float sl2 = a.scale_log2;
     const float alibi_slope = MOD == kModAlibi ? __ldg(a.alibi_slopes + h) * a.inv_scale : 0.f;  // raw units
-    // relative position bias: its row and the buckets' gradient, in dO's room where that is in TMEM. Beyond the reach on the right dS is added up
-    // per row. On the left it is not: a row's dS sum to zero over its keys, so the CTA's sum there is minus all the others'
-    // (adding them up cost the kernel 8%; the D that comes from the rounded O also shows less so, P of the few keys within the reach
-    // instead of the many beyond it). Only where such tiles were passed over, and not with split keys, whose CTAs do not see whole
-    // rows.
+    // relative position bias: its row and the buckets' gradient, in dO's room where that is in TMEM. Where a warp's places of a
+    // tile are all in one bucket, dS is added up per row (far_sum, of far_bucket) until a tile lies in another one. Every bucket is
+    // summed from its own pairs: a row's dS sum to zero, but only with the exact D, and the D from O rounded to bf16 would leave
+    // its error of the whole row in a bucket that was taken as minus the others, however little weight its keys have (with a
+    // bias of -12 seventeen times the entry's own gradient; without that sum B32 H16 N512 d64 dQ 141 us, 145 with it, B2 H16 over 4
+    // N8192 d128 559 and 561).
     const RelGrad<kDqRelPad> rel_grad{a.rel, smem_u32(C::DO_TMEM ? sdO : smem + C::OFF_BAR + 256)};
     const RelRow<kDqRelPad> rel{a.rel, rel_grad.row(), h};
-    float right_sum = 0.f;
-    bool left_out = false;
+    float far_sum = 0.f;
+    int far_bucket = a.rel.left;
     bool rows_ok = true;  // every row of the warp has keys
     if constexpr (is_rel(MOD)) {
       rel_grad.prefetch(rel.global() - a.rel.reach - kDqRelPad, static_cast<int>(threadIdx.x), kSoftThreads);
@@ -1706,17 +1707,17 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lane == 0) mbar_arrive(&bar->ds_full);
       if constexpr (is_rel(MOD)) {  // while the tensor core takes dS
         if (!near) {
-          const bool right = r00 - 31 >= a.rel.reach;
-          if (right || split || (MOD == kModRelWide && one_bucket >= 0)) {
+          if (a.rel.parts != nullptr) {
+            const int bucket = one_bucket >= 0 ? one_bucket : r00 - 31 >= a.rel.reach ? a.rel.right : a.rel.left;
+            if (bucket != far_bucket) {
+              rel_grad.add(static_cast<int>(warp), far_bucket, lse2 != INFINITY ? far_sum : 0.f);
+              far_sum = 0.f, far_bucket = bucket;
+            }
             float2 t2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
             for (int e = 0; e < 64; e += 2)
               t2[(e / 2) & 1] = fadd2(t2[(e / 2) & 1], make_float2(__uint_as_float(s[e]), __uint_as_float(s[e + 1])));
-            float x = (t2[0].x + t2[0].y) + (t2[1].x + t2[1].y);
-            if (right) right_sum += x;
-            else rel_grad.add(static_cast<int>(warp), MOD == kModRelWide && one_bucket >= 0 ? one_bucket : a.rel.left, lse2 != INFINITY ? x : 0.f);
-          } else {
-            left_out = left_out || radd > -INFINITY;
+            far_sum += (t2[0].x + t2[0].y) + (t2[1].x + t2[1].y);
           }
         } else if (grad) {
           float x[64], diag[3];
@@ -1733,26 +1734,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     if constexpr (is_rel(MOD)) {
       if (a.rel.parts != nullptr) {
-        rel_grad.add(static_cast<int>(warp), a.rel.right, lse2 != INFINITY ? right_sum : 0.f);
-        const bool any = named_barrier_or(1, kSoftThreads, left_out);
+        rel_grad.add(static_cast<int>(warp), far_bucket, lse2 != INFINITY ? far_sum : 0.f);
+        named_barrier_sync(1, kSoftThreads);
         const int64_t place = a.cu_q != nullptr ? static_cast<int64_t>(U.q_start) / MB + U.unit + m
                                                 : (static_cast<int64_t>(U.b) * a.n_qblk + m) * (split ? a.dq_split : 1) + range;
         if (warp == 0 && place >= 0 && place < a.rel.part_rows) {  // (else offsets overrun total_q)
-          float sum[4], all = 0.f;  // of bucket lane + 32 k, the warps' sums in order
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            sum[k] = 0.f;
-#pragma unroll
-            for (int y = 0; y < kSoftThreads / 32; ++y) sum[k] += ld_shared_f32(rel_grad.sum(y, static_cast<int>(lane) + 32 * k));
-            all += sum[k];
-          }
-#pragma unroll
-          for (int d = 16; d > 0; d >>= 1) all += __shfl_xor_sync(0xffffffffu, all, d);
           float* dst = a.rel.parts + (static_cast<int64_t>(h) * a.rel.part_rows + place) * a.rel.buckets;
+          for (int b = static_cast<int>(lane); b < a.rel.buckets; b += 32) {  // the warps' sums, in order
+            float sum = 0.f;
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const int b = static_cast<int>(lane) + 32 * k;
-            if (b < a.rel.buckets) dst[b] = sum[k] - (any && b == a.rel.left ? all : 0.f);
+            for (int y = 0; y < kSoftThreads / 32; ++y) sum += ld_shared_f32(rel_grad.sum(y, b));
+            dst[b] = sum;
           }
         }
       }

@@ -713,6 +713,12 @@ def _append_fields(k, v, k_cache, v_cache, slot_mapping):
             ks[0], ks[1], ks[2], vs[2], kcs[1], kcs[0]), ks
 
 
+def _no_table_gradient(cos, sin):
+    for name, t in (("cos", cos), ("sin", sin)):
+        if isinstance(t, torch.Tensor) and t.requires_grad and torch.is_grad_enabled():
+            raise ValueError(f"{name} has no gradient here: pass it detached")
+
+
 def _check_rotation(cos, sin, device: int, rotary_offset: int, head: int):
     """The checked tables' fields: pointers, row stride, positions, rotary_dim."""
     for name, t in (("cos", cos), ("sin", sin)):
@@ -720,8 +726,6 @@ def _check_rotation(cos, sin, device: int, rotary_offset: int, head: int):
             raise ValueError(f"{name} must be a float32 CUDA tensor [positions, rotary_dim / 2] with contiguous rows")
         if t.get_device() != device:
             raise ValueError(f"{name} is on {t.device} but the call is on cuda:{device}")
-        if t.requires_grad and torch.is_grad_enabled():
-            raise ValueError(f"{name} has no gradient here: pass it detached")
     (n, half), (row, col) = cos.shape, cos.stride()
     if sin.shape != cos.shape or (n > 1 and sin.stride() != (row, col)) or col != 1 or sin.stride(1) != 1:
         raise ValueError(f"cos {tuple(cos.shape)} and sin {tuple(sin.shape)} must be alike, strides too, with contiguous rows")
@@ -741,6 +745,7 @@ def attn_kv_append_rotary(q: Optional[torch.Tensor], k: torch.Tensor, v: torch.T
     [tokens, H, d_qk], unless None, is rotated into ``q_out`` (which may be q; made when not given). A token whose
     position lies outside the tables writes nothing, one whose slot is outside the cache only its row of q_out.
     Returns q_out (None without q)."""
+    _no_table_gradient(cos, sin)
     append, ks = _append_fields(k, v, k_cache, v_cache, slot_mapping)
     dev = k.get_device()
     _check_int32("positions", positions, dev, ks[0])
@@ -786,6 +791,7 @@ def attn_rotary(q: torch.Tensor, k: Optional[torch.Tensor], cos: torch.Tensor, s
     is int32 [B, N] or [N] ([total]); without it a row's position is its index. ``inverse`` turns back: of the
     gradients of the outputs it gives those of the inputs. q_out and k_out may be q and k. Rows whose position lies
     outside the tables are not written. Returns (q_out, k_out)."""
+    _no_table_gradient(cos, sin)
     dim = 3 if isinstance(q, torch.Tensor) and q.dim() == 3 else 4
     qs, qt = _bf16_layout("q", q, dim)
     dev = q.get_device()
@@ -1000,5 +1006,6 @@ class _Rotary(torch.autograd.Function):
 
 def rotary(q, k, cos, sin, positions: Optional[torch.Tensor] = None, rotary_offset: int = 0, interleaved: bool = False):
     """Autograd wrapper over attn_rotary: (q, k) rotated, or q alone where k is None. Every row needs a position inside
-    the tables (rows without one are not written)."""
+    the tables (rows without one are not written). The tables get no gradient; ones that ask for it are refused."""
+    _no_table_gradient(cos, sin)  # (inside the function no gradients are recorded)
     return _Rotary.apply(q, k, cos, sin, positions, rotary_offset, interleaved)

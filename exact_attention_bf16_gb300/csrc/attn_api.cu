@@ -1228,7 +1228,8 @@ attn_status_t run_rotary(const attn_rotary_params* p, cudaStream_t stream) {
     if (p->heads_kv < 1) return ATTN_ERR_INVALID_ARG;
     ATTN_TRY(check_turned(p->k, p->k_batch_stride, p->k_row_stride, p->k_head_stride, p->k_out, p->k_out_batch_stride,
                           p->k_out_row_stride, p->k_out_head_stride, p->batch, p->seqlen, p->heads_kv, none));
-    if (!none && p->q_out == p->k_out) return ATTN_ERR_INVALID_ARG;
+    // (one launch turns both: an output at the other's input would be written before that is read)
+    if (!none && (p->q_out == p->k_out || p->q_out == p->k || p->k_out == p->q)) return ATTN_ERR_INVALID_ARG;
   }
   if (p->positions ? (reinterpret_cast<uintptr_t>(p->positions) & 3u) != 0 || p->positions_batch_stride < 0
                    : p->seqlen > p->num_positions)
@@ -1277,6 +1278,8 @@ attn_status_t run_kv_append_rotary(const attn_kv_append_rotary_params* p, cudaSt
     if (p->heads < 1) return ATTN_ERR_INVALID_ARG;
     ATTN_TRY(check_turned(p->q, 0, p->q_row_stride, p->q_head_stride, p->q_out, 0, p->q_out_row_stride, p->q_out_head_stride, 1,
                           w.tokens, p->heads, none));
+    for (const void* x : {w.k, w.v, static_cast<const void*>(w.k_cache), static_cast<const void*>(w.v_cache)})
+      if (!none && p->q_out == x) return ATTN_ERR_INVALID_ARG;
   }
   if (none) return ATTN_OK;
   if (!aligned4(p->positions)) return ATTN_ERR_INVALID_ARG;

@@ -511,7 +511,8 @@ attn_status_t attn_kv_append(const attn_kv_append_params* p, attn_stream_t strea
  *
  * attn_rotary rotates q [batch, seqlen, heads, d_qk] and, when given, k [batch, seqlen,
  * heads_kv, d_qk] (bf16; packed tensors are batch 1) into q_out and k_out, which may be
- * q and k themselves (same base and strides) but must not overlap them otherwise.
+ * q and k themselves (same base and strides) but must not overlap them otherwise (at the
+ * same address as the other input or output: ATTN_ERR_INVALID_ARG).
  * inverse != 0 turns by the negative angle: applied to dQ and dK of the rotated tensors,
  * it gives the gradients of the ones before. positions (int32, row b at
  * b * positions_batch_stride) may be NULL: a row's position is then its index in seqlen,
@@ -546,7 +547,7 @@ attn_status_t attn_rotary(const attn_rotary_params* p, attn_stream_t stream);
 
 /* attn_kv_append with the rotation on the way: K rows are rotated by positions[i] as they
  * go to their slots, V rows copied, and, when q is given (q [tokens, heads, d_qk]), q is
- * rotated into q_out (which may be q). `append` and its rules are attn_kv_append's; the
+ * rotated into q_out (which may be q, but none of the append's tensors). `append` and its rules are attn_kv_append's; the
  * rotation's are attn_rotary's, positions is required (int32 [tokens], as attn_kv_plan
  * writes it). A token whose position lies outside [0, num_positions) writes nothing, one
  * whose slot does writes its q_out alone. */

@@ -293,7 +293,8 @@ def attn_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, *, causal: bool 
     ``alibi_slopes`` or ``rel_bias`` select a score modification (include/attn.h, attn_fwd_params.score_mod):
     ``rel_bias`` [buckets, H] (bf16 or float32, up to 128 buckets) adds a learned bias by the bucket of the key's position
     relative to the query's, both sides apart with ``rel_bidirectional`` (else all keys behind the query share bucket 0),
-    whole distances first and then logarithmic up to ``rel_max_distance`` (attn_fwd_params.rel_bias).
+    whole distances first and then logarithmic up to ``rel_max_distance`` (attn_fwd_params.rel_bias); -inf masks a bucket, and
+    finite entries count up to +-65536.
     q, k, v may instead all be torch.float8_e4m3fn (d = 128), standing for their values times
     ``q_descale``, ``k_descale``, ``v_descale``. ``cta_pair`` runs the two-SM forward (d = 128)."""
     f8 = _check_inputs(q, k, v, 4)

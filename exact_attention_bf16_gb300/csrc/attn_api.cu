@@ -223,7 +223,7 @@ attn_status_t check_rel(const P* p) {
   if (p->rel_buckets < 1 || p->rel_buckets > kRelMaxBuckets || (p->rel_bidirectional && p->rel_buckets % 2))
     return ATTN_ERR_INVALID_ARG;
   const int side = p->rel_bidirectional ? p->rel_buckets / 2 : p->rel_buckets;
-  if (!std::isfinite(1.f / p->softmax_scale)) return ATTN_ERR_INVALID_ARG;  // the bias is taken over the scale
+  if (!std::isfinite(kRelMaxEntry / p->softmax_scale)) return ATTN_ERR_INVALID_ARG;  // the bias is taken over the scale
   return p->rel_max_distance > side / 2 && p->rel_max_distance <= 65536 ? ATTN_OK : ATTN_ERR_INVALID_ARG;
 }
 

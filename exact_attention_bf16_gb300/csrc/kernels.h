@@ -121,6 +121,10 @@ cudaError_t launch_early(K kern, dim3 grid, int threads, int smem, cudaStream_t 
 // start[k] on, up to start[k + 1] or without end.
 constexpr int kRelPad = 160;  // places that a warp's logits (32 rows, 128 keys) can reach past the reach
 constexpr int kRelMaxBuckets = 128;
+// Finite entries count up to this size. A logit of size m is held, and its LSE stored, in steps of 2^-24 m: P comes out within 2^-5
+// at 65536, but a row that saw nothing but -1e9 or a type's lowest value had steps of 64, in which P overflows, or infinities once
+// the entry is taken over the scale.
+constexpr float kRelMaxEntry = 65536.f;
 constexpr int kRelWide = 190;  // places: a warp's 32 rows and 64 keys span 95
 struct RelTable {
   const void* table;  // [buckets, heads], bf16 or fp32

@@ -36,8 +36,9 @@ __device__ __forceinline__ void rel_layout(const RelLayout& l, int block, int bl
     }
     const int b = rel_bucket(t, x - t.reach - kRelPad);
     const int64_t at = static_cast<int64_t>(b) * t.heads + h;
-    const float v = t.f32 ? __ldg(static_cast<const float*>(t.table) + at)
+    float v = t.f32 ? __ldg(static_cast<const float*>(t.table) + at)
                           : __bfloat162float(static_cast<const __nv_bfloat16*>(t.table)[at]);
+    if (isfinite(v)) v = fminf(fmaxf(v, -kRelMaxEntry), kRelMaxEntry);
     l.by_place[i] = v * t.inv_scale;
     if (h == 0) l.bucket[x] = static_cast<uint8_t>(b);
   }

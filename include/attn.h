@@ -221,8 +221,10 @@ typedef struct attn_fwd_params {
    *   min(n_b - 1, m + floor((n_b - m) log(n / m) / log(rel_max_distance / m))),
    * borders that fall on a whole distance decided exactly; n_b = 1 is one bucket for
    * all. rel_buckets is 1 to 128, rel_max_distance m + 1 to 65536 (else
-   * ATTN_ERR_INVALID_ARG). An entry of -inf masks its bucket; a row left without keys
-   * by that has O = 0, LSE = -inf and dQ = 0. The bias works with the dense and the
+   * ATTN_ERR_INVALID_ARG), softmax_scale above 2^-112. An entry of -inf masks its
+   * bucket; a row left without keys by that has O = 0, LSE = -inf and dQ = 0. Finite
+   * entries count up to +-65536 (their steps in fp32 are all of a logit beyond): a row
+   * whose keys all have a type's lowest value is that of equal entries. The bias works with the dense and the
    * variable-length forward and backward and attn_fwd_paged, with shared K/V heads;
    * the block-sparse pair gives ATTN_ERR_UNSUPPORTED. The workspaces then hold, in
    * addition, the bias by distance, and in the backward its gradient's partial sums. */

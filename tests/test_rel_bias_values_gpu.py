@@ -1,4 +1,5 @@
-"""Tables with large finite entries (masks by a type's lowest value)."""
+"""Tables with entries that are no ordinary numbers: large finite ones (masks by a type's lowest value), and, over the paged
+cache, infinities and NaN."""
 import math
 
 import numpy as np
@@ -140,6 +141,28 @@ def _paged(ea, seed, h, hk, new, table, clean, far, two_sided, causal, d=64, pag
         part = slice(int(cu[i]), int(cu[i + 1]))
         out, off = _ref(q[part], keys, values, clean, far, two_sided, causal, p_step=2.0 ** -8)
         _check((o[part], lse[:, part]), out, off, ("o", "lse"))
+
+
+@pytest.mark.parametrize("h,hk,new", PAGED)
+@pytest.mark.parametrize("causal,two_sided", [(True, False), (False, True)])
+def test_paged_masked_buckets(ea, h, hk, new, causal, two_sided):
+    """-inf far away, whole segments of a long context, near by, and everywhere."""
+    rng = np.random.default_rng(h)
+    left = 7 if two_sided else 15
+    for masked in ([left], [0, 1], list(range(left)), list(range(16))):
+        table = torch.tensor(rng.standard_normal((16, h)), dtype=torch.float32, device="cuda")
+        table[masked] = NEG
+        _paged(ea, 1, h, hk, new, table, table, 60, two_sided, causal)
+
+
+@pytest.mark.parametrize("h,hk,new", PAGED)
+@pytest.mark.parametrize("bad", [math.nan, math.inf, NEG])
+def test_paged_entries_that_no_pair_falls_in(ea, h, hk, new, bad):
+    rng = np.random.default_rng(h)
+    table = torch.tensor(rng.standard_normal((32, h)), dtype=torch.float32, device="cuda")
+    clean = table.clone()
+    table[16:], clean[16:] = bad, 0.0  # two-sided under a causal mask: no key lies behind its query
+    _paged(ea, 2, h, hk, new, table, clean, 60, True, True)
 
 
 @pytest.mark.parametrize("h,hk,new", PAGED)

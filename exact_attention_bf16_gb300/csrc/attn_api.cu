@@ -1370,7 +1370,7 @@ PagedPlan paged_plan(const attn_paged_params* p) {
     pl.off_items = pl.off_list + 256;
     pl.bytes = pl.off_items + round256(pl.items * static_cast<int64_t>(sizeof(ChunkItem)));
   }
-  pl.rel_group = pl.even ? 1 : group;  // RelPaged
+  pl.rel_group = pl.even || !rel_in_fours(group) ? 1 : group;  // RelPaged
   pl.rel = rel_plan(p, std::max<int64_t>(static_cast<int64_t>(p->max_pages) * p->page_size, p->max_seqlen_q),
                     pl.rel_group > 1 ? static_cast<int64_t>(p->heads_kv) * ((group + 3) / 4 * 4) : p->heads);
   pl.off_rel = pl.bytes;

@@ -126,6 +126,8 @@ constexpr int kRelMaxBuckets = 128;
 // the entry is taken over the scale.
 constexpr float kRelMaxEntry = 65536.f;
 constexpr int kRelWide = 190;  // places: a warp's 32 rows and 64 keys span 95
+// Query heads that share a K/V head, by which paged_kernel reads rows of four heads place by place (RelPaged, which has both measured).
+__host__ __device__ constexpr bool rel_in_fours(int group) { return group > 2; }
 struct RelTable {
   const void* table;  // [buckets, heads], bf16 or fp32
   float inv_scale;    // 1 / softmax_scale

@@ -81,17 +81,18 @@ struct RelRow {
   }
 };
 
-// A head's row in L1 as paged_kernel reads it: by itself, or (FOURS, heads that share a K/V head) place by place among four of
-// them (RelTable::fours): a warp's rows are a few tokens of all these heads, and a load takes a step per line. Chunks of 300 to 1500
-// tokens over up to 8192 keys, 16 heads over 4, 2 and 1, by themselves 118, 108 and 110 us, in fours 114, 102 and 100 (all heads
-// of the group side by side, a stride known at run time: 126 for 127, but 16 over 16 156 for 148). Not where one tile of rows
-// holds any request's tokens (16 requests of 20: 56.3 us so, 55.0).
+// A head's row in L1 as paged_kernel reads it: by itself, or (FOURS, three or more heads that share a K/V head) place by place
+// among four of them (RelTable::fours): a warp's rows are a few tokens of all these heads, and a load takes a step per line. Chunks of
+// 300 to 1500 tokens over up to 8192 keys, by themselves and in fours: 12 heads over 4 99 and 98 us, 16 over 4 120 and 114, 15 over 3 112
+// and 111, 12 over 2 93 and 92, 14 over 2 89 and 87, 16 over 2 112 and 109, 16 over 1 110 and 100. Two heads leave half of every line
+// empty: 16 over 8 123 and 135. (All heads of the group side by side, a stride known at run time: 126 for 127 of 16 over 4, but 16 over
+// 16 156 for 148.) Not where one tile of rows holds any request's tokens (16 requests of 20: 56.3 us so, 55.0).
 template <bool FOURS>
 struct RelPaged {
   const RelBias& b;
   const float* at0;  // of place 0
   bool fours;
-  __device__ __forceinline__ RelPaged(const RelBias& bias, int hk, int group, int h) : b(bias), fours(FOURS && group > 1) {
+  __device__ __forceinline__ RelPaged(const RelBias& bias, int hk, int group, int h) : b(bias), fours(FOURS && rel_in_fours(group)) {
     const int64_t width = 2 * bias.reach + 2 * kRelPad, zero = bias.reach + kRelPad;
     at0 = fours ? bias.by_place + 4 * ((static_cast<int64_t>(hk) * ((group + 3) / 4) + h / 4) * width + zero) + h % 4
                 : bias.by_place + (static_cast<int64_t>(hk) * group + h) * width + zero;

@@ -43,7 +43,7 @@ __global__ void __launch_bounds__(1024) sum_parts_kernel(const float* parts, int
     else static_cast<__nv_bfloat16*>(out)[at] = __float2bfloat16_rn(sum);
   }
   // Beside the dK/dV kernel, behind the parts' kernel: over before this one is. (Behind both, the backward of
-  // 7 packed sequences of up to 500 took 39.4 us, 38.1 so; of 32 x 512, 16 heads, 327 and 324.)
+  // 7 packed sequences of up to 500 took 39.3 us, 38.1 so; of 32 x 512, 16 heads, 329 and 326.)
   asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 

@@ -8,9 +8,9 @@
 // takes one load per logit, neighbouring lanes neighbouring addresses, from a
 // row wide enough that no index needs a test.
 //
-// What it costs: at N = 8192 (B2, 16 heads over 4, d = 128, causal, 32 buckets up to 128) the forward 391 us against
-// 363 without a bias and the backward 1450 against 1385; at N = 512 (B32, 16 heads, d = 64, both sides, half of the warps'
-// tiles within the reach) 89 against 84 and 325 against 283, 27 of them for the table's gradient.
+// What it costs: at N = 8192 (B2, 16 heads over 4, d = 128, causal, 32 buckets up to 128) the forward 387 us against
+// 367 without a bias and the backward 1444 against 1396; at N = 512 (B32, 16 heads, d = 64, both sides, half of the warps'
+// tiles within the reach) 89 against 84 and 327 against 283, 27 of them for the table's gradient.
 #pragma once
 #include "kernels.h"
 #include "ptx_sm100.cuh"

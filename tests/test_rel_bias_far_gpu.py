@@ -41,7 +41,7 @@ def _table_gradient(q, k, v, do, table, far, two_sided, causal):
         y = x // (h // hk)
         a = d ** -0.5 * f(q[:, x]) @ f(k[:, y]).T + f(table[:, x])[which]
         a = torch.where(seen, a, -math.inf)
-        p = torch.where(seen.any(1, keepdim=True), torch.softmax(a, 1), 0.0)
+        p = torch.where((a > -math.inf).any(1, keepdim=True), torch.softmax(a, 1), 0.0)
         g, vv = f(do[:, x]), f(v[:, y])
         dp, terms, o = g @ vv.T, g.abs() @ vv.abs().T, p @ vv
         ds = p * (dp - (p * dp).sum(1, keepdim=True))
